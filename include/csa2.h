@@ -352,13 +352,158 @@ int csa2_concat_parts(int32_t parts, int32_t batch, int32_t k, const int32_t* id
 int csa2_merge_attn(int32_t parts, int32_t rows, int32_t v_dim, const float* out_parts, const float* lse_parts,
                     float* out, float* lse, csa2_stream_t stream);
 
+/* ---------------------------------------------------------------- drafted tokens and bounded caches
+ * A decode step that verifies several drafted tokens per sequence at once, and
+ * caches that are held at a fixed size.  In the order of a step: csa2_rope
+ * turns the drafted queries and keys to their positions, csa2_index_topk
+ * (shape.tokens = T) selects each drafted token's entries, csa2_tree_attn
+ * attends them along the tree; once the caller has chosen the accepted path,
+ * csa2_attn_weights gives the accepted queries' attention weights,
+ * csa2_tree_commit pushes the path into the windows and adds the weights up,
+ * and csa2_kv_evict shrinks the caches that have filled.  The pages describe
+ * neither drafting nor eviction; these calls keep the method's own definitions
+ * (bullet "Sparse attention": selected entries plus the last W tokens) and
+ * bookkeeping.  Their kernels read nothing before the preceding kernel of the
+ * stream has completed. */
+
+/* Frequencies of rotary positions, in radians per position, for rot_dim / 2
+ * pairs (host only; the caller copies them to the device once).  With
+ * f_i = base^(-2i / rot_dim):
+ *   CSA2_ROPE_PLAIN   f_i
+ *   CSA2_ROPE_LINEAR  f_i / factor
+ *   CSA2_ROPE_NTK     as PLAIN with base * factor^(rot_dim / (rot_dim - 2)), rot_dim > 2
+ *   CSA2_ROPE_YARN    pairs that turn more than beta_fast times over orig_ctx positions keep f_i, pairs that turn less than
+ *                     beta_slow times get f_i / factor, a linear ramp over the pairs between them; the magnitude is
+ *                     0.1 ln(factor) + 1
+ * *mag (nullable) receives the magnitude (1 but for YARN).  rot_dim even,
+ * 2..1024; base > 1; factor >= 1; YARN: orig_ctx >= 1, beta_fast > beta_slow > 0. */
+typedef enum { CSA2_ROPE_PLAIN = 0, CSA2_ROPE_LINEAR = 1, CSA2_ROPE_NTK = 2, CSA2_ROPE_YARN = 3 } csa2_rope_scaling;
+int csa2_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, int32_t orig_ctx, double beta_fast,
+                    double beta_slow, double* freqs, float* mag);
+
+/* One tensor of csa2_rope: x and out [rows, heads, dim] in dtype (csa2_dtype).
+ * Dims rot_off .. rot_off + rot_dim - 1 of every head are turned, the others
+ * copied.  out == x works in place (only the turned dims are touched); any
+ * other overlap is refused. */
+typedef struct {
+  const void* x;
+  void* out;
+  int32_t heads, dim, rot_off, dtype;
+} csa2_rope_slot;
+
+/* Rotary positions, partial and in either layout, for several tensors of the
+ * same rows (queries, keys, indexer queries, ...) in one launch:
+ * the pair (a, b) of row r, pair i becomes
+ *   mag * (a cos t - b sin t, b cos t + a sin t),  t = pos[r] * freqs[i];
+ * inverse = 1 turns back: the angle is -t and the magnitude 1 / mag.
+ * Pairs are dims (i, i + rot_dim / 2) of the turned range, or (2i, 2i + 1)
+ * when interleaved = 1.  The angle is reduced exactly for any int32 position
+ * (fixed-point turns), the arithmetic is fp32, rounded once.
+ *   pos [rows] int32   freqs [rot_dim / 2] double (device)
+ * 1 <= n_slots <= 16; mag finite and > 0. */
+int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,
+              const int32_t* pos, const double* freqs, float mag, int32_t inverse, csa2_stream_t stream);
+
+/* Sparse attention of a tree of drafted tokens (shape.tokens = T <= 128,
+ * B = S * T queries, query b = s*T + t is drafted token t of sequence s).
+ * One softmax per query and head over
+ *   - the main-KV rows idx[b, :] (entries < 0 are skipped, as in csa2_sparse_attn);
+ *   - token t itself and its ancestors in the tree, rows of k_draft / v_draft;
+ *   - the sequence's committed window rows,
+ * the last two limited to the W = shape.swa tokens that end at token t along
+ * its path: a token of depth d (0 for a root) sees the nearest min(d + 1, W)
+ * drafted tokens of its path and the newest W - (d + 1) committed ones.
+ * parent[s, t] is the token's parent, an earlier token (0 <= parent < t), or
+ * -1 for a root; anything else is recorded (bad index) and taken as -1.
+ * parent == NULL is a chain (parent = t - 1).  Tokens t >= n_draft[s] are not
+ * live: out = 0, lse = -inf (n_draft == NULL: all T are).  A live token must
+ * not have a parent that is not live; parent < t ensures that.
+ * The window is what csa2_swa_append and csa2_tree_commit keep: a full ring
+ * (n_swa[s] == W) has its oldest row at swa_head[s] (swa_head == NULL: row 0),
+ * one that is not full holds its rows oldest first from row 0.
+ *   q [B, H, dk]  k_main [S, N, dk]  v_main [S, N, dv]  idx [B, K]
+ *   k_swa [S, W, dk]  v_swa [S, W, dv]  swa_head, n_swa [S]
+ *   k_draft [S, T, dk]  v_draft [S, T, dv]  parent [S, T]  n_draft [S] (1..T)
+ *   out [B, H, dv] in the element type (it feeds the output projection)
+ *   lse [B, H] fp32 (nullable)
+ * shape.swa >= 1.  A chain of T gives what T steps of csa2_swa_append and
+ * csa2_sparse_attn give. */
+int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, const void* v_main, const int32_t* idx,
+                   const void* k_swa, const void* v_swa, const int32_t* swa_head, const int32_t* n_swa,
+                   const void* k_draft, const void* v_draft, const int32_t* parent, const int32_t* n_draft, void* out,
+                   float* lse, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/* The attention weight of every selected entry, summed over the heads:
+ *   weights[b, j] = sum_h exp(scale * q[b, h] . k_main[idx[b, j]] - lse[b, h])
+ * with the lse of csa2_tree_attn, csa2_sparse_attn or a layer of
+ * csa2_layer_group; 0 where idx[b, j] < 0, and heads with lse = -inf add
+ * nothing.  live[b] = 0 leaves the query out: its weights are written as 0
+ * and nothing of it is read (NULL: all are wanted).
+ *   q [B, H, dk]  k_main [B / T, N, dk]  idx [B, K]  lse [B, H]  live [B]
+ *   weights [B, K] fp32 */
+int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main, const int32_t* idx, const float* lse,
+                      const int32_t* live, float* weights, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/* One layer's part of csa2_tree_commit (B = S * T as in csa2_tree_attn). */
+typedef struct {
+  const void* k_draft;    /* [S, T, dk] */
+  const void* v_draft;    /* [S, T, dv] */
+  void* k_swa;            /* [S, W, dk] the layer's window (updated in place) */
+  void* v_swa;            /* [S, W, dv] */
+  const int32_t* idx;     /* [B, K] the layer's selected entries, or NULL */
+  const float* weights;   /* [B, K] their weights (csa2_attn_weights), or NULL: the layer adds nothing */
+} csa2_tree_slot;
+
+/* Commit the accepted path of every sequence: path[s, 0 .. n_path[s]) are its
+ * drafted tokens, root first (n_path[s] in 0..T; the rest of path is not
+ * read).  Every layer's rows k_draft / v_draft of these tokens go into its
+ * window ring at swa_head[s], swa_head[s] + 1, ... modulo W, as as many
+ * csa2_swa_append calls would put them (one head and one fill count per
+ * sequence, shared by the layers); then swa_head and n_swa are advanced.
+ * mass (nullable) accumulates attention weights per cache entry, for
+ * csa2_kv_evict: for every accepted token b = s*T + path[s, i] and layer with
+ * weights,
+ *   mass[s, idx[b, j]] += rint(weights[b, j] * 2^32)
+ * in integers, so that the sums depend on no order and lose nothing over long
+ * runs.  Entries with idx < 0 add nothing; a weight that is not in
+ * [0, 2^20] is recorded (bad weight, bit 4 of the error word) and adds
+ * nothing, an idx >= N is recorded and skipped.  A path id outside 0..T-1 is
+ * recorded (bad index) and ends the path before it.
+ *   path [S, T]  n_path [S]  swa_head [S], n_swa [S] (read and updated)
+ *   mass [S, N] int64 (read and updated)
+ * 1 <= n_layers <= 64; shape.swa >= 1; shape.tokens = T.  Windows, heads and
+ * mass must not overlap what the call reads. */
+int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int32_t n_layers, const int32_t* path,
+                     const int32_t* n_path, int32_t* swa_head, int32_t* n_swa, int64_t* mass, void* ws, size_t ws_bytes,
+                     csa2_stream_t stream);
+
+/* Evict from every sequence that holds more than `trigger` entries, down to
+ * `keep`: the first `sink` and the last `recent` entries stay, and of the
+ * others the keep - sink - recent with the greatest mass (ties: the lowest
+ * index).  What stays moves together in its order; sequences at or below the
+ * trigger keep all.  0 <= sink, recent; 1 <= keep <= trigger <= N;
+ * sink + recent <= keep; shape.tokens <= 1.
+ *   k_main [S, N, dk]  v_main [S, N, dv]  k_idx [S, N, dI]  mass [S, N] int64  n_valid [S]
+ *   k_main_out, v_main_out, k_idx_out, mass_out, n_valid_out: the same shapes
+ *   kept [S, N] int32 (output): the entry that each row held before, -1 behind the last
+ *   kb_out [S, ceil(N / block), dI] (nullable): block keys of the result, as csa2_block_keys gives them
+ * Rows behind the last entry stay as they were, but for mass_out, which is 0
+ * there.  Either every _out is its input (in place: a sequence that is not
+ * evicted from is not written, its row of kept apart), or the
+ * outputs overlap no input (then every sequence is copied). */
+int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_t sink, int32_t recent,
+                  const void* k_main, const void* v_main, const void* k_idx, const int64_t* mass, const int32_t* n_valid,
+                  void* k_main_out, void* v_main_out, void* k_idx_out, int64_t* mass_out, int32_t* n_valid_out,
+                  int32_t* kept, void* kb_out, int32_t round_to_int, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
 /* Static description of a status code. */
 const char* csa2_status_str(int status);
 
 /* Synchronise `stream`, read and clear the sticky device error word of `ws`.
  * Returns CSA2_OK, CSA2_ERR_DEVICE_CHECK or CSA2_ERR_TIMEOUT (a bounded wait
  * gave up); *detail (nullable) receives the error bits (bit 0 bad index,
- * bit 1 bad count, bit 2 timeout, bit 3 bad pooled block) in its low byte. */
+ * bit 1 bad count, bit 2 timeout, bit 3 bad pooled block, bit 4 bad weight) in
+ * its low byte. */
 int csa2_read_device_error(void* ws, csa2_stream_t stream, int32_t* detail);
 
 /* 1 when the fast (tensor-core) kernels serve this shape, 0 when the generic

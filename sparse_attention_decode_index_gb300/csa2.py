@@ -76,6 +76,13 @@ _SIGS = {
     "csa2_shard_counts": (ctypes.c_int, [_VP, _I32, _I32, _I32, _I32, _VP, _VP]),
     "csa2_concat_parts": (ctypes.c_int, [_I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP]),
     "csa2_merge_attn": (ctypes.c_int, [_I32, _I32, _I32, _VP, _VP, _VP, _VP, _VP]),
+    "csa2_rope_freqs": (ctypes.c_int, [_I32, ctypes.c_double, _I32, ctypes.c_double, _I32, ctypes.c_double,
+                                       ctypes.c_double, _VP, ctypes.POINTER(ctypes.c_float)]),
+    "csa2_rope": (ctypes.c_int, [_VP, _I32, _I32, _I32, _I32, _VP, _VP, ctypes.c_float, _I32, _VP]),
+    "csa2_tree_attn": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_VP] * 15 + [_SZ, _VP]),
+    "csa2_attn_weights": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_VP] * 7 + [_SZ, _VP]),
+    "csa2_tree_commit": (ctypes.c_int, [ctypes.POINTER(CShape), _VP, _I32] + [_VP] * 6 + [_SZ, _VP]),
+    "csa2_kv_evict": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_I32] * 4 + [_VP] * 12 + [_I32, _VP, _SZ, _VP]),
     "csa2_debug_wait_timeout": (ctypes.c_int, [ctypes.POINTER(CShape), _VP, _VP, _VP, _VP, _I32, _VP, ctypes.c_uint32,
                                                _VP, _SZ, _VP]),
 }
@@ -368,6 +375,212 @@ def merge_attn(out_parts, lse_parts, out, lse=None, stream=None):
     _check(lib().csa2_merge_attn(parts, rows, v_dim, _ptr(out_parts, torch.float32, "out_parts"),
                                  _ptr(lse_parts, torch.float32, "lse_parts"), _ptr(out, torch.float32, "out"),
                                  _ptr(lse, torch.float32, "lse"), _stream(stream)), "csa2_merge_attn")
+
+
+# ------------------------------------------------------------------ drafted tokens and bounded caches
+
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = 0, 1, 2, 3
+_ROPE_SCALING = {"plain": ROPE_PLAIN, "linear": ROPE_LINEAR, "ntk": ROPE_NTK, "yarn": ROPE_YARN}
+
+
+def _arr(t, dtype, shape, name: str, device=None, optional: bool = False):
+    """Pointer of a contiguous CUDA tensor of exactly this dtype, shape and device (None: NULL where optional)."""
+    if t is None:
+        if optional:
+            return None
+        raise TypeError(f"{name} is missing")
+    p = _ptr(t, dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+    return p
+
+
+class _Call:
+    """A marshalled call: arguments checked once, launched any number of times on the device of its tensors.
+
+    It holds its tensors, so that their memory lives as long as it does."""
+
+    def _bind(self, what: str, device, keep, args):
+        self.what, self.device, self._keep, self._args = what, device, keep, args
+        self._fn = getattr(lib(), what)
+
+    def __call__(self, stream=None):
+        if torch.cuda.current_device() == self.device.index:
+            status = self._fn(*self._args, _stream(stream))
+        else:
+            with torch.cuda.device(self.device):
+                status = self._fn(*self._args, _stream(stream))
+        if status != OK:
+            raise CSA2Error(status, self.what)
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0, orig_ctx: int = 0,
+               beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """Rotary frequencies of ``rot_dim / 2`` pairs (radians per position, float64 on ``device``) and the magnitude;
+    ``scaling`` is "plain", "linear", "ntk" or "yarn" (csa2_rope_freqs)."""
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}, got {scaling!r}")
+    host = (ctypes.c_double * max(1, int(rot_dim) // 2))()
+    mag = ctypes.c_float(1.0)
+    _check(lib().csa2_rope_freqs(int(rot_dim), float(base), _ROPE_SCALING[scaling], float(factor), int(orig_ctx),
+                                 float(beta_fast), float(beta_slow), ctypes.cast(host, ctypes.c_void_p),
+                                 ctypes.byref(mag)), "csa2_rope_freqs")
+    return torch.tensor(list(host), dtype=torch.float64, device=device), float(mag.value)
+
+
+class CRopeSlot(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("rot_off", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class RopeCall(_Call):
+    """A prepared csa2_rope call.  ``slots`` is a list of (x, out, rot_off): x [rows, heads, dim] or [rows, dim] in
+    bf16 or fp32, out of the same shape and type (out is x: in place)."""
+
+    def __init__(self, slots, pos, freqs, mag: float = 1.0, interleaved: bool = False, inverse: bool = False):
+        slots = list(slots)
+        rows = int(pos.shape[0])
+        dev = pos.device
+        arr = (CRopeSlot * max(1, len(slots)))()
+        for k, (x, out, off) in enumerate(slots):
+            if x.dim() not in (2, 3) or x.dtype not in (torch.bfloat16, torch.float32) or int(x.shape[0]) != rows:
+                raise ValueError(f"slot {k}: x must be bf16 or fp32 [{rows}, heads, dim] or [{rows}, dim], got "
+                                 f"{x.dtype} {tuple(x.shape)}")
+            arr[k] = CRopeSlot(_arr(x, x.dtype, x.shape, "x", dev), _arr(out, x.dtype, x.shape, "out", dev),
+                               int(x.shape[1]) if x.dim() == 3 else 1, int(x.shape[-1]), int(off),
+                               F32 if x.dtype == torch.float32 else BF16)
+        self._bind("csa2_rope", dev, (slots, pos, freqs, arr),
+                   (ctypes.cast(arr, ctypes.c_void_p), len(slots), rows, 2 * int(freqs.shape[0]), int(bool(interleaved)),
+                    _arr(pos, torch.int32, (rows,), "pos", dev),
+                    _arr(freqs, torch.float64, (int(freqs.shape[0]),), "freqs", dev), float(mag), int(bool(inverse))))
+
+
+def rope(slots, pos, freqs, mag: float = 1.0, interleaved: bool = False, inverse: bool = False, stream=None):
+    """Turn the tensors of ``slots`` to their rows' positions (csa2_rope; RopeCall describes the arguments)."""
+    RopeCall(slots, pos, freqs, mag, interleaved, inverse)(stream)
+
+
+def _tree_sizes(shape):
+    T = max(1, int(getattr(shape, "tokens", 1)))
+    return int(shape.batch), int(shape.batch) // T, T
+
+
+def _ws_arg(ws, device):
+    if ws is None:
+        return None, 0
+    return _arr(ws, torch.uint8, ws.shape, "ws", device), ws.numel()
+
+
+class TreeAttnCall(_Call):
+    """A prepared csa2_tree_attn call (shape.tokens drafted tokens per sequence)."""
+
+    def __init__(self, shape, q, k_main, v_main, idx, k_swa, v_swa, n_swa, k_draft, v_draft, out, ws, swa_head=None,
+                 parent=None, n_draft=None, lse=None):
+        s, e, dev = c_shape(shape), elem_dtype(shape), q.device
+        B, S, T = _tree_sizes(shape)
+        N, H, dk, dv, W, K = s.n_entries, s.q_heads, s.k_dim, s.v_dim, s.swa, s.topk
+        i32 = torch.int32
+        self._bind("csa2_tree_attn", dev,
+                   (s, q, k_main, v_main, idx, k_swa, v_swa, n_swa, k_draft, v_draft, out, ws, swa_head, parent, n_draft, lse),
+                   (ctypes.byref(s), _arr(q, e, (B, H, dk), "q", dev), _arr(k_main, e, (S, N, dk), "k_main", dev),
+                    _arr(v_main, e, (S, N, dv), "v_main", dev), _arr(idx, i32, (B, K), "idx", dev),
+                    _arr(k_swa, e, (S, W, dk), "k_swa", dev), _arr(v_swa, e, (S, W, dv), "v_swa", dev),
+                    _arr(swa_head, i32, (S,), "swa_head", dev, True), _arr(n_swa, i32, (S,), "n_swa", dev),
+                    _arr(k_draft, e, (S, T, dk), "k_draft", dev), _arr(v_draft, e, (S, T, dv), "v_draft", dev),
+                    _arr(parent, i32, (S, T), "parent", dev, True), _arr(n_draft, i32, (S,), "n_draft", dev, True),
+                    _arr(out, e, (B, H, dv), "out", dev), _arr(lse, torch.float32, (B, H), "lse", dev, True),
+                    *_ws_arg(ws, dev)))
+
+
+def tree_attn(shape, q, k_main, v_main, idx, k_swa, v_swa, n_swa, k_draft, v_draft, out, ws, swa_head=None, parent=None,
+              n_draft=None, lse=None, stream=None):
+    """Attention of a tree of drafted tokens (csa2_tree_attn): q [B, H, dk] of S * T drafted tokens, the sequences'
+    windows [S, W, ...] and drafted rows [S, T, ...], parent [S, T] (None: chains); out in the element type."""
+    TreeAttnCall(shape, q, k_main, v_main, idx, k_swa, v_swa, n_swa, k_draft, v_draft, out, ws, swa_head, parent, n_draft,
+                 lse)(stream)
+
+
+class AttnWeightsCall(_Call):
+    """A prepared csa2_attn_weights call."""
+
+    def __init__(self, shape, q, k_main, idx, lse, weights, ws, live=None):
+        s, e, dev = c_shape(shape), elem_dtype(shape), q.device
+        B, S, _ = _tree_sizes(shape)
+        f32, i32 = torch.float32, torch.int32
+        self._bind("csa2_attn_weights", dev, (s, q, k_main, idx, lse, weights, ws, live),
+                   (ctypes.byref(s), _arr(q, e, (B, s.q_heads, s.k_dim), "q", dev),
+                    _arr(k_main, e, (S, s.n_entries, s.k_dim), "k_main", dev), _arr(idx, i32, (B, s.topk), "idx", dev),
+                    _arr(lse, f32, (B, s.q_heads), "lse", dev), _arr(live, i32, (B,), "live", dev, True),
+                    _arr(weights, f32, (B, s.topk), "weights", dev), *_ws_arg(ws, dev)))
+
+
+def attn_weights(shape, q, k_main, idx, lse, weights, ws, live=None, stream=None):
+    """The softmax weight of every selected entry, summed over the heads, into weights [B, K] (csa2_attn_weights)."""
+    AttnWeightsCall(shape, q, k_main, idx, lse, weights, ws, live)(stream)
+
+
+class CTreeSlot(ctypes.Structure):
+    _fields_ = [("k_draft", ctypes.c_void_p), ("v_draft", ctypes.c_void_p), ("k_swa", ctypes.c_void_p),
+                ("v_swa", ctypes.c_void_p), ("idx", ctypes.c_void_p), ("weights", ctypes.c_void_p)]
+
+
+class TreeCommitCall(_Call):
+    """A prepared csa2_tree_commit call.  ``slots`` holds one (k_draft, v_draft, k_swa, v_swa, idx, weights) per layer;
+    idx and weights may be None."""
+
+    def __init__(self, shape, slots, path, n_path, swa_head, n_swa, ws, mass=None):
+        s, e, dev = c_shape(shape), elem_dtype(shape), path.device
+        B, S, T = _tree_sizes(shape)
+        dk, dv, W, K = s.k_dim, s.v_dim, s.swa, s.topk
+        slots = list(slots)
+        arr = (CTreeSlot * max(1, len(slots)))(*[
+            CTreeSlot(_arr(kd, e, (S, T, dk), "k_draft", dev), _arr(vd, e, (S, T, dv), "v_draft", dev),
+                      _arr(ks, e, (S, W, dk), "k_swa", dev), _arr(vs, e, (S, W, dv), "v_swa", dev),
+                      _arr(ix, torch.int32, (B, K), "idx", dev, True),
+                      _arr(wt, torch.float32, (B, K), "weights", dev, True)) for kd, vd, ks, vs, ix, wt in slots])
+        i32 = torch.int32
+        self._bind("csa2_tree_commit", dev, (s, slots, arr, path, n_path, swa_head, n_swa, ws, mass),
+                   (ctypes.byref(s), ctypes.cast(arr, ctypes.c_void_p), len(slots), _arr(path, i32, (S, T), "path", dev),
+                    _arr(n_path, i32, (S,), "n_path", dev), _arr(swa_head, i32, (S,), "swa_head", dev),
+                    _arr(n_swa, i32, (S,), "n_swa", dev), _arr(mass, torch.int64, (S, s.n_entries), "mass", dev, True),
+                    *_ws_arg(ws, dev)))
+
+
+def tree_commit(shape, slots, path, n_path, swa_head, n_swa, ws, mass=None, stream=None):
+    """Push the accepted path [S, T] / n_path [S] of every sequence into the layers' windows and add the accepted
+    queries' weights to mass [S, N] int64, in units of 2^-32 (csa2_tree_commit).  ``ws`` may be None."""
+    TreeCommitCall(shape, slots, path, n_path, swa_head, n_swa, ws, mass)(stream)
+
+
+class KvEvictCall(_Call):
+    """A prepared csa2_kv_evict call.  ``out`` is (k_main, v_main, k_idx, mass, n_valid) of the result, or None: in place."""
+
+    def __init__(self, shape, trigger: int, keep: int, sink: int, recent: int, k_main, v_main, k_idx, mass, n_valid, kept, ws,
+                 kb=None, out=None, round_to_int: bool = True):
+        s, e, dev = c_shape(shape), elem_dtype(shape), k_main.device
+        B, N = s.batch, s.n_entries
+        ins = (k_main, v_main, k_idx, mass, n_valid)
+        outs = ins if out is None else tuple(out)
+        if len(outs) != 5:
+            raise ValueError("out must be (k_main, v_main, k_idx, mass, n_valid)")
+        kinds = ((e, (B, N, s.k_dim), "k_main"), (e, (B, N, s.v_dim), "v_main"), (e, (B, N, s.idx_dim), "k_idx"),
+                 (torch.int64, (B, N), "mass"), (torch.int32, (B,), "n_valid"))
+        ptrs = [_arr(t, d, z, n + w, dev) for w, ts in (("", ins), ("_out", outs)) for t, (d, z, n) in zip(ts, kinds)]
+        nb = -(-N // max(1, s.block))
+        self._bind("csa2_kv_evict", dev, (s, ins, outs, kept, kb, ws),
+                   (ctypes.byref(s), int(trigger), int(keep), int(sink), int(recent), *ptrs,
+                    _arr(kept, torch.int32, (B, N), "kept", dev), _arr(kb, e, (B, nb, s.idx_dim), "kb", dev, True),
+                    int(bool(round_to_int)), *_ws_arg(ws, dev)))
+
+
+def kv_evict(shape, trigger: int, keep: int, sink: int, recent: int, k_main, v_main, k_idx, mass, n_valid, kept, ws, kb=None,
+             out=None, round_to_int: bool = True, stream=None):
+    """Shrink every cache with more than ``trigger`` entries to ``keep``: the first ``sink``, the last ``recent`` and the
+    greatest by mass stay, in order (csa2_kv_evict).  In place, or into ``out``; ``ws`` may be None."""
+    KvEvictCall(shape, trigger, keep, sink, recent, k_main, v_main, k_idx, mass, n_valid, kept, ws, kb, out,
+                round_to_int)(stream)
 
 
 def debug_wait_timeout(shape, q_idx, w, k_idx, n_valid, k: int, idx_out, wait_limit_ns: int, ws, stream=None):

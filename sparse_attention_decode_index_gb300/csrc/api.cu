@@ -8,6 +8,7 @@
 // and every layer attends with its own query and SWA KV.
 #include <atomic>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -102,6 +103,7 @@ T* at(void* ws, size_t off) {
   } while (0)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 int check_shape(const csa2_shape* s) {
   if (s == nullptr) return CSA2_ERR_INVALID_ARG;
@@ -134,6 +136,15 @@ int check_ws(const csa2_shape& s, void* ws, size_t bytes) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return CSA2_ERR_WORKSPACE;
   if (bytes < layout(s).total) return CSA2_ERR_WORKSPACE;
   return CSA2_OK;
+}
+
+constexpr int kMaxRotDim = 1024;
+constexpr int kMaxGridY = 65535;   // queries or sequences are a grid's y dimension
+
+// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
+bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
 }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
@@ -686,6 +697,271 @@ int csa2_merge_attn(int32_t parts, int32_t rows, int32_t v_dim, const float* out
   a.rows = rows;
   a.v_dim = v_dim;
   return cuda_status(launch_merge_attn(a, stream));
+}
+
+// ---------------------------------------------------------------- drafted tokens and bounded caches
+
+int csa2_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor, int32_t orig_ctx, double beta_fast,
+                    double beta_slow, double* freqs, float* mag) {
+  if (freqs == nullptr || rot_dim < 2 || rot_dim > kMaxRotDim || rot_dim % 2 != 0) return CSA2_ERR_INVALID_ARG;
+  if (!(base > 1.0) || !std::isfinite(base)) return CSA2_ERR_INVALID_ARG;
+  if (scaling < CSA2_ROPE_PLAIN || scaling > CSA2_ROPE_YARN) return CSA2_ERR_INVALID_ARG;
+  if (scaling != CSA2_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor))) return CSA2_ERR_INVALID_ARG;
+  if (scaling == CSA2_ROPE_NTK && rot_dim == 2) return CSA2_ERR_INVALID_ARG;
+  if (scaling == CSA2_ROPE_YARN &&
+      (orig_ctx < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
+    return CSA2_ERR_INVALID_ARG;
+  const double b = scaling == CSA2_ROPE_NTK ? base * std::pow(factor, double(rot_dim) / (rot_dim - 2)) : base;
+  // the (real-valued) pair that turns `turns` times over orig_ctx positions
+  const double two_pi = 6.283185307179586476925286766559;
+  auto pair_of = [&](double turns) { return rot_dim * std::log(orig_ctx / (turns * two_pi)) / (2.0 * std::log(base)); };
+  double lo = 0.0, hi = 1.0;
+  if (scaling == CSA2_ROPE_YARN) {
+    lo = std::fmax(0.0, std::floor(pair_of(beta_fast)));
+    hi = std::fmin(rot_dim - 1.0, std::ceil(pair_of(beta_slow)));
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(b, -2.0 * i / rot_dim);
+    if (scaling == CSA2_ROPE_LINEAR) f /= factor;
+    if (scaling == CSA2_ROPE_YARN) {
+      const double keep = 1.0 - std::fmin(1.0, std::fmax(0.0, (i - lo) / std::fmax(hi - lo, 0.001)));
+      f = f / factor * (1.0 - keep) + f * keep;
+    }
+    freqs[i] = f;
+  }
+  if (mag != nullptr) *mag = scaling == CSA2_ROPE_YARN ? float(0.1 * std::log(factor) + 1.0) : 1.f;
+  return CSA2_OK;
+}
+
+int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,
+              const int32_t* pos, const double* freqs, float mag, int32_t inverse, csa2_stream_t stream) {
+  if (slots == nullptr || n_slots < 1 || n_slots > kMaxRopeSlots || rows < 1) return CSA2_ERR_INVALID_ARG;
+  if (rot_dim < 2 || rot_dim % 2 != 0 || pos == nullptr || freqs == nullptr || !aligned8(freqs))
+    return CSA2_ERR_INVALID_ARG;
+  if (rot_dim > kMaxRotDim) return CSA2_ERR_UNSUPPORTED;
+  if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return CSA2_ERR_INVALID_ARG;
+  if (!(mag > 0.f) || !std::isfinite(mag) || !std::isfinite(1.f / mag)) return CSA2_ERR_INVALID_ARG;
+  RopeArgs a{};
+  for (int k = 0; k < n_slots; ++k) {
+    const csa2_rope_slot& y = slots[k];
+    if (y.x == nullptr || y.out == nullptr || y.heads < 1 || y.dim < 1 || y.rot_off < 0) return CSA2_ERR_INVALID_ARG;
+    if (int64_t(y.rot_off) + rot_dim > y.dim) return CSA2_ERR_INVALID_ARG;
+    if (y.dtype != CSA2_BF16 && y.dtype != CSA2_F32) return CSA2_ERR_INVALID_ARG;
+    if (y.heads > 1024 || y.dim > 1024) return CSA2_ERR_UNSUPPORTED;
+    a.slot[k].x = y.x;
+    a.slot[k].out = y.out;
+    a.slot[k].heads = y.heads;
+    a.slot[k].dim = y.dim;
+    a.slot[k].off = y.rot_off;
+    a.slot[k].dtype = y.dtype;
+  }
+  // an output may be its own input; it may touch nothing else that the call reads or writes
+  auto bytes = [&](int k) { return uint64_t(rows) * slots[k].heads * slots[k].dim * (slots[k].dtype == CSA2_F32 ? 4 : 2); };
+  for (int k = 0; k < n_slots; ++k) {
+    if (overlap(slots[k].out, bytes(k), pos, uint64_t(rows) * 4) || overlap(slots[k].out, bytes(k), freqs, uint64_t(rot_dim) * 4))
+      return CSA2_ERR_INVALID_ARG;
+    for (int j = 0; j < n_slots; ++j) {
+      if ((j != k || slots[k].out != slots[k].x) && overlap(slots[k].out, bytes(k), slots[j].x, bytes(j)))
+        return CSA2_ERR_INVALID_ARG;
+      if (j != k && overlap(slots[k].out, bytes(k), slots[j].out, bytes(j))) return CSA2_ERR_INVALID_ARG;
+    }
+  }
+  a.n_slots = n_slots;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.inverse = inverse;
+  a.mag = mag;
+  a.pos = pos;
+  a.freqs = freqs;
+  return cuda_status(launch_rope(a, rows, stream));
+}
+
+int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, const void* v_main, const int32_t* idx,
+                   const void* k_swa, const void* v_swa, const int32_t* swa_head, const int32_t* n_swa,
+                   const void* k_draft, const void* v_draft, const int32_t* parent, const int32_t* n_draft, void* out,
+                   float* lse, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  CSA2_TRY(check_ws(s, ws, ws_bytes));
+  if (s.swa < 1) return CSA2_ERR_INVALID_ARG;
+  if (seqdiv(s) > kMaxTreeTokens || s.batch > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
+  for (const void* p : {q, k_main, v_main, static_cast<const void*>(idx), k_swa, v_swa, static_cast<const void*>(n_swa),
+                        k_draft, v_draft, static_cast<const void*>(out)})
+    if (p == nullptr) return CSA2_ERR_INVALID_ARG;
+  if (attn_fast(s))
+    for (const void* p : {q, k_main, v_main, k_swa, v_swa, k_draft, v_draft, static_cast<const void*>(out)})
+      if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+  TreeArgs a{};
+  a.q = q;
+  a.k_main = k_main;
+  a.v_main = v_main;
+  a.idx = idx;
+  a.k_swa = k_swa;
+  a.v_swa = v_swa;
+  a.swa_head = swa_head;
+  a.n_swa = n_swa;
+  a.k_draft = k_draft;
+  a.v_draft = v_draft;
+  a.parent = parent;
+  a.n_draft = n_draft;
+  a.out = out;
+  a.lse = lse;
+  a.tokens = seqdiv(s);
+  a.n_entries = s.n_entries;
+  a.topk = s.topk;
+  a.swa = s.swa;
+  a.heads = s.q_heads;
+  a.k_dim = s.k_dim;
+  a.v_dim = s.v_dim;
+  a.dtype = s.dtype;
+  a.scale = softmax_scale(s);
+  a.err = static_cast<int*>(ws);
+  return cuda_status(launch_tree_attn(a, attn_fast(s), s.batch, stream));
+}
+
+int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main, const int32_t* idx, const float* lse,
+                      const int32_t* live, float* weights, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  CSA2_TRY(check_ws(s, ws, ws_bytes));
+  if (s.batch > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
+  if (q == nullptr || k_main == nullptr || idx == nullptr || lse == nullptr || weights == nullptr)
+    return CSA2_ERR_INVALID_ARG;
+  const bool fast = s.dtype == CSA2_BF16 && s.q_heads == 64 && s.k_dim == 192;
+  if (fast && (!aligned16(q) || !aligned16(k_main))) return CSA2_ERR_INVALID_ARG;
+  AttnWeightsArgs a{};
+  a.q = q;
+  a.k_main = k_main;
+  a.idx = idx;
+  a.lse = lse;
+  a.live = live;
+  a.weights = weights;
+  a.seq_div = seqdiv(s);
+  a.n_entries = s.n_entries;
+  a.topk = s.topk;
+  a.heads = s.q_heads;
+  a.k_dim = s.k_dim;
+  a.dtype = s.dtype;
+  a.scale = softmax_scale(s);
+  a.err = static_cast<int*>(ws);
+  return cuda_status(launch_attn_weights(a, fast, s.batch, stream));
+}
+
+int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int32_t n_layers, const int32_t* path,
+                     const int32_t* n_path, int32_t* swa_head, int32_t* n_swa, int64_t* mass, void* ws, size_t ws_bytes,
+                     csa2_stream_t stream) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  if (s.swa < 1 || layers == nullptr || n_layers < 1 || n_layers > kMaxTreeLayers) return CSA2_ERR_INVALID_ARG;
+  if (path == nullptr || n_path == nullptr || swa_head == nullptr || n_swa == nullptr) return CSA2_ERR_INVALID_ARG;
+  if (!aligned8(mass)) return CSA2_ERR_INVALID_ARG;
+  const int T = seqdiv(s), S = s.batch / T;
+  if (T > kMaxTreeTokens || S > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
+  int* err = nullptr;
+  CSA2_TRY(error_word(s, ws, ws_bytes, &err));
+  TreeCommitArgs a{};
+  const int esize = s.dtype == CSA2_F32 ? 4 : 2;
+  a.k_bytes = s.k_dim * esize;
+  a.v_bytes = s.v_dim * esize;
+  a.wide = a.k_bytes % 16 == 0 && a.v_bytes % 16 == 0;
+  for (int l = 0; l < n_layers; ++l) {
+    const csa2_tree_slot& y = layers[l];
+    if (y.k_draft == nullptr || y.v_draft == nullptr || y.k_swa == nullptr || y.v_swa == nullptr)
+      return CSA2_ERR_INVALID_ARG;
+    if ((y.idx == nullptr) != (y.weights == nullptr)) return CSA2_ERR_INVALID_ARG;
+    if (!aligned16(y.k_draft) || !aligned16(y.v_draft) || !aligned16(y.k_swa) || !aligned16(y.v_swa)) a.wide = 0;
+    a.slot[l] = TreeCommitArgs::Slot{y.k_draft, y.v_draft, y.k_swa, y.v_swa, y.idx, y.weights};
+  }
+  a.n_layers = n_layers;
+  a.path = path;
+  a.n_path = n_path;
+  a.head = swa_head;
+  a.n_swa = n_swa;
+  a.mass = reinterpret_cast<unsigned long long*>(mass);
+  a.tokens = T;
+  a.n_entries = s.n_entries;
+  a.topk = s.topk;
+  a.swa = s.swa;
+  a.err = err;
+  return cuda_status(launch_tree_commit(a, S, stream));
+}
+
+int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_t sink, int32_t recent,
+                  const void* k_main, const void* v_main, const void* k_idx, const int64_t* mass, const int32_t* n_valid,
+                  void* k_main_out, void* v_main_out, void* k_idx_out, int64_t* mass_out, int32_t* n_valid_out,
+                  int32_t* kept, void* kb_out, int32_t round_to_int, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  if (seqdiv(s) != 1) return CSA2_ERR_UNSUPPORTED;   // caches are per sequence: pass a one-token shape
+  if (s.batch > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
+  if (keep < 1 || trigger < keep || trigger > s.n_entries || sink < 0 || recent < 0 || sink > keep || recent > keep - sink)
+    return CSA2_ERR_INVALID_ARG;
+  if (round_to_int != 0 && round_to_int != 1) return CSA2_ERR_INVALID_ARG;
+  const uint64_t B = s.batch, N = s.n_entries, nb = uint64_t(ceil_div(s.n_entries, s.block));
+  const uint64_t esize = s.dtype == CSA2_F32 ? 4 : 2;
+  struct Span {
+    const void* in;
+    void* out;
+    uint64_t bytes;
+  };
+  const Span io[5] = {{k_main, k_main_out, B * N * s.k_dim * esize},
+                      {v_main, v_main_out, B * N * s.v_dim * esize},
+                      {k_idx, k_idx_out, B * N * s.idx_dim * esize},
+                      {mass, mass_out, B * N * 8},
+                      {n_valid, n_valid_out, B * 4}};
+  const Span extra[2] = {{nullptr, kept, B * N * 4}, {nullptr, kb_out, B * nb * s.idx_dim * esize}};
+  if (kept == nullptr || !aligned8(mass) || !aligned8(mass_out)) return CSA2_ERR_INVALID_ARG;
+  int same = 0;
+  for (const Span& x : io) {
+    if (x.in == nullptr || x.out == nullptr) return CSA2_ERR_INVALID_ARG;
+    same += x.in == x.out;
+  }
+  if (same != 0 && same != 5) return CSA2_ERR_INVALID_ARG;   // in place wholly, or not at all
+  for (int i = 0; i < 5; ++i)
+    for (int j = 0; j < 5; ++j) {
+      if (!(same && i == j) && overlap(io[i].out, io[i].bytes, io[j].in, io[j].bytes)) return CSA2_ERR_INVALID_ARG;
+      if (i != j && overlap(io[i].out, io[i].bytes, io[j].out, io[j].bytes)) return CSA2_ERR_INVALID_ARG;
+    }
+  for (const Span& x : extra) {
+    if (x.out == nullptr) continue;
+    for (const Span& y : io)
+      if (overlap(x.out, x.bytes, y.in, y.bytes) || overlap(x.out, x.bytes, y.out, y.bytes)) return CSA2_ERR_INVALID_ARG;
+  }
+  if (kb_out != nullptr && overlap(kept, extra[0].bytes, kb_out, extra[1].bytes)) return CSA2_ERR_INVALID_ARG;
+  int* err = nullptr;
+  CSA2_TRY(error_word(s, ws, ws_bytes, &err));
+  EvictArgs a{};
+  a.k_main = k_main;
+  a.v_main = v_main;
+  a.k_idx = k_idx;
+  a.mass = reinterpret_cast<const long long*>(mass);
+  a.n_valid = n_valid;
+  a.k_main_out = k_main_out;
+  a.v_main_out = v_main_out;
+  a.k_idx_out = k_idx_out;
+  a.mass_out = reinterpret_cast<long long*>(mass_out);
+  a.n_valid_out = n_valid_out;
+  a.kept = kept;
+  a.kb = kb_out;
+  a.trigger = trigger;
+  a.keep = keep;
+  a.sink = sink;
+  a.recent = recent;
+  a.n_entries = s.n_entries;
+  a.nb_cap = int(nb);
+  a.idx_dim = s.idx_dim;
+  a.block = s.block;
+  a.round_to_int = round_to_int;
+  a.dtype = s.dtype;
+  a.k_bytes = int(s.k_dim * esize);
+  a.v_bytes = int(s.v_dim * esize);
+  a.x_bytes = int(s.idx_dim * esize);
+  a.wide = a.k_bytes % 16 == 0 && a.v_bytes % 16 == 0 && a.x_bytes % 16 == 0;
+  for (int i = 0; i < 3; ++i)
+    if (!aligned16(io[i].in) || !aligned16(io[i].out)) a.wide = 0;
+  a.in_place = same != 0;
+  a.err = err;
+  return cuda_status(launch_kv_evict(a, s.batch, stream));
 }
 
 const char* csa2_status_str(int status) {

@@ -35,8 +35,14 @@
 // every CTA resident until its partials have been read.  (Writing the partials
 // to workspace scratch in L2 instead was measured slower at small batches and
 // equal at batch 64.)
+//
+// The tree form (csa2_tree_attn, kTree) differs in the window's slots alone:
+// slot r holds the r-th drafted token of the query's path (0: itself), and
+// behind the path the newest committed rows, so that the window never takes
+// more than W slots and the launch keeps its geometry.  Its output is bf16.
 #include "common.cuh"
 #include "internal.h"
+#include "tree.cuh"
 
 namespace csa2 {
 
@@ -56,13 +62,15 @@ constexpr int kOffM = kOffV + kSlots * kVRow;     // 107,520: [kMaxCluster][kH] 
 constexpr int kOffL = kOffM + kMaxCluster * kH * 4;   // [kMaxCluster][kH] l of every CTA
 constexpr int kOffValid = kOffL + kMaxCluster * kH * 4;
 constexpr int kSmemBytes = kOffValid + kSlots * 4;
+constexpr int kTreeSmemBytes = kSmemBytes + kMaxTreeTokens * 4;   // + the path
 constexpr int kHalf = kSlots / 2;                 // slots per gather barrier (80)
 constexpr int kPRow = kDv + 8;                    // partial O row (fp32): padded against bank conflicts
 static_assert(kH * kPRow * 4 + kMaxCluster * kH * 4 <= kSlots * kKRow, "partials and weights fit the K region");
 static_assert(kSlots % 16 == 0, "PV k-steps need 16-key groups");
 static_assert(kNT % 4 == 0, "each gather half covers whole n-tile pairs");
 
-__global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a) {
+template <bool kTree>
+__global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a, const TreeArgs tree) {
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* sK = smem + kOffK;
   uint8_t* sV = smem + kOffV;
@@ -75,7 +83,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a)
   const int g = lane >> 2, t = lane & 3;
   const uint32_t crank = cluster_rank(), ncta = cluster_size();
 
-  if (!a.release_at_end) pdl_launch_dependents();
+  if (kTree) pdl_wait();   // the calls before this one write its queries, windows and counts
+  else if (!a.release_at_end) pdl_launch_dependents();
   const int mp = (a.topk + int(ncta) - 1) / int(ncta);   // main index slots of this CTA
   const int sp = (a.swa + int(ncta) - 1) / int(ncta);    // SWA rows of this CTA (local slots first)
 
@@ -127,25 +136,45 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a)
 
   // --- group 0: this CTA's SWA rows (inputs of this launch), before waiting on the preceding one.
   // Local slots are handled in quads [4m, 4m + 4), quad m by warp m mod 4.
-  const int ns = clamp_count(a.n_swa[b], a.swa, a.err);
+  const int ns = kTree ? 0 : clamp_count(a.n_swa[b], a.swa, a.err);
+  TreeWindow win;
+  if constexpr (kTree) win = tree_window(tree, b, reinterpret_cast<int*>(smem + kSmemBytes), crank == 0);
+  // K and V row of window slot r (false: the slot holds none)
+  auto window_row = [&](int r, const uint8_t*& kr, const uint8_t*& vr) -> bool {
+    long long row;
+    const void *kb = a.k_swa, *vb = a.v_swa;
+    if (kTree) {
+      bool drafted;
+      if (r >= a.swa || !win.row(r, row, drafted)) return false;
+      if (drafted) {
+        kb = tree.k_draft;
+        vb = tree.v_draft;
+      }
+    } else {
+      if (r >= a.swa || r >= ns) return false;
+      row = (long long)b * a.swa + r;
+    }
+    kr = static_cast<const uint8_t*>(kb) + row * (kDk * 2);
+    vr = static_cast<const uint8_t*>(vb) + row * (kDv * 2);
+    return true;
+  };
   for (int q0 = 4 * warp; q0 < (sp & ~3); q0 += 16) {
     const int ls = q0 + (lane & 3);
-    const int r = int(crank) * sp + ls;
-    const bool ok = lane < 4 && r < a.swa && r < ns;
-    const long long row = (long long)b * a.swa + r;
-    copy_quad(q0, ok ? static_cast<const uint8_t*>(a.k_swa) + row * (kDk * 2) : nullptr,
-              ok ? static_cast<const uint8_t*>(a.v_swa) + row * (kDv * 2) : nullptr);
+    const uint8_t *kr = nullptr, *vr = nullptr;
+    const bool ok = lane < 4 && window_row(int(crank) * sp + ls, kr, vr);
+    copy_quad(q0, ok ? kr : nullptr, ok ? vr : nullptr);
     if (lane < 4) sValid[ls] = ok ? 1 : 0;
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 
-  pdl_wait();   // the indices come from the preceding launch
+  if (!kTree) pdl_wait();   // the indices come from the preceding launch
 
   // --- main index of every slot of this warp's quads 4 * warp + 16i: lane l holds
   // quad i = l / 4 (slot l % 4) in e0 and quad i = 8 + l / 4 in e1 (l < 8); -1: no main row
   auto main_index = [&](int ls) -> int {
     const int lm = ls - sp;
     if (ls >= kSlots || lm < 0 || lm >= mp || int(crank) * mp + lm >= a.topk) return -1;
+    if (kTree && !win.live) return -1;
     return a.idx[(long long)b * a.topk + int(crank) * mp + lm];
   };
   const int e0 = main_index(4 * warp + 16 * (lane >> 2) + (lane & 3));
@@ -166,11 +195,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a)
       bool ok = false;
       if (lane < 4) {
         if (ls < sp) {
-          const int r = int(crank) * sp + ls;
-          ok = r < a.swa && r < ns;
-          const long long row = (long long)b * a.swa + r;
-          kr = static_cast<const uint8_t*>(a.k_swa) + row * (kDk * 2);
-          vr = static_cast<const uint8_t*>(a.v_swa) + row * (kDv * 2);
+          ok = window_row(int(crank) * sp + ls, kr, vr);
         } else {
           if (e >= a.n_entries) report(a.err, kErrBadIndex, e);
           ok = e >= 0 && e < a.n_entries;
@@ -333,7 +358,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a)
           acc.z += wr * v[m][r].z;
           acc.w += wr * v[m][r].w;
         }
-      *reinterpret_cast<float4*>(a.out + ((long long)b * kH + h) * kDv + 4 * d4) = acc;
+      const long long o = ((long long)b * kH + h) * kDv + 4 * d4;
+      if (kTree)
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(tree.out) + o) =
+            make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+      else
+        *reinterpret_cast<float4*>(a.out + o) = acc;
     }
   }
   cluster_arrive();   // this CTA has read its peers' partials
@@ -350,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a)
   // Before another attention launch (a Reuse or SWA layer next), its CTAs are
   // let in only now: placed early, they slowed this launch's last clusters
   // (encoder stack Full + 5 Reuse: 321 -> 293 us per group step).
-  if (a.release_at_end) pdl_launch_dependents();
+  if (!kTree && a.release_at_end) pdl_launch_dependents();
 }
 
 // Generic path: any head count / dims / element type; one CTA per (query, head).
@@ -441,14 +471,40 @@ cudaError_t launch_attn(const AttnArgs& a, bool fast, int batch, cudaStream_t st
     return launch_pdl(attn_generic_kernel, grid, dim3(128), smem, st, 1, a);
   }
   const cudaError_t e = once_per_device(kSetupAttn, [] {
-    return cudaFuncSetAttribute(attn_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return cudaFuncSetAttribute(attn_mma_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (e != cudaSuccess) return e;
   const int ncta = attn_cluster(a.topk, a.swa);
   if (ncta == 0) return cudaErrorInvalidValue;
   note_launch();
-  return launch_pdl(attn_mma_kernel, dim3(unsigned(ncta), unsigned(batch), 1), dim3(kThreads), kSmemBytes, st,
-                    unsigned(ncta), a);
+  return launch_pdl(attn_mma_kernel<false>, dim3(unsigned(ncta), unsigned(batch), 1), dim3(kThreads), kSmemBytes, st,
+                    unsigned(ncta), a, TreeArgs{});
+}
+
+cudaError_t launch_tree_attn_cluster(const TreeArgs& t, int batch, cudaStream_t st) {
+  const cudaError_t e = once_per_device(kSetupTree, [] {
+    return cudaFuncSetAttribute(attn_mma_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  const int ncta = attn_cluster(t.topk, t.swa);
+  if (ncta == 0) return cudaErrorInvalidValue;
+  AttnArgs a{};
+  a.q = t.q;
+  a.k_main = t.k_main;
+  a.v_main = t.v_main;
+  a.seq_div = t.tokens;
+  a.idx = t.idx;
+  a.k_swa = t.k_swa;
+  a.v_swa = t.v_swa;
+  a.lse = t.lse;
+  a.n_entries = t.n_entries;
+  a.topk = t.topk;
+  a.swa = t.swa;
+  a.scale = t.scale;
+  a.err = t.err;
+  note_launch();
+  return launch_pdl(attn_mma_kernel<true>, dim3(unsigned(ncta), unsigned(batch), 1), dim3(kThreads), kTreeSmemBytes, st,
+                    unsigned(ncta), a, t);
 }
 
 // Smallest cluster whose CTAs can each hold ceil(topk / C) main and

@@ -1,0 +1,109 @@
+// Commit of an accepted path (csa2_tree_commit): the accepted drafted tokens'
+// K and V rows into every layer's window ring, and the accepted queries'
+// attention weights into the per-entry mass.
+//
+// One cluster of CTAs per sequence; CTA c takes the layers c, c + C, ... All of
+// them read the shared head and fill count, meet at a cluster barrier, and the
+// first then advances both.  The mass is a 64-bit integer in units of 2^-32:
+// integer atomics commute, so the sums depend on no order, and they stay exact
+// where fp32 sums would stop growing.  rint(w * 2^32) is exact in fp64.
+// Bound by the latency of the loads behind each other (count, path, rows) for
+// few sequences and by the rate of the 64-bit L2 atomics for many.
+//
+// Like the cache-maintenance kernels it lets no later launch start early: the
+// attention reads n_swa and the windows before its own wait.
+#include "common.cuh"
+#include "internal.h"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr float kMaxWeight = 1048576.f;   // 2^20: rint(w * 2^32) < 2^53
+
+template <typename U>
+CSA2_DEV void copy_rows(void* dst, const void* src, int row_bytes, long long dst_row0, long long src_row0, int j0,
+                        int n, int slot, int ring, const int* path) {
+  const int per = row_bytes / int(sizeof(U));
+  for (int i = threadIdx.x; i < (n - j0) * per; i += kThreads) {
+    const int j = j0 + i / per, u = i % per;
+    int r = slot + j;                       // slot < ring, j < n: fold below
+    r %= ring;
+    static_cast<U*>(dst)[(dst_row0 + r) * per + u] = static_cast<const U*>(src)[(src_row0 + path[j]) * per + u];
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_constant__ TreeCommitArgs a) {
+  __shared__ int path[kMaxTreeTokens];
+  __shared__ int end_s;
+  const int seq = blockIdx.y, tid = threadIdx.x;
+  const int rank = int(cluster_rank()), ncta = int(cluster_size());
+  pdl_wait();
+  int* err = rank == 0 ? a.err : nullptr;
+  if (tid == 0) end_s = a.tokens;
+  int n = clamp_count(a.n_path[seq], a.tokens, tid == 0 ? err : nullptr);
+  int slot = a.head[seq];
+  if (slot < 0 || slot >= a.swa) {
+    if (tid == 0) report(err, kErrBadCount, slot);
+    slot = slot < 0 ? 0 : a.swa - 1;
+  }
+  const int fill = clamp_count(a.n_swa[seq], a.swa, tid == 0 ? err : nullptr);
+  __syncthreads();
+  if (tid < n) {
+    const int t = a.path[(long long)seq * a.tokens + tid];
+    path[tid] = t;
+    if (t < 0 || t >= a.tokens) {
+      report(err, kErrBadIndex, t);
+      atomicMin(&end_s, tid);
+    }
+  }
+  __syncthreads();
+  n = min(n, end_s);                         // a bad id ends the path before it
+  cluster_arrive();                          // this CTA has read the head and the fill count
+  const int j0 = max(0, n - a.swa);          // rows that a longer path would push out again are not written
+  const long long draft0 = (long long)seq * a.tokens, ring0 = (long long)seq * a.swa;
+  for (int l = rank; l < a.n_layers; l += ncta) {
+    const TreeCommitArgs::Slot& y = a.slot[l];
+    if (a.wide) {
+      copy_rows<uint4>(y.k_swa, y.k_draft, a.k_bytes, ring0, draft0, j0, n, slot, a.swa, path);
+      copy_rows<uint4>(y.v_swa, y.v_draft, a.v_bytes, ring0, draft0, j0, n, slot, a.swa, path);
+    } else {
+      copy_rows<uint16_t>(y.k_swa, y.k_draft, a.k_bytes, ring0, draft0, j0, n, slot, a.swa, path);
+      copy_rows<uint16_t>(y.v_swa, y.v_draft, a.v_bytes, ring0, draft0, j0, n, slot, a.swa, path);
+    }
+    if (a.mass == nullptr || y.weights == nullptr) continue;
+    unsigned long long* mass = a.mass + (long long)seq * a.n_entries;
+    for (int i = tid; i < n * a.topk; i += kThreads) {
+      const int j = i / a.topk;
+      const long long at = (draft0 + path[j]) * a.topk + (i - j * a.topk);
+      const int e = y.idx[at];
+      const float w = y.weights[at];
+      if (e < 0) continue;
+      if (e >= a.n_entries) {
+        report(a.err, kErrBadIndex, e);
+      } else if (!(w >= 0.f && w <= kMaxWeight)) {
+        report(a.err, kErrBadWeight, e);
+      } else {
+        const long long units = __double2ll_rn(double(w) * 4294967296.0);
+        if (units != 0) atomicAdd(mass + e, (unsigned long long)units);
+      }
+    }
+  }
+  cluster_wait();
+  if (rank == 0 && tid == 0) {
+    a.head[seq] = (slot + n) % a.swa;
+    a.n_swa[seq] = min(fill + n, a.swa);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, int seqs, cudaStream_t st) {
+  if (seqs == 0) return cudaSuccess;
+  const int c = a.n_layers < 8 ? a.n_layers : 8;   // a portable cluster: a CTA per layer, up to 8
+  note_launch();
+  return launch_pdl(tree_commit_kernel, dim3(unsigned(c), unsigned(seqs)), dim3(kThreads), 0, st, unsigned(c), a);
+}
+
+}  // namespace csa2

@@ -1,0 +1,224 @@
+"""Host-side checks of the drafted-tree operators (no GPU): the calls that the header refuses are refused before
+anything is enqueued (the fake pointers are never dereferenced), and the rotary frequencies against their formulas."""
+import ctypes
+import math
+
+import pytest
+
+from sparse_attention_decode_index_gb300 import build as B
+from sparse_attention_decode_index_gb300 import workloads as W
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, -1, -2, -3
+FAKE = 0x7f0000000000
+STEP = 1 << 36                      # fake arrays far apart
+MIS = FAKE + 8
+
+
+@pytest.fixture(scope="module")
+def csa2():
+    B.build()
+    from sparse_attention_decode_index_gb300 import csa2 as m
+    m.lib()
+    return m
+
+
+def _shape(csa2, **kw):
+    base = dict(batch=8, n_entries=4096, pool_blocks=0, tokens=4)
+    base.update(kw)
+    return csa2.c_shape(W.Shape(**base))
+
+
+def _ws(csa2, s):
+    return csa2.lib().csa2_workspace_bytes(ctypes.byref(s))
+
+
+def test_rope_freqs(csa2):
+    lib = csa2.lib()
+    buf = (ctypes.c_double * 512)()
+    mag = ctypes.c_float(0)
+
+    def call(rot=8, base=10000.0, kind=0, factor=1.0, ctx=0, fast=32.0, slow=1.0, out=buf):
+        return lib.csa2_rope_freqs(rot, base, kind, factor, ctx, fast, slow, ctypes.cast(out, ctypes.c_void_p) if out else None,
+                                   ctypes.byref(mag))
+
+    for bad in (dict(rot=0), dict(rot=7), dict(rot=-2), dict(rot=1026), dict(base=1.0), dict(base=math.nan), dict(base=math.inf),
+                dict(kind=4), dict(kind=-1), dict(kind=1, factor=0.5), dict(kind=1, factor=math.nan), dict(kind=2, rot=2, factor=2.0),
+                dict(kind=3, factor=2.0), dict(kind=3, factor=2.0, ctx=100, fast=1.0), dict(kind=3, factor=2.0, ctx=100, slow=0.0),
+                dict(out=None)):
+        assert call(**bad) == INVALID, bad
+    assert call() == OK and mag.value == 1.0
+    assert list(buf[:4]) == pytest.approx([1.0, 0.1, 0.01, 0.001], rel=1e-15)
+    assert call(kind=1, factor=4.0) == OK
+    assert list(buf[:4]) == pytest.approx([0.25, 0.025, 0.0025, 0.00025], rel=1e-15)
+    assert call(kind=2, factor=16.0) == OK                 # base 10000 * 16^(8/6)
+    b = 10000.0 * 16.0 ** (8.0 / 6.0)
+    assert list(buf[:4]) == pytest.approx([b ** (-i / 4.0) for i in range(4)], rel=1e-14)
+    # the slowest pair of the scaled base turns as the slowest of the plain one does at 1 / factor
+    assert buf[3] == pytest.approx(0.001 / 16.0, rel=1e-12)
+    assert call(rot=64, kind=3, factor=8.0, ctx=4096) == OK
+    assert mag.value == pytest.approx(0.1 * math.log(8.0) + 1.0, rel=1e-7)
+    for i in range(32):
+        f = 10000.0 ** (-i / 32.0)
+        turns = 4096 * f / (2 * math.pi)
+        if turns > 36:                                     # well above beta_fast: kept
+            assert buf[i] == pytest.approx(f, rel=1e-14)
+        elif turns < 0.75:                                 # well below beta_slow: scaled
+            assert buf[i] == pytest.approx(f / 8.0, rel=1e-14)
+        else:
+            assert f / 8.0 * (1 - 1e-12) <= buf[i] <= f * (1 + 1e-12)
+    assert all(buf[i] > buf[i + 1] for i in range(31))
+
+
+def test_rope_refusals(csa2):
+    lib = csa2.lib()
+    good = dict(x=FAKE, out=FAKE + STEP, heads=64, dim=192, rot_off=128, dtype=0)
+
+    def call(slots=(good,), n=None, rows=4, rot=64, inter=0, pos=FAKE + 4 * STEP, freqs=FAKE + 5 * STEP, mag=1.0, inv=0):
+        arr = (csa2.CRopeSlot * max(1, len(slots)))(*[csa2.CRopeSlot(*[y[k] for k in ("x", "out", "heads", "dim", "rot_off", "dtype")])
+                                                      for y in slots])
+        return lib.csa2_rope(ctypes.cast(arr, ctypes.c_void_p), len(slots) if n is None else n, rows, rot, inter, pos, freqs, mag,
+                             inv, None)
+
+    for bad in (dict(n=0), dict(n=17), dict(rows=0), dict(rows=-1), dict(rot=0), dict(rot=63), dict(inter=2), dict(inv=-1), dict(pos=None),
+                dict(freqs=None), dict(freqs=FAKE + 5 * STEP + 4), dict(mag=0.0), dict(mag=-1.0), dict(mag=math.nan), dict(mag=math.inf),
+                dict(rot=66)):
+        assert call(**bad) == INVALID, bad
+    for bad in (dict(x=None), dict(out=None), dict(heads=0), dict(dim=0), dict(rot_off=-1), dict(rot_off=129), dict(dtype=2),
+                dict(out=FAKE + 2),                        # overlaps its input without being it
+                dict(out=FAKE + 4 * STEP), dict(out=FAKE + 5 * STEP)):   # the positions, the frequencies
+        assert call(slots=({**good, **bad},)) == INVALID, bad
+    assert call(slots=({**good, "heads": 1025},)) == UNSUPPORTED
+    assert call(slots=({**good, "dim": 1025},)) == UNSUPPORTED
+    assert call(rot=1026, slots=({**good, "dim": 1026, "rot_off": 0},)) == UNSUPPORTED
+    other = dict(good, x=FAKE + 2 * STEP)
+    assert call(slots=(good, other)) == INVALID            # one output twice
+    assert call(slots=(good, dict(other, out=FAKE))) == INVALID   # over another slot's input
+
+
+def _tree_args(**kw):
+    names = ("q", "k_main", "v_main", "idx", "k_swa", "v_swa", "swa_head", "n_swa", "k_draft", "v_draft", "parent", "n_draft", "out",
+             "lse")
+    d = {n: FAKE + i * STEP for i, n in enumerate(names)}
+    d.update(kw)
+    return [d[n] for n in names]
+
+
+def test_tree_attn_refusals(csa2):
+    lib = csa2.lib()
+    s = _shape(csa2)
+
+    def call(s=s, ws=FAKE, nbytes=None, **kw):
+        n = _ws(csa2, s) if nbytes is None else nbytes
+        return lib.csa2_tree_attn(ctypes.byref(s), *_tree_args(**kw), ws, n, None)
+
+    for n in ("q", "k_main", "v_main", "idx", "k_swa", "v_swa", "n_swa", "k_draft", "v_draft", "out"):
+        assert call(**{n: None}) == INVALID, n
+    for n in ("q", "k_main", "v_main", "k_swa", "v_swa", "k_draft", "v_draft", "out"):
+        assert call(**{n: MIS}) == INVALID, n
+    assert call(nbytes=_ws(csa2, s) - 1) == WORKSPACE
+    assert call(ws=None) == WORKSPACE and call(ws=FAKE + 16) == WORKSPACE
+    assert call(s=_shape(csa2, swa=0)) == INVALID
+    assert call(s=_shape(csa2, batch=129, tokens=129)) == UNSUPPORTED
+    assert call(s=_shape(csa2, batch=65536, n_entries=1, topk=1, swa=1)) == UNSUPPORTED
+    bad = _shape(csa2)
+    bad.batch = 6                                          # not whole sequences of 4 tokens
+    assert lib.csa2_tree_attn(ctypes.byref(bad), *_tree_args(), FAKE, 1 << 30, None) == INVALID
+    assert lib.csa2_tree_attn(None, *_tree_args(), FAKE, 1 << 30, None) == INVALID
+
+
+def test_attn_weights_refusals(csa2):
+    lib = csa2.lib()
+    s = _shape(csa2)
+
+    def call(s=s, ws=FAKE, nbytes=None, **kw):
+        d = dict(q=FAKE, k_main=FAKE, idx=FAKE, lse=FAKE, live=None, weights=FAKE)
+        d.update(kw)
+        return lib.csa2_attn_weights(ctypes.byref(s), *d.values(), ws, _ws(csa2, s) if nbytes is None else nbytes, None)
+
+    for n in ("q", "k_main", "idx", "lse", "weights"):
+        assert call(**{n: None}) == INVALID, n
+    assert call(q=MIS) == INVALID and call(k_main=MIS) == INVALID
+    assert call(nbytes=0) == WORKSPACE and call(ws=None) == WORKSPACE
+    assert call(s=_shape(csa2, batch=65536, n_entries=1, topk=1, swa=1)) == UNSUPPORTED
+
+
+def test_tree_commit_refusals(csa2):
+    lib = csa2.lib()
+    s = _shape(csa2)
+    slot = (FAKE, FAKE, FAKE, FAKE, FAKE, FAKE)
+
+    def call(s=s, slots=(slot,), n=None, ws=FAKE, nbytes=None, **kw):
+        d = dict(path=FAKE, n_path=FAKE, head=FAKE, n_swa=FAKE, mass=FAKE)
+        d.update(kw)
+        arr = (csa2.CTreeSlot * max(1, len(slots)))(*[csa2.CTreeSlot(*y) for y in slots])
+        return lib.csa2_tree_commit(ctypes.byref(s), ctypes.cast(arr, ctypes.c_void_p), len(slots) if n is None else n, *d.values(),
+                                    ws, _ws(csa2, s) if nbytes is None else nbytes, None)
+
+    for n in ("path", "n_path", "head", "n_swa"):
+        assert call(**{n: None}) == INVALID, n
+    assert call(n=0) == INVALID and call(n=65) == INVALID and call(mass=FAKE + 4) == INVALID
+    for i in range(4):
+        assert call(slots=(slot, slot[:i] + (None,) + slot[i + 1:])) == INVALID
+    assert call(slots=(slot[:4] + (None, FAKE),)) == INVALID and call(slots=(slot[:4] + (FAKE, None),)) == INVALID
+    assert call(s=_shape(csa2, swa=0)) == INVALID
+    assert call(s=_shape(csa2, batch=129, tokens=129)) == UNSUPPORTED
+    assert call(nbytes=8) == WORKSPACE
+
+
+def test_kv_evict_refusals(csa2):
+    lib = csa2.lib()
+    s = _shape(csa2, tokens=1)
+    names = ("k", "v", "x", "mass", "n", "ko", "vo", "xo", "masso", "no", "kept", "kb")
+
+    def call(s=s, trigger=4000, keep=3000, sink=4, recent=64, rnd=1, ws=FAKE, nbytes=None, **kw):
+        d = {n: FAKE + i * STEP for i, n in enumerate(names)}
+        d.update(kw)
+        return lib.csa2_kv_evict(ctypes.byref(s), trigger, keep, sink, recent, *d.values(), rnd, ws,
+                                 _ws(csa2, s) if nbytes is None else nbytes, None)
+
+    for n in names[:-1]:
+        assert call(**{n: None}) == INVALID, n
+    for bad in (dict(keep=0), dict(trigger=2999), dict(trigger=4097), dict(sink=-1), dict(recent=-1), dict(sink=2000, recent=1001),
+                dict(sink=3001, recent=0), dict(rnd=2), dict(mass=FAKE + 3 * STEP + 4), dict(masso=FAKE + 8 * STEP + 4)):
+        assert call(**bad) == INVALID, bad
+    at = {n: FAKE + i * STEP for i, n in enumerate(names)}
+    assert call(ko=at["k"]) == INVALID                     # in place for one array only
+    assert call(ko=at["k"] + 16) == INVALID                # overlaps its input
+    assert call(ko=at["v"]) == INVALID and call(kept=at["k"]) == INVALID and call(kb=at["xo"]) == INVALID
+    assert call(kb=at["kept"] + 4) == INVALID and call(vo=at["ko"]) == INVALID
+    assert call(s=_shape(csa2, tokens=4)) == UNSUPPORTED
+    assert call(nbytes=16) == WORKSPACE
+    assert call(ws=FAKE + 16) == WORKSPACE
+
+
+def test_binding_refuses_tensors_that_do_not_fit(csa2):
+    torch = pytest.importorskip("torch")
+    cpu = torch.zeros(4, 192)
+    with pytest.raises(ValueError, match="CUDA"):
+        csa2.rope([(cpu, cpu, 0)], torch.zeros(4, dtype=torch.int32), torch.zeros(8, dtype=torch.float64))
+    with pytest.raises(ValueError, match="x must be"):
+        csa2.rope([(cpu.half(), cpu.half(), 0)], torch.zeros(4, dtype=torch.int32), torch.zeros(8, dtype=torch.float64))
+    with pytest.raises(ValueError, match="scaling"):
+        csa2.rope_freqs(64, scaling="other", device="cpu")
+    f, mag = csa2.rope_freqs(64, scaling="linear", factor=2.0, device="cpu")
+    assert f.dtype == torch.float64 and tuple(f.shape) == (32,) and mag == 1.0
+
+    class Fake(torch.Tensor):                              # a CUDA tensor as far as the checks look
+        is_cuda = True
+
+        def data_ptr(self):
+            return FAKE
+
+    t = torch.zeros(4, 3, dtype=torch.int32).as_subclass(Fake)
+    assert csa2._arr(t, torch.int32, (4, 3), "t") == FAKE
+    with pytest.raises(ValueError, match="shape"):
+        csa2._arr(t, torch.int32, (4, 4), "t")
+    with pytest.raises(TypeError, match="int32|float32"):
+        csa2._arr(t, torch.float32, (4, 3), "t")
+    with pytest.raises(ValueError, match="contiguous"):
+        csa2._arr(t[:, ::2], torch.int32, (4, 2), "t")
+    with pytest.raises(ValueError, match="is on"):
+        csa2._arr(t, torch.int32, (4, 3), "t", torch.device("cuda", 1))
+    with pytest.raises(TypeError, match="missing"):
+        csa2._arr(None, torch.int32, (4, 3), "t")
+    assert csa2._arr(None, torch.int32, (4, 3), "t", optional=True) is None

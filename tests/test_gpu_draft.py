@@ -1,0 +1,642 @@
+"""The operators around drafted tokens (csa2_rope, csa2_tree_attn, csa2_attn_weights, csa2_tree_commit, csa2_kv_evict)
+on the GPU against plain 64-bit definitions, alone and as a serving step runs them together."""
+import types
+
+import numpy as np
+import pytest
+
+from tests import draft_reference as R
+from tests.gpu_helpers import assert_no_device_error, lib_ready, need_gpu, torch
+
+pytestmark = pytest.mark.gpu
+
+BAD_INDEX, BAD_COUNT, BAD_WEIGHT = 1, 2, 16
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}   # half a rounding step, relative
+EPS32 = 2.0 ** -23
+
+
+@pytest.fixture(scope="module")
+def csa2():
+    need_gpu()
+    return lib_ready()
+
+
+def shape(batch, **kw):
+    d = dict(batch=batch, n_entries=64, idx_heads=8, idx_dim=64, block=8, pool_blocks=0, topk=512, q_heads=64, k_dim=192,
+             v_dim=128, swa=128, scale=0.0, relu=1, dtype="bf16", tokens=1)
+    d.update(kw)
+    return types.SimpleNamespace(**d)
+
+
+def randn(g, size, dtype, div=1.0):
+    return (torch.randn(size, generator=g) / div).to(dtype).cuda()
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x, dtype=np.int32)).cuda()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+# ------------------------------------------------------------------ rotary positions
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("rows,heads,dim,rot,off,inverse", [
+    (1, 1, 2, 2, 0, False), (3, 64, 192, 64, 128, False), (5, 8, 64, 64, 0, True), (17, 3, 40, 8, 32, False),
+    (2, 5, 10, 6, 3, True), (700, 4, 96, 16, 0, False), (4, 128, 1024, 1024, 0, False), (9, 2, 24, 12, 8, True)])
+def test_rope_matches_definition(csa2, dtype, inter, rows, heads, dim, rot, off, inverse):
+    g = torch.Generator().manual_seed(rows * 31 + dim)
+    x = randn(g, (rows, heads, dim), dtype)
+    k = randn(g, (rows, dim), dtype)
+    pos = torch.randint(0, 2 ** 20, (rows,), generator=g, dtype=torch.int32)
+    pos[0] = 2 ** 31 - 1
+    if rows > 2:
+        pos[1], pos[2] = -12345, 0
+    freqs, mag = csa2.rope_freqs(rot, 10000.0, scaling="yarn", factor=8.0, orig_ctx=4096)
+    out, ko = torch.full_like(x, 7.0), torch.full_like(k, 7.0)
+    csa2.rope([(x, out, off), (k, ko, off)], pos.cuda(), freqs, mag=mag, interleaved=inter, inverse=inverse)
+    t = pos.numpy().astype(np.longdouble)[:, None] * freqs.cpu().numpy().astype(np.longdouble)[None]
+    m = 1.0 / mag if inverse else mag
+    c, s = np.cos(t) * m, np.sin(t) * (-m if inverse else m)
+    for src, dst in ((x, out), (k[:, None], ko[:, None])):
+        want = f64(src)
+        r = want[..., off:off + rot].copy()
+        a, b = (r[..., 0::2], r[..., 1::2]) if inter else (r[..., :rot // 2], r[..., rot // 2:])
+        u, v = a * c[:, None] - b * s[:, None], b * c[:, None] + a * s[:, None]
+        turned = np.empty_like(r)
+        if inter:
+            turned[..., 0::2], turned[..., 1::2] = u, v
+        else:
+            turned[..., :rot // 2], turned[..., rot // 2:] = u, v
+        want[..., off:off + rot] = turned
+        # the angle: 2^-52 of it from the frequency's rounding, 2^-25 turns in fp32; cos and sin 2 ulp; three roundings
+        angle = np.abs(t).max() * 2.0 ** -51 + 2 * np.pi * 2.0 ** -25
+        tol = (np.abs(a) + np.abs(b)) * m * (float(angle) + 2.5 * EPS32)
+        tol = np.concatenate([tol, tol], -1) if not inter else np.repeat(tol, 2, -1)
+        err = np.abs(f64(dst) - want)
+        lim = np.zeros_like(want)
+        lim[..., off:off + rot] = tol.astype(np.float64) + HALF[dtype] * np.abs(turned) * 1.01
+        assert np.all(err <= lim), float((err - lim).max())
+
+
+@pytest.mark.parametrize("dtype,dim,rot,off", [(torch.bfloat16, 192, 64, 128), (torch.float32, 20, 6, 5)])
+def test_rope_in_place_equals_out_of_place_and_turns_back(csa2, dtype, dim, rot, off):
+    g = torch.Generator().manual_seed(3)
+    x = randn(g, (33, 16, dim), dtype)
+    pos = torch.randint(0, 100000, (33,), generator=g, dtype=torch.int32).cuda()
+    freqs, _ = csa2.rope_freqs(rot, 500000.0, scaling="ntk", factor=4.0)
+    out, y = torch.empty_like(x), x.clone()
+    csa2.rope([(x, out, off)], pos, freqs, mag=1.25)
+    csa2.rope([(y, y, off)], pos, freqs, mag=1.25)
+    assert torch.equal(out, y)
+    csa2.rope([(y, y, off)], pos, freqs, mag=1.25, inverse=True)
+    # two roundings to the type, each half a step of values up to 1.25 (|a| + |b|), and fp32 arithmetic
+    lim = 3 * HALF[dtype] * float(x.abs().max()) * 2 * 1.25 + 1e-5
+    assert float((y.float() - x.float()).abs().max()) <= lim
+    assert torch.equal(y[..., :off], x[..., :off]) and torch.equal(y[..., off + rot:], x[..., off + rot:])
+
+
+def test_rope_unaligned_tensors_and_offsets(csa2):
+    g = torch.Generator().manual_seed(5)
+    freqs, _ = csa2.rope_freqs(16)
+    pos = i32(np.arange(6) * 1000)
+    whole = randn(g, (6 * 8 * 32 + 1,), torch.bfloat16)
+    x = whole[1:].view(6, 8, 32)                       # two bytes behind a 16-byte boundary
+    a, b = torch.empty_like(x), torch.empty(6 * 8 * 32, dtype=torch.bfloat16, device="cuda").view(6, 8, 32)
+    csa2.rope([(x, a, 16)], pos, freqs)
+    csa2.rope([(x.clone(), b, 16)], pos, freqs)
+    assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ tree attention
+
+def make_parents(rng, S, T, roots=1):
+    p = np.full((S, T), -1)
+    for s in range(S):
+        for t in range(min(roots, T), T):
+            p[s, t] = rng.integers(max(0, t - 5), t)
+    return p
+
+
+def tree_inputs(sh, seed, fill=None, holes=0.0, roots=1, spread=4.0):
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    dt = torch.float32 if sh.dtype == "f32" else torch.bfloat16
+    B, T, N, W, K = sh.batch, sh.tokens, sh.n_entries, sh.swa, sh.topk
+    S = B // T
+    d = types.SimpleNamespace(dt=dt)
+    d.q = randn(g, (B, sh.q_heads, sh.k_dim), dt)
+    d.k_main, d.v_main = randn(g, (S, N, sh.k_dim), dt, np.sqrt(sh.k_dim) / spread), randn(g, (S, N, sh.v_dim), dt)
+    d.k_swa, d.v_swa = randn(g, (S, W, sh.k_dim), dt, np.sqrt(sh.k_dim) / spread), randn(g, (S, W, sh.v_dim), dt)
+    d.k_draft, d.v_draft = randn(g, (S, T, sh.k_dim), dt, np.sqrt(sh.k_dim) / spread), randn(g, (S, T, sh.v_dim), dt)
+    idx = np.full((B, K), -1)
+    for b in range(B):
+        n = min(K, N) if holes == 0.0 else int(rng.integers(0, min(K, N) + 1))
+        idx[b, :n] = np.sort(rng.choice(N, n, replace=False))
+    d.idx = i32(idx)
+    n_swa = rng.integers(0, W + 1, S) if fill is None else np.full(S, fill)
+    d.n_swa = i32(n_swa)
+    d.head = i32(np.where(n_swa == W, rng.integers(0, W, S), n_swa))
+    d.parent = i32(make_parents(rng, S, T, roots))
+    d.out = torch.full((B, sh.q_heads, sh.v_dim), 9.0, dtype=dt, device="cuda")
+    d.lse = torch.full((B, sh.q_heads), 9.0, device="cuda")
+    return d
+
+
+def run_tree(csa2, sh, d, n_draft=None, parent="own", head="own"):
+    ws = csa2.workspace(sh)
+    p = d.parent if isinstance(parent, str) else parent
+    h = d.head if isinstance(head, str) else head
+    csa2.tree_attn(sh, d.q, d.k_main, d.v_main, d.idx, d.k_swa, d.v_swa, d.n_swa, d.k_draft, d.v_draft, d.out, ws,
+                   swa_head=h, parent=p, n_draft=n_draft, lse=d.lse)
+    return ws
+
+
+def check_tree(sh, d, n_draft=None, parent=None, head=None):
+    S = sh.batch // sh.tokens
+    par = d.parent.cpu().numpy() if parent is None else parent
+    hd = d.head.cpu().numpy() if head is None else head
+    scale = sh.scale if sh.scale > 0 else 1.0 / np.sqrt(sh.k_dim)
+    out, lse, absum, dot = R.tree_attention(f64(d.q), f64(d.k_main), f64(d.v_main), d.idx.cpu().numpy(), f64(d.k_swa),
+                                            f64(d.v_swa), d.n_swa.cpu().numpy(), f64(d.k_draft), f64(d.v_draft), par,
+                                            None if n_draft is None else n_draft.cpu().numpy(), hd, scale, sh.tokens)
+    assert par.shape == (S, sh.tokens)
+    got, gl = f64(d.out), f64(d.lse)
+    empty = np.isneginf(lse)
+    assert np.array_equal(np.isneginf(gl), empty)
+    assert np.all(got[empty] == 0.0)
+    # a logit: k_dim products summed in fp32, each addition half a step of at most the sum of |q k|
+    logit = dot * (sh.k_dim + 4) * 2.0 ** -24
+    # exp and log within 4 steps of a value up to |lse|, the sum of up to 1024 terms in fp32
+    tol = 2 * logit + 8 * EPS32 * (1.0 + np.abs(lse[~empty])) + 64 * 2.0 ** -24
+    assert np.all(np.abs(gl[~empty] - lse[~empty]) <= tol), float(np.abs(gl[~empty] - lse[~empty]).max())
+    # a weight: twice the logit's error (itself and the sum), bf16: half a step of rounding; the output's own rounding
+    rel = 4 * logit + 64 * EPS32 + (HALF[torch.bfloat16] if d.dt == torch.bfloat16 else 0.0) + sh.swa * 2.0 ** -24 + 512 * 2.0 ** -24
+    lim = absum * rel * 1.01 + HALF[d.dt] * np.abs(out) * 1.01 + 1e-30
+    err = np.abs(got - out)
+    assert np.all(err <= lim), (float(err.max()), float((err - lim).max()))
+
+
+FAST = dict(q_heads=64, k_dim=192, v_dim=128, dtype="bf16")
+
+
+@pytest.mark.parametrize("S,T,N,K,W,roots,holes", [
+    (1, 1, 40, 1, 1, 1, 0.0), (1, 8, 600, 512, 128, 1, 0.0), (3, 7, 700, 512, 128, 2, 1.0), (2, 33, 300, 99, 37, 1, 1.0),
+    (1, 128, 64, 40, 128, 3, 0.0), (5, 2, 513, 512, 4, 1, 0.0), (65, 1, 96, 64, 16, 1, 1.0), (2, 64, 1024, 512, 8, 1, 0.0),
+    (20, 16, 600, 512, 128, 2, 1.0), (1, 3, 1200, 1000, 24, 1, 0.0)])
+def test_tree_attention_fast_path(csa2, S, T, N, K, W, roots, holes):
+    sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, **FAST)
+    d = tree_inputs(sh, S * 1000 + T, holes=holes, roots=roots)
+    ws = run_tree(csa2, sh, d)
+    assert_no_device_error(csa2, ws)
+    check_tree(sh, d)
+
+
+@pytest.mark.parametrize("H,dk,dv,dtype", [(4, 16, 16, "f32"), (1, 1, 1, "f32"), (16, 64, 72, "bf16"), (40, 100, 33, "f32"),
+                                           (9, 192, 128, "bf16"), (3, 1024, 1024, "bf16"), (64, 192, 128, "f32")])
+@pytest.mark.parametrize("S,T,N,K,W", [(2, 5, 50, 33, 7), (1, 1, 9, 3, 4)])
+def test_tree_attention_any_shape(csa2, H, dk, dv, dtype, S, T, N, K, W):
+    sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, q_heads=H, k_dim=dk, v_dim=dv, dtype=dtype)
+    d = tree_inputs(sh, H * 7 + T, holes=1.0)
+    ws = run_tree(csa2, sh, d)
+    assert_no_device_error(csa2, ws)
+    check_tree(sh, d)
+
+
+@pytest.mark.parametrize("kind", ["fast", "generic"])
+@pytest.mark.parametrize("fill", [0, 1, 15, 16])
+def test_tree_window_edges_and_chains(csa2, kind, fill):
+    """Windows that are empty, filling and full, chains longer than the window, no parents and no heads given."""
+    kw = FAST if kind == "fast" else dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32")
+    T = 24
+    sh = shape(2 * T, tokens=T, n_entries=80, topk=20, swa=16, **kw)
+    d = tree_inputs(sh, 50 + fill, fill=fill)
+    chain = np.tile(np.arange(T) - 1, (2, 1))
+    run_tree(csa2, sh, d, parent=None)
+    check_tree(sh, d, parent=chain)
+    run_tree(csa2, sh, d, parent=i32(chain), head=None)
+    check_tree(sh, d, parent=chain, head=np.zeros(2, dtype=int))
+
+
+@pytest.mark.parametrize("kind", ["fast", "generic"])
+def test_tree_rows_without_keys_and_dead_tokens(csa2, kind):
+    kw = FAST if kind == "fast" else dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32")
+    sh = shape(3 * 6, tokens=6, n_entries=70, topk=40, swa=9, **kw)
+    d = tree_inputs(sh, 77, holes=1.0)
+    n_draft = i32([6, 1, 4])
+    # what a dead token or an unused row holds must not matter
+    nan = float("nan")
+    for s, n in enumerate([6, 1, 4]):
+        d.k_draft[s, n:], d.v_draft[s, n:] = nan, nan
+        d.idx[s * 6 + n:(s + 1) * 6] = -1
+        d.k_swa[s, int(d.n_swa[s]):], d.v_swa[s, int(d.n_swa[s]):] = nan, nan
+        used = set(d.idx[s * 6:(s + 1) * 6].flatten().tolist())
+        free = [e for e in range(70) if e not in used]
+        d.k_main[s, free], d.v_main[s, free] = nan, float("inf")
+    d.q.view(3, 6, sh.q_heads, -1)[1, 1:] = nan
+    ws = run_tree(csa2, sh, d, n_draft=n_draft)
+    assert_no_device_error(csa2, ws)
+    check_tree(sh, d, n_draft=n_draft)
+    assert torch.isinf(d.lse.view(3, 6, -1)[1, 1:]).all() and (d.out.view(3, 6, -1)[1, 1:] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["fast", "generic"])
+def test_tree_bad_inputs_are_recorded(csa2, kind):
+    kw = FAST if kind == "fast" else dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32")
+    sh = shape(2 * 4, tokens=4, n_entries=30, topk=10, swa=6, **kw)
+    d = tree_inputs(sh, 9, fill=6)
+    d.idx[3, 2] = 30                                       # an entry behind the cache
+    ws = run_tree(csa2, sh, d)
+    assert csa2.read_device_error(ws) == (-5, BAD_INDEX)
+    check_tree(sh, d)
+    d.idx[3, 2] = -7
+    d.parent[1] = i32([-1, 1, 5, -9])                      # not earlier tokens: roots
+    ws = run_tree(csa2, sh, d)
+    assert csa2.read_device_error(ws) == (-5, BAD_INDEX)
+    check_tree(sh, d)
+    d.parent[1] = i32([-1, 0, 0, 1])
+    d.n_swa[0] = 99                                        # clamped to the window
+    d.head[1] = 6                                          # clamped to its last row
+    ws = run_tree(csa2, sh, d)
+    assert csa2.read_device_error(ws) == (-5, BAD_COUNT)
+    d.n_swa[0], d.head[1] = 6, 5
+    check_tree(sh, d)
+
+
+def test_tree_repeated_entries_count_each_time(csa2):
+    """The same index twice, and lists that do not ascend: as in csa2_sparse_attn."""
+    sh = shape(2 * 4, tokens=4, n_entries=64, topk=48, swa=8, **FAST)
+    d = tree_inputs(sh, 13)
+    rng = np.random.default_rng(4)
+    d.idx.copy_(i32(rng.integers(-1, 64, (8, 48))))
+    ws = run_tree(csa2, sh, d)
+    assert_no_device_error(csa2, ws)
+    check_tree(sh, d)
+
+
+def test_tree_large_logits(csa2):
+    sh = shape(2 * 6, tokens=6, n_entries=600, topk=512, swa=128, **FAST)
+    d = tree_inputs(sh, 21, spread=400.0)
+    run_tree(csa2, sh, d)
+    assert torch.isfinite(d.out).all() and torch.isfinite(d.lse).all()
+    out, lse, _, dot = R.tree_attention(f64(d.q), f64(d.k_main), f64(d.v_main), d.idx.cpu().numpy(), f64(d.k_swa), f64(d.v_swa),
+                                        d.n_swa.cpu().numpy(), f64(d.k_draft), f64(d.v_draft), d.parent.cpu().numpy(), None,
+                                        d.head.cpu().numpy(), 1 / np.sqrt(192), 6)
+    assert np.abs(f64(d.lse) - lse).max() <= dot * 196 * 2.0 ** -24 + 8 * EPS32 * np.abs(lse).max()
+
+
+def test_chain_equals_steps_of_append_and_attention(csa2):
+    """A chain of T drafted tokens gives what T steps of swa_append and sparse_attn give."""
+    S, T, W = 3, 6, 8
+    sh = shape(S * T, tokens=T, n_entries=200, topk=64, swa=W, **FAST)
+    one = shape(S, n_entries=200, topk=64, swa=W, **FAST)
+    d = tree_inputs(sh, 31, fill=5)
+    run_tree(csa2, sh, d, parent=None)
+    ws = csa2.workspace(one)
+    ks, vs, head, n = d.k_swa.clone(), d.v_swa.clone(), d.head.clone(), d.n_swa.clone()
+    pick = lambda x, t: x.view(S, T, *x.shape[1:])[:, t].contiguous()  # noqa: E731
+    for t in range(T):
+        csa2.swa_append(one, [(d.k_draft[:, t].contiguous(), d.v_draft[:, t].contiguous(), ks, vs)], head, n, ws)
+        out = torch.empty((S, 64, 128), device="cuda")
+        lse = torch.empty((S, 64), device="cuda")
+        csa2.sparse_attn(one, pick(d.q, t), d.k_main, d.v_main, pick(d.idx, t), ks, vs, n, out, ws, lse=lse)
+        # the same keys in another order: a bf16 rounding of each weight on both sides, then of the output
+        assert float((pick(d.lse, t) - lse).abs().max()) <= 2e-5
+        lim = 2.0 ** -8 * (2 * float(d.v_main.abs().max()) + out.abs()) + 1e-5
+        assert bool(((pick(d.out, t).float() - out).abs() <= lim).all())
+    # and committing the whole chain leaves the windows that the steps left
+    kt, vt, ht, nt = d.k_swa.clone(), d.v_swa.clone(), d.head.clone(), d.n_swa.clone()
+    path = i32(np.tile(np.arange(T), (S, 1)))
+    csa2.tree_commit(sh, [(d.k_draft, d.v_draft, kt, vt, None, None)], path, i32([T] * S), ht, nt, None)
+    assert torch.equal(kt, ks) and torch.equal(vt, vs) and torch.equal(ht, head) and torch.equal(nt, n)
+
+
+# ------------------------------------------------------------------ attention weights
+
+@pytest.mark.parametrize("H,dk,dtype", [(64, 192, "bf16"), (5, 24, "f32"), (16, 64, "bf16"), (1, 1, "f32"), (12, 1024, "bf16")])
+@pytest.mark.parametrize("S,T,N,K", [(1, 1, 5, 1), (2, 3, 300, 130), (1, 2, 700, 512)])
+def test_attention_weights(csa2, H, dk, dtype, S, T, N, K):
+    sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=4, q_heads=H, k_dim=dk, v_dim=16, dtype=dtype)
+    d = tree_inputs(sh, 5 + H, holes=1.0)
+    g = torch.Generator().manual_seed(1)
+    lse = (torch.randn((S * T, H), generator=g) * 0.1 + np.log(K + 1.0)).cuda()
+    lse[0, 0] = float("-inf")
+    w = torch.full((S * T, K), 9.0, device="cuda")
+    ws = csa2.workspace(sh)
+    csa2.attn_weights(sh, d.q, d.k_main, d.idx, lse, w, ws)
+    assert_no_device_error(csa2, ws)
+    scale = 1 / np.sqrt(dk)
+    want = R.attention_weights(f64(d.q), f64(d.k_main), d.idx.cpu().numpy(), f64(lse), scale, T)
+    dot = float((np.abs(f64(d.q)).max(0).max(0) @ np.abs(f64(d.k_main)).reshape(-1, dk).max(0))) * scale
+    # logits' fp32 sums, lse * log2(e) and the exponential's argument rounded, the heads added up
+    rel = dot * (dk + 4) * 2.0 ** -24 + 16 * EPS32 * (4 + np.log(K + 1.0)) + H * 2.0 ** -24
+    assert np.all(np.abs(f64(w) - want) <= want * rel + 1e-30)
+    live = i32([1] * (S * T))
+    live[0] = 0
+    w2 = torch.full_like(w, 9.0)
+    csa2.attn_weights(sh, d.q, d.k_main, d.idx, lse, w2, ws, live=live)
+    assert (w2[0] == 0).all() and torch.equal(w2[1:], w[1:])
+
+
+def test_attention_weights_of_a_whole_row_sum_to_the_heads(csa2):
+    """With the window empty and one token, an attention's weights add up to the head count, less the token's own."""
+    sh = shape(4, n_entries=600, topk=512, swa=128, **FAST)
+    d = tree_inputs(sh, 8, fill=0)
+    ws = run_tree(csa2, sh, d)
+    w = torch.empty((4, 512), device="cuda")
+    csa2.attn_weights(sh, d.q, d.k_main, d.idx, d.lse, w, ws)
+    own = torch.exp((d.q.double() * d.k_draft.double()).sum(-1) / np.sqrt(192) - d.lse.double()).sum(1)
+    assert float((w.double().sum(1) + own - 64).abs().max()) <= 64 * 1e-4
+    d.idx[2, 5] = 600
+    csa2.attn_weights(sh, d.q, d.k_main, d.idx, d.lse, w, ws)
+    assert csa2.read_device_error(ws) == (-5, BAD_INDEX) and float(w[2, 5]) == 0.0
+
+
+# ------------------------------------------------------------------ commit
+
+def commit_inputs(S, T, L, N, K, W, dk, dv, dtype, seed):
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, k_dim=dk, v_dim=dv, dtype=dtype)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    d = types.SimpleNamespace(sh=sh)
+    d.kd, d.vd = randn(g, (L, S, T, dk), dt), randn(g, (L, S, T, dv), dt)
+    d.ks, d.vs = randn(g, (L, S, W, dk), dt), randn(g, (L, S, W, dv), dt)
+    d.idx = i32(rng.integers(-1, N, (L, S * T, K)))         # unsorted, entries repeated
+    d.w = torch.rand((L, S * T, K), generator=g).cuda()
+    d.path = i32(np.stack([rng.permutation(T) for _ in range(S)]))
+    d.n_path = i32(rng.integers(0, T + 1, S))
+    n_swa = rng.integers(0, W + 1, S)
+    d.n_swa, d.head = i32(n_swa), i32(np.where(n_swa == W, rng.integers(0, W, S), n_swa % W))
+    d.mass = torch.randint(0, 2 ** 40, (S, N), generator=g).cuda()
+    return d
+
+
+def commit_reference(d, L, S, T, W, N):
+    ks, vs, mass = d.ks.cpu().clone(), d.vs.cpu().clone(), d.mass.cpu().numpy().copy()
+    head, n = d.head.cpu().numpy().copy(), d.n_swa.cpu().numpy().copy()
+    idx, w = d.idx.cpu().numpy(), d.w.cpu().numpy()
+    for s in range(S):
+        for i in range(int(d.n_path[s])):
+            t = int(d.path[s, i])
+            if not 0 <= t < T:
+                break
+            for l in range(L):
+                ks[l, s, head[s]], vs[l, s, head[s]] = d.kd[l, s, t].cpu(), d.vd[l, s, t].cpu()
+                for j in range(idx.shape[2]):
+                    e, x = idx[l, s * T + t, j], float(w[l, s * T + t, j])
+                    if 0 <= e < N and 0 <= x <= 2 ** 20:
+                        mass[s, e] += int(np.rint(np.float64(x) * 2.0 ** 32))
+            head[s] = (head[s] + 1) % W
+            n[s] = min(n[s] + 1, W)
+    return ks, vs, mass, head, n
+
+
+@pytest.mark.parametrize("S,T,L,N,K,W,dk,dv,dtype", [
+    (1, 1, 1, 9, 3, 1, 192, 128, "bf16"), (4, 8, 4, 200, 64, 16, 192, 128, "bf16"), (3, 20, 11, 50, 30, 7, 24, 12, "f32"),
+    (2, 128, 2, 40, 5, 37, 5, 3, "bf16"), (7, 3, 64, 33, 4, 8, 8, 8, "bf16")])
+def test_tree_commit(csa2, S, T, L, N, K, W, dk, dv, dtype):
+    d = commit_inputs(S, T, L, N, K, W, dk, dv, dtype, S * 10 + T)
+    want = commit_reference(d, L, S, T, W, N)
+    ws = csa2.workspace(d.sh)
+    slots = [(d.kd[l], d.vd[l], d.ks[l], d.vs[l], d.idx[l], d.w[l]) for l in range(L)]
+    csa2.tree_commit(d.sh, slots, d.path, d.n_path, d.head, d.n_swa, ws, mass=d.mass)
+    assert_no_device_error(csa2, ws)
+    for got, ref in zip((d.ks, d.vs, d.mass, d.head, d.n_swa), want):
+        assert torch.equal(got.cpu(), torch.as_tensor(ref))
+
+
+def test_tree_commit_bad_inputs(csa2):
+    S, T, L, N, K, W = 3, 4, 2, 20, 6, 5
+    d = commit_inputs(S, T, L, N, K, W, 16, 8, "bf16", 3)
+    d.n_path.copy_(i32([4, 4, 3]))
+    d.path[1, 2] = 4                                       # ends the path behind two tokens
+    d.w[0, 0, 0], d.w[0, 0, 1], d.w[1, 0, 2] = float("nan"), -1.0, float("inf")
+    d.idx[0, 0, :3] = 1
+    d.idx[1, 0, 2], d.idx[1, 0, 3] = 1, N
+    want = commit_reference(d, L, S, T, W, N)
+    ws = csa2.workspace(d.sh)
+    slots = [(d.kd[l], d.vd[l], d.ks[l], d.vs[l], d.idx[l], d.w[l]) for l in range(L)]
+    csa2.tree_commit(d.sh, slots, d.path, d.n_path, d.head, d.n_swa, ws, mass=d.mass)
+    assert csa2.read_device_error(ws) == (-5, BAD_INDEX | BAD_WEIGHT)
+    for got, ref in zip((d.ks, d.vs, d.mass, d.head, d.n_swa), want):
+        assert torch.equal(got.cpu(), torch.as_tensor(ref))
+    # counts out of range are clamped; no mass, no weights, no workspace
+    d.n_path[0], d.head[1], d.n_swa[2] = -3, 77, -1
+    head, n, m = d.head.clone(), d.n_swa.clone(), d.mass.clone()
+    csa2.read_static_device_error()
+    csa2.tree_commit(d.sh, [x[:4] + (None, None) for x in slots], d.path, d.n_path, d.head, d.n_swa, None)
+    assert csa2.read_static_device_error() == (-5, BAD_INDEX | BAD_COUNT)
+    assert int(d.head[0]) == int(head[0]) and int(d.n_swa[0]) == int(n[0])
+    assert int(d.head[1]) == (W - 1 + 2) % W and int(d.n_swa[2]) == 3 and torch.equal(m, d.mass)
+
+
+# ------------------------------------------------------------------ eviction
+
+def evict_inputs(S, N, dk, dv, dI, block, dtype, seed, kind, n_valid=None):
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    d = types.SimpleNamespace(sh=shape(S, n_entries=N, k_dim=dk, v_dim=dv, idx_dim=dI, block=block, dtype=dtype))
+    d.k, d.v, d.x = randn(g, (S, N, dk), dt), randn(g, (S, N, dv), dt), randn(g, (S, N, dI), dt, 0.25)
+    m = {"spread": lambda: rng.integers(0, 2 ** 40, (S, N)), "ties": lambda: rng.integers(0, 4, (S, N)),
+         "equal": lambda: np.full((S, N), 5), "zero": lambda: np.zeros((S, N), dtype=np.int64),
+         "wide": lambda: rng.integers(-2 ** 63, 2 ** 63 - 1, (S, N)),
+         "rising": lambda: np.tile(np.arange(N), (S, 1)), "falling": lambda: np.tile(-np.arange(N), (S, 1))}[kind]()
+    d.mass = torch.as_tensor(np.asarray(m, dtype=np.int64)).cuda()
+    d.n = i32(rng.integers(0, N + 1, S) if n_valid is None else n_valid)
+    return d
+
+
+def check_evict(d, before, got, kept, kb, args, rounded=True, untouched=None):
+    """`before`, `got`: (k, v, x, mass, n) host copies; untouched: what rows behind the last hold."""
+    trigger, keep, sink, recent = args
+    N, block = d.sh.n_entries, d.sh.block
+    for s in range(d.sh.batch):
+        n = int(before[4][s])
+        ids = R.evict(n, trigger, keep, sink, recent, before[3][s].numpy())
+        assert int(got[4][s]) == len(ids)
+        assert kept[s].tolist() == ids + [-1] * (N - len(ids)), s
+        for a, b in zip(got[:4], before[:4]):
+            assert torch.equal(a[s, :len(ids)], b[s][ids]), s
+        if n > trigger or untouched is not None:
+            assert not got[3][s, len(ids):].any()
+        if untouched is not None:
+            for a, u in zip(got[:3], untouched):
+                assert torch.equal(a[s, len(ids):], u[s, len(ids):])
+        if kb is not None and (n > trigger or untouched is not None):
+            want = R.block_means(before[2][s][ids].double().numpy() if ids else np.zeros((0, d.sh.idx_dim)), len(ids), block, rounded)
+            mean = f64(kb[s])
+            assert np.abs(mean[len(want):]).max(initial=0.0) == 0.0
+            tol = 0.0 if rounded else (HALF[kb.dtype] + 8 * EPS32) * np.abs(want) + 8 * EPS32
+            if rounded:                                    # a mean within fp32 rounding of a half may go either way
+                raw = R.block_means(before[2][s][ids].double().numpy() if ids else np.zeros((0, d.sh.idx_dim)), len(ids), block, False)
+                near = np.abs(np.abs(raw - np.floor(raw)) - 0.5) < 1e-5
+                assert np.all((mean[:len(want)] == want) | near)
+            else:
+                assert np.all(np.abs(mean[:len(want)] - want) <= tol)
+
+
+def host(*ts):
+    return tuple(t.cpu().clone() for t in ts)
+
+
+CASES = [(3, 40, 30, 2, 5, "spread"), (1, 9, 1, 0, 0, "ties"), (4, 700, 512, 16, 100, "ties"), (2, 129, 128, 0, 0, "equal"),
+         (2, 5000, 777, 0, 0, "wide"), (1, 30000, 20000, 16, 1024, "spread"), (2, 600, 100, 60, 40, "spread"),
+         (3, 300, 299, 0, 1, "zero"), (2, 300, 200, 3, 0, "rising"), (2, 300, 200, 0, 3, "falling"), (1, 20001, 19000, 1, 1, "zero")]
+
+
+@pytest.mark.parametrize("S,N,keep,sink,recent,kind", CASES)
+@pytest.mark.parametrize("in_place", [False, True])
+def test_kv_evict(csa2, S, N, keep, sink, recent, kind, in_place):
+    d = evict_inputs(S, N, 192, 128, 64, 8, "bf16", N + S, kind, n_valid=[N] + list(np.random.default_rng(N).integers(0, N + 1, S - 1)))
+    run_evict(csa2, d, (keep, keep, sink, recent), in_place)
+
+
+def run_evict(csa2, d, args, in_place, rounded=True, with_kb=True):
+    S, N = d.sh.batch, d.sh.n_entries
+    nb = -(-N // d.sh.block)
+    before = host(d.k, d.v, d.x, d.mass, d.n)
+    kept = torch.full((S, N), 99, dtype=torch.int32, device="cuda")
+    kb = torch.full((S, nb, d.sh.idx_dim), 99.0, dtype=d.k.dtype, device="cuda") if with_kb else None
+    ws = csa2.workspace(d.sh)
+    call = dict(kb=kb, round_to_int=rounded)
+    if in_place:
+        csa2.kv_evict(d.sh, *args, d.k, d.v, d.x, d.mass, d.n, kept, ws, **call)
+        got, untouched = host(d.k, d.v, d.x, d.mass, d.n), None
+        for s in range(S):
+            if int(before[4][s]) <= args[0]:
+                assert all(torch.equal(a[s], b[s]) for a, b in zip(got, before))
+                assert kb is None or bool((kb[s] == 99).all())
+    else:
+        outs = [torch.full_like(t, 3) for t in (d.k, d.v, d.x, d.mass, d.n)]
+        untouched = host(*outs[:3])
+        csa2.kv_evict(d.sh, *args, d.k, d.v, d.x, d.mass, d.n, kept, ws, out=outs, **call)
+        got = host(*outs)
+        assert all(torch.equal(a, b) for a, b in zip(host(d.k, d.v, d.x, d.mass, d.n), before))
+    assert_no_device_error(csa2, ws)
+    check_evict(d, before, got, kept.cpu(), None if kb is None else kb.cpu(), args, rounded, untouched)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("dk,dv,dI,block,dtype", [(5, 3, 1, 3, "bf16"), (20, 12, 8, 16, "f32"), (7, 7, 7, 1, "f32"),
+                                                  (64, 72, 64, 300, "bf16"), (1024, 1, 16, 8, "bf16")])
+def test_kv_evict_any_shape(csa2, dk, dv, dI, block, dtype, in_place):
+    d = evict_inputs(3, 203, dk, dv, dI, block, dtype, dk, "ties", n_valid=[203, 150, 20])
+    run_evict(csa2, d, (140, 120, 4, 9), in_place, rounded=False)
+
+
+def test_kv_evict_counts_and_no_workspace(csa2):
+    d = evict_inputs(3, 50, 16, 16, 8, 8, "bf16", 2, "spread", n_valid=[99, -4, 50])
+    csa2.read_static_device_error()
+    kept = torch.empty((3, 50), dtype=torch.int32, device="cuda")
+    csa2.kv_evict(d.sh, 40, 30, 0, 0, d.k, d.v, d.x, d.mass, d.n, kept, None)
+    assert csa2.read_static_device_error() == (-5, BAD_COUNT)
+    assert d.n.tolist() == [30, 0, 30]
+
+
+# ------------------------------------------------------------------ together
+
+def step_state(csa2, seed):
+    S, T = 3, 6
+    sh = shape(S * T, tokens=T, n_entries=256, topk=64, swa=16, **FAST)
+    one = shape(S, n_entries=256, topk=64, swa=16, **FAST)
+    d = tree_inputs(sh, seed, fill=16)
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    d.n_valid = i32([256, 251, 200])
+    for s in range(S):
+        for t in range(T):
+            d.idx[s * T + t] = i32(np.sort(rng.choice(200, 64, replace=False)))
+    d.qr, d.kr = torch.empty_like(d.q), torch.empty_like(d.k_draft)
+    par = d.parent.cpu().numpy()
+    depth = np.array([[len(R.path_of(par[s], t)) - 1 for t in range(T)] for s in range(S)])
+    d.pos = i32((1000 + depth).reshape(-1))
+    d.freqs, _ = csa2.rope_freqs(64)
+    # k_draft [S, T, dk] as rows of one head
+    d.k_draft = d.k_draft.view(S * T, -1)
+    d.kr = d.kr.view(S * T, -1)
+    paths = [R.path_of(par[s], T - 1)[::-1] for s in range(S)]
+    d.path = i32([p + [0] * (T - len(p)) for p in paths])
+    d.n_path = i32([len(p) for p in paths])
+    live = np.zeros((S, T))
+    for s, p in enumerate(paths):
+        live[s, p] = 1
+    d.live = i32(live.reshape(-1))
+    d.w = torch.empty((S * T, 64), device="cuda")
+    d.mass = torch.zeros((S, 256), dtype=torch.int64, device="cuda")
+    d.k_idx = randn(g, (S, 256, 64), torch.bfloat16)
+    d.kept = torch.empty((S, 256), dtype=torch.int32, device="cuda")
+    d.kb = torch.zeros((S, 32, 64), dtype=torch.bfloat16, device="cuda")
+    return sh, one, d
+
+
+def run_step(csa2, sh, one, d, ws, ws1):
+    """Positions, attention, the accepted queries' weights, the commit and the eviction, on the current stream."""
+    csa2.rope([(d.q, d.qr, 128), (d.k_draft, d.kr, 128)], d.pos, d.freqs, interleaved=True)
+    kr = d.kr.view(sh.batch // sh.tokens, sh.tokens, -1)
+    csa2.tree_attn(sh, d.qr, d.k_main, d.v_main, d.idx, d.k_swa, d.v_swa, d.n_swa, kr, d.v_draft, d.out, ws,
+                   swa_head=d.head, parent=d.parent, lse=d.lse)
+    csa2.attn_weights(sh, d.qr, d.k_main, d.idx, d.lse, d.w, ws, live=d.live)
+    csa2.tree_commit(sh, [(kr, d.v_draft, d.k_swa, d.v_swa, d.idx, d.w)], d.path, d.n_path, d.head, d.n_swa, ws, mass=d.mass)
+    csa2.kv_evict(one, 250, 200, 4, 32, d.k_main, d.v_main, d.k_idx, d.mass, d.n_valid, d.kept, ws1, kb=d.kb)
+
+
+STATE = ("qr", "kr", "out", "lse", "w", "k_swa", "v_swa", "head", "n_swa", "mass", "k_main", "v_main", "k_idx", "n_valid", "kept", "kb")
+
+
+def test_a_step_of_all_operators(csa2):
+    """Eager on the current stream, eager on another stream, and captured and replayed: the same state, and the attention,
+    the mass and the eviction are what the definitions give on the step's own intermediate results."""
+    sh, one, a = step_state(csa2, 17)
+    before = {k: getattr(a, k).clone() for k in ("k_swa", "v_swa", "n_swa", "head", "k_main", "v_main", "k_idx", "mass", "n_valid")}
+    ws, ws1 = csa2.workspace(sh), csa2.workspace(one)
+    run_step(csa2, sh, one, a, ws, ws1)
+    assert_no_device_error(csa2, ws)
+    assert_no_device_error(csa2, ws1)
+    # attention on the turned queries and keys
+    ref = types.SimpleNamespace(**vars(a))
+    ref.q, ref.k_draft = a.qr, a.kr.view(3, 6, -1)
+    for k in ("k_swa", "v_swa", "n_swa", "head", "k_main", "v_main"):
+        setattr(ref, k, before[k])
+    check_tree(sh, ref)
+    # the mass of the accepted queries, then the eviction by it
+    mass = np.zeros((3, 256), dtype=np.int64)
+    w, idx, live = a.w.cpu().numpy(), a.idx.cpu().numpy(), a.live.cpu().numpy()
+    for b in range(18):
+        if live[b]:
+            for j in range(64):
+                mass[b // 6, idx[b, j]] += int(np.rint(np.float64(w[b, j]) * 2.0 ** 32))
+        else:
+            assert not w[b].any()
+    for s, n in enumerate([256, 251, 200]):
+        ids = R.evict(n, 250, 200, 4, 32, mass[s])
+        assert a.kept[s, :len(ids)].tolist() == ids
+        assert a.mass[s, :len(ids)].tolist() == mass[s][ids].tolist()
+        assert torch.equal(a.k_main[s, :len(ids)], before["k_main"][s][ids])
+    assert a.n_valid.tolist() == [200, 200, 200]
+
+    _, _, b = step_state(csa2, 17)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run_step(csa2, sh, one, b, ws, ws1)
+    torch.cuda.synchronize()
+    for k in STATE:
+        assert torch.equal(getattr(a, k), getattr(b, k)), k
+
+    _, _, c = step_state(csa2, 17)
+    first = {k: getattr(c, k).clone() for k in STATE}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run_step(csa2, sh, one, c, ws, ws1)
+    for _ in range(2):
+        for k in STATE:
+            getattr(c, k).copy_(first[k])
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in STATE:
+            assert torch.equal(getattr(a, k), getattr(c, k)), k
