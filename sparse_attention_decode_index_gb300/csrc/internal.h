@@ -153,11 +153,10 @@ struct RopeArgs {
     const void* x;           // [rows, heads, dim]
     void* out;               // [rows, heads, dim]; == x: in place
     int heads, dim, off, dtype;
-    int first;               // first head chunk of this slot among all slots'
-    int per_chunk;           // heads per chunk
-    int vec;                 // elements per vector access (1: scalar)
+    int wide;                // whole 16-byte vectors at 16-byte addresses (set by the launcher)
   } slot[kMaxRopeSlots];
   int n_slots;
+  int rows, per_block;       // rows, rows per block (set by the launcher)
   int rot, interleaved, inverse;
   float mag;
   const int* pos;            // [rows]

@@ -11,10 +11,15 @@
 // from fp64, so the angle is off by at most |t| 2^-52 for any int32 position,
 // and sincospif takes the reduced angle in half turns.
 //
-// Memory bound: every element is read once and written once, and the cos and
-// sin of a row are made once per block (shared memory) and used by all its heads.  A block
-// takes one row and a chunk of heads; an item is one 16-byte vector that is
-// copied, or the vectors that hold the two halves of pairs.
+// Memory bound: every element is read once and written once.  A block takes
+// up to 8 rows and makes all their cos and sin at once (one angle a thread,
+// kept in shared memory and used by all the heads of all the tensors), so that
+// the chain position -> angle -> sincospif is waited for once per 8 rows; with one
+// row a block its latency, not the memory, set the time (8,192 rows of 64
+// heads of 192: 237 us against 60 us for the bytes).  Few rows are split over the heads
+// instead.  An item is one 16-byte vector that is copied, or the vectors that
+// hold the two halves of pairs; its head comes from a multiplication by a
+// precomputed reciprocal.
 #include "common.cuh"
 #include "internal.h"
 
@@ -23,114 +28,233 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxPairs = 512;
-constexpr int kBatch = 4;   // items a thread loads before it stores any
-
-template <typename T, int V>
-struct alignas(sizeof(T) * V) Vec {
-  T e[V];
-};
+constexpr int kMaxRows = 8;   // rows a block: the angles' table takes at most 32 KB
+constexpr int kBatch = 4;   // vectors a thread loads before it stores any
 
 CSA2_DEV float to_f32(float v) { return v; }
 CSA2_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 CSA2_DEV void from_f32(float& d, float v) { d = v; }
 CSA2_DEV void from_f32(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 
-// The heads [h0, h1) of one row.  Items of a head: first the rotating ones
-// (half layout: the vector pair at i and i + rot / 2; interleaved: one vector
-// of V / 2 pairs, or for V = 1 the two elements of a pair), then, out of place,
-// the copied vectors before and behind the turned range.
-template <typename T, int V>
-CSA2_DEV void turn_heads(const RopeArgs::Slot& y, long long row, int h0, int h1, int rot, bool inter,
-                         const float2* cs) {
-  using W = Vec<T, V>;
-  const int half = rot / 2;
-  const bool copy = y.x != y.out;
-  const bool two = !inter || V == 1;                     // an item holds two vectors
-  const int n_rot = two ? half / V : rot / V;
-  const int before = y.off / V, n_copy = copy ? (y.dim - rot) / V : 0;
-  const int per_head = n_rot + n_copy;
-  const int total = (h1 - h0) * per_head;
-  const T* x = static_cast<const T*>(y.x) + (row * y.heads + h0) * (long long)y.dim;
-  T* out = static_cast<T*>(y.out) + (row * y.heads + h0) * (long long)y.dim;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kBatch * kThreads) {
-    W a[kBatch], b[kBatch];
-    int at[kBatch], pair[kBatch];                        // pair < 0: a copied vector
+// n / d for n * d < 2^32, with m = ceil(2^32 / d) (0 for d = 1).
+CSA2_DEV int fast_div(int n, uint32_t m) { return m == 0 ? n : int(__umulhi(uint32_t(n), m)); }
+
+// The heads [h0, h0 + nh) of rows row0 .. row0 + nr - 1 of one tensor; `items`
+// of a head are shared out over the block's threads.
+struct Heads {
+  int items, nh, dim, skip, total;
+  uint32_t m_item, m_head;
+
+  CSA2_DEV Heads(const RopeArgs::Slot& y, int nr, int nh_, int items_)
+      : items(items_), nh(nh_), dim(y.dim), skip((y.heads - nh_) * y.dim), total(nr * nh_ * items_) {
+    m_item = items <= 1 ? 0u : 0xffffffffu / uint32_t(items) + 1u;
+    m_head = nh <= 1 ? 0u : 0xffffffffu / uint32_t(nh) + 1u;
+  }
+  // Item i: its place in its head, its row, and the head's offset (total <= 2^21, items <= 1024).
+  CSA2_DEV int at(int i, int& it, int& row) const {
+    const int h = fast_div(i, m_item);
+    it = i - h * items;
+    row = fast_div(h, m_head);
+    return h * dim + row * skip;
+  }
+};
+
+// (a, b) -> (a c - b s, b c + a s), two bf16 pairs: words (a0, a1), (b0, b1).
+CSA2_DEV void turn_words(uint32_t& a, uint32_t& b, float4 cs) {
+  const float a0 = __uint_as_float(a << 16), a1 = __uint_as_float(a & 0xffff0000u);
+  const float b0 = __uint_as_float(b << 16), b1 = __uint_as_float(b & 0xffff0000u);
+  a = pack_bf16(a0 * cs.x - b0 * cs.y, a1 * cs.z - b1 * cs.w);
+  b = pack_bf16(b0 * cs.x + a0 * cs.y, b1 * cs.z + a1 * cs.w);
+}
+
+// The turned vectors of the half layout: vector i and its partner rot / 2 further.
+template <bool kBf16>
+CSA2_DEV void turn_half(const Heads& n, const uint8_t* x, uint8_t* out, int off, int half, const float2* cs) {
+  constexpr int kE = kBf16 ? 2 : 4, kV = 16 / kE, kB = kBatch / 2;
+  for (int i0 = threadIdx.x; i0 < n.total; i0 += kB * kThreads) {
+    uint4 a[kB], b[kB];
+    int at[kB], p[kB];
 #pragma unroll
-    for (int m = 0; m < kBatch; ++m) {
+    for (int m = 0; m < kB; ++m) {
       const int i = i0 + m * kThreads;
-      if (i >= total) continue;
-      const int h = i / per_head, it = i - h * per_head;
-      if (it < n_rot) {
-        const int e = two ? (inter ? 2 * it : it * V) : it * V;   // first element in the turned range
-        pair[m] = inter ? e / 2 : e;
-        at[m] = h * y.dim + y.off + e;
-      } else {
-        const int c = it - n_rot;
-        pair[m] = -1;
-        at[m] = h * y.dim + (c < before ? c * V : (c - before) * V + y.off + rot);
+      int it = 0, row = 0;
+      at[m] = i < n.total ? n.at(i, it, row) : 0;
+      at[m] = (at[m] + off + it * kV) * kE;
+      p[m] = row * half + it * kV;
+      if (i < n.total) {
+        a[m] = *reinterpret_cast<const uint4*>(x + at[m]);
+        b[m] = *reinterpret_cast<const uint4*>(x + at[m] + half * kE);
       }
-      a[m] = *reinterpret_cast<const W*>(x + at[m]);
-      if (two && pair[m] >= 0) b[m] = *reinterpret_cast<const W*>(x + at[m] + (inter ? 1 : half));
     }
 #pragma unroll
-    for (int m = 0; m < kBatch; ++m) {
-      const int i = i0 + m * kThreads;
-      if (i >= total) continue;
-      if (pair[m] >= 0) {
-        if (two) {
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            const float2 r = cs[pair[m] + e];
-            const float u = to_f32(a[m].e[e]), v = to_f32(b[m].e[e]);
-            from_f32(a[m].e[e], u * r.x - v * r.y);
-            from_f32(b[m].e[e], v * r.x + u * r.y);
-          }
-          *reinterpret_cast<W*>(out + at[m] + (inter ? 1 : half)) = b[m];
-        } else {
-#pragma unroll
-          for (int e = 0; e + 1 < V; e += 2) {
-            const float2 r = cs[pair[m] + e / 2];
-            const float u = to_f32(a[m].e[e]), v = to_f32(a[m].e[e + 1]);
-            from_f32(a[m].e[e], u * r.x - v * r.y);
-            from_f32(a[m].e[e + 1], v * r.x + u * r.y);
-          }
-        }
+    for (int m = 0; m < kB; ++m) {
+      if (i0 + m * kThreads >= n.total) break;
+      const float4* c = reinterpret_cast<const float4*>(cs + p[m]);   // p and half are even here
+      if (kBf16) {
+        turn_words(a[m].x, b[m].x, c[0]);
+        turn_words(a[m].y, b[m].y, c[1]);
+        turn_words(a[m].z, b[m].z, c[2]);
+        turn_words(a[m].w, b[m].w, c[3]);
+      } else {
+        auto turn = [](uint32_t& u, uint32_t& v, float cc, float ss) {
+          const float f = __uint_as_float(u), g = __uint_as_float(v);
+          u = __float_as_uint(f * cc - g * ss);
+          v = __float_as_uint(g * cc + f * ss);
+        };
+        const float4 c0 = c[0], c1 = c[1];
+        turn(a[m].x, b[m].x, c0.x, c0.y);
+        turn(a[m].y, b[m].y, c0.z, c0.w);
+        turn(a[m].z, b[m].z, c1.x, c1.y);
+        turn(a[m].w, b[m].w, c1.z, c1.w);
       }
-      *reinterpret_cast<W*>(out + at[m]) = a[m];
+      *reinterpret_cast<uint4*>(out + at[m]) = a[m];
+      *reinterpret_cast<uint4*>(out + at[m] + half * kE) = b[m];
     }
   }
 }
 
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float2 cs[kMaxPairs];
-  const long long row = blockIdx.x;
-  int k = 0;
-  while (k + 1 < a.n_slots && int(blockIdx.y) >= a.slot[k + 1].first) ++k;
-  const RopeArgs::Slot& y = a.slot[k];
-  const int h0 = (int(blockIdx.y) - y.first) * y.per_chunk, h1 = min(y.heads, h0 + y.per_chunk);
+// The turned vectors of the interleaved layout: pairs of neighbours.
+template <bool kBf16>
+CSA2_DEV void turn_inter(const Heads& n, const uint8_t* x, uint8_t* out, int off, int half, const float2* cs) {
+  constexpr int kE = kBf16 ? 2 : 4, kV = 16 / kE;
+  for (int i0 = threadIdx.x; i0 < n.total; i0 += kBatch * kThreads) {
+    uint4 a[kBatch];
+    int at[kBatch], p[kBatch];
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      const int i = i0 + m * kThreads;
+      int it = 0, row = 0;
+      at[m] = i < n.total ? n.at(i, it, row) : 0;
+      at[m] = (at[m] + off + it * kV) * kE;
+      p[m] = row * half + it * (kV / 2);
+      if (i < n.total) a[m] = *reinterpret_cast<const uint4*>(x + at[m]);
+    }
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      if (i0 + m * kThreads >= n.total) break;
+      const float4* c = reinterpret_cast<const float4*>(cs + p[m]);
+      auto turn = [](float f, float g, float cc, float ss) { return make_float2(f * cc - g * ss, g * cc + f * ss); };
+      if (kBf16) {
+        auto word = [&](uint32_t& w, float cc, float ss) {
+          const float2 r = turn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u), cc, ss);
+          w = pack_bf16(r.x, r.y);
+        };
+        const float4 c0 = c[0], c1 = c[1];
+        word(a[m].x, c0.x, c0.y);
+        word(a[m].y, c0.z, c0.w);
+        word(a[m].z, c1.x, c1.y);
+        word(a[m].w, c1.z, c1.w);
+      } else {
+        const float4 c0 = c[0];
+        const float2 r = turn(__uint_as_float(a[m].x), __uint_as_float(a[m].y), c0.x, c0.y);
+        const float2 q = turn(__uint_as_float(a[m].z), __uint_as_float(a[m].w), c0.z, c0.w);
+        a[m] = make_uint4(__float_as_uint(r.x), __float_as_uint(r.y), __float_as_uint(q.x), __float_as_uint(q.y));
+      }
+      *reinterpret_cast<uint4*>(out + at[m]) = a[m];
+    }
+  }
+}
+
+// The vectors that are not turned: `before` of them in front of the turned range, the others behind it.
+CSA2_DEV void copy_rest(const Heads& n, const uint8_t* x, uint8_t* out, int before, int rot_vecs, int esize) {
+  for (int i0 = threadIdx.x; i0 < n.total; i0 += kBatch * kThreads) {
+    uint4 a[kBatch];
+    int at[kBatch];
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      const int i = i0 + m * kThreads;
+      int it = 0, row = 0;
+      at[m] = i < n.total ? n.at(i, it, row) * esize : 0;
+      at[m] += (it < before ? it : it + rot_vecs) * 16;
+      if (i < n.total) a[m] = *reinterpret_cast<const uint4*>(x + at[m]);
+    }
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m)
+      if (i0 + m * kThreads < n.total) *reinterpret_cast<uint4*>(out + at[m]) = a[m];
+  }
+}
+
+// Any size and alignment: an item is a pair, or an element that is copied.
+template <typename T>
+CSA2_DEV void turn_scalar(const RopeArgs::Slot& y, int nr, int nh, const T* x, T* out, int rot, bool inter,
+                          const float2* cs) {
+  const int half = rot / 2;
+  const Heads n(y, nr, nh, half + (y.x != y.out ? y.dim - rot : 0));
+  for (int i = threadIdx.x; i < n.total; i += kThreads) {
+    int it, row;
+    int at = n.at(i, it, row);
+    if (it < half) {
+      at += y.off + (inter ? 2 * it : it);
+      const int to = at + (inter ? 1 : half);
+      const float2 r = cs[row * half + it];
+      const float u = to_f32(x[at]), v = to_f32(x[to]);
+      from_f32(out[at], u * r.x - v * r.y);
+      from_f32(out[to], v * r.x + u * r.y);
+    } else {
+      const int c = it - half;
+      at += c < y.off ? c : c + rot;
+      out[at] = x[at];
+    }
+  }
+}
+
+template <bool kInter>
+__global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) float2 cs[];           // [per_block][rot / 2]
+  const long long row0 = (long long)blockIdx.x * a.per_block;
+  const int nr = int(min((long long)a.per_block, a.rows - row0));
   pdl_wait();   // no early trigger: the attention may read what this kernel writes before its own wait
-  const long long pos = a.pos[row];
-  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) {
-    double f = a.freqs[i] * 0.15915494309189533577;      // turns per position
+  const int half = a.rot / 2;
+  const float mag = a.inverse ? 1.f / a.mag : a.mag;
+  for (int i = threadIdx.x; i < nr * half; i += kThreads) {
+    const int r = i / half, p = i - r * half;
+    const long long pos = a.pos[row0 + r];
+    double f = a.freqs[p] * 0.15915494309189533577;      // turns per position
     f -= rint(f);                                        // whole turns change nothing
     const long long F = __double2ll_rn(f * 18446744073709551616.0);   // saturates at half a turn, 2^-64 off
     const unsigned long long t = (unsigned long long)pos * (unsigned long long)F;
-    // the top 32 bits as a signed fraction of a turn, the next ones added in fp32
-    const float turn = float((long long)t) * 5.421010862427522e-20f;   // 2^-64: in [-1/2, 1/2]
+    const float turn = float((long long)t) * 5.421010862427522e-20f;  // * 2^-64: in [-1/2, 1/2]
     float s, c;
     sincospif(2.f * turn, &s, &c);
-    const float m = a.inverse ? 1.f / a.mag : a.mag;
-    cs[i] = make_float2(c * m, (a.inverse ? -s : s) * m);
+    cs[i] = make_float2(c * mag, (a.inverse ? -s : s) * mag);
   }
-  __syncthreads();
-  const bool inter = a.interleaved != 0;
-  if (y.dtype == 1) {
-    if (y.vec == 4) turn_heads<float, 4>(y, row, h0, h1, a.rot, inter, cs);
-    else turn_heads<float, 1>(y, row, h0, h1, a.rot, inter, cs);
-  } else {
-    if (y.vec == 8) turn_heads<__nv_bfloat16, 8>(y, row, h0, h1, a.rot, inter, cs);
-    else turn_heads<__nv_bfloat16, 1>(y, row, h0, h1, a.rot, inter, cs);
+  // tensor k's heads of this block (nh == 0: none) and their place
+  auto part = [&](int k, int& nh, const uint8_t*& x, uint8_t*& out) -> const RopeArgs::Slot& {
+    const RopeArgs::Slot& y = a.slot[k];
+    const int h0 = int((long long)y.heads * blockIdx.y / gridDim.y);
+    nh = int((long long)y.heads * (blockIdx.y + 1) / gridDim.y) - h0;
+    const long long base = (row0 * y.heads + h0) * (long long)y.dim * (y.dtype == 1 ? 4 : 2);
+    x = static_cast<const uint8_t*>(y.x) + base;
+    out = static_cast<uint8_t*>(y.out) + base;
+    return y;
+  };
+  for (int k = 0; k < a.n_slots; ++k) {
+    int nh;
+    const uint8_t* x;
+    uint8_t* out;
+    const RopeArgs::Slot& y = part(k, nh, x, out);
+    const int esize = y.dtype == 1 ? 4 : 2, v = 16 / esize;
+    if (y.wide && y.x != y.out) copy_rest(Heads(y, nr, nh, (y.dim - a.rot) / v), x, out, y.off / v, a.rot / v, esize);
+  }
+  __syncthreads();                                       // the angles
+  for (int k = 0; k < a.n_slots; ++k) {
+    int nh;
+    const uint8_t* x;
+    uint8_t* out;
+    const RopeArgs::Slot& y = part(k, nh, x, out);
+    if (!y.wide) {
+      if (y.dtype == 1)
+        turn_scalar(y, nr, nh, reinterpret_cast<const float*>(x), reinterpret_cast<float*>(out), a.rot, kInter, cs);
+      else
+        turn_scalar(y, nr, nh, reinterpret_cast<const __nv_bfloat16*>(x), reinterpret_cast<__nv_bfloat16*>(out), a.rot,
+                    kInter, cs);
+      continue;
+    }
+    const Heads n(y, nr, nh, (kInter ? a.rot : half) / (y.dtype == 1 ? 4 : 8));
+    if (kInter)
+      y.dtype == 1 ? turn_inter<false>(n, x, out, y.off, half, cs) : turn_inter<true>(n, x, out, y.off, half, cs);
+    else
+      y.dtype == 1 ? turn_half<false>(n, x, out, y.off, half, cs) : turn_half<true>(n, x, out, y.off, half, cs);
   }
 }
 
@@ -138,22 +262,27 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 
 cudaError_t launch_rope(RopeArgs& a, int rows, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  // Heads per block: all of a row's when the rows alone fill the SMs (the
-  // angles are then made once per row), fewer for few rows.
-  const int want = 2 * device_sm_count();
-  int split = rows >= want ? 1 : (want + rows - 1) / rows;
-  int chunks = 0;
+  int heads = 0;   // of the tensor with the most
   for (int k = 0; k < a.n_slots; ++k) {
     RopeArgs::Slot& y = a.slot[k];
     const int v = y.dtype == 1 ? 4 : 8;
     const uintptr_t at = reinterpret_cast<uintptr_t>(y.x) | reinterpret_cast<uintptr_t>(y.out);
-    y.vec = (at % 16 == 0 && y.dim % v == 0 && y.off % v == 0 && (a.interleaved ? a.rot : a.rot / 2) % v == 0) ? v : 1;
-    y.per_chunk = (y.heads + split - 1) / split;
-    y.first = chunks;
-    chunks += (y.heads + y.per_chunk - 1) / y.per_chunk;
+    y.wide = at % 16 == 0 && y.dim % v == 0 && y.off % v == 0 && a.rot % v == 0 && (a.interleaved || a.rot / 2 % v == 0);
+    heads = heads > y.heads ? heads : y.heads;
   }
+  // Four blocks for every SM: as many rows a block as that leaves, up to 8;
+  // when one row each does not give that many blocks, the heads are split.
+  const int want = 4 * device_sm_count();
+  a.rows = rows;
+  a.per_block = rows / want < 1 ? 1 : rows / want > kMaxRows ? kMaxRows : rows / want;
+  for (int k = 0; k < a.n_slots; ++k)   // keeps fast_div's products below 2^32
+    while (a.per_block > 1 && a.per_block * a.slot[k].heads * a.slot[k].dim > (1 << 21)) --a.per_block;
+  const int blocks = (rows + a.per_block - 1) / a.per_block;
+  int split = blocks >= want ? 1 : (want + blocks - 1) / blocks;
+  split = split > heads ? heads : split;
   note_launch();
-  return launch_pdl(rope_kernel, dim3(unsigned(rows), unsigned(chunks)), dim3(kThreads), 0, st, 1, a);
+  return launch_pdl(a.interleaved ? rope_kernel<true> : rope_kernel<false>, dim3(unsigned(blocks), unsigned(split)),
+                    dim3(kThreads), size_t(a.per_block) * (a.rot / 2) * sizeof(float2), st, 1, a);
 }
 
 }  // namespace csa2
