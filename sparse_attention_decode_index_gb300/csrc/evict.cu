@@ -2,9 +2,13 @@
 //
 // evict_select_kernel -- one cluster per sequence: the entries that stay, in
 //   ascending order.  The k-th greatest 64-bit mass is found by a radix select
-//   over the bits in which the masses differ (11 bits a pass: the histograms
-//   of the cluster's CTAs are added up through distributed shared memory),
-//   ties go to the lowest index; each warp then lists its share in order.
+//   over the bits in which the masses differ, 8 bits a pass; ties go to the
+//   lowest index; each warp then lists its share in order.  Every CTA keeps
+//   its share of the masses in shared memory, read once, so that a pass costs a
+//   sweep of shared memory, one push of 256 counts into every CTA of the
+//   cluster and one cluster barrier.  Masses are skewed (many entries draw next to
+//   none), so the sweep adds up a warp's most frequent bin by a ballot before
+//   its shared-memory atomics.
 // evict_move_kernel -- out of place: every row is gathered by its entry, 16
 //   bytes a thread, so it runs at the rate of a copy.
 // evict_shift_kernel -- in place: rows only ever move down, but a row's new
@@ -13,9 +17,12 @@
 //   so that no CTA waits for another: it reads a tile of rows, meets at a
 //   barrier, and writes the tile, whose rows lie at or below the rows that
 //   later tiles read.
-// evict_block_keys_kernel -- the result's block keys (block_key_elem).
+// evict_block_keys_kernel -- the result's block keys, where the move has not
+//   made them (in place, or blocks that do not divide its tiles).
 // evict_counts_kernel -- in place, n_valid changes last: the launches before
 //   read from it which sequences are evicted from.
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -25,33 +32,33 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
-constexpr int kBits = 11, kBins = 1 << kBits;
-constexpr int kMaxCluster = 8;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kBins = 256;
+constexpr int kMaxCluster = 16;
+constexpr int kMaxCached = 24576;   // masses a CTA keeps in shared memory (192 KB)
+static_assert(kMaxCached / kSelWarps <= 32 * 32, "a warp's ballots fit one register a lane");
 
 CSA2_DEV u64 mass_key(long long m) { return u64(m) ^ 0x8000000000000000ull; }   // signed order
 
-CSA2_DEV u64 dsmem_ld_u64(uint32_t addr) {
-  u64 v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr) : "memory");
-  return v;
+CSA2_DEV void dsmem_st_u64(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-CSA2_DEV int dsmem_ld_s32(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
+struct SelectShared {
+  int table[2][kMaxCluster][kBins];   // every CTA's counts, of even and odd passes
+  u64 range[kMaxCluster][2];          // every CTA's least and greatest key
+  int taken[kMaxCluster][2];          // every CTA's keys above the cut and at it
+  int hist[kBins];
+  int warp_a[kSelWarps], warp_b[kSelWarps];
+  u64 warp_mn[kSelWarps], warp_mx[kSelWarps];
+  int bin, above, total;
+};
 
+template <bool kCached>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[kBins];
-  __shared__ int sum[kBins];
-  __shared__ u64 mn_s[kSelWarps], mx_s[kSelWarps];
-  __shared__ u64 mn_c, mx_c;
-  __shared__ int warp_s[kSelWarps];
-  __shared__ int pick_bin, pick_above;
-  __shared__ int gt_w[kSelWarps], eq_w[kSelWarps];
-  __shared__ int gt_c, eq_c;
+  extern __shared__ __align__(16) uint8_t dyn[];
+  SelectShared& sh = *reinterpret_cast<SelectShared*>(dyn);
+  u64* cache = reinterpret_cast<u64*>(dyn + sizeof(SelectShared));
   const int seq = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = int(cluster_rank()), ncta = int(cluster_size());
   pdl_wait();
@@ -67,156 +74,207 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     if (rank == 0 && tid == 0 && !a.in_place) a.n_valid_out[seq] = n;
     return;
   }
-  // entries [lo, hi) compete for `need` places; this warp's share of [0, n)
+  // entries [lo, hi) compete for `need` places.  Shares of [0, n): a CTA's, and
+  // in it a warp's (whole groups of 32, so that ballots keep the order).
   const int lo = a.sink, hi = n - a.recent;
   int need = a.keep - a.sink - a.recent;
   const int per_warp = ((n + ncta * kSelWarps - 1) / (ncta * kSelWarps) + 31) & ~31;
+  const int cta0 = min(n, rank * kSelWarps * per_warp);
   const int w0 = min(n, (rank * kSelWarps + warp) * per_warp), w1 = min(n, w0 + per_warp);
   const int c0 = max(w0, lo), c1 = min(w1, hi);
+  // its own warp's keys only: no barrier between filling the cache and reading it
+  auto key = [&](int j) -> u64 { return kCached ? cache[j - cta0] : mass_key(mass[j]); };
 
-  // bits in which the competing masses differ
+  // the keys, and the bits in which the competing ones differ
   u64 mn = ~0ull, mx = 0;
-  for (int j = c0 + lane; j < c1; j += 32) {
+#pragma unroll 8
+  for (int j = w0 + lane; j < w1; j += 32) {
     const u64 k = mass_key(mass[j]);
-    mn = min(mn, k);
-    mx = max(mx, k);
+    if (kCached) cache[j - cta0] = k;
+    if (j >= c0 && j < c1) {
+      mn = min(mn, k);
+      mx = max(mx, k);
+    }
   }
   for (int o = 16; o > 0; o >>= 1) {
     mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   }
   if (lane == 0) {
-    mn_s[warp] = mn;
-    mx_s[warp] = mx;
+    sh.warp_mn[warp] = mn;
+    sh.warp_mx[warp] = mx;
   }
+  cluster_arrive();   // (every CTA of the cluster runs before any writes into it)
   __syncthreads();
-  if (tid == 0) {
-    for (int w = 0; w < kSelWarps; ++w) {
-      mn = min(mn, mn_s[w]);
-      mx = max(mx, mx_s[w]);
+  if (warp == 0) {
+    mn = sh.warp_mn[lane];
+    mx = sh.warp_mx[lane];
+    for (int o = 16; o > 0; o >>= 1) {
+      mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
-    mn_c = mn;
-    mx_c = mx;
+  }
+  cluster_wait();
+  if (warp == 0 && lane < ncta) {
+    dsmem_st_u64(dsmem_addr(&sh.range[rank][0], lane), mn);
+    dsmem_st_u64(dsmem_addr(&sh.range[rank][1], lane), mx);
   }
   cluster_sync_all();
   mn = ~0ull;
   mx = 0;
   for (int r = 0; r < ncta; ++r) {
-    mn = min(mn, dsmem_ld_u64(dsmem_addr(&mn_c, r)));
-    mx = max(mx, dsmem_ld_u64(dsmem_addr(&mx_c, r)));
+    mn = min(mn, sh.range[r][0]);
+    mx = max(mx, sh.range[r][1]);
   }
-  // (count of competing keys > need >= 0, so mn <= mx here)
-  // Invariant: the keys whose bits from `shift` up equal `prefix` hold the
-  // need-th greatest, and every key with greater such bits is taken.
-  int shift = 64 - __clzll((long long)(mn ^ mx));      // mn ^ mx == 0: clz 64, shift 0
-  u64 prefix = shift >= 64 ? 0 : mx >> shift;
-  bool whole = need == 0;                              // nothing competes for a place
-  while (shift > 0 && !whole) {
-    const int bits = min(kBits, shift), next = shift - bits, bins = 1 << bits;
-    for (int i = tid; i < bins; i += kSelThreads) hist[i] = 0;
+  // (More keys compete than there are places, so mn <= mx.)  The first pass
+  // bins k - mn by its octave and the two bits below its leading one, 4 bins an
+  // octave, the later ones by the next 8 bits.  Invariant: the keys k >= mn with
+  // (k - mn) >> shift == prefix hold the need-th greatest, and every key with
+  // a greater such value is taken.
+  int shift = 64;
+  u64 prefix = 0;
+  auto top = [&](u64 k) -> u64 { return shift >= 64 ? 0 : (k - mn) >> shift; };
+  bool whole = need == 0 || mn == mx;                  // no digit is left to look at
+  if (mn == mx) shift = 0;
+  for (int pass = 0; shift > 0 && !whole; ++pass) {
+    const bool first = pass == 0;
+    const int bits = first ? 8 : min(8, shift), next = shift - bits, bins = 1 << bits;
+    if (tid < kBins) sh.hist[tid] = 0;
     __syncthreads();
-    for (int j = c0 + lane; j < c1; j += 32) {
-      const u64 k = mass_key(mass[j]);
-      if ((shift >= 64 ? 0 : k >> shift) == prefix) atomicAdd(&hist[int((k >> next) & u64(bins - 1))], 1);
+    for (int j0 = c0 & ~31; j0 < c1; j0 += 32) {
+      const int j = j0 + lane;
+      int bin = -1;
+      if (j >= c0 && j < c1) {
+        const u64 k = key(j) - mn;
+        if (first) {
+          const int e = 63 - __clzll((long long)(k | 3));           // >= 1
+          bin = k < 4 ? int(k) : (e - 1) * 4 + (int(k >> (e - 2)) & 3);
+        } else if ((k >> shift) == prefix) {
+          bin = int(k >> next) & (bins - 1);
+        }
+      }
+      // the bin of the first lane that has one is added up for the warp
+      const unsigned has = __ballot_sync(0xffffffffu, bin >= 0);
+      if (has == 0) continue;
+      const int lead = __shfl_sync(0xffffffffu, bin, __ffs(has) - 1);
+      const unsigned same = __ballot_sync(0xffffffffu, bin == lead);
+      if (lane == __ffs(has) - 1) atomicAdd(&sh.hist[lead], __popc(same));
+      else if (bin >= 0 && bin != lead) atomicAdd(&sh.hist[bin], 1);
+    }
+    __syncthreads();
+    int(*table)[kBins] = sh.table[pass & 1];
+    for (int i = tid; i < ncta * bins; i += kSelThreads) {
+      const int r = i >> bits, b = i & (bins - 1);
+      dsmem_st_u32(dsmem_addr(&table[rank][b], r), uint32_t(sh.hist[b]));
     }
     cluster_sync_all();
-    for (int i = tid; i < bins; i += kSelThreads) {
+    // the bin of the need-th greatest: lane l of warp 0 owns bins 8 l .. 8 l + 7, counted from the top
+    if (tid < bins) {
       int s = 0;
-      for (int r = 0; r < ncta; ++r) s += dsmem_ld_s32(dsmem_addr(&hist[i], r));
-      sum[i] = s;
+      for (int r = 0; r < ncta; ++r) s += table[r][tid];
+      sh.hist[tid] = s;
     }
     __syncthreads();
-    // the bin of the need-th greatest: thread t owns bins [4t, 4t + 4), counted from the top
-    int own = 0;
-    for (int i = 0; i < kBins / kSelThreads; ++i) {
-      const int bin = bins - 1 - (tid * (kBins / kSelThreads) + i);
-      if (bin >= 0) own += sum[bin];
-    }
-    int incl = own;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_s[warp] = incl;
-    __syncthreads();
-    int above = incl - own;
-    for (int w = 0; w < warp; ++w) above += warp_s[w];
-    for (int i = 0; i < kBins / kSelThreads; ++i) {
-      const int bin = bins - 1 - (tid * (kBins / kSelThreads) + i);
-      if (bin < 0) break;
-      if (above < need && need <= above + sum[bin]) {
-        pick_bin = bin;
-        pick_above = above;
+    if (warp == 0) {
+      int own = 0, v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int b = bins - 1 - (lane * 8 + i);
+        v[i] = b >= 0 ? sh.hist[b] : 0;
+        own += v[i];
       }
-      above += sum[bin];
+      int incl = own;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      int above = incl - own;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (above < need && need <= above + v[i]) {
+          sh.bin = bins - 1 - (lane * 8 + i);
+          sh.above = above;
+          sh.total = v[i];
+        }
+        above += v[i];
+      }
     }
     __syncthreads();
-    const int bin = pick_bin;
-    need -= pick_above;
-    whole = need == sum[bin];                          // all of the bin's keys are taken
-    prefix = (prefix << bits) | u64(bin);
-    shift = next;
-    cluster_sync_all();                                // the peers have read this CTA's histogram
+    need -= sh.above;
+    whole = need == sh.total;                          // all of the bin's keys are taken
+    if (!first) {
+      prefix = (prefix << bits) | u64(sh.bin);
+      shift = next;
+    } else if (sh.bin < 4) {                           // one value a bin
+      prefix = u64(sh.bin);
+      shift = 0;
+    } else {
+      prefix = u64(4 + (sh.bin & 3));
+      shift = sh.bin / 4 - 1;                          // the octave e = bin / 4 + 1, less the two bits
+    }
   }
-  // a key is taken if its bits from `shift` up are above the prefix, or equal
-  // to it while places are left (ties: `need` of them by index; whole: all)
-  auto above_cut = [&](u64 k) { return (shift >= 64 ? 0 : k >> shift) > prefix; };
-  auto at_cut = [&](u64 k) { return (shift >= 64 ? 0 : k >> shift) == prefix; };
+  // A key is taken if its bits from `shift` up are above the prefix, or equal
+  // to it while places are left: `need` of them, the lowest indices.
   int gt = 0, eq = 0;
-  for (int j0 = w0; j0 < w1; j0 += 32) {
+  unsigned gt_mask = 0, eq_mask = 0;                   // lane i: the warp's i-th group of 32 entries (kCached: at most 32 groups)
+  for (int j0 = w0, it = 0; j0 < w1; j0 += 32, ++it) {
     const int j = j0 + lane;
     bool g = false, e = false;
     if (j < w1) {
       if (j < lo || j >= hi) {
         g = true;
       } else {
-        const u64 k = mass_key(mass[j]);
-        g = above_cut(k);
-        e = at_cut(k);
-      }
-    }
-    gt += __popc(__ballot_sync(0xffffffffu, g));
-    eq += __popc(__ballot_sync(0xffffffffu, e));
-  }
-  if (lane == 0) {
-    gt_w[warp] = gt;
-    eq_w[warp] = eq;
-  }
-  __syncthreads();
-  if (tid == 0) {
-    int g = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      g += gt_w[w];
-      e += eq_w[w];
-    }
-    gt_c = g;
-    eq_c = e;
-  }
-  cluster_sync_all();
-  int gt_before = 0, eq_before = 0;
-  for (int r = 0; r < rank; ++r) {
-    gt_before += dsmem_ld_s32(dsmem_addr(&gt_c, r));
-    eq_before += dsmem_ld_s32(dsmem_addr(&eq_c, r));
-  }
-  for (int w = 0; w < warp; ++w) {
-    gt_before += gt_w[w];
-    eq_before += eq_w[w];
-  }
-  cluster_arrive();                                    // this CTA has read its peers' counts
-  const unsigned below = (1u << lane) - 1u;
-  for (int j0 = w0; j0 < w1; j0 += 32) {
-    const int j = j0 + lane;
-    bool g = false, e = false;
-    if (j < w1) {
-      if (j < lo || j >= hi) {
-        g = true;
-      } else {
-        const u64 k = mass_key(mass[j]);
-        g = above_cut(k);
-        e = at_cut(k);
+        const u64 t = top(key(j));
+        g = t > prefix;
+        e = t == prefix;
       }
     }
     const unsigned mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
+    if (lane == it) {
+      gt_mask = mg;
+      eq_mask = me;
+    }
+    gt += __popc(mg);
+    eq += __popc(me);
+  }
+  if (lane == 0) {
+    sh.warp_a[warp] = gt;
+    sh.warp_b[warp] = eq;
+  }
+  __syncthreads();
+  // before this warp: the CTA's earlier warps (lanes as warps), then the earlier CTAs
+  int ga = sh.warp_a[lane], eb = sh.warp_b[lane];
+  int g_cta = ga, e_cta = eb, g_warp = lane < warp ? ga : 0, e_warp = lane < warp ? eb : 0;
+  for (int o = 16; o > 0; o >>= 1) {
+    g_cta += __shfl_xor_sync(0xffffffffu, g_cta, o);
+    e_cta += __shfl_xor_sync(0xffffffffu, e_cta, o);
+    g_warp += __shfl_xor_sync(0xffffffffu, g_warp, o);
+    e_warp += __shfl_xor_sync(0xffffffffu, e_warp, o);
+  }
+  if (warp == 0 && lane < ncta) {
+    dsmem_st_u32(dsmem_addr(&sh.taken[rank][0], lane), uint32_t(g_cta));
+    dsmem_st_u32(dsmem_addr(&sh.taken[rank][1], lane), uint32_t(e_cta));
+  }
+  cluster_sync_all();                                  // the last access to a peer's memory is before it
+  int gt_before = g_warp, eq_before = e_warp;
+  for (int r = 0; r < rank; ++r) {
+    gt_before += sh.taken[r][0];
+    eq_before += sh.taken[r][1];
+  }
+  const unsigned below = (1u << lane) - 1u;
+  for (int j0 = w0, it = 0; j0 < w1; j0 += 32, ++it) {
+    const int j = j0 + lane;
+    unsigned mg, me;
+    if (kCached) {
+      mg = __shfl_sync(0xffffffffu, gt_mask, it);
+      me = __shfl_sync(0xffffffffu, eq_mask, it);
+    } else {
+      const bool in = j < w1, free = in && j >= lo && j < hi;
+      const u64 t = free ? top(key(j)) : 0;
+      mg = __ballot_sync(0xffffffffu, in && (!free || t > prefix));
+      me = __ballot_sync(0xffffffffu, free && t == prefix);
+    }
+    const bool g = (mg >> lane) & 1u, e = (me >> lane) & 1u;
     const int eq_at = eq_before + __popc(me & below);
     const int at = gt_before + __popc(mg & below) + min(eq_at, need);
     if ((g || (e && eq_at < need)) && at < a.keep) kept[at] = j;
@@ -224,7 +282,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     eq_before += __popc(me);
   }
   if (rank == 0 && tid == 0 && !a.in_place) a.n_valid_out[seq] = n_out;
-  cluster_wait();                                      // the peers have read this CTA's counts
 }
 
 // ------------------------------------------------------------------ moving the rows
@@ -238,10 +295,12 @@ CSA2_DEV int evict_counts(const EvictArgs& a, int seq, int& n_out) {
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;
+constexpr int kMoveRows = 32;   // a tile holds whole blocks of 8 (or any divisor of 32)
 
+// Rows r0 .. r0 + nr - 1 from rows `from`; `copy` (shared memory, nullable) gets them too.
 template <typename U>
-CSA2_DEV void gather_rows(void* dst, const void* src, int row_bytes, long long row0, int r0, int nr, const int* from) {
+CSA2_DEV void gather_rows(void* dst, const void* src, int row_bytes, long long row0, int r0, int nr, const int* from,
+                          U* copy = nullptr) {
   const int per = row_bytes / int(sizeof(U)), total = nr * per;
   U* d = static_cast<U*>(dst) + (row0 + r0) * per;
   const U* s = static_cast<const U*>(src) + row0 * per;
@@ -256,13 +315,17 @@ CSA2_DEV void gather_rows(void* dst, const void* src, int row_bytes, long long r
 #pragma unroll
     for (int m = 0; m < kU; ++m) {
       const int i = i0 + m * kMoveThreads;
-      if (i < total) d[i] = v[m];
+      if (i >= total) break;
+      d[i] = v[m];
+      if (copy != nullptr) copy[i] = v[m];
     }
   }
 }
 
+template <typename U>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs a) {
   __shared__ int from[kMoveRows];
+  extern __shared__ __align__(16) uint8_t keys[];       // [kMoveRows] indexer keys, where the tile makes block keys
   const int seq = blockIdx.y, r0 = blockIdx.x * kMoveRows, tid = threadIdx.x;
   pdl_wait();
   int n;
@@ -275,14 +338,17 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
     a.mass_out[row0 + r0 + tid] = e >= 0 ? a.mass[row0 + e] : 0;
   }
   __syncthreads();
-  if (a.wide) {
-    gather_rows<uint4>(a.k_main_out, a.k_main, a.k_bytes, row0, r0, nr, from);
-    gather_rows<uint4>(a.v_main_out, a.v_main, a.v_bytes, row0, r0, nr, from);
-    gather_rows<uint4>(a.k_idx_out, a.k_idx, a.x_bytes, row0, r0, nr, from);
-  } else {
-    gather_rows<uint16_t>(a.k_main_out, a.k_main, a.k_bytes, row0, r0, nr, from);
-    gather_rows<uint16_t>(a.v_main_out, a.v_main, a.v_bytes, row0, r0, nr, from);
-    gather_rows<uint16_t>(a.k_idx_out, a.k_idx, a.x_bytes, row0, r0, nr, from);
+  const bool blocks = a.kb != nullptr && kMoveRows % a.block == 0;
+  gather_rows<U>(a.k_idx_out, a.k_idx, a.x_bytes, row0, r0, nr, from, blocks ? reinterpret_cast<U*>(keys) : nullptr);
+  gather_rows<U>(a.k_main_out, a.k_main, a.k_bytes, row0, r0, nr, from);
+  gather_rows<U>(a.v_main_out, a.v_main, a.v_bytes, row0, r0, nr, from);
+  if (!blocks) return;
+  __syncthreads();
+  const int j0 = r0 / a.block, nb = min(kMoveRows / a.block, a.nb_cap - j0);
+  for (int i = tid; i < nb * a.idx_dim; i += kMoveThreads) {
+    const int j = j0 + i / a.idx_dim, d = i % a.idx_dim;
+    const float v = block_key_rows(keys, [&](int r) { return r - r0; }, a.idx_dim, a.block, n, j, d, a.dtype, a.round_to_int);
+    store_elem(a.kb, ((long long)seq * a.nb_cap + j) * a.idx_dim + d, a.dtype, v);
   }
 }
 
@@ -371,19 +437,90 @@ __global__ void __launch_bounds__(256) evict_counts_kernel(const EvictArgs a, in
 
 }  // namespace
 
+// Masses of one CTA of a cluster of c: whole groups of 32 for every warp.
+static int share(const EvictArgs& a, int c) {
+  return ((a.n_entries + c * kSelWarps - 1) / (c * kSelWarps) + 31) / 32 * 32 * kSelWarps;
+}
+
+static cudaError_t select_setup() {
+  return once_per_device(kSetupEvict, [] {
+    constexpr int most = int(sizeof(SelectShared)) + kMaxCached * 8;
+    const cudaError_t r = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (r != cudaSuccess) return r;
+    return cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  });
+}
+
+// Whether clusters of 16 CTAs with full caches can run on the current device (asked once per device).
+static cudaError_t wide_clusters(bool& fits) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = select_setup();
+  if (e != cudaSuccess) return e;
+  const bool slot = dev >= 0 && dev < kDevices;
+  int got = slot ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (got == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = sizeof(SelectShared) + kMaxCached * 8;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int active = 0;
+    e = cudaOccupancyMaxActiveClusters(&active, evict_select_kernel<true>, &cfg);
+    if (e != cudaSuccess) return e;
+    got = active > 0 ? 1 : 2;
+    if (slot) known[dev].store(got, std::memory_order_relaxed);
+  }
+  fits = got == 1;
+  return cudaSuccess;
+}
+
 cudaError_t launch_kv_evict(const EvictArgs& a, int seqs, cudaStream_t st) {
   if (seqs == 0) return cudaSuccess;
-  // CTAs per sequence: 8, unless the sequences alone fill the SMs or are short
-  int c = kMaxCluster;
-  while (c > 1 && (c * seqs > 2 * device_sm_count() || a.n_entries < c * 2048)) c >>= 1;
+  // CTAs per sequence: as many as leave every sequence's cluster resident (one
+  // CTA an SM) and a CTA a thousand masses, up to 8; more where 8, or those,
+  // could not keep their masses in shared memory.  16 is not a portable size.
+  int c = 8;
+  while (c > 1 && (c * seqs > device_sm_count() || a.n_entries < c * 1024)) c >>= 1;
+  while (c < 8 && share(a, c) > kMaxCached) c <<= 1;
+  if (share(a, 8) > kMaxCached && share(a, 16) <= kMaxCached) {
+    bool fits = false;
+    const cudaError_t r = wide_clusters(fits);
+    if (r != cudaSuccess) return r;
+    if (fits) c = 16;
+  }
+  const bool cached = share(a, c) <= kMaxCached;
+  if (cached) {
+    const cudaError_t r = select_setup();
+    if (r != cudaSuccess) return r;
+  }
+  const size_t smem = sizeof(SelectShared) + (cached ? size_t(share(a, c)) * 8 : 0);
   note_launch();
-  cudaError_t e = launch_pdl(evict_select_kernel, dim3(unsigned(c), unsigned(seqs)), dim3(kSelThreads), 0, st,
-                             unsigned(c), a);
+  cudaError_t e = launch_pdl(cached ? evict_select_kernel<true> : evict_select_kernel<false>,
+                             dim3(unsigned(c), unsigned(seqs)), dim3(kSelThreads), smem, st, unsigned(c), a);
   if (e != cudaSuccess) return e;
   note_launch();
   if (!a.in_place) {
-    e = launch_pdl(evict_move_kernel, dim3(unsigned((a.n_entries + kMoveRows - 1) / kMoveRows), unsigned(seqs)),
-                   dim3(kMoveThreads), 0, st, 1, a);
+    const dim3 grid(unsigned((a.n_entries + kMoveRows - 1) / kMoveRows), unsigned(seqs));
+    const size_t keys = a.kb != nullptr && kMoveRows % a.block == 0 ? size_t(kMoveRows) * a.x_bytes : 0;
+    if (keys > 48 * 1024) {
+      e = once_per_device(kSetupEvictMove, [] {
+        const cudaError_t r = cudaFuncSetAttribute(evict_move_kernel<uint4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kMoveRows * 4096);
+        if (r != cudaSuccess) return r;
+        return cudaFuncSetAttribute(evict_move_kernel<uint16_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMoveRows * 4096);
+      });
+      if (e != cudaSuccess) return e;
+    }
+    e = launch_pdl(a.wide ? evict_move_kernel<uint4> : evict_move_kernel<uint16_t>, grid, dim3(kMoveThreads), keys, st, 1, a);
   } else {
     const int unit = a.wide ? 16 : 2;
     // slices of 128 bytes, down to 32 (a sector) while the CTAs do not fill the SMs
@@ -399,7 +536,7 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int seqs, cudaStream_t st) {
                : launch_pdl(evict_shift_kernel<uint16_t>, grid, dim3(kShiftThreads), 0, st, 1, a, width);
   }
   if (e != cudaSuccess) return e;
-  if (a.kb != nullptr) {
+  if (a.kb != nullptr && (a.in_place || kMoveRows % a.block != 0)) {
     note_launch();
     const long long elems = (long long)a.nb_cap * a.idx_dim;
     e = launch_pdl(evict_block_keys_kernel, dim3(unsigned((elems + 255) / 256), unsigned(seqs)), dim3(256), 0, st, 1, a);
