@@ -2,13 +2,18 @@
 // K and V rows into every layer's window ring, and the accepted queries'
 // attention weights into the per-entry mass.
 //
-// One cluster of CTAs per sequence; CTA c takes the layers c, c + C, ... All of
-// them read the shared head and fill count, meet at a cluster barrier, and the
-// first then advances both.  The mass is a 64-bit integer in units of 2^-32:
-// integer atomics commute, so the sums depend on no order, and they stay exact
-// where fp32 sums would stop growing.  rint(w * 2^32) is exact in fp64.
+// One cluster of CTAs per sequence.  All of them read the shared head and fill
+// count, meet at a cluster barrier, and the first then advances both.  The
+// window rows are shared out by layer, the weights by (token, slot): a thread
+// takes one selected slot through all the layers and adds up neighbouring layers that
+// selected the same entry (Reuse layers attend with their indexing layer's
+// list) before one atomic.  The mass is a 64-bit integer in units of 2^-32:
+// integer sums depend on no order, so neither the atomics nor the merging
+// change them, and they stay exact where fp32 sums would stop growing.  The
+// scaling by 2^32 is exact in fp32 and the conversion rounds once.
 // Bound by the latency of the loads behind each other (count, path, rows) for
-// few sequences and by the rate of the 64-bit L2 atomics for many.
+// few sequences and by the reads of idx and weights and the 64-bit L2 atomics
+// for many.
 //
 // Like the cache-maintenance kernels it lets no later launch start early: the
 // attention reads n_swa and the windows before its own wait.
@@ -20,7 +25,8 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr float kMaxWeight = 1048576.f;   // 2^20: rint(w * 2^32) < 2^53
+constexpr int kBatch = 4;                 // layers whose idx and weights a thread has in flight
+constexpr float kMaxWeight = 1048576.f;   // 2^20: w * 2^32 stays below 2^53
 
 template <typename U>
 CSA2_DEV void copy_rows(void* dst, const void* src, int row_bytes, long long dst_row0, long long src_row0, int j0,
@@ -72,22 +78,43 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
       copy_rows<uint16_t>(y.k_swa, y.k_draft, a.k_bytes, ring0, draft0, j0, n, slot, a.swa, path);
       copy_rows<uint16_t>(y.v_swa, y.v_draft, a.v_bytes, ring0, draft0, j0, n, slot, a.swa, path);
     }
-    if (a.mass == nullptr || y.weights == nullptr) continue;
+  }
+  if (a.mass != nullptr) {
     unsigned long long* mass = a.mass + (long long)seq * a.n_entries;
-    for (int i = tid; i < n * a.topk; i += kThreads) {
+    for (int i = rank * kThreads + tid; i < n * a.topk; i += ncta * kThreads) {
       const int j = i / a.topk;
       const long long at = (draft0 + path[j]) * a.topk + (i - j * a.topk);
-      const int e = y.idx[at];
-      const float w = y.weights[at];
-      if (e < 0) continue;
-      if (e >= a.n_entries) {
-        report(a.err, kErrBadIndex, e);
-      } else if (!(w >= 0.f && w <= kMaxWeight)) {
-        report(a.err, kErrBadWeight, e);
-      } else {
-        const long long units = __double2ll_rn(double(w) * 4294967296.0);
-        if (units != 0) atomicAdd(mass + e, (unsigned long long)units);
+      int cur = -1;                          // the entry that `sum` is for
+      unsigned long long sum = 0;
+      for (int l0 = 0; l0 < a.n_layers; l0 += kBatch) {
+        int e[kBatch];
+        float w[kBatch];
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+          const bool on = l0 + m < a.n_layers && a.slot[l0 + m].weights != nullptr;
+          e[m] = on ? a.slot[l0 + m].idx[at] : -1;
+          w[m] = on ? a.slot[l0 + m].weights[at] : 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+          if (e[m] < 0) continue;
+          if (e[m] >= a.n_entries) {
+            report(a.err, kErrBadIndex, e[m]);
+            continue;
+          }
+          if (!(w[m] >= 0.f && w[m] <= kMaxWeight)) {
+            report(a.err, kErrBadWeight, e[m]);
+            continue;
+          }
+          if (e[m] != cur) {
+            if (sum != 0) atomicAdd(mass + cur, sum);
+            cur = e[m];
+            sum = 0;
+          }
+          sum += (unsigned long long)__float2ll_rn(w[m] * 4294967296.f);
+        }
       }
+      if (sum != 0) atomicAdd(mass + cur, sum);
     }
   }
   cluster_wait();
@@ -101,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
 
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, int seqs, cudaStream_t st) {
   if (seqs == 0) return cudaSuccess;
-  const int c = a.n_layers < 8 ? a.n_layers : 8;   // a portable cluster: a CTA per layer, up to 8
+  const int c = a.n_layers < 8 && a.mass == nullptr ? a.n_layers : 8;   // a portable cluster
   note_launch();
   return launch_pdl(tree_commit_kernel, dim3(unsigned(c), unsigned(seqs)), dim3(kThreads), 0, st, unsigned(c), a);
 }
