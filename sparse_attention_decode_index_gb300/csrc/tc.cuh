@@ -101,6 +101,14 @@ CSA2_DEV void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool ac
       : "memory");
 }
 
+// One lane of the (converged) warp: the warp runs the issuing code together, so
+// that its operands stay in uniform registers, and this lane issues.
+CSA2_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // `bar` gets one arrival when every tcgen05 operation that this thread has issued is complete.
 CSA2_DEV void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))

@@ -294,13 +294,12 @@ __global__ void __launch_bounds__(256) weights_generic_kernel(const AttnWeightsA
   if (lane == 0 && j < a.topk) a.weights[(long long)b * a.topk + j] = w;
 }
 
-// Tokens a CTA of the tensor-core kernel, or 0 for a cluster of CTAs per query.
-int tree_group(const TreeArgs& a, int batch, size_t plan_bytes) {
+// Pairs of tokens on the tensor cores, or a cluster of CTAs per query.
+bool tree_pairs(const TreeArgs& a, int batch, size_t plan_bytes) {
   static const int force = getenv("CSA2_GROUP") ? atoi(getenv("CSA2_GROUP")) : -1;
-  const int seqs = batch / a.tokens;
-  auto fits = [&](int g) { return tree_plan_words(seqs, a.tokens, a.topk, a.swa, g) * 4 <= plan_bytes; };
-  if (force >= 0) return force > 0 && fits(force) ? force : 0;
-  return 0;
+  if (tree_plan_words(batch / a.tokens, a.tokens, a.topk, a.swa) * 4 > plan_bytes) return false;
+  if (force >= 0) return force > 0;
+  return false;
 }
 
 }  // namespace
@@ -308,8 +307,8 @@ int tree_group(const TreeArgs& a, int batch, size_t plan_bytes) {
 cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan, size_t plan_bytes, cudaStream_t st) {
   if (batch == 0) return cudaSuccess;
   if (fast) {
-    const int group = tree_group(a, batch, plan_bytes);
-    return group == 0 ? launch_tree_attn_cluster(a, batch, st) : launch_tree_attn_tc(a, batch / a.tokens, group, plan, st);
+    return tree_pairs(a, batch, plan_bytes) ? launch_tree_attn_tc(a, batch / a.tokens, plan, st)
+                                            : launch_tree_attn_cluster(a, batch, st);
   }
   const cudaError_t e = once_per_device(kSetupTreeGeneric, [] {
     return cudaFuncSetAttribute(tree_generic_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGenSmemMax));

@@ -2,35 +2,37 @@
 // that fill the GPU (bf16, 64 heads sharing one KV head, dk 192, dv 128).
 //
 // The drafted tokens of a sequence are neighbours: their Top-K lists overlap
-// and their windows are nearly the same.  One CTA therefore attends with up to
-// 2 or 4 tokens of a sequence at once, over the union of their keys, and masks
-// each key to the tokens that have it: a key that several tokens select is
-// gathered once.  The gather sets the time of this attention (the load path of
-// an SM takes about 34 bytes a cycle of 16-byte cp.async pieces, 12,000 cycles
-// for the 640 keys of one query), and the tensor cores' rows come in 128s,
-// which two tokens' 64 heads fill, so that attending two tokens to a key that
-// only one of them has costs nothing on the tensor cores.
+// and their windows are nearly the same.  One CTA therefore attends with two
+// tokens of a sequence at once (one, where a sequence has one), over the union
+// of their keys, and masks each key to the tokens that have it: a key that both
+// select is gathered once.  The gather sets the time of this attention, and the tensor cores'
+// rows come in 128s, which two tokens' 64 heads fill, so that attending both
+// tokens to a key that only one of them has costs nothing there.
 //
 // tree_plan_kernel -- one block per group of tokens: the union of the lists
-//   (an entry belongs to the first list that has it; its other lists are found
-//   by binary search), the window's committed rows and the drafted rows on the
+//   (an entry belongs to the first list that has it; its other list is looked
+//   up by binary search), the window's committed rows and the drafted rows on the
 //   tokens' paths, each with a mask of the group's tokens.  Lists that do not
 //   ascend strictly are not merged: their entries are taken one by one.
 //
 // tree_tc_kernel -- persistent, one CTA an SM, one group at a time:
-//   4 producer warps gather tiles of 64 keys into a ring of stages, K rows
+//   4 producer warps gather tiles of 64 keys into a ring of 5 stages, K rows
 //     K-major and V rows MN-major, both 128-byte swizzled;
-//   1 MMA thread issues S = Q K^T (128 rows x 64 keys, 12 steps) into TMEM and,
-//     a tile later, O += P V (P from TMEM, 4 steps);
-//   4 softmax warps per 128 rows: a thread owns a row (a token's head), so the
-//     maximum and the sum need no exchange; P goes back to TMEM as bf16, over
-//     its S.  O is rescaled only when a row's maximum grows by more than 2^8
-//     (P then stays below 256, whose rounding is relative like any other).
-//   S is double buffered: the scores of tile i + 1 are computed while tile i is in
-//   its softmax.
+//   1 warp issues S = Q K^T (128 rows x 64 keys, 12 steps) into TMEM and, a
+//     tile later, O += P V (4 steps).  Q and P are read from TMEM: with Q in
+//     shared memory every step of 64 keys reads its 4 KB again, and the shared
+//     memory, not the tensor core, set the rate (58 cycles a step against 32);
+//   4 softmax warps: a thread owns a row (a token's head), so the maximum and
+//     the sum need no exchange; P goes back to TMEM as bf16, over its S.  O is
+//     rescaled only when a row's maximum grows by more than 2^8 (P then stays
+//     below 256, whose rounding is relative like any other);
+//   4 end warps put the next group's Q into TMEM and write the last one's O
+//     out, both through shared memory for whole lines, while the others go on.
+//   S and O are double buffered: the scores of tile i + 1 are computed while tile i
+//   is in its softmax, and a group starts while the one before it is written out.
 //
-// P is rounded to bf16 (half a step, 2^-9 of a weight on average 2^-10), which
-// the tensor core asks for; the sums of the weights stay fp32 and unrounded.
+// P is rounded to bf16 (half a step, 2^-8 of a weight), which the tensor core
+// asks for; the sums of the weights stay fp32 and unrounded.
 // A V row that holds an infinity or NaN for one token must not reach another
 // that masks it (0 * inf): rows of O that are not finite are computed again
 // from their own keys.
@@ -44,7 +46,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kH = 64, kDk = 192, kDv = 128;
-constexpr int kRow = 28;                       // bits of a row id in a plan entry; the mask above
+constexpr int kRow = 28;                       // bits of a row id in a plan entry (ids < 2^28); the mask above
 constexpr uint32_t kRowMask = (1u << kRow) - 1;
 constexpr int kHeader = 4;                     // words before a group's entries: counts of main, ring, drafted
 
@@ -78,8 +80,8 @@ CSA2_DEV int block_slot(bool keep, int& base, int* warp_s) {
 
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs a, uint32_t* plan, int group) {
   extern __shared__ int sid[];                 // [group][topk]
-  __shared__ int path[4][kMaxTreeTokens];
-  __shared__ int n_path[4], n_ring[4], n_list[4], live_s[4];
+  __shared__ int path[2][kMaxTreeTokens];
+  __shared__ int n_path[2], n_ring[2], n_list[2], live_s[2];
   __shared__ uint32_t drafted[kMaxTreeTokens];
   __shared__ int warp_s[kPlanWarps];
   __shared__ int merge, newest_s;
@@ -87,6 +89,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
   const int per_seq = (a.tokens + group - 1) / group;
   const int seq = blockIdx.x / per_seq, t0 = (blockIdx.x - seq * per_seq) * group;
   const int ng = min(group, a.tokens - t0);
+  pdl_launch_dependents();   // the attention's CTAs set themselves up meanwhile, and wait for this launch's end
   pdl_wait();
   if (tid == 0) merge = 1;
   if (tid < kMaxTreeTokens) drafted[tid] = 0;
@@ -107,10 +110,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
       live_s[warp] = live;
       if (warp == 0) newest_s = w.newest;
     }
-  } else if (warp < 4 && lane == 0) {
+  } else if (warp < 2 && lane == 0) {
     n_path[warp] = n_ring[warp] = live_s[warp] = 0;
   }
-  if (tid < 4) n_list[tid] = 0;
+  if (tid < 2) n_list[tid] = 0;
   __syncthreads();
   const int total = ng * a.topk;
   for (int i = tid; i < total; i += kPlanThreads) {
@@ -133,31 +136,34 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
   }
   __syncthreads();
   uint32_t* out = plan + (long long)blockIdx.x * plan_stride(a, group);
+  // Both tokens' keys first, then either's own: most tiles are then wholly a
+  // token's or wholly not, which the softmax takes without looking at keys.
+  const uint32_t all = (1u << ng) - 1u;
+  uint32_t masks = 0;                          // this thread's elements, 4 bits each: mask, 0 where not listed
   int n_main = 0;
-  for (int i0 = 0; i0 < total; i0 += kPlanThreads) {
+  for (int i0 = 0, x = 0; i0 < total; i0 += kPlanThreads, ++x) {
     const int i = i0 + tid;
     const int e = i < total ? sid[i] : -1;
     const int g = i < total ? i / a.topk : 0;
-    bool keep = e >= 0;
-    uint32_t mask = 1u << g;
-    if (keep && merge) {
-      for (int o = 0; o < ng; ++o) {
-        if (o == g) continue;
-        const int* list = sid + o * a.topk;
-        int lo = 0, hi = n_list[o];            // first element >= e
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (list[mid] < e) lo = mid + 1;
-          else hi = mid;
-        }
-        if (lo < n_list[o] && list[lo] == e) {
-          if (o < g) keep = false;
-          mask |= 1u << o;
-        }
+    uint32_t mask = e >= 0 ? 1u << g : 0u;
+    if (e >= 0 && merge && ng == 2) {
+      const int* list = sid + (1 - g) * a.topk;
+      int lo = 0, hi = n_list[1 - g];          // first element >= e
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid] < e) lo = mid + 1;
+        else hi = mid;
       }
+      if (lo < n_list[1 - g] && list[lo] == e) mask = g == 0 ? 3u : 0u;
     }
-    const int at = block_slot(keep, n_main, warp_s);
-    if (keep) out[kHeader + at] = uint32_t(e) | (mask << kRow);
+    masks |= mask << (4 * x);                  // (at most 2,048 elements: x < 4)
+  }
+  for (uint32_t want = all; want != 0; --want) {
+    for (int i0 = 0, x = 0; i0 < total; i0 += kPlanThreads, ++x) {
+      const bool keep = ((masks >> (4 * x)) & 15u) == want;
+      const int at = block_slot(keep, n_main, warp_s);
+      if (keep) out[kHeader + at] = uint32_t(sid[i0 + tid]) | (want << kRow);
+    }
   }
   // committed rows, newest first, to the tokens whose window reaches them
   int ring = 0;
@@ -188,36 +194,31 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
 
 constexpr int kTile = 64;                      // keys a stage
 constexpr int kKBytes = kTile * kDk * 2, kVBytes = kTile * kDv * 2;
-constexpr int kQBytes = 128 * kDk * 2;         // two tokens' queries
-constexpr int kProducers = 128;
+constexpr int kStages = 5;
+constexpr int kSoftmaxWarps = 4, kEndWarps = 4, kProducerWarps = 4;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kEndWarps + kProducerWarps + 1);
+constexpr uint32_t kTmemCols = 512;            // a power of two over two O (128 each), two S (64 each) and Q (96)
+constexpr uint32_t kOCol = 0, kSCol = 256, kQCol = 384;
 
-template <int MT>
-struct Conf {
-  static constexpr int stages = MT == 2 ? 3 : 4;
-  static constexpr int softmax_warps = 4 * MT;
-  static constexpr int threads = 32 * softmax_warps + kProducers + 32;
-  static constexpr int q = 0, k = q + MT * kQBytes, v = k + stages * kKBytes, ctl = v + stages * kVBytes;
-  static constexpr uint32_t cols = MT == 2 ? 512 : 256;
-  static constexpr uint32_t o_col = 0, s_col = MT * 128;   // O: 128 columns a row tile; S: two buffers of 64 each
-};
-
-template <int MT>
-struct Ctl {
-  uint64_t full[Conf<MT>::stages], empty[Conf<MT>::stages];
-  uint64_t s_full[MT][2], p_full[MT][2];
-  uint64_t o_done[MT], o_last[MT], o_free[MT];   // O holds a tile more; the item's last; has been read
-  uint64_t q_full, q_empty, fin;
-  uint64_t mask[Conf<MT>::stages][4];          // the tile's keys of each token
+struct Shared {
+  uint8_t k[kStages][kKBytes];                 // 3 blocks of 64 dims: 64 rows of 128 bytes
+  uint8_t v[kStages][kVBytes];                 // 2 blocks of 64 dims: 64 keys of 128 bytes
+  uint64_t row[kProducerWarps][2][16][2];      // K and V addresses of a producer warp's keys, of even and odd tiles
+  uint4 turn[kEndWarps][32 * 4];               // 64 bytes of each of an end warp's rows
+  float2 stat[128];                            // (exponent, sum) of the rows of an item
+  uint64_t mask[kStages][2];                   // the tile's keys of each token
+  uint64_t full[kStages], empty[kStages];      // a tile has landed; has been used
+  uint64_t s_full[2], p_full[2];               // S has been computed; P has been written
+  uint64_t o_done, o_last[2], o_free[2];       // O holds a tile more; the item's last; has been read
+  uint64_t q_full, q_empty, stat_full, stat_free;
+  uint64_t fin;                                // every MMA is done
   uint32_t tmem;
   volatile int abort;
 };
-
-template <int MT>
-constexpr int tc_smem = Conf<MT>::ctl + int(sizeof(Ctl<MT>)) + 1024;   // + room to align to 1,024
+constexpr int kSmem = int(sizeof(Shared)) + 1024;   // + room to align to 1,024
 
 // A bounded wait that also ends when another role has given up.
-template <typename C>
-CSA2_DEV bool tc_wait(C& c, uint64_t* bar, uint32_t parity, int* err) {
+CSA2_DEV bool tc_wait(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   for (uint32_t i = 1;; ++i) {
@@ -234,8 +235,7 @@ CSA2_DEV bool tc_wait(C& c, uint64_t* bar, uint32_t parity, int* err) {
 }
 
 // The same by a whole warp, which goes on or gives up together.
-template <typename C>
-CSA2_DEV bool tc_wait_warp(C& c, uint64_t* bar, uint32_t parity, int* err) {
+CSA2_DEV bool tc_wait_warp(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
   return __all_sync(0xffffffffu, tc_wait(c, bar, parity, err)) != 0;
 }
 
@@ -269,9 +269,9 @@ CSA2_DEV Key resolve(const TreeArgs& a, int seq, int pos, uint32_t entry, int n_
   return y;
 }
 
-CSA2_DEV void cp16(uint32_t dst, const uint8_t* src, const void* any) {   // src null: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src != nullptr ? static_cast<const void*>(src) : any),
-               "r"(src != nullptr ? 16u : 0u)
+CSA2_DEV void cp16(uint32_t dst, uint64_t src, int offset, const void* any) {   // src 0: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(src != 0 ? src + offset : reinterpret_cast<uint64_t>(any)), "r"(src != 0 ? 16u : 0u)
                : "memory");
 }
 
@@ -304,36 +304,58 @@ __device__ __noinline__ float4 row_alone(const TreeArgs& a, int seq, int query, 
   return o;
 }
 
-template <int MT>
-__global__ void __launch_bounds__(Conf<MT>::threads, 1)
+// The 32 rows of a warp, 64 bytes each, between rows by lane (a lane's four
+// pieces are its row's) and by line (piece j of lane l is row 8 j + l / 4,
+// part l % 4), through shared memory without bank conflicts.
+CSA2_DEV uint4& turn_at(uint4* t, int row, int part) { return t[row * 4 + (part ^ ((row >> 1) & 3))]; }
+
+CSA2_DEV void rows_to_lines(uint4* t, uint4 (&w)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) turn_at(t, lane, p) = w[p];
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = turn_at(t, 8 * j + (lane >> 2), lane & 3);
+  __syncwarp();
+}
+
+CSA2_DEV void lines_to_rows(uint4* t, uint4* w) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) turn_at(t, 8 * j + (lane >> 2), lane & 3) = w[j];
+  __syncwarp();
+#pragma unroll
+  for (int p = 0; p < 4; ++p) w[p] = turn_at(t, lane, p);
+  __syncwarp();
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
     tree_tc_kernel(const TreeArgs a, const uint32_t* plan, int group, int n_groups) {
-  using C = Conf<MT>;
   extern __shared__ uint8_t raw[];
-  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  Ctl<MT>& c = *reinterpret_cast<Ctl<MT>*>(smem + C::ctl);
+  Shared& c = *reinterpret_cast<Shared*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    for (int i = 0; i < C::stages; ++i) {
-      mbar_init(&c.full[i], kProducers + 16);   // every producer's copies, 4 masks of every producer warp
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&c.full[i], 32 * kProducerWarps + 2 * kProducerWarps);   // every producer's copies, the masks
       mbar_init(&c.empty[i], 1);
     }
-    for (int m = 0; m < MT; ++m) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&c.s_full[m][b], 1);
-        mbar_init(&c.p_full[m][b], 128);
-      }
-      mbar_init(&c.o_done[m], 1);
-      mbar_init(&c.o_last[m], 1);
-      mbar_init(&c.o_free[m], 128);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&c.s_full[b], 1);
+      mbar_init(&c.p_full[b], 128);
+      mbar_init(&c.o_last[b], 1);
+      mbar_init(&c.o_free[b], 128);
     }
-    mbar_init(&c.q_full, kProducers);
+    mbar_init(&c.o_done, 1);
+    mbar_init(&c.q_full, 128);
     mbar_init(&c.q_empty, 1);
+    mbar_init(&c.stat_full, 128);
+    mbar_init(&c.stat_free, 128);
     mbar_init(&c.fin, 1);
     c.abort = 0;
     mbar_fence_init();
   }
   __syncwarp();
-  if (warp == 0) tmem_alloc(&c.tmem, C::cols);
+  if (warp == 0) tmem_alloc(&c.tmem, kTmemCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -341,162 +363,235 @@ __global__ void __launch_bounds__(Conf<MT>::threads, 1)
   pdl_wait();
   const int per_seq = (a.tokens + group - 1) / group, stride = plan_stride(a, group);
   const float sl2 = a.scale * 1.4426950408889634f;
+  auto keys_of = [&](int item) -> int {
+    const uint32_t* list = plan + (long long)item * stride;
+    return int(list[0]) + int(list[1]) + int(list[2]);
+  };
 
-  if (warp < C::softmax_warps) {
+  if (warp < kSoftmaxWarps) {
     // ---------------------------------------------------------------- softmax: thread = row
-    const int mt = warp >> 2, row = (warp & 3) * 32 + lane;
-    const int token = mt * 2 + (row >> 6), head = row & 63;   // of the group (uniform in a warp)
-    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t o_addr = tmem + lanes + C::o_col + mt * 128;
-    uint32_t tiles = 0, items = 0;             // of this CTA so far
+    const int token = tid >> 6;                               // of the group (uniform in a warp)
+    const uint32_t lanes = uint32_t(warp * 32) << 16;
+    uint32_t tiles = 0, items = 0;                            // of this CTA so far
     bool ok = true;
     for (int item = blockIdx.x; item < n_groups && ok; item += gridDim.x) {
-      const uint32_t* list = plan + (long long)item * stride;
-      const int n_main = int(list[0]), n_ring = int(list[1]), n_all = n_main + n_ring + int(list[2]);
-      const int seq = item / per_seq, t = (item - seq * per_seq) * group + token;
-      const bool mine = token < group && t < a.tokens;
-      const int query = seq * a.tokens + t;
-      const int nt = (n_all + kTile - 1) / kTile;
+      const int nt = (keys_of(item) + kTile - 1) / kTile;
+      if (nt == 0) continue;
+      const uint32_t o_addr = tmem + lanes + kOCol + (items & 1) * 128;
       float ref = -INFINITY, sum = 0.f;        // the exponent that P and O are relative to, and the weights' sum
       for (int i = 0; i < nt; ++i, ++tiles) {
-        const uint32_t buf = tiles & 1, st = tiles % C::stages;
-        if (!tc_wait_warp(c, &c.full[st], (tiles / C::stages) & 1, a.err) ||
-            !tc_wait_warp(c, &c.s_full[mt][buf], (tiles >> 1) & 1, a.err)) {
-          ok = false;
-          break;
-        }
+        const uint32_t buf = tiles & 1, st = tiles % kStages;
+        ok = tc_wait_warp(c, &c.full[st], (tiles / kStages) & 1, a.err) &&
+             tc_wait_warp(c, &c.s_full[buf], (tiles >> 1) & 1, a.err);
+        if (!ok) break;
         tc_fence_after();
         const uint64_t mask = c.mask[st][token];
-        const uint32_t s_addr = tmem + lanes + C::s_col + (mt * 2 + buf) * 64;
-        uint32_t s[64];
-        tmem_ld64(s, s_addr);
-        if (mask != ~0ull) {
-          const uint32_t lo = uint32_t(mask), hi = uint32_t(mask >> 32);
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (!(((j < 32 ? lo : hi) >> (j & 31)) & 1u)) s[j] = 0xff800000u;   // -inf
-        }
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          m0 = fmaxf(m0, __uint_as_float(s[j]));
-          m1 = fmaxf(m1, __uint_as_float(s[32 + j]));
-        }
-        const float top = fmaxf(m0, m1) * sl2;
-        const bool grows = top > ref + 8.f;
-        if (i == 0) {
-          ref = top;
-        } else if (__any_sync(0xffffffffu, grows)) {
-          // O holds tiles up to i - 1: wait for the last of them.  (S of tile i comes behind O of tile i - 2,
-          // so that the barrier is in the phase of tile i - 1 or behind it, and the parity tells which.)
-          if (!tc_wait_warp(c, &c.o_done[mt], (tiles - 1) & 1, a.err)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const float f = grows ? ex2(ref - top) : 1.f;
-          if (grows) ref = top;
-          sum *= f;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            tmem_ld32(o, o_addr + 32 * q);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32(o_addr + 32 * q, o);
-          }
-        }
-        const float base = ref == -INFINITY ? 0.f : ref;
+        const uint32_t s_addr = tmem + lanes + kSCol + buf * 64;
         uint32_t p[32];
-        float s0 = 0.f, s1 = 0.f;
+        if (mask != 0) {
+          uint32_t s[64];
+          tmem_ld64(s, s_addr);
+          if (mask != ~0ull) {
+            const uint32_t lo = uint32_t(mask), hi = uint32_t(mask >> 32);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float x = ex2(__fmaf_rn(__uint_as_float(s[2 * j]), sl2, -base));
-          const float y = ex2(__fmaf_rn(__uint_as_float(s[2 * j + 1]), sl2, -base));
-          s0 += x;
-          s1 += y;
-          p[j] = pack_bf16(x, y);
+            for (int j = 0; j < 64; ++j)
+              if (!(((j < 32 ? lo : hi) >> (j & 31)) & 1u)) s[j] = 0xff800000u;   // -inf
+          }
+          float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            m0 = fmaxf(m0, __uint_as_float(s[j]));
+            m1 = fmaxf(m1, __uint_as_float(s[32 + j]));
+          }
+          const float top = fmaxf(m0, m1) * sl2;
+          const bool grows = top > ref + 8.f;
+          if (i == 0) {
+            ref = top;
+          } else if (__any_sync(0xffffffffu, grows)) {
+            // O holds tiles up to i - 1: wait for the last of them.  (S of tile i comes behind O of tile i - 2,
+            // so that the barrier is in the phase of tile i - 1 or behind it, and the parity tells which.)
+            ok = tc_wait_warp(c, &c.o_done, (tiles - 1) & 1, a.err);
+            if (!ok) break;
+            tc_fence_after();
+            const float f = grows ? ex2(ref - top) : 1.f;
+            if (grows) ref = top;
+            sum *= f;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[32];
+              tmem_ld32(o, o_addr + 32 * q);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(o_addr + 32 * q, o);
+            }
+          }
+          const float base = ref == -INFINITY ? 0.f : ref;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float x = ex2(__fmaf_rn(__uint_as_float(s[2 * j]), sl2, -base));
+            const float y = ex2(__fmaf_rn(__uint_as_float(s[2 * j + 1]), sl2, -base));
+            s0 += x;
+            s1 += y;
+            p[j] = pack_bf16(x, y);
+          }
+          sum += s0 + s1;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) p[j] = 0;
         }
-        sum += s0 + s1;
         tmem_st32(s_addr, p);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&c.p_full[mt][buf]);
+        mbar_arrive(&c.p_full[buf]);
       }
       if (!ok) break;
-      // epilogue
-      const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);   // NaN stays NaN
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + ((long long)query * kH + head) * kDv;
-      if (nt > 0) {   // (o_done may be two phases further by now: a barrier of its own)
-        if (!tc_wait_warp(c, &c.o_last[mt], items & 1, a.err)) break;
-        ++items;
-        tc_fence_after();
+      ok = items == 0 || tc_wait_warp(c, &c.stat_free, (items - 1) & 1, a.err);
+      if (!ok) break;
+      c.stat[tid] = make_float2(ref, sum);
+      mbar_arrive(&c.stat_full);
+      ++items;
+    }
+  } else if (warp < kSoftmaxWarps + kEndWarps) {
+    // ---------------------------------------------------------------- ends of items: Q in, O out; thread = row
+    const int row = tid - 32 * kSoftmaxWarps, w = warp - kSoftmaxWarps;
+    const int token = row >> 6, head0 = (w & 1) * 32;         // of the group; the warp's rows are heads head0 .. head0 + 31
+    const uint32_t lanes = uint32_t(w * 32) << 16;
+    uint4* turn = c.turn[w];
+    auto query_of = [&](int item) -> int {                    // -1: the group has no such token
+      const int seq = item / per_seq, t = (item - seq * per_seq) * group + token;
+      return token < group && t < a.tokens ? seq * a.tokens + t : -1;
+    };
+    uint4 q[24];                                              // a group's queries: 64 bytes of the rows in every four
+    auto fetch_q = [&](int item) {
+      const int query = query_of(item);
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
+                                                        ((long long)max(query, 0) * kH + head0) * (kDk * 2));
+#pragma unroll
+      for (int x = 0; x < 24; ++x)
+        q[x] = query >= 0 ? src[(8 * (x & 3) + (lane >> 2)) * (kDk / 8) + (x >> 2) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
+    };
+    auto store_q = [&]() {
+#pragma unroll
+      for (int b = 0; b < 3; ++b) {
+        uint32_t r[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          lines_to_rows(turn, q + 8 * b + 4 * h);
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const uint4 y = q[8 * b + 4 * h + x];
+            r[16 * h + 4 * x] = y.x;
+            r[16 * h + 4 * x + 1] = y.y;
+            r[16 * h + 4 * x + 2] = y.z;
+            r[16 * h + 4 * x + 3] = y.w;
+          }
+        }
+        tmem_st32(tmem + lanes + kQCol + 32 * b, r);
       }
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(&c.q_full);
+    };
+    auto next_item = [&](int item) -> int {                   // the next with any key, from `item` on
+      while (item < n_groups && keys_of(item) == 0) item += gridDim.x;
+      return item;
+    };
+    uint32_t items = 0;
+    const int first = next_item(blockIdx.x);
+    if (first < n_groups) {
+      fetch_q(first);
+      store_q();
+    }
+    for (int item = blockIdx.x; item < n_groups; item += gridDim.x) {
+      const int query = query_of(item);
+      uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((long long)max(query, 0) * kH + head0) * kDv);
+      float* lse = a.lse != nullptr ? a.lse + (long long)max(query, 0) * kH + head0 + lane : nullptr;
+      const int n_all = keys_of(item);
+      if (n_all == 0) {                                       // no live token
+        if (query >= 0) {
+          for (int x = lane; x < 32 * kDv / 8; x += 32) out[x] = make_uint4(0, 0, 0, 0);
+          if (lse != nullptr) *lse = -INFINITY;
+        }
+        continue;
+      }
+      const int next = next_item(item + gridDim.x);
+      if (next < n_groups) {
+        fetch_q(next);
+        if (!tc_wait_warp(c, &c.q_empty, items & 1, a.err)) break;
+        tc_fence_after();
+        store_q();
+      }
+      if (!tc_wait_warp(c, &c.stat_full, items & 1, a.err)) break;
+      const float ref = c.stat[row].x, sum = c.stat[row].y;
+      mbar_arrive(&c.stat_free);
+      const uint32_t o_addr = tmem + lanes + kOCol + (items & 1) * 128;
+      if (!tc_wait_warp(c, &c.o_last[items & 1], (items >> 1) & 1, a.err)) break;
+      tc_fence_after();
+      const float inv = sum > 0.f ? 1.f / sum : sum;          // no key: 0; NaN stays NaN
       bool bad = false;
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
+      for (int b = 0; b < 4; ++b) {
         uint32_t o[32];
-        if (nt > 0) {
-          tmem_ld32(o, o_addr + 32 * q);
-        } else {
+        tmem_ld32(o, o_addr + 32 * b);
+        if (query < 0) continue;
+        uint4 y[4];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0;
-        }
-        if (!mine) continue;
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          uint32_t w[4];
+        for (int x = 0; x < 4; ++x) {
+          uint32_t p[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float x = __uint_as_float(o[j + 2 * e]) * inv, y = __uint_as_float(o[j + 2 * e + 1]) * inv;
-            bad = bad || !(fabsf(x) < INFINITY) || !(fabsf(y) < INFINITY);
-            w[e] = pack_bf16(x, y);
+            const float u = __uint_as_float(o[8 * x + 2 * e]) * inv, v = __uint_as_float(o[8 * x + 2 * e + 1]) * inv;
+            bad = bad || !(fabsf(u) < INFINITY) || !(fabsf(v) < INFINITY);
+            p[e] = pack_bf16(u, v);
           }
-          *reinterpret_cast<uint4*>(out + 32 * q + j) = make_uint4(w[0], w[1], w[2], w[3]);
+          y[x] = make_uint4(p[0], p[1], p[2], p[3]);
         }
+        rows_to_lines(turn, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) out[(8 * j + (lane >> 2)) * (kDv / 8) + 4 * b + (lane & 3)] = y[j];
       }
-      if (mine && a.lse != nullptr)
-        a.lse[(long long)query * kH + head] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       tc_fence_before();
-      if (nt > 0) mbar_arrive(&c.o_free[mt]);
+      mbar_arrive(&c.o_free[items & 1]);
+      ++items;
+      if (query >= 0 && lse != nullptr) *lse = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
       // rows that are not finite: from their own keys, so that no other token's values reach them
       unsigned again = __ballot_sync(0xffffffffu, bad);
       while (again != 0) {
         const int l = __ffs(again) - 1;
         again &= again - 1;
+        const uint32_t* list = plan + (long long)item * stride;
         const float base = __shfl_sync(0xffffffffu, ref == -INFINITY ? 0.f : ref, l);
-        const float scale = __shfl_sync(0xffffffffu, sum > 0.f ? 1.f / sum : sum, l);
-        const int h = __shfl_sync(0xffffffffu, head, l);
-        float4 o = row_alone(a, seq, query, h, token, list + kHeader, n_main, n_ring, n_all, sl2, base);
+        const float scale = __shfl_sync(0xffffffffu, inv, l);
+        float4 o = row_alone(a, item / per_seq, query, head0 + l, token, list + kHeader, int(list[0]), int(list[1]), n_all, sl2, base);
         if (scale == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);   // no key at all
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + ((long long)query * kH + h) * kDv + 4 * lane) =
+        reinterpret_cast<uint2*>(out)[l * (kDv / 4) + lane] =
             make_uint2(pack_bf16(o.x * scale, o.y * scale), pack_bf16(o.z * scale, o.w * scale));
       }
     }
-  } else if (warp < C::softmax_warps + kProducers / 32) {
-    // ---------------------------------------------------------------- producers
-    const int w = warp - C::softmax_warps, ptid = w * 32 + lane;
-    // pieces of four keys (K row: 0..23, V row: 24..39 of each) in five copies a lane
-    int p_key[5], p_src[5], p_dst[5], p_chunk[5];
+  } else if (warp < kSoftmaxWarps + kEndWarps + kProducerWarps) {
+    // ---------------------------------------------------------------- producers: 16 keys of a tile a warp
+    const int w = warp - kSoftmaxWarps - kEndWarps;
+    // The 16-byte pieces of four keys (K row: 0..23, V row: 24..39 of each) in
+    // five copies a lane; key 4 q + x lies at row 16 w + 4 q + x of the tile,
+    // whose low three bits swizzle: those of x, and 4 more for odd q.
+    int p_row[5], p_src[5], p_dst[5];
     bool p_k[5];
 #pragma unroll
     for (int k = 0; k < 5; ++k) {
-      const int p = 32 * k + lane, part = p % 40;
-      p_key[k] = p / 40;
+      const int p = 32 * k + lane, part = p % 40, x = p / 40;
       p_k[k] = part < 24;
-      const int q = p_k[k] ? part : part - 24;
-      p_src[k] = q * 16;
-      p_dst[k] = (q >> 3) * (kTile * 128);     // 64-column block
-      p_chunk[k] = q & 7;
+      const int y = p_k[k] ? part : part - 24;
+      p_row[k] = 2 * x + (p_k[k] ? 0 : 1);
+      p_src[k] = y * 16;
+      p_dst[k] = (y >> 3) * (kTile * 128) + (w * 16 + x) * 128 + (((y & 7) ^ x) << 4);
     }
-    uint32_t tiles = 0, items = 0;
+    uint32_t tiles = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_groups && ok; item += gridDim.x) {
       const uint32_t* list = plan + (long long)item * stride;
       const int n_main = int(list[0]), n_ring = int(list[1]), n_all = n_main + n_ring + int(list[2]);
-      const int seq = item / per_seq, t0 = (item - seq * per_seq) * group;
-      const int nt = (n_all + kTile - 1) / kTile;
-      if (nt == 0) continue;
+      const int seq = item / per_seq, nt = (n_all + kTile - 1) / kTile;
       list += kHeader;
       int pos = w * 16 + (lane & 15);
       uint32_t entry = pos < n_all ? list[pos] : 0;
@@ -504,102 +599,81 @@ __global__ void __launch_bounds__(Conf<MT>::threads, 1)
         const Key key = resolve(a, seq, pos, entry, n_main, n_ring, n_all);
         pos += kTile;
         entry = pos < n_all ? list[pos] : 0;   // of the next tile
-        const uint32_t st = tiles % C::stages;
-        if (!tc_wait_warp(c, &c.empty[st], ((tiles / C::stages) & 1) ^ 1, a.err)) {
-          ok = false;
-          break;
+        uint64_t(*row)[2] = c.row[w][tiles & 1];
+        if (lane < 16) {
+          row[lane][0] = reinterpret_cast<uint64_t>(key.k);
+          row[lane][1] = reinterpret_cast<uint64_t>(key.v);
         }
-        // the masks of this warp's 16 keys, token by token
+        const uint32_t st = tiles % kStages;
+        ok = tc_wait_warp(c, &c.empty[st], ((tiles / kStages) & 1) ^ 1, a.err);   // (and the warp's rows are written)
+        if (!ok) break;
+        __syncwarp();
+        // the masks of this warp's 16 keys
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < 2; ++g) {
           const unsigned m = __ballot_sync(0xffffffffu, lane < 16 && ((key.mask >> g) & 1u));
           if (lane == g) reinterpret_cast<uint16_t*>(&c.mask[st][g])[w] = uint16_t(m);
         }
-        if (lane < 4) mbar_arrive(&c.full[st]);   // the masks; the copies arrive by themselves
-        const uint32_t k_st = smem_u32(smem + C::k + st * kKBytes), v_st = smem_u32(smem + C::v + st * kVBytes);
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
+        if (lane < 2) mbar_arrive(&c.full[st]);   // the masks; the copies arrive by themselves
+        const uint32_t k_st = smem_u32(c.k[st]), v_st = smem_u32(c.v[st]);
+        uint64_t src[4][5];
 #pragma unroll
-          for (int k = 0; k < 5; ++k) {
-            const int from = 4 * q + p_key[k], r = w * 16 + from;
-            const uint8_t* kr = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(key.k), from));
-            const uint8_t* vr = reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(key.v), from));
-            const uint8_t* src = p_k[k] ? kr : vr;
-            cp16((p_k[k] ? k_st : v_st) + p_dst[k] + r * 128 + ((p_chunk[k] ^ (r & 7)) << 4),
-                 src != nullptr ? src + p_src[k] : nullptr, a.k_main);
-          }
-        }
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < 5; ++k) src[q][k] = (&row[4 * q][0])[p_row[k]];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < 5; ++k)
+            cp16(((p_k[k] ? k_st : v_st) + p_dst[k] + q * 512) ^ ((q & 1) * 64), src[q][k], p_src[k], a.k_main);
         cp_arrive(&c.full[st]);
-        if (i == 0) {
-          // the group's queries, behind its first tile: row r of row tile m is head r % 64 of token 2 m + r / 64
-          if (!tc_wait_warp(c, &c.q_empty, (items & 1) ^ 1, a.err)) {
-            ok = false;
-            break;
-          }
-          for (int x = ptid; x < MT * 128 * 24; x += kProducers) {
-            const int r = x / 24, part = x - r * 24, tok = r >> 6;
-            const int t = t0 + tok;
-            const uint8_t* src = tok < group && t < a.tokens
-                                     ? static_cast<const uint8_t*>(a.q) +
-                                           (((long long)seq * a.tokens + t) * kH + (r & 63)) * (kDk * 2) + part * 16
-                                     : nullptr;
-            const int rr = r & 127;
-            cp16(smem_u32(smem + C::q + (r >> 7) * kQBytes) + (part >> 3) * (128 * 128) + rr * 128 +
-                     (((part & 7) ^ (rr & 7)) << 4),
-                 src, a.k_main);
-          }
-          cp_arrive(&c.q_full);
-        }
       }
-      ++items;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (lane == 0) {
+  } else {
     // ---------------------------------------------------------------- MMA issue
     constexpr uint32_t qk_desc = idesc_bf16(128, kTile, false), pv_desc = idesc_bf16(128, kDv, true);
+    const uint64_t k0 = smem_desc(smem_u32(c.k[0]), 16, 1024), v0 = smem_desc(smem_u32(c.v[0]), kTile * 128, 1024);
     uint32_t tiles = 0, items = 0;
     bool ok = true;
-    // O (+)= P V of tile x, tile i of its item
+    // O (+)= P V of tile x, of the current item
     auto pv = [&](uint32_t x, bool first, bool last) -> bool {
-      const uint32_t st = x % C::stages, buf = x & 1;
-      const uint32_t v = smem_u32(smem + C::v + st * kVBytes);
-      for (int m = 0; m < MT; ++m) {
-        if (first && items > 0 && !tc_wait(c, &c.o_free[m], (items - 1) & 1, a.err)) return false;
-        if (!tc_wait(c, &c.p_full[m][buf], (x >> 1) & 1, a.err)) return false;
-        tc_fence_after();
+      const uint32_t st = x % kStages, buf = x & 1, o = items & 1;
+      const uint64_t v = v0 + st * (kVBytes >> 4);
+      if (first && items > 1 && !tc_wait_warp(c, &c.o_free[o], ((items >> 1) - 1) & 1, a.err)) return false;
+      if (!tc_wait_warp(c, &c.p_full[buf], (x >> 1) & 1, a.err)) return false;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
-          mma_ts(tmem + C::o_col + m * 128, tmem + C::s_col + (m * 2 + buf) * 64 + 8 * k,
-                 smem_desc(v + k * 2048, kTile * 128, 1024), pv_desc, !(first && k == 0));
-        tc_commit(&c.o_done[m]);
-        if (last) tc_commit(&c.o_last[m]);
+          mma_ts(tmem + kOCol + o * 128, tmem + kSCol + buf * 64 + 8 * k, v + k * (2048 >> 4), pv_desc, !(first && k == 0));
+        tc_commit(&c.empty[st]);
+        tc_commit(&c.o_done);
+        if (last) tc_commit(&c.o_last[o]);
       }
-      tc_commit(&c.empty[st]);
+      __syncwarp();
       return true;
     };
     for (int item = blockIdx.x; item < n_groups && ok; item += gridDim.x) {
-      const uint32_t* list = plan + (long long)item * stride;
-      const int n_all = int(list[0]) + int(list[1]) + int(list[2]);
-      const int nt = (n_all + kTile - 1) / kTile;
+      const int nt = (keys_of(item) + kTile - 1) / kTile;
       if (nt == 0) continue;
       for (int i = 0; i < nt && ok; ++i, ++tiles) {
-        const uint32_t st = tiles % C::stages, buf = tiles & 1;
-        ok = tc_wait(c, &c.full[st], (tiles / C::stages) & 1, a.err) &&
-             (i > 0 || tc_wait(c, &c.q_full, items & 1, a.err));
+        const uint32_t st = tiles % kStages, buf = tiles & 1;
+        ok = tc_wait_warp(c, &c.full[st], (tiles / kStages) & 1, a.err) &&
+             (i > 0 || tc_wait_warp(c, &c.q_full, items & 1, a.err));
         if (!ok) break;
         fence_async_smem();                    // the copies are generic-proxy writes, the tensor core reads by the async proxy
         tc_fence_after();
-        const uint32_t k_st = smem_u32(smem + C::k + st * kKBytes);
-        for (int m = 0; m < MT; ++m) {
-          const uint32_t q_st = smem_u32(smem + C::q + m * kQBytes);
+        const uint64_t kd = k0 + st * (kKBytes >> 4);
+        if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < kDk / 16; ++k)
-            mma_ss(tmem + C::s_col + (m * 2 + buf) * 64,
-                   smem_desc(q_st + (k >> 2) * (128 * 128) + (k & 3) * 32, 16, 1024),
-                   smem_desc(k_st + (k >> 2) * (kTile * 128) + (k & 3) * 32, 16, 1024), qk_desc, k > 0);
-          tc_commit(&c.s_full[m][buf]);
+            mma_ts(tmem + kSCol + buf * 64, tmem + kQCol + 8 * k, kd + ((k >> 2) * (kTile * 128) + (k & 3) * 32) / 16, qk_desc,
+                   k > 0);
+          tc_commit(&c.s_full[buf]);
+          if (i == nt - 1) tc_commit(&c.q_empty);
         }
-        if (i == nt - 1) tc_commit(&c.q_empty);
+        __syncwarp();
         if (i > 0) ok = pv(tiles - 1, i == 1, false);
       }
       if (!ok) break;
@@ -607,43 +681,39 @@ __global__ void __launch_bounds__(Conf<MT>::threads, 1)
       ++items;
     }
     // every MMA has finished before the memory it uses is given up
-    tc_commit(&c.fin);
+    if (elect_one()) tc_commit(&c.fin);
+    __syncwarp();
     mbar_wait(&c.fin, 0);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_free(tmem, C::cols);
-}
-
-template <int MT>
-cudaError_t launch_tc(const TreeArgs& a, const uint32_t* plan, int group, int n_groups, cudaStream_t st) {
-  const cudaError_t e = once_per_device(MT == 2 ? kSetupTreeQuad : kSetupTreePair, [] {
-    return cudaFuncSetAttribute(tree_tc_kernel<MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, tc_smem<MT>);
-  });
-  if (e != cudaSuccess) return e;
-  const int grid = n_groups < device_sm_count() ? n_groups : device_sm_count();
-  note_launch();
-  return launch_pdl(tree_tc_kernel<MT>, dim3(unsigned(grid)), dim3(Conf<MT>::threads), tc_smem<MT>, st, 1, a, plan, group,
-                    n_groups);
+  if (warp == 0) tmem_free(tmem, kTmemCols);
 }
 
 }  // namespace
 
-// Words of the plan of a launch with `group` tokens a CTA.
-size_t tree_plan_words(int seqs, int tokens, int topk, int swa, int group) {
+// Words of the plan of a launch.
+size_t tree_plan_words(int seqs, int tokens, int topk, int swa) {
+  const int group = tokens > 1 ? 2 : 1;
   return size_t(seqs) * ((tokens + group - 1) / group) * (size_t(kHeader) + size_t(group) * topk + swa + tokens);
 }
 
-cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, int group, void* plan, cudaStream_t st) {
-  const int n_groups = seqs * ((a.tokens + group - 1) / group);
-  uint32_t* words = static_cast<uint32_t*>(plan);
-  note_launch();
-  const cudaError_t e = launch_pdl(tree_plan_kernel, dim3(unsigned(n_groups)), dim3(kPlanThreads),
-                                   size_t(group) * a.topk * 4, st, 1, a, words, group);
+cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStream_t st) {
+  cudaError_t e = once_per_device(kSetupTreePair, [] {
+    return cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
   if (e != cudaSuccess) return e;
-  return group > 2 ? launch_tc<2>(a, words, group, n_groups, st) : launch_tc<1>(a, words, group, n_groups, st);
+  const int group = a.tokens > 1 ? 2 : 1, n_groups = seqs * ((a.tokens + group - 1) / group);
+  const uint32_t* words = static_cast<const uint32_t*>(plan);
+  note_launch();
+  e = launch_pdl(tree_plan_kernel, dim3(unsigned(n_groups)), dim3(kPlanThreads), size_t(group) * a.topk * 4, st, 1, a,
+                 static_cast<uint32_t*>(plan), group);
+  if (e != cudaSuccess) return e;
+  const int grid = n_groups < device_sm_count() ? n_groups : device_sm_count();
+  note_launch();
+  return launch_pdl(tree_tc_kernel, dim3(unsigned(grid)), dim3(kThreads), kSmem, st, 1, a, words, group, n_groups);
 }
 
 }  // namespace csa2
