@@ -16,7 +16,7 @@
 //   ascend strictly are not merged: their entries are taken one by one.
 //
 // tree_tc_kernel -- persistent, one CTA an SM, one group at a time:
-//   4 producer warps gather tiles of 64 keys into a ring of 5 stages, K rows
+//   7 producer warps gather tiles of 64 keys into a ring of 5 stages, K rows
 //     K-major and V rows MN-major, both 128-byte swizzled;
 //   1 warp issues S = Q K^T (128 rows x 64 keys, 12 steps) into TMEM and, a
 //     tile later, O += P V (4 steps).  Q and P are read from TMEM: with Q in
@@ -30,6 +30,8 @@
 //     out, both through shared memory for whole lines, while the others go on.
 //   S and O are double buffered: the scores of tile i + 1 are computed while tile i
 //   is in its softmax, and a group starts while the one before it is written out.
+//   (Two softmax sets for even and odd tiles were slower: their warps share the
+//   schedulers, so that each tile waits longer for its weights.)
 //
 // P is rounded to bf16 (half a step, 2^-8 of a weight), which the tensor core
 // asks for; the sums of the weights stay fp32 and unrounded.
@@ -46,156 +48,231 @@ namespace csa2 {
 namespace {
 
 constexpr int kH = 64, kDk = 192, kDv = 128;
+constexpr int kTile = 64;                      // keys a stage
 constexpr int kRow = 28;                       // bits of a row id in a plan entry (ids < 2^28); the mask above
 constexpr uint32_t kRowMask = (1u << kRow) - 1;
-constexpr int kHeader = 4;                     // words before a group's entries: counts of main, ring, drafted
+// A group's part of the plan, in words: the counts of main, ring and drafted
+// rows and a spare one; for every tile of 64 keys and token the keys that the
+// token has, 64 bits each; the keys.
+constexpr int kHeader = 4;
+__host__ __device__ constexpr int plan_keys(int topk, int swa, int tokens, int group) {
+  return (group * topk + swa + tokens + kTile - 1) / kTile * kTile;
+}
+__host__ __device__ constexpr int plan_entries(int keys) { return kHeader + keys / kTile * 4; }
 
 // ------------------------------------------------------------------ plan
 
-constexpr int kPlanThreads = 512, kPlanWarps = kPlanThreads / 32;
+// 16 warps for the lists, a warp for each token's path.
+constexpr int kListThreads = 512, kListWarps = kListThreads / 32, kPlanThreads = kListThreads + 64;
+constexpr int kChunks = 2;                     // list elements a thread takes of each list: topk <= 1,024
 
 CSA2_DEV int plan_stride(const TreeArgs& a, int group) {
-  return kHeader + group * a.topk + a.swa + a.tokens;
+  const int keys = plan_keys(a.topk, a.swa, a.tokens, group);
+  return plan_entries(keys) + keys;
 }
 
-// Position of `keep`ing threads behind `base` in thread order; every thread
-// gets the block's total added to base.
-CSA2_DEV int block_slot(bool keep, int& base, int* warp_s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned m = __ballot_sync(0xffffffffu, keep);
-  __syncthreads();
-  if (lane == 0) warp_s[warp] = __popc(m);
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanWarps; ++w) {
-    const int v = warp_s[w];
-    before += w < warp ? v : 0;
-    total += v;
+// Elements of `list` [n], ascending, below e; `hit`: whether e is one.
+CSA2_DEV int below(const int* list, int n, int e, bool& hit) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] < e) lo = mid + 1;
+    else hi = mid;
   }
-  const int at = base + before + __popc(m & ((1u << lane) - 1u));
-  base += total;
-  return at;
+  hit = lo < n && list[lo] == e;
+  return lo;
 }
 
+// Bits [from, to) of the 32 bits that begin at `at`.
+CSA2_DEV uint32_t range_bits(int at, int from, int to) {
+  const int lo = max(from - at, 0), hi = min(to - at, 32);
+  if (hi <= lo) return 0;
+  return (hi == 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
+}
+
+// Bound by the latency of its steps (load, search, count, write), one block a group.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs a, uint32_t* plan, int group) {
-  extern __shared__ int sid[];                 // [group][topk]
+  extern __shared__ int sid[];                 // [2][topk], then the ranks [topk + 1]
+  int* rank = sid + 2 * a.topk;                // keys of the first list before each that the second has too
   __shared__ int path[2][kMaxTreeTokens];
-  __shared__ int n_path[2], n_ring[2], n_list[2], live_s[2];
+  __shared__ int n_path[2], n_ring[2], n_list[2];
   __shared__ uint32_t drafted[kMaxTreeTokens];
-  __shared__ int warp_s[kPlanWarps];
-  __shared__ int merge, newest_s;
+  __shared__ int warp_s[kChunks * kListWarps];
+  __shared__ int ordered, newest_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per_seq = (a.tokens + group - 1) / group;
   const int seq = blockIdx.x / per_seq, t0 = (blockIdx.x - seq * per_seq) * group;
   const int ng = min(group, a.tokens - t0);
   pdl_launch_dependents();   // the attention's CTAs set themselves up meanwhile, and wait for this launch's end
-  pdl_wait();
-  if (tid == 0) merge = 1;
+  if (tid == 0) ordered = 1;
   if (tid < kMaxTreeTokens) drafted[tid] = 0;
-  if (warp < ng) {                             // a warp per token: its path and its part of the ring
-    const int token = t0 + warp;
-    const bool live = tree_live(a, seq, token, lane == 0);
-    int depth = token + 1, n = min(depth, a.swa);
-    if (live && a.parent != nullptr) {
-      n = tree_walk(a, seq, token, path[warp], depth, true);
-    } else {
-      for (int i = lane; i < n; i += 32) path[warp][i] = token - i;
-    }
-    TreeWindow w;
-    tree_ring(a, seq, depth, w, lane == 0 && warp == 0 && t0 == 0);
-    if (lane == 0) {
-      n_path[warp] = live ? n : 0;
-      n_ring[warp] = live ? w.n_ring : 0;
-      live_s[warp] = live;
-      if (warp == 0) newest_s = w.newest;
-    }
-  } else if (warp < 2 && lane == 0) {
-    n_path[warp] = n_ring[warp] = live_s[warp] = 0;
-  }
-  if (tid < 2) n_list[tid] = 0;
+  if (tid < 2) n_list[tid] = n_path[tid] = n_ring[tid] = 0;
   __syncthreads();
-  const int total = ng * a.topk;
-  for (int i = tid; i < total; i += kPlanThreads) {
-    const int g = i / a.topk;
-    int e = live_s[g] ? a.idx[((long long)seq * a.tokens + t0) * a.topk + i] : -1;
-    if (e >= a.n_entries) {
-      report(a.err, kErrBadIndex, e);
-      e = -1;
+  pdl_wait();
+  if (warp >= kListWarps) {
+    const int g = warp - kListWarps, token = t0 + g;
+    if (g < ng) {
+      int depth = token + 1, n = min(depth, a.swa);
+      const bool live = tree_live(a, seq, token, lane == 0);
+      if (live && a.parent != nullptr) {
+        n = tree_walk(a, seq, token, path[g], depth, true);
+      } else {
+        for (int i = lane; i < n; i += 32) path[g][i] = token - i;
+      }
+      TreeWindow w;
+      tree_ring(a, seq, depth, w, lane == 0 && g == 0 && t0 == 0);
+      if (lane == 0) {
+        n_path[g] = live ? n : 0;
+        n_ring[g] = live ? w.n_ring : 0;
+        if (g == 0) newest_s = w.newest;
+      }
     }
-    sid[i] = e < 0 ? -1 : e;
-  }
-  __syncthreads();
-  // strictly ascending entries first, -1 behind them?
-  for (int i = tid; i < total; i += kPlanThreads) {
-    const int g = i / a.topk, j = i - g * a.topk, e = sid[i];
-    const int next = j + 1 < a.topk ? sid[i + 1] : -1;
-    if (next >= 0 && e >= next) merge = 0;     // (racing writes of the same value)
-    if (next >= 0 && e < 0) merge = 0;
-    if (e >= 0 && next < 0) n_list[g] = j + 1;
+  } else {
+    for (int g = 0; g < 2; ++g) {
+      const bool live = g < ng && tree_live(a, seq, t0 + g, false);
+      for (int j = tid; j < a.topk; j += kListThreads) {
+        int e = live ? a.idx[((long long)seq * a.tokens + t0 + g) * a.topk + j] : -1;
+        if (e >= a.n_entries) {
+          report(a.err, kErrBadIndex, e);
+          e = -1;
+        }
+        sid[g * a.topk + j] = e < 0 ? -1 : e;
+      }
+    }
   }
   __syncthreads();
+  // Do both lists ascend strictly, with nothing but -1 behind their entries?
+  if (warp < kListWarps)
+    for (int g = 0; g < 2; ++g)
+      for (int j = tid; j < a.topk; j += kListThreads) {
+        const int e = sid[g * a.topk + j], next = j + 1 < a.topk ? sid[g * a.topk + j + 1] : -1;
+        if (next >= 0 && e >= next) ordered = 0;   // (racing writes of the same value)
+        if (next >= 0 && e < 0) ordered = 0;
+        if (e >= 0 && next < 0) n_list[g] = j + 1;
+      }
+  __syncthreads();
+  const int max_keys = plan_keys(a.topk, a.swa, a.tokens, group);
   uint32_t* out = plan + (long long)blockIdx.x * plan_stride(a, group);
+  uint32_t* entries = out + plan_entries(max_keys);
+  const bool merge = ordered != 0;
   // Both tokens' keys first, then either's own: most tiles are then wholly a
   // token's or wholly not, which the softmax takes without looking at keys.
-  const uint32_t all = (1u << ng) - 1u;
-  uint32_t masks = 0;                          // this thread's elements, 4 bits each: mask, 0 where not listed
-  int n_main = 0;
-  for (int i0 = 0, x = 0; i0 < total; i0 += kPlanThreads, ++x) {
-    const int i = i0 + tid;
-    const int e = i < total ? sid[i] : -1;
-    const int g = i < total ? i / a.topk : 0;
-    uint32_t mask = e >= 0 ? 1u << g : 0u;
-    if (e >= 0 && merge && ng == 2) {
-      const int* list = sid + (1 - g) * a.topk;
-      int lo = 0, hi = n_list[1 - g];          // first element >= e
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (list[mid] < e) lo = mid + 1;
-        else hi = mid;
+  // Without order nothing is merged, and a list's entries are counted instead.
+  int n_both = 0, n_own[2];
+  bool hit[kChunks] = {};
+  for (int g = 0; g < (merge ? 1 : 2); ++g) {  // marks: shared entries of the first list, or any entries of either
+    int before[kChunks];
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      const int j = x * kListThreads + tid;
+      bool mark = false;
+      if (warp < kListWarps && j < a.topk) {
+        const int e = sid[g * a.topk + j];
+        if (merge) {
+          if (j < n_list[0]) below(sid + a.topk, n_list[1], e, hit[x]);
+          mark = hit[x];
+        } else {
+          mark = e >= 0;
+        }
       }
-      if (lo < n_list[1 - g] && list[lo] == e) mask = g == 0 ? 3u : 0u;
+      const unsigned m = __ballot_sync(0xffffffffu, mark);
+      before[x] = __popc(m & ((1u << lane) - 1u));
+      if (warp < kListWarps && lane == 0) warp_s[x * kListWarps + warp] = __popc(m);
     }
-    masks |= mask << (4 * x);                  // (at most 2,048 elements: x < 4)
+    __syncthreads();
+    const int v = warp_s[lane];                // (kChunks * kListWarps == 32)
+    int incl = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const int total = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      const int j = x * kListThreads + tid;
+      const int at = __shfl_sync(0xffffffffu, incl - v, (x * kListWarps + warp) & 31) + before[x];
+      if (warp >= kListWarps || j >= a.topk) continue;
+      if (merge) {
+        rank[j] = at;
+      } else if (sid[g * a.topk + j] >= 0) {
+        entries[(g == 0 ? 0 : n_own[0]) + at] = uint32_t(sid[g * a.topk + j]) | (1u << (kRow + g));
+      }
+    }
+    if (merge) {
+      n_both = total;
+      if (tid == 0) rank[a.topk] = total;
+    } else {
+      n_own[g] = total;
+    }
+    __syncthreads();
   }
-  for (uint32_t want = all; want != 0; --want) {
-    for (int i0 = 0, x = 0; i0 < total; i0 += kPlanThreads, ++x) {
-      const bool keep = ((masks >> (4 * x)) & 15u) == want;
-      const int at = block_slot(keep, n_main, warp_s);
-      if (keep) out[kHeader + at] = uint32_t(sid[i0 + tid]) | (want << kRow);
+  if (merge) {
+    n_own[0] = n_list[0] - n_both;
+    n_own[1] = n_list[1] - n_both;
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      const int j = x * kListThreads + tid;
+      if (warp >= kListWarps || j >= a.topk) continue;
+      if (j < n_list[0])
+        entries[hit[x] ? rank[j] : n_both + j - rank[j]] = uint32_t(sid[j]) | ((hit[x] ? 3u : 1u) << kRow);
+      if (j < n_list[1]) {                     // shared entries below: those of the first list below it
+        bool both;
+        const int e = sid[a.topk + j], lo = below(sid, n_list[0], e, both);
+        if (!both) entries[n_both + n_own[0] + j - (lo < a.topk ? rank[lo] : n_both)] = uint32_t(e) | (2u << kRow);
+      }
     }
   }
+  const int n_main = n_both + n_own[0] + n_own[1];
   // committed rows, newest first, to the tokens whose window reaches them
-  int ring = 0;
-  for (int g = 0; g < ng; ++g) ring = max(ring, n_ring[g]);
+  const int ring = max(n_ring[0], n_ring[1]);
   for (int i = tid; i < ring; i += kPlanThreads) {
-    uint32_t mask = 0;
-    for (int g = 0; g < ng; ++g) mask |= i < n_ring[g] ? 1u << g : 0u;
     int r = newest_s - i;
     if (r < 0) r += a.swa;
-    out[kHeader + n_main + i] = uint32_t(r) | (mask << kRow);
+    entries[n_main + i] = uint32_t(r) | ((i < n_ring[0] ? 1u : 0u) | (i < n_ring[1] ? 2u : 0u)) << kRow;
   }
-  // drafted rows on the paths
+  // drafted rows on the paths, by the first warp: 32 at a time, each token's bits kept for the masks
   for (int g = 0; g < ng; ++g)
     for (int i = tid; i < n_path[g]; i += kPlanThreads) atomicOr(&drafted[path[g][i]], 1u << g);
   __syncthreads();
-  int n_all = n_main + ring;
-  const uint32_t mask = tid < a.tokens ? drafted[tid] : 0;
-  const int at = block_slot(mask != 0, n_all, warp_s);
-  if (mask != 0) out[kHeader + at] = uint32_t(tid) | (mask << kRow);
-  if (tid == 0) {
-    out[0] = uint32_t(n_main);
-    out[1] = uint32_t(ring);
-    out[2] = uint32_t(n_all - n_main - ring);
+  if (warp == 0) {
+    int n = n_main + ring;
+    for (int t = 0; t < a.tokens; t += 32) {
+      const uint32_t mask = t + lane < a.tokens ? drafted[t + lane] : 0;
+      const unsigned m = __ballot_sync(0xffffffffu, mask != 0);
+      const int at = n + __popc(m & ((1u << lane) - 1u));
+      if (mask != 0) entries[at] = uint32_t(t + lane) | (mask << kRow);
+      __syncwarp();
+      if (mask != 0) path[0][at - n_main - ring] = int(mask);   // the paths have been read
+      n += __popc(m);
+    }
+    if (lane == 0) {
+      out[0] = uint32_t(n_main);
+      out[1] = uint32_t(ring);
+      out[2] = uint32_t(n - n_main - ring);
+      n_path[0] = n - n_main - ring;
+    }
+  }
+  __syncthreads();
+  // the tiles' masks: 32 keys w of token g at word (w / 2) * 4 + 2 g + w % 2
+  const int n_draft = n_path[0], draft0 = n_main + ring;
+  for (int i = tid; i < max_keys / kTile * 4; i += kPlanThreads) {
+    const int g = (i >> 1) & 1, at = ((i >> 2) * 2 + (i & 1)) * 32;
+    uint32_t m = range_bits(at, 0, n_both) | range_bits(at, n_main, n_main + n_ring[g]) |
+                 (g == 0 ? range_bits(at, n_both, n_both + n_own[0]) : range_bits(at, n_both + n_own[0], n_main));
+    for (int x = max(at, draft0); x < min(at + 32, draft0 + n_draft); ++x)
+      if ((path[0][x - draft0] >> g) & 1) m |= 1u << (x - at);
+    out[kHeader + i] = m;
   }
 }
 
 // ------------------------------------------------------------------ attention
 
-constexpr int kTile = 64;                      // keys a stage
 constexpr int kKBytes = kTile * kDk * 2, kVBytes = kTile * kDv * 2;
 constexpr int kStages = 5;
-constexpr int kSoftmaxWarps = 4, kEndWarps = 4, kProducerWarps = 4;
+constexpr int kSoftmaxWarps = 4, kEndWarps = 4, kProducerWarps = 7;
+constexpr int kFours = (kTile / 4 + kProducerWarps - 1) / kProducerWarps;   // fours of keys of a producer warp
+constexpr int kWarpKeys = 4 * kFours;
+static_assert(kWarpKeys <= 32, "a lane for every key");
 constexpr int kThreads = 32 * (kSoftmaxWarps + kEndWarps + kProducerWarps + 1);
 constexpr uint32_t kTmemCols = 512;            // a power of two over two O (128 each), two S (64 each) and Q (96)
 constexpr uint32_t kOCol = 0, kSCol = 256, kQCol = 384;
@@ -203,10 +280,9 @@ constexpr uint32_t kOCol = 0, kSCol = 256, kQCol = 384;
 struct Shared {
   uint8_t k[kStages][kKBytes];                 // 3 blocks of 64 dims: 64 rows of 128 bytes
   uint8_t v[kStages][kVBytes];                 // 2 blocks of 64 dims: 64 keys of 128 bytes
-  uint64_t row[kProducerWarps][2][16][2];      // K and V addresses of a producer warp's keys, of even and odd tiles
+  uint64_t row[kProducerWarps][2][kWarpKeys][2];   // K and V addresses of a producer warp's keys, of even and odd tiles
   uint4 turn[kEndWarps][32 * 4];               // 64 bytes of each of an end warp's rows
   float2 stat[128];                            // (exponent, sum) of the rows of an item
-  uint64_t mask[kStages][2];                   // the tile's keys of each token
   uint64_t full[kStages], empty[kStages];      // a tile has landed; has been used
   uint64_t s_full[2], p_full[2];               // S has been computed; P has been written
   uint64_t o_done, o_last[2], o_free[2];       // O holds a tile more; the item's last; has been read
@@ -336,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&c.full[i], 32 * kProducerWarps + 2 * kProducerWarps);   // every producer's copies, the masks
+      mbar_init(&c.full[i], 32 * kProducerWarps);
       mbar_init(&c.empty[i], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -362,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = c.tmem;
   pdl_wait();
   const int per_seq = (a.tokens + group - 1) / group, stride = plan_stride(a, group);
+  const int first_key = plan_entries(plan_keys(a.topk, a.swa, a.tokens, group));
   const float sl2 = a.scale * 1.4426950408889634f;
   auto keys_of = [&](int item) -> int {
     const uint32_t* list = plan + (long long)item * stride;
@@ -372,21 +449,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- softmax: thread = row
     const int token = tid >> 6;                               // of the group (uniform in a warp)
     const uint32_t lanes = uint32_t(warp * 32) << 16;
+    const float2 scale2 = make_float2(sl2, sl2);
     uint32_t tiles = 0, items = 0;                            // of this CTA so far
     bool ok = true;
     for (int item = blockIdx.x; item < n_groups && ok; item += gridDim.x) {
       const int nt = (keys_of(item) + kTile - 1) / kTile;
       if (nt == 0) continue;
+      const uint64_t* masks = reinterpret_cast<const uint64_t*>(plan + (long long)item * stride + kHeader) + token;
+      uint64_t mask_next = masks[0];                          // the token's keys of the next tile
       const uint32_t o_addr = tmem + lanes + kOCol + (items & 1) * 128;
       float ref = -INFINITY, sum = 0.f;        // the exponent that P and O are relative to, and the weights' sum
       for (int i = 0; i < nt; ++i, ++tiles) {
-        const uint32_t buf = tiles & 1, st = tiles % kStages;
-        ok = tc_wait_warp(c, &c.full[st], (tiles / kStages) & 1, a.err) &&
-             tc_wait_warp(c, &c.s_full[buf], (tiles >> 1) & 1, a.err);
+        const uint64_t mask = mask_next;
+        if (i + 1 < nt) mask_next = masks[2 * (i + 1)];
+        const uint32_t buf = tiles & 1, s_addr = tmem + lanes + kSCol + buf * 64;
+        ok = tc_wait_warp(c, &c.s_full[buf], (tiles >> 1) & 1, a.err);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t mask = c.mask[st][token];
-        const uint32_t s_addr = tmem + lanes + kSCol + buf * 64;
         uint32_t p[32];
         if (mask != 0) {
           uint32_t s[64];
@@ -397,13 +476,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 64; ++j)
               if (!(((j < 32 ? lo : hi) >> (j & 31)) & 1u)) s[j] = 0xff800000u;   // -inf
           }
-          float m0 = -INFINITY, m1 = -INFINITY;
+          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            m0 = fmaxf(m0, __uint_as_float(s[j]));
-            m1 = fmaxf(m1, __uint_as_float(s[32 + j]));
-          }
-          const float top = fmaxf(m0, m1) * sl2;
+          for (int j = 0; j < 64; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[e] = max3(m[e], __uint_as_float(s[j + 2 * e]), __uint_as_float(s[j + 2 * e + 1]));
+          const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * sl2;
           const bool grows = top > ref + 8.f;
           if (i == 0) {
             ref = top;
@@ -417,25 +495,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (grows) ref = top;
             sum *= f;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-              uint32_t o[32];
-              tmem_ld32(o, o_addr + 32 * q);
+            for (int q = 0; q < 8; ++q) {
+              uint32_t o[16];
+              tmem_ld16(o, o_addr + 16 * q);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(o_addr + 32 * q, o);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(o_addr + 16 * q, o);
             }
           }
-          const float base = ref == -INFINITY ? 0.f : ref;
-          float s0 = 0.f, s1 = 0.f;
+          const float base = ref == -INFINITY ? 0.f : -ref;
+          const float2 base2 = make_float2(base, base);
+          float2 total = make_float2(0.f, 0.f), other = make_float2(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
-            const float x = ex2(__fmaf_rn(__uint_as_float(s[2 * j]), sl2, -base));
-            const float y = ex2(__fmaf_rn(__uint_as_float(s[2 * j + 1]), sl2, -base));
-            s0 += x;
-            s1 += y;
-            p[j] = pack_bf16(x, y);
+            float2 x = fma2(make_float2(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1])), scale2, base2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            if (j & 1) other = add2(other, x);
+            else total = add2(total, x);
+            p[j] = pack_bf16(x.x, x.y);
           }
-          sum += s0 + s1;
+          total = add2(total, other);
+          sum += total.x + total.y;
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) p[j] = 0;
@@ -462,31 +543,33 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seq = item / per_seq, t = (item - seq * per_seq) * group + token;
       return token < group && t < a.tokens ? seq * a.tokens + t : -1;
     };
-    uint4 q[24];                                              // a group's queries: 64 bytes of the rows in every four
-    auto fetch_q = [&](int item) {
+    // A group's queries by thirds of 128 bytes a row: 64 bytes of the rows in every four pieces.
+    uint4 q[8];
+    auto fetch_q = [&](int item, int third) {
       const int query = query_of(item);
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
-                                                        ((long long)max(query, 0) * kH + head0) * (kDk * 2));
+                                                        ((long long)max(query, 0) * kH + head0) * (kDk * 2)) + third * 8;
 #pragma unroll
-      for (int x = 0; x < 24; ++x)
+      for (int x = 0; x < 8; ++x)
         q[x] = query >= 0 ? src[(8 * (x & 3) + (lane >> 2)) * (kDk / 8) + (x >> 2) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
     };
-    auto store_q = [&]() {
-#pragma unroll
+    auto store_q = [&](int item) {                            // the first third has been fetched
+#pragma unroll 1
       for (int b = 0; b < 3; ++b) {
         uint32_t r[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          lines_to_rows(turn, q + 8 * b + 4 * h);
+          lines_to_rows(turn, q + 4 * h);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const uint4 y = q[8 * b + 4 * h + x];
+            const uint4 y = q[4 * h + x];
             r[16 * h + 4 * x] = y.x;
             r[16 * h + 4 * x + 1] = y.y;
             r[16 * h + 4 * x + 2] = y.z;
             r[16 * h + 4 * x + 3] = y.w;
           }
         }
+        if (b < 2) fetch_q(item, b + 1);
         tmem_st32(tmem + lanes + kQCol + 32 * b, r);
       }
       tc_wait_st();
@@ -500,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t items = 0;
     const int first = next_item(blockIdx.x);
     if (first < n_groups) {
-      fetch_q(first);
-      store_q();
+      fetch_q(first, 0);
+      store_q(first);
     }
     for (int item = blockIdx.x; item < n_groups; item += gridDim.x) {
       const int query = query_of(item);
@@ -517,10 +600,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int next = next_item(item + gridDim.x);
       if (next < n_groups) {
-        fetch_q(next);
+        fetch_q(next, 0);
         if (!tc_wait_warp(c, &c.q_empty, items & 1, a.err)) break;
         tc_fence_after();
-        store_q();
+        store_q(next);
       }
       if (!tc_wait_warp(c, &c.stat_full, items & 1, a.err)) break;
       const float ref = c.stat[row].x, sum = c.stat[row].y;
@@ -563,18 +646,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t* list = plan + (long long)item * stride;
         const float base = __shfl_sync(0xffffffffu, ref == -INFINITY ? 0.f : ref, l);
         const float scale = __shfl_sync(0xffffffffu, inv, l);
-        float4 o = row_alone(a, item / per_seq, query, head0 + l, token, list + kHeader, int(list[0]), int(list[1]), n_all, sl2, base);
+        float4 o = row_alone(a, item / per_seq, query, head0 + l, token, list + first_key, int(list[0]), int(list[1]), n_all, sl2, base);
         if (scale == 0.f) o = make_float4(0.f, 0.f, 0.f, 0.f);   // no key at all
         reinterpret_cast<uint2*>(out)[l * (kDv / 4) + lane] =
             make_uint2(pack_bf16(o.x * scale, o.y * scale), pack_bf16(o.z * scale, o.w * scale));
       }
     }
   } else if (warp < kSoftmaxWarps + kEndWarps + kProducerWarps) {
-    // ---------------------------------------------------------------- producers: 16 keys of a tile a warp
+    // ---------------------------------------------------------------- producers: every seventh four keys of a tile a warp
     const int w = warp - kSoftmaxWarps - kEndWarps;
     // The 16-byte pieces of four keys (K row: 0..23, V row: 24..39 of each) in
-    // five copies a lane; key 4 q + x lies at row 16 w + 4 q + x of the tile,
-    // whose low three bits swizzle: those of x, and 4 more for odd q.
+    // five copies a lane.  Key x of four f lies at row 4 f + x of the tile,
+    // whose low three bits swizzle: those of x, and 4 more for odd f.
     int p_row[5], p_src[5], p_dst[5];
     bool p_k[5];
 #pragma unroll
@@ -584,49 +667,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int y = p_k[k] ? part : part - 24;
       p_row[k] = 2 * x + (p_k[k] ? 0 : 1);
       p_src[k] = y * 16;
-      p_dst[k] = (y >> 3) * (kTile * 128) + (w * 16 + x) * 128 + (((y & 7) ^ x) << 4);
+      p_dst[k] = (y >> 3) * (kTile * 128) + x * 128 + (((y & 7) ^ x) << 4);
     }
-    uint32_t tiles = 0;
+    const int mine = 4 * (w + kProducerWarps * (lane >> 2)) + (lane & 3);   // this lane's key of a tile
+    const bool on = lane < kWarpKeys && mine < kTile;
+    uint32_t tiles = 0, st = 0, lap = 0;
     bool ok = true;
     for (int item = blockIdx.x; item < n_groups && ok; item += gridDim.x) {
       const uint32_t* list = plan + (long long)item * stride;
       const int n_main = int(list[0]), n_ring = int(list[1]), n_all = n_main + n_ring + int(list[2]);
       const int seq = item / per_seq, nt = (n_all + kTile - 1) / kTile;
-      list += kHeader;
-      int pos = w * 16 + (lane & 15);
+      list += first_key;
+      int pos = on ? mine : n_all;
       uint32_t entry = pos < n_all ? list[pos] : 0;
       for (int i = 0; i < nt; ++i, ++tiles) {
         const Key key = resolve(a, seq, pos, entry, n_main, n_ring, n_all);
         pos += kTile;
         entry = pos < n_all ? list[pos] : 0;   // of the next tile
         uint64_t(*row)[2] = c.row[w][tiles & 1];
-        if (lane < 16) {
+        if (lane < kWarpKeys) {
           row[lane][0] = reinterpret_cast<uint64_t>(key.k);
           row[lane][1] = reinterpret_cast<uint64_t>(key.v);
         }
-        const uint32_t st = tiles % kStages;
-        ok = tc_wait_warp(c, &c.empty[st], ((tiles / kStages) & 1) ^ 1, a.err);   // (and the warp's rows are written)
+        ok = tc_wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
         if (!ok) break;
-        __syncwarp();
-        // the masks of this warp's 16 keys
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const unsigned m = __ballot_sync(0xffffffffu, lane < 16 && ((key.mask >> g) & 1u));
-          if (lane == g) reinterpret_cast<uint16_t*>(&c.mask[st][g])[w] = uint16_t(m);
-        }
-        if (lane < 2) mbar_arrive(&c.full[st]);   // the masks; the copies arrive by themselves
+        __syncwarp();                          // the warp's rows are written
         const uint32_t k_st = smem_u32(c.k[st]), v_st = smem_u32(c.v[st]);
-        uint64_t src[4][5];
+        uint64_t src[kFours][5];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kFours; ++q)
 #pragma unroll
           for (int k = 0; k < 5; ++k) src[q][k] = (&row[4 * q][0])[p_row[k]];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < kFours; ++q) {
+          const int f = w + kProducerWarps * q;
+          if (f < kTile / 4) {                 // a warp's last may not exist
 #pragma unroll
-          for (int k = 0; k < 5; ++k)
-            cp16(((p_k[k] ? k_st : v_st) + p_dst[k] + q * 512) ^ ((q & 1) * 64), src[q][k], p_src[k], a.k_main);
+            for (int k = 0; k < 5; ++k)
+              cp16(((p_k[k] ? k_st : v_st) + p_dst[k] + f * 512) ^ ((f & 1) * 64), src[q][k], p_src[k], a.k_main);
+          }
+        }
         cp_arrive(&c.full[st]);
+        if (++st == kStages) {
+          st = 0;
+          ++lap;
+        }
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -635,11 +720,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t qk_desc = idesc_bf16(128, kTile, false), pv_desc = idesc_bf16(128, kDv, true);
     const uint64_t k0 = smem_desc(smem_u32(c.k[0]), 16, 1024), v0 = smem_desc(smem_u32(c.v[0]), kTile * 128, 1024);
     uint32_t tiles = 0, items = 0;
+    uint32_t st = 0, lap = 0, st_pv = 0;       // stage of the next scores, times round the ring, stage of the next O
     bool ok = true;
     // O (+)= P V of tile x, of the current item
     auto pv = [&](uint32_t x, bool first, bool last) -> bool {
-      const uint32_t st = x % kStages, buf = x & 1, o = items & 1;
-      const uint64_t v = v0 + st * (kVBytes >> 4);
+      const uint32_t buf = x & 1, o = items & 1;
+      const uint64_t v = v0 + st_pv * (kVBytes >> 4);
       if (first && items > 1 && !tc_wait_warp(c, &c.o_free[o], ((items >> 1) - 1) & 1, a.err)) return false;
       if (!tc_wait_warp(c, &c.p_full[buf], (x >> 1) & 1, a.err)) return false;
       tc_fence_after();
@@ -647,20 +733,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k)
           mma_ts(tmem + kOCol + o * 128, tmem + kSCol + buf * 64 + 8 * k, v + k * (2048 >> 4), pv_desc, !(first && k == 0));
-        tc_commit(&c.empty[st]);
+        tc_commit(&c.empty[st_pv]);
         tc_commit(&c.o_done);
         if (last) tc_commit(&c.o_last[o]);
       }
       __syncwarp();
+      st_pv = st_pv + 1 == kStages ? 0 : st_pv + 1;
       return true;
     };
     for (int item = blockIdx.x; item < n_groups && ok; item += gridDim.x) {
       const int nt = (keys_of(item) + kTile - 1) / kTile;
       if (nt == 0) continue;
       for (int i = 0; i < nt && ok; ++i, ++tiles) {
-        const uint32_t st = tiles % kStages, buf = tiles & 1;
-        ok = tc_wait_warp(c, &c.full[st], (tiles / kStages) & 1, a.err) &&
-             (i > 0 || tc_wait_warp(c, &c.q_full, items & 1, a.err));
+        const uint32_t buf = tiles & 1;
+        ok = tc_wait_warp(c, &c.full[st], lap & 1, a.err) && (i > 0 || tc_wait_warp(c, &c.q_full, items & 1, a.err));
         if (!ok) break;
         fence_async_smem();                    // the copies are generic-proxy writes, the tensor core reads by the async proxy
         tc_fence_after();
@@ -674,6 +760,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (i == nt - 1) tc_commit(&c.q_empty);
         }
         __syncwarp();
+        if (++st == kStages) {
+          st = 0;
+          ++lap;
+        }
         if (i > 0) ok = pv(tiles - 1, i == 1, false);
       }
       if (!ok) break;
@@ -697,7 +787,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Words of the plan of a launch.
 size_t tree_plan_words(int seqs, int tokens, int topk, int swa) {
   const int group = tokens > 1 ? 2 : 1;
-  return size_t(seqs) * ((tokens + group - 1) / group) * (size_t(kHeader) + size_t(group) * topk + swa + tokens);
+  const int keys = plan_keys(topk, swa, tokens, group);
+  return size_t(seqs) * ((tokens + group - 1) / group) * size_t(plan_entries(keys) + keys);
 }
 
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStream_t st) {
@@ -708,7 +799,7 @@ cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStr
   const int group = a.tokens > 1 ? 2 : 1, n_groups = seqs * ((a.tokens + group - 1) / group);
   const uint32_t* words = static_cast<const uint32_t*>(plan);
   note_launch();
-  e = launch_pdl(tree_plan_kernel, dim3(unsigned(n_groups)), dim3(kPlanThreads), size_t(group) * a.topk * 4, st, 1, a,
+  e = launch_pdl(tree_plan_kernel, dim3(unsigned(n_groups)), dim3(kPlanThreads), (size_t(3) * a.topk + 1) * 4, st, 1, a,
                  static_cast<uint32_t*>(plan), group);
   if (e != cudaSuccess) return e;
   const int grid = n_groups < device_sm_count() ? n_groups : device_sm_count();
