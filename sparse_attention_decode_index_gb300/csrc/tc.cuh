@@ -157,9 +157,9 @@ CSA2_DEV float2 add2(float2 a, float2 b) {
   return d;
 }
 
-CSA2_DEV float max3(float a, float b, float c) {
+CSA2_DEV float max3_nan(float a, float b, float c) {   // NaN if any of them is
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 

@@ -12,7 +12,6 @@
 //   exp2(s - lse) over the heads in fixed order.  No maximum is needed, the
 //   lse is the normaliser.  It reads 60 % of what the attention reads (K only).
 // weights_generic_kernel -- any shape: a warp per slot.
-#include <cstdlib>
 #include "common.cuh"
 #include "internal.h"
 #include "tree.cuh"
@@ -294,12 +293,14 @@ __global__ void __launch_bounds__(256) weights_generic_kernel(const AttnWeightsA
   if (lane == 0 && j < a.topk) a.weights[(long long)b * a.topk + j] = w;
 }
 
-// Pairs of tokens on the tensor cores, or a cluster of CTAs per query.
+// A cluster of CTAs per query while all the clusters run at once (up to 7/8 of
+// two CTAs an SM: clusters do not fill every SM), pairs of tokens on the tensor
+// cores beyond.  Measured, clusters / pairs, 512 + 128 slots: 64 queries of one
+// token 15.3 / 15.0 us, 66 of trees of 33 16.4 / 19.9, 76 of trees of 4 25.9 / 19.0,
+// 256 of one token 60 / 26, 256 of trees of 16 59 / 21.
 bool tree_pairs(const TreeArgs& a, int batch, size_t plan_bytes) {
-  static const int force = getenv("CSA2_GROUP") ? atoi(getenv("CSA2_GROUP")) : -1;
   if (tree_plan_words(batch / a.tokens, a.tokens, a.topk, a.swa) * 4 > plan_bytes) return false;
-  if (force >= 0) return force > 0;
-  return false;
+  return 8 * batch * attn_cluster(a.topk, a.swa) > 7 * 2 * device_sm_count();
 }
 
 }  // namespace

@@ -62,21 +62,21 @@ __host__ __device__ constexpr int plan_entries(int keys) { return kHeader + keys
 
 // ------------------------------------------------------------------ plan
 
-// 16 warps for the lists, a warp for each token's path.
-constexpr int kListThreads = 512, kListWarps = kListThreads / 32, kPlanThreads = kListThreads + 64;
-constexpr int kChunks = 2;                     // list elements a thread takes of each list: topk <= 1,024
+// 8 warps for the lists, a warp for each token's path: 6 blocks an SM, so that the groups of a large batch run at once.
+constexpr int kListThreads = 256, kListWarps = kListThreads / 32, kPlanThreads = kListThreads + 64;
+constexpr int kChunks = 4;                     // list elements a thread takes of each list: topk <= 1,024
 
 CSA2_DEV int plan_stride(const TreeArgs& a, int group) {
   const int keys = plan_keys(a.topk, a.swa, a.tokens, group);
   return plan_entries(keys) + keys;
 }
 
-// Elements of `list` [n], ascending, below e; `hit`: whether e is one.
+// Elements of `list` [n], ascending with -1 behind them, below e; `hit`: whether e is one.
 CSA2_DEV int below(const int* list, int n, int e, bool& hit) {
   int lo = 0, hi = n;
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
-    if (list[mid] < e) lo = mid + 1;
+    if (uint32_t(list[mid]) < uint32_t(e)) lo = mid + 1;   // (-1 is above all)
     else hi = mid;
   }
   hit = lo < n && list[lo] == e;
@@ -90,48 +90,34 @@ CSA2_DEV uint32_t range_bits(int at, int from, int to) {
   return (hi == 32 ? ~0u : (1u << hi) - 1u) & ~((1u << lo) - 1u);
 }
 
-// Bound by the latency of its steps (load, search, count, write), one block a group.
+// One block a group, bound by the latency of its steps (load, search, count,
+// write): loads that do not need each other go out together, and the paths are
+// walked beside the search.
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs a, uint32_t* plan, int group) {
   extern __shared__ int sid[];                 // [2][topk], then the ranks [topk + 1]
   int* rank = sid + 2 * a.topk;                // keys of the first list before each that the second has too
   __shared__ int path[2][kMaxTreeTokens];
-  __shared__ int n_path[2], n_ring[2], n_list[2];
+  __shared__ int n_ring[2], n_list[2], n_draft;
   __shared__ uint32_t drafted[kMaxTreeTokens];
-  __shared__ int warp_s[kChunks * kListWarps];
+  __shared__ int warp_s[2][kChunks * kListWarps];
   __shared__ int ordered, newest_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool lists = warp < kListWarps;
   const int per_seq = (a.tokens + group - 1) / group;
   const int seq = blockIdx.x / per_seq, t0 = (blockIdx.x - seq * per_seq) * group;
   const int ng = min(group, a.tokens - t0);
   pdl_launch_dependents();   // the attention's CTAs set themselves up meanwhile, and wait for this launch's end
   if (tid == 0) ordered = 1;
   if (tid < kMaxTreeTokens) drafted[tid] = 0;
-  if (tid < 2) n_list[tid] = n_path[tid] = n_ring[tid] = 0;
+  if (tid < 2) n_list[tid] = n_ring[tid] = 0;
   __syncthreads();
   pdl_wait();
-  if (warp >= kListWarps) {
-    const int g = warp - kListWarps, token = t0 + g;
-    if (g < ng) {
-      int depth = token + 1, n = min(depth, a.swa);
-      const bool live = tree_live(a, seq, token, lane == 0);
-      if (live && a.parent != nullptr) {
-        n = tree_walk(a, seq, token, path[g], depth, true);
-      } else {
-        for (int i = lane; i < n; i += 32) path[g][i] = token - i;
-      }
-      TreeWindow w;
-      tree_ring(a, seq, depth, w, lane == 0 && g == 0 && t0 == 0);
-      if (lane == 0) {
-        n_path[g] = live ? n : 0;
-        n_ring[g] = live ? w.n_ring : 0;
-        if (g == 0) newest_s = w.newest;
-      }
-    }
-  } else {
+  if (lists) {
     for (int g = 0; g < 2; ++g) {
       const bool live = g < ng && tree_live(a, seq, t0 + g, false);
       for (int j = tid; j < a.topk; j += kListThreads) {
-        int e = live ? a.idx[((long long)seq * a.tokens + t0 + g) * a.topk + j] : -1;
+        int e = g < ng ? a.idx[((long long)seq * a.tokens + t0 + g) * a.topk + j] : -1;   // (does not wait for `live`)
+        if (!live) e = -1;
         if (e >= a.n_entries) {
           report(a.err, kErrBadIndex, e);
           e = -1;
@@ -141,127 +127,147 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
     }
   }
   __syncthreads();
-  // Do both lists ascend strictly, with nothing but -1 behind their entries?
-  if (warp < kListWarps)
-    for (int g = 0; g < 2; ++g)
-      for (int j = tid; j < a.topk; j += kListThreads) {
+  const int max_keys = plan_keys(a.topk, a.swa, a.tokens, group);
+  uint32_t* out = plan + (long long)blockIdx.x * plan_stride(a, group);
+  uint32_t* entries = out + plan_entries(max_keys);
+  int* ids = path[0];                          // the drafted rows on either path, when both have been walked
+  bool hit[kChunks] = {};                      // this thread's elements of the first list: the second has them
+  int before[2][kChunks] = {};                 // elements of the warp's before them: shared ones, or any, of either list
+  int lower[kChunks] = {};                     // of the second: elements of the first below them, -1 where it has them
+  if (lists) {
+    // Do both lists ascend strictly, with nothing but -1 behind their entries?
+    // The searches take it for granted; without it nothing of theirs is used.
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {
+      if (x * kListThreads >= a.topk) break;
+      const int j = x * kListThreads + tid;
+      if (j >= a.topk) continue;
+      for (int g = 0; g < 2; ++g) {
         const int e = sid[g * a.topk + j], next = j + 1 < a.topk ? sid[g * a.topk + j + 1] : -1;
         if (next >= 0 && e >= next) ordered = 0;   // (racing writes of the same value)
         if (next >= 0 && e < 0) ordered = 0;
         if (e >= 0 && next < 0) n_list[g] = j + 1;
       }
+      if (sid[j] >= 0) below(sid + a.topk, a.topk, sid[j], hit[x]);
+      if (sid[a.topk + j] >= 0) {
+        bool both;
+        lower[x] = below(sid, a.topk, sid[a.topk + j], both);
+        if (both) lower[x] = -1;
+      }
+    }
+  } else if (warp - kListWarps < ng) {
+    const int g = warp - kListWarps, token = t0 + g;
+    TreeWindow w;
+    tree_ring(a, seq, 0, w, lane == 0 && g == 0 && t0 == 0);
+    const bool live = tree_live(a, seq, token, lane == 0);
+    int depth = token + 1, n = min(depth, a.swa);
+    if (a.parent != nullptr) {
+      n = tree_walk(a, seq, token, path[g], depth, live);
+    } else {
+      for (int i = lane; i < n; i += 32) path[g][i] = token - i;
+    }
+    if (!live) n = 0;
+    __syncwarp();
+    for (int i = lane; i < n; i += 32) atomicOr(&drafted[path[g][i]], 1u << g);
+    if (lane == 0) {
+      n_ring[g] = live ? min(w.n_ring, max(0, a.swa - depth)) : 0;
+      if (g == 0) newest_s = w.newest;
+    }
+  }
   __syncthreads();
-  const int max_keys = plan_keys(a.topk, a.swa, a.tokens, group);
-  uint32_t* out = plan + (long long)blockIdx.x * plan_stride(a, group);
-  uint32_t* entries = out + plan_entries(max_keys);
   const bool merge = ordered != 0;
-  // Both tokens' keys first, then either's own: most tiles are then wholly a
-  // token's or wholly not, which the softmax takes without looking at keys.
-  // Without order nothing is merged, and a list's entries are counted instead.
-  int n_both = 0, n_own[2];
-  bool hit[kChunks] = {};
-  for (int g = 0; g < (merge ? 1 : 2); ++g) {  // marks: shared entries of the first list, or any entries of either
-    int before[kChunks];
+  if (lists) {
 #pragma unroll
     for (int x = 0; x < kChunks; ++x) {
       const int j = x * kListThreads + tid;
-      bool mark = false;
-      if (warp < kListWarps && j < a.topk) {
-        const int e = sid[g * a.topk + j];
-        if (merge) {
-          if (j < n_list[0]) below(sid + a.topk, n_list[1], e, hit[x]);
-          mark = hit[x];
-        } else {
-          mark = e >= 0;
-        }
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const bool mark = j < a.topk && (merge ? g == 0 && hit[x] : sid[g * a.topk + j] >= 0);
+        const unsigned m = __ballot_sync(0xffffffffu, mark);
+        before[g][x] = __popc(m & ((1u << lane) - 1u));
+        if (lane == 0) warp_s[g][x * kListWarps + warp] = __popc(m);
       }
-      const unsigned m = __ballot_sync(0xffffffffu, mark);
-      before[x] = __popc(m & ((1u << lane) - 1u));
-      if (warp < kListWarps && lane == 0) warp_s[x * kListWarps + warp] = __popc(m);
     }
-    __syncthreads();
-    const int v = warp_s[lane];                // (kChunks * kListWarps == 32)
+  } else if (warp == kListWarps) {
+    // the drafted rows in order, each with its mask
+    int n = 0;
+    for (int t = 0; t < a.tokens; t += 32) {
+      const uint32_t mask = t + lane < a.tokens ? drafted[t + lane] : 0;
+      const unsigned m = __ballot_sync(0xffffffffu, mask != 0);
+      if (mask != 0) ids[n + __popc(m & ((1u << lane) - 1u))] = int(uint32_t(t + lane) | (mask << kRow));
+      n += __popc(m);
+    }
+    if (lane == 0) n_draft = n;
+  }
+  __syncthreads();
+  int total[2], first[2][kChunks];             // marked elements, and those before this thread's
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int v = warp_s[g][lane];             // (kChunks * kListWarps == 32)
     int incl = v;
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
+    total[g] = __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x)
+      first[g][x] = __shfl_sync(0xffffffffu, incl - v, (x * kListWarps + warp) & 31) + before[g][x];
+  }
+  // Both tokens' keys first, then either's own: most tiles are then wholly a
+  // token's or wholly not, which the softmax takes without looking at keys.
+  const int n_both = merge ? total[0] : 0;
+  const int n_a = merge ? n_list[0] - n_both : total[0], n_b = merge ? n_list[1] - n_both : total[1];
+  const int n_main = n_both + n_a + n_b;
+  if (lists) {
 #pragma unroll
     for (int x = 0; x < kChunks; ++x) {
       const int j = x * kListThreads + tid;
-      const int at = __shfl_sync(0xffffffffu, incl - v, (x * kListWarps + warp) & 31) + before[x];
-      if (warp >= kListWarps || j >= a.topk) continue;
+      if (j >= a.topk) break;
+      const int e = sid[j], f = sid[a.topk + j];
       if (merge) {
-        rank[j] = at;
-      } else if (sid[g * a.topk + j] >= 0) {
-        entries[(g == 0 ? 0 : n_own[0]) + at] = uint32_t(sid[g * a.topk + j]) | (1u << (kRow + g));
-      }
-    }
-    if (merge) {
-      n_both = total;
-      if (tid == 0) rank[a.topk] = total;
-    } else {
-      n_own[g] = total;
-    }
-    __syncthreads();
-  }
-  if (merge) {
-    n_own[0] = n_list[0] - n_both;
-    n_own[1] = n_list[1] - n_both;
-#pragma unroll
-    for (int x = 0; x < kChunks; ++x) {
-      const int j = x * kListThreads + tid;
-      if (warp >= kListWarps || j >= a.topk) continue;
-      if (j < n_list[0])
-        entries[hit[x] ? rank[j] : n_both + j - rank[j]] = uint32_t(sid[j]) | ((hit[x] ? 3u : 1u) << kRow);
-      if (j < n_list[1]) {                     // shared entries below: those of the first list below it
-        bool both;
-        const int e = sid[a.topk + j], lo = below(sid, n_list[0], e, both);
-        if (!both) entries[n_both + n_own[0] + j - (lo < a.topk ? rank[lo] : n_both)] = uint32_t(e) | (2u << kRow);
+        rank[j] = first[0][x];
+        if (e >= 0) entries[hit[x] ? first[0][x] : n_both + j - first[0][x]] = uint32_t(e) | ((hit[x] ? 3u : 1u) << kRow);
+      } else {
+        if (e >= 0) entries[first[0][x]] = uint32_t(e) | (1u << kRow);
+        if (f >= 0) entries[n_a + first[1][x]] = uint32_t(f) | (2u << kRow);
       }
     }
   }
-  const int n_main = n_both + n_own[0] + n_own[1];
-  // committed rows, newest first, to the tokens whose window reaches them
-  const int ring = max(n_ring[0], n_ring[1]);
+  // committed rows, newest first, to the tokens whose window reaches them; drafted rows
+  const int ring = max(n_ring[0], n_ring[1]), draft0 = n_main + ring;
   for (int i = tid; i < ring; i += kPlanThreads) {
     int r = newest_s - i;
     if (r < 0) r += a.swa;
     entries[n_main + i] = uint32_t(r) | ((i < n_ring[0] ? 1u : 0u) | (i < n_ring[1] ? 2u : 0u)) << kRow;
   }
-  // drafted rows on the paths, by the first warp: 32 at a time, each token's bits kept for the masks
-  for (int g = 0; g < ng; ++g)
-    for (int i = tid; i < n_path[g]; i += kPlanThreads) atomicOr(&drafted[path[g][i]], 1u << g);
-  __syncthreads();
-  if (warp == 0) {
-    int n = n_main + ring;
-    for (int t = 0; t < a.tokens; t += 32) {
-      const uint32_t mask = t + lane < a.tokens ? drafted[t + lane] : 0;
-      const unsigned m = __ballot_sync(0xffffffffu, mask != 0);
-      const int at = n + __popc(m & ((1u << lane) - 1u));
-      if (mask != 0) entries[at] = uint32_t(t + lane) | (mask << kRow);
-      __syncwarp();
-      if (mask != 0) path[0][at - n_main - ring] = int(mask);   // the paths have been read
-      n += __popc(m);
-    }
-    if (lane == 0) {
-      out[0] = uint32_t(n_main);
-      out[1] = uint32_t(ring);
-      out[2] = uint32_t(n - n_main - ring);
-      n_path[0] = n - n_main - ring;
-    }
+  for (int i = tid; i < n_draft; i += kPlanThreads) entries[draft0 + i] = uint32_t(ids[i]);
+  if (tid == 0) {
+    out[0] = uint32_t(n_main);
+    out[1] = uint32_t(ring);
+    out[2] = uint32_t(n_draft);
   }
-  __syncthreads();
   // the tiles' masks: 32 keys w of token g at word (w / 2) * 4 + 2 g + w % 2
-  const int n_draft = n_path[0], draft0 = n_main + ring;
   for (int i = tid; i < max_keys / kTile * 4; i += kPlanThreads) {
     const int g = (i >> 1) & 1, at = ((i >> 2) * 2 + (i & 1)) * 32;
     uint32_t m = range_bits(at, 0, n_both) | range_bits(at, n_main, n_main + n_ring[g]) |
-                 (g == 0 ? range_bits(at, n_both, n_both + n_own[0]) : range_bits(at, n_both + n_own[0], n_main));
+                 (g == 0 ? range_bits(at, n_both, n_both + n_a) : range_bits(at, n_both + n_a, n_main));
     for (int x = max(at, draft0); x < min(at + 32, draft0 + n_draft); ++x)
-      if ((path[0][x - draft0] >> g) & 1) m |= 1u << (x - at);
+      if ((uint32_t(ids[x - draft0]) >> (kRow + g)) & 1u) m |= 1u << (x - at);
     out[kHeader + i] = m;
+  }
+  if (!merge) return;
+  __syncthreads();                             // the ranks
+  if (lists) {
+#pragma unroll
+    for (int x = 0; x < kChunks; ++x) {        // the second's own: less the shared ones, which are the first's below it
+      const int j = x * kListThreads + tid;
+      if (j >= a.topk) break;
+      if (sid[a.topk + j] >= 0 && lower[x] >= 0) {
+        const int shared = lower[x] < n_list[0] ? rank[lower[x]] : n_both;
+        entries[n_both + n_a + j - shared] = uint32_t(sid[a.topk + j]) | (2u << kRow);
+      }
+    }
   }
 }
 
@@ -308,6 +314,19 @@ CSA2_DEV bool tc_wait(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
       }
     }
   }
+}
+
+// Whether a phase is over, without waiting: tests of several barriers are in flight at once, where waits follow each other.
+CSA2_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
 }
 
 // The same by a whole warp, which goes on or gives up together.
@@ -476,12 +495,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 64; ++j)
               if (!(((j < 32 ? lo : hi) >> (j & 31)) & 1u)) s[j] = 0xff800000u;   // -inf
           }
-          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float m[8];
 #pragma unroll
-          for (int j = 0; j < 64; j += 8)
+          for (int e = 0; e < 8; ++e) {
+            m[e] = __uint_as_float(s[e]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) m[e] = max3(m[e], __uint_as_float(s[j + 2 * e]), __uint_as_float(s[j + 2 * e + 1]));
-          const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * sl2;
+            for (int j = 8; j + 8 < 64; j += 16) m[e] = max3_nan(m[e], __uint_as_float(s[j + e]), __uint_as_float(s[j + 8 + e]));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m[e] = fmaxf(m[e], __uint_as_float(s[56 + e]));
+          const float top = max3_nan(max3_nan(m[0], m[1], m[2]), max3_nan(m[3], m[4], m[5]), fmaxf(m[6], m[7])) * sl2;
+          if (!(top < INFINITY)) sum = NAN;                   // as the definition has it
           const bool grows = top > ref + 8.f;
           if (i == 0) {
             ref = top;
@@ -543,34 +567,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seq = item / per_seq, t = (item - seq * per_seq) * group + token;
       return token < group && t < a.tokens ? seq * a.tokens + t : -1;
     };
-    // A group's queries by thirds of 128 bytes a row: 64 bytes of the rows in every four pieces.
-    uint4 q[8];
-    auto fetch_q = [&](int item, int third) {
+    uint4 q[24];                                              // a group's queries: 64 bytes of the rows in every four
+    auto fetch_q = [&](int item) {
       const int query = query_of(item);
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
-                                                        ((long long)max(query, 0) * kH + head0) * (kDk * 2)) + third * 8;
+                                                        ((long long)max(query, 0) * kH + head0) * (kDk * 2));
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
+      for (int x = 0; x < 24; ++x)
         q[x] = query >= 0 ? src[(8 * (x & 3) + (lane >> 2)) * (kDk / 8) + (x >> 2) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
     };
-    auto store_q = [&](int item) {                            // the first third has been fetched
-#pragma unroll 1
-      for (int b = 0; b < 3; ++b) {
-        uint32_t r[32];
+    auto store_q = [&]() {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          lines_to_rows(turn, q + 4 * h);
+      for (int b = 0; b < 6; ++b) {
+        lines_to_rows(turn, q + 4 * b);
+        uint32_t r[16];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint4 y = q[4 * h + x];
-            r[16 * h + 4 * x] = y.x;
-            r[16 * h + 4 * x + 1] = y.y;
-            r[16 * h + 4 * x + 2] = y.z;
-            r[16 * h + 4 * x + 3] = y.w;
-          }
+        for (int x = 0; x < 4; ++x) {
+          r[4 * x] = q[4 * b + x].x;
+          r[4 * x + 1] = q[4 * b + x].y;
+          r[4 * x + 2] = q[4 * b + x].z;
+          r[4 * x + 3] = q[4 * b + x].w;
         }
-        if (b < 2) fetch_q(item, b + 1);
-        tmem_st32(tmem + lanes + kQCol + 32 * b, r);
+        tmem_st16(tmem + lanes + kQCol + 16 * b, r);
       }
       tc_wait_st();
       tc_fence_before();
@@ -583,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t items = 0;
     const int first = next_item(blockIdx.x);
     if (first < n_groups) {
-      fetch_q(first, 0);
-      store_q(first);
+      fetch_q(first);
+      store_q();
     }
     for (int item = blockIdx.x; item < n_groups; item += gridDim.x) {
       const int query = query_of(item);
@@ -600,10 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int next = next_item(item + gridDim.x);
       if (next < n_groups) {
-        fetch_q(next, 0);
+        fetch_q(next);
         if (!tc_wait_warp(c, &c.q_empty, items & 1, a.err)) break;
         tc_fence_after();
-        store_q(next);
+        store_q();
       }
       if (!tc_wait_warp(c, &c.stat_full, items & 1, a.err)) break;
       const float ref = c.stat[row].x, sum = c.stat[row].y;
@@ -721,13 +739,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t k0 = smem_desc(smem_u32(c.k[0]), 16, 1024), v0 = smem_desc(smem_u32(c.v[0]), kTile * 128, 1024);
     uint32_t tiles = 0, items = 0;
     uint32_t st = 0, lap = 0, st_pv = 0;       // stage of the next scores, times round the ring, stage of the next O
-    bool ok = true;
+    bool ok = true, landed = false;
     // O (+)= P V of tile x, of the current item
     auto pv = [&](uint32_t x, bool first, bool last) -> bool {
       const uint32_t buf = x & 1, o = items & 1;
       const uint64_t v = v0 + st_pv * (kVBytes >> 4);
       if (first && items > 1 && !tc_wait_warp(c, &c.o_free[o], ((items >> 1) - 1) & 1, a.err)) return false;
-      if (!tc_wait_warp(c, &c.p_full[buf], (x >> 1) & 1, a.err)) return false;
+      const bool here = mbar_test(&c.p_full[buf], (x >> 1) & 1);
+      landed = mbar_test(&c.full[st], lap & 1);               // of the next scores
+      if (!__all_sync(0xffffffffu, here) && !tc_wait_warp(c, &c.p_full[buf], (x >> 1) & 1, a.err)) return false;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -746,8 +766,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (nt == 0) continue;
       for (int i = 0; i < nt && ok; ++i, ++tiles) {
         const uint32_t buf = tiles & 1;
-        ok = tc_wait_warp(c, &c.full[st], lap & 1, a.err) && (i > 0 || tc_wait_warp(c, &c.q_full, items & 1, a.err));
+        ok = (__all_sync(0xffffffffu, landed) || tc_wait_warp(c, &c.full[st], lap & 1, a.err)) &&
+             (i > 0 || tc_wait_warp(c, &c.q_full, items & 1, a.err));
         if (!ok) break;
+        landed = false;
         fence_async_smem();                    // the copies are generic-proxy writes, the tensor core reads by the async proxy
         tc_fence_after();
         const uint64_t kd = k0 + st * (kKBytes >> 4);

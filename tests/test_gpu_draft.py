@@ -182,11 +182,25 @@ def check_tree(sh, d, n_draft=None, parent=None, head=None):
 
 FAST = dict(q_heads=64, k_dim=192, v_dim=128, dtype="bf16")
 
+# Queries of a case by kernel: a cluster of CTAs per query up to 66 queries of 640 slots (266 of 160 slots), pairs of
+# tokens on the tensor cores beyond; any other shape is generic.
+KINDS = {"clusters": (FAST, 1), "pairs": (FAST, 0), "generic": (dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32"), 1)}
+
+
+def of_kind(kind, seqs, tokens, slots=100):
+    """(shape arguments, sequences): enough of them for the kernel."""
+    kw, few = KINDS[kind]
+    ctas = -(-slots // 160)
+    return kw, seqs if few else -(-(266 // ctas + 2) // tokens)
+
 
 @pytest.mark.parametrize("S,T,N,K,W,roots,holes", [
     (1, 1, 40, 1, 1, 1, 0.0), (1, 8, 600, 512, 128, 1, 0.0), (3, 7, 700, 512, 128, 2, 1.0), (2, 33, 300, 99, 37, 1, 1.0),
     (1, 128, 64, 40, 128, 3, 0.0), (5, 2, 513, 512, 4, 1, 0.0), (65, 1, 96, 64, 16, 1, 1.0), (2, 64, 1024, 512, 8, 1, 0.0),
-    (20, 16, 600, 512, 128, 2, 1.0), (1, 3, 1200, 1000, 24, 1, 0.0)])
+    (20, 16, 600, 512, 128, 2, 1.0), (1, 3, 1200, 1000, 24, 1, 0.0),
+    # pairs of tokens on the tensor cores: odd token counts, one token, full and short lists, the longest ones
+    (10, 7, 700, 512, 128, 1, 0.0), (67, 1, 513, 512, 128, 1, 1.0), (3, 33, 900, 512, 64, 3, 0.0), (1, 128, 700, 512, 128, 1, 1.0),
+    (70, 1, 600, 512, 128, 1, 0.0), (20, 2, 1100, 1000, 24, 1, 0.0), (90, 3, 30, 9, 7, 1, 1.0), (160, 2, 64, 40, 1, 1, 0.0)])
 def test_tree_attention_fast_path(csa2, S, T, N, K, W, roots, holes):
     sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, **FAST)
     d = tree_inputs(sh, S * 1000 + T, holes=holes, roots=roots)
@@ -206,49 +220,104 @@ def test_tree_attention_any_shape(csa2, H, dk, dv, dtype, S, T, N, K, W):
     check_tree(sh, d)
 
 
-@pytest.mark.parametrize("kind", ["fast", "generic"])
+@pytest.mark.parametrize("kind", list(KINDS))
 @pytest.mark.parametrize("fill", [0, 1, 15, 16])
 def test_tree_window_edges_and_chains(csa2, kind, fill):
     """Windows that are empty, filling and full, chains longer than the window, no parents and no heads given."""
-    kw = FAST if kind == "fast" else dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32")
     T = 24
-    sh = shape(2 * T, tokens=T, n_entries=80, topk=20, swa=16, **kw)
+    kw, S = of_kind(kind, 2, T)
+    sh = shape(S * T, tokens=T, n_entries=80, topk=20, swa=16, **kw)
     d = tree_inputs(sh, 50 + fill, fill=fill)
-    chain = np.tile(np.arange(T) - 1, (2, 1))
+    chain = np.tile(np.arange(T) - 1, (S, 1))
     run_tree(csa2, sh, d, parent=None)
     check_tree(sh, d, parent=chain)
     run_tree(csa2, sh, d, parent=i32(chain), head=None)
-    check_tree(sh, d, parent=chain, head=np.zeros(2, dtype=int))
+    check_tree(sh, d, parent=chain, head=np.zeros(S, dtype=int))
 
 
-@pytest.mark.parametrize("kind", ["fast", "generic"])
+@pytest.mark.parametrize("kind", list(KINDS))
 def test_tree_rows_without_keys_and_dead_tokens(csa2, kind):
-    kw = FAST if kind == "fast" else dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32")
-    sh = shape(3 * 6, tokens=6, n_entries=70, topk=40, swa=9, **kw)
+    T = 6
+    kw, S = of_kind(kind, 3, T)
+    sh = shape(S * T, tokens=T, n_entries=70, topk=40, swa=9, **kw)
     d = tree_inputs(sh, 77, holes=1.0)
-    n_draft = i32([6, 1, 4])
+    live = [(6, 1, 4)[s % 3] for s in range(S)]
+    n_draft = i32(live)
     # what a dead token or an unused row holds must not matter
     nan = float("nan")
-    for s, n in enumerate([6, 1, 4]):
+    n_swa, idx = d.n_swa.tolist(), d.idx.cpu()
+    for s, n in enumerate(live):
         d.k_draft[s, n:], d.v_draft[s, n:] = nan, nan
-        d.idx[s * 6 + n:(s + 1) * 6] = -1
-        d.k_swa[s, int(d.n_swa[s]):], d.v_swa[s, int(d.n_swa[s]):] = nan, nan
-        used = set(d.idx[s * 6:(s + 1) * 6].flatten().tolist())
-        free = [e for e in range(70) if e not in used]
+        idx[s * T + n:(s + 1) * T] = -1
+        d.k_swa[s, n_swa[s]:], d.v_swa[s, n_swa[s]:] = nan, nan
+        free = sorted(set(range(70)) - set(idx[s * T:(s + 1) * T].flatten().tolist()))
         d.k_main[s, free], d.v_main[s, free] = nan, float("inf")
-    d.q.view(3, 6, sh.q_heads, -1)[1, 1:] = nan
+    d.idx.copy_(idx)
+    dead = torch.arange(T, device="cuda") >= n_draft[:, None]
+    d.q.view(S, T, sh.q_heads, -1)[dead] = nan
     ws = run_tree(csa2, sh, d, n_draft=n_draft)
     assert_no_device_error(csa2, ws)
     check_tree(sh, d, n_draft=n_draft)
-    assert torch.isinf(d.lse.view(3, 6, -1)[1, 1:]).all() and (d.out.view(3, 6, -1)[1, 1:] == 0).all()
+    assert torch.isinf(d.lse.view(S, T, -1)[dead]).all() and (d.out.view(S, T, sh.q_heads, -1)[dead] == 0).all()
 
 
-@pytest.mark.parametrize("kind", ["fast", "generic"])
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), float("-inf")])
+def test_tree_values_of_one_token_stay_with_it(csa2, kind, what):
+    """A value row that is not finite reaches the tokens that attend it and no others: a selected entry of one token, the
+    drafted row of another."""
+    T = 4
+    kw, S = of_kind(kind, 2, T)
+    sh = shape(S * T, tokens=T, n_entries=90, topk=20, swa=8, **kw)
+    d = tree_inputs(sh, 5)
+    d.parent.copy_(i32([[-1, 0, 0, 2]] * S))
+    rng = np.random.default_rng(0)
+    idx = np.stack([np.sort(rng.choice(80, 20, replace=False)) for _ in range(S * T)]).reshape(S, T, 20)
+    idx[:, 1, 19] = 85                                     # token 1 alone selects entry 85
+    d.idx.copy_(i32(idx.reshape(S * T, 20)))
+    run_tree(csa2, sh, d)
+    clean, lse = d.out.clone(), d.lse.clone()
+    d.v_main[:, 85, 3] = what
+    d.v_draft[:, 2, 1] = what                              # token 2 and its child 3
+    run_tree(csa2, sh, d)
+    out, was = d.out.view(S, T, sh.q_heads, -1), clean.view(S, T, sh.q_heads, -1)
+    assert torch.equal(d.lse, lse)
+    bad = ~torch.isfinite(out)
+    want = torch.zeros_like(bad)
+    want[:, 1, :, 3] = True
+    want[:, 2:, :, 1] = True
+    assert torch.equal(bad, want)
+    rest = out.masked_fill(want, 0).float() - was.masked_fill(want, 0).float()
+    # Beside such a row an output may be computed again with unrounded weights: a weight's rounding moves a weighted mean
+    # of the values by at most half a step of the largest, and both outputs are rounded once.
+    most = max(float(x[x.isfinite()].abs().max()) for x in (d.v_main, d.v_swa, d.v_draft))
+    lim = 3 * HALF[d.dt] * most + 1e-5
+    assert float(rest.abs().max()) <= lim
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_tree_scores_that_are_not_finite(csa2, kind):
+    """A NaN key makes its tokens' heads NaN, as the definition does, and leaves the others alone."""
+    T = 2
+    kw, S = of_kind(kind, 2, T)
+    sh = shape(S * T, tokens=T, n_entries=90, topk=20, swa=8, **kw)
+    d = tree_inputs(sh, 6)
+    idx = np.tile(np.arange(20), (S * T, 1)).reshape(S, T, 20)
+    idx[:, 1, 19] = 85
+    d.idx.copy_(i32(idx.reshape(S * T, 20)))
+    d.k_main[:, 85] = float("nan")
+    run_tree(csa2, sh, d)
+    assert torch.isfinite(d.out.view(S, T, -1)[:, 0]).all() and torch.isfinite(d.lse.view(S, T, -1)[:, 0]).all()
+    assert torch.isnan(d.out.view(S, T, -1)[:, 1]).all() and torch.isnan(d.lse.view(S, T, -1)[:, 1]).all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 def test_tree_bad_inputs_are_recorded(csa2, kind):
-    kw = FAST if kind == "fast" else dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32")
-    sh = shape(2 * 4, tokens=4, n_entries=30, topk=10, swa=6, **kw)
+    T = 4
+    kw, S = of_kind(kind, 2, T)
+    sh = shape(S * T, tokens=T, n_entries=70, topk=10, swa=6, **kw)
     d = tree_inputs(sh, 9, fill=6)
-    d.idx[3, 2] = 30                                       # an entry behind the cache
+    d.idx[3, 2] = 70                                       # an entry behind the cache
     ws = run_tree(csa2, sh, d)
     assert csa2.read_device_error(ws) == (-5, BAD_INDEX)
     check_tree(sh, d)
@@ -266,25 +335,29 @@ def test_tree_bad_inputs_are_recorded(csa2, kind):
     check_tree(sh, d)
 
 
-def test_tree_repeated_entries_count_each_time(csa2):
+@pytest.mark.parametrize("kind", ["clusters", "pairs"])
+def test_tree_repeated_entries_count_each_time(csa2, kind):
     """The same index twice, and lists that do not ascend: as in csa2_sparse_attn."""
-    sh = shape(2 * 4, tokens=4, n_entries=64, topk=48, swa=8, **FAST)
+    kw, S = of_kind(kind, 2, 4)
+    sh = shape(S * 4, tokens=4, n_entries=64, topk=48, swa=8, **kw)
     d = tree_inputs(sh, 13)
     rng = np.random.default_rng(4)
-    d.idx.copy_(i32(rng.integers(-1, 64, (8, 48))))
+    d.idx.copy_(i32(rng.integers(-1, 64, (S * 4, 48))))
     ws = run_tree(csa2, sh, d)
     assert_no_device_error(csa2, ws)
     check_tree(sh, d)
 
 
-def test_tree_large_logits(csa2):
-    sh = shape(2 * 6, tokens=6, n_entries=600, topk=512, swa=128, **FAST)
+@pytest.mark.parametrize("S,T", [(2, 6), (17, 4), (70, 1)])
+def test_tree_large_logits(csa2, S, T):
+    sh = shape(S * T, tokens=T, n_entries=600, topk=512, swa=128, **FAST)
     d = tree_inputs(sh, 21, spread=400.0)
-    run_tree(csa2, sh, d)
+    ws = run_tree(csa2, sh, d)
+    assert_no_device_error(csa2, ws)
     assert torch.isfinite(d.out).all() and torch.isfinite(d.lse).all()
     out, lse, _, dot = R.tree_attention(f64(d.q), f64(d.k_main), f64(d.v_main), d.idx.cpu().numpy(), f64(d.k_swa), f64(d.v_swa),
                                         d.n_swa.cpu().numpy(), f64(d.k_draft), f64(d.v_draft), d.parent.cpu().numpy(), None,
-                                        d.head.cpu().numpy(), 1 / np.sqrt(192), 6)
+                                        d.head.cpu().numpy(), 1 / np.sqrt(192), T)
     assert np.abs(f64(d.lse) - lse).max() <= dot * 196 * 2.0 ** -24 + 8 * EPS32 * np.abs(lse).max()
 
 
