@@ -7,13 +7,16 @@
 //   registers, so a K row is read once per 8 heads; after the softmax (fp32,
 //   one maximum and sum per head over all slots, which fit shared memory) the
 //   V rows are read the same way.  Bound by issue and the row loads' latency.
-// weights_mma_kernel -- bf16, 64 heads of 192: one CTA per (query, 128 slots)
-//   gathers the K rows with 16-byte cp.async, S = Q K^T on mma.sync, and sums
-//   exp2(s - lse) over the heads in fixed order.  No maximum is needed, the
-//   lse is the normaliser.  It reads 60 % of what the attention reads (K only).
+// weights_mma_kernel -- bf16, 64 heads of 192: a CTA takes a query's slots, or a
+//   part of them when there are few queries, 64 at a time through a ring of
+//   four stages of K rows gathered with 16-byte cp.async; S = Q K^T on mma.sync,
+//   and exp2(s - lse) is summed over the heads in fixed order.  No maximum is
+//   needed, the lse is the normaliser.  It reads 60 % of what the attention
+//   reads (K only), and is bound by the gather.
 // weights_generic_kernel -- any shape: a warp per slot.
 #include "common.cuh"
 #include "internal.h"
+#include "tc.cuh"
 #include "tree.cuh"
 
 namespace csa2 {
@@ -163,46 +166,62 @@ constexpr size_t kGenSmemMax = (size_t(kGenHeads) * 1024 + size_t(kMaxSlots) * k
 
 constexpr int kH = 64, kDk = 192;
 constexpr int kWThreads = 128;
-constexpr int kWSlots = 128;                    // slots per CTA
-constexpr int kWNT = kWSlots / 8;
+constexpr int kWSlots = 64;                     // slots a chunk
+constexpr int kWStages = 4;
 constexpr int kKRow = kDk * 2 + 16;             // padded: ldmatrix rows hit distinct banks
-constexpr int kWOffSum = kWSlots * kKRow;       // [4 warps][kWSlots]
-constexpr int kWSmem = kWOffSum + 4 * kWSlots * 4;
+constexpr int kWOffSum = kWStages * kWSlots * kKRow;          // [2][4 warps][kWSlots]
+constexpr int kWOffId = kWOffSum + 2 * 4 * kWSlots * 4;       // [kWStages + 1][kWSlots]
+constexpr int kWSmem = kWOffId + (kWStages + 1) * kWSlots * 4;
 
-__global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeightsArgs a) {
+__global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeightsArgs a, int chunks) {
   extern __shared__ __align__(128) uint8_t smem[];
   float* sum_s = reinterpret_cast<float*>(smem + kWOffSum);
-  const int b = blockIdx.y, j0 = blockIdx.x * kWSlots, nj = min(kWSlots, a.topk - j0);
+  int* id_s = reinterpret_cast<int*>(smem + kWOffId);
+  const int b = blockIdx.y, j0 = blockIdx.x * chunks * kWSlots, nj = min(chunks * kWSlots, a.topk - j0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int nc = (nj + kWSlots - 1) / kWSlots;
   pdl_wait();
   float* out = a.weights + (long long)b * a.topk + j0;
   if (a.live != nullptr && a.live[b] == 0) {
     for (int j = tid; j < nj; j += kWThreads) out[j] = 0.f;
     return;
   }
-  // this thread's slot
-  int e = tid < nj ? a.idx[(long long)b * a.topk + j0 + tid] : -1;
-  if (e >= a.n_entries) {
-    report(a.err, kErrBadIndex, e);
-    e = -1;
-  }
-  // K rows: the warp copies its own 32 slots, 24 pieces of 16 bytes each, four slots in three instructions
-  {
-    const uint8_t* k0 = static_cast<const uint8_t*>(a.k_main) + (long long)(b / a.seq_div) * a.n_entries * (kDk * 2);
-#pragma unroll 2
-    for (int q = 0; q < 8; ++q) {
+  const int* idx = a.idx + (long long)b * a.topk + j0;
+  const uint8_t* k0 = static_cast<const uint8_t*>(a.k_main) + (long long)(b / a.seq_div) * a.n_entries * (kDk * 2);
+  // This lane's entry of a chunk: the warp copies slots 16 * warp .. + 15 of it.
+  auto entry = [&](int c) -> int {
+    const int j = c * kWSlots + warp * 16 + lane;
+    int e = lane < 16 && j < nj ? idx[j] : -1;
+    if (e >= a.n_entries) {
+      report(a.err, kErrBadIndex, e);
+      e = -1;
+    }
+    return e;
+  };
+  // Four rows (24 pieces of 16 bytes each) in three copies a lane; a commit group a chunk.
+  auto copy = [&](int c, int e) {
+    if (c < nc) {
+      uint8_t* st = smem + (c % kWStages) * kWSlots * kKRow;
+      if (lane < 16) id_s[(c % (kWStages + 1)) * kWSlots + warp * 16 + lane] = e;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        const int p = 32 * i + lane, s = 4 * q + p / 24, part = p % 24;
-        const int es = __shfl_sync(0xffffffffu, e, s);
-        const uint32_t d = smem_u32(smem + (warp * 32 + s) * kKRow + part * 16);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d),
-                     "l"(k0 + (es >= 0 ? (long long)es * (kDk * 2) + part * 16 : 0)), "r"(es >= 0 ? 16u : 0u)
-                     : "memory");
-      }
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int p = 32 * i + lane, s = 4 * q + p / 24, part = p % 24;
+          const int es = __shfl_sync(0xffffffffu, e, s);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(st + (warp * 16 + s) * kKRow + part * 16)),
+                       "l"(k0 + (es >= 0 ? (long long)es * (kDk * 2) + part * 16 : 0)), "r"(es >= 0 ? 16u : 0u)
+                       : "memory");
+        }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-  }
+  };
+  int ahead[kWStages];
+#pragma unroll
+  for (int c = 0; c < kWStages; ++c) ahead[c] = entry(c);
+#pragma unroll
+  for (int c = 0; c < kWStages - 1; ++c) copy(c, ahead[c]);
+  int e_next = ahead[kWStages - 1];             // of the chunk that is copied next
   uint32_t qa[kDk / 16][4];
   {
     const uint32_t* q0 = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.q) +
@@ -221,36 +240,45 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeight
   n0 = n0 == -INFINITY ? -INFINITY : -n0 * kLog2e;
   n1 = n1 == -INFINITY ? -INFINITY : -n1 * kLog2e;
   const float sl2 = a.scale * kLog2e;
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
-  const uint8_t* krow = smem + ((lane & 7) + 8 * (lane >> 4)) * kKRow + ((lane >> 3) & 1) * 16;
-#pragma unroll 2
-  for (int jp = 0; jp < kWNT / 2; ++jp) {
-    float s[2][4] = {};
+  auto write = [&](int c) {                     // the warps' sums of a chunk, added up in their order
+    const int j = c * kWSlots + tid;
+    if (tid >= kWSlots || j >= nj) return;
+    const float* s = sum_s + (c & 1) * 4 * kWSlots + tid;
+    out[j] = id_s[(c % (kWStages + 1)) * kWSlots + tid] < 0 ? 0.f : (s[0] + s[kWSlots]) + (s[2 * kWSlots] + s[3 * kWSlots]);
+  };
+  for (int c = 0; c < nc; ++c) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kWStages - 2) : "memory");
+    __syncthreads();                            // chunk c has landed, chunk c - 1 is done with
+    if (c > 0) write(c - 1);
+    copy(c + kWStages - 1, e_next);
+    e_next = entry(c + kWStages);
+    const uint8_t* krow =
+        smem + (c % kWStages) * kWSlots * kKRow + ((lane & 7) + 8 * (lane >> 4)) * kKRow + ((lane >> 3) & 1) * 16;
+    float* sum = sum_s + ((c & 1) * 4 + warp) * kWSlots;
+    float s[kWSlots / 8][4] = {};               // 8 keys each: independent sums, whose steps overlap
 #pragma unroll
-    for (int ks = 0; ks < kDk / 16; ++ks) {
-      uint32_t b0, b1, b2, b3;
-      ldsm_x4(b0, b1, b2, b3, krow + jp * 16 * kKRow + ks * 32);
-      mma_bf16(s[0], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
-      mma_bf16(s[1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
-    }
+    for (int ks = 0; ks < kDk / 16; ++ks)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      float w0 = exp2f(__fmaf_rn(s[n][0], sl2, n0)) + exp2f(__fmaf_rn(s[n][2], sl2, n1));
-      float w1 = exp2f(__fmaf_rn(s[n][1], sl2, n0)) + exp2f(__fmaf_rn(s[n][3], sl2, n1));
+      for (int jp = 0; jp < kWSlots / 16; ++jp) {
+        uint32_t b0, b1, b2, b3;
+        ldsm_x4(b0, b1, b2, b3, krow + jp * 16 * kKRow + ks * 32);
+        mma_bf16(s[2 * jp], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
+        mma_bf16(s[2 * jp + 1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
+      }
+#pragma unroll
+    for (int n = 0; n < kWSlots / 8; ++n) {
+      float w0 = ex2(__fmaf_rn(s[n][0], sl2, n0)) + ex2(__fmaf_rn(s[n][2], sl2, n1));
+      float w1 = ex2(__fmaf_rn(s[n][1], sl2, n0)) + ex2(__fmaf_rn(s[n][3], sl2, n1));
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
         w0 += __shfl_xor_sync(0xffffffffu, w0, o);
         w1 += __shfl_xor_sync(0xffffffffu, w1, o);
       }
-      if (g == 0)
-        *reinterpret_cast<float2*>(sum_s + warp * kWSlots + 16 * jp + 8 * n + 2 * t) = make_float2(w0, w1);
+      if (g == 0) *reinterpret_cast<float2*>(sum + 8 * n + 2 * t) = make_float2(w0, w1);
     }
   }
   __syncthreads();
-  if (tid < nj)
-    out[tid] = e < 0 ? 0.f
-                     : (sum_s[tid] + sum_s[kWSlots + tid]) + (sum_s[2 * kWSlots + tid] + sum_s[3 * kWSlots + tid]);
+  write(nc - 1);
 }
 
 __global__ void __launch_bounds__(256) weights_generic_kernel(const AttnWeightsArgs a) {
@@ -330,8 +358,14 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, 
     return cudaFuncSetAttribute(weights_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(weights_mma_kernel, dim3(unsigned((a.topk + kWSlots - 1) / kWSlots), unsigned(batch)),
-                    dim3(kWThreads), kWSmem, st, 1, a);
+  // CTAs a query: one while the queries alone fill two CTAs an SM, up to one a
+  // chunk for few queries (1 query of 512 slots: 8 CTAs).
+  const int all = (a.topk + kWSlots - 1) / kWSlots;
+  int split = 2 * device_sm_count() / batch;
+  split = split < 1 ? 1 : split > all ? all : split;
+  const int chunks = (all + split - 1) / split;
+  return launch_pdl(weights_mma_kernel, dim3(unsigned((all + chunks - 1) / chunks), unsigned(batch)), dim3(kWThreads), kWSmem,
+                    st, 1, a, chunks);
 }
 
 }  // namespace csa2
