@@ -206,6 +206,7 @@ cudaError_t launch_tree_attn_cluster(const TreeArgs& a, int batch, cudaStream_t 
 // Pairs of tokens on the tensor cores (tree_tc.cu); `plan` holds tree_plan_words.
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStream_t st);
 size_t tree_plan_words(int seqs, int tokens, int topk, int swa);
+cudaError_t launch_attn_weights_tc(const AttnWeightsArgs& a, int batch, cudaStream_t st);   // weights_tc.cu
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, cudaStream_t st);
 
 // Commit of an accepted path (commit.cu).
@@ -335,7 +336,8 @@ void note_launch();
 // (0..63) is seen on that device, and again until it succeeds.  Thread-safe.
 enum SetupKey { kSetupAttn = 0, kSetupIndexerFlat = 1, kSetupIndexerPooled = 2, kSetupSelectFlat = 3,
                 kSetupSelectPooled = 4, kSetupTree = 5, kSetupTreeGeneric = 6, kSetupWeights = 7,
-                kSetupWeightsGeneric = 8, kSetupEvict = 9, kSetupTreePair = 10, kSetupEvictMove = 11 };
+                kSetupWeightsGeneric = 8, kSetupEvict = 9, kSetupTreePair = 10, kSetupEvictMove = 11,
+                kSetupWeightsTc = 12 };
 cudaError_t once_per_device(int key, cudaError_t (*set)());
 
 cudaError_t launch_block_keys(const BlockKeyArgs& a, int batch, cudaStream_t st);

@@ -169,4 +169,48 @@ CSA2_DEV float ex2(float x) {   // 2^x within 2 steps, results below 2^-126 flus
   return y;
 }
 
+// ------------------------------------------------------------------ roles of a CTA
+
+// A bounded wait that also ends when another role has given up (`c.abort`, in shared memory).
+template <typename Shared>
+CSA2_DEV bool tc_wait(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31u) == 0u) {
+      if (c.abort) return false;
+      if (global_ns() - t0 > kWaitLimitNs) {
+        c.abort = 1;
+        report(err, kErrTimeout, int(threadIdx.x));   // which role gave up first
+        return false;
+      }
+    }
+  }
+}
+
+// Whether a phase is over, without waiting: tests of several barriers are in flight at once, where waits follow each other.
+CSA2_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// The same by a whole warp, which goes on or gives up together.
+template <typename Shared>
+CSA2_DEV bool tc_wait_warp(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
+  return __all_sync(0xffffffffu, tc_wait(c, bar, parity, err)) != 0;
+}
+
+// `bar` gets one arrival when this thread's copies so far have landed; nobody waits for them here.
+CSA2_DEV void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 }  // namespace csa2

@@ -167,7 +167,7 @@ constexpr size_t kGenSmemMax = (size_t(kGenHeads) * 1024 + size_t(kMaxSlots) * k
 constexpr int kH = 64, kDk = 192;
 constexpr int kWThreads = 128;
 constexpr int kWSlots = 64;                     // slots a chunk
-constexpr int kWStages = 4;
+constexpr int kWStages = 2;
 constexpr int kKRow = kDk * 2 + 16;             // padded: ldmatrix rows hit distinct banks
 constexpr int kWOffSum = kWStages * kWSlots * kKRow;          // [2][4 warps][kWSlots]
 constexpr int kWOffId = kWOffSum + 2 * 4 * kWSlots * 4;       // [kWStages + 1][kWSlots]
@@ -350,6 +350,7 @@ cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan
 
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, cudaStream_t st) {
   if (batch == 0) return cudaSuccess;
+  if (fast && batch >= 64) return launch_attn_weights_tc(a, batch, st);
   note_launch();
   if (!fast)
     return launch_pdl(weights_generic_kernel, dim3(unsigned((a.topk + 7) / 8), unsigned(batch)), dim3(256),
@@ -361,7 +362,7 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, 
   // CTAs a query: one while the queries alone fill two CTAs an SM, up to one a
   // chunk for few queries (1 query of 512 slots: 8 CTAs).
   const int all = (a.topk + kWSlots - 1) / kWSlots;
-  int split = 2 * device_sm_count() / batch;
+  int split = 4 * device_sm_count() / batch;
   split = split < 1 ? 1 : split > all ? all : split;
   const int chunks = (all + split - 1) / split;
   return launch_pdl(weights_mma_kernel, dim3(unsigned((all + chunks - 1) / chunks), unsigned(batch)), dim3(kWThreads), kWSmem,

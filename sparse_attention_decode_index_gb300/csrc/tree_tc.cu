@@ -299,41 +299,6 @@ struct Shared {
 };
 constexpr int kSmem = int(sizeof(Shared)) + 1024;   // + room to align to 1,024
 
-// A bounded wait that also ends when another role has given up.
-CSA2_DEV bool tc_wait(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 31u) == 0u) {
-      if (c.abort) return false;
-      if (global_ns() - t0 > kWaitLimitNs) {
-        c.abort = 1;
-        report(err, kErrTimeout, int(threadIdx.x));   // which role gave up first
-        return false;
-      }
-    }
-  }
-}
-
-// Whether a phase is over, without waiting: tests of several barriers are in flight at once, where waits follow each other.
-CSA2_DEV bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-// The same by a whole warp, which goes on or gives up together.
-CSA2_DEV bool tc_wait_warp(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
-  return __all_sync(0xffffffffu, tc_wait(c, bar, parity, err)) != 0;
-}
-
 // Row `pos` of a group's keys: K and V addresses (null behind the last) and token mask.
 struct Key {
   const uint8_t *k, *v;
@@ -368,11 +333,6 @@ CSA2_DEV void cp16(uint32_t dst, uint64_t src, int offset, const void* any) {   
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
                "l"(src != 0 ? src + offset : reinterpret_cast<uint64_t>(any)), "r"(src != 0 ? 16u : 0u)
                : "memory");
-}
-
-// `bar` gets one arrival when this thread's copies so far have landed; nobody waits for them here.
-CSA2_DEV void cp_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // One row of O from its own keys alone, by a warp: lane l ends with columns 4 l .. 4 l + 3, unscaled by 1 / l.

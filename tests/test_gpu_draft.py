@@ -389,8 +389,13 @@ def test_chain_equals_steps_of_append_and_attention(csa2):
 
 # ------------------------------------------------------------------ attention weights
 
-@pytest.mark.parametrize("H,dk,dtype", [(64, 192, "bf16"), (5, 24, "f32"), (16, 64, "bf16"), (1, 1, "f32"), (12, 1024, "bf16")])
-@pytest.mark.parametrize("S,T,N,K", [(1, 1, 5, 1), (2, 3, 300, 130), (1, 2, 700, 512)])
+SHAPES = [(64, 192, "bf16"), (5, 24, "f32"), (16, 64, "bf16"), (1, 1, "f32"), (12, 1024, "bf16")]
+
+
+@pytest.mark.parametrize("H,dk,dtype,S,T,N,K", [
+    (*x, *y) for x in SHAPES for y in [(1, 1, 5, 1), (2, 3, 300, 130), (1, 2, 700, 512)]] + [
+    # the fast shape in batches that fill the GPU: a tile or several a query, part tiles, more queries than CTAs
+    (64, 192, "bf16", *y) for y in [(70, 1, 300, 130), (16, 5, 700, 512), (200, 1, 40, 9), (33, 9, 300, 128), (3, 50, 1100, 1000)]])
 def test_attention_weights(csa2, H, dk, dtype, S, T, N, K):
     sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=4, q_heads=H, k_dim=dk, v_dim=16, dtype=dtype)
     d = tree_inputs(sh, 5 + H, holes=1.0)
@@ -407,19 +412,22 @@ def test_attention_weights(csa2, H, dk, dtype, S, T, N, K):
     # logits' fp32 sums, lse * log2(e) and the exponential's argument rounded, the heads added up
     rel = dot * (dk + 4) * 2.0 ** -24 + 16 * EPS32 * (4 + np.log(K + 1.0)) + H * 2.0 ** -24
     assert np.all(np.abs(f64(w) - want) <= want * rel + 1e-30)
-    live = i32([1] * (S * T))
-    live[0] = 0
+    live = i32(np.arange(S * T) % 3 > 0)
+    d.q[live == 0] = float("nan")
+    d.idx[live == 0] = N
     w2 = torch.full_like(w, 9.0)
     csa2.attn_weights(sh, d.q, d.k_main, d.idx, lse, w2, ws, live=live)
-    assert (w2[0] == 0).all() and torch.equal(w2[1:], w[1:])
+    assert_no_device_error(csa2, ws)
+    assert (w2[live == 0] == 0).all() and torch.equal(w2[live == 1], w[live == 1])
 
 
-def test_attention_weights_of_a_whole_row_sum_to_the_heads(csa2):
+@pytest.mark.parametrize("B", [4, 90])
+def test_attention_weights_of_a_whole_row_sum_to_the_heads(csa2, B):
     """With the window empty and one token, an attention's weights add up to the head count, less the token's own."""
-    sh = shape(4, n_entries=600, topk=512, swa=128, **FAST)
+    sh = shape(B, n_entries=600, topk=512, swa=128, **FAST)
     d = tree_inputs(sh, 8, fill=0)
     ws = run_tree(csa2, sh, d)
-    w = torch.empty((4, 512), device="cuda")
+    w = torch.empty((B, 512), device="cuda")
     csa2.attn_weights(sh, d.q, d.k_main, d.idx, d.lse, w, ws)
     own = torch.exp((d.q.double() * d.k_draft.double()).sum(-1) / np.sqrt(192) - d.lse.double()).sum(1)
     assert float((w.double().sum(1) + own - 64).abs().max()) <= 64 * 1e-4
