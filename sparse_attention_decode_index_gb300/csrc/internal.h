@@ -335,9 +335,8 @@ void note_launch();
 // attribute): runs `set` with the current device current the first time `key`
 // (0..63) is seen on that device, and again until it succeeds.  Thread-safe.
 enum SetupKey { kSetupAttn = 0, kSetupIndexerFlat = 1, kSetupIndexerPooled = 2, kSetupSelectFlat = 3,
-                kSetupSelectPooled = 4, kSetupTree = 5, kSetupTreeGeneric = 6, kSetupWeights = 7,
-                kSetupWeightsGeneric = 8, kSetupEvict = 9, kSetupTreePair = 10, kSetupEvictMove = 11,
-                kSetupWeightsTc = 12 };
+                kSetupSelectPooled = 4, kSetupTree = 5, kSetupTreeGeneric = 6, kSetupTreePair = 7,
+                kSetupWeightsTc = 8, kSetupEvict = 9, kSetupEvictMove = 10 };
 cudaError_t once_per_device(int key, cudaError_t (*set)());
 
 cudaError_t launch_block_keys(const BlockKeyArgs& a, int batch, cudaStream_t st);

@@ -7,12 +7,11 @@
 //   registers, so a K row is read once per 8 heads; after the softmax (fp32,
 //   one maximum and sum per head over all slots, which fit shared memory) the
 //   V rows are read the same way.  Bound by issue and the row loads' latency.
-// weights_mma_kernel -- bf16, 64 heads of 192: a CTA takes a query's slots, or a
-//   part of them when there are few queries, 64 at a time through a ring of
-//   four stages of K rows gathered with 16-byte cp.async; S = Q K^T on mma.sync,
-//   and exp2(s - lse) is summed over the heads in fixed order.  No maximum is
-//   needed, the lse is the normaliser.  It reads 60 % of what the attention
-//   reads (K only), and is bound by the gather.
+// weights_mma_kernel -- bf16, 64 heads of 192, few queries: one CTA per (query, 64
+//   slots) gathers the K rows with 16-byte cp.async; S = Q K^T on mma.sync, and
+//   exp2(s - lse) is summed over the heads in fixed order.  No maximum is
+//   needed, the lse is the normaliser.  A latency chain (index, rows, product,
+//   sum): 3.5 us a launch for up to 16 queries of 512 slots.
 // weights_generic_kernel -- any shape: a warp per slot.
 #include "common.cuh"
 #include "internal.h"
@@ -166,20 +165,14 @@ constexpr size_t kGenSmemMax = (size_t(kGenHeads) * 1024 + size_t(kMaxSlots) * k
 
 constexpr int kH = 64, kDk = 192;
 constexpr int kWThreads = 128;
-constexpr int kWSlots = 64;                     // slots a chunk
-constexpr int kWStages = 2;
+constexpr int kWSlots = 64;                     // slots per CTA
 constexpr int kKRow = kDk * 2 + 16;             // padded: ldmatrix rows hit distinct banks
-constexpr int kWOffSum = kWStages * kWSlots * kKRow;          // [2][4 warps][kWSlots]
-constexpr int kWOffId = kWOffSum + 2 * 4 * kWSlots * 4;       // [kWStages + 1][kWSlots]
-constexpr int kWSmem = kWOffId + (kWStages + 1) * kWSlots * 4;
 
-__global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeightsArgs a, int chunks) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  float* sum_s = reinterpret_cast<float*>(smem + kWOffSum);
-  int* id_s = reinterpret_cast<int*>(smem + kWOffId);
-  const int b = blockIdx.y, j0 = blockIdx.x * chunks * kWSlots, nj = min(chunks * kWSlots, a.topk - j0);
+__global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeightsArgs a) {
+  __shared__ __align__(128) uint8_t rows[kWSlots * kKRow];
+  __shared__ float sum_s[4][kWSlots];
+  const int b = blockIdx.y, j0 = blockIdx.x * kWSlots, nj = min(kWSlots, a.topk - j0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int nc = (nj + kWSlots - 1) / kWSlots;
   pdl_wait();
   float* out = a.weights + (long long)b * a.topk + j0;
   if (a.live != nullptr && a.live[b] == 0) {
@@ -187,41 +180,24 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeight
     return;
   }
   const int* idx = a.idx + (long long)b * a.topk + j0;
+  // The warp copies slots 16 * warp .. + 15: four rows (24 pieces of 16 bytes each) in three copies a lane.
+  int e = lane < 16 && warp * 16 + lane < nj ? idx[warp * 16 + lane] : -1;
+  if (e >= a.n_entries) {
+    report(a.err, kErrBadIndex, e);
+    e = -1;
+  }
   const uint8_t* k0 = static_cast<const uint8_t*>(a.k_main) + (long long)(b / a.seq_div) * a.n_entries * (kDk * 2);
-  // This lane's entry of a chunk: the warp copies slots 16 * warp .. + 15 of it.
-  auto entry = [&](int c) -> int {
-    const int j = c * kWSlots + warp * 16 + lane;
-    int e = lane < 16 && j < nj ? idx[j] : -1;
-    if (e >= a.n_entries) {
-      report(a.err, kErrBadIndex, e);
-      e = -1;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int p = 32 * i + lane, s = 4 * q + p / 24, part = p % 24;
+      const int es = __shfl_sync(0xffffffffu, e, s);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(rows + (warp * 16 + s) * kKRow + part * 16)),
+                   "l"(k0 + (es >= 0 ? (long long)es * (kDk * 2) + part * 16 : 0)), "r"(es >= 0 ? 16u : 0u)
+                   : "memory");
     }
-    return e;
-  };
-  // Four rows (24 pieces of 16 bytes each) in three copies a lane; a commit group a chunk.
-  auto copy = [&](int c, int e) {
-    if (c < nc) {
-      uint8_t* st = smem + (c % kWStages) * kWSlots * kKRow;
-      if (lane < 16) id_s[(c % (kWStages + 1)) * kWSlots + warp * 16 + lane] = e;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int p = 32 * i + lane, s = 4 * q + p / 24, part = p % 24;
-          const int es = __shfl_sync(0xffffffffu, e, s);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(st + (warp * 16 + s) * kKRow + part * 16)),
-                       "l"(k0 + (es >= 0 ? (long long)es * (kDk * 2) + part * 16 : 0)), "r"(es >= 0 ? 16u : 0u)
-                       : "memory");
-        }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  int ahead[kWStages];
-#pragma unroll
-  for (int c = 0; c < kWStages; ++c) ahead[c] = entry(c);
-#pragma unroll
-  for (int c = 0; c < kWStages - 1; ++c) copy(c, ahead[c]);
-  int e_next = ahead[kWStages - 1];             // of the chunk that is copied next
+  asm volatile("cp.async.commit_group;" ::: "memory");
   uint32_t qa[kDk / 16][4];
   {
     const uint32_t* q0 = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.q) +
@@ -240,45 +216,35 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeight
   n0 = n0 == -INFINITY ? -INFINITY : -n0 * kLog2e;
   n1 = n1 == -INFINITY ? -INFINITY : -n1 * kLog2e;
   const float sl2 = a.scale * kLog2e;
-  auto write = [&](int c) {                     // the warps' sums of a chunk, added up in their order
-    const int j = c * kWSlots + tid;
-    if (tid >= kWSlots || j >= nj) return;
-    const float* s = sum_s + (c & 1) * 4 * kWSlots + tid;
-    out[j] = id_s[(c % (kWStages + 1)) * kWSlots + tid] < 0 ? 0.f : (s[0] + s[kWSlots]) + (s[2 * kWSlots] + s[3 * kWSlots]);
-  };
-  for (int c = 0; c < nc; ++c) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kWStages - 2) : "memory");
-    __syncthreads();                            // chunk c has landed, chunk c - 1 is done with
-    if (c > 0) write(c - 1);
-    copy(c + kWStages - 1, e_next);
-    e_next = entry(c + kWStages);
-    const uint8_t* krow =
-        smem + (c % kWStages) * kWSlots * kKRow + ((lane & 7) + 8 * (lane >> 4)) * kKRow + ((lane >> 3) & 1) * 16;
-    float* sum = sum_s + ((c & 1) * 4 + warp) * kWSlots;
-    float s[kWSlots / 8][4] = {};               // 8 keys each: independent sums, whose steps overlap
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  const uint8_t* krow = rows + ((lane & 7) + 8 * (lane >> 4)) * kKRow + ((lane >> 3) & 1) * 16;
+  float s[kWSlots / 8][4] = {};                 // 8 keys each: independent sums, whose steps overlap
 #pragma unroll
-    for (int ks = 0; ks < kDk / 16; ++ks)
+  for (int ks = 0; ks < kDk / 16; ++ks)
 #pragma unroll
-      for (int jp = 0; jp < kWSlots / 16; ++jp) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(b0, b1, b2, b3, krow + jp * 16 * kKRow + ks * 32);
-        mma_bf16(s[2 * jp], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
-        mma_bf16(s[2 * jp + 1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
-      }
-#pragma unroll
-    for (int n = 0; n < kWSlots / 8; ++n) {
-      float w0 = ex2(__fmaf_rn(s[n][0], sl2, n0)) + ex2(__fmaf_rn(s[n][2], sl2, n1));
-      float w1 = ex2(__fmaf_rn(s[n][1], sl2, n0)) + ex2(__fmaf_rn(s[n][3], sl2, n1));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        w0 += __shfl_xor_sync(0xffffffffu, w0, o);
-        w1 += __shfl_xor_sync(0xffffffffu, w1, o);
-      }
-      if (g == 0) *reinterpret_cast<float2*>(sum + 8 * n + 2 * t) = make_float2(w0, w1);
+    for (int jp = 0; jp < kWSlots / 16; ++jp) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4(b0, b1, b2, b3, krow + jp * 16 * kKRow + ks * 32);
+      mma_bf16(s[2 * jp], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b0, b1);
+      mma_bf16(s[2 * jp + 1], qa[ks][0], qa[ks][1], qa[ks][2], qa[ks][3], b2, b3);
     }
+#pragma unroll
+  for (int n = 0; n < kWSlots / 8; ++n) {
+    float w0 = ex2(__fmaf_rn(s[n][0], sl2, n0)) + ex2(__fmaf_rn(s[n][2], sl2, n1));
+    float w1 = ex2(__fmaf_rn(s[n][1], sl2, n0)) + ex2(__fmaf_rn(s[n][3], sl2, n1));
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      w0 += __shfl_xor_sync(0xffffffffu, w0, o);
+      w1 += __shfl_xor_sync(0xffffffffu, w1, o);
+    }
+    if (g == 0) *reinterpret_cast<float2*>(&sum_s[warp][8 * n + 2 * t]) = make_float2(w0, w1);
   }
   __syncthreads();
-  write(nc - 1);
+  if (tid < nj) {                               // the warps' sums in their order
+    const int id = idx[tid];
+    out[tid] = id < 0 || id >= a.n_entries ? 0.f : (sum_s[0][tid] + sum_s[1][tid]) + (sum_s[2][tid] + sum_s[3][tid]);
+  }
 }
 
 __global__ void __launch_bounds__(256) weights_generic_kernel(const AttnWeightsArgs a) {
@@ -350,23 +316,17 @@ cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan
 
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, cudaStream_t st) {
   if (batch == 0) return cudaSuccess;
-  if (fast && batch >= 64) return launch_attn_weights_tc(a, batch, st);
+  // Few queries: a CTA for every 64 slots, while each has an SM of its own; the
+  // persistent tensor-core kernel beyond.  Measured, former / latter, 512 slots:
+  // 1 query 3.5 / 4.3 us, 16 3.5 / 4.4, 24 5.2 / 4.4, 64 7.8 / 5.6, 256 16.0 / 10.8.
+  const long long ctas = (long long)batch * ((a.topk + kWSlots - 1) / kWSlots);
+  if (fast && ctas > device_sm_count()) return launch_attn_weights_tc(a, batch, st);
   note_launch();
-  if (!fast)
-    return launch_pdl(weights_generic_kernel, dim3(unsigned((a.topk + 7) / 8), unsigned(batch)), dim3(256),
-                      size_t(kGenHeads) * a.k_dim * sizeof(float), st, 1, a);
-  const cudaError_t e = once_per_device(kSetupWeights, [] {
-    return cudaFuncSetAttribute(weights_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWSmem);
-  });
-  if (e != cudaSuccess) return e;
-  // CTAs a query: one while the queries alone fill two CTAs an SM, up to one a
-  // chunk for few queries (1 query of 512 slots: 8 CTAs).
-  const int all = (a.topk + kWSlots - 1) / kWSlots;
-  int split = 4 * device_sm_count() / batch;
-  split = split < 1 ? 1 : split > all ? all : split;
-  const int chunks = (all + split - 1) / split;
-  return launch_pdl(weights_mma_kernel, dim3(unsigned((all + chunks - 1) / chunks), unsigned(batch)), dim3(kWThreads), kWSmem,
-                    st, 1, a, chunks);
+  if (fast)
+    return launch_pdl(weights_mma_kernel, dim3(unsigned((a.topk + kWSlots - 1) / kWSlots), unsigned(batch)), dim3(kWThreads), 0,
+                      st, 1, a);
+  return launch_pdl(weights_generic_kernel, dim3(unsigned((a.topk + 7) / 8), unsigned(batch)), dim3(256),
+                    size_t(kGenHeads) * a.k_dim * sizeof(float), st, 1, a);
 }
 
 }  // namespace csa2
