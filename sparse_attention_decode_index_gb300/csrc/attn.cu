@@ -36,10 +36,12 @@
 // to workspace scratch in L2 instead was measured slower at small batches and
 // equal at batch 64.)
 //
-// The tree form (csa2_tree_attn, kTree) differs in the window's slots alone:
-// slot r holds the r-th drafted token of the query's path (0: itself), and
-// behind the path the newest committed rows, so that the window never takes
-// more than W slots and the launch keeps its geometry.  Its output is bf16.
+// The tree form (csa2_tree_attn, kTree; few queries, tree_tc.cu takes the
+// others) differs in the window's slots: slot r holds the r-th drafted token of
+// the query's path (0: itself), and behind the path the newest committed rows,
+// so that the window never takes more than W slots and the launch keeps its
+// geometry.  Its output is bf16, and it reads nothing before the launch in front
+// of it is complete.  8 queries of 640 slots take 12.0 us, 64 take 15.3.
 #include "common.cuh"
 #include "internal.h"
 #include "tree.cuh"

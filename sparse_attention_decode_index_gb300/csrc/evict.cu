@@ -14,9 +14,8 @@
 // evict_shift_kernel -- in place: rows only ever move down, but a row's new
 //   place may still hold a row that another one needs.  A CTA therefore owns a
 //   column slice of all of a sequence's rows and moves it in ascending order,
-//   so that no CTA waits for another: it reads a tile of rows, meets at a
-//   barrier, and writes the tile, whose rows lie at or below the rows that
-//   later tiles read.
+//   so that no CTA waits for another.  Few sequences leave it few CTAs: it is
+//   bound by their loads' latency then.
 // evict_block_keys_kernel -- the result's block keys, where the move has not
 //   made them (in place, or blocks that do not divide its tiles).
 // evict_counts_kernel -- in place, n_valid changes last: the launches before
@@ -355,27 +354,40 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArg
 constexpr int kShiftThreads = 512;
 
 // Columns [u0, u0 + w) of the rows of `base` (row length `per` units), moved
-// down to the places of `kept`, tile by tile.
+// down to the places of `kept`, tile by tile.  A tile's rows are read while the
+// one before it is written: they lie at or above its own first place, which
+// the earlier tile never writes.  Its writes wait until the whole CTA has read it.
 template <typename U>
 CSA2_DEV void shift_columns(U* base, int per, int u0, int w, const int* kept, int first, int n) {
   constexpr int kU = 8;
   const int step = kShiftThreads / w;                   // rows per round
   const int r = threadIdx.x / w, u = u0 + threadIdx.x - r * w;
   const bool on = r < step;
-  for (int t0 = first; t0 < n; t0 += kU * step) {
-    U v[kU];
+  int from[kU];
+  auto indices = [&](int t0) {
 #pragma unroll
     for (int m = 0; m < kU; ++m) {
       const int j = t0 + m * step + r;
-      if (on && j < n) v[m] = base[(long long)kept[j] * per + u];
+      from[m] = on && j < n ? kept[j] : -1;
     }
-    // The tile has been read.  Its writes need no barrier behind them: the next
-    // tile reads rows at or above its own first place, which this one never writes.
+  };
+  U now[kU], next[kU];
+  indices(first);
+#pragma unroll
+  for (int m = 0; m < kU; ++m)
+    if (from[m] >= 0) now[m] = base[(long long)from[m] * per + u];
+  indices(first + kU * step);
+  for (int t0 = first; t0 < n; t0 += kU * step) {
+#pragma unroll
+    for (int m = 0; m < kU; ++m)
+      if (from[m] >= 0) next[m] = base[(long long)from[m] * per + u];
+    indices(t0 + 2 * kU * step);
     __syncthreads();
 #pragma unroll
     for (int m = 0; m < kU; ++m) {
       const int j = t0 + m * step + r;
-      if (on && j < n) base[(long long)j * per + u] = v[m];
+      if (on && j < n) base[(long long)j * per + u] = now[m];
+      now[m] = next[m];
     }
   }
 }
@@ -523,14 +535,14 @@ cudaError_t launch_kv_evict(const EvictArgs& a, int seqs, cudaStream_t st) {
     e = launch_pdl(a.wide ? evict_move_kernel<uint4> : evict_move_kernel<uint16_t>, grid, dim3(kMoveThreads), keys, st, 1, a);
   } else {
     const int unit = a.wide ? 16 : 2;
-    // slices of 128 bytes, down to 32 (a sector) while the CTAs do not fill the SMs
+    // slices of 128 bytes, down to 16 while the CTAs do not fill the SMs
     int width = 128 / unit;
     auto slices = [&](int w) {
       int s = 1;
       for (int bytes : {a.k_bytes, a.v_bytes, a.x_bytes}) s += (bytes / unit + w - 1) / w;
       return s;
     };
-    while (width * unit > 32 && slices(width) * seqs < 2 * device_sm_count()) width >>= 1;
+    while (width * unit > 16 && slices(width) * seqs < 2 * device_sm_count()) width >>= 1;
     const dim3 grid(unsigned(slices(width)), unsigned(seqs));
     e = a.wide ? launch_pdl(evict_shift_kernel<uint4>, grid, dim3(kShiftThreads), 0, st, 1, a, width)
                : launch_pdl(evict_shift_kernel<uint16_t>, grid, dim3(kShiftThreads), 0, st, 1, a, width);

@@ -58,8 +58,8 @@ CSA2_DEV int tree_walk(const TreeArgs& a, int seq, int token, int* path, int& de
   return min(n, a.swa);
 }
 
-// The window's rows from the sequence's counts and the path's length.
-CSA2_DEV void tree_ring(const TreeArgs& a, int seq, int depth, TreeWindow& w, bool reports) {
+// The sequence's committed rows, all of them: a path of `depth` tokens leaves the newest swa - depth.
+CSA2_DEV void tree_ring(const TreeArgs& a, int seq, TreeWindow& w, bool reports) {
   const int ns = clamp_count(a.n_swa[seq], a.swa, reports ? a.err : nullptr);
   int head = a.swa_head != nullptr ? a.swa_head[seq] : 0;
   if (ns == a.swa && (head < 0 || head >= a.swa)) {
@@ -68,7 +68,7 @@ CSA2_DEV void tree_ring(const TreeArgs& a, int seq, int depth, TreeWindow& w, bo
   }
   w.swa = a.swa;
   w.newest = ns == a.swa ? (head == 0 ? a.swa - 1 : head - 1) : ns - 1;
-  w.n_ring = max(0, min(ns, a.swa - depth));
+  w.n_ring = ns;
   w.ring0 = (long long)seq * a.swa;
   w.draft0 = (long long)seq * a.tokens;
 }
@@ -78,7 +78,8 @@ CSA2_DEV bool tree_live(const TreeArgs& a, int seq, int token, bool reports) {
   return token < clamp_count(a.n_draft[seq], a.tokens, reports ? a.err : nullptr);
 }
 
-// The window of query b, by the whole block; `path` is shared memory.
+// The window of query b, by the whole block; `path` is shared memory.  The
+// counts, the parents and whether the token is live are read together.
 CSA2_DEV TreeWindow tree_window(const TreeArgs& a, int b, int* path, bool reports) {
   __shared__ int depth_s;
   TreeWindow w;
@@ -86,20 +87,20 @@ CSA2_DEV TreeWindow tree_window(const TreeArgs& a, int b, int* path, bool report
   reports = reports && threadIdx.x == 0;
   w.token = b - seq * a.tokens;
   w.live = tree_live(a, seq, w.token, reports);
+  tree_ring(a, seq, w, reports);
   int depth = w.token + 1;
   w.path = nullptr;
   if (a.parent != nullptr) {
-    if (w.live && threadIdx.x < 32) {
-      tree_walk(a, seq, w.token, path, depth, reports);
+    if (threadIdx.x < 32) {
+      tree_walk(a, seq, w.token, path, depth, reports && w.live);
       if (threadIdx.x == 0) depth_s = depth;
     }
     __syncthreads();
-    if (w.live) depth = depth_s;
+    depth = depth_s;
     w.path = path;
   }
-  tree_ring(a, seq, depth, w, reports);
-  w.n_path = min(depth, a.swa);
-  if (!w.live) w.n_path = w.n_ring = 0;
+  w.n_path = w.live ? min(depth, a.swa) : 0;
+  w.n_ring = w.live ? min(w.n_ring, max(0, a.swa - depth)) : 0;
   return w;
 }
 

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
   } else if (warp - kListWarps < ng) {
     const int g = warp - kListWarps, token = t0 + g;
     TreeWindow w;
-    tree_ring(a, seq, 0, w, lane == 0 && g == 0 && t0 == 0);
+    tree_ring(a, seq, w, lane == 0 && g == 0 && t0 == 0);
     const bool live = tree_live(a, seq, token, lane == 0);
     int depth = token + 1, n = min(depth, a.swa);
     if (a.parent != nullptr) {
