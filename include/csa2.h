@@ -400,7 +400,7 @@ typedef struct {
  * when interleaved = 1.  The angle is reduced exactly for any int32 position
  * (fixed-point turns), the arithmetic is fp32, rounded once.
  *   pos [rows] int32   freqs [rot_dim / 2] double (device)
- * 1 <= n_slots <= 16; mag finite and > 0. */
+ * rows >= 1; 1 <= n_slots <= 16; mag finite and > 0. */
 int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,
               const int32_t* pos, const double* freqs, float mag, int32_t inverse, csa2_stream_t stream);
 
@@ -423,11 +423,14 @@ int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_
  * one that is not full holds its rows oldest first from row 0.
  *   q [B, H, dk]  k_main [S, N, dk]  v_main [S, N, dv]  idx [B, K]
  *   k_swa [S, W, dk]  v_swa [S, W, dv]  swa_head, n_swa [S]
- *   k_draft [S, T, dk]  v_draft [S, T, dv]  parent [S, T]  n_draft [S] (1..T)
+ *   k_draft [S, T, dk]  v_draft [S, T, dv]  parent [S, T]  n_draft [S] (0..T)
  *   out [B, H, dv] in the element type (it feeds the output projection)
  *   lse [B, H] fp32 (nullable)
- * shape.swa >= 1.  A chain of T gives what T steps of csa2_swa_append and
- * csa2_sparse_attn give. */
+ * shape.swa >= 1; batch <= 65,535; out and lse overlap nothing that is read.
+ * A chain of T gives what T steps of csa2_swa_append and csa2_sparse_attn
+ * give.  Weights are rounded to bf16 before they meet bf16 values, their sums
+ * are not.  Large batches keep lists of the sequences' keys in the part of ws
+ * that the indexing calls use for token scores. */
 int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, const void* v_main, const int32_t* idx,
                    const void* k_swa, const void* v_swa, const int32_t* swa_head, const int32_t* n_swa,
                    const void* k_draft, const void* v_draft, const int32_t* parent, const int32_t* n_draft, void* out,
@@ -440,7 +443,8 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
  * nothing.  live[b] = 0 leaves the query out: its weights are written as 0
  * and nothing of it is read (NULL: all are wanted).
  *   q [B, H, dk]  k_main [B / T, N, dk]  idx [B, K]  lse [B, H]  live [B]
- *   weights [B, K] fp32 */
+ *   weights [B, K] fp32
+ * batch <= 65,535. */
 int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main, const int32_t* idx, const float* lse,
                       const int32_t* live, float* weights, void* ws, size_t ws_bytes, csa2_stream_t stream);
 
@@ -471,8 +475,10 @@ typedef struct {
  * recorded (bad index) and ends the path before it.
  *   path [S, T]  n_path [S]  swa_head [S], n_swa [S] (read and updated)
  *   mass [S, N] int64 (read and updated)
- * 1 <= n_layers <= 64; shape.swa >= 1; shape.tokens = T.  Windows, heads and
- * mass must not overlap what the call reads. */
+ * 1 <= n_layers <= 64; shape.swa >= 1; shape.tokens = T <= 128; S <= 65,535.
+ * ws holds only the error word (NULL with ws_bytes = 0: the static scratch's,
+ * as for csa2_swa_append).  Windows, heads and mass must not overlap what the
+ * call reads, nor one layer's windows another's. */
 int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int32_t n_layers, const int32_t* path,
                      const int32_t* n_path, int32_t* swa_head, int32_t* n_swa, int64_t* mass, void* ws, size_t ws_bytes,
                      csa2_stream_t stream);
@@ -490,7 +496,8 @@ int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int3
  * Rows behind the last entry stay as they were, but for mass_out, which is 0
  * there.  Either every _out is its input (in place: a sequence that is not
  * evicted from is not written, its row of kept apart), or the
- * outputs overlap no input (then every sequence is copied). */
+ * outputs overlap no input (then every sequence is copied).  kept and kb_out
+ * overlap nothing.  ws as for csa2_tree_commit; batch <= 65,535. */
 int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_t sink, int32_t recent,
                   const void* k_main, const void* v_main, const void* k_idx, const int64_t* mass, const int32_t* n_valid,
                   void* k_main_out, void* v_main_out, void* k_idx_out, int64_t* mass_out, int32_t* n_valid_out,

@@ -14,7 +14,7 @@
 #include <mutex>
 
 #include "../../include/csa2.h"
-#include "internal.h"
+#include "draft.h"
 
 using namespace csa2;
 

@@ -43,7 +43,7 @@
 // geometry.  Its output is bf16, and it reads nothing before the launch in front
 // of it is complete.  8 queries of 640 slots take 12.0 us, 64 take 15.3.
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 #include "tree.cuh"
 
 namespace csa2 {

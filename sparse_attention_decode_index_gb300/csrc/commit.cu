@@ -18,7 +18,7 @@
 // Like the cache-maintenance kernels it lets no later launch start early: the
 // attention reads n_swa and the windows before its own wait.
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 
 namespace csa2 {
 

@@ -253,23 +253,16 @@ CSA2_DEV void store_elem(void* base, long long i, int dtype, float v) {
 // order in fp32, optionally rounded half-to-even; 0 for a block with no valid
 // entry.  Shared by the from-scratch and the incremental (append) kernels so
 // that both give bit-identical keys.
-// `row_of(r)` is the row that holds entry r.
-template <typename RowOf>
-CSA2_DEV float block_key_rows(const void* k_idx, const RowOf& row_of, int dim, int block, int nv, int j, int d,
+CSA2_DEV float block_key_elem(const void* k_idx, long long row0, int dim, int block, int nv, int j, int d,
                               int dtype, int round_to_int) {
   const int r0 = j * block;
   const int c = min(block, nv - r0);
   if (c <= 0) return 0.f;
   float s = 0.f;
-  for (int r = 0; r < c; ++r) s += load_elem(k_idx, row_of(r0 + r) * dim + d, dtype);
+  for (int r = 0; r < c; ++r) s += load_elem(k_idx, (row0 + r0 + r) * dim + d, dtype);
   float v = s / float(c);
   if (round_to_int) v = rintf(v);
   return v;
-}
-
-CSA2_DEV float block_key_elem(const void* k_idx, long long row0, int dim, int block, int nv, int j, int d,
-                              int dtype, int round_to_int) {
-  return block_key_rows(k_idx, [&](int r) { return row0 + r; }, dim, block, nv, j, d, dtype, round_to_int);
 }
 
 }  // namespace csa2

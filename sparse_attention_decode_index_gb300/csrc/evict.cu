@@ -23,7 +23,7 @@
 #include <atomic>
 
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 
 namespace csa2 {
 
@@ -284,6 +284,18 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 }
 
 // ------------------------------------------------------------------ moving the rows
+
+// block_key_elem for entries whose rows lie elsewhere: entry r in row row_of(r).
+template <typename RowOf>
+CSA2_DEV float block_key_rows(const void* k_idx, const RowOf& row_of, int dim, int block, int n, int j, int d, int dtype,
+                              int round_to_int) {
+  const int r0 = j * block, members = min(block, n - r0);
+  if (members <= 0) return 0.f;
+  float sum = 0.f;
+  for (int r = 0; r < members; ++r) sum += load_elem(k_idx, (long long)row_of(r0 + r) * dim + d, dtype);
+  const float mean = sum / float(members);
+  return round_to_int ? rintf(mean) : mean;
+}
 
 // Entries of a sequence before and after; in place n_valid holds the former
 // until evict_counts_kernel, the last launch.

@@ -21,7 +21,7 @@
 // hold the two halves of pairs; its head comes from a multiplication by a
 // precomputed reciprocal.
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 
 namespace csa2 {
 

@@ -14,7 +14,7 @@
 //   sum): 3.5 us a launch for up to 16 queries of 512 slots.
 // weights_generic_kernel -- any shape: a warp per slot.
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 #include "tc.cuh"
 #include "tree.cuh"
 

@@ -2,7 +2,7 @@
 // it along its path (device side, shared by the tree attention kernels).
 #pragma once
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 
 namespace csa2 {
 

@@ -39,7 +39,7 @@
 // that masks it (0 * inf): rows of O that are not finite are computed again
 // from their own keys.
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 #include "tc.cuh"
 #include "tree.cuh"
 

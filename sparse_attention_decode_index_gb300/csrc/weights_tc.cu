@@ -12,7 +12,7 @@
 //   4 warps turn the scores into weights.
 // Bound by the gather (49 KB a tile).
 #include "common.cuh"
-#include "internal.h"
+#include "draft.h"
 #include "tc.cuh"
 
 namespace csa2 {

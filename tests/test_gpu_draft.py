@@ -600,6 +600,13 @@ def run_evict(csa2, d, args, in_place, rounded=True, with_kb=True):
         assert all(torch.equal(a, b) for a, b in zip(host(d.k, d.v, d.x, d.mass, d.n), before))
     assert_no_device_error(csa2, ws)
     check_evict(d, before, got, kept.cpu(), None if kb is None else kb.cpu(), args, rounded, untouched)
+    if with_kb:   # bit for bit what csa2_block_keys gives
+        x, n = (d.x, d.n) if in_place else (outs[2], outs[4])
+        ref = torch.empty_like(kb)
+        csa2.block_keys(d.sh, x, n, ref, ws, round_to_int=rounded)
+        for s in range(S):
+            if not in_place or int(before[4][s]) > args[0]:
+                assert torch.equal(kb[s], ref[s])
 
 
 @pytest.mark.parametrize("in_place", [False, True])
@@ -608,6 +615,13 @@ def run_evict(csa2, d, args, in_place, rounded=True, with_kb=True):
 def test_kv_evict_any_shape(csa2, dk, dv, dI, block, dtype, in_place):
     d = evict_inputs(3, 203, dk, dv, dI, block, dtype, dk, "ties", n_valid=[203, 150, 20])
     run_evict(csa2, d, (140, 120, 4, 9), in_place, rounded=False)
+
+
+@pytest.mark.parametrize("N,keep", [(400001, 300000), (250000, 100), (200000, 199999)])
+def test_kv_evict_long_caches(csa2, N, keep):
+    """Caches whose masses fit the shared memory of 8 CTAs, of 16, or of none."""
+    d = evict_inputs(1, N, 8, 4, 2, 8, "bf16", N, "ties" if keep > 1000 else "spread", n_valid=[N])
+    run_evict(csa2, d, (keep, keep, 3, 7), False)
 
 
 def test_kv_evict_counts_and_no_workspace(csa2):
