@@ -25,18 +25,37 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kBatch = 4;                 // layers whose idx and weights a thread has in flight
+constexpr int kCopies = 2;                // row units a thread has in flight
+constexpr int kBatch = 8;                 // layers whose idx and weights a thread has in flight
 constexpr float kMaxWeight = 1048576.f;   // 2^20: w * 2^32 stays below 2^53
 
+// The path's rows [j0, n) into the rings of layers rank, rank + ncta, ...: all
+// the units of all these rows are one list, so that a thread waits for its
+// loads once or twice, not layer by layer.
 template <typename U>
-CSA2_DEV void copy_rows(void* dst, const void* src, int row_bytes, long long dst_row0, long long src_row0, int j0,
-                        int n, int slot, int ring, const int* path) {
-  const int per = row_bytes / int(sizeof(U));
-  for (int i = threadIdx.x; i < (n - j0) * per; i += kThreads) {
-    const int j = j0 + i / per, u = i % per;
-    int r = slot + j;                       // slot < ring, j < n: fold below
-    r %= ring;
-    static_cast<U*>(dst)[(dst_row0 + r) * per + u] = static_cast<const U*>(src)[(src_row0 + path[j]) * per + u];
+CSA2_DEV void copy_rows(const TreeCommitArgs& a, int rank, int ncta, long long ring0, long long draft0, int j0, int n, int slot,
+                        const int* path) {
+  const int ku = a.k_bytes / int(sizeof(U)), per_row = ku + a.v_bytes / int(sizeof(U)), per_layer = (n - j0) * per_row;
+  const int total = (a.n_layers - rank + ncta - 1) / ncta * per_layer;
+  for (int i0 = threadIdx.x; i0 < total; i0 += kCopies * kThreads) {
+    U w[kCopies];
+    U* to[kCopies];
+#pragma unroll
+    for (int m = 0; m < kCopies; ++m) {
+      const int i = i0 + m * kThreads;
+      if (i >= total) break;
+      const int l = i / per_layer, x = i - l * per_layer, j = j0 + x / per_row;
+      int u = x % per_row;
+      const TreeCommitArgs::Slot& y = a.slot[rank + l * ncta];
+      const bool k = u < ku;
+      if (!k) u -= ku;
+      const int per = k ? ku : per_row - ku;
+      to[m] = static_cast<U*>(k ? y.k_swa : y.v_swa) + (ring0 + (slot + j) % a.swa) * per + u;
+      w[m] = static_cast<const U*>(k ? y.k_draft : y.v_draft)[(draft0 + path[j]) * per + u];
+    }
+#pragma unroll
+    for (int m = 0; m < kCopies; ++m)
+      if (i0 + m * kThreads < total) *to[m] = w[m];
   }
 }
 
@@ -69,16 +88,8 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
   cluster_arrive();                          // this CTA has read the head and the fill count
   const int j0 = max(0, n - a.swa);          // rows that a longer path would push out again are not written
   const long long draft0 = (long long)seq * a.tokens, ring0 = (long long)seq * a.swa;
-  for (int l = rank; l < a.n_layers; l += ncta) {
-    const TreeCommitArgs::Slot& y = a.slot[l];
-    if (a.wide) {
-      copy_rows<uint4>(y.k_swa, y.k_draft, a.k_bytes, ring0, draft0, j0, n, slot, a.swa, path);
-      copy_rows<uint4>(y.v_swa, y.v_draft, a.v_bytes, ring0, draft0, j0, n, slot, a.swa, path);
-    } else {
-      copy_rows<uint16_t>(y.k_swa, y.k_draft, a.k_bytes, ring0, draft0, j0, n, slot, a.swa, path);
-      copy_rows<uint16_t>(y.v_swa, y.v_draft, a.v_bytes, ring0, draft0, j0, n, slot, a.swa, path);
-    }
-  }
+  if (a.wide) copy_rows<uint4>(a, rank, ncta, ring0, draft0, j0, n, slot, path);
+  else copy_rows<uint16_t>(a, rank, ncta, ring0, draft0, j0, n, slot, path);
   if (a.mass != nullptr) {
     unsigned long long* mass = a.mass + (long long)seq * a.n_entries;
     for (int i = rank * kThreads + tid; i < n * a.topk; i += ncta * kThreads) {
