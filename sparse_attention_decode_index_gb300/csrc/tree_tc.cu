@@ -527,19 +527,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seq = item / per_seq, t = (item - seq * per_seq) * group + token;
       return token < group && t < a.tokens ? seq * a.tokens + t : -1;
     };
-    uint4 q[24];                                              // a group's queries: 64 bytes of the rows in every four
+    // A group's queries, this thread's row.  A third at a time is on its way: all
+    // of them at once need more lines than the L1 beside this much shared memory
+    // has, and the producers' copies then wait behind them.
+    uint4 q[24];
     auto fetch_q = [&](int item) {
       const int query = query_of(item);
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) +
                                                         ((long long)max(query, 0) * kH + head0) * (kDk * 2));
 #pragma unroll
-      for (int x = 0; x < 24; ++x)
-        q[x] = query >= 0 ? src[(8 * (x & 3) + (lane >> 2)) * (kDk / 8) + (x >> 2) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
+      for (int b = 0; b < 3; ++b) {
+#pragma unroll
+        for (int x = 8 * b; x < 8 * b + 8; ++x)
+          q[x] = query >= 0 ? src[(8 * (x & 3) + (lane >> 2)) * (kDk / 8) + (x >> 2) * 4 + (lane & 3)] : make_uint4(0, 0, 0, 0);
+        lines_to_rows(turn, q + 8 * b);
+        lines_to_rows(turn, q + 8 * b + 4);
+      }
     };
     auto store_q = [&]() {
 #pragma unroll
       for (int b = 0; b < 6; ++b) {
-        lines_to_rows(turn, q + 4 * b);
         uint32_t r[16];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
