@@ -429,8 +429,8 @@ int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_
  * shape.swa >= 1; batch <= 65,535; out and lse overlap nothing that is read.
  * A chain of T gives what T steps of csa2_swa_append and csa2_sparse_attn
  * give.  Weights are rounded to bf16 before they meet bf16 values, their sums
- * are not.  Large batches keep lists of the sequences' keys in the part of ws
- * that the indexing calls use for token scores. */
+ * are not.  Large batches keep lists of the sequences' keys in ws, where the
+ * indexing calls keep scores, lists and the group's indices. */
 int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, const void* v_main, const int32_t* idx,
                    const void* k_swa, const void* v_swa, const int32_t* swa_head, const int32_t* n_swa,
                    const void* k_draft, const void* v_draft, const int32_t* parent, const int32_t* n_draft, void* out,

@@ -816,9 +816,9 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
   a.dtype = s.dtype;
   a.scale = softmax_scale(s);
   a.err = static_cast<int*>(ws);
-  // the groups' key lists live in the token scores' part of the workspace, which only the indexing calls use
+  // the groups' key lists live in the workspace from the token scores on, which hold nothing between calls
   const WsLayout L = layout(s);
-  return cuda_status(launch_tree_attn(a, attn_fast(s), s.batch, at<void>(ws, L.tok_scores), L.n_cand - L.tok_scores, stream));
+  return cuda_status(launch_tree_attn(a, attn_fast(s), s.batch, at<void>(ws, L.tok_scores), L.total - L.tok_scores, stream));
 }
 
 int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main, const int32_t* idx, const float* lse,

@@ -9,7 +9,8 @@ namespace csa2 {
 constexpr int kErrBadWeight = 16;   // error word: an attention weight outside [0, 2^20]
 
 // Keys of once_per_device, behind SetupKey's.
-enum DraftSetupKey { kSetupTree = 16, kSetupTreeGeneric, kSetupTreePair, kSetupWeightsTc, kSetupEvict, kSetupEvictMove };
+enum DraftSetupKey { kSetupTree = 16, kSetupTreePair, kSetupWeightsTc, kSetupEvict, kSetupEvictMove,
+                     kSetupTreeGeneric };   // and the next three: element types, warps
 
 // Rotary positions (rope.cu).
 constexpr int kMaxRopeSlots = 16;

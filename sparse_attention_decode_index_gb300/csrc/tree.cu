@@ -2,17 +2,22 @@
 // attention weights of selected entries (csa2_tree_attn, csa2_attn_weights).
 //
 // tree_generic_kernel -- any head count, dims and element type.  One CTA per
-//   (query, up to 8 heads): a warp takes a key slot at a time, its lanes
-//   striding the key's dims, and scores all the CTA's heads with the key in
-//   registers, so a K row is read once per 8 heads; after the softmax (fp32,
-//   one maximum and sum per head over all slots, which fit shared memory) the
-//   V rows are read the same way.  Bound by issue and the row loads' latency.
+//   (query, up to 8 heads).  A warp scores four key slots at a time against the
+//   CTA's heads, its lanes striding the dims, so that four rows are on their
+//   way at once and a row is read once per 8 heads; the 32 sums meet in a
+//   transposed reduction that leaves one on every lane.  The softmax (fp32)
+//   has all slots of its heads in shared memory.  For P V the slots go round
+//   the warps, the lanes have four dims each and 8 rows on their way; the
+//   warps' sums are added up in their order.  Bound by the rows' latency for
+//   few queries (10 queries, 4 heads of 128, 640 slots, fp32: 24 us), by the
+//   fp32 products for many (128 queries, 40 heads of 100 / 128, 549 slots: 80 us,
+//   16 TFLOP/s).
 // weights_mma_kernel -- bf16, 64 heads of 192, few queries: one CTA per (query, 64
 //   slots) gathers the K rows with 16-byte cp.async; S = Q K^T on mma.sync, and
 //   exp2(s - lse) is summed over the heads in fixed order.  No maximum is
 //   needed, the lse is the normaliser.  A latency chain (index, rows, product,
 //   sum): 3.5 us a launch for up to 16 queries of 512 slots.
-// weights_generic_kernel -- any shape: a warp per slot.
+// weights_generic_kernel -- any shape: four slots a warp, as above, 8 heads at a time.
 #include "common.cuh"
 #include "draft.h"
 #include "tc.cuh"
@@ -26,90 +31,130 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------ generic tree attention
 
-constexpr int kGenThreads = 256;
 constexpr int kGenHeads = 8;
+constexpr int kDimBatch = 2;         // elements of each row a lane has on their way
 constexpr int kMaxSlots = 1024;     // topk + swa
+constexpr int kPvDims = 128;        // dims of a P V pass: four a lane
+constexpr int kPvRows = 8;          // V rows a warp has on their way
 
-CSA2_DEV float warp_sum(float v) {
+// Scores of four keys against 8 heads (queries in shared memory, fp32), by a
+// warp: lane 8 x + h ends with q_h . k_x.  A null row scores 0.
+template <int kDtype>
+CSA2_DEV float score_four(const void* const (&row)[4], const float* sq, int dim) {
+  const int lane = threadIdx.x & 31;
+  float acc[32];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int i = 0; i < 32; ++i) acc[i] = 0.f;
+  for (int d0 = lane; d0 < dim; d0 += 32 * kDimBatch) {
+    float k[kDimBatch][4];
+#pragma unroll
+    for (int y = 0; y < kDimBatch; ++y)
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        k[y][x] = row[x] != nullptr && d0 + 32 * y < dim ? load_elem(row[x], d0 + 32 * y, kDtype) : 0.f;
+#pragma unroll
+    for (int y = 0; y < kDimBatch; ++y) {
+      const int d = d0 + 32 * y;
+      if (d >= dim) break;
+#pragma unroll
+      for (int h = 0; h < kGenHeads; ++h) {
+        const float q = sq[h * dim + d];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[8 * x + h] = __fmaf_rn(q, k[y][x], acc[8 * x + h]);
+      }
+    }
+  }
+  // each step halves the values a lane holds and doubles the lanes they are summed over
+#pragma unroll
+  for (int n = 16; n >= 1; n >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const bool up = (lane & n) != 0;
+      const float keep = up ? acc[i + n] : acc[i], give = up ? acc[i] : acc[i + n];
+      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+    }
+  return acc[0];
 }
 
-__global__ void __launch_bounds__(kGenThreads) tree_generic_kernel(const TreeArgs a) {
-  extern __shared__ float sh[];
+// Four elements from `i` on (wide: one access; otherwise those below `end`).
+template <int kDtype>
+CSA2_DEV float4 load_four(const void* base, int i, int end, bool wide) {
+  if (wide) {
+    if (kDtype == 1) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+  }
+  float4 r;
+  r.x = load_elem(base, i, kDtype);
+  r.y = i + 1 < end ? load_elem(base, i + 1, kDtype) : 0.f;
+  r.z = i + 2 < end ? load_elem(base, i + 2, kDtype) : 0.f;
+  r.w = i + 3 < end ? load_elem(base, i + 3, kDtype) : 0.f;
+  return r;
+}
+
+template <int kDtype, int kThreads>
+__global__ void __launch_bounds__(kThreads) tree_generic_kernel(const TreeArgs a, int wide) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(16) float sh[];
+  __shared__ int path[kMaxTreeTokens];
+  __shared__ float red[kWarps * kGenHeads], inv_s[kGenHeads];
   const int b = blockIdx.y, h0 = blockIdx.x * kGenHeads, nh = min(kGenHeads, a.heads - h0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nslots = a.topk + a.swa;
-  float* sq = sh;                                       // [kGenHeads][k_dim]
-  float* sp = sq + kGenHeads * a.k_dim;                 // [nslots][kGenHeads] logits -> weights
-  int* path = reinterpret_cast<int*>(sp + nslots * kGenHeads);
-  float* red = reinterpret_cast<float*>(path + kMaxTreeTokens);   // [8 warps][kGenHeads]
-  float* acc_s = red + 8 * kGenHeads;                   // [kGenThreads][kGenHeads]
+  const int nslots = a.topk + a.swa, rounded = (nslots + 3) & ~3;
+  const void** krow = reinterpret_cast<const void**>(sh);   // [rounded] rows of the slots (null: no key)
+  const void** vrow = krow + rounded;
+  float* sp = reinterpret_cast<float*>(vrow + rounded);     // [rounded][kGenHeads] logits -> weights
+  float* sq = sp + rounded * kGenHeads;                     // [kGenHeads][k_dim]
+  float* part = sq;                                         // later: [kWarps][kGenHeads][kPvDims] sums of P V
+  const int esize = kDtype == 1 ? 4 : 2, seq = b / a.tokens;
   pdl_wait();
-  for (int i = tid; i < kGenHeads * a.k_dim; i += kGenThreads) {
-    const int h = i / a.k_dim, d = i - h * a.k_dim;
-    sq[i] = h < nh ? load_elem(a.q, ((long long)b * a.heads + h0 + h) * a.k_dim + d, a.dtype) : 0.f;
+  for (int i = tid; i < kGenHeads * a.k_dim; i += kThreads) {
+    const int h = i / a.k_dim;
+    sq[i] = h < nh ? load_elem(a.q, ((long long)b * a.heads + h0) * a.k_dim + i, kDtype) : 0.f;
   }
   const TreeWindow win = tree_window(a, b, path, blockIdx.x == 0);
-  __syncthreads();
-  const int seq = b / a.tokens;
-  // K / V arrays and row of slot j; false: no key
-  auto slot_row = [&](int j, const void*& kb, const void*& vb, long long& row) -> bool {
+  for (int j = tid; j < rounded; j += kThreads) {
+    const void *kb = nullptr, *vb = nullptr;
+    long long row = 0;
     if (j < a.topk) {
-      if (!win.live) return false;
-      const int e = a.idx[(long long)b * a.topk + j];
-      if (e < 0 || e >= a.n_entries) {
-        if (e >= 0 && lane == 0 && blockIdx.x == 0) report(a.err, kErrBadIndex, e);
-        return false;
+      const int e = win.live ? a.idx[(long long)b * a.topk + j] : -1;
+      if (e >= a.n_entries && blockIdx.x == 0) report(a.err, kErrBadIndex, e);
+      if (e >= 0 && e < a.n_entries) {
+        kb = a.k_main;
+        vb = a.v_main;
+        row = (long long)seq * a.n_entries + e;
       }
-      kb = a.k_main;
-      vb = a.v_main;
-      row = (long long)seq * a.n_entries + e;
-      return true;
-    }
-    bool drafted;
-    if (!win.row(j - a.topk, row, drafted)) return false;
-    kb = drafted ? a.k_draft : a.k_swa;
-    vb = drafted ? a.v_draft : a.v_swa;
-    return true;
-  };
-  for (int j = warp; j < nslots; j += kGenThreads / 32) {
-    const void *kb, *vb;
-    long long row;
-    const bool ok = slot_row(j, kb, vb, row);
-    float s[kGenHeads];
-#pragma unroll
-    for (int h = 0; h < kGenHeads; ++h) s[h] = 0.f;
-    if (ok)
-      for (int d = lane; d < a.k_dim; d += 32) {
-        const float k = load_elem(kb, row * a.k_dim + d, a.dtype);
-#pragma unroll
-        for (int h = 0; h < kGenHeads; ++h) s[h] = __fmaf_rn(sq[h * a.k_dim + d], k, s[h]);
+    } else if (j < nslots) {
+      bool drafted;
+      if (win.row(j - a.topk, row, drafted)) {
+        kb = drafted ? a.k_draft : a.k_swa;
+        vb = drafted ? a.v_draft : a.v_swa;
       }
-#pragma unroll
-    for (int h = 0; h < kGenHeads; ++h) s[h] = warp_sum(s[h]);
-    if (lane < kGenHeads) {
-      float v = s[0];
-#pragma unroll
-      for (int h = 1; h < kGenHeads; ++h) v = lane == h ? s[h] : v;
-      sp[j * kGenHeads + lane] = ok ? v * a.scale : -INFINITY;
     }
+    krow[j] = kb != nullptr ? static_cast<const uint8_t*>(kb) + row * a.k_dim * esize : nullptr;
+    vrow[j] = vb != nullptr ? static_cast<const uint8_t*>(vb) + row * a.v_dim * esize : nullptr;
   }
   __syncthreads();
-  // softmax statistics: head tid % 8 of every eighth thread group
-  const int h = tid % kGenHeads, part = tid / kGenHeads;   // 32 parts
+  for (int j = 4 * warp; j < rounded; j += 4 * kWarps) {
+    const void* const row[4] = {krow[j], krow[j + 1], krow[j + 2], krow[j + 3]};
+    const float s = score_four<kDtype>(row, sq, a.k_dim);
+    sp[j * kGenHeads + lane] = krow[j + (lane >> 3)] != nullptr ? s * a.scale : -INFINITY;
+  }
+  __syncthreads();
+  // softmax statistics: head tid % 8, every (threads / 8)th slot
+  const int h = tid % kGenHeads, first = tid / kGenHeads;
   float m = -INFINITY;
-  for (int j = part; j < nslots; j += kGenThreads / kGenHeads) m = fmaxf(m, sp[j * kGenHeads + h]);
+  for (int j = first; j < nslots; j += kThreads / kGenHeads) m = fmaxf(m, sp[j * kGenHeads + h]);
   for (int o = kGenHeads; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane < kGenHeads) red[warp * kGenHeads + lane] = m;
   __syncthreads();
   m = red[h];
-  for (int w = 1; w < 8; ++w) m = fmaxf(m, red[w * kGenHeads + h]);
+  for (int w = 1; w < kWarps; ++w) m = fmaxf(m, red[w * kGenHeads + h]);
   __syncthreads();
   const float base = m == -INFINITY ? 0.f : m;
   float l = 0.f;
-  for (int j = part; j < nslots; j += kGenThreads / kGenHeads) {
+  for (int j = first; j < nslots; j += kThreads / kGenHeads) {
     const float p = expf(sp[j * kGenHeads + h] - base);
     sp[j * kGenHeads + h] = p;
     l += p;
@@ -117,49 +162,80 @@ __global__ void __launch_bounds__(kGenThreads) tree_generic_kernel(const TreeArg
   for (int o = kGenHeads; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   if (lane < kGenHeads) red[warp * kGenHeads + lane] = l;
   __syncthreads();
-  l = 0.f;
-  for (int w = 0; w < 8; ++w) l += red[w * kGenHeads + h];
+  if (tid < kGenHeads) {
+    l = 0.f;
+    for (int w = 0; w < kWarps; ++w) l += red[w * kGenHeads + h];
+    inv_s[tid] = l > 0.f ? 1.f / l : l;       // no key: 0; NaN stays NaN
+    if (tid < nh && a.lse != nullptr)
+      a.lse[(long long)b * a.heads + h0 + tid] = l == 0.f ? -INFINITY : base + logf(l);
+  }
   __syncthreads();
-  if (tid < nh && a.lse != nullptr)
-    a.lse[(long long)b * a.heads + h0 + tid] = m == -INFINITY ? -INFINITY : m + logf(l);
-  if (tid < kGenHeads) red[tid] = l > 0.f ? 1.f / l : 0.f;
-  __syncthreads();
-  // O: `wide` threads cover the dims, the thread groups share out the slots
-  int wide = 32;
-  while (wide < a.v_dim && wide < kGenThreads) wide <<= 1;
-  const int groups = kGenThreads / wide, grp = tid / wide, col = tid - grp * wide;
-  for (int d0 = 0; d0 < a.v_dim; d0 += wide) {
-    const int d = d0 + col;
-    float acc[kGenHeads];
+  for (int d0 = 0; d0 < a.v_dim; d0 += kPvDims) {
+    const int d = d0 + 4 * lane;
+    float4 acc[kGenHeads];
 #pragma unroll
-    for (int i = 0; i < kGenHeads; ++i) acc[i] = 0.f;
-    for (int j = grp; j < nslots; j += groups) {
-      const void *kb, *vb;
-      long long row;
-      if (!slot_row(j, kb, vb, row)) continue;
-      const float v = d < a.v_dim ? load_elem(vb, row * a.v_dim + d, a.dtype) : 0.f;
+    for (int i = 0; i < kGenHeads; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = warp; j0 < nslots; j0 += kPvRows * kWarps) {
+      float4 v[kPvRows];
 #pragma unroll
-      for (int i = 0; i < kGenHeads; ++i) acc[i] = __fmaf_rn(sp[j * kGenHeads + i], v, acc[i]);
+      for (int x = 0; x < kPvRows; ++x) {
+        const int j = j0 + x * kWarps;
+        const void* row = j < nslots ? vrow[j] : nullptr;
+        v[x] = row != nullptr && d < a.v_dim ? load_four<kDtype>(row, d, a.v_dim, wide != 0) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int x = 0; x < kPvRows; ++x) {
+        const int j = j0 + x * kWarps;
+        if (j >= nslots) break;
+        const float4 plo = *reinterpret_cast<const float4*>(sp + j * kGenHeads);
+        const float4 phi = *reinterpret_cast<const float4*>(sp + j * kGenHeads + 4);
+        const float ps[kGenHeads] = {plo.x, plo.y, plo.z, plo.w, phi.x, phi.y, phi.z, phi.w};
+#pragma unroll
+        for (int i = 0; i < kGenHeads; ++i) {
+          const float p = ps[i];
+          acc[i].x = __fmaf_rn(p, v[x].x, acc[i].x);
+          acc[i].y = __fmaf_rn(p, v[x].y, acc[i].y);
+          acc[i].z = __fmaf_rn(p, v[x].z, acc[i].z);
+          acc[i].w = __fmaf_rn(p, v[x].w, acc[i].w);
+        }
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kGenHeads; ++i) acc_s[tid * kGenHeads + i] = acc[i];
+    for (int i = 0; i < kGenHeads; ++i)
+      *reinterpret_cast<float4*>(part + (warp * kGenHeads + i) * kPvDims + 4 * lane) = acc[i];
     __syncthreads();
-    if (grp == 0 && d < a.v_dim)
-      for (int i = 0; i < nh; ++i) {
-        float o = 0.f;
-        for (int g = 0; g < groups; ++g) o += acc_s[(g * wide + col) * kGenHeads + i];
-        store_elem(a.out, ((long long)b * a.heads + h0 + i) * a.v_dim + d, a.dtype, o * red[i]);
-      }
+    for (int i = tid; i < nh * kPvDims; i += kThreads) {
+      const int head = i / kPvDims, x = i % kPvDims;
+      if (d0 + x >= a.v_dim) continue;
+      float o = 0.f;
+      for (int w = 0; w < kWarps; ++w) o += part[(w * kGenHeads + head) * kPvDims + x];
+      store_elem(a.out, ((long long)b * a.heads + h0 + head) * a.v_dim + d0 + x, kDtype, o * inv_s[head]);
+    }
     __syncthreads();
   }
 }
 
-size_t generic_smem(const TreeArgs& a) {
-  return (size_t(kGenHeads) * a.k_dim + size_t(a.topk + a.swa) * kGenHeads + kMaxTreeTokens + 8 * kGenHeads +
-          size_t(kGenThreads) * kGenHeads) * sizeof(float);
+constexpr size_t generic_smem(int slots, int k_dim, int threads) {
+  const size_t rounded = size_t(slots + 3) / 4 * 4;
+  const size_t q = size_t(kGenHeads) * k_dim, sums = size_t(threads / 32) * kGenHeads * kPvDims;
+  return rounded * 16 + (rounded * kGenHeads + (q > sums ? q : sums)) * sizeof(float);
 }
-constexpr size_t kGenSmemMax = (size_t(kGenHeads) * 1024 + size_t(kMaxSlots) * kGenHeads + kMaxTreeTokens +
-                                8 * kGenHeads + size_t(kGenThreads) * kGenHeads) * sizeof(float);
+
+// One CTA an SM with 16 warps while there are no more CTAs than SMs, two with
+// 8 warps beyond (10 queries, 4 heads: 28 us with 16 warps, 40 with 8; 128
+// queries, 40 heads: 116 and 95.
+template <int kDtype, int kThreads>
+cudaError_t launch_generic(const TreeArgs& a, int batch, int wide, cudaStream_t st) {
+  const cudaError_t e = once_per_device(kSetupTreeGeneric + 2 * kDtype + (kThreads == 512), [] {
+    return cudaFuncSetAttribute(tree_generic_kernel<kDtype, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                int(generic_smem(kMaxSlots, 1024, kThreads)));
+  });
+  if (e != cudaSuccess) return e;
+  note_launch();
+  return launch_pdl(tree_generic_kernel<kDtype, kThreads>,
+                    dim3(unsigned((a.heads + kGenHeads - 1) / kGenHeads), unsigned(batch)), dim3(kThreads),
+                    generic_smem(a.topk + a.swa, a.k_dim, kThreads), st, 1, a, wide);
+}
 
 // ------------------------------------------------------------------ attention weights
 
@@ -247,44 +323,41 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeight
   }
 }
 
-__global__ void __launch_bounds__(256) weights_generic_kernel(const AttnWeightsArgs a) {
+constexpr int kWGenThreads = 256, kWGenSlots = kWGenThreads / 8;   // four slots a warp
+
+template <int kDtype>
+__global__ void __launch_bounds__(kWGenThreads) weights_generic_kernel(const AttnWeightsArgs a) {
   extern __shared__ float sq[];                 // [kGenHeads][k_dim]
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int j = blockIdx.x * 8 + warp;
+  const int j0 = blockIdx.x * kWGenSlots + 4 * warp, esize = kDtype == 1 ? 4 : 2;
   pdl_wait();
   const bool live = a.live == nullptr || a.live[b] != 0;
-  int e = live && j < a.topk ? a.idx[(long long)b * a.topk + j] : -1;
-  if (e >= a.n_entries) {
-    if (lane == 0) report(a.err, kErrBadIndex, e);
-    e = -1;
+  const void* row[4];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    int e = live && j0 + x < a.topk ? a.idx[(long long)b * a.topk + j0 + x] : -1;
+    if (e >= a.n_entries) {
+      if (lane == 0) report(a.err, kErrBadIndex, e);
+      e = -1;
+    }
+    row[x] = e < 0 ? nullptr
+                   : static_cast<const uint8_t*>(a.k_main) + ((long long)(b / a.seq_div) * a.n_entries + e) * a.k_dim * esize;
   }
-  const long long row = ((long long)(b / a.seq_div) * a.n_entries + e) * a.k_dim;
-  float w = 0.f;
+  const bool key = (lane < 16 ? (lane < 8 ? row[0] : row[1]) : (lane < 24 ? row[2] : row[3])) != nullptr;
+  float w = 0.f;                                // of slot j0 + lane / 8, the heads of lane % 8
   for (int h0 = 0; live && h0 < a.heads; h0 += kGenHeads) {
-    const int nh = min(kGenHeads, a.heads - h0);
+    const int nh = min(kGenHeads, a.heads - h0), h = lane & 7;
     __syncthreads();
-    for (int i = tid; i < nh * a.k_dim; i += 256)
-      sq[i] = load_elem(a.q, ((long long)b * a.heads + h0) * a.k_dim + i, a.dtype);
+    for (int i = tid; i < kGenHeads * a.k_dim; i += kWGenThreads)
+      sq[i] = i < nh * a.k_dim ? load_elem(a.q, ((long long)b * a.heads + h0) * a.k_dim + i, kDtype) : 0.f;
+    const float l = h < nh ? a.lse[(long long)b * a.heads + h0 + h] : -INFINITY;
     __syncthreads();
-    if (e < 0) continue;
-    float s[kGenHeads];
-#pragma unroll
-    for (int h = 0; h < kGenHeads; ++h) s[h] = 0.f;
-    for (int d = lane; d < a.k_dim; d += 32) {
-      const float k = load_elem(a.k_main, row + d, a.dtype);
-#pragma unroll
-      for (int h = 0; h < kGenHeads; ++h)
-        if (h < nh) s[h] = __fmaf_rn(sq[h * a.k_dim + d], k, s[h]);
-    }
-#pragma unroll
-    for (int h = 0; h < kGenHeads; ++h) {
-      if (h >= nh) break;
-      const float d = warp_sum(s[h]);
-      const float l = a.lse[(long long)b * a.heads + h0 + h];
-      if (l != -INFINITY) w += expf(d * a.scale - l);
-    }
+    const float s = score_four<kDtype>(row, sq, a.k_dim);
+    if (key && l != -INFINITY) w += expf(s * a.scale - l);
   }
-  if (lane == 0 && j < a.topk) a.weights[(long long)b * a.topk + j] = w;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  if ((lane & 7) == 0 && j0 + (lane >> 3) < a.topk) a.weights[(long long)b * a.topk + j0 + (lane >> 3)] = w;
 }
 
 // A cluster of CTAs per query while all the clusters run at once (up to 7/8 of
@@ -305,13 +378,13 @@ cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan
     return tree_pairs(a, batch, plan_bytes) ? launch_tree_attn_tc(a, batch / a.tokens, plan, st)
                                             : launch_tree_attn_cluster(a, batch, st);
   }
-  const cudaError_t e = once_per_device(kSetupTreeGeneric, [] {
-    return cudaFuncSetAttribute(tree_generic_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kGenSmemMax));
-  });
-  if (e != cudaSuccess) return e;
-  note_launch();
-  return launch_pdl(tree_generic_kernel, dim3(unsigned((a.heads + kGenHeads - 1) / kGenHeads), unsigned(batch)),
-                    dim3(kGenThreads), generic_smem(a), st, 1, a);
+  // four V elements an access: whole fours at 16-byte addresses
+  uintptr_t at = 0;
+  for (const void* p : {a.v_main, a.v_swa, a.v_draft}) at |= reinterpret_cast<uintptr_t>(p);
+  const int wide = a.v_dim % 4 == 0 && at % 16 == 0;
+  const bool few = (long long)batch * ((a.heads + kGenHeads - 1) / kGenHeads) <= device_sm_count();
+  if (a.dtype == 1) return few ? launch_generic<1, 512>(a, batch, wide, st) : launch_generic<1, 256>(a, batch, wide, st);
+  return few ? launch_generic<0, 512>(a, batch, wide, st) : launch_generic<0, 256>(a, batch, wide, st);
 }
 
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, cudaStream_t st) {
@@ -325,7 +398,8 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, 
   if (fast)
     return launch_pdl(weights_mma_kernel, dim3(unsigned((a.topk + kWSlots - 1) / kWSlots), unsigned(batch)), dim3(kWThreads), 0,
                       st, 1, a);
-  return launch_pdl(weights_generic_kernel, dim3(unsigned((a.topk + 7) / 8), unsigned(batch)), dim3(256),
+  const dim3 grid(unsigned((a.topk + kWGenSlots - 1) / kWGenSlots), static_cast<unsigned>(batch));
+  return launch_pdl(a.dtype == 1 ? weights_generic_kernel<1> : weights_generic_kernel<0>, grid, dim3(kWGenThreads),
                     size_t(kGenHeads) * a.k_dim * sizeof(float), st, 1, a);
 }
 
