@@ -10,7 +10,8 @@ constexpr int kErrBadWeight = 16;   // error word: an attention weight outside [
 
 // Keys of once_per_device, behind SetupKey's.
 enum DraftSetupKey { kSetupTree = 16, kSetupTreePair, kSetupWeightsTc, kSetupEvict, kSetupEvictMove,
-                     kSetupTreeGeneric };   // and the next three: element types, warps
+                     kSetupTreeRows,        // and the next: warps
+                     kSetupTreeGeneric = kSetupTreeRows + 2 };   // and the next three: element types, warps
 
 // Rotary positions (rope.cu).
 constexpr int kMaxRopeSlots = 16;
@@ -73,6 +74,11 @@ cudaError_t launch_tree_attn_cluster(const TreeArgs& a, int batch, cudaStream_t 
 // Pairs of tokens on the tensor cores (tree_tc.cu); `plan` holds tree_plan_words.
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStream_t st);
 size_t tree_plan_words(int seqs, int tokens, int topk, int swa);
+// bf16 rows of whole 8-byte pieces, any heads and dims (tree_mma.cu).
+bool tree_rows_fit(const TreeArgs& a);
+bool weights_rows_fit(const AttnWeightsArgs& a);
+cudaError_t launch_tree_rows(const TreeArgs& a, int batch, cudaStream_t st);
+cudaError_t launch_weights_rows(const AttnWeightsArgs& a, int batch, cudaStream_t st);
 cudaError_t launch_attn_weights_tc(const AttnWeightsArgs& a, int batch, cudaStream_t st);   // weights_tc.cu
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, cudaStream_t st);
 

@@ -1,7 +1,8 @@
 // Attention of drafted trees for shapes outside the fast path, and the
 // attention weights of selected entries (csa2_tree_attn, csa2_attn_weights).
 //
-// tree_generic_kernel -- any head count, dims and element type.  One CTA per
+// tree_generic_kernel -- any head count, dims and element type (bf16 rows of
+//   whole 8-byte pieces go to tree_mma.cu).  One CTA per
 //   (query, up to 8 heads).  A warp scores four key slots at a time against the
 //   CTA's heads, its lanes striding the dims, so that four rows are on their
 //   way at once and a row is read once per 8 heads; the 32 sums meet in a
@@ -378,6 +379,7 @@ cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan
     return tree_pairs(a, batch, plan_bytes) ? launch_tree_attn_tc(a, batch / a.tokens, plan, st)
                                             : launch_tree_attn_cluster(a, batch, st);
   }
+  if (tree_rows_fit(a)) return launch_tree_rows(a, batch, st);
   // four V elements an access: whole fours at 16-byte addresses
   uintptr_t at = 0;
   for (const void* p : {a.v_main, a.v_swa, a.v_draft}) at |= reinterpret_cast<uintptr_t>(p);
@@ -394,6 +396,7 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, 
   // 1 query 3.5 / 4.3 us, 16 3.5 / 4.4, 24 5.2 / 4.4, 64 7.8 / 5.6, 256 16.0 / 10.8.
   const long long ctas = (long long)batch * ((a.topk + kWSlots - 1) / kWSlots);
   if (fast && ctas > device_sm_count()) return launch_attn_weights_tc(a, batch, st);
+  if (!fast && weights_rows_fit(a)) return launch_weights_rows(a, batch, st);
   note_launch();
   if (fast)
     return launch_pdl(weights_mma_kernel, dim3(unsigned((a.topk + kWSlots - 1) / kWSlots), unsigned(batch)), dim3(kWThreads), 0,

@@ -183,8 +183,9 @@ def check_tree(sh, d, n_draft=None, parent=None, head=None):
 FAST = dict(q_heads=64, k_dim=192, v_dim=128, dtype="bf16")
 
 # Queries of a case by kernel: a cluster of CTAs per query up to 66 queries of 640 slots (266 of 160 slots), pairs of
-# tokens on the tensor cores beyond; any other shape is generic.
-KINDS = {"clusters": (FAST, 1), "pairs": (FAST, 0), "generic": (dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32"), 1)}
+# tokens on the tensor cores beyond; any other shape of bf16 rows in whole 8-byte pieces is of kind rows, the rest generic.
+KINDS = {"clusters": (FAST, 1), "pairs": (FAST, 0), "rows": (dict(q_heads=20, k_dim=100, v_dim=72, dtype="bf16"), 1),
+         "generic": (dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32"), 1)}
 
 
 def of_kind(kind, seqs, tokens, slots=100):
@@ -215,6 +216,36 @@ def test_tree_attention_fast_path(csa2, S, T, N, K, W, roots, holes):
 def test_tree_attention_any_shape(csa2, H, dk, dv, dtype, S, T, N, K, W):
     sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, q_heads=H, k_dim=dk, v_dim=dv, dtype=dtype)
     d = tree_inputs(sh, H * 7 + T, holes=1.0)
+    ws = run_tree(csa2, sh, d)
+    assert_no_device_error(csa2, ws)
+    check_tree(sh, d)
+
+
+@pytest.mark.parametrize("H,dk,dv,dtype,S,T,N,K,W", [
+    # bf16 rows in whole 8-byte pieces: few and many CTAs, part tiles of heads, slots and dims, the largest
+    (4, 128, 128, "bf16", 2, 10, 600, 512, 128), (40, 100, 64, "bf16", 7, 18, 700, 512, 64), (17, 4, 4, "bf16", 3, 7, 90, 31, 17),
+    (1, 20, 132, "bf16", 1, 1, 5, 1, 1), (33, 72, 16, "bf16", 10, 11, 65, 40, 9), (16, 1024, 1024, "bf16", 1, 2, 1500, 900, 124),
+    (8, 192, 128, "bf16", 1, 128, 300, 99, 37),
+    # the generic kernel: bf16 rows that are not, many CTAs of fp32, part fours of V dims
+    (5, 18, 128, "bf16", 2, 9, 80, 33, 8), (5, 64, 7, "bf16", 30, 7, 80, 33, 8), (40, 100, 128, "f32", 4, 12, 600, 512, 37),
+    (9, 130, 130, "f32", 3, 2, 1500, 900, 124), (12, 1024, 1024, "f32", 1, 2, 90, 65, 3), (3, 33, 260, "f32", 64, 1, 50, 13, 5)])
+def test_tree_attention_other_shapes_by_kernel(csa2, H, dk, dv, dtype, S, T, N, K, W):
+    sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, q_heads=H, k_dim=dk, v_dim=dv, dtype=dtype)
+    d = tree_inputs(sh, H * 7 + T, holes=1.0)
+    ws = run_tree(csa2, sh, d)
+    assert_no_device_error(csa2, ws)
+    check_tree(sh, d)
+
+
+@pytest.mark.parametrize("off", [1, 2, 4])
+def test_tree_attention_of_rows_at_any_address(csa2, off):
+    """Caches that start `off` elements into an allocation: at 2, 4 and 8 bytes the kernels of each width."""
+    sh = shape(6, tokens=3, n_entries=60, topk=33, swa=7, q_heads=6, k_dim=20, v_dim=12, dtype="bf16")
+    d = tree_inputs(sh, 21, holes=1.0)
+    for n in ("q", "k_main", "v_main", "k_swa", "v_swa", "k_draft", "v_draft"):
+        t = getattr(d, n)
+        moved = torch.empty(t.numel() + off, dtype=t.dtype, device="cuda")[off:].view(t.shape)
+        setattr(d, n, moved.copy_(t))
     ws = run_tree(csa2, sh, d)
     assert_no_device_error(csa2, ws)
     check_tree(sh, d)
@@ -394,6 +425,8 @@ SHAPES = [(64, 192, "bf16"), (5, 24, "f32"), (16, 64, "bf16"), (1, 1, "f32"), (1
 
 @pytest.mark.parametrize("H,dk,dtype,S,T,N,K", [
     (*x, *y) for x in SHAPES for y in [(1, 1, 5, 1), (2, 3, 300, 130), (1, 2, 700, 512)]] + [
+    (17, 4, "bf16", 3, 5, 90, 65), (40, 100, "bf16", 8, 16, 600, 256), (5, 18, "bf16", 2, 3, 300, 130),
+    (40, 100, "f32", 8, 16, 600, 256)] + [
     # the fast shape in batches that fill the GPU: a tile or several a query, part tiles, more queries than CTAs
     (64, 192, "bf16", *y) for y in [(70, 1, 300, 130), (16, 5, 700, 512), (200, 1, 40, 9), (33, 9, 300, 128), (3, 50, 1100, 1000)]])
 def test_attention_weights(csa2, H, dk, dtype, S, T, N, K):
