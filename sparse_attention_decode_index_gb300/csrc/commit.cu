@@ -11,9 +11,11 @@
 // integer sums depend on no order, so neither the atomics nor the merging
 // change them, and they stay exact where fp32 sums would stop growing.  The
 // scaling by 2^32 is exact in fp32 and the conversion rounds once.
-// Bound by the latency of the loads behind each other (count, path, rows) for
-// few sequences and by the reads of idx and weights and the 64-bit L2 atomics
-// for many.
+// Bound by the latency of the loads behind each other (count, path, rows or
+// idx, weights, atomics): one sequence of 8 tokens and 4 layers 6.5 us, 64 sequences
+// of 16 tokens and 20 layers 18 to 22 us, where the bytes need 5.2.  Leaving out the atomics
+// or the copies changed neither by more than 2 us; adding up neighbours first
+// took the latter from 44 us.
 //
 // Like the cache-maintenance kernels it lets no later launch start early: the
 // attention reads n_swa and the windows before its own wait.

@@ -8,14 +8,17 @@
 //   sweep of shared memory, one push of 256 counts into every CTA of the
 //   cluster and one cluster barrier.  Masses are skewed (many entries draw next to
 //   none), so the sweep adds up a warp's most frequent bin by a ballot before
-//   its shared-memory atomics.
+//   its shared-memory atomics.  Bound by the passes' cluster barriers: 64 x 8,192
+//   masses 15.5 us, 1 x 262,144 on 16 CTAs 27 us (masses read again a pass: 29 and 100).
 // evict_move_kernel -- out of place: every row is gathered by its entry, 16
-//   bytes a thread, so it runs at the rate of a copy.
+//   bytes a thread, so it runs at the rate of a copy: 64 x 8,192 entries down to 6,145
+//   82 to 92 us, where a plain copy of these bytes takes 83.
 // evict_shift_kernel -- in place: rows only ever move down, but a row's new
 //   place may still hold a row that another one needs.  A CTA therefore owns a
 //   column slice of all of a sequence's rows and moves it in ascending order,
 //   so that no CTA waits for another.  Few sequences leave it few CTAs: it is
-//   bound by their loads' latency then.
+//   bound by their loads' latency then, a tile read ahead of the one that is written
+//   (64 x 8,192: 144 us with the selection, 1 x 262,144: 367 us, 49 CTAs).
 // evict_block_keys_kernel -- the result's block keys, where the move has not
 //   made them (in place, or blocks that do not divide its tiles).
 // evict_counts_kernel -- in place, n_valid changes last: the launches before

@@ -15,9 +15,9 @@
 // up to 8 rows and makes all their cos and sin at once (one angle a thread,
 // kept in shared memory and used by all the heads of all the tensors), so that
 // the chain position -> angle -> sincospif is waited for once per 8 rows; with one
-// row a block its latency, not the memory, set the time (8,192 rows of 64
-// heads of 192: 237 us against 60 us for the bytes).  Few rows are split over the heads
-// instead.  An item is one 16-byte vector that is copied, or the vectors that
+// row a block its latency, not the memory, set the time (8,192 rows of 64 + 1
+// heads of 192: 239 us; 8 rows a block 69.6 us, 5.9 TB/s, the floor being 60.3).
+// Few rows are split over the heads instead (8 rows: 5.8 us, a launch and that chain).  An item is one 16-byte vector that is copied, or the vectors that
 // hold the two halves of pairs; its head comes from a multiplication by a
 // precomputed reciprocal.
 #include "common.cuh"

@@ -11,7 +11,7 @@
 //   O = P V     the slots go round the warps, 16 a step.  B wants the pairs along the
 //     slots: a lane loads four dims of its four slots and interleaves them, so
 //     that column g of product j is dim 4 g + j.  P is rounded to bf16 as on
-//     the fast path (half a step, 2^-9 of a weight; its sum is not rounded).
+//     the fast path (half a step, 2^-8 of a weight; its sum is not rounded).
 //     The warps' sums are added up in their order.
 //   Bound by latency, two round trips to memory per 16 slots of a warp: 126
 //   queries, 40 heads of 100 / 64, 576 slots 28.6 us (fp32 products in

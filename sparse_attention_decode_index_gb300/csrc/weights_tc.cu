@@ -10,7 +10,8 @@
 //     64 rows and normalisers into one of two buffers;
 //   1 warp issues the 12 steps of a tile into one of two TMEM buffers;
 //   4 warps turn the scores into weights.
-// Bound by the gather (49 KB a tile).
+// Bound by the gather (49 KB a tile): 256 queries of 512 slots 10.9 us, of which the
+// distinct bytes need 4.3; plain loads and mma.sync took 16.1.
 #include "common.cuh"
 #include "draft.h"
 #include "tc.cuh"
