@@ -426,7 +426,7 @@ int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_
  *   k_draft [S, T, dk]  v_draft [S, T, dv]  parent [S, T]  n_draft [S] (0..T)
  *   out [B, H, dv] in the element type (it feeds the output projection)
  *   lse [B, H] fp32 (nullable)
- * shape.swa >= 1; batch <= 65,535; out and lse overlap nothing that is read.
+ * shape.swa >= 1; batch <= 65,535; out and lse overlap nothing else (refused).
  * A chain of T gives what T steps of csa2_swa_append and csa2_sparse_attn
  * give.  Weights are rounded to bf16 before they meet bf16 values, their sums
  * are not.  Large batches keep lists of the sequences' keys in ws, where the
@@ -443,7 +443,7 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
  * nothing.  live[b] = 0 leaves the query out: its weights are written as 0
  * and nothing of it is read (NULL: all are wanted).
  *   q [B, H, dk]  k_main [B / T, N, dk]  idx [B, K]  lse [B, H]  live [B]
- *   weights [B, K] fp32
+ *   weights [B, K] fp32 (overlaps nothing that is read: refused)
  * batch <= 65,535. */
 int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main, const int32_t* idx, const float* lse,
                       const int32_t* live, float* weights, void* ws, size_t ws_bytes, csa2_stream_t stream);
@@ -477,8 +477,8 @@ typedef struct {
  *   mass [S, N] int64 (read and updated)
  * 1 <= n_layers <= 64; shape.swa >= 1; shape.tokens = T <= 128; S <= 65,535.
  * ws holds only the error word (NULL with ws_bytes = 0: the static scratch's,
- * as for csa2_swa_append).  Windows, heads and mass must not overlap what the
- * call reads, nor one layer's windows another's. */
+ * as for csa2_swa_append).  Windows, heads and mass overlap neither each other
+ * nor anything else of the call (refused). */
 int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int32_t n_layers, const int32_t* path,
                      const int32_t* n_path, int32_t* swa_head, int32_t* n_swa, int64_t* mass, void* ws, size_t ws_bytes,
                      csa2_stream_t stream);

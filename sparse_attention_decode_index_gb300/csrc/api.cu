@@ -6,11 +6,13 @@
 // compute fresh Top-K indices over the group's shared indexer keys (Reindex
 // with its own indexer query), Reuse layers attend with the latest indices,
 // and every layer attends with its own query and SWA KV.
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <functional>
 #include <mutex>
 
 #include "../../include/csa2.h"
@@ -145,6 +147,27 @@ constexpr int kMaxGridY = 65535;   // queries or sequences are a grid's y dimens
 bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   const uint64_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
+}
+
+// An array of a call; null or empty ones touch nothing.
+struct Span {
+  const void* at;
+  uint64_t bytes;
+  bool written;
+};
+
+// Whether an array that the call writes shares a byte with any other (sorts `v`).
+bool written_overlap(Span* v, int n) {
+  n = int(std::remove_if(v, v + n, [](const Span& x) { return x.at == nullptr || x.bytes == 0; }) - v);
+  std::sort(v, v + n, [](const Span& x, const Span& y) { return std::less<const void*>()(x.at, y.at); });
+  uint64_t end = 0, end_written = 0;       // of the arrays so far, of those that are written
+  for (int i = 0; i < n; ++i) {
+    const uint64_t at = reinterpret_cast<uintptr_t>(v[i].at);
+    if (at < end_written || (v[i].written && at < end)) return true;
+    end = std::max(end, at + v[i].bytes);
+    if (v[i].written) end_written = std::max(end_written, at + v[i].bytes);
+  }
+  return false;
 }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
@@ -791,6 +814,13 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
   if (attn_fast(s))
     for (const void* p : {q, k_main, v_main, k_swa, v_swa, k_draft, v_draft, static_cast<const void*>(out)})
       if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+  const uint64_t B = s.batch, S = B / seqdiv(s), esize = s.dtype == CSA2_F32 ? 4 : 2;
+  const uint64_t kb = s.k_dim * esize, vb = s.v_dim * esize;
+  Span spans[] = {{q, B * s.q_heads * kb, false}, {k_main, S * s.n_entries * kb, false}, {v_main, S * s.n_entries * vb, false},
+                  {idx, B * s.topk * 4, false}, {k_swa, S * s.swa * kb, false}, {v_swa, S * s.swa * vb, false},
+                  {swa_head, S * 4, false}, {n_swa, S * 4, false}, {k_draft, B * kb, false}, {v_draft, B * vb, false},
+                  {parent, B * 4, false}, {n_draft, S * 4, false}, {out, B * s.q_heads * vb, true}, {lse, B * s.q_heads * 4, true}};
+  if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
   TreeArgs a{};
   a.q = q;
   a.k_main = k_main;
@@ -831,6 +861,10 @@ int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main
     return CSA2_ERR_INVALID_ARG;
   const bool fast = s.dtype == CSA2_BF16 && s.q_heads == 64 && s.k_dim == 192;
   if (fast && (!aligned16(q) || !aligned16(k_main))) return CSA2_ERR_INVALID_ARG;
+  const uint64_t B = s.batch, kb = uint64_t(s.k_dim) * (s.dtype == CSA2_F32 ? 4 : 2);
+  Span spans[] = {{q, B * s.q_heads * kb, false}, {k_main, B / seqdiv(s) * s.n_entries * kb, false}, {idx, B * s.topk * 4, false},
+                  {lse, B * s.q_heads * 4, false}, {live, B * 4, false}, {weights, B * s.topk * 4, true}};
+  if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
   AttnWeightsArgs a{};
   a.q = q;
   a.k_main = k_main;
@@ -866,6 +900,10 @@ int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int3
   a.k_bytes = s.k_dim * esize;
   a.v_bytes = s.v_dim * esize;
   a.wide = a.k_bytes % 16 == 0 && a.v_bytes % 16 == 0;
+  const uint64_t nb = uint64_t(s.batch) * 4, sb = uint64_t(S) * 4;
+  Span spans[5 + 6 * kMaxTreeLayers] = {{path, nb, false}, {n_path, sb, false}, {swa_head, sb, true}, {n_swa, sb, true},
+                                        {mass, uint64_t(S) * s.n_entries * 8, true}};
+  int n_spans = 5;
   for (int l = 0; l < n_layers; ++l) {
     const csa2_tree_slot& y = layers[l];
     if (y.k_draft == nullptr || y.v_draft == nullptr || y.k_swa == nullptr || y.v_swa == nullptr)
@@ -873,7 +911,12 @@ int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int3
     if ((y.idx == nullptr) != (y.weights == nullptr)) return CSA2_ERR_INVALID_ARG;
     if (!aligned16(y.k_draft) || !aligned16(y.v_draft) || !aligned16(y.k_swa) || !aligned16(y.v_swa)) a.wide = 0;
     a.slot[l] = TreeCommitArgs::Slot{y.k_draft, y.v_draft, y.k_swa, y.v_swa, y.idx, y.weights};
+    for (const Span& x : {Span{y.k_draft, uint64_t(s.batch) * a.k_bytes, false}, Span{y.v_draft, uint64_t(s.batch) * a.v_bytes, false},
+                          Span{y.k_swa, uint64_t(S) * s.swa * a.k_bytes, true}, Span{y.v_swa, uint64_t(S) * s.swa * a.v_bytes, true},
+                          Span{y.idx, nb * s.topk, false}, Span{y.weights, nb * s.topk, false}})
+      spans[n_spans++] = x;
   }
+  if (written_overlap(spans, n_spans)) return CSA2_ERR_INVALID_ARG;
   a.n_layers = n_layers;
   a.path = path;
   a.n_path = n_path;
@@ -901,20 +944,20 @@ int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_
   if (round_to_int != 0 && round_to_int != 1) return CSA2_ERR_INVALID_ARG;
   const uint64_t B = s.batch, N = s.n_entries, nb = uint64_t(ceil_div(s.n_entries, s.block));
   const uint64_t esize = s.dtype == CSA2_F32 ? 4 : 2;
-  struct Span {
+  struct Pair {
     const void* in;
     void* out;
     uint64_t bytes;
   };
-  const Span io[5] = {{k_main, k_main_out, B * N * s.k_dim * esize},
+  const Pair io[5] = {{k_main, k_main_out, B * N * s.k_dim * esize},
                       {v_main, v_main_out, B * N * s.v_dim * esize},
                       {k_idx, k_idx_out, B * N * s.idx_dim * esize},
                       {mass, mass_out, B * N * 8},
                       {n_valid, n_valid_out, B * 4}};
-  const Span extra[2] = {{nullptr, kept, B * N * 4}, {nullptr, kb_out, B * nb * s.idx_dim * esize}};
+  const Pair extra[2] = {{nullptr, kept, B * N * 4}, {nullptr, kb_out, B * nb * s.idx_dim * esize}};
   if (kept == nullptr || !aligned8(mass) || !aligned8(mass_out)) return CSA2_ERR_INVALID_ARG;
   int same = 0;
-  for (const Span& x : io) {
+  for (const Pair& x : io) {
     if (x.in == nullptr || x.out == nullptr) return CSA2_ERR_INVALID_ARG;
     same += x.in == x.out;
   }
@@ -924,9 +967,9 @@ int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_
       if (!(same && i == j) && overlap(io[i].out, io[i].bytes, io[j].in, io[j].bytes)) return CSA2_ERR_INVALID_ARG;
       if (i != j && overlap(io[i].out, io[i].bytes, io[j].out, io[j].bytes)) return CSA2_ERR_INVALID_ARG;
     }
-  for (const Span& x : extra) {
+  for (const Pair& x : extra) {
     if (x.out == nullptr) continue;
-    for (const Span& y : io)
+    for (const Pair& y : io)
       if (overlap(x.out, x.bytes, y.in, y.bytes) || overlap(x.out, x.bytes, y.out, y.bytes)) return CSA2_ERR_INVALID_ARG;
   }
   if (kb_out != nullptr && overlap(kept, extra[0].bytes, kb_out, extra[1].bytes)) return CSA2_ERR_INVALID_ARG;

@@ -126,6 +126,43 @@ def test_tree_attn_refusals(csa2):
     assert lib.csa2_tree_attn(None, *_tree_args(), FAKE, 1 << 30, None) == INVALID
 
 
+def test_outputs_over_other_arrays_are_refused(csa2):
+    """A written array that shares a byte with any other is refused, whichever of the two starts first; arrays that only
+    touch are not looked at here (nothing may be launched without a GPU)."""
+    lib = csa2.lib()
+    s = _shape(csa2)                                       # 8 queries, 2 sequences, 64 heads of 192 / 128
+    names = ("q", "k_main", "v_main", "idx", "k_swa", "v_swa", "swa_head", "n_swa", "k_draft", "v_draft", "parent", "n_draft", "out",
+             "lse")
+    size = dict(q=8 * 64 * 384, k_main=2 * 4096 * 384, v_main=2 * 4096 * 256, idx=8 * 2048, k_swa=2 * 128 * 384, v_swa=2 * 128 * 256,
+                swa_head=8, n_swa=8, k_draft=8 * 384, v_draft=8 * 256, parent=32, n_draft=8, out=8 * 64 * 256, lse=8 * 64 * 4)
+    at = {n: FAKE + i * STEP for i, n in enumerate(names)}
+    for n in names:
+        for w in ("out", "lse"):
+            if n == w:
+                continue
+            last = at[n] + (size[n] - 1) // 16 * 16        # in n's last bytes; and n in the written array's last ones
+            for p in (at[n], last, at[n] - (size[w] - 1) // 16 * 16):
+                assert lib.csa2_tree_attn(ctypes.byref(s), *_tree_args(**{w: p}), FAKE - STEP, _ws(csa2, s), None) == INVALID, (n, w)
+    keys = ("q", "k_main", "idx", "lse", "live", "weights")
+    for n in keys[:-1]:
+        d = {x: FAKE + i * STEP for i, x in enumerate(keys)}
+        d["weights"] = d[n] + (16 if n != "live" else 28)
+        assert lib.csa2_attn_weights(ctypes.byref(s), *d.values(), FAKE - STEP, _ws(csa2, s), None) == INVALID, n
+    far = [FAKE + i * STEP for i in range(20)]
+
+    def commit(slots, *rest):
+        arr = (csa2.CTreeSlot * len(slots))(*[csa2.CTreeSlot(*y) for y in slots])
+        return lib.csa2_tree_commit(ctypes.byref(s), ctypes.cast(arr, ctypes.c_void_p), len(slots), *rest, FAKE - STEP, _ws(csa2, s), None)
+
+    one, two, rest = far[:6], far[6:10] + far[4:6], far[10:15]   # the layers share their idx and weights
+    for i in (2, 3):                                       # a window: over each other array
+        for p in one[:2] + two[:4] + far[4:6] + rest:
+            assert commit([one, two[:i] + [p if p != two[i] else one[i]] + two[i + 1:]], *rest) == INVALID, (i, p)
+    for i in (2, 3, 4):                                    # head, fill count, mass
+        for p in one + two[:4] + [x for x in rest if x != rest[i]]:
+            assert commit([one, two], *rest[:i], p, *rest[i + 1:]) == INVALID, (i, p)
+
+
 def test_attn_weights_refusals(csa2):
     lib = csa2.lib()
     s = _shape(csa2)
