@@ -290,8 +290,9 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeight
   }
   // -lse in base 2; a head that attended nothing adds nothing
   float n0 = a.lse[(long long)b * kH + warp * 16 + g], n1 = a.lse[(long long)b * kH + warp * 16 + g + 8];
-  n0 = n0 == -INFINITY ? -INFINITY : -n0 * kLog2e;
-  n1 = n1 == -INFINITY ? -INFINITY : -n1 * kLog2e;
+  const bool off0 = n0 == -INFINITY, off1 = n1 == -INFINITY;
+  n0 *= -kLog2e;
+  n1 *= -kLog2e;
   const float sl2 = a.scale * kLog2e;
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
@@ -308,8 +309,8 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeight
     }
 #pragma unroll
   for (int n = 0; n < kWSlots / 8; ++n) {
-    float w0 = ex2(__fmaf_rn(s[n][0], sl2, n0)) + ex2(__fmaf_rn(s[n][2], sl2, n1));
-    float w1 = ex2(__fmaf_rn(s[n][1], sl2, n0)) + ex2(__fmaf_rn(s[n][3], sl2, n1));
+    float w0 = (off0 ? 0.f : ex2(__fmaf_rn(s[n][0], sl2, n0))) + (off1 ? 0.f : ex2(__fmaf_rn(s[n][2], sl2, n1)));
+    float w1 = (off0 ? 0.f : ex2(__fmaf_rn(s[n][1], sl2, n0))) + (off1 ? 0.f : ex2(__fmaf_rn(s[n][3], sl2, n1)));
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {
       w0 += __shfl_xor_sync(0xffffffffu, w0, o);

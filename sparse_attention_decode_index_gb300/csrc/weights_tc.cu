@@ -32,6 +32,7 @@ struct Shared {
   uint8_t k[kStages][kTile * kDk * 2];         // 3 blocks of 64 dims: 128 rows of 128 bytes
   uint8_t q[2][kH * kDk * 2];                  // 3 blocks of 64 dims: 64 rows of 128 bytes
   float shift[2][kH];                          // -lse in base 2
+  uint32_t none[2][kH / 32];                    // heads whose lse is -inf
   uint64_t full[kStages], empty[kStages];
   uint64_t q_full[2], shift_full[2], q_empty[2];
   uint64_t s_full[2], s_free[2];
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const AttnWeigh
       const bool on = wanted(b);
       const uint32_t qb = queries & 1;
       bool ok = !on || tc_wait_warp(c, &c.shift_full[qb], (queries >> 1) & 1, a.err);
+      const uint32_t none0 = ok && on ? c.none[qb][0] : 0, none1 = ok && on ? c.none[qb][1] : 0;
       for (; x < end && ok; ++x) {
         const int j = (x - b * tiles_per_query) * kTile + tid;
         const long long at = (long long)b * a.topk + j;
@@ -102,6 +104,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const AttnWeigh
         tc_fence_before();
         mbar_arrive(&c.s_free[buf]);
         ++tiles;
+        if ((none0 | none1) != 0) {             // a head that attended nothing adds nothing, whatever its scores are
+#pragma unroll
+          for (int h = 0; h < kH; ++h)
+            if (((h < 32 ? none0 : none1) >> (h & 31)) & 1u) s[h] = 0;
+        }
         float2 w0 = make_float2(0.f, 0.f), w1 = w0;
 #pragma unroll
         for (int h = 0; h < kH; h += 4) {
@@ -147,6 +154,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_tc_kernel(const AttnWeigh
       if (ptid < kH) {
         const float l = a.lse[(long long)b * kH + ptid];
         c.shift[qb][ptid] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        const unsigned none = __ballot_sync(0xffffffffu, l == -INFINITY);
+        if (lane == 0) c.none[qb][w] = none;
         mbar_arrive(&c.shift_full[qb]);
       }
       const uint8_t* q0 = static_cast<const uint8_t*>(a.q) + (long long)b * kH * (kDk * 2);

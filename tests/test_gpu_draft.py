@@ -454,6 +454,32 @@ def test_attention_weights(csa2, H, dk, dtype, S, T, N, K):
     assert (w2[live == 0] == 0).all() and torch.equal(w2[live == 1], w[live == 1])
 
 
+@pytest.mark.parametrize("H,dk,dtype,B", [(64, 192, "bf16", 3), (64, 192, "bf16", 200), (20, 100, "bf16", 3), (5, 18, "bf16", 3),
+                                          (5, 24, "f32", 3)])
+def test_heads_that_attended_nothing_add_nothing_whatever_they_hold(csa2, H, dk, dtype, B):
+    """A head whose lse is -inf adds nothing though its query is NaN or infinite, nor though the row is; the heads beside
+    it are not touched.  An lse of +inf, a score being so, stays the definition's NaN."""
+    sh = shape(B, n_entries=200, topk=130, swa=4, q_heads=H, k_dim=dk, v_dim=16, dtype=dtype)
+    d = tree_inputs(sh, 9)
+    lse = torch.full((B, H), 6.0, device="cuda")
+    lse[:, 1], lse[1] = float("-inf"), float("-inf")
+    d.k_main[1, int(d.idx[1, 0])] = float("inf")           # of a query whose heads all are
+    ws = csa2.workspace(sh)
+    w = [torch.empty((B, 130), device="cuda") for _ in range(3)]
+    q = d.q.clone()
+    q[:, 1], q[1] = 0, 0
+    csa2.attn_weights(sh, q, d.k_main, d.idx, lse, w[0], ws)
+    q[:, 1, ::2], q[:, 1, 1::2], q[1] = float("nan"), float("inf"), float("-inf")
+    csa2.attn_weights(sh, q, d.k_main, d.idx, lse, w[1], ws)
+    assert_no_device_error(csa2, ws)
+    assert torch.isfinite(w[1]).all() and torch.equal(w[0], w[1]) and (w[1][1] == 0).all() and (w[1][0] > 0).any()
+    lse[0, 0], q[0, 0] = float("inf"), 0
+    q[0, 0, 0] = 1.0
+    d.k_main[0, int(d.idx[0, 0]), 0] = float("inf")
+    csa2.attn_weights(sh, q, d.k_main, d.idx, lse, w[2], ws)
+    assert torch.isnan(w[2][0, 0])
+
+
 @pytest.mark.parametrize("B", [4, 90])
 def test_attention_weights_of_a_whole_row_sum_to_the_heads(csa2, B):
     """With the window empty and one token, an attention's weights add up to the head count, less the token's own."""
