@@ -2,20 +2,23 @@
 // K and V rows into every layer's window ring, and the accepted queries'
 // attention weights into the per-entry mass.
 //
-// One cluster of CTAs per sequence.  All of them read the shared head and fill
-// count, meet at a cluster barrier, and the first then advances both.  The
-// window rows are shared out by layer, the weights by (token, slot): a thread
-// takes one selected slot through all the layers and adds up neighbouring layers that
-// selected the same entry (Reuse layers attend with their indexing layer's
-// list) before one atomic.  The mass is a 64-bit integer in units of 2^-32:
-// integer sums depend on no order, so neither the atomics nor the merging
-// change them, and they stay exact where fp32 sums would stop growing.  The
-// scaling by 2^32 is exact in fp32 and the conversion rounds once.
-// Bound by the latency of the loads behind each other (count, path, rows or
-// idx, weights, atomics): one sequence of 8 tokens and 4 layers 6.5 us, 64 sequences
-// of 16 tokens and 20 layers 18 to 22 us, where the bytes need 5.2.  Leaving out the atomics
-// or the copies changed neither by more than 2 us; adding up neighbours first
-// took the latter from 44 us.
+// A sequence's first CTAs, a cluster, copy its window rows, shared out by
+// layer; all of them read the shared head and fill count, meet at a cluster
+// barrier, and the first then advances both.  Its other CTAs add up weights: a
+// thread takes one selected slot of an accepted token through 8 layers and adds
+// up neighbouring layers that selected the same entry (Reuse layers attend with
+// their indexing layer's list) before one atomic.  They need only the path,
+// which nobody writes, so no barrier holds them, and a sequence with a long
+// path has as many of them at work as it needs (paths differ: the weights in
+// the clusters, 8 CTAs of 512 threads a sequence, took 18.2 us for 64 sequences of 16
+// tokens and 20 layers where this takes 11.5; one sequence, 8 tokens, 4 layers: 3.7 and 2.5).
+// Bound by the latency of path, idx and weight behind each other, and for that case
+// by the reads of 24 MB of idx and weights (with the windows 5.2 us at HBM's rate);
+// without the atomics, or without the copies, it is 0.3 and 0.9 us faster.
+// The mass is a 64-bit integer in units of 2^-32: integer sums depend on no
+// order, so neither the atomics nor the merging change them, and they stay
+// exact where fp32 sums would stop growing.  A weight is split into its whole
+// part and the rest, which is exact, and the rest rounded once.
 //
 // Like the cache-maintenance kernels it lets no later launch start early: the
 // attention reads n_swa and the windows before its own wait.
@@ -26,10 +29,12 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kCopies = 2;                // row units a thread has in flight
-constexpr int kBatch = 8;                 // layers whose idx and weights a thread has in flight
-constexpr float kMaxWeight = 1048576.f;   // 2^20: w * 2^32 stays below 2^53
+constexpr int kThreads = 128;              // (256: 13.2 us, 64: 15.3, where 128 take 11.5)
+static_assert(kThreads >= kMaxTreeTokens, "a thread for every token of a path");
+constexpr int kCopies = 4;                // row units a thread has in flight
+constexpr int kBatch = 8;                 // layers of an item of the mass, their idx and weights in flight together
+constexpr float kMaxWeight = 1048576.f;   // 2^20
+constexpr int kMassCtas = 16;             // CTAs of the mass for every SM at most (24: 11.9 us, 8 to 16: 11.5)
 
 // The path's rows [j0, n) into the rings of layers rank, rank + ncta, ...: all
 // the units of all these rows are one list, so that a thread waits for its
@@ -61,79 +66,89 @@ CSA2_DEV void copy_rows(const TreeCommitArgs& a, int rank, int ncta, long long r
   }
 }
 
-__global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_constant__ TreeCommitArgs a) {
-  __shared__ int path[kMaxTreeTokens];
-  __shared__ int end_s;
-  const int seq = blockIdx.y, tid = threadIdx.x;
-  const int rank = int(cluster_rank()), ncta = int(cluster_size());
-  pdl_wait();
-  int* err = rank == 0 ? a.err : nullptr;
-  if (tid == 0) end_s = a.tokens;
-  int n = clamp_count(a.n_path[seq], a.tokens, tid == 0 ? err : nullptr);
-  int slot = a.head[seq];
-  if (slot < 0 || slot >= a.swa) {
-    if (tid == 0) report(err, kErrBadCount, slot);
-    slot = slot < 0 ? 0 : a.swa - 1;
-  }
-  const int fill = clamp_count(a.n_swa[seq], a.swa, tid == 0 ? err : nullptr);
+// The accepted path of a sequence into `path` (shared memory); its length, a bad id ending it.
+CSA2_DEV int load_path(const TreeCommitArgs& a, int seq, int* path, int* end, bool reports) {
+  const int tid = threadIdx.x;
+  if (tid == 0) *end = a.tokens;
+  const int n = clamp_count(a.n_path[seq], a.tokens, reports && tid == 0 ? a.err : nullptr);
   __syncthreads();
   if (tid < n) {
     const int t = a.path[(long long)seq * a.tokens + tid];
     path[tid] = t;
     if (t < 0 || t >= a.tokens) {
-      report(err, kErrBadIndex, t);
-      atomicMin(&end_s, tid);
+      if (reports) report(a.err, kErrBadIndex, t);
+      atomicMin(end, tid);
     }
   }
   __syncthreads();
-  n = min(n, end_s);                         // a bad id ends the path before it
-  cluster_arrive();                          // this CTA has read the head and the fill count
-  const int j0 = max(0, n - a.swa);          // rows that a longer path would push out again are not written
-  const long long draft0 = (long long)seq * a.tokens, ring0 = (long long)seq * a.swa;
-  if (a.wide) copy_rows<uint4>(a, rank, ncta, ring0, draft0, j0, n, slot, path);
-  else copy_rows<uint16_t>(a, rank, ncta, ring0, draft0, j0, n, slot, path);
-  if (a.mass != nullptr) {
-    unsigned long long* mass = a.mass + (long long)seq * a.n_entries;
-    for (int i = rank * kThreads + tid; i < n * a.topk; i += ncta * kThreads) {
-      const int j = i / a.topk;
-      const long long at = (draft0 + path[j]) * a.topk + (i - j * a.topk);
-      int cur = -1;                          // the entry that `sum` is for
-      unsigned long long sum = 0;
-      for (int l0 = 0; l0 < a.n_layers; l0 += kBatch) {
-        int e[kBatch];
-        float w[kBatch];
-#pragma unroll
-        for (int m = 0; m < kBatch; ++m) {
-          const bool on = l0 + m < a.n_layers && a.slot[l0 + m].weights != nullptr;
-          e[m] = on ? a.slot[l0 + m].idx[at] : -1;
-          w[m] = on ? a.slot[l0 + m].weights[at] : 0.f;
-        }
-#pragma unroll
-        for (int m = 0; m < kBatch; ++m) {
-          if (e[m] < 0) continue;
-          if (e[m] >= a.n_entries) {
-            report(a.err, kErrBadIndex, e[m]);
-            continue;
-          }
-          if (!(w[m] >= 0.f && w[m] <= kMaxWeight)) {
-            report(a.err, kErrBadWeight, e[m]);
-            continue;
-          }
-          if (e[m] != cur) {
-            if (sum != 0) atomicAdd(mass + cur, sum);
-            cur = e[m];
-            sum = 0;
-          }
-          sum += (unsigned long long)__float2ll_rn(w[m] * 4294967296.f);
-        }
-      }
-      if (sum != 0) atomicAdd(mass + cur, sum);
+  return min(n, *end);
+}
+
+// grid.x: the copying cluster of a sequence, then the CTAs of its mass (whole clusters).
+__global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_constant__ TreeCommitArgs a) {
+  __shared__ int path[kMaxTreeTokens];
+  __shared__ int end_s;
+  const int seq = blockIdx.y, tid = threadIdx.x;
+  const int ncta = int(cluster_size());
+  pdl_wait();
+  const long long draft0 = (long long)seq * a.tokens;
+  if (int(blockIdx.x) < ncta) {
+    const int rank = int(cluster_rank());
+    int* err = rank == 0 ? a.err : nullptr;
+    int slot = a.head[seq];
+    if (slot < 0 || slot >= a.swa) {
+      if (tid == 0) report(err, kErrBadCount, slot);
+      slot = slot < 0 ? 0 : a.swa - 1;
     }
+    const int fill = clamp_count(a.n_swa[seq], a.swa, tid == 0 ? err : nullptr);
+    const int n = load_path(a, seq, path, &end_s, rank == 0);
+    cluster_arrive();                        // this CTA has read the head and the fill count
+    const int j0 = max(0, n - a.swa);        // rows that a longer path would push out again are not written
+    const long long ring0 = (long long)seq * a.swa;
+    if (a.wide) copy_rows<uint4>(a, rank, ncta, ring0, draft0, j0, n, slot, path);
+    else copy_rows<uint16_t>(a, rank, ncta, ring0, draft0, j0, n, slot, path);
+    cluster_wait();
+    if (rank == 0 && tid == 0) {
+      a.head[seq] = (slot + n) % a.swa;
+      a.n_swa[seq] = min(fill + n, a.swa);
+    }
+    return;
   }
-  cluster_wait();
-  if (rank == 0 && tid == 0) {
-    a.head[seq] = (slot + n) % a.swa;
-    a.n_swa[seq] = min(fill + n, a.swa);
+  // an item: a selected slot of an accepted token in kBatch layers
+  const int n = load_path(a, seq, path, &end_s, false);
+  const int chunks = (a.n_layers + kBatch - 1) / kBatch, items = n * chunks * a.topk;
+  unsigned long long* mass = a.mass + (long long)seq * a.n_entries;
+  for (int i = (int(blockIdx.x) - ncta) * kThreads + tid; i < items; i += (int(gridDim.x) - ncta) * kThreads) {
+    const int row = i / a.topk, j = row / chunks, l0 = (row - j * chunks) * kBatch;
+    const long long at = (draft0 + path[j]) * a.topk + (i - row * a.topk);
+    int e[kBatch];
+    float w[kBatch];
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      const bool on = l0 + m < a.n_layers && a.slot[l0 + m].weights != nullptr;
+      e[m] = on ? a.slot[l0 + m].idx[at] : -1;
+      w[m] = on ? a.slot[l0 + m].weights[at] : 0.f;
+    }
+    int cur = -1, bad = 0, detail = 0;       // the entry that `sum` is for
+    unsigned long long sum = 0;
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      if (e[m] < 0) continue;
+      if (e[m] >= a.n_entries || !(w[m] >= 0.f && w[m] <= kMaxWeight)) {
+        bad |= e[m] >= a.n_entries ? kErrBadIndex : kErrBadWeight;
+        detail = e[m];
+        continue;
+      }
+      if (e[m] != cur) {
+        if (sum != 0) atomicAdd(mass + cur, sum);
+        cur = e[m];
+        sum = 0;
+      }
+      const uint32_t whole = __float2uint_rd(w[m]);
+      sum += ((unsigned long long)whole << 32) + __float2uint_rn((w[m] - float(whole)) * 4294967296.f);
+    }
+    if (sum != 0) atomicAdd(mass + cur, sum);
+    if (bad != 0) report(a.err, bad, detail);
   }
 }
 
@@ -141,9 +156,19 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
 
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, int seqs, cudaStream_t st) {
   if (seqs == 0) return cudaSuccess;
-  const int c = a.n_layers < 8 && a.mass == nullptr ? a.n_layers : 8;   // a portable cluster
+  const int c = a.n_layers < 8 ? a.n_layers : 8;   // a portable cluster
+  // CTAs of the mass: a thread an item for paths of all T tokens, in whole
+  // clusters; no more than kMassCtas an SM over all sequences (each then takes several
+  // items), as most of them find nothing to do, but a cluster at least.
+  int more = 0;
+  if (a.mass != nullptr) {
+    const long long items = (long long)a.tokens * ((a.n_layers + kBatch - 1) / kBatch) * a.topk;
+    const long long want = (items + kThreads - 1) / kThreads, most = (long long)kMassCtas * device_sm_count() / seqs;
+    more = int(((want < most ? want : most) + c - 1) / c) * c;
+    if (more < c) more = c;
+  }
   note_launch();
-  return launch_pdl(tree_commit_kernel, dim3(unsigned(c), unsigned(seqs)), dim3(kThreads), 0, st, unsigned(c), a);
+  return launch_pdl(tree_commit_kernel, dim3(unsigned(c + more), unsigned(seqs)), dim3(kThreads), 0, st, unsigned(c), a);
 }
 
 }  // namespace csa2

@@ -574,6 +574,25 @@ def test_tree_commit_bad_inputs(csa2):
     assert int(d.head[1]) == (W - 1 + 2) % W and int(d.n_swa[2]) == 3 and torch.equal(m, d.mass)
 
 
+def test_tree_commit_rounds_weights_once(csa2):
+    """Weights that end at, below and between the halves of 2^-32, whole and large ones, and entries selected twice by a
+    token: rint(w 2^32) each, in integers (w 2^32 is exact in 64 bits)."""
+    S, T, L, N, K, W = 1, 3, 11, 40, 32, 4
+    d = commit_inputs(S, T, L, N, K, W, 16, 8, "bf16", 8)
+    d.n_path.fill_(3)
+    vals = [2.0 ** -33, 3 * 2.0 ** -33, 2.0 ** -33 * 1.0001, 2.0 ** -32, 1e-40, 0.0, 0.99999994, 1.0, 1.5, 63.999996, 64.00001,
+            1000.3, 2.0 ** 20, 1048575.94, 2.0 ** -9 * 1.2345, 5 * 2.0 ** -33]
+    d.w.copy_(torch.tensor(vals).repeat(d.w.numel() // len(vals)).view(d.w.shape))
+    d.idx[:, :, 5:9] = d.idx[:, :, 4:5]                     # the same entry five times
+    d.idx[3:, :, :] = d.idx[2:3]                            # layers that share a list
+    want = commit_reference(d, L, S, T, W, N)
+    ws = csa2.workspace(d.sh)
+    csa2.tree_commit(d.sh, [(d.kd[l], d.vd[l], d.ks[l], d.vs[l], d.idx[l], d.w[l]) for l in range(L)], d.path, d.n_path, d.head,
+                     d.n_swa, ws, mass=d.mass)
+    assert_no_device_error(csa2, ws)
+    assert torch.equal(d.mass.cpu(), torch.as_tensor(want[2]))
+
+
 # ------------------------------------------------------------------ eviction
 
 def evict_inputs(S, N, dk, dv, dI, block, dtype, seed, kind, n_valid=None):
