@@ -7,9 +7,10 @@
 //   its share of the masses in shared memory, read once, so that a pass costs a
 //   sweep of shared memory, one push of 256 counts into every CTA of the
 //   cluster and one cluster barrier.  Masses are skewed (many entries draw next to
-//   none), so the sweep adds up a warp's most frequent bin by a ballot before
-//   its shared-memory atomics.  Bound by the passes' cluster barriers: 64 x 8,192
-//   masses 15.5 us, 1 x 262,144 on 16 CTAs 27 us (masses read again a pass: 29 and 100).
+//   none), so a bin has 16 counts in different banks, a lane's by its number.
+//   Bound by the sweeps' instructions and the passes' cluster barriers: 64 x 8,192
+//   masses 14.4 us, 1 x 262,144 on 16 CTAs 21.8 us (one count a bin: 15.5 and 27;
+//   masses read again a pass: 29 and 100).
 // evict_move_kernel -- out of place: every row is gathered by its entry, 16
 //   bytes a thread, so it runs at the rate of a copy: 64 x 8,192 entries down to 6,145
 //   82 to 92 us, where a plain copy of these bytes takes 83.
@@ -130,59 +131,66 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   // (More keys compete than there are places, so mn <= mx.)  The first pass
   // bins k - mn by its octave and the two bits below its leading one, 4 bins an
-  // octave, the later ones by the next 8 bits.  Invariant: the keys k >= mn with
-  // (k - mn) >> shift == prefix hold the need-th greatest, and every key with
-  // a greater such value is taken.
+  // octave, the later ones by the next 8 bits.  Invariant: the keys of
+  // [low, high], 2^shift values from a multiple of it above mn on, hold the
+  // need-th greatest, and every greater key is taken.
   int shift = 64;
-  u64 prefix = 0;
-  auto top = [&](u64 k) -> u64 { return shift >= 64 ? 0 : (k - mn) >> shift; };
-  bool whole = need == 0 || mn == mx;                  // no digit is left to look at
-  if (mn == mx) shift = 0;
+  u64 low = mn, high = ~0ull;
+  bool whole = need == 0;                              // all keys of the range are taken (or none, as no place is left)
+  if (mn == mx) {
+    shift = 0;
+    high = mn;
+  }
   for (int pass = 0; shift > 0 && !whole; ++pass) {
     const bool first = pass == 0;
-    const int bits = first ? 8 : min(8, shift), next = shift - bits, bins = 1 << bits;
-    if (tid < kBins) sh.hist[tid] = 0;
+    const int bits = first ? 8 : min(8, shift), next = shift - bits;
+    // Counts, 16 a bin: lanes of a warp that share a bin mostly count in words of
+    // their own.  They lie in the table that this pass's counts do not go
+    // to: the last pass's, which has been read, and which a peer writes only when all have finished this pass.
+    int* count = &sh.table[(pass + 1) & 1][0][0];
+    reinterpret_cast<int4*>(count)[tid] = make_int4(0, 0, 0, 0);
     __syncthreads();
+#pragma unroll 2
     for (int j0 = c0 & ~31; j0 < c1; j0 += 32) {
       const int j = j0 + lane;
-      int bin = -1;
-      if (j >= c0 && j < c1) {
-        const u64 k = key(j) - mn;
-        if (first) {
-          const int e = 63 - __clzll((long long)(k | 3));           // >= 1
-          bin = k < 4 ? int(k) : (e - 1) * 4 + (int(k >> (e - 2)) & 3);
-        } else if ((k >> shift) == prefix) {
-          bin = int(k >> next) & (bins - 1);
-        }
+      if (j < c0 || j >= c1) continue;
+      const u64 k = key(j);
+      int bin;
+      if (first) {
+        const u64 x = k - mn;
+        const int e = 63 - __clzll((long long)(x | 3));             // >= 1
+        bin = x < 4 ? int(x) : (e - 1) * 4 + (int(x >> (e - 2)) & 3);
+      } else {
+        if (k < low || k > high) continue;
+        bin = int((k - low) >> next);
       }
-      // the bin of the first lane that has one is added up for the warp
-      const unsigned has = __ballot_sync(0xffffffffu, bin >= 0);
-      if (has == 0) continue;
-      const int lead = __shfl_sync(0xffffffffu, bin, __ffs(has) - 1);
-      const unsigned same = __ballot_sync(0xffffffffu, bin == lead);
-      if (lane == __ffs(has) - 1) atomicAdd(&sh.hist[lead], __popc(same));
-      else if (bin >= 0 && bin != lead) atomicAdd(&sh.hist[bin], 1);
+      atomicAdd(count + bin * 16 + (lane & 15), 1);
     }
     __syncthreads();
     int(*table)[kBins] = sh.table[pass & 1];
-    for (int i = tid; i < ncta * bins; i += kSelThreads) {
-      const int r = i >> bits, b = i & (bins - 1);
-      dsmem_st_u32(dsmem_addr(&table[rank][b], r), uint32_t(sh.hist[b]));
-    }
+    const int4 c4 = reinterpret_cast<const int4*>(count)[tid];      // four threads a bin
+    int own4 = c4.x + c4.y + c4.z + c4.w;
+    own4 += __shfl_xor_sync(0xffffffffu, own4, 1);
+    own4 += __shfl_xor_sync(0xffffffffu, own4, 2);
+    if ((tid & 3) == 0) sh.hist[tid >> 2] = own4;
+    __syncthreads();
+    for (int i = tid; i < ncta * kBins; i += kSelThreads)           // (a warp's words go to one peer, side by side)
+      dsmem_st_u32(dsmem_addr(&table[rank][i & (kBins - 1)], i / kBins), uint32_t(sh.hist[i & (kBins - 1)]));
     cluster_sync_all();
-    // the bin of the need-th greatest: lane l of warp 0 owns bins 8 l .. 8 l + 7, counted from the top
-    if (tid < bins) {
-      int s = 0;
-      for (int r = 0; r < ncta; ++r) s += table[r][tid];
-      sh.hist[tid] = s;
+    if (tid < kBins) {
+      int all = 0;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r)
+        if (r < ncta) all += table[r][tid];
+      sh.hist[tid] = all;
     }
     __syncthreads();
+    // the bin of the need-th greatest: lane l of warp 0 owns bins 8 l .. 8 l + 7, counted from the top
     if (warp == 0) {
       int own = 0, v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int b = bins - 1 - (lane * 8 + i);
-        v[i] = b >= 0 ? sh.hist[b] : 0;
+        v[i] = sh.hist[kBins - 1 - (lane * 8 + i)];
         own += v[i];
       }
       int incl = own;
@@ -194,7 +202,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if (above < need && need <= above + v[i]) {
-          sh.bin = bins - 1 - (lane * 8 + i);
+          sh.bin = kBins - 1 - (lane * 8 + i);
           sh.above = above;
           sh.total = v[i];
         }
@@ -203,22 +211,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     }
     __syncthreads();
     need -= sh.above;
-    whole = need == sh.total;                          // all of the bin's keys are taken
+    whole = need == sh.total;
+    const int bin = sh.bin;
     if (!first) {
-      prefix = (prefix << bits) | u64(sh.bin);
+      low += u64(bin) << next;
       shift = next;
-    } else if (sh.bin < 4) {                           // one value a bin
-      prefix = u64(sh.bin);
+    } else if (bin < 4) {                              // one value a bin
+      low = mn + u64(bin);
       shift = 0;
-    } else {
-      prefix = u64(4 + (sh.bin & 3));
-      shift = sh.bin / 4 - 1;                          // the octave e = bin / 4 + 1, less the two bits
+    } else {                                           // the octave e = bin / 4 + 1, less the two bits
+      shift = bin / 4 - 1;
+      low = mn + (u64(4 + (bin & 3)) << shift);
     }
+    high = low + ((1ull << shift) - 1);
+    if (high < low) high = ~0ull;
   }
-  // A key is taken if its bits from `shift` up are above the prefix, or equal
-  // to it while places are left: `need` of them, the lowest indices.
+  // A key is taken if it is above the range, or in it while places are left:
+  // `need` of them, the lowest indices.
   int gt = 0, eq = 0;
   unsigned gt_mask = 0, eq_mask = 0;                   // lane i: the warp's i-th group of 32 entries (kCached: at most 32 groups)
+#pragma unroll 4
   for (int j0 = w0, it = 0; j0 < w1; j0 += 32, ++it) {
     const int j = j0 + lane;
     bool g = false, e = false;
@@ -226,9 +238,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       if (j < lo || j >= hi) {
         g = true;
       } else {
-        const u64 t = top(key(j));
-        g = t > prefix;
-        e = t == prefix;
+        const u64 k = key(j);
+        g = k > high;
+        e = k >= low && !g;
       }
     }
     const unsigned mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
@@ -236,8 +248,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       gt_mask = mg;
       eq_mask = me;
     }
-    gt += __popc(mg);
-    eq += __popc(me);
+    if (!kCached) {
+      gt += __popc(mg);
+      eq += __popc(me);
+    }
+  }
+  if (kCached) {
+    gt = __reduce_add_sync(0xffffffffu, __popc(gt_mask));
+    eq = __reduce_add_sync(0xffffffffu, __popc(eq_mask));
   }
   if (lane == 0) {
     sh.warp_a[warp] = gt;
@@ -264,24 +282,43 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     eq_before += sh.taken[r][1];
   }
   const unsigned below = (1u << lane) - 1u;
-  for (int j0 = w0, it = 0; j0 < w1; j0 += 32, ++it) {
-    const int j = j0 + lane;
-    unsigned mg, me;
-    if (kCached) {
-      mg = __shfl_sync(0xffffffffu, gt_mask, it);
-      me = __shfl_sync(0xffffffffu, eq_mask, it);
-    } else {
-      const bool in = j < w1, free = in && j >= lo && j < hi;
-      const u64 t = free ? top(key(j)) : 0;
-      mg = __ballot_sync(0xffffffffu, in && (!free || t > prefix));
-      me = __ballot_sync(0xffffffffu, free && t == prefix);
+  if (kCached) {
+    // lane i: the entries of group i that are taken, and the place of the first
+    const int pe = __popc(eq_mask);
+    int upto = pe;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += u;
     }
-    const bool g = (mg >> lane) & 1u, e = (me >> lane) & 1u;
-    const int eq_at = eq_before + __popc(me & below);
-    const int at = gt_before + __popc(mg & below) + min(eq_at, need);
-    if ((g || (e && eq_at < need)) && at < a.keep) kept[at] = j;
-    gt_before += __popc(mg);
-    eq_before += __popc(me);
+    const int left = max(0, min(pe, need - (eq_before + upto - pe)));
+    for (int k = pe; k > left; --k) eq_mask &= ~(1u << (31 - __clz(eq_mask)));   // (some of a group: once in a cluster)
+    const unsigned taken = gt_mask | eq_mask;
+    const int pt = __popc(taken);
+    int start = pt;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, start, o);
+      if (lane >= o) start += u;
+    }
+    start += gt_before + min(eq_before, need) - pt;
+#pragma unroll 4
+    for (int j0 = w0, it = 0; j0 < w1; j0 += 32, ++it) {
+      const unsigned t = __shfl_sync(0xffffffffu, taken, it);
+      const int at = __shfl_sync(0xffffffffu, start, it) + __popc(t & below);
+      if (((t >> lane) & 1u) && at < a.keep) kept[at] = j0 + lane;
+    }
+  } else {
+    for (int j0 = w0; j0 < w1; j0 += 32) {
+      const int j = j0 + lane;
+      const bool in = j < w1, free = in && j >= lo && j < hi;
+      const u64 k = free ? key(j) : 0;
+      const bool g = in && (!free || k > high), e = free && k >= low && k <= high;
+      const unsigned mg = __ballot_sync(0xffffffffu, g), me = __ballot_sync(0xffffffffu, e);
+      const int eq_at = eq_before + __popc(me & below);
+      const int at = gt_before + __popc(mg & below) + min(eq_at, need);
+      if ((g || (e && eq_at < need)) && at < a.keep) kept[at] = j;
+      gt_before += __popc(mg);
+      eq_before += __popc(me);
+    }
   }
   if (rank == 0 && tid == 0 && !a.in_place) a.n_valid_out[seq] = n_out;
 }
