@@ -136,6 +136,20 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a,
     }
   }
 
+  // --- main index of every slot of this warp's quads 4 * warp + 16i: lane l holds
+  // quad i = l / 4 (slot l % 4) in e0 and quad i = 8 + l / 4 in e1 (l < 8); -1: no main row
+  auto main_index = [&](int ls) -> int {
+    const int lm = ls - sp;
+    if (ls >= kSlots || lm < 0 || lm >= mp || int(crank) * mp + lm >= a.topk) return -1;
+    return a.idx[(long long)b * a.topk + int(crank) * mp + lm];
+  };
+  int e0, e1;
+  auto load_indices = [&]() {
+    e0 = main_index(4 * warp + 16 * (lane >> 2) + (lane & 3));
+    e1 = lane < 8 ? main_index(4 * warp + 16 * (8 + (lane >> 2)) + (lane & 3)) : -1;
+  };
+  if (kTree) load_indices();   // beside the loads that the window waits for
+
   // --- group 0: this CTA's SWA rows (inputs of this launch), before waiting on the preceding one.
   // Local slots are handled in quads [4m, 4m + 4), quad m by warp m mod 4.
   const int ns = kTree ? 0 : clamp_count(a.n_swa[b], a.swa, a.err);
@@ -169,18 +183,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a,
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
 
-  if (!kTree) pdl_wait();   // the indices come from the preceding launch
-
-  // --- main index of every slot of this warp's quads 4 * warp + 16i: lane l holds
-  // quad i = l / 4 (slot l % 4) in e0 and quad i = 8 + l / 4 in e1 (l < 8); -1: no main row
-  auto main_index = [&](int ls) -> int {
-    const int lm = ls - sp;
-    if (ls >= kSlots || lm < 0 || lm >= mp || int(crank) * mp + lm >= a.topk) return -1;
-    if (kTree && !win.live) return -1;
-    return a.idx[(long long)b * a.topk + int(crank) * mp + lm];
-  };
-  const int e0 = main_index(4 * warp + 16 * (lane >> 2) + (lane & 3));
-  const int e1 = lane < 8 ? main_index(4 * warp + 16 * (8 + (lane >> 2)) + (lane & 3)) : -1;
+  if (kTree) {
+    if (!win.live) e0 = e1 = -1;
+  } else {
+    pdl_wait();   // the indices come from the preceding launch
+    load_indices();
+  }
 
   // --- groups 1 and 2: the remaining quads (main rows, the last partial SWA quad, unused slots),
   // below / from local slot 80.  Lane j < 4 of a quad resolves slot q0 + j.
