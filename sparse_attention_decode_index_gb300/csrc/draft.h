@@ -11,7 +11,7 @@ constexpr int kErrBadWeight = 16;   // error word: an attention weight outside [
 // Keys of once_per_device, behind SetupKey's.
 enum DraftSetupKey { kSetupTree = 16, kSetupTreePair, kSetupWeightsTc, kSetupEvict, kSetupEvictMove,
                      kSetupTreeRows,        // and the next: warps
-                     kSetupTreeGeneric = kSetupTreeRows + 2 };   // and the next three: element types, warps
+                     kSetupTreeGeneric = kSetupTreeRows + 2 };   // and the next five: element types and widths, warps
 
 // Rotary positions (rope.cu).
 constexpr int kMaxRopeSlots = 16;

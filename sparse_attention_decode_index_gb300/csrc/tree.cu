@@ -3,22 +3,24 @@
 //
 // tree_generic_kernel -- any head count, dims and element type (bf16 rows of
 //   whole 8-byte pieces go to tree_mma.cu).  One CTA per
-//   (query, up to 8 heads).  A warp scores four key slots at a time against the
-//   CTA's heads, its lanes striding the dims, so that four rows are on their
-//   way at once and a row is read once per 8 heads; the 32 sums meet in a
-//   transposed reduction that leaves one on every lane.  The softmax (fp32)
+//   (query, up to 8 heads).  A warp scores 16 key slots at a time: a quarter of
+//   it takes four, its 8 lanes stride the dims, so that a row is read once per 8
+//   heads and 16 rows are on their way; the 32 sums meet in a transposed
+//   reduction that leaves four on every lane.  (All 32 lanes on one four of
+//   slots spent as long on the reduction as on 64 dims.)  The softmax (fp32)
 //   has all slots of its heads in shared memory.  For P V the slots go round
-//   the warps, the lanes have four dims each and 8 rows on their way; the
-//   warps' sums are added up in their order.  Bound by the rows' latency for
-//   few queries (10 queries, 4 heads of 128, 640 slots, fp32: 24 us), by the
-//   fp32 products for many (128 queries, 40 heads of 100 / 128, 549 slots: 80 us,
-//   16 TFLOP/s).
+//   the warps, and in a warp round as many groups of lanes as rows of four dims a lane
+//   leave; 8 rows of each are on their way, and the sums are added up in a
+//   fixed order.  Bound by the rows' latency for few queries (20 queries, 4 heads
+//   of 128, 640 slots, fp32: 18.5 us), by the fp32 products' instructions for many (128
+//   queries, 40 heads of 100 / 128, 549 slots: 69 us, 19 TFLOP/s).
 // weights_mma_kernel -- bf16, 64 heads of 192, few queries: one CTA per (query, 64
 //   slots) gathers the K rows with 16-byte cp.async; S = Q K^T on mma.sync, and
 //   exp2(s - lse) is summed over the heads in fixed order.  No maximum is
 //   needed, the lse is the normaliser.  A latency chain (index, rows, product,
 //   sum): 3.5 us a launch for up to 16 queries of 512 slots.
-// weights_generic_kernel -- any shape: four slots a warp, as above, 8 heads at a time.
+// weights_generic_kernel -- any shape: 16 slots a warp, as above, 8 heads at a time (128 queries of 256
+//   slots, 16 heads of 100, fp32: 9.7 us).
 #include "common.cuh"
 #include "draft.h"
 #include "tc.cuh"
@@ -33,59 +35,85 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ------------------------------------------------------------------ generic tree attention
 
 constexpr int kGenHeads = 8;
-constexpr int kDimBatch = 2;         // elements of each row a lane has on their way
 constexpr int kMaxSlots = 1024;     // topk + swa
 constexpr int kPvDims = 128;        // dims of a P V pass: four a lane
 constexpr int kPvRows = 8;          // V rows a warp has on their way
 
-// Scores of four keys against 8 heads (queries in shared memory, fp32), by a
-// warp: lane 8 x + h ends with q_h . k_x.  A null row scores 0.
-template <int kDtype>
-CSA2_DEV float score_four(const void* const (&row)[4], const float* sq, int dim) {
-  const int lane = threadIdx.x & 31;
+// Scores of 16 keys against 8 heads (queries in shared memory, fp32), by a
+// warp: a quarter of it takes four keys, `row` (null: 0), its 8 lanes the dims,
+// four neighbours at a time where rows are whole 16-byte pieces (kWide, fp32).
+// Lane l ends with key l / 2 and heads 4 (l % 2) .. + 3.
+template <int kDtype, bool kWide>
+CSA2_DEV float4 score_keys(const void* const (&row)[4], const float* sq, int dim) {
+  constexpr int kBatch = kWide ? 2 : 4;   // pieces of each row a lane has on their way
+  const int part = threadIdx.x & 7;
   float acc[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) acc[i] = 0.f;
-  for (int d0 = lane; d0 < dim; d0 += 32 * kDimBatch) {
-    float k[kDimBatch][4];
+  if constexpr (kWide) {
+    for (int d0 = 4 * part; d0 < dim; d0 += 32 * kBatch) {
+      float4 k[kBatch][4];
 #pragma unroll
-    for (int y = 0; y < kDimBatch; ++y)
+      for (int y = 0; y < kBatch; ++y)
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
-        k[y][x] = row[x] != nullptr && d0 + 32 * y < dim ? load_elem(row[x], d0 + 32 * y, kDtype) : 0.f;
+        for (int x = 0; x < 4; ++x)
+          k[y][x] = row[x] != nullptr && d0 + 32 * y < dim
+                        ? *reinterpret_cast<const float4*>(static_cast<const float*>(row[x]) + d0 + 32 * y)
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int y = 0; y < kDimBatch; ++y) {
-      const int d = d0 + 32 * y;
-      if (d >= dim) break;
+      for (int y = 0; y < kBatch; ++y) {
+        if (d0 + 32 * y >= dim) break;
 #pragma unroll
-      for (int h = 0; h < kGenHeads; ++h) {
-        const float q = sq[h * dim + d];
+        for (int h = 0; h < kGenHeads; ++h) {
+          const float4 q = *reinterpret_cast<const float4*>(sq + h * dim + d0 + 32 * y);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[8 * x + h] = __fmaf_rn(q, k[y][x], acc[8 * x + h]);
+          for (int x = 0; x < 4; ++x) {
+            float& c = acc[8 * x + h];
+            c = __fmaf_rn(q.x, k[y][x].x, c);
+            c = __fmaf_rn(q.y, k[y][x].y, c);
+            c = __fmaf_rn(q.z, k[y][x].z, c);
+            c = __fmaf_rn(q.w, k[y][x].w, c);
+          }
+        }
+      }
+    }
+  } else {
+    for (int d0 = part; d0 < dim; d0 += 8 * kBatch) {
+      float k[kBatch][4];
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          k[y][x] = row[x] != nullptr && d0 + 8 * y < dim ? load_elem(row[x], d0 + 8 * y, kDtype) : 0.f;
+#pragma unroll
+      for (int y = 0; y < kBatch; ++y) {
+        if (d0 + 8 * y >= dim) break;
+#pragma unroll
+        for (int h = 0; h < kGenHeads; ++h) {
+          const float q = sq[h * dim + d0 + 8 * y];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[8 * x + h] = __fmaf_rn(q, k[y][x], acc[8 * x + h]);
+        }
       }
     }
   }
+  __syncwarp();
   // each step halves the values a lane holds and doubles the lanes they are summed over
 #pragma unroll
-  for (int n = 16; n >= 1; n >>= 1)
+  for (int n = 16; n >= 4; n >>= 1)
 #pragma unroll
     for (int i = 0; i < n; ++i) {
-      const bool up = (lane & n) != 0;
+      const bool up = (part & (n >> 2)) != 0;
       const float keep = up ? acc[i + n] : acc[i], give = up ? acc[i] : acc[i + n];
-      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, n);
+      acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, n >> 2);
     }
-  return acc[0];
+  return make_float4(acc[0], acc[1], acc[2], acc[3]);
 }
 
-// Four elements from `i` on (wide: one access; otherwise those below `end`).
-template <int kDtype>
-CSA2_DEV float4 load_four(const void* base, int i, int end, bool wide) {
-  if (wide) {
-    if (kDtype == 1) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-    const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(base) + i);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                       __uint_as_float(v.y & 0xffff0000u));
-  }
+// Four elements from `i` on (kWide: one access; otherwise those below `end`).
+template <int kDtype, bool kWide>
+CSA2_DEV float4 load_four(const void* base, int i, int end) {
+  if (kWide) return *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
   float4 r;
   r.x = load_elem(base, i, kDtype);
   r.y = i + 1 < end ? load_elem(base, i + 1, kDtype) : 0.f;
@@ -94,15 +122,15 @@ CSA2_DEV float4 load_four(const void* base, int i, int end, bool wide) {
   return r;
 }
 
-template <int kDtype, int kThreads>
-__global__ void __launch_bounds__(kThreads) tree_generic_kernel(const TreeArgs a, int wide) {
+template <int kDtype, bool kWide, int kThreads>
+__global__ void __launch_bounds__(kThreads, 512 / kThreads) tree_generic_kernel(const TreeArgs a) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) float sh[];
   __shared__ int path[kMaxTreeTokens];
   __shared__ float red[kWarps * kGenHeads], inv_s[kGenHeads];
   const int b = blockIdx.y, h0 = blockIdx.x * kGenHeads, nh = min(kGenHeads, a.heads - h0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int nslots = a.topk + a.swa, rounded = (nslots + 3) & ~3;
+  const int nslots = a.topk + a.swa, rounded = (nslots + 15) & ~15;
   const void** krow = reinterpret_cast<const void**>(sh);   // [rounded] rows of the slots (null: no key)
   const void** vrow = krow + rounded;
   float* sp = reinterpret_cast<float*>(vrow + rounded);     // [rounded][kGenHeads] logits -> weights
@@ -137,10 +165,16 @@ __global__ void __launch_bounds__(kThreads) tree_generic_kernel(const TreeArgs a
     vrow[j] = vb != nullptr ? static_cast<const uint8_t*>(vb) + row * a.v_dim * esize : nullptr;
   }
   __syncthreads();
-  for (int j = 4 * warp; j < rounded; j += 4 * kWarps) {
-    const void* const row[4] = {krow[j], krow[j + 1], krow[j + 2], krow[j + 3]};
-    const float s = score_four<kDtype>(row, sq, a.k_dim);
-    sp[j * kGenHeads + lane] = krow[j + (lane >> 3)] != nullptr ? s * a.scale : -INFINITY;
+  for (int j = 16 * warp; j < rounded; j += 16 * kWarps) {
+    const int own = j + 4 * (lane >> 3);
+    const void* const row[4] = {krow[own], krow[own + 1], krow[own + 2], krow[own + 3]};
+    float4 s = score_keys<kDtype, kWide>(row, sq, a.k_dim);
+    const bool key = krow[j + (lane >> 1)] != nullptr;
+    s.x = key ? s.x * a.scale : -INFINITY;
+    s.y = key ? s.y * a.scale : -INFINITY;
+    s.z = key ? s.z * a.scale : -INFINITY;
+    s.w = key ? s.w * a.scale : -INFINITY;
+    *reinterpret_cast<float4*>(sp + j * kGenHeads + 4 * lane) = s;
   }
   __syncthreads();
   // softmax statistics: head tid % 8, every (threads / 8)th slot
@@ -172,21 +206,24 @@ __global__ void __launch_bounds__(kThreads) tree_generic_kernel(const TreeArgs a
   }
   __syncthreads();
   for (int d0 = 0; d0 < a.v_dim; d0 += kPvDims) {
-    const int d = d0 + 4 * lane;
+    // the lanes of a row, as few as have four dims each; the others take other rows
+    int lanes = 32;
+    while (lanes > 4 && 2 * lanes >= a.v_dim - d0) lanes >>= 1;
+    const int d = d0 + 4 * (lane & (lanes - 1)), step = kWarps * (32 / lanes);
     float4 acc[kGenHeads];
 #pragma unroll
     for (int i = 0; i < kGenHeads; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = warp; j0 < nslots; j0 += kPvRows * kWarps) {
+    for (int j0 = warp + kWarps * (lane / lanes); j0 < nslots; j0 += kPvRows * step) {
       float4 v[kPvRows];
 #pragma unroll
       for (int x = 0; x < kPvRows; ++x) {
-        const int j = j0 + x * kWarps;
+        const int j = j0 + x * step;
         const void* row = j < nslots ? vrow[j] : nullptr;
-        v[x] = row != nullptr && d < a.v_dim ? load_four<kDtype>(row, d, a.v_dim, wide != 0) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[x] = row != nullptr && d < a.v_dim ? load_four<kDtype, kWide>(row, d, a.v_dim) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int x = 0; x < kPvRows; ++x) {
-        const int j = j0 + x * kWarps;
+        const int j = j0 + x * step;
         if (j >= nslots) break;
         const float4 plo = *reinterpret_cast<const float4*>(sp + j * kGenHeads);
         const float4 phi = *reinterpret_cast<const float4*>(sp + j * kGenHeads + 4);
@@ -201,9 +238,19 @@ __global__ void __launch_bounds__(kThreads) tree_generic_kernel(const TreeArgs a
         }
       }
     }
+    __syncwarp();
+    for (int o = lanes; o < 32; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < kGenHeads; ++i)
-      *reinterpret_cast<float4*>(part + (warp * kGenHeads + i) * kPvDims + 4 * lane) = acc[i];
+      for (int i = 0; i < kGenHeads; ++i) {
+        acc[i].x += __shfl_xor_sync(0xffffffffu, acc[i].x, o);
+        acc[i].y += __shfl_xor_sync(0xffffffffu, acc[i].y, o);
+        acc[i].z += __shfl_xor_sync(0xffffffffu, acc[i].z, o);
+        acc[i].w += __shfl_xor_sync(0xffffffffu, acc[i].w, o);
+      }
+    if (lane < lanes)
+#pragma unroll
+      for (int i = 0; i < kGenHeads; ++i)
+        *reinterpret_cast<float4*>(part + (warp * kGenHeads + i) * kPvDims + 4 * lane) = acc[i];
     __syncthreads();
     for (int i = tid; i < nh * kPvDims; i += kThreads) {
       const int head = i / kPvDims, x = i % kPvDims;
@@ -217,25 +264,39 @@ __global__ void __launch_bounds__(kThreads) tree_generic_kernel(const TreeArgs a
 }
 
 constexpr size_t generic_smem(int slots, int k_dim, int threads) {
-  const size_t rounded = size_t(slots + 3) / 4 * 4;
+  const size_t rounded = size_t(slots + 15) / 16 * 16;
   const size_t q = size_t(kGenHeads) * k_dim, sums = size_t(threads / 32) * kGenHeads * kPvDims;
   return rounded * 16 + (rounded * kGenHeads + (q > sums ? q : sums)) * sizeof(float);
 }
 
 // One CTA an SM with 16 warps while there are no more CTAs than SMs, two with
-// 8 warps beyond (10 queries, 4 heads: 28 us with 16 warps, 40 with 8; 128
-// queries, 40 heads: 116 and 95.
-template <int kDtype, int kThreads>
-cudaError_t launch_generic(const TreeArgs& a, int batch, int wide, cudaStream_t st) {
-  const cudaError_t e = once_per_device(kSetupTreeGeneric + 2 * kDtype + (kThreads == 512), [] {
-    return cudaFuncSetAttribute(tree_generic_kernel<kDtype, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+// 8 warps beyond (measured on an earlier form, 20 queries of 4 heads: 28 us with 16
+// warps, 40 with 8; 128 queries of 40 heads: 116 and 95).
+template <int kDtype, bool kWide, int kThreads>
+cudaError_t launch_generic(const TreeArgs& a, int batch, cudaStream_t st) {
+  const cudaError_t e = once_per_device(kSetupTreeGeneric + 2 * (kDtype + kWide) + (kThreads == 512), [] {
+    return cudaFuncSetAttribute(tree_generic_kernel<kDtype, kWide, kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 int(generic_smem(kMaxSlots, 1024, kThreads)));
   });
   if (e != cudaSuccess) return e;
   note_launch();
-  return launch_pdl(tree_generic_kernel<kDtype, kThreads>,
+  return launch_pdl(tree_generic_kernel<kDtype, kWide, kThreads>,
                     dim3(unsigned((a.heads + kGenHeads - 1) / kGenHeads), unsigned(batch)), dim3(kThreads),
-                    generic_smem(a.topk + a.swa, a.k_dim, kThreads), st, 1, a, wide);
+                    generic_smem(a.topk + a.swa, a.k_dim, kThreads), st, 1, a);
+}
+
+template <int kDtype, bool kWide>
+cudaError_t launch_generic(const TreeArgs& a, int batch, cudaStream_t st) {
+  const bool few = (long long)batch * ((a.heads + kGenHeads - 1) / kGenHeads) <= device_sm_count();
+  return few ? launch_generic<kDtype, kWide, 512>(a, batch, st) : launch_generic<kDtype, kWide, 256>(a, batch, st);
+}
+
+// fp32 rows of whole 16-byte pieces.
+template <class... P>
+bool wide_rows(int dtype, int dim, P... p) {
+  uintptr_t at = 0;
+  for (const void* x : {static_cast<const void*>(p)...}) at |= reinterpret_cast<uintptr_t>(x);
+  return dtype == 1 && dim % 4 == 0 && at % 16 == 0;
 }
 
 // ------------------------------------------------------------------ attention weights
@@ -325,41 +386,46 @@ __global__ void __launch_bounds__(kWThreads) weights_mma_kernel(const AttnWeight
   }
 }
 
-constexpr int kWGenThreads = 256, kWGenSlots = kWGenThreads / 8;   // four slots a warp
+constexpr int kWGenThreads = 128, kWGenSlots = kWGenThreads / 2;   // 16 slots a warp
 
-template <int kDtype>
+template <int kDtype, bool kWide>
 __global__ void __launch_bounds__(kWGenThreads) weights_generic_kernel(const AttnWeightsArgs a) {
-  extern __shared__ float sq[];                 // [kGenHeads][k_dim]
+  extern __shared__ __align__(16) float sq[];   // [kGenHeads][k_dim]
   const int b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int j0 = blockIdx.x * kWGenSlots + 4 * warp, esize = kDtype == 1 ? 4 : 2;
+  const int j0 = blockIdx.x * kWGenSlots + 16 * warp, esize = kDtype == 1 ? 4 : 2;
   pdl_wait();
   const bool live = a.live == nullptr || a.live[b] != 0;
+  int e = live && lane < 16 && j0 + lane < a.topk ? a.idx[(long long)b * a.topk + j0 + lane] : -1;   // of slot j0 + lane
+  if (e >= a.n_entries) {
+    report(a.err, kErrBadIndex, e);
+    e = -1;
+  }
   const void* row[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) {
-    int e = live && j0 + x < a.topk ? a.idx[(long long)b * a.topk + j0 + x] : -1;
-    if (e >= a.n_entries) {
-      if (lane == 0) report(a.err, kErrBadIndex, e);
-      e = -1;
-    }
-    row[x] = e < 0 ? nullptr
-                   : static_cast<const uint8_t*>(a.k_main) + ((long long)(b / a.seq_div) * a.n_entries + e) * a.k_dim * esize;
+    const int y = __shfl_sync(0xffffffffu, e, 4 * (lane >> 3) + x);
+    row[x] = y < 0 ? nullptr
+                   : static_cast<const uint8_t*>(a.k_main) + ((long long)(b / a.seq_div) * a.n_entries + y) * a.k_dim * esize;
   }
-  const bool key = (lane < 16 ? (lane < 8 ? row[0] : row[1]) : (lane < 24 ? row[2] : row[3])) != nullptr;
-  float w = 0.f;                                // of slot j0 + lane / 8, the heads of lane % 8
+  const bool key = __shfl_sync(0xffffffffu, e, lane >> 1) >= 0;
+  float w = 0.f;                                // of slot j0 + lane / 2, every other four heads
   for (int h0 = 0; live && h0 < a.heads; h0 += kGenHeads) {
-    const int nh = min(kGenHeads, a.heads - h0), h = lane & 7;
+    const int nh = min(kGenHeads, a.heads - h0), h = 4 * (lane & 1);
     __syncthreads();
     for (int i = tid; i < kGenHeads * a.k_dim; i += kWGenThreads)
       sq[i] = i < nh * a.k_dim ? load_elem(a.q, ((long long)b * a.heads + h0) * a.k_dim + i, kDtype) : 0.f;
-    const float l = h < nh ? a.lse[(long long)b * a.heads + h0 + h] : -INFINITY;
-    __syncthreads();
-    const float s = score_four<kDtype>(row, sq, a.k_dim);
-    if (key && l != -INFINITY) w += expf(s * a.scale - l);
-  }
+    float l[4];
 #pragma unroll
-  for (int o = 1; o < 8; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-  if ((lane & 7) == 0 && j0 + (lane >> 3) < a.topk) a.weights[(long long)b * a.topk + j0 + (lane >> 3)] = w;
+    for (int i = 0; i < 4; ++i) l[i] = h + i < nh ? a.lse[(long long)b * a.heads + h0 + h + i] : -INFINITY;
+    __syncthreads();
+    const float4 s4 = score_keys<kDtype, kWide>(row, sq, a.k_dim);
+    const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (key && l[i] != -INFINITY) w += expf(s[i] * a.scale - l[i]);
+  }
+  w += __shfl_xor_sync(0xffffffffu, w, 1);
+  if ((lane & 1) == 0 && j0 + (lane >> 1) < a.topk) a.weights[(long long)b * a.topk + j0 + (lane >> 1)] = w;
 }
 
 // A cluster of CTAs per query while all the clusters run at once (up to 7/8 of
@@ -381,13 +447,9 @@ cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan
                                             : launch_tree_attn_cluster(a, batch, st);
   }
   if (tree_rows_fit(a)) return launch_tree_rows(a, batch, st);
-  // four V elements an access: whole fours at 16-byte addresses
-  uintptr_t at = 0;
-  for (const void* p : {a.v_main, a.v_swa, a.v_draft}) at |= reinterpret_cast<uintptr_t>(p);
-  const int wide = a.v_dim % 4 == 0 && at % 16 == 0;
-  const bool few = (long long)batch * ((a.heads + kGenHeads - 1) / kGenHeads) <= device_sm_count();
-  if (a.dtype == 1) return few ? launch_generic<1, 512>(a, batch, wide, st) : launch_generic<1, 256>(a, batch, wide, st);
-  return few ? launch_generic<0, 512>(a, batch, wide, st) : launch_generic<0, 256>(a, batch, wide, st);
+  if (wide_rows(a.dtype, a.k_dim, a.k_main, a.k_swa, a.k_draft) && wide_rows(a.dtype, a.v_dim, a.v_main, a.v_swa, a.v_draft))
+    return launch_generic<1, true>(a, batch, st);
+  return a.dtype == 1 ? launch_generic<1, false>(a, batch, st) : launch_generic<0, false>(a, batch, st);
 }
 
 cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, cudaStream_t st) {
@@ -403,8 +465,10 @@ cudaError_t launch_attn_weights(const AttnWeightsArgs& a, bool fast, int batch, 
     return launch_pdl(weights_mma_kernel, dim3(unsigned((a.topk + kWSlots - 1) / kWSlots), unsigned(batch)), dim3(kWThreads), 0,
                       st, 1, a);
   const dim3 grid(unsigned((a.topk + kWGenSlots - 1) / kWGenSlots), static_cast<unsigned>(batch));
-  return launch_pdl(a.dtype == 1 ? weights_generic_kernel<1> : weights_generic_kernel<0>, grid, dim3(kWGenThreads),
-                    size_t(kGenHeads) * a.k_dim * sizeof(float), st, 1, a);
+  const auto kernel = wide_rows(a.dtype, a.k_dim, a.k_main) ? weights_generic_kernel<1, true>
+                      : a.dtype == 1                        ? weights_generic_kernel<1, false>
+                                                            : weights_generic_kernel<0, false>;
+  return launch_pdl(kernel, grid, dim3(kWGenThreads), size_t(kGenHeads) * a.k_dim * sizeof(float), st, 1, a);
 }
 
 }  // namespace csa2
