@@ -4,20 +4,22 @@
 //
 // The angle.  pos * freq in fp32 is off by up to 2^-24 of the angle, 0.06 rad
 // at a million positions, and fp64 is slow on this GPU.  A frequency is
-// therefore turned once per block into turns per position as a 64-bit fixed-
-// point fraction F = freq / 2 pi mod 1 in units of 2^-64; pos * F modulo 2^64 is
-// then the exact angle of F in turns, whatever whole turns it passes, and its
-// top bits, read as a signed number, lie in [-1/2, 1/2) turns.  F is rounded
-// from fp64, so the angle is off by at most |t| 2^-52 for any int32 position,
-// and sincospif takes the reduced angle in half turns.
+// therefore turned into turns per position once (a block, where its threads
+// have several angles each): a 64-bit fixed-point fraction F = freq / 2 pi mod
+// 1 in units of 2^-64.  pos * F modulo 2^64 is then the exact angle of F in
+// turns, whatever whole turns it passes, and its top bits, read as a signed
+// number, lie in [-1/2, 1/2) turns.  F is rounded from fp64, so the angle is
+// off by at most |t| 2^-52 for any int32 position, and sincospif takes the
+// reduced angle in half turns.
 //
 // Memory bound: every element is read once and written once.  A block takes
-// up to 8 rows and makes all their cos and sin at once (one angle a thread,
-// kept in shared memory and used by all the heads of all the tensors), so that
-// the chain position -> angle -> sincospif is waited for once per 8 rows; with one
-// row a block its latency, not the memory, set the time (8,192 rows of 64 + 1
-// heads of 192: 239 us; 8 rows a block 69.6 us, 5.9 TB/s, the floor being 60.3).
-// Few rows are split over the heads instead (8 rows: 5.8 us, a launch and that chain).  An item is one 16-byte vector that is copied, or the vectors that
+// up to 8 rows, or 64 small ones, and makes all their cos and sin at once (kept
+// in shared memory and used by all the heads of all the tensors), so that the
+// chain position -> angle -> sincospif is waited for once a block; with one row
+// a block its latency, not the memory, set the time (8,192 rows of 64 + 1 heads
+// of 192: 239 us; 8 rows a block 69.6 us, 5.9 TB/s, the floor being 60.3).  Few
+// rows are split over the heads instead (8 rows: 5.8 us, a launch and that
+// chain).  An item is one 16-byte vector that is copied, or the vectors that
 // hold the two halves of pairs; its head comes from a multiplication by a
 // precomputed reciprocal.
 #include "common.cuh"
@@ -28,7 +30,8 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 8;   // rows a block: the angles' table takes at most 32 KB
+constexpr int kMaxPairs = 512;
+constexpr int kMaxRows = 8, kMaxAngles = kMaxRows * kMaxPairs, kMaxVecs = 4096;   // of a block
 constexpr int kBatch = 4;   // vectors a thread loads before it stores any
 
 CSA2_DEV float to_f32(float v) { return v; }
@@ -201,22 +204,32 @@ CSA2_DEV void turn_scalar(const RopeArgs::Slot& y, int nr, int nh, const T* x, T
 template <bool kInter>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];           // [per_block][rot / 2]
+  __shared__ long long step[kMaxPairs];                  // turns per position, in units of 2^-64
   const long long row0 = (long long)blockIdx.x * a.per_block;
   const int nr = int(min((long long)a.per_block, a.rows - row0));
   pdl_wait();   // no early trigger: the attention may read what this kernel writes before its own wait
   const int half = a.rot / 2;
   const float mag = a.inverse ? 1.f / a.mag : a.mag;
-  for (int i = threadIdx.x; i < nr * half; i += kThreads) {
-    const int r = i / half, p = i - r * half;
-    const long long pos = a.pos[row0 + r];
-    double f = a.freqs[p] * 0.15915494309189533577;      // turns per position
+  auto turns = [&](int p) -> long long {                 // per position, in units of 2^-64
+    double f = a.freqs[p] * 0.15915494309189533577;
     f -= rint(f);                                        // whole turns change nothing
-    const long long F = __double2ll_rn(f * 18446744073709551616.0);   // saturates at half a turn, 2^-64 off
-    const unsigned long long t = (unsigned long long)pos * (unsigned long long)F;
+    return __double2ll_rn(f * 18446744073709551616.0);   // saturates at half a turn, 2^-64 off
+  };
+  // Once a block where a thread has several angles (fp64 is slow); otherwise no
+  // barrier holds back the threads that have none (8 rows: 6.5 us, with the barrier 6.9).
+  auto angle = [&](int i, int r, long long F) {
+    const unsigned long long t = (unsigned long long)(long long)a.pos[row0 + r] * (unsigned long long)F;
     const float turn = float((long long)t) * 5.421010862427522e-20f;  // * 2^-64: in [-1/2, 1/2]
     float s, c;
     sincospif(2.f * turn, &s, &c);
     cs[i] = make_float2(c * mag, (a.inverse ? -s : s) * mag);
+  };
+  if (nr * half > kThreads) {
+    for (int p = threadIdx.x; p < half; p += kThreads) step[p] = turns(p);
+    __syncthreads();
+    for (int i = threadIdx.x; i < nr * half; i += kThreads) angle(i, i / half, step[i % half]);
+  } else if (int(threadIdx.x) < nr * half) {
+    angle(threadIdx.x, threadIdx.x / half, turns(threadIdx.x % half));
   }
   // tensor k's heads of this block (nh == 0: none) and their place
   auto part = [&](int k, int& nh, const uint8_t*& x, uint8_t*& out) -> const RopeArgs::Slot& {
@@ -263,18 +276,23 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
 cudaError_t launch_rope(RopeArgs& a, int rows, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   int heads = 0;   // of the tensor with the most
+  int vecs = 0;    // 16-byte pieces of a row of all tensors
   for (int k = 0; k < a.n_slots; ++k) {
     RopeArgs::Slot& y = a.slot[k];
     const int v = y.dtype == 1 ? 4 : 8;
     const uintptr_t at = reinterpret_cast<uintptr_t>(y.x) | reinterpret_cast<uintptr_t>(y.out);
     y.wide = at % 16 == 0 && y.dim % v == 0 && y.off % v == 0 && a.rot % v == 0 && (a.interleaved || a.rot / 2 % v == 0);
     heads = heads > y.heads ? heads : y.heads;
+    vecs += (y.heads * y.dim + v - 1) / v;
   }
-  // Four blocks for every SM: as many rows a block as that leaves, up to 8;
+  // Four blocks for every SM: as many rows a block as that leaves, up to 8, of
+  // small rows up to 64 (16,384 rows of one head of 192, 32 pairs: 22.0 us with 8, 12.2 with 26);
   // when one row each does not give that many blocks, the heads are split.
   const int want = 4 * device_sm_count();
   a.rows = rows;
-  a.per_block = rows / want < 1 ? 1 : rows / want > kMaxRows ? kMaxRows : rows / want;
+  int most = 64;
+  while (most > kMaxRows && (most * (a.rot / 2) > kMaxAngles || most * vecs > kMaxVecs)) --most;
+  a.per_block = rows / want < 1 ? 1 : rows / want > most ? most : rows / want;
   for (int k = 0; k < a.n_slots; ++k)   // keeps fast_div's products below 2^32
     while (a.per_block > 1 && a.per_block * a.slot[k].heads * a.slot[k].dim > (1 << 21)) --a.per_block;
   const int blocks = (rows + a.per_block - 1) / a.per_block;
