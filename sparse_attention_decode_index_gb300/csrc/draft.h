@@ -21,7 +21,7 @@ struct RopeArgs {
     const void* x;           // [rows, heads, dim]
     void* out;               // [rows, heads, dim]; == x: in place
     int heads, dim, off, dtype;
-    int wide;                // whole 16-byte vectors at 16-byte addresses (set by the launcher)
+    int wide;                // whole vectors at aligned addresses (set by the launcher)
   } slot[kMaxRopeSlots];
   int n_slots;
   int rows, per_block;       // rows, rows per block (set by the launcher)

@@ -19,8 +19,9 @@
 // a block its latency, not the memory, set the time (8,192 rows of 64 + 1 heads
 // of 192: 239 us; 8 rows a block 69.6 us, 5.9 TB/s, the floor being 60.3).  Few
 // rows are split over the heads instead (8 rows: 5.8 us, a launch and that
-// chain).  An item is one 16-byte vector that is copied, or the vectors that
-// hold the two halves of pairs; its head comes from a multiplication by a
+// chain).  An item is one vector that is copied, or the vectors that hold the
+// two halves of pairs: 16 bytes, or 8 where the sizes allow no more (7,716 rows of 48
+// heads of 40, 4 pairs: 16.1 us, element by element 71.3); its head comes from a multiplication by a
 // precomputed reciprocal.
 #include "common.cuh"
 #include "draft.h"
@@ -70,12 +71,38 @@ CSA2_DEV void turn_words(uint32_t& a, uint32_t& b, float4 cs) {
   b = pack_bf16(b0 * cs.x + a0 * cs.y, b1 * cs.z + a1 * cs.w);
 }
 
+// The same of two fp32 words.
+CSA2_DEV void turn_word(uint32_t& a, uint32_t& b, float c, float s) {
+  const float f = __uint_as_float(a), g = __uint_as_float(b);
+  a = __float_as_uint(f * c - g * s);
+  b = __float_as_uint(g * c + f * s);
+}
+
+// A vector of 16 or 8 bytes, as words.
+template <int kBytes>
+struct Vec {
+  uint32_t w[kBytes / 4];
+  CSA2_DEV void load(const uint8_t* p) {
+    if constexpr (kBytes == 16) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    }
+  }
+  CSA2_DEV void store(uint8_t* p) const {
+    if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+};
+
 // The turned vectors of the half layout: vector i and its partner rot / 2 further.
-template <bool kBf16>
+template <bool kBf16, int kBytes>
 CSA2_DEV void turn_half(const Heads& n, const uint8_t* x, uint8_t* out, int off, int half, const float2* cs) {
-  constexpr int kE = kBf16 ? 2 : 4, kV = 16 / kE, kB = kBatch / 2;
+  constexpr int kE = kBf16 ? 2 : 4, kV = kBytes / kE, kB = kBatch / 2;
   for (int i0 = threadIdx.x; i0 < n.total; i0 += kB * kThreads) {
-    uint4 a[kB], b[kB];
+    Vec<kBytes> a[kB], b[kB];
     int at[kB], p[kB];
 #pragma unroll
     for (int m = 0; m < kB; ++m) {
@@ -85,8 +112,8 @@ CSA2_DEV void turn_half(const Heads& n, const uint8_t* x, uint8_t* out, int off,
       at[m] = (at[m] + off + it * kV) * kE;
       p[m] = row * half + it * kV;
       if (i < n.total) {
-        a[m] = *reinterpret_cast<const uint4*>(x + at[m]);
-        b[m] = *reinterpret_cast<const uint4*>(x + at[m] + half * kE);
+        a[m].load(x + at[m]);
+        b[m].load(x + at[m] + half * kE);
       }
     }
 #pragma unroll
@@ -94,34 +121,28 @@ CSA2_DEV void turn_half(const Heads& n, const uint8_t* x, uint8_t* out, int off,
       if (i0 + m * kThreads >= n.total) break;
       const float4* c = reinterpret_cast<const float4*>(cs + p[m]);   // p and half are even here
       if (kBf16) {
-        turn_words(a[m].x, b[m].x, c[0]);
-        turn_words(a[m].y, b[m].y, c[1]);
-        turn_words(a[m].z, b[m].z, c[2]);
-        turn_words(a[m].w, b[m].w, c[3]);
+#pragma unroll
+        for (int e = 0; e < kBytes / 4; ++e) turn_words(a[m].w[e], b[m].w[e], c[e]);
       } else {
-        auto turn = [](uint32_t& u, uint32_t& v, float cc, float ss) {
-          const float f = __uint_as_float(u), g = __uint_as_float(v);
-          u = __float_as_uint(f * cc - g * ss);
-          v = __float_as_uint(g * cc + f * ss);
-        };
-        const float4 c0 = c[0], c1 = c[1];
-        turn(a[m].x, b[m].x, c0.x, c0.y);
-        turn(a[m].y, b[m].y, c0.z, c0.w);
-        turn(a[m].z, b[m].z, c1.x, c1.y);
-        turn(a[m].w, b[m].w, c1.z, c1.w);
+#pragma unroll
+        for (int e = 0; e < kBytes / 8; ++e) {
+          const float4 c2 = c[e];
+          turn_word(a[m].w[2 * e], b[m].w[2 * e], c2.x, c2.y);
+          turn_word(a[m].w[2 * e + 1], b[m].w[2 * e + 1], c2.z, c2.w);
+        }
       }
-      *reinterpret_cast<uint4*>(out + at[m]) = a[m];
-      *reinterpret_cast<uint4*>(out + at[m] + half * kE) = b[m];
+      a[m].store(out + at[m]);
+      b[m].store(out + at[m] + half * kE);
     }
   }
 }
 
 // The turned vectors of the interleaved layout: pairs of neighbours.
-template <bool kBf16>
+template <bool kBf16, int kBytes>
 CSA2_DEV void turn_inter(const Heads& n, const uint8_t* x, uint8_t* out, int off, int half, const float2* cs) {
-  constexpr int kE = kBf16 ? 2 : 4, kV = 16 / kE;
+  constexpr int kE = kBf16 ? 2 : 4, kV = kBytes / kE;
   for (int i0 = threadIdx.x; i0 < n.total; i0 += kBatch * kThreads) {
-    uint4 a[kBatch];
+    Vec<kBytes> a[kBatch];
     int at[kBatch], p[kBatch];
 #pragma unroll
     for (int m = 0; m < kBatch; ++m) {
@@ -130,50 +151,55 @@ CSA2_DEV void turn_inter(const Heads& n, const uint8_t* x, uint8_t* out, int off
       at[m] = i < n.total ? n.at(i, it, row) : 0;
       at[m] = (at[m] + off + it * kV) * kE;
       p[m] = row * half + it * (kV / 2);
-      if (i < n.total) a[m] = *reinterpret_cast<const uint4*>(x + at[m]);
+      if (i < n.total) a[m].load(x + at[m]);
     }
 #pragma unroll
     for (int m = 0; m < kBatch; ++m) {
       if (i0 + m * kThreads >= n.total) break;
-      const float4* c = reinterpret_cast<const float4*>(cs + p[m]);
-      auto turn = [](float f, float g, float cc, float ss) { return make_float2(f * cc - g * ss, g * cc + f * ss); };
-      if (kBf16) {
-        auto word = [&](uint32_t& w, float cc, float ss) {
-          const float2 r = turn(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u), cc, ss);
-          w = pack_bf16(r.x, r.y);
-        };
-        const float4 c0 = c[0], c1 = c[1];
-        word(a[m].x, c0.x, c0.y);
-        word(a[m].y, c0.z, c0.w);
-        word(a[m].z, c1.x, c1.y);
-        word(a[m].w, c1.z, c1.w);
+      const float2* c = cs + p[m];
+      float2 r[kV / 2];
+      if constexpr (kV >= 4) {                         // whole float4s: p is even here
+#pragma unroll
+        for (int e = 0; e < kV / 4; ++e) {
+          const float4 c2 = reinterpret_cast<const float4*>(c)[e];
+          r[2 * e] = make_float2(c2.x, c2.y);
+          r[2 * e + 1] = make_float2(c2.z, c2.w);
+        }
       } else {
-        const float4 c0 = c[0];
-        const float2 r = turn(__uint_as_float(a[m].x), __uint_as_float(a[m].y), c0.x, c0.y);
-        const float2 q = turn(__uint_as_float(a[m].z), __uint_as_float(a[m].w), c0.z, c0.w);
-        a[m] = make_uint4(__float_as_uint(r.x), __float_as_uint(r.y), __float_as_uint(q.x), __float_as_uint(q.y));
+        r[0] = c[0];
       }
-      *reinterpret_cast<uint4*>(out + at[m]) = a[m];
+#pragma unroll
+      for (int e = 0; e < kV / 2; ++e) {
+        if (kBf16) {
+          uint32_t& w = a[m].w[e];
+          const float f = __uint_as_float(w << 16), g = __uint_as_float(w & 0xffff0000u);
+          w = pack_bf16(f * r[e].x - g * r[e].y, g * r[e].x + f * r[e].y);
+        } else {
+          turn_word(a[m].w[2 * e], a[m].w[2 * e + 1], r[e].x, r[e].y);
+        }
+      }
+      a[m].store(out + at[m]);
     }
   }
 }
 
 // The vectors that are not turned: `before` of them in front of the turned range, the others behind it.
+template <int kBytes>
 CSA2_DEV void copy_rest(const Heads& n, const uint8_t* x, uint8_t* out, int before, int rot_vecs, int esize) {
   for (int i0 = threadIdx.x; i0 < n.total; i0 += kBatch * kThreads) {
-    uint4 a[kBatch];
+    Vec<kBytes> a[kBatch];
     int at[kBatch];
 #pragma unroll
     for (int m = 0; m < kBatch; ++m) {
       const int i = i0 + m * kThreads;
       int it = 0, row = 0;
       at[m] = i < n.total ? n.at(i, it, row) * esize : 0;
-      at[m] += (it < before ? it : it + rot_vecs) * 16;
-      if (i < n.total) a[m] = *reinterpret_cast<const uint4*>(x + at[m]);
+      at[m] += (it < before ? it : it + rot_vecs) * kBytes;
+      if (i < n.total) a[m].load(x + at[m]);
     }
 #pragma unroll
     for (int m = 0; m < kBatch; ++m)
-      if (i0 + m * kThreads < n.total) *reinterpret_cast<uint4*>(out + at[m]) = a[m];
+      if (i0 + m * kThreads < n.total) a[m].store(out + at[m]);
   }
 }
 
@@ -201,7 +227,9 @@ CSA2_DEV void turn_scalar(const RopeArgs::Slot& y, int nr, int nh, const T* x, T
   }
 }
 
-template <bool kInter>
+// kBytes: of the vectors of the tensors that are wide.  (One kernel for both sizes was 1 us slower: more
+// instructions to fetch.)
+template <bool kInter, int kBytes>
 __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];           // [per_block][rot / 2]
   __shared__ long long step[kMaxPairs];                  // turns per position, in units of 2^-64
@@ -246,8 +274,9 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
     const uint8_t* x;
     uint8_t* out;
     const RopeArgs::Slot& y = part(k, nh, x, out);
-    const int esize = y.dtype == 1 ? 4 : 2, v = 16 / esize;
-    if (y.wide && y.x != y.out) copy_rest(Heads(y, nr, nh, (y.dim - a.rot) / v), x, out, y.off / v, a.rot / v, esize);
+    const int esize = y.dtype == 1 ? 4 : 2, v = kBytes / esize;
+    if (y.wide && y.x != y.out)
+      copy_rest<kBytes>(Heads(y, nr, nh, (y.dim - a.rot) / v), x, out, y.off / v, a.rot / v, esize);
   }
   __syncthreads();                                       // the angles
   for (int k = 0; k < a.n_slots; ++k) {
@@ -263,11 +292,11 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
                     kInter, cs);
       continue;
     }
-    const Heads n(y, nr, nh, (kInter ? a.rot : half) / (y.dtype == 1 ? 4 : 8));
+    const Heads n(y, nr, nh, (kInter ? a.rot : half) / (y.dtype == 1 ? kBytes / 4 : kBytes / 2));
     if (kInter)
-      y.dtype == 1 ? turn_inter<false>(n, x, out, y.off, half, cs) : turn_inter<true>(n, x, out, y.off, half, cs);
+      y.dtype == 1 ? turn_inter<false, kBytes>(n, x, out, y.off, half, cs) : turn_inter<true, kBytes>(n, x, out, y.off, half, cs);
     else
-      y.dtype == 1 ? turn_half<false>(n, x, out, y.off, half, cs) : turn_half<true>(n, x, out, y.off, half, cs);
+      y.dtype == 1 ? turn_half<false, kBytes>(n, x, out, y.off, half, cs) : turn_half<true, kBytes>(n, x, out, y.off, half, cs);
   }
 }
 
@@ -277,14 +306,19 @@ cudaError_t launch_rope(RopeArgs& a, int rows, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
   int heads = 0;   // of the tensor with the most
   int vecs = 0;    // 16-byte pieces of a row of all tensors
+  int bytes = 16;  // of a vector: 8 where a tensor cannot have 16 but 8
+  auto fits = [&](const RopeArgs::Slot& y, int w) -> bool {   // whole vectors of w bytes, turned ones too
+    const uintptr_t at = reinterpret_cast<uintptr_t>(y.x) | reinterpret_cast<uintptr_t>(y.out);
+    const int e = w / (y.dtype == 1 ? 4 : 2);
+    return at % w == 0 && y.dim % e == 0 && y.off % e == 0 && a.rot % e == 0 && (a.interleaved || a.rot / 2 % e == 0);
+  };
   for (int k = 0; k < a.n_slots; ++k) {
     RopeArgs::Slot& y = a.slot[k];
-    const int v = y.dtype == 1 ? 4 : 8;
-    const uintptr_t at = reinterpret_cast<uintptr_t>(y.x) | reinterpret_cast<uintptr_t>(y.out);
-    y.wide = at % 16 == 0 && y.dim % v == 0 && y.off % v == 0 && a.rot % v == 0 && (a.interleaved || a.rot / 2 % v == 0);
+    if (!fits(y, 16) && fits(y, 8)) bytes = 8;
     heads = heads > y.heads ? heads : y.heads;
-    vecs += (y.heads * y.dim + v - 1) / v;
+    vecs += (y.heads * y.dim * (y.dtype == 1 ? 4 : 2) + 15) / 16;
   }
+  for (int k = 0; k < a.n_slots; ++k) a.slot[k].wide = fits(a.slot[k], bytes);
   // Four blocks for every SM: as many rows a block as that leaves, up to 8, of
   // small rows up to 64 (16,384 rows of one head of 192, 32 pairs: 22.0 us with 8, 12.2 with 26);
   // when one row each does not give that many blocks, the heads are split.
@@ -299,7 +333,9 @@ cudaError_t launch_rope(RopeArgs& a, int rows, cudaStream_t st) {
   int split = blocks >= want ? 1 : (want + blocks - 1) / blocks;
   split = split > heads ? heads : split;
   note_launch();
-  return launch_pdl(a.interleaved ? rope_kernel<true> : rope_kernel<false>, dim3(unsigned(blocks), unsigned(split)),
+  const auto kernel = a.interleaved ? (bytes == 16 ? rope_kernel<true, 16> : rope_kernel<true, 8>)
+                                    : (bytes == 16 ? rope_kernel<false, 16> : rope_kernel<false, 8>);
+  return launch_pdl(kernel, dim3(unsigned(blocks), unsigned(split)),
                     dim3(kThreads), size_t(a.per_block) * (a.rot / 2) * sizeof(float2), st, 1, a);
 }
 

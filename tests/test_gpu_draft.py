@@ -46,7 +46,9 @@ def f64(t):
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("rows,heads,dim,rot,off,inverse", [
     (1, 1, 2, 2, 0, False), (3, 64, 192, 64, 128, False), (5, 8, 64, 64, 0, True), (17, 3, 40, 8, 32, False),
-    (2, 5, 10, 6, 3, True), (700, 4, 96, 16, 0, False), (4, 128, 1024, 1024, 0, False), (9, 2, 24, 12, 8, True)])
+    (2, 5, 10, 6, 3, True), (700, 4, 96, 16, 0, False), (4, 128, 1024, 1024, 0, False), (9, 2, 24, 12, 8, True),
+    # vectors of 8 bytes; small rows, many a block
+    (33, 5, 64, 8, 56, False), (6, 3, 36, 24, 4, False), (3000, 1, 40, 40, 0, True), (5000, 1, 64, 8, 0, False), (2000, 2, 12, 4, 8, True)])
 def test_rope_matches_definition(csa2, dtype, inter, rows, heads, dim, rot, off, inverse):
     g = torch.Generator().manual_seed(rows * 31 + dim)
     x = randn(g, (rows, heads, dim), dtype)
