@@ -37,6 +37,7 @@ typedef unsigned long long u64;
 
 constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kBins = 256;
+constexpr int kLoads = 8;           // masses a thread has on their way
 constexpr int kMaxCluster = 16;
 constexpr int kMaxCached = 24576;   // masses a CTA keeps in shared memory (192 KB)
 static_assert(kMaxCached / kSelWarps <= 32 * 32, "a warp's ballots fit one register a lane");
@@ -45,6 +46,27 @@ CSA2_DEV u64 mass_key(long long m) { return u64(m) ^ 0x8000000000000000ull; }   
 
 CSA2_DEV void dsmem_st_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// The first pass's bin of a key: 0 for masses below 0, then 4 an octave, and the keys of one.
+constexpr u64 kZero = 0x8000000000000000ull;
+CSA2_DEV int first_bin(u64 k) {
+  if (k < kZero) return 0;
+  const u64 x = k - kZero;
+  const int e = 63 - __clzll((long long)(x | 3));      // >= 1
+  return 1 + (x < 4 ? int(x) : (e - 1) * 4 + (int(x >> (e - 2)) & 3));
+}
+CSA2_DEV void first_range(int bin, u64& low, u64& high) {
+  if (bin == 0) {
+    low = 0;
+    high = kZero - 1;
+  } else if (bin <= 4) {                               // one value a bin
+    low = high = kZero + u64(bin - 1);
+  } else {                                             // the octave e = (bin - 1) / 4 + 1, less the two bits
+    const int width = (bin - 1) / 4 - 1;
+    low = kZero + (u64(4 + ((bin - 1) & 3)) << width);
+    high = low + ((1ull << width) - 1);
+  }
 }
 
 struct SelectShared {
@@ -64,6 +86,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   u64* cache = reinterpret_cast<u64*>(dyn + sizeof(SelectShared));
   const int seq = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = int(cluster_rank()), ncta = int(cluster_size());
+  reinterpret_cast<int4*>(&sh.table[1][0][0])[tid] = make_int4(0, 0, 0, 0);
   pdl_wait();
   const int n = clamp_count(a.n_valid[seq], a.n_entries, rank == 0 && tid == 0 ? a.err : nullptr);
   int* kept = a.kept + (long long)seq * a.n_entries;
@@ -85,18 +108,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int cta0 = min(n, rank * kSelWarps * per_warp);
   const int w0 = min(n, (rank * kSelWarps + warp) * per_warp), w1 = min(n, w0 + per_warp);
   const int c0 = max(w0, lo), c1 = min(w1, hi);
+  __syncthreads();                                     // the zeros of the first pass's counts
   // its own warp's keys only: no barrier between filling the cache and reading it
   auto key = [&](int j) -> u64 { return kCached ? cache[j - cta0] : mass_key(mass[j]); };
 
-  // the keys, and the bits in which the competing ones differ
+  // The keys, their range, and the first pass's counts: 16 a bin, so that lanes
+  // of a warp that share a bin mostly count in words of their own.  A pass's
+  // lie in the table that the pass does not exchange counts in: the last pass's, which has
+  // been read, and which a peer writes only when all have finished this pass.
   u64 mn = ~0ull, mx = 0;
-#pragma unroll 8
-  for (int j = w0 + lane; j < w1; j += 32) {
-    const u64 k = mass_key(mass[j]);
-    if (kCached) cache[j - cta0] = k;
-    if (j >= c0 && j < c1) {
-      mn = min(mn, k);
-      mx = max(mx, k);
+  for (int j0 = w0 + lane; j0 < w1; j0 += 32 * kLoads) {
+    u64 k[kLoads];
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) k[x] = j0 + 32 * x < w1 ? mass_key(mass[j0 + 32 * x]) : 0;
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+      const int j = j0 + 32 * x;
+      if (j >= w1) break;
+      if (kCached) cache[j - cta0] = k[x];
+      if (j >= c0 && j < c1) {
+        mn = min(mn, k[x]);
+        mx = max(mx, k[x]);
+        atomicAdd(&sh.table[1][0][0] + first_bin(k[x]) * 16 + (lane & 15), 1);
+      }
     }
   }
   for (int o = 16; o > 0; o >>= 1) {
@@ -107,64 +141,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     sh.warp_mn[warp] = mn;
     sh.warp_mx[warp] = mx;
   }
-  cluster_arrive();   // (every CTA of the cluster runs before any writes into it)
-  __syncthreads();
-  if (warp == 0) {
-    mn = sh.warp_mn[lane];
-    mx = sh.warp_mx[lane];
-    for (int o = 16; o > 0; o >>= 1) {
-      mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    }
-  }
-  cluster_wait();
-  if (warp == 0 && lane < ncta) {
-    dsmem_st_u64(dsmem_addr(&sh.range[rank][0], lane), mn);
-    dsmem_st_u64(dsmem_addr(&sh.range[rank][1], lane), mx);
-  }
-  cluster_sync_all();
-  mn = ~0ull;
-  mx = 0;
-  for (int r = 0; r < ncta; ++r) {
-    mn = min(mn, sh.range[r][0]);
-    mx = max(mx, sh.range[r][1]);
-  }
-  // (More keys compete than there are places, so mn <= mx.)  The first pass
-  // bins k - mn by its octave and the two bits below its leading one, 4 bins an
-  // octave, the later ones by the next 8 bits.  Invariant: the keys of
-  // [low, high], 2^shift values from a multiple of it above mn on, hold the
-  // need-th greatest, and every greater key is taken.
+  cluster_arrive();                                    // (every CTA of the cluster runs before any writes into it)
+  // Invariant: the keys of [low, high] hold the need-th greatest, and every
+  // greater key is taken; high - low < 2^shift.  The first pass bins a key by its octave
+  // and the two bits below its leading one, the later ones by 8 bits of its
+  // distance to low; more keys compete than there are places.
   int shift = 64;
-  u64 low = mn, high = ~0ull;
+  u64 low = 0, high = ~0ull;
   bool whole = need == 0;                              // all keys of the range are taken (or none, as no place is left)
-  if (mn == mx) {
-    shift = 0;
-    high = mn;
-  }
+  if (whole) cluster_wait();
   for (int pass = 0; shift > 0 && !whole; ++pass) {
     const bool first = pass == 0;
-    const int bits = first ? 8 : min(8, shift), next = shift - bits;
-    // Counts, 16 a bin: lanes of a warp that share a bin mostly count in words of
-    // their own.  They lie in the table that this pass's counts do not go
-    // to: the last pass's, which has been read, and which a peer writes only when all have finished this pass.
+    const int bits = min(8, shift), next = shift - bits;
     int* count = &sh.table[(pass + 1) & 1][0][0];
-    reinterpret_cast<int4*>(count)[tid] = make_int4(0, 0, 0, 0);
-    __syncthreads();
+    if (!first) {
+      reinterpret_cast<int4*>(count)[tid] = make_int4(0, 0, 0, 0);
+      __syncthreads();
 #pragma unroll 2
-    for (int j0 = c0 & ~31; j0 < c1; j0 += 32) {
-      const int j = j0 + lane;
-      if (j < c0 || j >= c1) continue;
-      const u64 k = key(j);
-      int bin;
-      if (first) {
-        const u64 x = k - mn;
-        const int e = 63 - __clzll((long long)(x | 3));             // >= 1
-        bin = x < 4 ? int(x) : (e - 1) * 4 + (int(x >> (e - 2)) & 3);
-      } else {
-        if (k < low || k > high) continue;
-        bin = int((k - low) >> next);
+      for (int j0 = c0 & ~31; j0 < c1; j0 += 32) {
+        const int j = j0 + lane;
+        if (j < c0 || j >= c1) continue;
+        const u64 k = key(j);
+        if (k >= low && k <= high) atomicAdd(count + int((k - low) >> next) * 16 + (lane & 15), 1);
       }
-      atomicAdd(count + bin * 16 + (lane & 15), 1);
     }
     __syncthreads();
     int(*table)[kBins] = sh.table[pass & 1];
@@ -174,6 +173,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     own4 += __shfl_xor_sync(0xffffffffu, own4, 2);
     if ((tid & 3) == 0) sh.hist[tid >> 2] = own4;
     __syncthreads();
+    if (first) {
+      cluster_wait();
+      if (warp == 0) {
+        mn = sh.warp_mn[lane];
+        mx = sh.warp_mx[lane];
+        for (int o = 16; o > 0; o >>= 1) {
+          mn = min(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+          mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+        if (lane < ncta) {
+          dsmem_st_u64(dsmem_addr(&sh.range[rank][0], lane), mn);
+          dsmem_st_u64(dsmem_addr(&sh.range[rank][1], lane), mx);
+        }
+      }
+    }
     for (int i = tid; i < ncta * kBins; i += kSelThreads)           // (a warp's words go to one peer, side by side)
       dsmem_st_u32(dsmem_addr(&table[rank][i & (kBins - 1)], i / kBins), uint32_t(sh.hist[i & (kBins - 1)]));
     cluster_sync_all();
@@ -212,19 +226,20 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     __syncthreads();
     need -= sh.above;
     whole = need == sh.total;
-    const int bin = sh.bin;
     if (!first) {
-      low += u64(bin) << next;
+      low += u64(sh.bin) << next;
+      high = min(high, low + ((1ull << next) - 1));
       shift = next;
-    } else if (bin < 4) {                              // one value a bin
-      low = mn + u64(bin);
-      shift = 0;
-    } else {                                           // the octave e = bin / 4 + 1, less the two bits
-      shift = bin / 4 - 1;
-      low = mn + (u64(4 + (bin & 3)) << shift);
+    } else {
+      first_range(sh.bin, low, high);
+      for (int r = 0; r < ncta; ++r) {                 // no wider than the keys are
+        mn = min(r == 0 ? ~0ull : mn, sh.range[r][0]);
+        mx = max(r == 0 ? 0ull : mx, sh.range[r][1]);
+      }
+      low = max(low, mn);
+      high = min(high, mx);
+      shift = high == low ? 0 : 64 - __clzll((long long)(high - low));
     }
-    high = low + ((1ull << shift) - 1);
-    if (high < low) high = ~0ull;
   }
   // A key is taken if it is above the range, or in it while places are left:
   // `need` of them, the lowest indices.

@@ -606,7 +606,10 @@ def evict_inputs(S, N, dk, dv, dI, block, dtype, seed, kind, n_valid=None):
     m = {"spread": lambda: rng.integers(0, 2 ** 40, (S, N)), "ties": lambda: rng.integers(0, 4, (S, N)),
          "equal": lambda: np.full((S, N), 5), "zero": lambda: np.zeros((S, N), dtype=np.int64),
          "wide": lambda: rng.integers(-2 ** 63, 2 ** 63 - 1, (S, N)),
-         "rising": lambda: np.tile(np.arange(N), (S, 1)), "falling": lambda: np.tile(-np.arange(N), (S, 1))}[kind]()
+         "rising": lambda: np.tile(np.arange(N), (S, 1)), "falling": lambda: np.tile(-np.arange(N), (S, 1)),
+         "offset": lambda: 2 ** 40 + rng.integers(0, 1000, (S, N)), "below": lambda: -2 ** 62 + rng.integers(0, 2 ** 50, (S, N)),
+         "edges": lambda: rng.choice(np.array([-2 ** 63, 2 ** 63 - 1, -1, 0, 1, 2, 3, 4, 5, 7, 8, 2 ** 31, 2 ** 32 - 1, 2 ** 32, 2 ** 62,
+                                               2 ** 62 - 1, 3 * 2 ** 61, -2 ** 62], dtype=np.int64), (S, N))}[kind]()
     d.mass = torch.as_tensor(np.asarray(m, dtype=np.int64)).cuda()
     d.n = i32(rng.integers(0, N + 1, S) if n_valid is None else n_valid)
     return d
@@ -647,7 +650,9 @@ def host(*ts):
 
 CASES = [(3, 40, 30, 2, 5, "spread"), (1, 9, 1, 0, 0, "ties"), (4, 700, 512, 16, 100, "ties"), (2, 129, 128, 0, 0, "equal"),
          (2, 5000, 777, 0, 0, "wide"), (1, 30000, 20000, 16, 1024, "spread"), (2, 600, 100, 60, 40, "spread"),
-         (3, 300, 299, 0, 1, "zero"), (2, 300, 200, 3, 0, "rising"), (2, 300, 200, 0, 3, "falling"), (1, 20001, 19000, 1, 1, "zero")]
+         (3, 300, 299, 0, 1, "zero"), (2, 300, 200, 3, 0, "rising"), (2, 300, 200, 0, 3, "falling"), (1, 20001, 19000, 1, 1, "zero"),
+         (2, 3000, 1500, 5, 7, "offset"), (1, 40000, 33333, 2, 3, "offset"), (2, 2000, 900, 0, 0, "edges"), (1, 40000, 11111, 2, 3, "edges"),
+         (3, 1500, 40, 0, 0, "edges"), (1, 9000, 8000, 0, 9, "below"), (2, 100, 60, 30, 30, "spread")]
 
 
 @pytest.mark.parametrize("S,N,keep,sink,recent,kind", CASES)
