@@ -1,16 +1,17 @@
 // Eviction from full caches (csa2_kv_evict).
 //
 // evict_select_kernel -- one cluster per sequence: the entries that stay, in
-//   ascending order.  The k-th greatest 64-bit mass is found by a radix select
-//   over the bits in which the masses differ, 8 bits a pass; ties go to the
+//   ascending order.  The k-th greatest 64-bit mass is found by a radix select:
+//   first by octaves of the masses, counted while they are loaded, then 8 bits a
+//   pass over the range that is left, cut to the masses' own; ties go to the
 //   lowest index; each warp then lists its share in order.  Every CTA keeps
 //   its share of the masses in shared memory, read once, so that a pass costs a
 //   sweep of shared memory, one push of 256 counts into every CTA of the
 //   cluster and one cluster barrier.  Masses are skewed (many entries draw next to
 //   none), so a bin has 16 counts in different banks, a lane's by its number.
 //   Bound by the sweeps' instructions and the passes' cluster barriers: 64 x 8,192
-//   masses 14.4 us, 1 x 262,144 on 16 CTAs 21.8 us (one count a bin: 15.5 and 27;
-//   masses read again a pass: 29 and 100).
+//   masses 12.9 us, 1 x 262,144 on 16 CTAs 21.1 us (one count a bin and a pass of its
+//   own for the range: 15.5 and 27; masses read again a pass: 29 and 100).
 // evict_move_kernel -- out of place: every row is gathered by its entry, 16
 //   bytes a thread, so it runs at the rate of a copy: 64 x 8,192 entries down to 6,145
 //   82 to 92 us, where a plain copy of these bytes takes 83.
