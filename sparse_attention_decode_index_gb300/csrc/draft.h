@@ -21,7 +21,7 @@ struct RopeArgs {
     const void* x;           // [rows, heads, dim]
     void* out;               // [rows, heads, dim]; == x: in place
     int heads, dim, off, dtype;
-    int wide;                // whole vectors at aligned addresses (set by the launcher)
+    int wide, copy;          // whole vectors at aligned addresses; bytes of those that are copied (set by the launcher)
   } slot[kMaxRopeSlots];
   int n_slots;
   int rows, per_block;       // rows, rows per block (set by the launcher)

@@ -21,7 +21,7 @@
 // rows are split over the heads instead (8 rows: 5.8 us, a launch and that
 // chain).  An item is one vector that is copied, or the vectors that hold the
 // two halves of pairs: 16 bytes, or 8 where the sizes allow no more (7,716 rows of 48
-// heads of 40, 4 pairs: 16.1 us, element by element 71.3); its head comes from a multiplication by a
+// heads of 40, 4 pairs: 17.3 us, element by element 71.3); its head comes from a multiplication by a
 // precomputed reciprocal.
 #include "common.cuh"
 #include "draft.h"
@@ -274,9 +274,13 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
     const uint8_t* x;
     uint8_t* out;
     const RopeArgs::Slot& y = part(k, nh, x, out);
-    const int esize = y.dtype == 1 ? 4 : 2, v = kBytes / esize;
-    if (y.wide && y.x != y.out)
-      copy_rest<kBytes>(Heads(y, nr, nh, (y.dim - a.rot) / v), x, out, y.off / v, a.rot / v, esize);
+    if (!y.wide || y.x == y.out) continue;
+    const int esize = y.dtype == 1 ? 4 : 2, copy = kBytes == 16 ? 16 : y.copy, v = copy / esize;
+    const Heads n(y, nr, nh, (y.dim - a.rot) / v);
+    // 16 bytes where only the halves ask for 8 (2,562 rows of 64 heads of 192, 4 pairs: 34.3 -> 27.7 us; where
+    // nothing has 16, 48 heads of 40, the choice costs 16.5 -> 17.3)
+    if (copy == 16) copy_rest<16>(n, x, out, y.off / v, a.rot / v, esize);
+    else copy_rest<8>(n, x, out, y.off / v, a.rot / v, esize);
   }
   __syncthreads();                                       // the angles
   for (int k = 0; k < a.n_slots; ++k) {
@@ -307,10 +311,13 @@ cudaError_t launch_rope(RopeArgs& a, int rows, cudaStream_t st) {
   int heads = 0;   // of the tensor with the most
   int vecs = 0;    // 16-byte pieces of a row of all tensors
   int bytes = 16;  // of a vector: 8 where a tensor cannot have 16 but 8
-  auto fits = [&](const RopeArgs::Slot& y, int w) -> bool {   // whole vectors of w bytes, turned ones too
+  auto whole = [&](const RopeArgs::Slot& y, int w) -> bool {  // vectors of w bytes in front of, in and behind the turned dims
     const uintptr_t at = reinterpret_cast<uintptr_t>(y.x) | reinterpret_cast<uintptr_t>(y.out);
     const int e = w / (y.dtype == 1 ? 4 : 2);
-    return at % w == 0 && y.dim % e == 0 && y.off % e == 0 && a.rot % e == 0 && (a.interleaved || a.rot / 2 % e == 0);
+    return at % w == 0 && y.dim % e == 0 && y.off % e == 0 && a.rot % e == 0;
+  };
+  auto fits = [&](const RopeArgs::Slot& y, int w) -> bool {   // and in either half of them
+    return whole(y, w) && (a.interleaved || a.rot / 2 % (w / (y.dtype == 1 ? 4 : 2)) == 0);
   };
   for (int k = 0; k < a.n_slots; ++k) {
     RopeArgs::Slot& y = a.slot[k];
@@ -318,7 +325,10 @@ cudaError_t launch_rope(RopeArgs& a, int rows, cudaStream_t st) {
     heads = heads > y.heads ? heads : y.heads;
     vecs += (y.heads * y.dim * (y.dtype == 1 ? 4 : 2) + 15) / 16;
   }
-  for (int k = 0; k < a.n_slots; ++k) a.slot[k].wide = fits(a.slot[k], bytes);
+  for (int k = 0; k < a.n_slots; ++k) {
+    a.slot[k].wide = fits(a.slot[k], bytes);
+    a.slot[k].copy = whole(a.slot[k], 16) ? 16 : 8;   // (of wide ones)
+  }
   // Four blocks for every SM: as many rows a block as that leaves, up to 8, of
   // small rows up to 64 (16,384 rows of one head of 192, 32 pairs: 22.0 us with 8, 12.2 with 26);
   // when one row each does not give that many blocks, the heads are split.
