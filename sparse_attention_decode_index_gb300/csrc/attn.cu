@@ -36,7 +36,7 @@
 // to workspace scratch in L2 instead was measured slower at small batches and
 // equal at batch 64.)
 //
-// The tree form (csa2_tree_attn, kTree; few queries, tree_tc.cu takes the
+// The tree form (csa2_tree_attn, kTree; few queries of many keys, tree_tc.cu takes the
 // others) differs in the window's slots: slot r holds the r-th drafted token of
 // the query's path (0: itself), and behind the path the newest committed rows,
 // so that the window never takes more than W slots and the launch keeps its

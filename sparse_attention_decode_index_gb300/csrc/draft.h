@@ -71,7 +71,7 @@ struct AttnWeightsArgs {
 // fast: bf16, 64 heads, dk 192, dv 128
 cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan, size_t plan_bytes, cudaStream_t st);
 cudaError_t launch_tree_attn_cluster(const TreeArgs& a, int batch, cudaStream_t st);   // attn.cu
-// Pairs of tokens on the tensor cores (tree_tc.cu); `plan` holds tree_plan_words.
+// Tokens alone or in pairs on the tensor cores (tree_tc.cu); `plan` holds tree_plan_words.
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStream_t st);
 size_t tree_plan_words(int seqs, int tokens, int topk, int swa);
 // bf16 rows of whole 8-byte pieces, any heads and dims (tree_mma.cu).

@@ -428,14 +428,18 @@ __global__ void __launch_bounds__(kWGenThreads) weights_generic_kernel(const Att
   if ((lane & 1) == 0 && j0 + (lane >> 1) < a.topk) a.weights[(long long)b * a.topk + j0 + (lane >> 1)] = w;
 }
 
-// A cluster of CTAs per query while all the clusters run at once (up to 7/8 of
-// two CTAs an SM: clusters do not fill every SM), pairs of tokens on the tensor
-// cores beyond.  Measured, clusters / pairs, 512 + 128 slots: 64 queries of one
-// token 15.3 / 15.0 us, 66 of trees of 33 16.4 / 19.9, 76 of trees of 4 25.9 / 19.0,
-// 256 of one token 60 / 26, 256 of trees of 16 59 / 21.
-bool tree_pairs(const TreeArgs& a, int batch, size_t plan_bytes) {
+// A cluster of CTAs per query where it has more than 384 keys and all the
+// clusters run at once (up to 7/8 of two CTAs an SM: clusters do not fill every
+// SM); groups of tokens on the tensor cores (a plan and a persistent launch)
+// otherwise: their time goes with the keys, the clusters', of 160 slots a CTA,
+// does not.  Measured, clusters / groups: 8 queries of 640 slots 12.2 / 14.7 us, 36 12.3 / 15.1,
+// 64 15.2 / 15.9, 76 trees of 4 25.9 / 18.6, 256 queries 60 / 21; 32 queries of 549 slots
+// 12.5 / 14.6, of 448 13.1 / 13.4, of 384 13.0 / 12.3, of 136 13.6 / 10.6; 1 query of 384
+// 12.4 / 12.2.
+constexpr int kFewSlots = 384;
+bool tree_groups(const TreeArgs& a, int batch, size_t plan_bytes) {
   if (tree_plan_words(batch / a.tokens, a.tokens, a.topk, a.swa) * 4 > plan_bytes) return false;
-  return 8 * batch * attn_cluster(a.topk, a.swa) > 7 * 2 * device_sm_count();
+  return a.topk + a.swa <= kFewSlots || 8LL * batch * attn_cluster(a.topk, a.swa) > 7LL * 2 * device_sm_count();
 }
 
 }  // namespace
@@ -443,7 +447,7 @@ bool tree_pairs(const TreeArgs& a, int batch, size_t plan_bytes) {
 cudaError_t launch_tree_attn(const TreeArgs& a, bool fast, int batch, void* plan, size_t plan_bytes, cudaStream_t st) {
   if (batch == 0) return cudaSuccess;
   if (fast) {
-    return tree_pairs(a, batch, plan_bytes) ? launch_tree_attn_tc(a, batch / a.tokens, plan, st)
+    return tree_groups(a, batch, plan_bytes) ? launch_tree_attn_tc(a, batch / a.tokens, plan, st)
                                             : launch_tree_attn_cluster(a, batch, st);
   }
   if (tree_rows_fit(a)) return launch_tree_rows(a, batch, st);

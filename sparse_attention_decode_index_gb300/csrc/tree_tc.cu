@@ -1,10 +1,11 @@
 // Attention of drafted trees on the 5th-generation tensor cores, for batches
-// that fill the GPU (bf16, 64 heads sharing one KV head, dk 192, dv 128).
+// that fill the GPU and for few keys (bf16, 64 heads sharing one KV head, dk 192,
+// dv 128).
 //
 // The drafted tokens of a sequence are neighbours: their Top-K lists overlap
 // and their windows are nearly the same.  One CTA therefore attends with two
-// tokens of a sequence at once (one, where a sequence has one), over the union
-// of their keys, and masks each key to the tokens that have it: a key that both
+// tokens of a sequence at once (one, where a sequence has one or every token has
+// an SM), over the union of their keys, and masks each key to the tokens that have it: a key that both
 // select is gathered once.  The gather sets the time of this attention, and the tensor cores'
 // rows come in 128s, which two tokens' 64 heads fill, so that attending both
 // tokens to a key that only one of them has costs nothing there.
@@ -781,9 +782,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
+// Tokens of a group: two, but one where every token has an SM of its own, which
+// then goes through its own keys alone (96 queries of 640 slots, trees of 16: 19.1 us in
+// pairs, 15.8 alone; 152, trees of 8: 19.1 and 16.7).
+static int group_of(int seqs, int tokens) { return tokens > 1 && seqs * tokens > device_sm_count() ? 2 : 1; }
+
 // Words of the plan of a launch.
 size_t tree_plan_words(int seqs, int tokens, int topk, int swa) {
-  const int group = tokens > 1 ? 2 : 1;
+  const int group = group_of(seqs, tokens);
   const int keys = plan_keys(topk, swa, tokens, group);
   return size_t(seqs) * ((tokens + group - 1) / group) * size_t(plan_entries(keys) + keys);
 }
@@ -793,7 +799,7 @@ cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStr
     return cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (e != cudaSuccess) return e;
-  const int group = a.tokens > 1 ? 2 : 1, n_groups = seqs * ((a.tokens + group - 1) / group);
+  const int group = group_of(seqs, a.tokens), n_groups = seqs * ((a.tokens + group - 1) / group);
   const uint32_t* words = static_cast<const uint32_t*>(plan);
   note_launch();
   e = launch_pdl(tree_plan_kernel, dim3(unsigned(n_groups)), dim3(kPlanThreads), (size_t(3) * a.topk + 1) * 4, st, 1, a,

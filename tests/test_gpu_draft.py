@@ -149,10 +149,11 @@ def tree_inputs(sh, seed, fill=None, holes=0.0, roots=1, spread=4.0):
 
 
 def run_tree(csa2, sh, d, n_draft=None, parent="own", head="own"):
+    sh, idx = padded(sh, d)
     ws = csa2.workspace(sh)
     p = d.parent if isinstance(parent, str) else parent
     h = d.head if isinstance(head, str) else head
-    csa2.tree_attn(sh, d.q, d.k_main, d.v_main, d.idx, d.k_swa, d.v_swa, d.n_swa, d.k_draft, d.v_draft, d.out, ws,
+    csa2.tree_attn(sh, d.q, d.k_main, d.v_main, idx, d.k_swa, d.v_swa, d.n_swa, d.k_draft, d.v_draft, d.out, ws,
                    swa_head=h, parent=p, n_draft=n_draft, lse=d.lse)
     return ws
 
@@ -184,9 +185,10 @@ def check_tree(sh, d, n_draft=None, parent=None, head=None):
 
 FAST = dict(q_heads=64, k_dim=192, v_dim=128, dtype="bf16")
 
-# Queries of a case by kernel: a cluster of CTAs per query up to 66 queries of 640 slots (266 of 160 slots), pairs of
-# tokens on the tensor cores beyond; any other shape of bf16 rows in whole 8-byte pieces is of kind rows, the rest generic.
-KINDS = {"clusters": (FAST, 1), "pairs": (FAST, 0), "rows": (dict(q_heads=20, k_dim=100, v_dim=72, dtype="bf16"), 1),
+# Queries of a case by kernel: up to 384 slots a query's tokens are attended on the tensor cores by plan, alone (up to an SM
+# each) or in pairs; with more slots few queries have a cluster of CTAs each, to which lists are padded here with -1.  Any
+# other shape of bf16 rows in whole 8-byte pieces is of kind rows, the rest generic.
+KINDS = {"clusters": (dict(FAST, pad=440), 1), "alone": (FAST, 1), "pairs": (FAST, 0), "rows": (dict(q_heads=20, k_dim=100, v_dim=72, dtype="bf16"), 1),
          "generic": (dict(q_heads=5, k_dim=24, v_dim=8, dtype="f32"), 1)}
 
 
@@ -197,13 +199,23 @@ def of_kind(kind, seqs, tokens, slots=100):
     return kw, seqs if few else -(-(266 // ctas + 2) // tokens)
 
 
+def padded(sh, d):
+    """The shape and the lists of a call: sh.pad slots, -1 behind the list, where the shape has it."""
+    pad = getattr(sh, "pad", 0)
+    if not pad:
+        return sh, d.idx
+    more = torch.full((d.idx.shape[0], pad - sh.topk), -1, dtype=torch.int32, device="cuda")
+    return types.SimpleNamespace(**{**vars(sh), "topk": pad}), torch.cat([d.idx, more], 1)
+
+
 @pytest.mark.parametrize("S,T,N,K,W,roots,holes", [
     (1, 1, 40, 1, 1, 1, 0.0), (1, 8, 600, 512, 128, 1, 0.0), (3, 7, 700, 512, 128, 2, 1.0), (2, 33, 300, 99, 37, 1, 1.0),
     (1, 128, 64, 40, 128, 3, 0.0), (5, 2, 513, 512, 4, 1, 0.0), (65, 1, 96, 64, 16, 1, 1.0), (2, 64, 1024, 512, 8, 1, 0.0),
     (20, 16, 600, 512, 128, 2, 1.0), (1, 3, 1200, 1000, 24, 1, 0.0),
     # pairs of tokens on the tensor cores: odd token counts, one token, full and short lists, the longest ones
     (10, 7, 700, 512, 128, 1, 0.0), (67, 1, 513, 512, 128, 1, 1.0), (3, 33, 900, 512, 64, 3, 0.0), (1, 128, 700, 512, 128, 1, 1.0),
-    (70, 1, 600, 512, 128, 1, 0.0), (20, 2, 1100, 1000, 24, 1, 0.0), (90, 3, 30, 9, 7, 1, 1.0), (160, 2, 64, 40, 1, 1, 0.0)])
+    (70, 1, 600, 512, 128, 1, 0.0), (1, 1, 300, 256, 128, 1, 0.0), (4, 9, 200, 99, 37, 2, 1.0), (19, 8, 700, 512, 128, 1, 0.0), (1, 1, 9, 1, 1, 1, 0.0),
+    (51, 3, 700, 512, 128, 1, 1.0), (20, 2, 1100, 1000, 24, 1, 0.0), (90, 3, 30, 9, 7, 1, 1.0), (160, 2, 64, 40, 1, 1, 0.0)])
 def test_tree_attention_fast_path(csa2, S, T, N, K, W, roots, holes):
     sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, **FAST)
     d = tree_inputs(sh, S * 1000 + T, holes=holes, roots=roots)
@@ -368,7 +380,7 @@ def test_tree_bad_inputs_are_recorded(csa2, kind):
     check_tree(sh, d)
 
 
-@pytest.mark.parametrize("kind", ["clusters", "pairs"])
+@pytest.mark.parametrize("kind", ["clusters", "alone", "pairs"])
 def test_tree_repeated_entries_count_each_time(csa2, kind):
     """The same index twice, and lists that do not ascend: as in csa2_sparse_attn."""
     kw, S = of_kind(kind, 2, 4)
