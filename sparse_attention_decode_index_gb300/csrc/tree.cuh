@@ -31,31 +31,65 @@ struct TreeWindow {
 };
 
 // Path of query b into `path` [kMaxTreeTokens] by the calling warp (all lanes
-// call).  The parents are held four to a lane, so that a step of the walk is
-// a shuffle; a parent that is not an earlier token ends the path.  Returns
-// the number of slots (at most W) and, in `depth`, the whole path's length.
-CSA2_DEV int tree_walk(const TreeArgs& a, int seq, int token, int* path, int& depth, bool reports) {
+// call); `jump` [kMaxTreeTokens] is scratch.  Lane l finds the ancestors at
+// distances l, l + 32, ..., by the bits of the distance: after k rounds `jump`
+// leads 2^k tokens up, so that a path of any length takes log2 rounds (a walk
+// from parent to parent was 60 ns a token).  A parent that is not an earlier
+// token ends the path.  Returns the number of slots (at most W) and, in `depth`,
+// the whole path's length.
+CSA2_DEV int tree_walk(const TreeArgs& a, int seq, int token, int* path, int* jump, int& depth, bool reports) {
+  constexpr int kEach = kMaxTreeTokens / 32;
   const int lane = threadIdx.x & 31;
-  int p[kMaxTreeTokens / 32];
+  int cur[kEach];                              // at distance 32 j + lane; -1: there is none
+  unsigned bad = 0;
 #pragma unroll
-  for (int j = 0; j < kMaxTreeTokens / 32; ++j) {
+  for (int j = 0; j < kEach; ++j) {
     const int t = 32 * j + lane;
-    p[j] = t < a.tokens && t <= token ? a.parent[(long long)seq * a.tokens + t] : -1;
-  }
-  int cur = token, n = 0;
-  while (cur >= 0) {
-    if (n < a.swa && lane == 0) path[n] = cur;
-    ++n;
-    const int v = cur < 32 ? p[0] : cur < 64 ? p[1] : cur < 96 ? p[2] : p[3];
-    int up = __shfl_sync(0xffffffffu, v, cur & 31);
-    if (up >= cur || up < -1) {
-      if (lane == 0 && reports) report(a.err, kErrBadIndex, up);
-      up = -1;
+    cur[j] = -1;
+    if (t > token) continue;                   // (distances are at most `token`, too)
+    cur[j] = token;
+    int p = a.parent[(long long)seq * a.tokens + t];
+    if (p >= t || p < -1) {
+      bad |= 1u << j;
+      p = -1;
     }
-    cur = up;
+    jump[t] = p;
   }
-  depth = n;
-  return min(n, a.swa);
+  __syncwarp();
+  for (int k = 0; (1 << k) <= token; ++k) {
+    int up[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int t = 32 * j + lane;
+      if (t > token) continue;
+      if (((t >> k) & 1) != 0 && cur[j] >= 0) cur[j] = jump[cur[j]];
+      const int p = jump[t];
+      up[j] = p >= 0 ? jump[p] : -1;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (32 * j + lane <= token) jump[32 * j + lane] = up[j];
+    __syncwarp();
+  }
+  depth = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; ++j) {
+    const int t = 32 * j + lane;
+    if (cur[j] >= 0 && t < a.swa) path[t] = cur[j];
+    depth += __popc(__ballot_sync(0xffffffffu, cur[j] >= 0));
+  }
+  if (__any_sync(0xffffffffu, bad != 0) && __any_sync(0xffffffffu, reports)) {   // only the path's last token may be one that was cut off
+    int last = -1;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (32 * j + lane == depth - 1) last = cur[j];
+    if (last >= 0) {
+      const int p = a.parent[(long long)seq * a.tokens + last];
+      if (p >= last || p < -1) report(a.err, kErrBadIndex, p);
+    }
+  }
+  return min(depth, a.swa);
 }
 
 // The sequence's committed rows, all of them: a path of `depth` tokens leaves the newest swa - depth.
@@ -81,7 +115,7 @@ CSA2_DEV bool tree_live(const TreeArgs& a, int seq, int token, bool reports) {
 // The window of query b, by the whole block; `path` is shared memory.  The
 // counts, the parents and whether the token is live are read together.
 CSA2_DEV TreeWindow tree_window(const TreeArgs& a, int b, int* path, bool reports) {
-  __shared__ int depth_s;
+  __shared__ int depth_s, jump_s[kMaxTreeTokens];
   TreeWindow w;
   const int seq = b / a.tokens;
   reports = reports && threadIdx.x == 0;
@@ -92,7 +126,7 @@ CSA2_DEV TreeWindow tree_window(const TreeArgs& a, int b, int* path, bool report
   w.path = nullptr;
   if (a.parent != nullptr) {
     if (threadIdx.x < 32) {
-      tree_walk(a, seq, w.token, path, depth, reports && w.live);
+      tree_walk(a, seq, w.token, path, jump_s, depth, reports && w.live);
       if (threadIdx.x == 0) depth_s = depth;
     }
     __syncthreads();

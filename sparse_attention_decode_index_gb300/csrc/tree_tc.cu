@@ -105,7 +105,7 @@ CSA2_DEV uint32_t range_bits(int at, int from, int to) {
 __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs a, uint32_t* plan, int group) {
   extern __shared__ int sid[];                 // [2][topk], then the ranks [topk + 1]
   int* rank = sid + 2 * a.topk;                // keys of the first list before each that the second has too
-  __shared__ int path[2][kMaxTreeTokens];
+  __shared__ int path[2][kMaxTreeTokens], jump[2][kMaxTreeTokens];
   __shared__ int n_ring[2], n_list[2], n_draft;
   __shared__ uint32_t drafted[kMaxTreeTokens];
   __shared__ int warp_s[2][kChunks * kListWarps];
@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
     const bool live = tree_live(a, seq, token, lane == 0);
     int depth = token + 1, n = min(depth, a.swa);
     if (a.parent != nullptr) {
-      n = tree_walk(a, seq, token, path[g], depth, live);
+      n = tree_walk(a, seq, token, path[g], jump[g], depth, live);
     } else {
       for (int i = lane; i < n; i += 32) path[g][i] = token - i;
     }

@@ -215,7 +215,7 @@ def padded(sh, d):
     # pairs of tokens on the tensor cores: odd token counts, one token, full and short lists, the longest ones
     (10, 7, 700, 512, 128, 1, 0.0), (67, 1, 513, 512, 128, 1, 1.0), (3, 33, 900, 512, 64, 3, 0.0), (1, 128, 700, 512, 128, 1, 1.0),
     (70, 1, 600, 512, 128, 1, 0.0), (1, 1, 300, 256, 128, 1, 0.0), (4, 9, 200, 99, 37, 2, 1.0), (19, 8, 700, 512, 128, 1, 0.0), (1, 1, 9, 1, 1, 1, 0.0),
-    (51, 3, 700, 512, 128, 1, 1.0), (20, 2, 1100, 1000, 24, 1, 0.0), (90, 3, 30, 9, 7, 1, 1.0), (160, 2, 64, 40, 1, 1, 0.0)])
+    (51, 3, 700, 512, 128, 1, 1.0), (1, 60, 700, 512, 128, 1, 0.0), (2, 30, 700, 512, 128, 2, 1.0), (20, 2, 1100, 1000, 24, 1, 0.0), (90, 3, 30, 9, 7, 1, 1.0), (160, 2, 64, 40, 1, 1, 0.0)])
 def test_tree_attention_fast_path(csa2, S, T, N, K, W, roots, holes):
     sh = shape(S * T, tokens=T, n_entries=N, topk=K, swa=W, **FAST)
     d = tree_inputs(sh, S * 1000 + T, holes=holes, roots=roots)
@@ -278,6 +278,29 @@ def test_tree_window_edges_and_chains(csa2, kind, fill):
     check_tree(sh, d, parent=chain)
     run_tree(csa2, sh, d, parent=i32(chain), head=None)
     check_tree(sh, d, parent=chain, head=np.zeros(S, dtype=int))
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("T,W", [(128, 128), (127, 40), (65, 70), (33, 1), (2, 3)])
+def test_tree_paths_of_every_length(csa2, kind, T, W):
+    """A chain given by its parents, one long branch with leaves, and parents that are not earlier tokens in its middle."""
+    kw, S = of_kind(kind, 1, T)
+    S = max(S, 3)
+    sh = shape(S * T, tokens=T, n_entries=60, topk=12, swa=W, **{**kw, "pad": 440 if kind == "clusters" else 0})
+    d = tree_inputs(sh, T)
+    par = np.tile(np.arange(T) - 1, (S, 1))
+    par[1] = np.where(np.arange(T) % 3 == 2, np.arange(T) - 2, np.arange(T) - 1)
+    bad = T // 2
+    given = par.copy()
+    given[2, bad] = bad + 5                                # recorded, and a root
+    par[2, bad] = -1
+    d.parent.copy_(i32(given))
+    ws = run_tree(csa2, sh, d)
+    assert csa2.read_device_error(ws) == (-5, BAD_INDEX)
+    check_tree(sh, d, parent=par)
+    d.parent.copy_(i32(par))
+    assert_no_device_error(csa2, run_tree(csa2, sh, d))
+    check_tree(sh, d)
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
