@@ -280,7 +280,7 @@ int csa2_layer_group(const csa2_shape* shape, const csa2_layer* layers, int32_t 
  * workspace, and runs the same layer group on a 32 MiB scratch array that the
  * library holds in device memory (a file-scope __device__ array: every GPU
  * that loads the library keeps it until the process exits; it starts zeroed).
- *   - Shapes whose csa2_workspace_bytes exceeds 32 MiB return
+ *   - Shapes whose layer groups need more than 32 MiB of workspace return
  *     CSA2_ERR_WORKSPACE and enqueue nothing.
  *   - The first call made while a device is current looks up the array's
  *     device address (once per device, safe against host threads making
@@ -429,8 +429,9 @@ int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_
  * shape.swa >= 1; batch <= 65,535; out and lse overlap nothing else (refused).
  * A chain of T gives what T steps of csa2_swa_append and csa2_sparse_attn
  * give.  Weights are rounded to bf16 before they meet bf16 values, their sums
- * are not.  Large batches keep lists of the sequences' keys in ws, where the
- * indexing calls keep scores, lists and the group's indices. */
+ * are not.  ws also holds lists of the sequences' keys, where the indexing calls
+ * keep scores, lists and the group's indices (caches much shorter than topk need
+ * the most for them). */
 int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, const void* v_main, const int32_t* idx,
                    const void* k_swa, const void* v_swa, const int32_t* swa_head, const int32_t* n_swa,
                    const void* k_draft, const void* v_draft, const int32_t* parent, const int32_t* n_draft, void* out,

@@ -370,13 +370,22 @@ int check_attn_args(const csa2_shape& s, const void* q, const void* k_main, cons
 
 }  // namespace
 
+namespace csa2 {
+size_t layer_workspace_bytes(const csa2_shape* shape) { return check_shape(shape) == CSA2_OK ? layout(*shape).total : 0; }
+}  // namespace csa2
+
 // ====================================================================== C ABI
 
 extern "C" {
 
 size_t csa2_workspace_bytes(const csa2_shape* shape) {
   if (check_shape(shape) != CSA2_OK) return 0;
-  return layout(*shape).total;
+  const csa2_shape& s = *shape;
+  const WsLayout L = layout(s);
+  if (!attn_fast(s) || s.swa < 1 || seqdiv(s) > kMaxTreeTokens) return L.total;
+  // the key lists of csa2_tree_attn, where the caches are shorter than the lists
+  const size_t plan = align_up(tree_plan_most(s.batch / seqdiv(s), seqdiv(s), s.topk, s.swa) * 4);
+  return std::max(L.total, L.tok_scores + plan);
 }
 
 int csa2_workspace_init(void* ws, size_t ws_bytes, csa2_stream_t stream) {
@@ -848,7 +857,7 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
   a.err = static_cast<int*>(ws);
   // the groups' key lists live in the workspace from the token scores on, which hold nothing between calls
   const WsLayout L = layout(s);
-  return cuda_status(launch_tree_attn(a, attn_fast(s), s.batch, at<void>(ws, L.tok_scores), L.total - L.tok_scores, stream));
+  return cuda_status(launch_tree_attn(a, attn_fast(s), s.batch, at<void>(ws, L.tok_scores), ws_bytes - L.tok_scores, stream));
 }
 
 int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main, const int32_t* idx, const float* lse,

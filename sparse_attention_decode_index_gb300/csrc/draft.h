@@ -2,6 +2,7 @@
 // (rope.cu, the tree form of attn.cu, tree.cu, tree_tc.cu, weights_tc.cu,
 // commit.cu, evict.cu), beside internal.h.
 #pragma once
+#include "../../include/csa2.h"
 #include "internal.h"
 
 namespace csa2 {
@@ -74,6 +75,9 @@ cudaError_t launch_tree_attn_cluster(const TreeArgs& a, int batch, cudaStream_t 
 // Tokens alone or in pairs on the tensor cores (tree_tc.cu); `plan` holds tree_plan_words.
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStream_t st);
 size_t tree_plan_words(int seqs, int tokens, int topk, int swa);
+size_t tree_plan_most(int seqs, int tokens, int topk, int swa);
+// Bytes of workspace that all calls but csa2_tree_attn, which uses more where it gets it, need (0: a bad shape; api.cu).
+size_t layer_workspace_bytes(const csa2_shape* shape);
 // bf16 rows of whole 8-byte pieces, any heads and dims (tree_mma.cu).
 bool tree_rows_fit(const TreeArgs& a);
 bool weights_rows_fit(const AttnWeightsArgs& a);

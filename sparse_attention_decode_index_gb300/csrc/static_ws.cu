@@ -21,7 +21,7 @@
 #include <mutex>
 
 #include "../../include/csa2.h"
-#include "internal.h"
+#include "draft.h"
 
 namespace {
 
@@ -59,7 +59,7 @@ extern "C" {
 int csa2_layer_group_static(const csa2_shape* shape, const csa2_layer* layers, int32_t n_layers,
                             const void* k_main, const void* v_main, const void* k_idx, const void* kb,
                             const int32_t* n_valid, const int32_t* n_swa, csa2_stream_t stream) {
-  const size_t need = csa2_workspace_bytes(shape);
+  const size_t need = csa2::layer_workspace_bytes(shape);
   if (need == 0) return CSA2_ERR_INVALID_ARG;
   if (need > kStaticWorkspaceBytes) return CSA2_ERR_WORKSPACE;
   void* ws = nullptr;

@@ -787,11 +787,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // pairs, 15.8 alone; 152, trees of 8: 19.1 and 16.7).
 static int group_of(int seqs, int tokens) { return tokens > 1 && seqs * tokens > device_sm_count() ? 2 : 1; }
 
-// Words of the plan of a launch.
-size_t tree_plan_words(int seqs, int tokens, int topk, int swa) {
-  const int group = group_of(seqs, tokens);
+static size_t plan_words(int seqs, int tokens, int topk, int swa, int group) {
   const int keys = plan_keys(topk, swa, tokens, group);
   return size_t(seqs) * ((tokens + group - 1) / group) * size_t(plan_entries(keys) + keys);
+}
+
+// Words of the plan of a launch on the current device, and the most of one on any (of up to 1,024 SMs).
+size_t tree_plan_words(int seqs, int tokens, int topk, int swa) {
+  return plan_words(seqs, tokens, topk, swa, group_of(seqs, tokens));
+}
+size_t tree_plan_most(int seqs, int tokens, int topk, int swa) {
+  const size_t pairs = tokens > 1 ? plan_words(seqs, tokens, topk, swa, 2) : 0;
+  const size_t alone = tokens == 1 || (long long)seqs * tokens <= 1024 ? plan_words(seqs, tokens, topk, swa, 1) : 0;
+  return pairs > alone ? pairs : alone;
 }
 
 cudaError_t launch_tree_attn_tc(const TreeArgs& a, int seqs, void* plan, cudaStream_t st) {

@@ -163,6 +163,17 @@ def test_outputs_over_other_arrays_are_refused(csa2):
             assert commit([one, two], *rest[:i], p, *rest[i + 1:]) == INVALID, (i, p)
 
 
+def test_workspace_holds_the_key_lists_of_trees(csa2):
+    """Short caches with long lists: the workspace grows by the lists of csa2_tree_attn; fp32 and long caches keep theirs."""
+    small = _shape(csa2, batch=208, tokens=16, n_entries=57, topk=512, swa=128)
+    lists = 208 // 2 * (2 * 512 + 128 + 16) * 4            # two tokens a list: both selections, the window, the drafted rows
+    assert _ws(csa2, small) > lists
+    plain = _shape(csa2, batch=208, tokens=16, n_entries=57, topk=512, swa=128, dtype="f32")
+    assert _ws(csa2, plain) < lists + 65536
+    big = dict(batch=208, tokens=16, n_entries=4096, topk=512, swa=128)
+    assert _ws(csa2, _shape(csa2, **big)) == _ws(csa2, _shape(csa2, dtype="f32", **big))
+
+
 def test_attn_weights_refusals(csa2):
     lib = csa2.lib()
     s = _shape(csa2)
