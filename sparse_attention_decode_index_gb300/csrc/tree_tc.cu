@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
     // The searches take it for granted; without it nothing of theirs is used.
 #pragma unroll
     for (int x = 0; x < kChunks; ++x) {
-      if (x * kListThreads >= a.topk) break;
+      if (x * kListThreads >= a.topk || ng == 1) break;
       const int j = x * kListThreads + tid;
       if (j >= a.topk) continue;
       for (int g = 0; g < 2; ++g) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const TreeArgs 
     }
   }
   __syncthreads();
-  const bool merge = ordered != 0;
+  const bool merge = ng > 1 && ordered != 0;   // (a list alone is taken as it is)
   if (lists) {
 #pragma unroll
     for (int x = 0; x < kChunks; ++x) {
@@ -575,9 +575,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       return item;
     };
     uint32_t items = 0;
+    fetch_q(blockIdx.x);                                      // beside its counts
     const int first = next_item(blockIdx.x);
     if (first < n_groups) {
-      fetch_q(first);
+      if (first != int(blockIdx.x)) fetch_q(first);
       store_q();
     }
     for (int item = blockIdx.x; item < n_groups; item += gridDim.x) {
@@ -672,8 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_main = int(list[0]), n_ring = int(list[1]), n_all = n_main + n_ring + int(list[2]);
       const int seq = item / per_seq, nt = (n_all + kTile - 1) / kTile;
       list += first_key;
+      uint32_t entry = list[on ? mine : 0];   // (beside the counts: a plan has room for a tile at least)
       int pos = on ? mine : n_all;
-      uint32_t entry = pos < n_all ? list[pos] : 0;
       for (int i = 0; i < nt; ++i, ++tiles) {
         const Key key = resolve(a, seq, pos, entry, n_main, n_ring, n_all);
         pos += kTile;
