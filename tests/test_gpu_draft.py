@@ -611,6 +611,21 @@ def test_tree_commit_bad_inputs(csa2):
     assert int(d.head[1]) == (W - 1 + 2) % W and int(d.n_swa[2]) == 3 and torch.equal(m, d.mass)
 
 
+def test_tree_commit_of_a_token_twice(csa2):
+    """A path that names a token more than once pushes its rows and adds its weights each time; windows shorter than it."""
+    S, T, L, N, K, W = 3, 9, 5, 300, 64, 4
+    d = commit_inputs(S, T, L, N, K, W, 32, 16, "bf16", 4)
+    d.path.copy_(i32([[2] * 9, [0, 1, 0, 1, 0, 1, 0, 1, 0], [8, 8, 7, 7, 8, 0, 0, 1, 1]]))
+    d.n_path.copy_(i32([9, 8, 7]))
+    want = commit_reference(d, L, S, T, W, N)
+    ws = csa2.workspace(d.sh)
+    csa2.tree_commit(d.sh, [(d.kd[l], d.vd[l], d.ks[l], d.vs[l], d.idx[l], d.w[l]) for l in range(L)], d.path, d.n_path, d.head,
+                     d.n_swa, ws, mass=d.mass)
+    assert_no_device_error(csa2, ws)
+    for got, ref in zip((d.ks, d.vs, d.mass, d.head, d.n_swa), want):
+        assert torch.equal(got.cpu(), torch.as_tensor(ref))
+
+
 def test_tree_commit_rounds_weights_once(csa2):
     """Weights that end at, below and between the halves of 2^-32, whole and large ones, and entries selected twice by a
     token: rint(w 2^32) each, in integers (w 2^32 is exact in 64 bits)."""
@@ -855,3 +870,44 @@ def test_a_step_of_all_operators(csa2):
         torch.cuda.synchronize()
         for k in STATE:
             assert torch.equal(getattr(a, k), getattr(c, k)), k
+
+
+def test_calls_on_two_streams_at_once(csa2):
+    """The persistent and the cluster kernels of two streams, each with its own workspace and state, give what they give
+    one after the other."""
+    def state(seed):
+        sh = shape(40 * 16, tokens=16, n_entries=600, topk=512, swa=64, **FAST)
+        d = tree_inputs(sh, seed)
+        d.w = torch.empty((640, 512), device="cuda")
+        d.mass = torch.zeros((40, 600), dtype=torch.int64, device="cuda")
+        d.path = i32(np.tile(np.arange(16), (40, 1)))
+        d.n_path = i32([16] * 40)
+        d.one = shape(40, n_entries=600, topk=512, swa=64, **FAST)
+        d.k_idx = torch.zeros((40, 600, 64), dtype=torch.bfloat16, device="cuda")
+        d.kept = torch.empty((40, 600), dtype=torch.int32, device="cuda")
+        d.n_valid = i32([600] * 40)
+        return sh, d, csa2.workspace(sh), csa2.workspace(d.one)
+
+    def run(sh, d, ws, ws1):
+        csa2.tree_attn(sh, d.q, d.k_main, d.v_main, d.idx, d.k_swa, d.v_swa, d.n_swa, d.k_draft, d.v_draft, d.out, ws,
+                       swa_head=d.head, parent=d.parent, lse=d.lse)
+        csa2.attn_weights(sh, d.q, d.k_main, d.idx, d.lse, d.w, ws)
+        csa2.tree_commit(sh, [(d.k_draft, d.v_draft, d.k_swa, d.v_swa, d.idx, d.w)], d.path, d.n_path, d.head, d.n_swa, ws, mass=d.mass)
+        csa2.kv_evict(d.one, 500, 400, 4, 32, d.k_main, d.v_main, d.k_idx, d.mass, d.n_valid, d.kept, ws1)
+
+    alone = [state(31), state(32)]
+    for x in alone:
+        run(*x)
+    torch.cuda.synchronize()
+    both = [state(31), state(32)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for x, st in zip(both, streams):
+        with torch.cuda.stream(st):
+            run(*x)
+    torch.cuda.synchronize()
+    for x, y in zip(alone, both):
+        for ws in x[2:] + y[2:]:
+            assert_no_device_error(csa2, ws)
+        for k in ("out", "lse", "w", "mass", "k_swa", "v_swa", "head", "n_swa", "k_main", "v_main", "kept", "n_valid"):
+            assert torch.equal(getattr(x[1], k), getattr(y[1], k)), k
