@@ -14,9 +14,9 @@
 //     the fast path (half a step, 2^-8 of a weight; its sum is not rounded).
 //     The warps' sums are added up in their order.
 //   Bound by latency, two round trips to memory per 16 slots of a warp: 126
-//   queries, 40 heads of 100 / 64, 576 slots 28.6 us (fp32 products in
-//   tree_generic_kernel: 104), 110 queries, 40 heads of 64 / 16, 640 slots 23.3
-//   (84), 58 queries, 16 heads of 100 / 128, 640 slots 16.2 (30.2).
+//   queries, 40 heads of 100 / 64, 576 slots 23.4 us (fp32 products in
+//   tree_generic_kernel: 104), 110 queries, 40 heads of 64 / 16, 640 slots 19.6
+//   (84), 58 queries, 16 heads of 100 / 128, 640 slots 15.1 (30.2).
 // weights_rows_kernel -- one CTA per (query, 64 slots), the same scores for 16
 //   heads at a time; exp(s - lse) is summed over the heads in a fixed order.
 #include "common.cuh"
@@ -36,6 +36,12 @@ constexpr int kMaxSlots = 1024;     // topk + swa
 constexpr int q_stride(int k_dim) { return (k_dim * 2 + 127) / 128 * 128 + 32; }
 // Words of a head's logits: 8 past a multiple of 32, for the same reason.
 constexpr int p_stride(int slots) { return (slots + 31) / 32 * 32 + 8; }
+
+// Warps' sums of P V that are kept side by side: with 8 warps the upper four hand
+// theirs to the lower four, which leaves room for three CTAs an SM (126 queries of 40
+// heads of 100 / 64, 576 slots: 23.4 us, two CTAs 28.4; 320 slots 19.6 and 23.7); the one CTA of 16
+// warps has room for all, and the turns cost it 0.4 us.
+constexpr int sums_of(int threads) { return threads == 256 ? threads / 64 : threads / 32; }
 
 // 16 heads of Q (rows from `heads` on are zero, and so are dims up to the next multiple of 16).
 CSA2_DEV void stage_q(uint8_t* sq, const void* q, int heads, int k_dim, int threads) {
@@ -85,8 +91,8 @@ CSA2_DEV uint32_t bf16_pair(float2 p) {
 }
 
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads, 512 / kThreads) tree_rows_kernel(const TreeArgs a) {
-  constexpr int kWarps = kThreads / 32;
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 3 : 1) tree_rows_kernel(const TreeArgs a) {
+  constexpr int kWarps = kThreads / 32, kSums = sums_of(kThreads), kTurns = kWarps / kSums;
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ int path[kMaxTreeTokens];
   __shared__ float inv_s[kTileHeads];
@@ -98,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) tree_rows_kernel(con
   const uint8_t** vrow = krow + rounded;
   float* sp = reinterpret_cast<float*>(vrow + rounded);           // [kTileHeads][ld] logits -> weights
   uint8_t* sq = reinterpret_cast<uint8_t*>(sp + kTileHeads * ld); // [kTileHeads][q_stride]
-  float* part = reinterpret_cast<float*>(sq);                     // later: [kWarps][kTileHeads][kPassDims]
+  float* part = reinterpret_cast<float*>(sq);                     // later: [kSums][kTileHeads][kPassDims]
   pdl_wait();
   stage_q(sq, static_cast<const __nv_bfloat16*>(a.q) + ((long long)b * a.heads + h0) * a.k_dim, nh, a.k_dim, kThreads);
   const TreeWindow win = tree_window(a, b, path, blockIdx.x == 0);
@@ -201,21 +207,34 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) tree_rows_kernel(con
         }
       }
     }
-    // columns 2 t and 2 t + 1 of product j are dims 8 t + j and 8 t + 4 + j
+    // Columns 2 t and 2 t + 1 of product j are dims 8 t + j and 8 t + 4 + j
+    auto place = [&](int w, int x, int i) -> float4& {
+      return *reinterpret_cast<float4*>(part + (w * kTileHeads + g + 8 * (i >> 1)) * kPassDims + 32 * x + 8 * t + 4 * (i & 1));
+    };
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int turn = kTurns - 1; turn >= 0; --turn) {
+      if (warp / kSums == turn) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float* to = part + (warp * kTileHeads + g + 8 * (i >> 1)) * kPassDims + 32 * x + 8 * t + 4 * (i & 1);
-        *reinterpret_cast<float4*>(to) = make_float4(acc[x][0][i], acc[x][1][i], acc[x][2][i], acc[x][3][i]);
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float4 v = make_float4(acc[x][0][i], acc[x][1][i], acc[x][2][i], acc[x][3][i]);
+            float4& to = place(warp % kSums, x, i);
+            if (turn < kTurns - 1) {
+              const float4 u = to;
+              v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+            to = v;
+          }
       }
-    __syncthreads();
+      __syncthreads();
+    }
     for (int i = tid; i < nh * kPassDims; i += kThreads) {
       const int h = i / kPassDims, x = i % kPassDims;
       if (d0 + x >= a.v_dim) continue;
       float o = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) o += part[(w * kTileHeads + h) * kPassDims + x];
+      for (int w = 0; w < kSums; ++w) o += part[(w * kTileHeads + h) * kPassDims + x];
       store_elem(a.out, ((long long)b * a.heads + h0 + h) * a.v_dim + d0 + x, 0, o * inv_s[h]);
     }
     __syncthreads();
@@ -224,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) tree_rows_kernel(con
 
 constexpr size_t rows_smem(int slots, int k_dim, int threads) {
   const size_t rounded = size_t(slots + kTileSlots - 1) / kTileSlots * kTileSlots;
-  const size_t q = size_t(kTileHeads) * q_stride(k_dim), sums = size_t(threads / 32) * kTileHeads * kPassDims * sizeof(float);
+  const size_t q = size_t(kTileHeads) * q_stride(k_dim), sums = size_t(sums_of(threads)) * kTileHeads * kPassDims * sizeof(float);
   return rounded * 16 + size_t(kTileHeads) * p_stride(slots) * sizeof(float) + (q > sums ? q : sums);
 }
 
@@ -309,7 +328,7 @@ bool tree_rows_fit(const TreeArgs& a) {
 
 bool weights_rows_fit(const AttnWeightsArgs& a) { return a.dtype == 0 && pieces(a.k_dim, a.q, a.k_main); }
 
-// 16 warps and one CTA an SM while there are no more CTAs than SMs, 8 warps and two beyond, as in tree.cu.
+// 16 warps and one CTA an SM while there are no more CTAs than SMs, 8 warps and up to three beyond (tree.cu has both measured).
 cudaError_t launch_tree_rows(const TreeArgs& a, int batch, cudaStream_t st) {
   const bool few = (long long)batch * ((a.heads + kTileHeads - 1) / kTileHeads) <= device_sm_count();
   return few ? launch_rows<512>(a, batch, st) : launch_rows<256>(a, batch, st);
