@@ -425,7 +425,7 @@ int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_
  *   k_swa [S, W, dk]  v_swa [S, W, dv]  swa_head, n_swa [S]
  *   k_draft [S, T, dk]  v_draft [S, T, dv]  parent [S, T]  n_draft [S] (0..T)
  *   out [B, H, dv] in the element type (it feeds the output projection)
- *   lse [B, H] fp32 (nullable)
+ *   lse [B, H] fp32 (nullable); NaN where a key that is attended scores NaN or +inf, as out is
  * shape.swa >= 1; batch <= 65,535; out and lse overlap nothing else (refused).
  * A chain of T gives what T steps of csa2_swa_append and csa2_sparse_attn
  * give.  Weights are rounded to bf16 before they meet bf16 values, their sums

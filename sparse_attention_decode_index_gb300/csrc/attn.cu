@@ -40,8 +40,11 @@
 // others) differs in the window's slots: slot r holds the r-th drafted token of
 // the query's path (0: itself), and behind the path the newest committed rows,
 // so that the window never takes more than W slots and the launch keeps its
-// geometry.  Its output is bf16, and it reads nothing before the launch in front
-// of it is complete.  8 queries of 640 slots take 12.0 us, 64 take 15.3.
+// geometry.  Its output is bf16, its lse is NaN where a key scores NaN, and it reads nothing before the
+// launch in front of it is complete.  8 queries of 640 slots take 12.0 us, 64 take 15.3.
+//
+// P is rounded to bf16, which mma.sync asks for beside bf16 values (half a step, 2^-8 of a weight, as
+// much as the tree form's output is rounded by); its sums stay fp32 and unrounded.
 #include "common.cuh"
 #include "draft.h"
 #include "tree.cuh"
@@ -382,9 +385,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_mma_kernel(const AttnArgs a,
     float M = -INFINITY;
     for (uint32_t r = 0; r < ncta; ++r) M = fmaxf(M, sM[r * kH + h]);
     float L = 0.f;
-    for (uint32_t r = 0; r < ncta; ++r)
+    bool nan = false;   // a key scores NaN: its CTA's sum is NaN, its maximum (fmaxf) may not be
+    for (uint32_t r = 0; r < ncta; ++r) {
       if (sM[r * kH + h] != -INFINITY) L += exp2f(sM[r * kH + h] - M) * sL[r * kH + h];
-    a.lse[(long long)b * kH + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      if (kTree) nan = nan || sL[r * kH + h] != sL[r * kH + h];
+    }
+    const float lse = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+    a.lse[(long long)b * kH + h] = nan ? NAN : lse;   // (-inf says that nothing was attended)
   }
   cluster_wait();     // every peer has read this CTA's partials: its shared memory may be released
   // Before another attention launch (a Reuse or SWA layer next), its CTAs are

@@ -380,6 +380,37 @@ def test_tree_scores_that_are_not_finite(csa2, kind):
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
+def test_tree_scores_that_are_all_nan_make_lse_nan(csa2, kind):
+    """A live token whose query is NaN, and a stretch of the window whose keys are: out and lse are NaN, as the definition has
+    them, though no key or no key of a cluster's CTA scores a number.  -inf stays the lse of tokens that attend nothing."""
+    T, W = 2, 8
+    kw, S = of_kind(kind, 2, T)
+    sh = shape(S * T, tokens=T, n_entries=90, topk=20, swa=W, **kw)
+    d = tree_inputs(sh, 8, fill=W)
+    d.parent.copy_(i32([[-1, -1]] * S))
+    d.head.copy_(i32([0] * S))                             # newest committed row: W - 1
+    q = d.q.clone()
+    d.q.view(S, T, -1)[:, 1] = float("nan")
+    assert_no_device_error(csa2, run_tree(csa2, sh, d))
+    out, lse = d.out.view(S, T, -1), d.lse.view(S, T, -1)
+    assert torch.isfinite(out[:, 0]).all() and torch.isfinite(lse[:, 0]).all()
+    assert torch.isnan(out[:, 1]).all() and torch.isnan(lse[:, 1]).all()
+    # Window slots are dealt to a cluster's CTAs in order, ceil(8 / CTAs) each, and the listed entries all lie with its first
+    # CTA of three: slots 3 to 5 are all the keys that the second has.
+    d.q.copy_(q)
+    d.k_swa[:, W - 5:W - 2] = float("nan")
+    assert_no_device_error(csa2, run_tree(csa2, sh, d))
+    assert torch.isnan(d.out).all() and torch.isnan(d.lse).all()
+    # and the weights of such a query say so
+    weights = torch.empty((S * T, sh.topk), device="cuda")
+    csa2.attn_weights(sh, d.q, d.k_main, d.idx, d.lse, weights, csa2.workspace(sh))
+    assert torch.isnan(weights).all()
+    n_draft = i32([0] * S)
+    assert_no_device_error(csa2, run_tree(csa2, sh, d, n_draft=n_draft))
+    assert (d.out == 0).all() and (d.lse == -float("inf")).all()
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
 def test_tree_bad_inputs_are_recorded(csa2, kind):
     T = 4
     kw, S = of_kind(kind, 2, T)
