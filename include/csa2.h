@@ -470,7 +470,10 @@ typedef struct {
  * weights,
  *   mass[s, idx[b, j]] += rint(weights[b, j] * 2^32)
  * in integers, so that the sums depend on no order and lose nothing over long
- * runs.  Entries with idx < 0 add nothing; a weight that is not in
+ * runs.  A mass stops at 2^63 - 1, a weight of 2^31 in all, and does not wrap
+ * (64 heads of 20 layers that give one entry all their weight reach it in 1.7
+ * million tokens); entries that stand there tie in csa2_kv_evict, so a caller
+ * whose runs are longer scales its masses down in time.  Entries with idx < 0 add nothing; a weight that is not in
  * [0, 2^20] is recorded (bad weight, bit 4 of the error word) and adds
  * nothing, an idx >= N is recorded and skipped.  A path id outside 0..T-1 is
  * recorded (bad index) and ends the path before it.

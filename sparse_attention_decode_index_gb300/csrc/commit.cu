@@ -11,13 +11,15 @@
 // which nobody writes, so no barrier holds them, and a sequence with a long
 // path has as many of them at work as it needs (paths differ: the weights in
 // the clusters, 8 CTAs of 512 threads a sequence, took 18.2 us for 64 sequences of 16
-// tokens and 20 layers where this takes 11.5; one sequence, 8 tokens, 4 layers: 3.7 and 2.5).
-// Bound by the latency of path, idx and weight behind each other, and for that case
-// by the reads of 24 MB of idx and weights (with the windows 5.2 us at HBM's rate);
-// without the atomics, or without the copies, it is 0.3 and 0.9 us faster.
+// tokens and 20 layers where these took 11.5, both with atomics that return nothing).
+// That case takes 14.5 us, one sequence of 8 tokens and 4 layers 2.8.  Bound by the
+// latency of path, idx and weight behind each other, by the reads of 24 MB of idx and
+// weights (with the windows 5.2 us at HBM's rate) and by the atomics' old values, which
+// come back for the check of the range: 3.0 and 0.4 us of the two.  (Loads of the masses
+// behind or in front of atomics that return nothing cost 2 us more than that.)
 // The mass is a 64-bit integer in units of 2^-32: integer sums depend on no
 // order, so neither the atomics nor the merging change them, and they stay
-// exact where fp32 sums would stop growing.  A weight is split into its whole
+// exact where fp32 sums would stop growing; they end at 2^63 - 1.  A weight is split into its whole
 // part and the rest, which is exact, and the rest rounded once.
 //
 // Like the cache-maintenance kernels it lets no later launch start early: the
@@ -29,12 +31,13 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kThreads = 128;              // (256: 13.2 us, 64: 15.3, where 128 take 11.5)
+constexpr int kThreads = 128;              // (256: 13.2 us, 64: 15.3, where 128 took 11.5)
 static_assert(kThreads >= kMaxTreeTokens, "a thread for every token of a path");
 constexpr int kCopies = 4;                // row units a thread has in flight
 constexpr int kBatch = 8;                 // layers of an item of the mass, their idx and weights in flight together
 constexpr float kMaxWeight = 1048576.f;   // 2^20
-constexpr int kMassCtas = 16;             // CTAs of the mass for every SM at most (24: 11.9 us, 8 to 16: 11.5)
+constexpr long long kMostMass = 0x7fffffffffffffffll;
+constexpr int kMassCtas = 16;             // CTAs of the mass for every SM at most (24 took 11.9 us, 8 to 16 11.5)
 
 // The path's rows [j0, n) into the rings of layers rank, rank + ncta, ...: all
 // the units of all these rows are one list, so that a thread waits for its
@@ -64,6 +67,16 @@ CSA2_DEV void copy_rows(const TreeCommitArgs& a, int rank, int ncta, long long r
     for (int m = 0; m < kCopies; ++m)
       if (i0 + m * kThreads < total) *to[m] = w[m];
   }
+}
+
+// mass += sum, up to 2^63 - 1 and no further.  Sums here are not negative, so a
+// sum that leaves the range passes 2^63 in exactly one addition, whose own old value shows
+// it; that thread puts the maximum in its place, and so does any that passes it
+// again behind that.  What is left is min(true sum, 2^63 - 1), whatever the order.
+CSA2_DEV void add_mass(unsigned long long* mass, unsigned long long sum) {
+  const unsigned long long old = atomicAdd(mass, sum);
+  if (static_cast<long long>(old) >= 0 && static_cast<long long>(old + sum) < 0)
+    atomicMax(reinterpret_cast<long long*>(mass), kMostMass);
 }
 
 // The accepted path of a sequence into `path` (shared memory); its length, a bad id ending it.
@@ -140,14 +153,14 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const __grid_cons
         continue;
       }
       if (e[m] != cur) {
-        if (sum != 0) atomicAdd(mass + cur, sum);
+        if (sum != 0) add_mass(mass + cur, sum);
         cur = e[m];
         sum = 0;
       }
       const uint32_t whole = __float2uint_rd(w[m]);
       sum += ((unsigned long long)whole << 32) + __float2uint_rn((w[m] - float(whole)) * 4294967296.f);
     }
-    if (sum != 0) atomicAdd(mass + cur, sum);
+    if (sum != 0) add_mass(mass + cur, sum);
     if (bad != 0) report(a.err, bad, detail);
   }
 }

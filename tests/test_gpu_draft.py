@@ -676,6 +676,41 @@ def test_tree_commit_rounds_weights_once(csa2):
     assert torch.equal(d.mass.cpu(), torch.as_tensor(want[2]))
 
 
+def test_tree_commit_saturates_the_mass(csa2):
+    """A mass ends at 2^63 - 1 and does not wrap: sums that end below, at and beyond it, by one weight and by many, from
+    masses that are great, small and below zero, and the eviction that follows keeps such an entry."""
+    S, T, L, N, K, W = 2, 128, 9, 12, 10, 4
+    d = commit_inputs(S, T, L, N, K, W, 16, 8, "bf16", 12)
+    most, unit = 2 ** 63 - 1, 2 ** 32
+    d.n_path.copy_(i32([1, 128]))
+    d.path.copy_(i32(np.tile(np.arange(T), (S, 1))))
+    d.idx.copy_(torch.arange(K, dtype=torch.int32, device="cuda").expand_as(d.idx))
+    d.w.fill_(1.0)                                         # 9 units in sequence 0, 1,152 in sequence 1
+    d.w[:, T:, 7] = 2.0 ** 20                              # 1,152 * 2^52: past 2^62, not 2^63
+    d.w[:, T:, 8] = 2.0 ** 20
+    for s, n in ((0, 9), (1, 1152)):
+        d.mass[s] = torch.tensor([most, most - n * unit, most - n * unit + 1, most - n * unit - 1, most - unit, -2 ** 63, -5, 0,
+                                  2 ** 62, 3, most, 0])
+    before = d.mass.cpu().numpy().copy()
+    ws = csa2.workspace(d.sh)
+    csa2.tree_commit(d.sh, [(d.kd[l], d.vd[l], d.ks[l], d.vs[l], d.idx[l], d.w[l]) for l in range(L)], d.path, d.n_path, d.head,
+                     d.n_swa, ws, mass=d.mass)
+    assert_no_device_error(csa2, ws)
+    for s, n in ((0, 9), (1, 1152)):
+        add = [n * unit] * K + [0, 0]
+        if s == 1:
+            add[7] = add[8] = n * 2 ** 52
+        assert d.mass[s].tolist() == [min(int(b) + a, most) for b, a in zip(before[s], add)], s
+    sh = shape(S, n_entries=N, k_dim=16, v_dim=8, idx_dim=8)
+    k, v, x = (torch.zeros((S, N, z), dtype=torch.bfloat16, device="cuda") for z in (16, 8, 8))
+    kept, n_valid = torch.empty((S, N), dtype=torch.int32, device="cuda"), i32([N, N])
+    mass = d.mass.cpu().numpy()
+    csa2.kv_evict(sh, 4, 4, 0, 0, k, v, x, d.mass, n_valid, kept, None)
+    for s in range(S):
+        assert kept[s, :4].tolist() == R.evict(N, 4, 4, 0, 0, mass[s])
+        assert 0 in kept[s, :4].tolist()                   # the greatest before the commit still is
+
+
 # ------------------------------------------------------------------ eviction
 
 def evict_inputs(S, N, dk, dv, dI, block, dtype, seed, kind, n_valid=None):
