@@ -364,7 +364,8 @@ int csa2_merge_attn(int32_t parts, int32_t rows, int32_t v_dim, const float* out
  * neither drafting nor eviction; these calls keep the method's own definitions
  * (bullet "Sparse attention": selected entries plus the last W tokens) and
  * bookkeeping.  Their kernels read nothing before the preceding kernel of the
- * stream has completed. */
+ * stream has completed.  No array of theirs may lie in the ws_bytes of the call's
+ * ws (refused). */
 
 /* Frequencies of rotary positions, in radians per position, for rot_dim / 2
  * pairs (host only; the caller copies them to the device once).  With
@@ -444,7 +445,7 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
  * nothing.  live[b] = 0 leaves the query out: its weights are written as 0
  * and nothing of it is read (NULL: all are wanted).
  *   q [B, H, dk]  k_main [B / T, N, dk]  idx [B, K]  lse [B, H]  live [B]
- *   weights [B, K] fp32 (overlaps nothing that is read: refused)
+ *   weights [B, K] fp32 (overlaps nothing else: refused)
  * batch <= 65,535. */
 int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main, const int32_t* idx, const float* lse,
                       const int32_t* live, float* weights, void* ws, size_t ws_bytes, csa2_stream_t stream);

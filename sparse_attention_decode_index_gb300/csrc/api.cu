@@ -828,7 +828,8 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
   Span spans[] = {{q, B * s.q_heads * kb, false}, {k_main, S * s.n_entries * kb, false}, {v_main, S * s.n_entries * vb, false},
                   {idx, B * s.topk * 4, false}, {k_swa, S * s.swa * kb, false}, {v_swa, S * s.swa * vb, false},
                   {swa_head, S * 4, false}, {n_swa, S * 4, false}, {k_draft, B * kb, false}, {v_draft, B * vb, false},
-                  {parent, B * 4, false}, {n_draft, S * 4, false}, {out, B * s.q_heads * vb, true}, {lse, B * s.q_heads * 4, true}};
+                  {parent, B * 4, false}, {n_draft, S * 4, false}, {out, B * s.q_heads * vb, true}, {lse, B * s.q_heads * 4, true},
+                  {ws, ws_bytes, true}};
   if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
   TreeArgs a{};
   a.q = q;
@@ -872,7 +873,7 @@ int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main
   if (fast && (!aligned16(q) || !aligned16(k_main))) return CSA2_ERR_INVALID_ARG;
   const uint64_t B = s.batch, kb = uint64_t(s.k_dim) * (s.dtype == CSA2_F32 ? 4 : 2);
   Span spans[] = {{q, B * s.q_heads * kb, false}, {k_main, B / seqdiv(s) * s.n_entries * kb, false}, {idx, B * s.topk * 4, false},
-                  {lse, B * s.q_heads * 4, false}, {live, B * 4, false}, {weights, B * s.topk * 4, true}};
+                  {lse, B * s.q_heads * 4, false}, {live, B * 4, false}, {weights, B * s.topk * 4, true}, {ws, ws_bytes, true}};
   if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
   AttnWeightsArgs a{};
   a.q = q;
@@ -910,9 +911,9 @@ int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int3
   a.v_bytes = s.v_dim * esize;
   a.wide = a.k_bytes % 16 == 0 && a.v_bytes % 16 == 0;
   const uint64_t nb = uint64_t(s.batch) * 4, sb = uint64_t(S) * 4;
-  Span spans[5 + 6 * kMaxTreeLayers] = {{path, nb, false}, {n_path, sb, false}, {swa_head, sb, true}, {n_swa, sb, true},
-                                        {mass, uint64_t(S) * s.n_entries * 8, true}};
-  int n_spans = 5;
+  Span spans[6 + 6 * kMaxTreeLayers] = {{path, nb, false}, {n_path, sb, false}, {swa_head, sb, true}, {n_swa, sb, true},
+                                        {mass, uint64_t(S) * s.n_entries * 8, true}, {ws, ws_bytes, true}};
+  int n_spans = 6;
   for (int l = 0; l < n_layers; ++l) {
     const csa2_tree_slot& y = layers[l];
     if (y.k_draft == nullptr || y.v_draft == nullptr || y.k_swa == nullptr || y.v_swa == nullptr)
@@ -984,6 +985,12 @@ int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_
   if (kb_out != nullptr && overlap(kept, extra[0].bytes, kb_out, extra[1].bytes)) return CSA2_ERR_INVALID_ARG;
   int* err = nullptr;
   CSA2_TRY(error_word(s, ws, ws_bytes, &err));
+  if (ws != nullptr) {
+    for (const Pair& x : io)
+      if (overlap(x.in, x.bytes, ws, ws_bytes) || overlap(x.out, x.bytes, ws, ws_bytes)) return CSA2_ERR_INVALID_ARG;
+    for (const Pair& x : extra)
+      if (x.out != nullptr && overlap(x.out, x.bytes, ws, ws_bytes)) return CSA2_ERR_INVALID_ARG;
+  }
   EvictArgs a{};
   a.k_main = k_main;
   a.v_main = v_main;

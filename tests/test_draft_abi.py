@@ -163,6 +163,43 @@ def test_outputs_over_other_arrays_are_refused(csa2):
             assert commit([one, two], *rest[:i], p, *rest[i + 1:]) == INVALID, (i, p)
 
 
+def test_arrays_in_the_workspace_are_refused(csa2):
+    """The workspace is written (its error word, the key lists of trees), so that no array of a call may share a byte with it:
+    not its first, not its last."""
+    lib = csa2.lib()
+    s, one = _shape(csa2), _shape(csa2, tokens=1)
+    n, n1, ws = _ws(csa2, s), _ws(csa2, one), FAKE - STEP
+    names = ("q", "k_main", "v_main", "idx", "k_swa", "v_swa", "swa_head", "n_swa", "k_draft", "v_draft", "parent", "n_draft", "out",
+             "lse")
+    for x in names:
+        for p in (ws, ws + n - 16, ws - 16):               # (every array is longer than 16 bytes or starts inside)
+            if p < ws and x in ("swa_head", "n_swa", "n_draft"):
+                p = ws - 4
+            assert lib.csa2_tree_attn(ctypes.byref(s), *_tree_args(**{x: p}), ws, n, None) == INVALID, (x, p)
+    keys = ("q", "k_main", "idx", "lse", "live", "weights")
+    for x in keys:
+        for p in (ws, ws + n - 16, ws - 16):
+            d = {y: FAKE + i * STEP for i, y in enumerate(keys)}
+            d[x] = p
+            assert lib.csa2_attn_weights(ctypes.byref(s), *d.values(), ws, n, None) == INVALID, (x, p)
+    far = [FAKE + i * STEP for i in range(20)]
+    for i in range(11):
+        for p in (ws, ws + n - 16, ws - 4):
+            at = far[:i] + [p] + far[i + 1:]
+            arr = (csa2.CTreeSlot * 1)(csa2.CTreeSlot(*at[:6]))
+            rest = at[6:11]
+            if i == 10 and p == ws - 4:
+                continue                                   # (masses are 8 bytes apart)
+            assert lib.csa2_tree_commit(ctypes.byref(s), ctypes.cast(arr, ctypes.c_void_p), 1, *rest, ws, n, None) == INVALID, (i, p)
+    for i in range(12):
+        for p in (ws, ws + n1 - 16, ws - 16):
+            at = far[:i] + [p] + far[i + 1:12]
+            assert lib.csa2_kv_evict(ctypes.byref(one), 4000, 3000, 4, 64, *at, 1, ws, n1, None) == INVALID, (i, p)
+    for i in range(5):                                     # in place
+        at = far[:i] + [ws] + far[i + 1:5]
+        assert lib.csa2_kv_evict(ctypes.byref(one), 4000, 3000, 4, 64, *at, *at, *far[10:12], 1, ws, n1, None) == INVALID, i
+
+
 def test_workspace_holds_the_key_lists_of_trees(csa2):
     """Short caches with long lists: the workspace grows by the lists of csa2_tree_attn; fp32 and long caches keep theirs."""
     small = _shape(csa2, batch=208, tokens=16, n_entries=57, topk=512, swa=128)
