@@ -365,7 +365,7 @@ int csa2_merge_attn(int32_t parts, int32_t rows, int32_t v_dim, const float* out
  * (bullet "Sparse attention": selected entries plus the last W tokens) and
  * bookkeeping.  Their kernels read nothing before the preceding kernel of the
  * stream has completed.  No array of theirs may lie in the ws_bytes of the call's
- * ws (refused). */
+ * ws, and each begins at a multiple of its elements' size (refused). */
 
 /* Frequencies of rotary positions, in radians per position, for rot_dim / 2
  * pairs (host only; the caller copies them to the device once).  With

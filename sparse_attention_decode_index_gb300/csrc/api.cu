@@ -107,6 +107,16 @@ T* at(void* ws, size_t off) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
+// Whether every pointer is a multiple of `bytes` (a power of two; null is).
+template <class... P>
+bool aligned(size_t bytes, P... p) {
+  uintptr_t at = 0;
+  for (const void* x : {static_cast<const void*>(p)...}) at |= reinterpret_cast<uintptr_t>(x);
+  return (at & (bytes - 1)) == 0;
+}
+
+size_t elem_size(int dtype) { return dtype == CSA2_F32 ? 4 : 2; }
+
 int check_shape(const csa2_shape* s) {
   if (s == nullptr) return CSA2_ERR_INVALID_ARG;
   if (s->batch < 1 || s->n_entries < 1 || s->idx_heads < 1 || s->idx_dim < 1 || s->block < 1 ||
@@ -768,7 +778,7 @@ int csa2_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor
 int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,
               const int32_t* pos, const double* freqs, float mag, int32_t inverse, csa2_stream_t stream) {
   if (slots == nullptr || n_slots < 1 || n_slots > kMaxRopeSlots || rows < 1) return CSA2_ERR_INVALID_ARG;
-  if (rot_dim < 2 || rot_dim % 2 != 0 || pos == nullptr || freqs == nullptr || !aligned8(freqs))
+  if (rot_dim < 2 || rot_dim % 2 != 0 || pos == nullptr || freqs == nullptr || !aligned(4, pos) || !aligned8(freqs))
     return CSA2_ERR_INVALID_ARG;
   if (rot_dim > kMaxRotDim) return CSA2_ERR_UNSUPPORTED;
   if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1)) return CSA2_ERR_INVALID_ARG;
@@ -779,6 +789,7 @@ int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_
     if (y.x == nullptr || y.out == nullptr || y.heads < 1 || y.dim < 1 || y.rot_off < 0) return CSA2_ERR_INVALID_ARG;
     if (int64_t(y.rot_off) + rot_dim > y.dim) return CSA2_ERR_INVALID_ARG;
     if (y.dtype != CSA2_BF16 && y.dtype != CSA2_F32) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(elem_size(y.dtype), y.x, y.out)) return CSA2_ERR_INVALID_ARG;
     if (y.heads > 1024 || y.dim > 1024) return CSA2_ERR_UNSUPPORTED;
     a.slot[k].x = y.x;
     a.slot[k].out = y.out;
@@ -823,6 +834,9 @@ int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, c
   if (attn_fast(s))
     for (const void* p : {q, k_main, v_main, k_swa, v_swa, k_draft, v_draft, static_cast<const void*>(out)})
       if (!aligned16(p)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned(elem_size(s.dtype), q, k_main, v_main, k_swa, v_swa, k_draft, v_draft, out) ||
+      !aligned(4, idx, swa_head, n_swa, parent, n_draft, lse))
+    return CSA2_ERR_INVALID_ARG;
   const uint64_t B = s.batch, S = B / seqdiv(s), esize = s.dtype == CSA2_F32 ? 4 : 2;
   const uint64_t kb = s.k_dim * esize, vb = s.v_dim * esize;
   Span spans[] = {{q, B * s.q_heads * kb, false}, {k_main, S * s.n_entries * kb, false}, {v_main, S * s.n_entries * vb, false},
@@ -871,6 +885,7 @@ int csa2_attn_weights(const csa2_shape* shape, const void* q, const void* k_main
     return CSA2_ERR_INVALID_ARG;
   const bool fast = s.dtype == CSA2_BF16 && s.q_heads == 64 && s.k_dim == 192;
   if (fast && (!aligned16(q) || !aligned16(k_main))) return CSA2_ERR_INVALID_ARG;
+  if (!aligned(elem_size(s.dtype), q, k_main) || !aligned(4, idx, lse, live, weights)) return CSA2_ERR_INVALID_ARG;
   const uint64_t B = s.batch, kb = uint64_t(s.k_dim) * (s.dtype == CSA2_F32 ? 4 : 2);
   Span spans[] = {{q, B * s.q_heads * kb, false}, {k_main, B / seqdiv(s) * s.n_entries * kb, false}, {idx, B * s.topk * 4, false},
                   {lse, B * s.q_heads * 4, false}, {live, B * 4, false}, {weights, B * s.topk * 4, true}, {ws, ws_bytes, true}};
@@ -900,7 +915,7 @@ int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int3
   const csa2_shape& s = *shape;
   if (s.swa < 1 || layers == nullptr || n_layers < 1 || n_layers > kMaxTreeLayers) return CSA2_ERR_INVALID_ARG;
   if (path == nullptr || n_path == nullptr || swa_head == nullptr || n_swa == nullptr) return CSA2_ERR_INVALID_ARG;
-  if (!aligned8(mass)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned8(mass) || !aligned(4, path, n_path, swa_head, n_swa)) return CSA2_ERR_INVALID_ARG;
   const int T = seqdiv(s), S = s.batch / T;
   if (T > kMaxTreeTokens || S > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
   int* err = nullptr;
@@ -919,6 +934,8 @@ int csa2_tree_commit(const csa2_shape* shape, const csa2_tree_slot* layers, int3
     if (y.k_draft == nullptr || y.v_draft == nullptr || y.k_swa == nullptr || y.v_swa == nullptr)
       return CSA2_ERR_INVALID_ARG;
     if ((y.idx == nullptr) != (y.weights == nullptr)) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(elem_size(s.dtype), y.k_draft, y.v_draft, y.k_swa, y.v_swa) || !aligned(4, y.idx, y.weights))
+      return CSA2_ERR_INVALID_ARG;
     if (!aligned16(y.k_draft) || !aligned16(y.v_draft) || !aligned16(y.k_swa) || !aligned16(y.v_swa)) a.wide = 0;
     a.slot[l] = TreeCommitArgs::Slot{y.k_draft, y.v_draft, y.k_swa, y.v_swa, y.idx, y.weights};
     for (const Span& x : {Span{y.k_draft, uint64_t(s.batch) * a.k_bytes, false}, Span{y.v_draft, uint64_t(s.batch) * a.v_bytes, false},
@@ -966,6 +983,9 @@ int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_
                       {n_valid, n_valid_out, B * 4}};
   const Pair extra[2] = {{nullptr, kept, B * N * 4}, {nullptr, kb_out, B * nb * s.idx_dim * esize}};
   if (kept == nullptr || !aligned8(mass) || !aligned8(mass_out)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned(size_t(esize), k_main, v_main, k_idx, k_main_out, v_main_out, k_idx_out, kb_out) ||
+      !aligned(4, n_valid, n_valid_out, kept))
+    return CSA2_ERR_INVALID_ARG;
   int same = 0;
   for (const Pair& x : io) {
     if (x.in == nullptr || x.out == nullptr) return CSA2_ERR_INVALID_ARG;

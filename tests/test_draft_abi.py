@@ -200,6 +200,37 @@ def test_arrays_in_the_workspace_are_refused(csa2):
         assert lib.csa2_kv_evict(ctypes.byref(one), 4000, 3000, 4, 64, *at, *at, *far[10:12], 1, ws, n1, None) == INVALID, i
 
 
+@pytest.mark.parametrize("dtype,heads,dk", [("bf16", 64, 192), ("bf16", 5, 7), ("f32", 5, 7)])
+def test_arrays_between_elements_are_refused(csa2, dtype, heads, dk):
+    """An array that does not begin at a multiple of its elements' size would fault the kernel."""
+    lib = csa2.lib()
+    e = 4 if dtype == "f32" else 2
+    kw = dict(dtype=dtype, q_heads=heads, k_dim=dk, v_dim=128 if heads == 64 else 9, swa=128)
+    s, one = _shape(csa2, **kw), _shape(csa2, tokens=1, **kw)
+    n, n1, ws = _ws(csa2, s), _ws(csa2, one), FAKE - STEP
+    elems = ("q", "k_main", "v_main", "k_swa", "v_swa", "k_draft", "v_draft", "out")
+    for i, x in enumerate(("q", "k_main", "v_main", "idx", "k_swa", "v_swa", "swa_head", "n_swa", "k_draft", "v_draft", "parent",
+                           "n_draft", "out", "lse")):
+        for off in ((e // 2,) if x in elems else (1, 2)):
+            assert lib.csa2_tree_attn(ctypes.byref(s), *_tree_args(**{x: FAKE + i * STEP + off}), ws, n, None) == INVALID, x
+    far = [FAKE + i * STEP for i in range(20)]
+    for i in range(6):
+        at = far[:i] + [far[i] + (e // 2 if i < 2 else 2)] + far[i + 1:6]
+        assert lib.csa2_attn_weights(ctypes.byref(s), *at, ws, n, None) == INVALID, i
+    for i in range(11):                                    # k_draft, v_draft, k_swa, v_swa, idx, weights, path, n_path, head, n_swa, mass
+        at = far[:i] + [far[i] + (e // 2 if i < 4 else 4 if i == 10 else 2)] + far[i + 1:11]
+        arr = (csa2.CTreeSlot * 1)(csa2.CTreeSlot(*at[:6]))
+        assert lib.csa2_tree_commit(ctypes.byref(s), ctypes.cast(arr, ctypes.c_void_p), 1, *at[6:], ws, n, None) == INVALID, i
+    for i in range(12):                                    # k, v, x, mass, n, the same behind, kept, kb
+        off = 4 if i in (3, 8) else 2 if i in (4, 9, 10) else e // 2
+        at = far[:i] + [far[i] + off] + far[i + 1:12]
+        assert lib.csa2_kv_evict(ctypes.byref(one), 4000, 3000, 4, 64, *at, 1, ws, n1, None) == INVALID, i
+    for i in range(4):                                     # x, out, pos, freqs
+        at = far[:i] + [far[i] + (e // 2 if i < 2 else 2)] + far[i + 1:4]
+        arr = (csa2.CRopeSlot * 1)(csa2.CRopeSlot(at[0], at[1], 3, 16, 0, 1 if dtype == "f32" else 0))
+        assert lib.csa2_rope(ctypes.cast(arr, ctypes.c_void_p), 1, 4, 8, 0, at[2], at[3], 1.0, 0, None) == INVALID, i
+
+
 def test_workspace_holds_the_key_lists_of_trees(csa2):
     """Short caches with long lists: the workspace grows by the lists of csa2_tree_attn; fp32 and long caches keep theirs."""
     small = _shape(csa2, batch=208, tokens=16, n_entries=57, topk=512, swa=128)
