@@ -45,8 +45,9 @@
 // P is rounded to bf16 (half a step, 2^-8 of a weight), which the tensor core
 // asks for; the sums of the weights stay fp32 and unrounded.
 // A V row that holds an infinity or NaN for one token must not reach another
-// that masks it (0 * inf): rows of O that are not finite are computed again
-// from their own keys.
+// that masks it (0 * inf): rows of O that are not finite though their sum is a number are computed again
+// from their own keys (32 trees of 16 with infinities in every row: 5.6 ms, a warp's 32
+// rows one after the other; NaN scores make no such rows and cost nothing).
 #include "common.cuh"
 #include "draft.h"
 #include "tc.cuh"
@@ -345,25 +346,52 @@ CSA2_DEV void cp16(uint32_t dst, uint64_t src, int offset, const void* any) {   
 }
 
 // One row of O from its own keys alone, by a warp: lane l ends with columns 4 l .. 4 l + 3, unscaled by 1 / l.
+// 32 keys at a time: a lane scores one of them, then all lanes add up the values of those that the token has, 8
+// rows on their way.
 __device__ __noinline__ float4 row_alone(const TreeArgs& a, int seq, int query, int head, int token, const uint32_t* list, int n_main, int n_ring,
                           int n_all, float sl2, float base) {
   const int lane = threadIdx.x & 31;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((long long)query * kH + head) * kDk;
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + ((long long)query * kH + head) * kDk);
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < n_all; ++p) {
-    const Key y = resolve(a, seq, p, list[p], n_main, n_ring, n_all);
-    if (!((y.mask >> token) & 1u)) continue;
-    const __nv_bfloat16* k = reinterpret_cast<const __nv_bfloat16*>(y.k);
-    float s = 0.f;
+  for (int p0 = 0; p0 < n_all; p0 += 32) {
+    const int p = p0 + lane;
+    const Key y = resolve(a, seq, p, p < n_all ? list[p] : 0, n_main, n_ring, n_all);
+    const bool has = ((y.mask >> token) & 1u) != 0;
+    float w = 0.f;
+    if (has) {
+      const uint4* k = reinterpret_cast<const uint4*>(y.k);
+      float s = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < kDk / 8; ++d) {
+        const uint4 u = q[d], v = k[d];
+        const uint32_t us[4] = {u.x, u.y, u.z, u.w}, vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int d = 0; d < kDk / 32; ++d) s = __fmaf_rn(__bfloat162float(q[d * 32 + lane]), __bfloat162float(k[d * 32 + lane]), s);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    const float w = ex2(__fmaf_rn(s, sl2, -base));
-    const uint2 v = reinterpret_cast<const uint2*>(y.v)[lane];
-    o.x = __fmaf_rn(w, __uint_as_float(v.x << 16), o.x);
-    o.y = __fmaf_rn(w, __uint_as_float(v.x & 0xffff0000u), o.y);
-    o.z = __fmaf_rn(w, __uint_as_float(v.y << 16), o.z);
-    o.w = __fmaf_rn(w, __uint_as_float(v.y & 0xffff0000u), o.w);
+        for (int e = 0; e < 4; ++e) {
+          s = __fmaf_rn(__uint_as_float(us[e] << 16), __uint_as_float(vs[e] << 16), s);
+          s = __fmaf_rn(__uint_as_float(us[e] & 0xffff0000u), __uint_as_float(vs[e] & 0xffff0000u), s);
+        }
+      }
+      w = ex2(__fmaf_rn(s, sl2, -base));
+    }
+    __syncwarp();
+    const unsigned keys = __ballot_sync(0xffffffffu, has);
+    for (int j0 = 0; j0 < 32; j0 += 8) {
+      if (((keys >> j0) & 0xffu) == 0) continue;
+      uint2 v[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const uint64_t at = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(y.v), j0 + x);
+        v[x] = (keys >> (j0 + x)) & 1u ? reinterpret_cast<const uint2*>(at)[lane] : make_uint2(0u, 0u);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const float z = __shfl_sync(0xffffffffu, w, j0 + x);   // 0 where the token has no such key, as v is
+        o.x = __fmaf_rn(z, __uint_as_float(v[x].x << 16), o.x);
+        o.y = __fmaf_rn(z, __uint_as_float(v[x].x & 0xffff0000u), o.y);
+        o.z = __fmaf_rn(z, __uint_as_float(v[x].y << 16), o.z);
+        o.w = __fmaf_rn(z, __uint_as_float(v[x].y & 0xffff0000u), o.w);
+      }
+    }
   }
   return o;
 }
@@ -633,8 +661,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&c.o_free[items & 1]);
       ++items;
       if (query >= 0 && lse != nullptr) *lse = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-      // rows that are not finite: from their own keys, so that no other token's values reach them
-      unsigned again = __ballot_sync(0xffffffffu, bad);
+      // rows that are not finite: from their own keys, so that no other token's values reach them (one whose sum is
+      // NaN is NaN whatever they hold)
+      unsigned again = __ballot_sync(0xffffffffu, bad && inv == inv);
       while (again != 0) {
         const int l = __ffs(again) - 1;
         again &= again - 1;
