@@ -372,7 +372,7 @@ int csa2_merge_attn(int32_t parts, int32_t rows, int32_t v_dim, const float* out
  * f_i = base^(-2i / rot_dim):
  *   CSA2_ROPE_PLAIN   f_i
  *   CSA2_ROPE_LINEAR  f_i / factor
- *   CSA2_ROPE_NTK     as PLAIN with base * factor^(rot_dim / (rot_dim - 2)), rot_dim > 2
+ *   CSA2_ROPE_NTK     as PLAIN with base * factor^(rot_dim / (rot_dim - 2)), rot_dim > 2; refused where that is not finite
  *   CSA2_ROPE_YARN    pairs that turn more than beta_fast times over orig_ctx positions keep f_i, pairs that turn less than
  *                     beta_slow times get f_i / factor, a linear ramp over the pairs between them; the magnitude is
  *                     0.1 ln(factor) + 1

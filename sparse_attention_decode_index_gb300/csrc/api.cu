@@ -754,6 +754,7 @@ int csa2_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor
       (orig_ctx < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow) || !std::isfinite(beta_fast)))
     return CSA2_ERR_INVALID_ARG;
   const double b = scaling == CSA2_ROPE_NTK ? base * std::pow(factor, double(rot_dim) / (rot_dim - 2)) : base;
+  if (!std::isfinite(b)) return CSA2_ERR_INVALID_ARG;   // (its pairs would not turn at all)
   // the (real-valued) pair that turns `turns` times over orig_ctx positions
   const double two_pi = 6.283185307179586476925286766559;
   auto pair_of = [&](double turns) { return rot_dim * std::log(orig_ctx / (turns * two_pi)) / (2.0 * std::log(base)); };

@@ -69,6 +69,16 @@ def test_rope_freqs(csa2):
     assert all(buf[i] > buf[i + 1] for i in range(31))
 
 
+def test_rope_freqs_of_a_base_that_overflows(csa2):
+    """An NTK base beyond doubles (10000 * 1e160^2) would leave every pair but the first unturned."""
+    lib = csa2.lib()
+    buf, mag = (ctypes.c_double * 2)(), ctypes.c_float(0)
+    args = (4, 10000.0, 2), (0, 32.0, 1.0, ctypes.cast(buf, ctypes.c_void_p), ctypes.byref(mag))
+    assert lib.csa2_rope_freqs(*args[0], 1e160, *args[1]) == INVALID
+    assert lib.csa2_rope_freqs(*args[0], 1e150, *args[1]) == OK
+    assert list(buf) == pytest.approx([1.0, 1e-152], rel=1e-12)
+
+
 def test_rope_refusals(csa2):
     lib = csa2.lib()
     good = dict(x=FAKE, out=FAKE + STEP, heads=64, dim=192, rot_off=128, dtype=0)
