@@ -303,6 +303,34 @@ def test_tree_paths_of_every_length(csa2, kind, T, W):
     check_tree(sh, d)
 
 
+@pytest.mark.parametrize("kind,T,W", [(k, *x) for k, longest in (("clusters", 88), ("alone", 128), ("pairs", 128), ("rows", 128), ("generic", 128))
+                                      for x in ((longest, 128), (longest - 1, 40), (65, 70), (33, 1), (2, 3))])
+def test_tree_long_paths_in_the_kernel_of_each_kind(csa2, kind, T, W):
+    """A chain given by its parents, a long branch with leaves and a parent that is not an earlier token, each alone in a call,
+    in the kernel that is named: so few queries that every one has a cluster or an SM, or so many that they go in pairs.
+    Clusters take 385 slots and more (three CTAs a query: up to 88 queries of 152 SMs), as one launch; plan and attention are two."""
+    kw, _ = KINDS[kind]
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    S = -(-(sms + 1) // T) if kind == "pairs" else 1
+    assert kind != "clusters" or 8 * T * 3 <= 14 * sms
+    sh = shape(S * T, tokens=T, n_entries=60, topk=12, swa=W, **{**kw, "pad": 400 - W if kind == "clusters" else 0})
+    d = tree_inputs(sh, T)
+    chain = np.arange(T) - 1
+    branch = np.where(np.arange(T) % 3 == 2, np.arange(T) - 2, np.arange(T) - 1)
+    cut = chain.copy()
+    cut[T // 2] = -1
+    for given, means in ((chain, chain), (branch, branch), (np.where(cut == chain, chain, T // 2 + 5), cut)):
+        d.parent.copy_(i32(np.tile(given, (S, 1))))
+        before = csa2.launch_count()
+        ws = run_tree(csa2, sh, d)
+        assert csa2.launch_count() - before == (2 if kind in ("alone", "pairs") else 1)
+        if given is means:
+            assert_no_device_error(csa2, ws)
+        else:
+            assert csa2.read_device_error(ws) == (-5, BAD_INDEX)
+        check_tree(sh, d, parent=np.tile(means, (S, 1)))
+
+
 @pytest.mark.parametrize("kind", list(KINDS))
 def test_tree_rows_without_keys_and_dead_tokens(csa2, kind):
     T = 6
