@@ -398,8 +398,9 @@ typedef struct {
  *   mag * (a cos t - b sin t, b cos t + a sin t),  t = pos[r] * freqs[i];
  * inverse = 1 turns back: the angle is -t and the magnitude 1 / mag.
  * Pairs are dims (i, i + rot_dim / 2) of the turned range, or (2i, 2i + 1)
- * when interleaved = 1.  The angle is reduced exactly for any int32 position
- * (fixed-point turns), the arithmetic is fp32, rounded once.
+ * when interleaved = 1.  The angle is reduced in fixed-point turns, off by at
+ * most |t| 2^-52 + |pos| 2 pi 2^-65 + 2 pi 2^-26 for any int32 position; the
+ * arithmetic is fp32, rounded once.
  *   pos [rows] int32   freqs [rot_dim / 2] double (device)
  * rows >= 1; 1 <= n_slots <= 16; mag finite and > 0. */
 int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,

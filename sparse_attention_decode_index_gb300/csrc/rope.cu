@@ -8,9 +8,10 @@
 // have several angles each): a 64-bit fixed-point fraction F = freq / 2 pi mod
 // 1 in units of 2^-64.  pos * F modulo 2^64 is then the exact angle of F in
 // turns, whatever whole turns it passes, and its top bits, read as a signed
-// number, lie in [-1/2, 1/2) turns.  F is rounded from fp64, so the angle is
-// off by at most |t| 2^-52 for any int32 position, and sincospif takes the
-// reduced angle in half turns.
+// number, lie in [-1/2, 1/2) turns.  F is rounded from fp64 to whole units, and
+// the reduced angle to fp32, which sincospif takes in half turns: the angle is
+// off by at most |t| 2^-52 + |pos| 2 pi 2^-65 + 2 pi 2^-26 for any int32 position
+// (the last term, 9.4e-8, for all but those beyond a few hundred million radians).
 //
 // Memory bound: every element is read once and written once.  A block takes
 // up to 8 rows, or 64 small ones, and makes all their cos and sin at once (kept

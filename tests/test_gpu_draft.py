@@ -84,6 +84,27 @@ def test_rope_matches_definition(csa2, dtype, inter, rows, heads, dim, rot, off,
         assert np.all(err <= lim), float((err - lim).max())
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("base,scaling,factor", [(10000.0, "plain", 1.0), (1e8, "plain", 1.0), (10000.0, "yarn", 40.0), (500000.0, "linear", 8.0)])
+def test_rope_angles_of_every_position(csa2, base, scaling, factor, inter):
+    """cos and sin of each position to its own bound: a frequency is rounded to 2^-52 of it and to 2^-65 turns, the reduced angle
+    to fp32 (2^-26 turns); their own errors are 2 steps, and two products are rounded."""
+    rot = 64
+    pos = np.array([0, 1, -1, 2, 7, 100, -4095, 32767, 10 ** 5, 2 ** 20, -(2 ** 24) - 1, 10 ** 9, 2 ** 31 - 1, -2 ** 31])
+    freqs, mag = csa2.rope_freqs(rot, base, scaling=scaling, factor=factor, orig_ctx=4096)
+    x = torch.zeros((len(pos), rot), device="cuda")
+    x[:, slice(0, None, 2) if inter else slice(0, rot // 2)] = 1.0          # pairs (1, 0): cos and sin come out
+    out = torch.empty_like(x)
+    csa2.rope([(x, out, 0)], i32(pos), freqs, mag=mag, interleaved=inter)
+    t = pos.astype(np.longdouble)[:, None] * freqs.cpu().numpy().astype(np.longdouble)[None]
+    off = np.abs(t) * 2.0 ** -52 + np.abs(pos)[:, None] * 2 * np.pi * 2.0 ** -65 + 2 * np.pi * 2.0 ** -26
+    got = f64(out)
+    c, s = (got[:, 0::2], got[:, 1::2]) if inter else (got[:, :rot // 2], got[:, rot // 2:])
+    for have, want, other in ((c, np.cos(t), np.sin(t)), (s, np.sin(t), np.cos(t))):
+        lim = mag * (off * (np.abs(other) + off) + 3.1 * EPS32 * np.abs(want))
+        assert np.all(np.abs(have - want * mag) <= lim), float((np.abs(have - want * mag) - lim).max())
+
+
 @pytest.mark.parametrize("dtype,dim,rot,off", [(torch.bfloat16, 192, 64, 128), (torch.float32, 20, 6, 5)])
 def test_rope_in_place_equals_out_of_place_and_turns_back(csa2, dtype, dim, rot, off):
     g = torch.Generator().manual_seed(3)
