@@ -1061,3 +1061,77 @@ def test_calls_on_two_streams_at_once(csa2):
             assert_no_device_error(csa2, ws)
         for k in ("out", "lse", "w", "mass", "k_swa", "v_swa", "head", "n_swa", "k_main", "v_main", "kept", "n_valid"):
             assert torch.equal(getattr(x[1], k), getattr(y[1], k)), k
+
+
+@pytest.mark.parametrize("S,T", [(3, 6), (40, 8)])
+def test_steps_back_to_back_with_the_indexing_between(csa2, S, T):
+    """Several steps as a server runs them, positions and evictions in place, with the calls that read some inputs before the
+    launch in front of them is over (index_topk the queries behind rope, sparse_attn the windows behind a commit, index_topk the
+    keys behind an eviction): the same as with a wait behind every call, and as a replayed graph."""
+    N, K, W, B = 1024, 128, 16, S * T
+    sh = shape(B, tokens=T, n_entries=N, topk=K, swa=W, **FAST)
+    one = shape(S, n_entries=N, topk=K, swa=W, **FAST)
+    g = torch.Generator().manual_seed(S)
+    src = tree_inputs(sh, 40 + S, fill=W)
+    src.k_draft = src.k_draft.view(B, -1)
+    src.q_idx, src.w_idx = randn(g, (B, 8, 64), torch.bfloat16), torch.rand((B, 8), generator=g).cuda()
+    src.k_idx, src.k1 = randn(g, (S, N, 64), torch.bfloat16), randn(g, (S, 64, 192), torch.bfloat16)
+    src.n_query, src.n_valid = i32([N - 300] * B), i32([N] * S)
+    src.pos, src.live = i32(np.arange(B) * 37), i32(np.arange(B) % 3 == 0)
+    src.path, src.n_path = i32(np.tile(np.arange(T), (S, 1))), i32(np.arange(S) % (T + 1))
+    src.weights = torch.empty((B, K), device="cuda")
+    src.mass = torch.zeros((S, N), dtype=torch.int64, device="cuda")
+    src.kept, src.kb = torch.empty((S, N), dtype=torch.int32, device="cuda"), torch.zeros((S, N // 8, 64), dtype=torch.bfloat16, device="cuda")
+    src.idx1 = src.idx.view(S, T, K)[:, 0].contiguous()
+    src.out1, src.lse1 = torch.empty((S, 64, 128), device="cuda"), torch.empty((S, 64), device="cuda")
+    freqs, _ = csa2.rope_freqs(64)
+    tensors = {k: v for k, v in vars(src).items() if isinstance(v, torch.Tensor)}
+
+    def copy():
+        return types.SimpleNamespace(**{k: v.clone() for k, v in tensors.items()})
+
+    ws, ws1 = csa2.workspace(sh), csa2.workspace(one)
+
+    def run(d, wait):
+        for step in range(4):
+            for call in (
+                    lambda: csa2.rope([(d.q, d.q, 128), (d.k_draft, d.k_draft, 128), (d.q_idx, d.q_idx, 0)], d.pos, freqs),
+                    lambda: csa2.index_topk(sh, d.q_idx, d.w_idx, d.k_idx, d.n_query, K, d.idx, ws),
+                    lambda: csa2.tree_attn(sh, d.q, d.k_main, d.v_main, d.idx, d.k_swa, d.v_swa, d.n_swa, d.k_draft.view(S, T, -1),
+                                           d.v_draft, d.out, ws, swa_head=d.head, parent=d.parent, lse=d.lse),
+                    lambda: csa2.attn_weights(sh, d.q, d.k_main, d.idx, d.lse, d.weights, ws, live=d.live),
+                    lambda: csa2.tree_commit(sh, [(d.k_draft.view(S, T, -1), d.v_draft, d.k_swa, d.v_swa, d.idx, d.weights)], d.path,
+                                             d.n_path, d.head, d.n_swa, ws, mass=d.mass),
+                    lambda: csa2.sparse_attn(one, d.k1, d.k_main, d.v_main, d.idx1, d.k_swa, d.v_swa, d.n_swa, d.out1, ws1, lse=d.lse1),
+                    lambda: csa2.kv_evict(one, N - 1, N - 100 - step, 4, 32, d.k_main, d.v_main, d.k_idx, d.mass, d.n_valid, d.kept, ws1,
+                                          kb=d.kb),
+                    lambda: csa2.index_topk(one, d.q_idx.view(S, T, 8, 64)[:, 0].contiguous(), d.w_idx.view(S, T, 8)[:, 0].contiguous(),
+                                            d.k_idx, d.n_valid, K, d.idx1, ws1),
+                    lambda: d.n_valid.fill_(N)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+
+    a = copy()
+    run(a, True)
+    assert torch.isfinite(a.out).all() and torch.isfinite(a.out1).all() and int(a.mass.max()) > 0
+    for _ in range(5):
+        b = copy()
+        torch.cuda.synchronize()
+        run(b, False)
+        torch.cuda.synchronize()
+        for k in tensors:
+            assert torch.equal(getattr(a, k), getattr(b, k)), k
+    c = copy()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(c, False)
+    for _ in range(3):
+        for k, v in tensors.items():
+            getattr(c, k).copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in tensors:
+            assert torch.equal(getattr(a, k), getattr(c, k)), k
+    assert_no_device_error(csa2, ws)
+    assert_no_device_error(csa2, ws1)
