@@ -430,8 +430,10 @@ int csa2_rope(const csa2_rope_slot* slots, int32_t n_slots, int32_t rows, int32_
  *   lse [B, H] fp32 (nullable); NaN where a key that is attended scores NaN or +inf, as out is
  * shape.swa >= 1; batch <= 65,535; out and lse overlap nothing else (refused).
  * A chain of T gives what T steps of csa2_swa_append and csa2_sparse_attn
- * give.  Weights are rounded to bf16 before they meet bf16 values, their sums
- * are not.  ws also holds lists of the sequences' keys, where the indexing calls
+ * give.  Weights are rounded to bf16 (half a step, 2^-8 of a weight) before they
+ * meet bf16 values on tensor cores, as csa2_sparse_attn rounds them; bf16 rows that
+ * are not whole 8-byte pieces are multiplied in fp32.  The weights' sums and lse are never rounded.
+ * csa2_merge_attn takes fp32 parts, so that out cannot be one of them.  ws also holds lists of the sequences' keys, where the indexing calls
  * keep scores, lists and the group's indices (caches much shorter than topk need
  * the most for them). */
 int csa2_tree_attn(const csa2_shape* shape, const void* q, const void* k_main, const void* v_main, const int32_t* idx,

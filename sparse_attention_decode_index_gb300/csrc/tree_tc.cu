@@ -38,7 +38,12 @@
 // (their 64 exponentials a row are 570, the maximum 200, TMEM loads and stores 150) and
 // the issue of 16 tensor-core steps (690) with its waits.  32 trees of 32 tokens,
 // 640 slots: 52.9 us with the plan, 0.50 PFLOP/s by every token's own keys, the tensor
-// cores active in 28 % of the cycles; 16 trees of 16: 21.1 us, of which the plan is 5.
+// cores active in 30 % of the cycles; 16 trees of 16: 21.2 us.  Stamps of the latter, from the
+// plan's start in ns: its end 5,500; the attention's wait over 6,100, the first tile's copies
+// issued 8,200 (counts, entries and rows are read one behind the other) and landed 8,400; the
+// first scores 8,900; 13 tiles of 630 until 17,000; O written 18,300, the end 18,700.  Of the
+// former: 9,600 until the wait is over, first scores 13,400, then 735 a tile; a CTA has 41
+// tiles on average and 51 at most (whole pairs, 3.4 an SM), so that they end between 40,000 and 52,500.
 // Groups of four tokens (two row tiles) took 79 us for the former, two softmax sets
 // 70, half of the exponentials by a polynomial 66.
 //
