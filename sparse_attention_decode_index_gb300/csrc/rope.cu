@@ -340,7 +340,7 @@ cudaError_t launch_rope(RopeArgs& a, int rows, cudaStream_t st) {
   a.per_block = rows / want < 1 ? 1 : rows / want > most ? most : rows / want;
   for (int k = 0; k < a.n_slots; ++k)   // keeps fast_div's products below 2^32
     while (a.per_block > 1 && a.per_block * a.slot[k].heads * a.slot[k].dim > (1 << 21)) --a.per_block;
-  const int blocks = (rows + a.per_block - 1) / a.per_block;
+  const int blocks = (rows - 1) / a.per_block + 1;   // (rows go up to 2^31 - 1)
   int split = blocks >= want ? 1 : (want + blocks - 1) / blocks;
   split = split > heads ? heads : split;
   note_launch();

@@ -105,6 +105,23 @@ def test_rope_angles_of_every_position(csa2, base, scaling, factor, inter):
         assert np.all(np.abs(have - want * mag) <= lim), float((np.abs(have - want * mag) - lim).max())
 
 
+def test_rope_of_the_most_rows(csa2):
+    """2^31 - 1 rows of one pair, in place (17 GB): the first, the last and some between."""
+    rows = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    x = torch.zeros((rows, 2), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    pos = torch.arange(rows, dtype=torch.int32, device="cuda")
+    freqs = torch.tensor([0.5], dtype=torch.float64, device="cuda")
+    csa2.rope([(x, x, 0)], pos, freqs)
+    at = np.concatenate([np.arange(200), rows // 3 + np.arange(200), rows - 200 + np.arange(200)])
+    got = f64(x[torch.as_tensor(at, device="cuda")])
+    t = at.astype(np.longdouble) * 0.5
+    # half a step of bf16, and the angle: 2^-52 of it and 2^-26 turns
+    assert np.abs(got - np.stack([np.cos(t), np.sin(t)], 1)).max() <= 2.0 ** -8 * 0.5 + 2.0 ** 30 * 2.0 ** -52 + 1e-6
+
+
 @pytest.mark.parametrize("dtype,dim,rot,off", [(torch.bfloat16, 192, 64, 128), (torch.float32, 20, 6, 5)])
 def test_rope_in_place_equals_out_of_place_and_turns_back(csa2, dtype, dim, rot, off):
     g = torch.Generator().manual_seed(3)
