@@ -587,6 +587,37 @@ def test_chain_equals_steps_of_append_and_attention(csa2):
     assert torch.equal(kt, ks) and torch.equal(vt, vs) and torch.equal(ht, head) and torch.equal(nt, n)
 
 
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_tree_and_weights_of_caches_beyond_32_bit_offsets(csa2, kind):
+    """Rows that lie beyond 2^32 bytes of K and of V: bit for bit what the same rows give in a cache of 90 entries."""
+    S, T = (2, 80) if kind == "pairs" else (1, 4)
+    kw = KINDS[kind][0]
+    sh = shape(S * T, tokens=T, n_entries=90, topk=20, swa=8, **kw)
+    d = tree_inputs(sh, 3, holes=1.0)
+    N = 2 ** 32 // (sh.v_dim * (4 if sh.dtype == "f32" else 2)) + 1000
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GB")
+    lse = torch.full((S * T, sh.q_heads), 4.0, device="cuda")
+    w = [torch.empty((S * T, 20), device="cuda") for _ in range(2)]
+    assert_no_device_error(csa2, run_tree(csa2, sh, d))
+    csa2.attn_weights(sh, d.q, d.k_main, d.idx, lse, w[0], csa2.workspace(sh))
+    out, out_lse = d.out.clone(), d.lse.clone()
+    check_tree(sh, d)
+    far = torch.arange(90, device="cuda") * ((N - 1) // 89)
+    for n in ("k_main", "v_main"):
+        t = getattr(d, n)
+        big = torch.zeros((S, N, t.shape[-1]), dtype=t.dtype, device="cuda")
+        big[:, far] = t
+        setattr(d, n, big)
+    d.idx = torch.where(d.idx < 0, d.idx, far.int()[d.idx.clamp(min=0).long()])
+    sh.n_entries = N
+    d.out.fill_(9.0)
+    ws = run_tree(csa2, sh, d)
+    csa2.attn_weights(sh, d.q, d.k_main, d.idx, lse, w[1], ws)
+    assert_no_device_error(csa2, ws)
+    assert torch.equal(d.out, out) and torch.equal(d.lse, out_lse) and torch.equal(w[0], w[1])
+
+
 # ------------------------------------------------------------------ attention weights
 
 SHAPES = [(64, 192, "bf16"), (5, 24, "f32"), (16, 64, "bf16"), (1, 1, "f32"), (12, 1024, "bf16")]
@@ -933,6 +964,39 @@ def test_kv_evict_counts_and_no_workspace(csa2):
     csa2.kv_evict(d.sh, 40, 30, 0, 0, d.k, d.v, d.x, d.mass, d.n, kept, None)
     assert csa2.read_static_device_error() == (-5, BAD_COUNT)
     assert d.n.tolist() == [30, 0, 30]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_kv_evict_of_a_cache_beyond_32_bit_offsets(csa2, in_place):
+    """K, V and indexer keys of more than 2^32 bytes each, masses of more than any cluster keeps."""
+    N, keep = 2 ** 32 // 256 + 4099, 2 ** 32 // 256 - 100001
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    sh = shape(1, n_entries=N, topk=8, swa=4, k_dim=128, v_dim=128, idx_dim=128)
+    e = torch.arange(N, device="cuda")
+    ins = [torch.empty((1, N, 128), dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    for i, x in enumerate(ins):                            # a row says which entry it is, in digits that bf16 holds
+        x.zero_()
+        for c in range(4):
+            x[0, :, 31 * c + i] = ((e >> (7 * c)) & 127).to(torch.bfloat16)
+    mass = torch.where(e % 3 == 0, 5, 1 + e % 2)[None].contiguous()
+    ins += [mass, i32([N])]
+    kept = torch.empty((1, N), dtype=torch.int32, device="cuda")
+    kb = torch.empty((1, -(-N // 8), 128), dtype=torch.bfloat16, device="cuda")
+    outs = ins if in_place else [torch.zeros_like(t) for t in ins]
+    sink, recent = 1000, 5000
+    mid = e[sink:N - recent]
+    order = torch.sort(mass[0][mid], descending=True, stable=True).indices[:keep - sink - recent]
+    want = torch.cat([e[:sink], torch.sort(mid[order]).values, e[N - recent:]])
+    was = mass.clone()
+    csa2.kv_evict(sh, keep, keep, sink, recent, *ins, kept, None, kb=kb, out=None if in_place else outs)
+    assert int(outs[4][0]) == keep and torch.equal(kept[0, :keep].long(), want) and bool((kept[0, keep:] == -1).all())
+    assert torch.equal(outs[3][0, :keep], was[0][want]) and not outs[3][0, keep:].any()
+    for i in range(3):
+        for c in range(4):
+            assert torch.equal(outs[i][0, :keep, 31 * c + i].float(), ((want >> (7 * c)) & 127).float())
+    x = outs[2][0, :keep // 8 * 8, 2].float().view(-1, 8).mean(1)
+    assert torch.equal(kb[0, :keep // 8, 2].float(), x.round().to(torch.bfloat16).float())
 
 
 # ------------------------------------------------------------------ together
