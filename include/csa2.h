@@ -511,6 +511,105 @@ int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_
                   void* k_main_out, void* v_main_out, void* k_idx_out, int64_t* mass_out, int32_t* n_valid_out,
                   int32_t* kept, void* kb_out, int32_t round_to_int, void* ws, size_t ws_bytes, csa2_stream_t stream);
 
+/* ---------------------------------------------------------------- main caches held in 4 bits
+ * A main cache of a third of the bytes: an entry's key and value lie side by
+ * side in kv4 [S, N, csa2_kv4_bytes(k_dim, v_dim)] (S = B / T sequences), 192 bytes
+ * for 192 / 128 dims where bf16 rows take 640.  In the order of a step:
+ * csa2_norm_rope normalises and turns the queries and keys, csa2_kv4_append packs
+ * the new entries (as csa2_kv_append stores them), the indexing calls select,
+ * and csa2_kv4_attn attends (as csa2_sparse_attn does).  csa2_kv4_rows gives
+ * rows back as numbers, for calls that take them so (csa2_attn_weights,
+ * csa2_tree_attn on a cache of the selected rows).  Indexer keys, block keys and
+ * windows stay in the element type.  The pages describe no quantised cache.
+ *
+ * An entry: each group of 16 dims of the key, then of the value (the last group
+ * of either filled up with zeros), has 16 codes of 4 bits and one scale of 8:
+ *   byte 8 g + i / 2, low bits for even i: code i of group g, e2m1: bit 3 the
+ *     sign, bits 0..2 one of 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   byte 8 G + g (G groups in all): the group's scale, e4m3 (2^-9 .. 448)
+ *   zeros up to a multiple of 16 bytes
+ * and a dim's value is code * scale * 2^exp, exp being k_exp for keys and v_exp for
+ * values, both -64 .. 64 and the same in every call on a cache (they place the
+ * scales' range: 0 suits groups whose largest magnitude is 0.1 .. 2,688).  bf16
+ * holds every such value exactly, but for scales of NaN (see csa2_kv4_append).
+ * The kernels read nothing before the preceding kernel of the stream has
+ * completed.  kv4 is 16-byte aligned, every other array a multiple of its
+ * elements' size, and none lies in the ws_bytes of the call's ws (refused). */
+
+/* Bytes of a packed entry, 9 a group of 16 dims, up to a multiple of 16
+ * (host only; 0 unless both dims are 1..1024). */
+size_t csa2_kv4_bytes(int32_t k_dim, int32_t v_dim);
+
+/* One tensor of csa2_norm_rope: x and out are rows of [heads, dim] in dtype,
+ * x_stride and out_stride elements apart (heads * dim .. 2^28, so that they may be
+ * parts of a wider projection's rows).  gain [dim], or [heads, dim] with gain_each = 1;
+ * NULL: ones.  Dims rot_off .. rot_off + rot_dim - 1 are turned after the norm.
+ * out == x with equal strides works in place; any other overlap is refused (tensors
+ * of one stride may lie in the same rows, beside each other). */
+typedef struct {
+  const void* x;
+  void* out;
+  const float* gain;
+  int64_t x_stride, out_stride;
+  int32_t heads, dim, rot_off, dtype, gain_each;
+} csa2_norm_rope_slot;
+
+/* The norm of every head of several tensors of the same rows, and their rotary
+ * positions as in csa2_rope, in one pass:
+ *   center = 0:  y = x / sqrt(mean(x^2) + eps) * gain
+ *   center = 1:  y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * gain
+ * over a head's dim numbers; then the pairs of y are turned by pos[r] * freqs[i]
+ * and multiplied by mag.  rot_dim = 0 turns nothing (pos and freqs are not
+ * read and may be NULL).  The arithmetic is fp32, rounded once.
+ *   pos [rows] int32   freqs [rot_dim / 2] double (device)
+ * rows >= 1; 1 <= n_slots <= 16; mag finite and > 0; eps finite and >= 0;
+ * rot_dim even, 0..1024; heads and dim up to 1024.  Rows that are not whole vectors of
+ * 16 or 8 bytes (dims, turned range, strides and addresses) are taken number by number. */
+int csa2_norm_rope(const csa2_norm_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,
+                   int32_t center, const int32_t* pos, const double* freqs, float mag, float eps, csa2_stream_t stream);
+
+/* csa2_kv_append for a packed cache: the first n_new[b] rows (0..max_new) of
+ * k_new[b] and v_new[b] are packed at entries n_valid[b], n_valid[b] + 1, ... of
+ * kv4, kidx_new[b] is written to k_idx there, the summary keys of the blocks they fall in
+ * are recomputed (kb nullable), and n_valid[b] grows; entries beyond N are
+ * dropped and recorded (bad count).  max_new may be a whole prompt.
+ * Of a group, with a its largest magnitude / 2^exp: the scale is the e4m3 number
+ * nearest to a / 6 (ties to even), at least 2^-9 and at most 448; a code is the e2m1
+ * number nearest to x / 2^exp / scale (ties to even), at most 6.  A group whose a is not
+ * finite gets the scale NaN: all its dims read as NaN.
+ *   k_new [B, max_new, dk]  v_new [B, max_new, dv]  kidx_new [B, max_new, dI]  n_new [B]
+ *   kv4 [B, N, csa2_kv4_bytes]  k_idx [B, N, dI]  kb [B, ceil(N / block), dI] or NULL
+ *   n_valid [B] (read and updated)
+ * shape.tokens <= 1; batch <= 65,535; max_new >= 1.  kv4, k_idx, kb and n_valid overlap
+ * nothing else (refused).  ws holds only the error word (NULL with ws_bytes = 0: the
+ * static scratch's, as for csa2_kv_append). */
+int csa2_kv4_append(const csa2_shape* shape, int32_t max_new, const int32_t* n_new, const void* k_new, const void* v_new,
+                    const void* kidx_new, void* kv4, void* k_idx, void* kb, int32_t* n_valid, int32_t k_exp,
+                    int32_t v_exp, int32_t round_to_int, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/* Rows of a packed cache as numbers: k_out[b, j] and v_out[b, j] are entry
+ * idx[b, j] of sequence b / T, or zeros where idx[b, j] < 0; an index >= N is recorded
+ * (bad index) and gives zeros.
+ *   kv4 [B / T, N, csa2_kv4_bytes]  idx [B, n_rows]
+ *   k_out [B, n_rows, dk]  v_out [B, n_rows, dv] (element type; overlap nothing else: refused)
+ * n_rows >= 1; batch * n_rows < 2^31.  ws as for csa2_kv4_append. */
+int csa2_kv4_rows(const csa2_shape* shape, const void* kv4, const int32_t* idx, int32_t n_rows, void* k_out, void* v_out,
+                  int32_t k_exp, int32_t v_exp, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
+/* csa2_sparse_attn over a packed cache: one softmax over the entries idx[b, :]
+ * (< 0 skipped; >= N recorded and skipped) and the window rows 0..n_swa[b]-1.
+ *   q [B, H, dk]  kv4 [B / T, N, csa2_kv4_bytes]  idx [B, K]
+ *   k_swa [B, W, dk]  v_swa [B, W, dv]  n_swa [B] (0..W)   (windows NULL where W = 0)
+ *   out [B, H, dv] in the element type (as csa2_tree_attn's)
+ *   lse [B, H] fp32 (nullable); out = 0 and -inf where nothing is attended,
+ *   both NaN where a key that is attended scores NaN or +inf
+ * batch <= 65,535; out and lse overlap nothing else (refused).  Weights are rounded to bf16
+ * (half a step, 2^-8 of a weight) where they meet bf16 values on tensor cores; their sums
+ * and lse are not. */
+int csa2_kv4_attn(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa,
+                  const void* v_swa, const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp, void* ws,
+                  size_t ws_bytes, csa2_stream_t stream);
+
 /* Static description of a status code. */
 const char* csa2_status_str(int status);
 

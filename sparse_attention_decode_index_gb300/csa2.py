@@ -83,6 +83,11 @@ _SIGS = {
     "csa2_attn_weights": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_VP] * 7 + [_SZ, _VP]),
     "csa2_tree_commit": (ctypes.c_int, [ctypes.POINTER(CShape), _VP, _I32] + [_VP] * 6 + [_SZ, _VP]),
     "csa2_kv_evict": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_I32] * 4 + [_VP] * 12 + [_I32, _VP, _SZ, _VP]),
+    "csa2_kv4_bytes": (_SZ, [_I32, _I32]),
+    "csa2_norm_rope": (ctypes.c_int, [_VP, _I32, _I32, _I32, _I32, _I32, _VP, _VP, ctypes.c_float, ctypes.c_float, _VP]),
+    "csa2_kv4_append": (ctypes.c_int, [ctypes.POINTER(CShape), _I32] + [_VP] * 8 + [_I32] * 3 + [_VP, _SZ, _VP]),
+    "csa2_kv4_rows": (ctypes.c_int, [ctypes.POINTER(CShape), _VP, _VP, _I32, _VP, _VP, _I32, _I32, _VP, _SZ, _VP]),
+    "csa2_kv4_attn": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_VP] * 8 + [_I32, _I32, _VP, _SZ, _VP]),
     "csa2_debug_wait_timeout": (ctypes.c_int, [ctypes.POINTER(CShape), _VP, _VP, _VP, _VP, _I32, _VP, ctypes.c_uint32,
                                                _VP, _SZ, _VP]),
 }
@@ -581,6 +586,145 @@ def kv_evict(shape, trigger: int, keep: int, sink: int, recent: int, k_main, v_m
     greatest by mass stay, in order (csa2_kv_evict).  In place, or into ``out``; ``ws`` may be None."""
     KvEvictCall(shape, trigger, keep, sink, recent, k_main, v_main, k_idx, mass, n_valid, kept, ws, kb, out,
                 round_to_int)(stream)
+
+
+# ------------------------------------------------------------------ main caches held in 4 bits
+
+_NORMS = {"rms": 0, "layer": 1}
+
+
+def kv4_bytes(shape) -> int:
+    """Bytes of a packed entry (csa2_kv4_bytes): the cache is uint8 [S, N, kv4_bytes(shape)]."""
+    n = int(lib().csa2_kv4_bytes(int(shape.k_dim), int(shape.v_dim)))
+    if n == 0:
+        raise CSA2Error(-1, "csa2_kv4_bytes")
+    return n
+
+
+def _kv4(kv4, shape, sequences: int, device):
+    return _arr(kv4, torch.uint8, (sequences, int(shape.n_entries), kv4_bytes(shape)), "kv4", device)
+
+
+class CNormRopeSlot(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("out", ctypes.c_void_p), ("gain", ctypes.c_void_p), ("x_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32), ("rot_off", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("gain_each", ctypes.c_int32)]
+
+
+def _head_rows(t, name: str, dtype, size, device):
+    """Pointer and row stride (elements) of [rows, heads, dim] or [rows, dim] whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device} (it is on {t.device})")
+    if t.dtype != dtype or tuple(t.shape) != tuple(size):
+        raise ValueError(f"{name} must be {dtype} {tuple(size)}, got {t.dtype} {tuple(t.shape)}")
+    width = t[0].numel() if t.shape[0] else 0
+    if t.shape[0] and not t[0].is_contiguous():
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else width
+
+
+class NormRopeCall(_Call):
+    """A prepared csa2_norm_rope call.  ``slots`` is a list of (x, out, gain, rot_off): x and out [rows, heads, dim] or
+    [rows, dim] in bf16 or fp32, whose rows may lie apart (parts of one projection; out is x: in place); gain fp32 [dim],
+    [heads, dim] or None.  ``norm`` is "rms" or "layer"; with pos and freqs None nothing is turned."""
+
+    def __init__(self, slots, pos=None, freqs=None, mag: float = 1.0, eps: float = 1e-6, norm: str = "rms",
+                 interleaved: bool = False):
+        slots = list(slots)
+        if norm not in _NORMS:
+            raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
+        if (pos is None) != (freqs is None):
+            raise ValueError("pos and freqs go together")
+        if not slots:
+            raise ValueError("slots is empty")
+        dev, rows = slots[0][0].device, int(slots[0][0].shape[0])
+        arr = (CNormRopeSlot * len(slots))()
+        for k, (x, out, gain, off) in enumerate(slots):
+            if x.dim() not in (2, 3) or x.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"slot {k}: x must be bf16 or fp32 [rows, heads, dim] or [rows, dim], got {x.dtype} {tuple(x.shape)}")
+            size = (rows, *x.shape[1:])
+            heads, dim = (int(x.shape[1]) if x.dim() == 3 else 1), int(x.shape[-1])
+            each = gain is not None and gain.dim() == 2
+            xp, xs = _head_rows(x, f"slot {k}: x", x.dtype, size, dev)
+            op, os_ = _head_rows(out, f"slot {k}: out", x.dtype, size, dev)
+            arr[k] = CNormRopeSlot(xp, op, _arr(gain, torch.float32, (heads, dim) if each else (dim,), "gain", dev, True), xs, os_,
+                                   heads, dim, int(off), F32 if x.dtype == torch.float32 else BF16, int(each))
+        pairs = 0 if freqs is None else int(freqs.shape[0])
+        self._bind("csa2_norm_rope", dev, (slots, pos, freqs, arr),
+                   (ctypes.cast(arr, ctypes.c_void_p), len(slots), rows, 2 * pairs, int(bool(interleaved)), _NORMS[norm],
+                    _arr(pos, torch.int32, (rows,), "pos", dev, True), _arr(freqs, torch.float64, (pairs,), "freqs", dev, True),
+                    float(mag), float(eps)))
+
+
+def norm_rope(slots, pos=None, freqs=None, mag: float = 1.0, eps: float = 1e-6, norm: str = "rms", interleaved: bool = False,
+              stream=None):
+    """Normalise every head of the tensors of ``slots`` and turn them to their rows' positions, in one pass
+    (csa2_norm_rope; NormRopeCall describes the arguments)."""
+    NormRopeCall(slots, pos, freqs, mag, eps, norm, interleaved)(stream)
+
+
+class Kv4AppendCall(_Call):
+    """A prepared csa2_kv4_append call; kb and ws may be None."""
+
+    def __init__(self, shape, n_new, k_new, v_new, kidx_new, kv4, k_idx, kb, n_valid, ws, k_exp: int = 0, v_exp: int = 0,
+                 round_to_int: bool = True):
+        s, e, dev = c_shape(shape), elem_dtype(shape), k_new.device
+        B, N, M = s.batch, s.n_entries, int(k_new.shape[1])
+        nb = -(-N // max(1, s.block))
+        self._bind("csa2_kv4_append", dev, (s, n_new, k_new, v_new, kidx_new, kv4, k_idx, kb, n_valid, ws),
+                   (ctypes.byref(s), M, _arr(n_new, torch.int32, (B,), "n_new", dev), _arr(k_new, e, (B, M, s.k_dim), "k_new", dev),
+                    _arr(v_new, e, (B, M, s.v_dim), "v_new", dev), _arr(kidx_new, e, (B, M, s.idx_dim), "kidx_new", dev),
+                    _kv4(kv4, shape, B, dev), _arr(k_idx, e, (B, N, s.idx_dim), "k_idx", dev),
+                    _arr(kb, e, (B, nb, s.idx_dim), "kb", dev, True), _arr(n_valid, torch.int32, (B,), "n_valid", dev),
+                    int(k_exp), int(v_exp), int(bool(round_to_int)), *_ws_arg(ws, dev)))
+
+
+def kv4_append(shape, n_new, k_new, v_new, kidx_new, kv4, k_idx, kb, n_valid, ws, k_exp: int = 0, v_exp: int = 0,
+               round_to_int: bool = True, stream=None):
+    """Pack n_new[b] entries per sequence (rows of k_new / v_new / kidx_new, [B, max_new, ...]) at n_valid[b] of the packed
+    cache kv4, write their indexer keys, recompute the touched block keys, grow n_valid (csa2_kv4_append)."""
+    Kv4AppendCall(shape, n_new, k_new, v_new, kidx_new, kv4, k_idx, kb, n_valid, ws, k_exp, v_exp, round_to_int)(stream)
+
+
+class Kv4RowsCall(_Call):
+    """A prepared csa2_kv4_rows call; ws may be None."""
+
+    def __init__(self, shape, kv4, idx, k_out, v_out, ws, k_exp: int = 0, v_exp: int = 0):
+        s, e, dev = c_shape(shape), elem_dtype(shape), kv4.device
+        B, S, _ = _tree_sizes(shape)
+        R = int(idx.shape[1])
+        self._bind("csa2_kv4_rows", dev, (s, kv4, idx, k_out, v_out, ws),
+                   (ctypes.byref(s), _kv4(kv4, shape, S, dev), _arr(idx, torch.int32, (B, R), "idx", dev), R,
+                    _arr(k_out, e, (B, R, s.k_dim), "k_out", dev), _arr(v_out, e, (B, R, s.v_dim), "v_out", dev), int(k_exp),
+                    int(v_exp), *_ws_arg(ws, dev)))
+
+
+def kv4_rows(shape, kv4, idx, k_out, v_out, ws, k_exp: int = 0, v_exp: int = 0, stream=None):
+    """Entries idx [B, R] of the packed cache as numbers, zeros where idx < 0 (csa2_kv4_rows)."""
+    Kv4RowsCall(shape, kv4, idx, k_out, v_out, ws, k_exp, v_exp)(stream)
+
+
+class Kv4AttnCall(_Call):
+    """A prepared csa2_kv4_attn call."""
+
+    def __init__(self, shape, q, kv4, idx, k_swa, v_swa, n_swa, out, ws, lse=None, k_exp: int = 0, v_exp: int = 0):
+        s, e, dev = c_shape(shape), elem_dtype(shape), q.device
+        B, S, _ = _tree_sizes(shape)
+        H, dk, dv, W = s.q_heads, s.k_dim, s.v_dim, s.swa
+        self._bind("csa2_kv4_attn", dev, (s, q, kv4, idx, k_swa, v_swa, n_swa, out, ws, lse),
+                   (ctypes.byref(s), _arr(q, e, (B, H, dk), "q", dev), _kv4(kv4, shape, S, dev),
+                    _arr(idx, torch.int32, (B, s.topk), "idx", dev), _arr(k_swa, e, (B, W, dk), "k_swa", dev, W == 0),
+                    _arr(v_swa, e, (B, W, dv), "v_swa", dev, W == 0), _arr(n_swa, torch.int32, (B,), "n_swa", dev),
+                    _arr(out, e, (B, H, dv), "out", dev), _arr(lse, torch.float32, (B, H), "lse", dev, True), int(k_exp),
+                    int(v_exp), *_ws_arg(ws, dev)))
+
+
+def kv4_attn(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, ws, lse=None, k_exp: int = 0, v_exp: int = 0, stream=None):
+    """Sparse attention over the packed cache's entries idx [B, K] and the queries' windows (csa2_kv4_attn); out in the
+    element type."""
+    Kv4AttnCall(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, ws, lse, k_exp, v_exp)(stream)
 
 
 def debug_wait_timeout(shape, q_idx, w, k_idx, n_valid, k: int, idx_out, wait_limit_ns: int, ws, stream=None):

@@ -17,6 +17,7 @@
 
 #include "../../include/csa2.h"
 #include "draft.h"
+#include "kv4.h"
 
 using namespace csa2;
 
@@ -178,6 +179,27 @@ bool written_overlap(Span* v, int n) {
     if (v[i].written) end_written = std::max(end_written, at + v[i].bytes);
   }
   return false;
+}
+
+// Rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  const void* at;
+  uint64_t width, stride, rows;
+};
+
+// Whether two of them share a byte.  Rows of one stride may lie between each other (parts of one projection);
+// of different strides, the whole ranges count.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.at == nullptr || b.at == nullptr) return false;
+  if (!overlap(a.at, (a.rows - 1) * a.stride + a.width, b.at, (b.rows - 1) * b.stride + b.width)) return false;
+  if (a.stride != b.stride || a.rows != b.rows || a.rows == 1) return true;
+  const uint64_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  const uint64_t d = y >= x ? (y - x) % a.stride : (a.stride - (x - y) % a.stride) % a.stride;   // b behind a row of a
+  return d < a.width || d + b.width > a.stride;
+}
+
+int check_exps(int32_t k_exp, int32_t v_exp) {
+  return k_exp < -64 || k_exp > 64 || v_exp < -64 || v_exp > 64 ? CSA2_ERR_INVALID_ARG : CSA2_OK;
 }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
@@ -1044,6 +1066,186 @@ int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_
   a.in_place = same != 0;
   a.err = err;
   return cuda_status(launch_kv_evict(a, s.batch, stream));
+}
+
+// ---------------------------------------------------------------- main caches held in 4 bits
+
+size_t csa2_kv4_bytes(int32_t k_dim, int32_t v_dim) {
+  if (k_dim < 1 || k_dim > 1024 || v_dim < 1 || v_dim > 1024) return 0;
+  return size_t(kv4_bytes(k_dim, v_dim));
+}
+
+int csa2_norm_rope(const csa2_norm_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,
+                   int32_t center, const int32_t* pos, const double* freqs, float mag, float eps, csa2_stream_t stream) {
+  if (slots == nullptr || n_slots < 1 || n_slots > kMaxRopeSlots || rows < 1) return CSA2_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim % 2 != 0) return CSA2_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (pos == nullptr || freqs == nullptr || !aligned(4, pos) || !aligned8(freqs))) return CSA2_ERR_INVALID_ARG;
+  if (rot_dim > kMaxRotDim) return CSA2_ERR_UNSUPPORTED;
+  if ((interleaved != 0 && interleaved != 1) || (center != 0 && center != 1)) return CSA2_ERR_INVALID_ARG;
+  if (!(mag > 0.f) || !std::isfinite(mag) || !(eps >= 0.f) || !std::isfinite(eps)) return CSA2_ERR_INVALID_ARG;
+  NormRopeArgs a{};
+  Rows x[kMaxRopeSlots], out[kMaxRopeSlots], gain[kMaxRopeSlots];
+  for (int k = 0; k < n_slots; ++k) {
+    const csa2_norm_rope_slot& y = slots[k];
+    if (y.x == nullptr || y.out == nullptr || y.heads < 1 || y.dim < 1 || y.rot_off < 0) return CSA2_ERR_INVALID_ARG;
+    if (rot_dim > 0 && int64_t(y.rot_off) + rot_dim > y.dim) return CSA2_ERR_INVALID_ARG;
+    if (y.dtype != CSA2_BF16 && y.dtype != CSA2_F32) return CSA2_ERR_INVALID_ARG;
+    if (y.gain_each != 0 && y.gain_each != 1) return CSA2_ERR_INVALID_ARG;
+    if (!aligned(elem_size(y.dtype), y.x, y.out) || !aligned(4, y.gain)) return CSA2_ERR_INVALID_ARG;
+    if (y.heads > 1024 || y.dim > 1024) return CSA2_ERR_UNSUPPORTED;
+    const int64_t width = int64_t(y.heads) * y.dim;
+    if (y.x_stride < width || y.out_stride < width) return CSA2_ERR_INVALID_ARG;
+    if (y.x_stride > (int64_t(1) << 28) || y.out_stride > (int64_t(1) << 28)) return CSA2_ERR_UNSUPPORTED;
+    if (y.x == y.out && y.x_stride != y.out_stride && rows > 1) return CSA2_ERR_INVALID_ARG;
+    const uint64_t e = elem_size(y.dtype);
+    a.slot[k] = NormRopeArgs::Slot{y.x, y.out, y.gain, y.x_stride, y.out_stride, y.heads, y.dim, rot_dim > 0 ? y.rot_off : 0,
+                                   y.dtype, y.gain_each, 0, 0, 0};
+    x[k] = {y.x, width * e, y.x_stride * e, uint64_t(rows)};
+    out[k] = {y.out, width * e, y.out_stride * e, uint64_t(rows)};
+    gain[k] = {y.gain, uint64_t(y.gain_each ? width : y.dim) * 4, 0, 1};
+  }
+  // an output may be its own input; it may touch nothing else that the call reads or writes
+  const Rows pos_rows{rot_dim > 0 ? pos : nullptr, uint64_t(rows) * 4, 0, 1}, freq_rows{rot_dim > 0 ? freqs : nullptr, uint64_t(rot_dim) * 4, 0, 1};
+  for (int k = 0; k < n_slots; ++k) {
+    if (overlap(out[k], pos_rows) || overlap(out[k], freq_rows)) return CSA2_ERR_INVALID_ARG;
+    for (int j = 0; j < n_slots; ++j) {
+      if ((j != k || out[k].at != x[k].at) && overlap(out[k], x[j])) return CSA2_ERR_INVALID_ARG;
+      if ((j != k && overlap(out[k], out[j])) || overlap(out[k], gain[j])) return CSA2_ERR_INVALID_ARG;
+    }
+  }
+  a.n_slots = n_slots;
+  a.rot = rot_dim;
+  a.interleaved = interleaved;
+  a.center = center;
+  a.mag = mag;
+  a.eps = eps;
+  a.pos = pos;
+  a.freqs = freqs;
+  return cuda_status(launch_norm_rope(a, rows, stream));
+}
+
+int csa2_kv4_append(const csa2_shape* shape, int32_t max_new, const int32_t* n_new, const void* k_new, const void* v_new,
+                    const void* kidx_new, void* kv4, void* k_idx, void* kb, int32_t* n_valid, int32_t k_exp,
+                    int32_t v_exp, int32_t round_to_int, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  if (seqdiv(s) != 1 || s.batch > kMaxGridY) return CSA2_ERR_UNSUPPORTED;   // caches are per sequence: pass a one-token shape
+  if (max_new < 1 || (round_to_int != 0 && round_to_int != 1)) return CSA2_ERR_INVALID_ARG;
+  CSA2_TRY(check_exps(k_exp, v_exp));
+  for (const void* p : {static_cast<const void*>(n_new), k_new, v_new, kidx_new, static_cast<const void*>(kv4),
+                        static_cast<const void*>(k_idx), static_cast<const void*>(n_valid)})
+    if (p == nullptr) return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(kv4) || !aligned(elem_size(s.dtype), k_new, v_new, kidx_new, k_idx, kb) || !aligned(4, n_new, n_valid))
+    return CSA2_ERR_INVALID_ARG;
+  int* err = nullptr;
+  CSA2_TRY(error_word(s, ws, ws_bytes, &err));
+  const uint64_t B = s.batch, N = s.n_entries, M = max_new, e = elem_size(s.dtype), x = s.idx_dim * e;
+  const int64_t nb = ceil_div(s.n_entries, s.block);
+  Span spans[] = {{n_new, B * 4, false}, {k_new, B * M * s.k_dim * e, false}, {v_new, B * M * s.v_dim * e, false},
+                  {kidx_new, B * M * x, false}, {kv4, B * N * kv4_bytes(s.k_dim, s.v_dim), true}, {k_idx, B * N * x, true},
+                  {kb, B * uint64_t(nb) * x, true}, {n_valid, B * 4, true}, {ws, ws_bytes, true}};
+  if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
+  Kv4AppendArgs a{};
+  a.n_new = n_new;
+  a.max_new = max_new;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.kidx_new = kidx_new;
+  a.kv = static_cast<uint8_t*>(kv4);
+  a.k_idx = k_idx;
+  a.kb = kb;
+  a.n_valid = n_valid;
+  a.n_entries = s.n_entries;
+  a.nb_cap = int(nb);
+  a.k_dim = s.k_dim;
+  a.v_dim = s.v_dim;
+  a.idx_dim = s.idx_dim;
+  a.block = s.block;
+  a.round_to_int = round_to_int;
+  a.dtype = s.dtype;
+  a.k_down = std::ldexp(1.f, -k_exp);
+  a.v_down = std::ldexp(1.f, -v_exp);
+  a.wide = s.k_dim % 16 == 0 && s.v_dim % 16 == 0 && aligned16(k_new) && aligned16(v_new);
+  a.wide_idx = x % 16 == 0 && aligned16(kidx_new) && aligned16(k_idx);
+  a.err = err;
+  return cuda_status(launch_kv4_append(a, s.batch, stream));
+}
+
+int csa2_kv4_rows(const csa2_shape* shape, const void* kv4, const int32_t* idx, int32_t n_rows, void* k_out, void* v_out,
+                  int32_t k_exp, int32_t v_exp, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  if (n_rows < 1) return CSA2_ERR_INVALID_ARG;
+  if (int64_t(s.batch) * n_rows > 0x7fffffffLL) return CSA2_ERR_UNSUPPORTED;
+  CSA2_TRY(check_exps(k_exp, v_exp));
+  if (kv4 == nullptr || idx == nullptr || k_out == nullptr || v_out == nullptr) return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(kv4) || !aligned(elem_size(s.dtype), k_out, v_out) || !aligned(4, idx)) return CSA2_ERR_INVALID_ARG;
+  int* err = nullptr;
+  CSA2_TRY(error_word(s, ws, ws_bytes, &err));
+  const uint64_t B = s.batch, R = n_rows, e = elem_size(s.dtype);
+  Span spans[] = {{kv4, B / seqdiv(s) * s.n_entries * kv4_bytes(s.k_dim, s.v_dim), false}, {idx, B * R * 4, false},
+                  {k_out, B * R * s.k_dim * e, true}, {v_out, B * R * s.v_dim * e, true}, {ws, ws_bytes, true}};
+  if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
+  Kv4RowsArgs a{};
+  a.kv = static_cast<const uint8_t*>(kv4);
+  a.idx = idx;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.seq_div = seqdiv(s);
+  a.n_entries = s.n_entries;
+  a.rows = n_rows;
+  a.k_dim = s.k_dim;
+  a.v_dim = s.v_dim;
+  a.dtype = s.dtype;
+  a.k_up = std::ldexp(1.f, k_exp);
+  a.v_up = std::ldexp(1.f, v_exp);
+  a.wide = s.k_dim * e % 16 == 0 && s.v_dim * e % 16 == 0 && aligned16(k_out) && aligned16(v_out);
+  a.err = err;
+  return cuda_status(launch_kv4_rows(a, s.batch, stream));
+}
+
+int csa2_kv4_attn(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa,
+                  const void* v_swa, const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp, void* ws,
+                  size_t ws_bytes, csa2_stream_t stream) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  CSA2_TRY(check_ws(s, ws, ws_bytes));
+  if (s.batch > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
+  CSA2_TRY(check_exps(k_exp, v_exp));
+  if (q == nullptr || kv4 == nullptr || idx == nullptr || out == nullptr) return CSA2_ERR_INVALID_ARG;
+  CSA2_TRY(check_sswa(s, k_swa, v_swa, n_swa));
+  const bool fast = attn_fast(s);
+  if (!aligned16(kv4) || (fast && !(aligned16(q) && aligned16(k_swa) && aligned16(v_swa) && aligned16(out))))
+    return CSA2_ERR_INVALID_ARG;
+  if (!aligned(elem_size(s.dtype), q, k_swa, v_swa, out) || !aligned(4, idx, n_swa, lse)) return CSA2_ERR_INVALID_ARG;
+  const uint64_t B = s.batch, kb = s.k_dim * elem_size(s.dtype), vb = s.v_dim * elem_size(s.dtype);
+  Span spans[] = {{q, B * s.q_heads * kb, false}, {kv4, B / seqdiv(s) * s.n_entries * kv4_bytes(s.k_dim, s.v_dim), false},
+                  {idx, B * s.topk * 4, false}, {k_swa, B * s.swa * kb, false}, {v_swa, B * s.swa * vb, false}, {n_swa, B * 4, false},
+                  {out, B * s.q_heads * vb, true}, {lse, B * s.q_heads * 4, true}, {ws, ws_bytes, true}};
+  if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
+  Kv4AttnArgs a{};
+  a.q = q;
+  a.kv = static_cast<const uint8_t*>(kv4);
+  a.idx = idx;
+  a.k_swa = k_swa;
+  a.v_swa = v_swa;
+  a.n_swa = n_swa;
+  a.out = out;
+  a.lse = lse;
+  a.seq_div = seqdiv(s);
+  a.n_entries = s.n_entries;
+  a.topk = s.topk;
+  a.swa = s.swa;
+  a.heads = s.q_heads;
+  a.k_dim = s.k_dim;
+  a.v_dim = s.v_dim;
+  a.dtype = s.dtype;
+  a.scale = softmax_scale(s);
+  a.k_up = std::ldexp(1.f, k_exp);
+  a.v_up = std::ldexp(1.f, v_exp);
+  a.wide = s.k_dim % 16 == 0 && s.v_dim % 16 == 0 && aligned16(k_swa) && aligned16(v_swa);
+  a.err = static_cast<int*>(ws);
+  return cuda_status(launch_kv4_attn(a, fast, s.batch, stream));
 }
 
 const char* csa2_status_str(int status) {

@@ -1,0 +1,72 @@
+// Device side of the packed entries: groups of 16 dims, 16 codes of 4 bits (e2m1:
+// 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and one scale of 8 bits (e4m3), value = code *
+// scale * 2^exp.  A code has 2 significant bits and a scale 4, so that a value has 6
+// and bf16 and fp16 hold code * scale (up to 2,688, at least 2^-10) exactly.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kv4.h"
+
+namespace csa2 {
+
+// A scale as a number: NaN for the byte 0x7f, which marks a group that held a NaN or an infinity.
+CSA2_DEV __half kv4_scale(uint8_t byte) { return __half(__nv_cvt_fp8_to_halfraw(byte, __NV_E4M3)); }
+
+// Two codes (the first in the low bits) as numbers.
+CSA2_DEV __half2 kv4_pair(uint8_t byte) { return __half2(__nv_cvt_fp4x2_to_halfraw2(byte, __NV_E2M1)); }
+
+// Eight codes times their scale, exactly.
+CSA2_DEV void kv4_eight(uint32_t codes, __half2 scale, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __half22float2(__hmul2(kv4_pair(uint8_t(codes >> (8 * i))), scale));
+    x[2 * i] = v.x;
+    x[2 * i + 1] = v.y;
+  }
+}
+
+// Eight codes times their scale as bf16 pairs, exactly.
+CSA2_DEV uint4 kv4_eight_bf16(uint32_t codes, __half2 scale) {
+  float x[8];
+  kv4_eight(codes, scale, x);
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+
+// 16 numbers as codes and a scale's byte.  The scale is the e4m3 number nearest to a sixth of the
+// largest magnitude (ties to even, at least 2^-9, at most 448), a code the e2m1 number nearest to x / scale (ties to even, at
+// most 6).  kDivide: x are any fp32 numbers, whose quotients are rounded to fp32 first; that moves none onto a
+// border between two codes, as the border times the scale is itself an fp32 number and its neighbours' quotients
+// are more than half a step away.  Without it they have 8 significant bits (bf16): a quotient that
+// is not on a border is 2^-8 away from it, so that a product with 1 / scale, off by 2^-23, rounded to 14 bits tells.
+template <bool kDivide>
+CSA2_DEV uint8_t kv4_quantise(float (&x)[16], float down, uint2& codes) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    x[i] *= down;
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+  }
+  codes = make_uint2(0u, 0u);
+  if (!(top < INFINITY)) return 0x7f;
+  const uint8_t byte = __nv_cvt_float_to_fp8(fmaxf(__fdiv_rn(top, 6.f), 0.001953125f), __NV_SATFINITE, __NV_E4M3);
+  const float scale = __half2float(kv4_scale(byte)), inv = __fdiv_rn(1.f, scale);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float2 y;
+    if (kDivide) {
+      y = make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
+    } else {
+      y = make_float2(__uint_as_float((__float_as_uint(x[2 * i] * inv) + 0x200u) & ~0x3ffu),
+                      __uint_as_float((__float_as_uint(x[2 * i + 1] * inv) + 0x200u) & ~0x3ffu));
+    }
+    w[i >> 2] |= uint32_t(__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest)) << (8 * (i & 3));
+  }
+  codes = make_uint2(w[0], w[1]);
+  return byte;
+}
+
+}  // namespace csa2

@@ -26,13 +26,14 @@
 // precomputed reciprocal.
 #include "common.cuh"
 #include "draft.h"
+#include "rope.cuh"
 
 namespace csa2 {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxPairs = 512;
+constexpr int kThreads = kRopeThreads;
+constexpr int kMaxPairs = kMaxRopePairs;
 constexpr int kMaxRows = 8, kMaxAngles = kMaxRows * kMaxPairs, kMaxVecs = 4096;   // of a block
 constexpr int kBatch = 4;   // vectors a thread loads before it stores any
 
@@ -40,9 +41,6 @@ CSA2_DEV float to_f32(float v) { return v; }
 CSA2_DEV float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 CSA2_DEV void from_f32(float& d, float v) { d = v; }
 CSA2_DEV void from_f32(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
-
-// n / d for n * d < 2^32, with m = ceil(2^32 / d) (0 for d = 1).
-CSA2_DEV int fast_div(int n, uint32_t m) { return m == 0 ? n : int(__umulhi(uint32_t(n), m)); }
 
 // The heads [h0, h0 + nh) of rows row0 .. row0 + nr - 1 of one tensor; `items`
 // of a head are shared out over the block's threads.
@@ -78,25 +76,6 @@ CSA2_DEV void turn_word(uint32_t& a, uint32_t& b, float c, float s) {
   a = __float_as_uint(f * c - g * s);
   b = __float_as_uint(g * c + f * s);
 }
-
-// A vector of 16 or 8 bytes, as words.
-template <int kBytes>
-struct Vec {
-  uint32_t w[kBytes / 4];
-  CSA2_DEV void load(const uint8_t* p) {
-    if constexpr (kBytes == 16) {
-      const uint4 v = *reinterpret_cast<const uint4*>(p);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
-      w[0] = v.x, w[1] = v.y;
-    }
-  }
-  CSA2_DEV void store(uint8_t* p) const {
-    if constexpr (kBytes == 16) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  }
-};
 
 // The turned vectors of the half layout: vector i and its partner rot / 2 further.
 template <bool kBf16, int kBytes>
@@ -239,27 +218,7 @@ __global__ void __launch_bounds__(kThreads, 4) rope_kernel(const __grid_constant
   pdl_wait();   // no early trigger: the attention may read what this kernel writes before its own wait
   const int half = a.rot / 2;
   const float mag = a.inverse ? 1.f / a.mag : a.mag;
-  auto turns = [&](int p) -> long long {                 // per position, in units of 2^-64
-    double f = a.freqs[p] * 0.15915494309189533577;
-    f -= rint(f);                                        // whole turns change nothing
-    return __double2ll_rn(f * 18446744073709551616.0);   // saturates at half a turn, 2^-64 off
-  };
-  // Once a block where a thread has several angles (fp64 is slow); otherwise no
-  // barrier holds back the threads that have none (8 rows: 6.5 us, with the barrier 6.9).
-  auto angle = [&](int i, int r, long long F) {
-    const unsigned long long t = (unsigned long long)(long long)a.pos[row0 + r] * (unsigned long long)F;
-    const float turn = float((long long)t) * 5.421010862427522e-20f;  // * 2^-64: in [-1/2, 1/2]
-    float s, c;
-    sincospif(2.f * turn, &s, &c);
-    cs[i] = make_float2(c * mag, (a.inverse ? -s : s) * mag);
-  };
-  if (nr * half > kThreads) {
-    for (int p = threadIdx.x; p < half; p += kThreads) step[p] = turns(p);
-    __syncthreads();
-    for (int i = threadIdx.x; i < nr * half; i += kThreads) angle(i, i / half, step[i % half]);
-  } else if (int(threadIdx.x) < nr * half) {
-    angle(threadIdx.x, threadIdx.x / half, turns(threadIdx.x % half));
-  }
+  rope_angles(cs, step, row0, nr, half, a.pos, a.freqs, mag, a.inverse != 0);
   // tensor k's heads of this block (nh == 0: none) and their place
   auto part = [&](int k, int& nh, const uint8_t*& x, uint8_t*& out) -> const RopeArgs::Slot& {
     const RopeArgs::Slot& y = a.slot[k];
