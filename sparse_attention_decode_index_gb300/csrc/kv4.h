@@ -6,7 +6,7 @@
 namespace csa2 {
 
 // Keys of once_per_device, behind DraftSetupKey's.
-enum Kv4SetupKey { kSetupKv4Attn = 32, kSetupKv4Tc, kSetupKv4Generic };   // the last and the next five: element types, heads a CTA
+enum Kv4SetupKey { kSetupKv4Tc = 32, kSetupKv4Generic };   // the last and the next two: heads a CTA
 
 // Norm of heads with rotary positions (norm_rope.cu).
 struct NormRopeArgs {
@@ -82,7 +82,8 @@ struct Kv4AttnArgs {
   int* err;
 };
 
-// fast: bf16, 64 heads, dk 192, dv 128
+// bf16, 64 heads, dk 192, dv 128
+cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, int batch, cudaStream_t st);   // kv4_tc.cu
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, bool fast, int batch, cudaStream_t st);
 
 }  // namespace csa2

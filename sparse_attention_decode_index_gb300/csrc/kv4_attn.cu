@@ -234,8 +234,8 @@ cudaError_t launch_generic(const Kv4AttnArgs& a, int batch, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, bool fast, int batch, cudaStream_t st) {
-  (void)fast;
   if (batch == 0) return cudaSuccess;
+  if (fast) return launch_kv4_attn_tc(a, batch, st);
   return launch_generic<4>(a, batch, st);
 }
 
