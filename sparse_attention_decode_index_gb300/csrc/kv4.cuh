@@ -18,21 +18,36 @@ CSA2_DEV __half kv4_scale(uint8_t byte) { return __half(__nv_cvt_fp8_to_halfraw(
 // Two codes (the first in the low bits) as numbers.
 CSA2_DEV __half2 kv4_pair(uint8_t byte) { return __half2(__nv_cvt_fp4x2_to_halfraw2(byte, __NV_E2M1)); }
 
+// Eight codes of a word as four pairs.  (The bytes are named in the conversion: taken out of the word first, each cost two
+// instructions more.)
+CSA2_DEV void kv4_pairs(uint32_t codes, __half2 (&x)[4]) {
+  uint32_t y[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+      : "r"(codes));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const __half2*>(&y[i]);
+}
+
+// Two scales, in the low bits, as numbers.
+CSA2_DEV __half2 kv4_scales(uint32_t two) {
+  uint32_t y;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(y) : "r"(two));
+  return *reinterpret_cast<const __half2*>(&y);
+}
+
 // Eight codes times their scale, exactly.
 CSA2_DEV void kv4_eight(uint32_t codes, __half2 scale, float (&x)[8]) {
+  __half2 y[4];
+  kv4_pairs(codes, y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 v = __half22float2(__hmul2(kv4_pair(uint8_t(codes >> (8 * i))), scale));
+    const float2 v = __half22float2(__hmul2(y[i], scale));
     x[2 * i] = v.x;
     x[2 * i + 1] = v.y;
   }
-}
-
-// Eight codes times their scale as bf16 pairs, exactly.
-CSA2_DEV uint4 kv4_eight_bf16(uint32_t codes, __half2 scale) {
-  float x[8];
-  kv4_eight(codes, scale, x);
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
 // 16 numbers as codes and a scale's byte.  The scale is the e4m3 number nearest to a sixth of the

@@ -25,6 +25,8 @@
 // cluster of up to 8 CTAs, whose partial O are merged through distributed shared memory as in attn.cu.
 //
 // P is rounded to fp16 (entries) or bf16 (window) as the tensor core asks for; the weights' sums stay fp32 and unrounded.
+#include <cuda.h>
+
 #include "kv4.cuh"
 #include "tc.cuh"
 
@@ -43,6 +45,7 @@ constexpr int kSoftmaxWarps = 4, kEndWarps = 4, kProducerWarps = 8;
 constexpr int kRows = kTile / kProducerWarps;  // entries of a producer warp: 8
 constexpr int kPackedRow = kEntry + 16;        // padded: rows of 4 lanes' words meet no bank twice
 constexpr int kThreads = 32 * (kSoftmaxWarps + kEndWarps + kProducerWarps + 1);
+constexpr int kIndexRing = 4 * kAhead;         // tiles whose indices are on their way or there
 constexpr int kMaxCluster = 8;
 constexpr int kQRow = kDk * 2 + 16;            // query rows on their way to TMEM
 constexpr int kXRow = 36;                      // fp32 columns of a row that the halves exchange, padded
@@ -57,6 +60,7 @@ struct Shared {
   uint8_t k[kStages][kKBytes];                 // 3 blocks of 64 dims: 64 rows of 128 bytes
   uint8_t v[kStages][kVBytes];                 // 2 blocks of 64 dims: 64 keys of 128 bytes
   uint8_t packed[kProducerWarps][kAhead][kRows * kPackedRow];
+  int index[kProducerWarps][kIndexRing][kRows];
   uint8_t q[kH * kQRow];
   float x[128 * kXRow];
   uint64_t mask[kStages];                      // the tile's keys that are there
@@ -67,6 +71,7 @@ struct Shared {
   uint64_t s_full[2], p_full[2];               // S has been computed; P has been written
   uint64_t o_done, o_last, o_free;             // O holds a tile more; the item's last; has been read
   uint64_t q_full, q_empty, stat_full, stat_free;
+  uint64_t window;                             // a window tile that is not full has landed
   uint64_t ends;                               // the end warps have come here
   uint64_t fin;                                // every MMA is done
   uint32_t tmem;
@@ -89,6 +94,34 @@ CSA2_DEV uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// A bounded wait of a whole warp, which goes on or gives up together (as tc_wait_warp, counted in cycles: many warps wait here).
+constexpr long long kWaitCycles = 4000000000ll;   // 2 s at the highest clock
+CSA2_DEV bool wait_warp(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
+  bool here = mbar_try_wait(bar, parity);
+  if (!here) {
+    const long long t0 = clock64();
+    for (uint32_t i = 1;; ++i) {
+      here = mbar_try_wait(bar, parity);
+      if (here) break;
+      if ((i & 31u) == 0u) {
+        if (c.abort) break;
+        if (clock64() - t0 > kWaitCycles) {
+          c.abort = 1;
+          report(err, kErrTimeout, int(threadIdx.x));   // which role gave up first
+          break;
+        }
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, here) != 0;
+}
+
+// One arrival for a whole warp's reads and writes so far.
+CSA2_DEV void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // The tiles of a query that CTA `rank` of `n` takes.
 struct Range {
   int first, last, window;                     // [first, last) of a query's tiles; how many are the window's
@@ -100,7 +133,17 @@ struct Range {
   }
 };
 
-__global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a, int n_items, int ncta) {
+// A box of 64 rows of 64 dims, swizzled, from dim x of row y (TMA).
+CSA2_DEV void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    kv4_tc_kernel(const Kv4AttnArgs a, int n_items, int ncta, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map) {
   extern __shared__ uint8_t raw[];
   Shared& c = *reinterpret_cast<Shared*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -108,20 +151,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
   const int item0 = int(blockIdx.x) / ncta, step = int(gridDim.x) / ncta;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&c.full[i], 33 * kProducerWarps);              // every lane's rows, every warp's mask
+      mbar_init(&c.full[i], kProducerWarps);
       mbar_init(&c.empty[i], 1 + kSoftmaxWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.s_full[b], 1);
-      mbar_init(&c.p_full[b], 128);
+      mbar_init(&c.p_full[b], kSoftmaxWarps);
     }
     mbar_init(&c.o_done, 1);
     mbar_init(&c.o_last, 1);
-    mbar_init(&c.o_free, 128);
-    mbar_init(&c.q_full, 128);
+    mbar_init(&c.o_free, kEndWarps);
+    mbar_init(&c.q_full, kEndWarps);
     mbar_init(&c.q_empty, 1);
-    mbar_init(&c.stat_full, 128);
-    mbar_init(&c.stat_free, 128);
+    mbar_init(&c.stat_full, kSoftmaxWarps);
+    mbar_init(&c.stat_free, kEndWarps);
+    mbar_init(&c.window, 1);
     mbar_init(&c.ends, kEndWarps);
     mbar_init(&c.fin, 1);
     c.abort = 0;
@@ -151,11 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
       float ref = -INFINITY, sum = 0.f;        // the exponent that P and O are relative to, and the weights' sum
       bool first = true;
       for (int t = range.first; t < range.last; ++t) {
-        ok = tc_wait_warp(c, &c.full[st], lap & 1, a.err);
+        ok = wait_warp(c, &c.full[st], lap & 1, a.err);
         if (!ok) break;
         const uint64_t all = c.mask[st];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c.empty[st]);
+        warp_arrive(&c.empty[st]);
         if (++st == kStages) {
           st = 0;
           ++lap;
@@ -164,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
         const uint32_t mask = uint32_t(all >> (32 * half));
         const bool window = t < range.window;
         const uint32_t buf = tiles & 1, s_addr = tmem + lanes + kSCol + buf * 64;
-        ok = tc_wait_warp(c, &c.s_full[buf], (tiles >> 1) & 1, a.err);
+        ok = wait_warp(c, &c.s_full[buf], (tiles >> 1) & 1, a.err);
         if (!ok) break;
         tc_fence_after();
         uint32_t p[16];
@@ -193,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
           } else if (__any_sync(0xffffffffu, grows)) {
             // O holds tiles up to the one before: wait for it.  (S of this tile comes behind O of the last but one,
             // so that the barrier is in the phase of the last or behind it, and the parity tells which.)
-            ok = tc_wait_warp(c, &c.o_done, (tiles - 1) & 1, a.err);
+            ok = wait_warp(c, &c.o_done, (tiles - 1) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
             const float f = grows ? ex2(ref - top) : 1.f;
@@ -218,7 +261,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
             x.y = ex2(x.y);
             if (j & 1) other = add2(other, x);
             else total = add2(total, x);
-            p[j] = window ? pack_bf16(x.x * window_up, x.y * window_up) : pack_f16(x.x, x.y);
+            s[2 * j] = __float_as_uint(x.x);
+            s[2 * j + 1] = __float_as_uint(x.y);
+          }
+          if (window) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = pack_bf16(__uint_as_float(s[2 * j]) * window_up, __uint_as_float(s[2 * j + 1]) * window_up);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) p[j] = pack_f16(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
           }
           total = add2(total, other);
           sum += total.x + total.y;
@@ -235,14 +286,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
         tmem_st16(s_addr + 16 * (1 - half), zero);
         tc_wait_st();
         tc_fence_before();
-        mbar_arrive(&c.p_full[buf]);
+        warp_arrive(&c.p_full[buf]);
         ++tiles;
       }
       if (!ok) break;
-      ok = items == 0 || tc_wait_warp(c, &c.stat_free, (items - 1) & 1, a.err);
+      ok = items == 0 || wait_warp(c, &c.stat_free, (items - 1) & 1, a.err);
       if (!ok) break;
       c.stat[tid] = make_float2(ref - kUp, sum);
-      mbar_arrive(&c.stat_full);
+      warp_arrive(&c.stat_full);
       ++items;
     }
   } else if (warp < kSoftmaxWarps + kEndWarps) {
@@ -251,9 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
     const uint32_t lanes = uint32_t(w * 32) << 16;
     uint32_t met = 0;
     auto end_sync = [&]() -> bool {                           // the end warps wait for each other (a bounded wait, as all are)
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.ends);
-      return tc_wait_warp(c, &c.ends, met++ & 1, a.err);
+      warp_arrive(&c.ends);
+      return wait_warp(c, &c.ends, met++ & 1, a.err);
     };
     auto copy_q = [&](int item) {                             // into shared memory
       if (item < n_items) {
@@ -302,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
       c.q_scale[parity][row] = fminf(ldexpf(a.scale * log2e * a.k_up, e), 3e38f);
       tc_wait_st();
       tc_fence_before();
-      mbar_arrive(&c.q_full);
+      warp_arrive(&c.q_full);
       return end_sync();                                      // the copy in shared memory has been read
     };
     uint32_t items = 0;
@@ -315,20 +365,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
     for (int item = item0; item < n_items && ok; item += step, ++items) {
       if (item + step < n_items) {
         // (its scales lie where those of the item before this one lay, whose softmax is over)
-        if (!tc_wait_warp(c, &c.q_empty, items & 1, a.err)) break;
+        if (!wait_warp(c, &c.q_empty, items & 1, a.err)) break;
         tc_fence_after();
         if (!store_q((items + 1) & 1)) break;
         copy_q(item + 2 * step);
       }
-      if (!tc_wait_warp(c, &c.stat_full, items & 1, a.err)) break;
+      if (!wait_warp(c, &c.stat_full, items & 1, a.err)) break;
       const float2 mine = c.stat[row], theirs = c.stat[row ^ 64];
-      mbar_arrive(&c.stat_free);
+      warp_arrive(&c.stat_free);
       const float top = fmaxf(mine.x, theirs.x);
       const float weight = mine.x == -INFINITY ? 0.f : ex2(mine.x - top);
       const float sum = mine.y * weight + theirs.y * (theirs.x == -INFINITY ? 0.f : ex2(theirs.x - top));
       const bool none = sum == 0.f;                           // no key: O may hold anything
       const float f = ncta > 1 ? weight : weight * (a.v_up / sum);
-      if (!tc_wait_warp(c, &c.o_last, items & 1, a.err)) break;
+      if (!wait_warp(c, &c.o_last, items & 1, a.err)) break;
       tc_fence_after();
       // a thread ends with 64 columns of its head: it gives its part of the others to its partner of the other half
 #pragma unroll 1
@@ -343,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
         tmem_ld32(o, tmem + lanes + kOCol + 64 * side + 32 * b);
         if (b == 1) {
           tc_fence_before();
-          mbar_arrive(&c.o_free);
+          warp_arrive(&c.o_free);
         }
         ok = end_sync();
         if (!ok) break;
@@ -398,117 +448,150 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
     const int w = warp - kSoftmaxWarps - kEndWarps;
     const int m0 = max(range.first, range.window) - range.window, nm = max(range.last, range.window) - range.window - m0;
     const uint32_t ring = smem_u32(c.packed[w][0]);
-    // the index of this lane's row (lanes 0..7) of main tile i of an item
-    auto index_of = [&](int item, int i) -> int {
-      const int slot = (m0 + i) * kTile + kRows * w + lane;
-      if (lane >= kRows || item >= n_items || slot >= a.topk) return -1;
-      return a.idx[(long long)item * a.topk + slot];
+    // The main tiles of this CTA's items are one stream.  A tile's indices are copied 2 kAhead tiles before it is turned into
+    // rows, its entries kAhead before.  (As loads into registers the indices were waited for a tile at a time, 0.5 us each.)
+    const int my_slot = m0 * kTile + kRows * w + (lane & 7);
+    auto copy_index = [&](int n, int item, int i) {           // of tile n of the stream, lanes 0..7
+      const int slot = my_slot + i * kTile;
+      if (lane < kRows && item < n_items && slot < a.topk)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&c.index[w][n % kIndexRing][lane])),
+                     "l"(a.idx + (long long)item * a.topk + slot)
+                     : "memory");
     };
-    int f_item = item0, f_i = 0;               // the main tile whose indices are loaded next
-    auto advance = [&]() {
-      if (++f_i == nm) {
-        f_i = 0;
-        f_item += step;
+    struct Place {
+      int item, i;
+    };
+    auto advance = [&](Place& p) {
+      if (++p.i == nm) {
+        p.i = 0;
+        p.item += step;
       }
     };
     uint32_t there = 0;                        // 8 bits for each tile on its way
-    auto fetch = [&](int slot, int item, int e) {
+    int last_item = -1;                        // whose sequence's cache this is
+    const uint8_t* cache = a.kv;
+    auto fetch = [&](int slot, Place p, int e) {
+      if (lane >= kRows || p.item >= n_items || my_slot + p.i * kTile >= a.topk) e = -1;
       if (e >= a.n_entries) {
         report(a.err, kErrBadIndex, e);
         e = -1;
       }
       there = (there & ~(0xffu << (8 * slot))) | (__ballot_sync(0xffffffffu, e >= 0) & 0xffu) << (8 * slot);
-      if (item < n_items) {
-        const uint8_t* cache = a.kv + (long long)(item / a.seq_div) * a.n_entries * kEntry;
+      if (p.item < n_items) {
+        if (p.item != last_item) {
+          last_item = p.item;
+          cache = a.kv + (long long)(p.item / a.seq_div) * a.n_entries * kEntry;
+        }
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
-          const int p = 32 * x + lane, r = p / 12, part = p - 12 * r;
+          const int p12 = 32 * x + lane, r = p12 / 12, part = p12 - 12 * r;
           const int entry = __shfl_sync(0xffffffffu, e, r);
           cp16(ring + slot * (kRows * kPackedRow) + r * kPackedRow + 16 * part,
                entry >= 0 ? cache + (long long)entry * kEntry + 16 * part : nullptr, a.kv);
         }
       }
-      cp_commit();                             // (possibly of nothing: the groups count the tiles)
     };
-    int e = -1, e_item = n_items;              // the indices of the tile to fetch next
+    Place next{item0, 0}, next_index{item0, 0};   // the tile to fetch next, and the one whose indices are
+    int n_index = 0;                           // its place in the stream
     if (nm > 0) {
-      int es[kAhead], its[kAhead];             // (their loads together)
+      int es[kAhead];                          // (the first loads together)
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        its[j] = f_item;
-        es[j] = index_of(f_item, f_i);
-        advance();
+        const int slot = my_slot + next_index.i * kTile;
+        es[j] = a.idx[(long long)min(next_index.item, n_items - 1) * a.topk + min(slot, a.topk - 1)];
+        advance(next_index);
       }
+      n_index = kAhead;
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) fetch(j, its[j], es[j]);
-      e_item = f_item;
-      e = index_of(f_item, f_i);
-      advance();
+      for (int j = 0; j < kAhead; ++j) {
+        fetch(j, next, es[j]);
+        advance(next);
+        copy_index(n_index++, next_index.item, next_index.i);
+        advance(next_index);
+        cp_commit();                           // (possibly of nothing: the groups count the tiles)
+      }
     }
+    int n_fetch = kAhead;                      // the place in the stream of the tile to fetch next
     uint32_t st = 0, lap = 0;
     int slot = 0;
     const int r8 = lane & 7, q4 = lane >> 3;
+    const uint32_t pick = q4 < 2 ? 0x4420u : 0x4431u;   // bytes 0 and 2, or 1 and 3, of four
     // byte offsets of this lane's pieces 4 (k % 2) + q4 of a stage's row 8 w + r8
     const uint32_t even = (kRows * w + r8) * 128 + ((q4 ^ r8) << 4), odd = (kRows * w + r8) * 128 + (((4 + q4) ^ r8) << 4);
     bool ok = true;
+    uint32_t waits = 0;
     int n_next = item0 < n_items ? a.n_swa[item0] : 0;
     for (int item = item0; item < n_items && ok; item += step) {
       const int ns = clamp_count(n_next, a.swa, w == 0 && lane == 0 && crank == 0 ? a.err : nullptr);
       if (item + step < n_items) n_next = a.n_swa[item + step];
       for (int t = range.first; t < range.last; ++t) {
-        ok = tc_wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
+        ok = wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
         if (!ok) break;
         const uint32_t k_st = smem_u32(c.k[st]), v_st = smem_u32(c.v[st]);
-        uint8_t* mask = reinterpret_cast<uint8_t*>(&c.mask[st]) + w;
         if (t < range.window) {
-          const int row0 = t * kTile + kRows * w;             // of the window
-          const long long base = (long long)item * a.swa + row0;
+          // window rows lie one behind the other: the first warp has them copied by TMA, the others only count the tile (every
+          // warp passes every stage's turns, as their parity tells no more than one from the next)
+          const int n = min(max(ns - t * kTile, 0), kTile), y = item * a.swa + t * kTile;
+          if (w > 0 || n == 0) {
+            if (w == 0 && lane == 0) c.mask[st] = 0;
+            warp_arrive(&c.full[st]);
+          } else {
+            uint64_t* bar = n == kTile ? &c.full[st] : &c.window;
+            if (lane == 0) {
+              c.mask[st] = n == kTile ? ~0ull : (1ull << n) - 1ull;
+              mbar_arrive_expect_tx(bar, kKBytes + kVBytes);
 #pragma unroll
-          for (int x = 0; x < 10; ++x) {
-            const int p = 32 * x + lane, r = p / 40, part = p - 40 * r;
-            const bool key = part < 24, has = row0 + r < ns;
-            const int y = key ? part : part - 24;
-            const uint8_t* src = key ? static_cast<const uint8_t*>(a.k_swa) + (base + r) * (kDk * 2)
-                                     : static_cast<const uint8_t*>(a.v_swa) + (base + r) * (kDv * 2);
-            cp16((key ? k_st : v_st) + (y >> 3) * (kTile * 128) + (kRows * w + r) * 128 + (((y & 7) ^ r) << 4),
-                 has ? src + 16 * y : nullptr, a.kv);
+              for (int b = 0; b < kDk / 64; ++b) load_box(k_st + b * (kTile * 128), &k_map, 64 * b, y, bar);
+#pragma unroll
+              for (int b = 0; b < kDv / 64; ++b) load_box(v_st + b * (kTile * 128), &v_map, 64 * b, y, bar);
+            }
+            __syncwarp();
+            if (n < kTile) {                   // values behind the count are zeroed: they meet weights of 0, and might be NaN
+              ok = wait_warp(c, &c.window, waits++ & 1, a.err);
+              if (!ok) break;
+              for (int i = lane; i < (kTile - n) * 16; i += 32) {
+                const int r = n + (i >> 4), p = i & 15;
+                *reinterpret_cast<uint4*>(c.v[st] + (p >> 3) * (kTile * 128) + r * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+              }
+              warp_arrive(&c.full[st]);
+            }
           }
-          if (lane == 0) {
-            *mask = uint8_t((1u << min(max(ns - row0, 0), kRows)) - 1u);
-            mbar_arrive(&c.full[st]);
-          }
-          cp_arrive(&c.full[st]);
         } else {
           asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
           __syncwarp();
+          // (all loads before the first store, which they would otherwise wait for)
           const uint8_t* src = c.packed[w][slot] + r8 * kPackedRow;
-          const uint32_t* codes = reinterpret_cast<const uint32_t*>(src) + q4;
-          const uint32_t* scales = reinterpret_cast<const uint32_t*>(src + kScales);
+          uint32_t word[10], four[5];
+          __half2 two[5];                                     // the scales of groups 4 k + q4 / 2 and 2 behind it
+#pragma unroll
+          for (int k = 0; k < 5; ++k) four[k] = reinterpret_cast<const uint32_t*>(src + kScales)[k];
+#pragma unroll
+          for (int k = 0; k < 10; ++k) word[k] = reinterpret_cast<const uint32_t*>(src)[4 * k + q4];
+#pragma unroll
+          for (int k = 0; k < 5; ++k) two[k] = kv4_scales(__byte_perm(four[k], 0, pick));
 #pragma unroll
           for (int k = 0; k < 10; ++k) {                      // words 4 k + q4: 0..23 of the key, 24..39 of the value
-            const uint32_t pair = scales[k >> 1] >> (8 * (q4 >> 1));   // groups 2 k + q4 / 2, k even and odd
-            const __half2 scale = __half2half2(kv4_scale(uint8_t(k & 1 ? pair >> 16 : pair)));
-            const uint32_t word = codes[4 * k];
+            const __half2 scale = k & 1 ? __high2half2(two[k >> 1]) : __low2half2(two[k >> 1]);
+            __half2 x[4];
+            kv4_pairs(word[k], x);
             uint32_t y[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __half2 h = __hmul2(kv4_pair(uint8_t(word >> (8 * i))), scale);
-              y[i] = *reinterpret_cast<const uint32_t*>(&h);
+              x[i] = __hmul2(x[i], scale);
+              y[i] = *reinterpret_cast<const uint32_t*>(&x[i]);
             }
             const uint32_t to = (k < 6 ? k_st + (k >> 1) * (kTile * 128) : v_st + ((k - 6) >> 1) * (kTile * 128)) + (k & 1 ? odd : even);
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
           }
-          if (lane == 0) {
-            *mask = uint8_t(there >> (8 * slot));
-            mbar_arrive(&c.full[st]);
-          }
-          fence_async_smem();
-          mbar_arrive(&c.full[st]);
-          __syncwarp();                        // every lane has read the packed entries
-          fetch(slot, e_item, e);
-          e_item = f_item;
-          e = index_of(f_item, f_i);
-          advance();
+          if (lane == 0) reinterpret_cast<uint8_t*>(&c.mask[st])[w] = uint8_t(there >> (8 * slot));
+          const int e = c.index[w][n_fetch % kIndexRing][lane & 7];
+          warp_arrive(&c.full[st]);            // (and every lane has read the packed entries)
+          fetch(slot, next, e);
+          advance(next);
+          ++n_fetch;
+          copy_index(n_index++, next_index.item, next_index.i);
+          advance(next_index);
+          cp_commit();
           slot = (slot + 1) % kAhead;
         }
         if (++st == kStages) {
@@ -518,6 +601,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok) {                                 // given up: 10 ms for window rows that may still be on their way
+      const long long t0 = clock64();
+      while (clock64() - t0 < 20000000) {
+      }
+    }
   } else {
     // ---------------------------------------------------------------- MMA issue
     constexpr uint32_t qk_h = idesc_f16(128, kTile, false), pv_h = idesc_f16(128, kDv, true);
@@ -530,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
       uint32_t was_st = 0;
       auto pv = [&]() -> bool {
         const uint32_t x = tiles - 1, buf = x & 1;
-        if (first && items > 0 && !tc_wait_warp(c, &c.o_free, (items - 1) & 1, a.err)) return false;
-        if (!tc_wait_warp(c, &c.p_full[buf], (x >> 1) & 1, a.err)) return false;
+        if (first && items > 0 && !wait_warp(c, &c.o_free, (items - 1) & 1, a.err)) return false;
+        if (!wait_warp(c, &c.p_full[buf], (x >> 1) & 1, a.err)) return false;
         tc_fence_after();
         const uint64_t v = v0 + was_st * (kVBytes >> 4);
         if (elect_one()) {
@@ -545,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
         first = false;
         return true;
       };
-      ok = tc_wait_warp(c, &c.q_full, items & 1, a.err);
+      ok = wait_warp(c, &c.q_full, items & 1, a.err);
       for (int t = range.first; t < range.last && ok; ++t) {
-        ok = tc_wait_warp(c, &c.full[st], lap & 1, a.err);
+        ok = wait_warp(c, &c.full[st], lap & 1, a.err);
         if (!ok) break;
         const uint64_t mask = c.mask[st];
         const uint32_t here = st;
@@ -555,14 +643,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
           st = 0;
           ++lap;
         }
+        // The rows are generic-proxy writes, which the tensor core reads, and TMA overwrites, by the async proxy.  The fence stands
+        // here, behind the wait, and not with the producers: theirs would wait for the copies that are on their way (1.5 us a tile).
+        fence_async_smem();
         if (mask == 0) {                       // no key: nobody looks at it
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&c.empty[here]);
+          warp_arrive(&c.empty[here]);
           if (pending) ok = pv();              // (its stage may be what the next tile waits for)
           pending = false;
           continue;
         }
-        fence_async_smem();                    // the window's copies are generic-proxy writes, the tensor core reads by the async proxy
         tc_fence_after();
         const bool window = t < range.window;
         const uint32_t buf = tiles & 1, q = tmem + (window ? kQbCol : kQhCol), desc = window ? qk_b : qk_h;
@@ -645,6 +734,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_tc_kernel(const Kv4AttnArgs a
 
 }  // namespace
 
+// Rows of `dim` bf16 numbers as boxes of 64 by 64 in the 128-byte swizzle.
+static bool window_map(CUtensorMap* map, const void* rows, int dim, long long n) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static const Encode encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+                    found == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<Encode>(fn) : nullptr;
+  }();
+  if (encode == nullptr) return false;
+  const cuuint64_t size[2] = {cuuint64_t(dim), cuuint64_t(n)}, stride[1] = {cuuint64_t(dim) * 2};
+  const cuuint32_t box[2] = {64, kTile}, each[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(rows), size, stride, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, int batch, cudaStream_t st) {
   const cudaError_t e = once_per_device(kSetupKv4Tc, [] {
     return cudaFuncSetAttribute(kv4_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -654,8 +761,11 @@ cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, int batch, cudaStream_t st)
   int ncta = 1;
   while (ncta < kMaxCluster && 2 * ncta <= tiles && 2 * ncta * batch <= sms) ncta *= 2;
   const int grid = ncta > 1 || batch < sms ? batch * ncta : sms;
+  CUtensorMap k_map{}, v_map{};
+  if (a.swa > 0 && !(window_map(&k_map, a.k_swa, kDk, (long long)batch * a.swa) && window_map(&v_map, a.v_swa, kDv, (long long)batch * a.swa)))
+    return cudaErrorInvalidValue;
   note_launch();
-  return launch_pdl(kv4_tc_kernel, dim3(unsigned(grid)), dim3(kThreads), kSmem, st, unsigned(ncta), a, batch, ncta);
+  return launch_pdl(kv4_tc_kernel, dim3(unsigned(grid)), dim3(kThreads), kSmem, st, unsigned(ncta), a, batch, ncta, k_map, v_map);
 }
 
 }  // namespace csa2
