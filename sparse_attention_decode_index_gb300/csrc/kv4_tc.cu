@@ -40,12 +40,13 @@ constexpr int kEntry = kv4_bytes(kDk, kDv);    // 192: codes 0..159, scales 160.
 constexpr int kScales = 160;
 constexpr int kKBytes = kTile * kDk * 2, kVBytes = kTile * kDv * 2;
 constexpr int kStages = 3;
-constexpr int kAhead = 4;                      // tiles of packed entries on their way
 constexpr int kSoftmaxWarps = 4, kEndWarps = 4, kProducerWarps = 8;
-constexpr int kRows = kTile / kProducerWarps;  // entries of a producer warp: 8
+constexpr int kGroups = 2, kGroupWarps = kProducerWarps / kGroups;   // of producers, which take turns at the tiles
+constexpr int kAhead = 2;                      // tiles of packed entries on their way, of a group
+constexpr int kRows = kTile / kGroupWarps;     // entries of a producer warp: 16
 constexpr int kPackedRow = kEntry + 16;        // padded: rows of 4 lanes' words meet no bank twice
-constexpr int kThreads = 32 * (kSoftmaxWarps + kEndWarps + kProducerWarps + 1);
-constexpr int kIndexRing = 4 * kAhead;         // tiles whose indices are on their way or there
+constexpr int kThreads = 32 * (kSoftmaxWarps + kEndWarps + kProducerWarps + 2);
+constexpr int kIndexRing = 4 * kAhead;         // tiles whose indices are on their way or there, of a group
 constexpr int kMaxCluster = 8;
 constexpr int kQRow = kDk * 2 + 16;            // query rows on their way to TMEM
 constexpr int kXRow = 36;                      // fp32 columns of a row that the halves exchange, padded
@@ -69,9 +70,10 @@ struct Shared {
   float2 part[kMaxCluster][kH];                // (exponent, sum) of the CTAs of a split, of the heads that this one adds up
   uint64_t full[kStages], empty[kStages];      // a tile has landed; has been used
   uint64_t s_full[2], p_full[2];               // S has been computed; P has been written
-  uint64_t o_done, o_last, o_free;             // O holds a tile more; the item's last; has been read
+  uint64_t s_free[2];                          // O holds the tile whose weights lay there
+  uint64_t o_last, o_free;                     // O holds the item's last tile; has been read
   uint64_t q_full, q_empty, stat_full, stat_free;
-  uint64_t window;                             // a window tile that is not full has landed
+  uint64_t window[kGroups];                    // a window tile that is not full has landed
   uint64_t ends;                               // the end warps have come here
   uint64_t fin;                                // every MMA is done
   uint32_t tmem;
@@ -141,6 +143,11 @@ CSA2_DEV void load_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint6
       : "memory");
 }
 
+// The same into L2.
+CSA2_DEV void prefetch_box(const CUtensorMap* map, int x, int y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(map), "r"(x), "r"(y) : "memory");
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     kv4_tc_kernel(const Kv4AttnArgs a, int n_items, int ncta, const __grid_constant__ CUtensorMap k_map,
                   const __grid_constant__ CUtensorMap v_map) {
@@ -151,23 +158,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int item0 = int(blockIdx.x) / ncta, step = int(gridDim.x) / ncta;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&c.full[i], kProducerWarps);
-      mbar_init(&c.empty[i], 1 + kSoftmaxWarps);
+      mbar_init(&c.full[i], kGroupWarps);
+      mbar_init(&c.empty[i], 2 + kSoftmaxWarps);   // the values' end; everyone else who looks at its mask
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&c.s_full[b], 1);
       mbar_init(&c.p_full[b], kSoftmaxWarps);
+      mbar_init(&c.s_free[b], 1);
     }
-    mbar_init(&c.o_done, 1);
     mbar_init(&c.o_last, 1);
     mbar_init(&c.o_free, kEndWarps);
     mbar_init(&c.q_full, kEndWarps);
     mbar_init(&c.q_empty, 1);
     mbar_init(&c.stat_full, kSoftmaxWarps);
     mbar_init(&c.stat_free, kEndWarps);
-    mbar_init(&c.window, 1);
+    for (int g = 0; g < kGroups; ++g) mbar_init(&c.window[g], 1);
     mbar_init(&c.ends, kEndWarps);
-    mbar_init(&c.fin, 1);
+    mbar_init(&c.fin, 2);
     c.abort = 0;
     mbar_fence_init();
   }
@@ -234,9 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (first) {
             ref = top;
           } else if (__any_sync(0xffffffffu, grows)) {
-            // O holds tiles up to the one before: wait for it.  (S of this tile comes behind O of the last but one,
-            // so that the barrier is in the phase of the last or behind it, and the parity tells which.)
-            ok = wait_warp(c, &c.o_done, (tiles - 1) & 1, a.err);
+            // O holds tiles up to the one before: wait for it.
+            ok = wait_warp(c, &c.s_free[buf ^ 1], ((tiles - 1) >> 1) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
             const float f = grows ? ex2(ref - top) : 1.f;
@@ -444,46 +450,52 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp < kSoftmaxWarps + kEndWarps + kProducerWarps) {
-    // ---------------------------------------------------------------- producers: 8 rows of every tile a warp
-    const int w = warp - kSoftmaxWarps - kEndWarps;
-    const int m0 = max(range.first, range.window) - range.window, nm = max(range.last, range.window) - range.window - m0;
-    const uint32_t ring = smem_u32(c.packed[w][0]);
-    // The main tiles of this CTA's items are one stream.  A tile's indices are copied 2 kAhead tiles before it is turned into
-    // rows, its entries kAhead before.  (As loads into registers the indices were waited for a tile at a time, 0.5 us each.)
-    const int my_slot = m0 * kTile + kRows * w + (lane & 7);
-    auto copy_index = [&](int n, int item, int i) {           // of tile n of the stream, lanes 0..7
-      const int slot = my_slot + i * kTile;
-      if (lane < kRows && item < n_items && slot < a.topk)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&c.index[w][n % kIndexRing][lane])),
-                     "l"(a.idx + (long long)item * a.topk + slot)
-                     : "memory");
-    };
+    // ---------------------------------------------------------------- producers: 16 rows of every second tile a warp
+    // (Eight warps on the same tile spent most of it on the latencies of its steps.)
+    const int pw = warp - kSoftmaxWarps - kEndWarps, group = pw / kGroupWarps, w = pw % kGroupWarps;
+    const int nt = range.last - range.first;   // tiles of an item
+    const uint32_t ring = smem_u32(c.packed[pw][0]);
+    // The group's tiles are every second one of all items'.  A main tile's indices are copied 2 kAhead turns before it is turned
+    // into rows, its entries kAhead before.  (As loads into registers the indices were waited for a tile at a time, 0.5 us each.)
     struct Place {
-      int item, i;
+      int item, t;
     };
-    auto advance = [&](Place& p) {
-      if (++p.i == nm) {
-        p.i = 0;
+    auto move = [&](Place& p, int n) {
+      p.t += n;
+      while (p.t >= range.last) {
+        p.t -= nt;
         p.item += step;
       }
     };
-    uint32_t there = 0;                        // 8 bits for each tile on its way
+    auto next_main = [&](Place& p) {           // the group's next tile of entries
+      do move(p, kGroups);
+      while (p.t < range.window && p.item < n_items);
+    };
+    const int my_slot = kRows * w + (lane & 15) - range.window * kTile;   // (+ 64 t: of tile t)
+    auto copy_index = [&](int n, Place p) {    // of the n-th tile of entries, lanes 0..15
+      const int slot = my_slot + p.t * kTile;
+      if (lane < kRows && p.item < n_items && slot < a.topk)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&c.index[pw][n % kIndexRing][lane])),
+                     "l"(a.idx + (long long)p.item * a.topk + slot)
+                     : "memory");
+    };
+    uint32_t there = 0;                        // 16 bits for each tile on its way
     int last_item = -1;                        // whose sequence's cache this is
     const uint8_t* cache = a.kv;
     auto fetch = [&](int slot, Place p, int e) {
-      if (lane >= kRows || p.item >= n_items || my_slot + p.i * kTile >= a.topk) e = -1;
+      if (lane >= kRows || p.item >= n_items || my_slot + p.t * kTile >= a.topk) e = -1;
       if (e >= a.n_entries) {
         report(a.err, kErrBadIndex, e);
         e = -1;
       }
-      there = (there & ~(0xffu << (8 * slot))) | (__ballot_sync(0xffffffffu, e >= 0) & 0xffu) << (8 * slot);
+      there = (there & ~(0xffffu << (16 * slot))) | (__ballot_sync(0xffffffffu, e >= 0) & 0xffffu) << (16 * slot);
       if (p.item < n_items) {
         if (p.item != last_item) {
           last_item = p.item;
           cache = a.kv + (long long)(p.item / a.seq_div) * a.n_entries * kEntry;
         }
 #pragma unroll
-        for (int x = 0; x < 3; ++x) {
+        for (int x = 0; x < 6; ++x) {
           const int p12 = 32 * x + lane, r = p12 / 12, part = p12 - 12 * r;
           const int entry = __shfl_sync(0xffffffffu, e, r);
           cp16(ring + slot * (kRows * kPackedRow) + r * kPackedRow + 16 * part,
@@ -491,78 +503,105 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    Place next{item0, 0}, next_index{item0, 0};   // the tile to fetch next, and the one whose indices are
-    int n_index = 0;                           // its place in the stream
-    if (nm > 0) {
+    Place here{item0, range.first}, next, next_index;   // the tile in hand, the entries to fetch next, the indices to copy next
+    if (nt > 0) {
+      move(here, group);
+      next = here;
+      if (next.t < range.window) next_main(next);
+      next_index = next;
+    }
+    int n_index = 0, n_fetch = 0;              // their places among the group's tiles of entries
+    if (nt > 0) {
       int es[kAhead];                          // (the first loads together)
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
-        const int slot = my_slot + next_index.i * kTile;
-        es[j] = a.idx[(long long)min(next_index.item, n_items - 1) * a.topk + min(slot, a.topk - 1)];
-        advance(next_index);
+        const int slot = my_slot + next_index.t * kTile;
+        es[j] = a.idx[(long long)min(next_index.item, n_items - 1) * a.topk + max(min(slot, a.topk - 1), 0)];
+        next_main(next_index);
       }
       n_index = kAhead;
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         fetch(j, next, es[j]);
-        advance(next);
-        copy_index(n_index++, next_index.item, next_index.i);
-        advance(next_index);
-        cp_commit();                           // (possibly of nothing: the groups count the tiles)
+        next_main(next);
+        copy_index(n_index++, next_index);
+        next_main(next_index);
+        cp_commit();                           // (possibly of nothing: the commit groups count the tiles)
       }
+      n_fetch = kAhead;
     }
-    int n_fetch = kAhead;                      // the place in the stream of the tile to fetch next
-    uint32_t st = 0, lap = 0;
-    int slot = 0;
     const int r8 = lane & 7, q4 = lane >> 3;
     const uint32_t pick = q4 < 2 ? 0x4420u : 0x4431u;   // bytes 0 and 2, or 1 and 3, of four
-    // byte offsets of this lane's pieces 4 (k % 2) + q4 of a stage's row 8 w + r8
+    // byte offsets of this lane's pieces 4 (k % 2) + q4 of a stage's row 16 w + r8
     const uint32_t even = (kRows * w + r8) * 128 + ((q4 ^ r8) << 4), odd = (kRows * w + r8) * 128 + (((4 + q4) ^ r8) << 4);
-    bool ok = true;
-    uint32_t waits = 0;
-    int n_next = item0 < n_items ? a.n_swa[item0] : 0;
-    for (int item = item0; item < n_items && ok; item += step) {
-      const int ns = clamp_count(n_next, a.swa, w == 0 && lane == 0 && crank == 0 ? a.err : nullptr);
-      if (item + step < n_items) n_next = a.n_swa[item + step];
-      for (int t = range.first; t < range.last; ++t) {
-        ok = wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
-        if (!ok) break;
-        const uint32_t k_st = smem_u32(c.k[st]), v_st = smem_u32(c.v[st]);
-        if (t < range.window) {
-          // window rows lie one behind the other: the first warp has them copied by TMA, the others only count the tile (every
-          // warp passes every stage's turns, as their parity tells no more than one from the next)
-          const int n = min(max(ns - t * kTile, 0), kTile), y = item * a.swa + t * kTile;
-          if (w > 0 || n == 0) {
-            if (w == 0 && lane == 0) c.mask[st] = 0;
-            warp_arrive(&c.full[st]);
-          } else {
-            uint64_t* bar = n == kTile ? &c.full[st] : &c.window;
-            if (lane == 0) {
-              c.mask[st] = n == kTile ? ~0ull : (1ull << n) - 1ull;
-              mbar_arrive_expect_tx(bar, kKBytes + kVBytes);
-#pragma unroll
-              for (int b = 0; b < kDk / 64; ++b) load_box(k_st + b * (kTile * 128), &k_map, 64 * b, y, bar);
-#pragma unroll
-              for (int b = 0; b < kDv / 64; ++b) load_box(v_st + b * (kTile * 128), &v_map, 64 * b, y, bar);
-            }
-            __syncwarp();
-            if (n < kTile) {                   // values behind the count are zeroed: they meet weights of 0, and might be NaN
-              ok = wait_warp(c, &c.window, waits++ & 1, a.err);
-              if (!ok) break;
-              for (int i = lane; i < (kTile - n) * 16; i += 32) {
-                const int r = n + (i >> 4), p = i & 15;
-                *reinterpret_cast<uint4*>(c.v[st] + (p >> 3) * (kTile * 128) + r * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
-              }
-              warp_arrive(&c.full[st]);
-            }
-          }
+    uint32_t st = uint32_t(group) % kStages, lap = uint32_t(group) / kStages, waits = 0;
+    int slot = 0, n_item = -1, ns = 0;
+    bool ok = true, owed = false;              // a fetch into the slot that has just been turned into rows
+    auto pay = [&]() {
+      if (!owed) return;
+      owed = false;
+      fetch(slot, next, c.index[pw][n_fetch % kIndexRing][lane & 15]);
+      next_main(next);
+      ++n_fetch;
+      copy_index(n_index++, next_index);
+      next_main(next_index);
+      cp_commit();
+      slot = (slot + 1) % kAhead;
+    };
+    while (nt > 0 && here.item < n_items) {
+      const bool window = here.t < range.window;
+      if (!window) pay();                      // (window rows are asked for first)
+      ok = wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
+      if (!ok) break;
+      const uint32_t k_st = smem_u32(c.k[st]), v_st = smem_u32(c.v[st]);
+      if (window) {
+        // window rows lie one behind the other: the group's first warp has them copied by TMA, the others only count the tile
+        if (w == 0 && here.item != n_item) {
+          n_item = here.item;
+          ns = clamp_count(a.n_swa[n_item], a.swa, group == 0 && lane == 0 && crank == 0 ? a.err : nullptr);
+        }
+        const int n = min(max(ns - here.t * kTile, 0), kTile), y = here.item * a.swa + here.t * kTile;
+        if (w > 0 || n == 0) {
+          if (w == 0 && lane == 0) c.mask[st] = 0;
+          warp_arrive(&c.full[st]);
         } else {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+          uint64_t* bar = n == kTile ? &c.full[st] : &c.window[group];
+          if (lane == 0) {
+            c.mask[st] = n == kTile ? ~0ull : (1ull << n) - 1ull;
+            mbar_arrive_expect_tx(bar, kKBytes + kVBytes);
+#pragma unroll
+            for (int b = 0; b < kDk / 64; ++b) load_box(k_st + b * (kTile * 128), &k_map, 64 * b, y, bar);
+#pragma unroll
+            for (int b = 0; b < kDv / 64; ++b) load_box(v_st + b * (kTile * 128), &v_map, 64 * b, y, bar);
+          }
           __syncwarp();
+          if (lane == 0 && here.item + step < n_items) {   // the next item's, which would come from memory (2 us)
+            const int far = y + step * a.swa;
+#pragma unroll
+            for (int b = 0; b < kDk / 64; ++b) prefetch_box(&k_map, 64 * b, far);
+#pragma unroll
+            for (int b = 0; b < kDv / 64; ++b) prefetch_box(&v_map, 64 * b, far);
+          }
+          __syncwarp();
+          if (n < kTile) {                     // values behind the count are zeroed: they meet weights of 0, and might be NaN
+            ok = wait_warp(c, &c.window[group], waits++ & 1, a.err);
+            if (!ok) break;
+            for (int i = lane; i < (kTile - n) * 16; i += 32) {
+              const int r = n + (i >> 4), p = i & 15;
+              *reinterpret_cast<uint4*>(c.v[st] + (p >> 3) * (kTile * 128) + r * 128 + (p & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            warp_arrive(&c.full[st]);
+          }
+        }
+      } else {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
           // (all loads before the first store, which they would otherwise wait for)
-          const uint8_t* src = c.packed[w][slot] + r8 * kPackedRow;
+          const uint8_t* src = c.packed[pw][slot] + (8 * hf + r8) * kPackedRow;
           uint32_t word[10], four[5];
-          __half2 two[5];                                     // the scales of groups 4 k + q4 / 2 and 2 behind it
+          __half2 two[5];                      // the scales of groups 4 k + q4 / 2 and 2 behind it
 #pragma unroll
           for (int k = 0; k < 5; ++k) four[k] = reinterpret_cast<const uint32_t*>(src + kScales)[k];
 #pragma unroll
@@ -570,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 5; ++k) two[k] = kv4_scales(__byte_perm(four[k], 0, pick));
 #pragma unroll
-          for (int k = 0; k < 10; ++k) {                      // words 4 k + q4: 0..23 of the key, 24..39 of the value
+          for (int k = 0; k < 10; ++k) {       // words 4 k + q4: 0..23 of the key, 24..39 of the value
             const __half2 scale = k & 1 ? __high2half2(two[k >> 1]) : __low2half2(two[k >> 1]);
             __half2 x[4];
             kv4_pairs(word[k], x);
@@ -580,24 +619,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[i] = __hmul2(x[i], scale);
               y[i] = *reinterpret_cast<const uint32_t*>(&x[i]);
             }
-            const uint32_t to = (k < 6 ? k_st + (k >> 1) * (kTile * 128) : v_st + ((k - 6) >> 1) * (kTile * 128)) + (k & 1 ? odd : even);
+            const uint32_t to = (k < 6 ? k_st + (k >> 1) * (kTile * 128) : v_st + ((k - 6) >> 1) * (kTile * 128)) + (k & 1 ? odd : even) + hf * 1024;
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
           }
-          if (lane == 0) reinterpret_cast<uint8_t*>(&c.mask[st])[w] = uint8_t(there >> (8 * slot));
-          const int e = c.index[w][n_fetch % kIndexRing][lane & 7];
-          warp_arrive(&c.full[st]);            // (and every lane has read the packed entries)
-          fetch(slot, next, e);
-          advance(next);
-          ++n_fetch;
-          copy_index(n_index++, next_index.item, next_index.i);
-          advance(next_index);
-          cp_commit();
-          slot = (slot + 1) % kAhead;
         }
-        if (++st == kStages) {
-          st = 0;
-          ++lap;
-        }
+        if (lane == 0) reinterpret_cast<uint16_t*>(&c.mask[st])[w] = uint16_t(there >> (16 * slot));
+        warp_arrive(&c.full[st]);              // (and every lane has read the packed entries)
+        owed = true;
+      }
+      move(here, kGroups);
+      st += kGroups;
+      if (st >= kStages) {
+        st -= kStages;
+        ++lap;
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -607,38 +641,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---------------------------------------------------------------- MMA issue
+    // ---------------------------------------------------------------- MMA issue: scores by one warp, values by another
+    // (One warp for both left the tensor cores idle while it looked at its barriers: 1,680 cycles a tile.)
     constexpr uint32_t qk_h = idesc_f16(128, kTile, false), pv_h = idesc_f16(128, kDv, true);
     constexpr uint32_t qk_b = idesc_bf16(128, kTile, false), pv_b = idesc_bf16(128, kDv, true);
+    const bool scores = warp == kSoftmaxWarps + kEndWarps + kProducerWarps;
     const uint64_t k0 = smem_desc(smem_u32(c.k[0]), 16, 1024), v0 = smem_desc(smem_u32(c.v[0]), kTile * 128, 1024);
-    uint32_t tiles = 0, items = 0, st = 0, lap = 0;
+    uint32_t tiles = 0, items = 0, st = 0, lap = 0;           // tiles that have keys, so far
     bool ok = true;
-    for (int item = item0; item < n_items && ok; item += step) {
-      bool pending = false, first = true, was_window = false;   // a tile whose O is to be added
-      uint32_t was_st = 0;
-      auto pv = [&]() -> bool {
-        const uint32_t x = tiles - 1, buf = x & 1;
-        if (first && items > 0 && !wait_warp(c, &c.o_free, (items - 1) & 1, a.err)) return false;
-        if (!wait_warp(c, &c.p_full[buf], (x >> 1) & 1, a.err)) return false;
-        tc_fence_after();
-        const uint64_t v = v0 + was_st * (kVBytes >> 4);
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tmem + kOCol, tmem + kSCol + buf * 64 + 8 * k, v + k * (2048 >> 4), was_window ? pv_b : pv_h, !(first && k == 0));
-          tc_commit(&c.empty[was_st]);
-          tc_commit(&c.o_done);
-        }
-        __syncwarp();
-        first = false;
-        return true;
-      };
-      ok = wait_warp(c, &c.q_full, items & 1, a.err);
+    for (int item = item0; item < n_items && ok; item += step, ++items) {
+      bool first = true;
+      if (scores) ok = wait_warp(c, &c.q_full, items & 1, a.err);
       for (int t = range.first; t < range.last && ok; ++t) {
         ok = wait_warp(c, &c.full[st], lap & 1, a.err);
         if (!ok) break;
         const uint64_t mask = c.mask[st];
         const uint32_t here = st;
+        if (scores) warp_arrive(&c.empty[here]);
         if (++st == kStages) {
           st = 0;
           ++lap;
@@ -646,37 +665,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The rows are generic-proxy writes, which the tensor core reads, and TMA overwrites, by the async proxy.  The fence stands
         // here, behind the wait, and not with the producers: theirs would wait for the copies that are on their way (1.5 us a tile).
         fence_async_smem();
+        const bool window = t < range.window;
+        const uint32_t buf = tiles & 1;
         if (mask == 0) {                       // no key: nobody looks at it
-          warp_arrive(&c.empty[here]);
-          if (pending) ok = pv();              // (its stage may be what the next tile waits for)
-          pending = false;
+          // (given back behind the tiles before: the producers take it that stages come back in their order)
+          if (!scores && elect_one()) tc_commit(&c.empty[here]);
+          __syncwarp();
           continue;
         }
-        tc_fence_after();
-        const bool window = t < range.window;
-        const uint32_t buf = tiles & 1, q = tmem + (window ? kQbCol : kQhCol), desc = window ? qk_b : qk_h;
-        const uint64_t kd = k0 + here * (kKBytes >> 4);
-        if (elect_one()) {
+        if (scores) {
+          // (S lies where the weights of the last but one lay)
+          if (tiles >= 2) ok = wait_warp(c, &c.s_free[buf], ((tiles >> 1) - 1) & 1, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = k0 + here * (kKBytes >> 4);
+          const uint32_t q = tmem + (window ? kQbCol : kQhCol), desc = window ? qk_b : qk_h;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kDk / 16; ++k)
-            mma_ts(tmem + kSCol + buf * 64, q + 8 * k, kd + ((k >> 2) * (kTile * 128) + (k & 3) * 32) / 16, desc, k > 0);
-          tc_commit(&c.s_full[buf]);
+            for (int k = 0; k < kDk / 16; ++k)
+              mma_ts(tmem + kSCol + buf * 64, q + 8 * k, kd + ((k >> 2) * (kTile * 128) + (k & 3) * 32) / 16, desc, k > 0);
+            tc_commit(&c.s_full[buf]);
+          }
+        } else {
+          if (first && items > 0) ok = wait_warp(c, &c.o_free, (items - 1) & 1, a.err);
+          ok = ok && wait_warp(c, &c.p_full[buf], (tiles >> 1) & 1, a.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t v = v0 + here * (kVBytes >> 4);
+          const uint32_t desc = window ? pv_b : pv_h;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_ts(tmem + kOCol, tmem + kSCol + buf * 64 + 8 * k, v + k * (2048 >> 4), desc, !(first && k == 0));
+            tc_commit(&c.empty[here]);
+            tc_commit(&c.s_free[buf]);
+          }
+          first = false;
         }
         __syncwarp();
-        if (pending) ok = pv();
-        pending = true;
-        was_st = here;
-        was_window = window;
         ++tiles;
       }
       if (!ok) break;
-      if (elect_one()) tc_commit(&c.q_empty);
+      if (elect_one()) tc_commit(scores ? &c.q_empty : &c.o_last);
       __syncwarp();
-      if (pending) ok = pv();
-      if (!ok) break;
-      if (elect_one()) tc_commit(&c.o_last);
-      __syncwarp();
-      ++items;
     }
     // every MMA has finished before the memory it uses is given up
     if (elect_one()) tc_commit(&c.fin);
