@@ -1,8 +1,8 @@
 // Sparse attention over a packed main cache (kv4.cuh) on the 5th-generation tensor
 // cores (bf16, 64 heads sharing one KV head, dk 192, dv 128).
 //
-// A query's keys come in tiles of 64: its window rows first, then its selected
-// entries.  Code * scale is exact in fp16, so that an entry's row becomes fp16 and its
+// A query's keys come in tiles of 64: its selected entries first, then its
+// window rows.  Code * scale is exact in fp16, so that an entry's row becomes fp16 and its
 // products with the query, which is put into fp16's range by a power of two a head, are
 // as exact as bf16's (an element 2^34 below its head's largest is lost); its weights have 11 bits
 // there instead of 8.  Window rows stay bf16, with bf16 weights and the query as it is.
@@ -72,7 +72,8 @@ struct Shared {
   uint64_t s_full[2], p_full[2];               // S has been computed; P has been written
   uint64_t s_free[2];                          // O holds the tile whose weights lay there
   uint64_t o_last, o_free;                     // O holds the item's last tile; has been read
-  uint64_t q_full, q_empty, stat_full, stat_free;
+  uint64_t q_full[2], q_empty[2];              // of the query as fp16 and as bf16
+  uint64_t stat_full, stat_free;
   uint64_t window[kGroups];                    // a window tile that is not full has landed
   uint64_t ends;                               // the end warps have come here
   uint64_t fin;                                // every MMA is done
@@ -124,12 +125,13 @@ CSA2_DEV void warp_arrive(uint64_t* bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// The tiles of a query that CTA `rank` of `n` takes.
+// The tiles of a query that CTA `rank` of `n` takes: [first, last) of its tiles, of which those from `window` on are the
+// window's.
 struct Range {
-  int first, last, window;                     // [first, last) of a query's tiles; how many are the window's
+  int first, last, window;
   CSA2_DEV Range(const Kv4AttnArgs& a, int rank, int n) {
-    window = (a.swa + kTile - 1) / kTile;
-    const int all = window + (a.topk + kTile - 1) / kTile;
+    window = (a.topk + kTile - 1) / kTile;
+    const int all = window + (a.swa + kTile - 1) / kTile;
     first = all * rank / n;
     last = all * (rank + 1) / n;
   }
@@ -168,8 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&c.o_last, 1);
     mbar_init(&c.o_free, kEndWarps);
-    mbar_init(&c.q_full, kEndWarps);
-    mbar_init(&c.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&c.q_full[i], kEndWarps);
+      mbar_init(&c.q_empty[i], 1);
+    }
     mbar_init(&c.stat_full, kSoftmaxWarps);
     mbar_init(&c.stat_free, kEndWarps);
     for (int g = 0; g < kGroups; ++g) mbar_init(&c.window[g], 1);
@@ -212,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (all == 0) continue;
         const uint32_t mask = uint32_t(all >> (32 * half));
-        const bool window = t < range.window;
+        const bool window = t >= range.window;
         const uint32_t buf = tiles & 1, s_addr = tmem + lanes + kSCol + buf * 64;
         ok = wait_warp(c, &c.s_full[buf], (tiles >> 1) & 1, a.err);
         if (!ok) break;
@@ -322,27 +326,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       cp_commit();
     };
-    auto store_q = [&](uint32_t parity) -> bool {             // into TMEM
+    auto q_here = [&]() -> bool {                             // the copy in shared memory is complete
       asm volatile("cp.async.wait_all;" ::: "memory");
-      if (!end_sync()) return false;
-      const uint4* src = reinterpret_cast<const uint4*>(c.q + head * kQRow);
-      uint32_t top = 0;                                       // bits of the largest magnitude
-#pragma unroll 1
-      for (int b = 0; b < 6; ++b) {
-        uint32_t r[16];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint4 y = src[4 * b + x];
-          r[4 * x] = y.x, r[4 * x + 1] = y.y, r[4 * x + 2] = y.z, r[4 * x + 3] = y.w;
-        }
-#pragma unroll
-        for (int x = 0; x < 16; ++x) top = max(top, max(r[x] & 0x7fffu, (r[x] >> 16) & 0x7fffu));
-        tmem_st16(tmem + lanes + kQbCol + 16 * b, r);
-      }
+      return end_sync();
+    };
+    const uint4* src = reinterpret_cast<const uint4*>(c.q + head * kQRow);
+    int e = 0;                                                // of this row's power of two
+    auto scale_q = [&]() {
       // largest magnitudes of 2^9 .. 2^10 (queries below 2^-91 keep less; their products are 0 all the same)
-      const int e = max(int(top >> 7) - 127 - 9, -100);
+      uint32_t top = 0;                                       // bits of the largest magnitude
+#pragma unroll 4
+      for (int x = 0; x < kDk / 8; ++x) {
+        const uint4 y = src[x];
+        const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+      }
+      e = max(int(top >> 7) - 127 - 9, -100);
+    };
+    auto store_half = [&](uint32_t parity) {                  // as fp16 into TMEM
       const float down = __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll 1
+#pragma unroll 2
       for (int b = 0; b < 6; ++b) {
         uint32_t r[16];
 #pragma unroll
@@ -358,22 +362,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       c.q_scale[parity][row] = fminf(ldexpf(a.scale * log2e * a.k_up, e), 3e38f);
       tc_wait_st();
       tc_fence_before();
-      warp_arrive(&c.q_full);
-      return end_sync();                                      // the copy in shared memory has been read
+      warp_arrive(&c.q_full[0]);
+    };
+    auto store_q = [&]() {                                    // as it is
+#pragma unroll 2
+      for (int b = 0; b < 6; ++b) {
+        uint32_t r[16];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint4 y = src[4 * b + x];
+          r[4 * x] = y.x, r[4 * x + 1] = y.y, r[4 * x + 2] = y.z, r[4 * x + 3] = y.w;
+        }
+        tmem_st16(tmem + lanes + kQbCol + 16 * b, r);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      warp_arrive(&c.q_full[1]);
     };
     uint32_t items = 0;
     bool ok = true;
     if (item0 < n_items) {
       copy_q(item0);
-      ok = store_q(0);
+      ok = q_here();
+      scale_q();
+      store_half(0);
+      store_q();
+      ok = ok && end_sync();                                  // it has been read
       copy_q(item0 + step);
     }
     for (int item = item0; item < n_items && ok; item += step, ++items) {
       if (item + step < n_items) {
+        if (!q_here()) break;
+        scale_q();
         // (its scales lie where those of the item before this one lay, whose softmax is over)
-        if (!wait_warp(c, &c.q_empty, items & 1, a.err)) break;
+        if (!wait_warp(c, &c.q_empty[0], items & 1, a.err)) break;
         tc_fence_after();
-        if (!store_q((items + 1) & 1)) break;
+        store_half((items + 1) & 1);
+        if (!wait_warp(c, &c.q_empty[1], items & 1, a.err)) break;
+        tc_fence_after();
+        store_q();
+        if (!end_sync()) break;                               // it has been read
         copy_q(item + 2 * step);
       }
       if (!wait_warp(c, &c.stat_full, items & 1, a.err)) break;
@@ -469,9 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto next_main = [&](Place& p) {           // the group's next tile of entries
       do move(p, kGroups);
-      while (p.t < range.window && p.item < n_items);
+      while (p.t >= range.window && p.item < n_items);
     };
-    const int my_slot = kRows * w + (lane & 15) - range.window * kTile;   // (+ 64 t: of tile t)
+    const int my_slot = kRows * w + (lane & 15);              // (+ 64 t: of tile t)
     auto copy_index = [&](int n, Place p) {    // of the n-th tile of entries, lanes 0..15
       const int slot = my_slot + p.t * kTile;
       if (lane < kRows && p.item < n_items && slot < a.topk)
@@ -507,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (nt > 0) {
       move(here, group);
       next = here;
-      if (next.t < range.window) next_main(next);
+      if (next.t >= range.window) next_main(next);
       next_index = next;
     }
     int n_index = 0, n_fetch = 0;              // their places among the group's tiles of entries
@@ -516,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int slot = my_slot + next_index.t * kTile;
-        es[j] = a.idx[(long long)min(next_index.item, n_items - 1) * a.topk + max(min(slot, a.topk - 1), 0)];
+        es[j] = a.idx[(long long)min(next_index.item, n_items - 1) * a.topk + min(slot, a.topk - 1)];
         next_main(next_index);
       }
       n_index = kAhead;
@@ -549,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       slot = (slot + 1) % kAhead;
     };
     while (nt > 0 && here.item < n_items) {
-      const bool window = here.t < range.window;
+      const bool window = here.t >= range.window;
       if (!window) pay();                      // (window rows are asked for first)
       ok = wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
       if (!ok) break;
@@ -558,9 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // window rows lie one behind the other: the group's first warp has them copied by TMA, the others only count the tile
         if (w == 0 && here.item != n_item) {
           n_item = here.item;
-          ns = clamp_count(a.n_swa[n_item], a.swa, group == 0 && lane == 0 && crank == 0 ? a.err : nullptr);
+          ns = clamp_count(a.n_swa[n_item], a.swa, lane == 0 ? a.err : nullptr);
         }
-        const int n = min(max(ns - here.t * kTile, 0), kTile), y = here.item * a.swa + here.t * kTile;
+        const int row0 = (here.t - range.window) * kTile;
+        const int n = min(max(ns - row0, 0), kTile), y = here.item * a.swa + row0;
         if (w > 0 || n == 0) {
           if (w == 0 && lane == 0) c.mask[st] = 0;
           warp_arrive(&c.full[st]);
@@ -651,7 +680,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int item = item0; item < n_items && ok; item += step, ++items) {
       bool first = true;
-      if (scores) ok = wait_warp(c, &c.q_full, items & 1, a.err);
+      if (scores) ok = wait_warp(c, &c.q_full[0], items & 1, a.err);
+      else if (items > 0) ok = wait_warp(c, &c.o_free, (items - 1) & 1, a.err);   // (of every item, with keys or without)
+      bool half = true;                        // the query as fp16 is still wanted
+      auto half_done = [&]() -> bool {
+        half = false;
+        if (elect_one()) tc_commit(&c.q_empty[0]);
+        __syncwarp();
+        return wait_warp(c, &c.q_full[1], items & 1, a.err);
+      };
       for (int t = range.first; t < range.last && ok; ++t) {
         ok = wait_warp(c, &c.full[st], lap & 1, a.err);
         if (!ok) break;
@@ -665,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The rows are generic-proxy writes, which the tensor core reads, and TMA overwrites, by the async proxy.  The fence stands
         // here, behind the wait, and not with the producers: theirs would wait for the copies that are on their way (1.5 us a tile).
         fence_async_smem();
-        const bool window = t < range.window;
+        const bool window = t >= range.window;
         const uint32_t buf = tiles & 1;
         if (mask == 0) {                       // no key: nobody looks at it
           // (given back behind the tiles before: the producers take it that stages come back in their order)
@@ -674,8 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if (scores) {
+          if (window && half) ok = half_done();
           // (S lies where the weights of the last but one lay)
-          if (tiles >= 2) ok = wait_warp(c, &c.s_free[buf], ((tiles >> 1) - 1) & 1, a.err);
+          if (ok && tiles >= 2) ok = wait_warp(c, &c.s_free[buf], ((tiles >> 1) - 1) & 1, a.err);
           if (!ok) break;
           tc_fence_after();
           const uint64_t kd = k0 + here * (kKBytes >> 4);
@@ -687,8 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(&c.s_full[buf]);
           }
         } else {
-          if (first && items > 0) ok = wait_warp(c, &c.o_free, (items - 1) & 1, a.err);
-          ok = ok && wait_warp(c, &c.p_full[buf], (tiles >> 1) & 1, a.err);
+          ok = wait_warp(c, &c.p_full[buf], (tiles >> 1) & 1, a.err);
           if (!ok) break;
           tc_fence_after();
           const uint64_t v = v0 + here * (kVBytes >> 4);
@@ -705,8 +742,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++tiles;
       }
+      if (ok && scores && half) ok = half_done();
       if (!ok) break;
-      if (elect_one()) tc_commit(scores ? &c.q_empty : &c.o_last);
+      if (elect_one()) tc_commit(scores ? &c.q_empty[1] : &c.o_last);
       __syncwarp();
     }
     // every MMA has finished before the memory it uses is given up
