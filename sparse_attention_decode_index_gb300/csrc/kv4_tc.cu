@@ -37,40 +37,42 @@ namespace {
 constexpr int kH = 64, kDk = 192, kDv = 128;
 constexpr int kTile = 64;                      // keys a stage
 constexpr int kEntry = kv4_bytes(kDk, kDv);    // 192: codes 0..159, scales 160..179
-constexpr int kScales = 160;
 constexpr int kKBytes = kTile * kDk * 2, kVBytes = kTile * kDv * 2;
-constexpr int kStages = 3;
+constexpr int kStages = 4;                     // an even number: a stage always belongs to the same group of producers
+constexpr int kScores = 3;                     // buffers of S and P
 constexpr int kSoftmaxWarps = 4, kEndWarps = 4, kProducerWarps = 8;
 constexpr int kGroups = 2, kGroupWarps = kProducerWarps / kGroups;   // of producers, which take turns at the tiles
-constexpr int kAhead = 2;                      // tiles of packed entries on their way, of a group
 constexpr int kRows = kTile / kGroupWarps;     // entries of a producer warp: 16
-constexpr int kPackedRow = kEntry + 16;        // padded: rows of 4 lanes' words meet no bank twice
 constexpr int kThreads = 32 * (kSoftmaxWarps + kEndWarps + kProducerWarps + 2);
-constexpr int kIndexRing = 4 * kAhead;         // tiles whose indices are on their way or there, of a group
+constexpr int kPackedRow = kEntry + 16;        // padded: rows of 4 lanes' words meet no bank twice
+constexpr int kScales = 160;                   // where an entry's scales begin
+constexpr int kIndexAhead = 3, kIndexRing = 4;   // tiles whose indices are on their way, of a group, and room for them
 constexpr int kMaxCluster = 8;
 constexpr int kQRow = kDk * 2 + 16;            // query rows on their way to TMEM
-constexpr int kXRow = 36;                      // fp32 columns of a row that the halves exchange, padded
+constexpr int kXRow = 68;                      // fp32 columns of a row that the halves exchange, padded
 constexpr int kPRow = kDv + 4;                 // partial O of a split
 // Weights are held as 2^7 times their relation to their row's exponent: at most 2^15, as that grows by steps of 2^8, which
 // fp16 holds, and rounded by 2^-12 of themselves or, below 2^-21, by 2^-32 of the greatest.
 constexpr float kUp = 7.f;
-constexpr uint32_t kTmemCols = 512;            // a power of two over O (128), two S (64 each), Q as fp16 and as bf16 (96 each)
-constexpr uint32_t kOCol = 0, kSCol = 128, kQhCol = 256, kQbCol = 352;
+constexpr uint32_t kTmemCols = 512;            // O (128), three S (64 each), Q as fp16 and as bf16 (96 each)
+constexpr uint32_t kOCol = 0, kSCol = 128, kQhCol = 320, kQbCol = 416;
 
 struct Shared {
   uint8_t k[kStages][kKBytes];                 // 3 blocks of 64 dims: 64 rows of 128 bytes
   uint8_t v[kStages][kVBytes];                 // 2 blocks of 64 dims: 64 keys of 128 bytes
-  uint8_t packed[kProducerWarps][kAhead][kRows * kPackedRow];
+  uint8_t packed[kProducerWarps][kRows * kPackedRow];
   int index[kProducerWarps][kIndexRing][kRows];
-  uint8_t q[kH * kQRow];
-  float x[128 * kXRow];
+  union {                                      // the next query until it is in TMEM, then what the halves of an O exchange
+    uint8_t q[kH * kQRow];
+    float x[128 * kXRow];
+  };
   uint64_t mask[kStages];                      // the tile's keys that are there
   float2 stat[128];                            // (exponent, sum) of the rows of an item
   float q_scale[2][128];                       // what a row's fp16 products are multiplied by, of even and odd items
-  float2 part[kMaxCluster][kH];                // (exponent, sum) of the CTAs of a split, of the heads that this one adds up
+  float2 part[kH];                             // (exponent, sum) of the CTAs of a split, of the heads that this one adds up
   uint64_t full[kStages], empty[kStages];      // a tile has landed; has been used
-  uint64_t s_full[2], p_full[2];               // S has been computed; P has been written
-  uint64_t s_free[2];                          // O holds the tile whose weights lay there
+  uint64_t s_full[kScores], p_full[kScores];   // S has been computed; P has been written
+  uint64_t s_free[kScores];                    // O holds the tile whose weights lay there
   uint64_t o_last, o_free;                     // O holds the item's last tile; has been read
   uint64_t q_full[2], q_empty[2];              // of the query as fp16 and as bf16
   uint64_t stat_full, stat_free;
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c.full[i], kGroupWarps);
       mbar_init(&c.empty[i], 2 + kSoftmaxWarps);   // the values' end; everyone else who looks at its mask
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < kScores; ++b) {
       mbar_init(&c.s_full[b], 1);
       mbar_init(&c.p_full[b], kSoftmaxWarps);
       mbar_init(&c.s_free[b], 1);
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = uint32_t(warp * 32) << 16;
     const uint32_t o_addr = tmem + lanes + kOCol;
     const float window_scale = a.scale * log2e, window_up = 1.f / a.v_up;
-    uint32_t tiles = 0, items = 0, st = 0, lap = 0;           // tiles that have keys, so far
+    uint32_t items = 0, st = 0, lap = 0, buf = 0, turn = 0;   // buf: of S, turn: its times round, for tiles that have keys
     bool ok = true;
     for (int item = item0; item < n_items && ok; item += step) {
       float ref = -INFINITY, sum = 0.f;        // the exponent that P and O are relative to, and the weights' sum
@@ -217,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (all == 0) continue;
         const uint32_t mask = uint32_t(all >> (32 * half));
         const bool window = t >= range.window;
-        const uint32_t buf = tiles & 1, s_addr = tmem + lanes + kSCol + buf * 64;
-        ok = wait_warp(c, &c.s_full[buf], (tiles >> 1) & 1, a.err);
+        const uint32_t s_addr = tmem + lanes + kSCol + buf * 64;
+        ok = wait_warp(c, &c.s_full[buf], turn & 1, a.err);
         if (!ok) break;
         tc_fence_after();
         uint32_t p[16];
@@ -246,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ref = top;
           } else if (__any_sync(0xffffffffu, grows)) {
             // O holds tiles up to the one before: wait for it.
-            ok = wait_warp(c, &c.s_free[buf ^ 1], ((tiles - 1) >> 1) & 1, a.err);
+            ok = buf > 0 ? wait_warp(c, &c.s_free[buf - 1], turn & 1, a.err) : wait_warp(c, &c.s_free[kScores - 1], (turn - 1) & 1, a.err);
             if (!ok) break;
             tc_fence_after();
             const float f = grows ? ex2(ref - top) : 1.f;
@@ -297,7 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_st();
         tc_fence_before();
         warp_arrive(&c.p_full[buf]);
-        ++tiles;
+        if (++buf == kScores) {
+          buf = 0;
+          ++turn;
+        }
       }
       if (!ok) break;
       ok = items == 0 || wait_warp(c, &c.stat_free, (items - 1) & 1, a.err);
@@ -388,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       store_half(0);
       store_q();
       ok = ok && end_sync();                                  // it has been read
-      copy_q(item0 + step);
+      copy_q(item0 + step);                                   // (later ones when the exchange is over)
     }
     for (int item = item0; item < n_items && ok; item += step, ++items) {
       if (item + step < n_items) {
@@ -401,8 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!wait_warp(c, &c.q_empty[1], items & 1, a.err)) break;
         tc_fence_after();
         store_q();
-        if (!end_sync()) break;                               // it has been read
-        copy_q(item + 2 * step);
       }
       if (!wait_warp(c, &c.stat_full, items & 1, a.err)) break;
       const float2 mine = c.stat[row], theirs = c.stat[row ^ 64];
@@ -414,63 +417,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = ncta > 1 ? weight : weight * (a.v_up / sum);
       if (!wait_warp(c, &c.o_last, items & 1, a.err)) break;
       tc_fence_after();
-      // a thread ends with 64 columns of its head: it gives its part of the others to its partner of the other half
-#pragma unroll 1
-      for (int b = 0; b < 2 && ok; ++b) {
-        uint32_t o[32];
-        tmem_ld32(o, tmem + lanes + kOCol + 64 * (1 - side) + 32 * b);
+      // A thread ends with 64 columns of its head: it gives its part of the others to its partner of the other half.  O is free
+      // for the next item as soon as this thread's columns are in registers.
+      if (!end_sync()) break;                                 // the next query has been read: x lies where it lay
+      uint32_t o[64];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        uint32_t y[32];
+        tmem_ld32(y, tmem + lanes + kOCol + 64 * (1 - side) + 32 * b);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4*>(c.x + row * kXRow + 4 * j) =
-              make_float4(__uint_as_float(o[4 * j]) * f, __uint_as_float(o[4 * j + 1]) * f, __uint_as_float(o[4 * j + 2]) * f,
-                          __uint_as_float(o[4 * j + 3]) * f);
-        tmem_ld32(o, tmem + lanes + kOCol + 64 * side + 32 * b);
-        if (b == 1) {
-          tc_fence_before();
-          warp_arrive(&c.o_free);
+          *reinterpret_cast<float4*>(c.x + row * kXRow + 32 * b + 4 * j) =
+              make_float4(__uint_as_float(y[4 * j]) * f, __uint_as_float(y[4 * j + 1]) * f, __uint_as_float(y[4 * j + 2]) * f,
+                          __uint_as_float(y[4 * j + 3]) * f);
+      }
+      tmem_ld64(o, tmem + lanes + kOCol + 64 * side);
+      tc_fence_before();
+      warp_arrive(&c.o_free);
+      if (!end_sync()) break;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float4 z = *reinterpret_cast<const float4*>(c.x + (row ^ 64) * kXRow + 4 * j);
+        o[4 * j] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j]), f, z.x));
+        o[4 * j + 1] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 1]), f, z.y));
+        o[4 * j + 2] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 2]), f, z.z));
+        o[4 * j + 3] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 3]), f, z.w));
+      }
+      if (ncta > 1) {
+        uint4* part = reinterpret_cast<uint4*>(reinterpret_cast<float*>(c.k) + head * kPRow + 64 * side);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      } else {
+        if (!end_sync()) break;                               // what was given has been read
+        // the warp's 32 rows of 128 bytes as whole pieces of lines, through its part of x
+        uint4* turn = reinterpret_cast<uint4*>(c.x + w * 32 * kXRow);
+        auto at = [&](int r, int p) -> uint4& { return turn[r * 8 + (p ^ (r & 7))]; };
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = pack_bf16(__uint_as_float(o[8 * p + 2 * i]), __uint_as_float(o[8 * p + 2 * i + 1]));
+          at(lane, p) = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        ok = end_sync();
-        if (!ok) break;
-        float y[32];
+        __syncwarp();
+        uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((long long)item * kH + (w & 1) * 32) * kDv);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const float4 z = *reinterpret_cast<const float4*>(c.x + (row ^ 64) * kXRow + 4 * j);
-          y[4 * j] = none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j]), f, z.x);
-          y[4 * j + 1] = none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 1]), f, z.y);
-          y[4 * j + 2] = none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 2]), f, z.z);
-          y[4 * j + 3] = none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 3]), f, z.w);
+          const int r = 4 * j + (lane >> 3);
+          out[r * (kDv / 8) + 8 * side + (lane & 7)] = at(r, lane & 7);
         }
-        ok = end_sync();                                      // what was given has been read
-        if (!ok) break;
-        if (ncta > 1) {
-          float* part = reinterpret_cast<float*>(c.k) + head * kPRow + 64 * side + 32 * b;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) reinterpret_cast<float4*>(part)[j] = make_float4(y[4 * j], y[4 * j + 1], y[4 * j + 2], y[4 * j + 3]);
-        } else {
-          // the warp's 32 rows of 64 bytes as whole pieces of lines, through its part of x
-          uint4* turn = reinterpret_cast<uint4*>(c.x + w * 32 * kXRow);
-          auto at = [&](int r, int p) -> uint4& { return turn[r * 4 + (p ^ ((r >> 1) & 3))]; };
-#pragma unroll
-          for (int p = 0; p < 4; ++p)
-            at(lane, p) = make_uint4(pack_bf16(y[8 * p], y[8 * p + 1]), pack_bf16(y[8 * p + 2], y[8 * p + 3]),
-                                     pack_bf16(y[8 * p + 4], y[8 * p + 5]), pack_bf16(y[8 * p + 6], y[8 * p + 7]));
-          __syncwarp();
-          uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + ((long long)item * kH + (w & 1) * 32) * kDv);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int r = 8 * j + (lane >> 2);
-            out[r * (kDv / 8) + 8 * side + 4 * b + (lane & 3)] = at(r, lane & 3);
-          }
-          __syncwarp();
-        }
+        if (!end_sync()) break;                               // and x is free again
+        copy_q(item + 2 * step);
       }
-      if (!ok) break;
       if (ncta > 1) {
         cluster_wait();                                       // the peers have begun
         joined = true;
         const int own = head / (kH / ncta);
         if (side == 0) {
-          const uint32_t to = dsmem_addr(&c.part[crank][head], uint32_t(own));
+          const uint32_t to = dsmem_addr(&c.part[crank * (kH / ncta) + head % (kH / ncta)], uint32_t(own));
           dsmem_st_v2(to, top, sum);
         }
       } else if (a.lse != nullptr && side == 0) {
@@ -482,9 +486,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (Eight warps on the same tile spent most of it on the latencies of its steps.)
     const int pw = warp - kSoftmaxWarps - kEndWarps, group = pw / kGroupWarps, w = pw % kGroupWarps;
     const int nt = range.last - range.first;   // tiles of an item
-    const uint32_t ring = smem_u32(c.packed[pw][0]);
-    // The group's tiles are every second one of all items'.  A main tile's indices are copied 2 kAhead turns before it is turned
-    // into rows, its entries kAhead before.  (As loads into registers the indices were waited for a tile at a time, 0.5 us each.)
+    // The group's tiles are every second one of all items'.  A tile's entries are copied while the group waits for its turn, its
+    // indices kIndexAhead turns before that.  (Either as loads into registers was slower: they take their lines in an L1 that has
+    // few beside this much shared memory.)
     struct Place {
       int item, t;
     };
@@ -507,78 +511,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                      "l"(a.idx + (long long)p.item * a.topk + slot)
                      : "memory");
     };
-    uint32_t there = 0;                        // 16 bits for each tile on its way
+    const uint32_t packed = smem_u32(c.packed[pw]);
+    uint32_t there = 0;                        // the copied tile's rows that are there
     int last_item = -1;                        // whose sequence's cache this is
     const uint8_t* cache = a.kv;
-    auto fetch = [&](int slot, Place p, int e) {
+    auto fetch = [&](Place p, int e) {
       if (lane >= kRows || p.item >= n_items || my_slot + p.t * kTile >= a.topk) e = -1;
       if (e >= a.n_entries) {
         report(a.err, kErrBadIndex, e);
         e = -1;
       }
-      there = (there & ~(0xffffu << (16 * slot))) | (__ballot_sync(0xffffffffu, e >= 0) & 0xffffu) << (16 * slot);
-      if (p.item < n_items) {
-        if (p.item != last_item) {
-          last_item = p.item;
-          cache = a.kv + (long long)(p.item / a.seq_div) * a.n_entries * kEntry;
-        }
+      there = __ballot_sync(0xffffffffu, e >= 0);
+      if (p.item != last_item && p.item < n_items) {
+        last_item = p.item;
+        cache = a.kv + (long long)(p.item / a.seq_div) * a.n_entries * kEntry;
+      }
 #pragma unroll
-        for (int x = 0; x < 6; ++x) {
-          const int p12 = 32 * x + lane, r = p12 / 12, part = p12 - 12 * r;
-          const int entry = __shfl_sync(0xffffffffu, e, r);
-          cp16(ring + slot * (kRows * kPackedRow) + r * kPackedRow + 16 * part,
-               entry >= 0 ? cache + (long long)entry * kEntry + 16 * part : nullptr, a.kv);
-        }
+      for (int x = 0; x < 6; ++x) {            // 16 rows of 12 pieces
+        const int i = 32 * x + lane, r = i / 12, part = i - 12 * r, entry = __shfl_sync(0xffffffffu, e, r);
+        cp16(packed + r * kPackedRow + 16 * part, entry >= 0 ? cache + (long long)entry * kEntry + 16 * part : nullptr, a.kv);
       }
     };
-    Place here{item0, range.first}, next, next_index;   // the tile in hand, the entries to fetch next, the indices to copy next
-    if (nt > 0) {
-      move(here, group);
-      next = here;
-      if (next.t >= range.window) next_main(next);
-      next_index = next;
-    }
+    Place here{item0, range.first}, next, next_index;   // the tile in hand, the entries to load next, the indices to copy next
+    move(here, group);
+    next = here;
+    if (next.t >= range.window) next_main(next);
+    next_index = next;
     int n_index = 0, n_fetch = 0;              // their places among the group's tiles of entries
-    if (nt > 0) {
-      int es[kAhead];                          // (the first loads together)
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        const int slot = my_slot + next_index.t * kTile;
-        es[j] = a.idx[(long long)min(next_index.item, n_items - 1) * a.topk + min(slot, a.topk - 1)];
-        next_main(next_index);
-      }
-      n_index = kAhead;
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        fetch(j, next, es[j]);
-        next_main(next);
-        copy_index(n_index++, next_index);
-        next_main(next_index);
-        cp_commit();                           // (possibly of nothing: the commit groups count the tiles)
-      }
-      n_fetch = kAhead;
+    for (int j = 0; j < kIndexAhead; ++j) {
+      copy_index(n_index++, next_index);
+      next_main(next_index);
     }
-    const int r8 = lane & 7, q4 = lane >> 3;
-    const uint32_t pick = q4 < 2 ? 0x4420u : 0x4431u;   // bytes 0 and 2, or 1 and 3, of four
-    // byte offsets of this lane's pieces 4 (k % 2) + q4 of a stage's row 16 w + r8
-    const uint32_t even = (kRows * w + r8) * 128 + ((q4 ^ r8) << 4), odd = (kRows * w + r8) * 128 + (((4 + q4) ^ r8) << 4);
-    uint32_t st = uint32_t(group) % kStages, lap = uint32_t(group) / kStages, waits = 0;
-    int slot = 0, n_item = -1, ns = 0;
-    bool ok = true, owed = false;              // a fetch into the slot that has just been turned into rows
-    auto pay = [&]() {
-      if (!owed) return;
-      owed = false;
-      fetch(slot, next, c.index[pw][n_fetch % kIndexRing][lane & 15]);
+    cp_commit();
+    auto copy_next = [&]() {                   // (every copy of this warp has landed)
+      fetch(next, c.index[pw][n_fetch % kIndexRing][lane & 15]);
       next_main(next);
       ++n_fetch;
       copy_index(n_index++, next_index);
       next_main(next_index);
       cp_commit();
-      slot = (slot + 1) % kAhead;
     };
-    while (nt > 0 && here.item < n_items) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    copy_next();
+    const int r8 = lane & 7, q4 = lane >> 3;
+    const uint32_t pick = q4 < 2 ? 0x4420u : 0x4431u;   // bytes 0 and 2, or 1 and 3, of four
+    // byte offsets of this lane's pieces 4 (k % 2) + q4 of a stage's row 16 w + r8
+    const uint32_t even = (kRows * w + r8) * 128 + ((q4 ^ r8) << 4), odd = (kRows * w + r8) * 128 + (((4 + q4) ^ r8) << 4);
+    uint32_t st = uint32_t(group) % kStages, lap = uint32_t(group) / kStages, waits = 0;
+    int n_item = -1, ns = 0;
+    bool ok = true;
+    while (here.item < n_items) {
       const bool window = here.t >= range.window;
-      if (!window) pay();                      // (window rows are asked for first)
       ok = wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
       if (!ok) break;
       const uint32_t k_st = smem_u32(c.k[st]), v_st = smem_u32(c.v[st]);
@@ -623,12 +606,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncwarp();
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
           // (all loads before the first store, which they would otherwise wait for)
-          const uint8_t* src = c.packed[pw][slot] + (8 * hf + r8) * kPackedRow;
+          const uint8_t* src = c.packed[pw] + (8 * hf + r8) * kPackedRow;
           uint32_t word[10], four[5];
           __half2 two[5];                      // the scales of groups 4 k + q4 / 2 and 2 behind it
 #pragma unroll
@@ -652,9 +635,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
           }
         }
-        if (lane == 0) reinterpret_cast<uint16_t*>(&c.mask[st])[w] = uint16_t(there >> (16 * slot));
+        if (lane == 0) reinterpret_cast<uint16_t*>(&c.mask[st])[w] = uint16_t(there);
         warp_arrive(&c.full[st]);              // (and every lane has read the packed entries)
-        owed = true;
+        copy_next();
       }
       move(here, kGroups);
       st += kGroups;
@@ -676,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t qk_b = idesc_bf16(128, kTile, false), pv_b = idesc_bf16(128, kDv, true);
     const bool scores = warp == kSoftmaxWarps + kEndWarps + kProducerWarps;
     const uint64_t k0 = smem_desc(smem_u32(c.k[0]), 16, 1024), v0 = smem_desc(smem_u32(c.v[0]), kTile * 128, 1024);
-    uint32_t tiles = 0, items = 0, st = 0, lap = 0;           // tiles that have keys, so far
+    uint32_t items = 0, st = 0, lap = 0, buf = 0, turn = 0;   // as above
     bool ok = true;
     for (int item = item0; item < n_items && ok; item += step, ++items) {
       bool first = true;
@@ -690,7 +673,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         return wait_warp(c, &c.q_full[1], items & 1, a.err);
       };
       for (int t = range.first; t < range.last && ok; ++t) {
-        ok = wait_warp(c, &c.full[st], lap & 1, a.err);
+        // (S lies where the weights of the third tile before lay)
+        if (scores && turn > 0) ok = wait_warp(c, &c.s_free[buf], (turn - 1) & 1, a.err);
+        ok = ok && wait_warp(c, &c.full[st], lap & 1, a.err);
         if (!ok) break;
         const uint64_t mask = c.mask[st];
         const uint32_t here = st;
@@ -703,17 +688,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // here, behind the wait, and not with the producers: theirs would wait for the copies that are on their way (1.5 us a tile).
         fence_async_smem();
         const bool window = t >= range.window;
-        const uint32_t buf = tiles & 1;
         if (mask == 0) {                       // no key: nobody looks at it
-          // (given back behind the tiles before: the producers take it that stages come back in their order)
           if (!scores && elect_one()) tc_commit(&c.empty[here]);
           __syncwarp();
           continue;
         }
         if (scores) {
           if (window && half) ok = half_done();
-          // (S lies where the weights of the last but one lay)
-          if (ok && tiles >= 2) ok = wait_warp(c, &c.s_free[buf], ((tiles >> 1) - 1) & 1, a.err);
           if (!ok) break;
           tc_fence_after();
           const uint64_t kd = k0 + here * (kKBytes >> 4);
@@ -725,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(&c.s_full[buf]);
           }
         } else {
-          ok = wait_warp(c, &c.p_full[buf], (tiles >> 1) & 1, a.err);
+          ok = wait_warp(c, &c.p_full[buf], turn & 1, a.err);
           if (!ok) break;
           tc_fence_after();
           const uint64_t v = v0 + here * (kVBytes >> 4);
@@ -740,7 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           first = false;
         }
         __syncwarp();
-        ++tiles;
+        if (++buf == kScores) {
+          buf = 0;
+          ++turn;
+        }
       }
       if (ok && scores && half) ok = half_done();
       if (!ok) break;
@@ -768,9 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid < per) {
     const int h = hb + tid;
     float top = -INFINITY, sum = 0.f;
-    for (int r = 0; r < ncta; ++r) top = fmaxf(top, c.part[r][h].x);
+    for (int r = 0; r < ncta; ++r) top = fmaxf(top, c.part[r * per + tid].x);
     for (int r = 0; r < ncta; ++r) {
-      const float2 y = c.part[r][h];
+      const float2 y = c.part[r * per + tid];
       const float f = y.x == -INFINITY && y.y == 0.f ? 0.f : ex2(y.x - top);   // (a NaN sum stays)
       weight[r * kH + h] = f;
       sum += f * y.y;
