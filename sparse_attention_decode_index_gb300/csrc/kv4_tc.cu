@@ -47,6 +47,7 @@ constexpr int kThreads = 32 * (kSoftmaxWarps + kEndWarps + kProducerWarps + 2);
 constexpr int kPackedRow = kEntry + 16;        // padded: rows of 4 lanes' words meet no bank twice
 constexpr int kScales = 160;                   // where an entry's scales begin
 constexpr int kIndexAhead = 3, kIndexRing = 4;   // tiles whose indices are on their way, of a group, and room for them
+constexpr int kScoresWarp = kSoftmaxWarps + kEndWarps + kProducerWarps, kValuesWarp = kScoresWarp + 1;
 constexpr int kMaxCluster = 8;
 constexpr int kQRow = kDk * 2 + 16;            // query rows on their way to TMEM
 constexpr int kXRow = 68;                      // fp32 columns of a row that the halves exchange, padded
@@ -481,27 +482,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.lse[(long long)item * kH + head] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       }
     }
-  } else if (warp < kSoftmaxWarps + kEndWarps + kProducerWarps) {
+  } else if (warp != kScoresWarp && warp != kValuesWarp) {
     // ---------------------------------------------------------------- producers: 16 rows of every second tile a warp
     // (Eight warps on the same tile spent most of it on the latencies of its steps.)
     const int pw = warp - kSoftmaxWarps - kEndWarps, group = pw / kGroupWarps, w = pw % kGroupWarps;
-    const int nt = range.last - range.first;   // tiles of an item
+    const int nt = range.last - range.first, main_end = min(range.window, range.last);   // tiles of an item, end of its entries'
     // The group's tiles are every second one of all items'.  A tile's entries are copied while the group waits for its turn, its
     // indices kIndexAhead turns before that.  (Either as loads into registers was slower: they take their lines in an L1 that has
     // few beside this much shared memory.)
     struct Place {
-      int item, t;
+      int item, t, start;                      // start: the group's first tile of the item
     };
-    auto move = [&](Place& p, int n) {
-      p.t += n;
-      while (p.t >= range.last) {
-        p.t -= nt;
-        p.item += step;
-      }
+    auto next_item = [&](Place& p) {
+      p.item += step;
+      p.t = p.start = range.first + ((p.start - range.first + nt) & 1);
     };
     auto next_main = [&](Place& p) {           // the group's next tile of entries
-      do move(p, kGroups);
-      while (p.t >= range.window && p.item < n_items);
+      p.t += kGroups;
+      while (p.t >= main_end && p.item < n_items) next_item(p);
     };
     const int my_slot = kRows * w + (lane & 15);              // (+ 64 t: of tile t)
     auto copy_index = [&](int n, Place p) {    // of the n-th tile of entries, lanes 0..15
@@ -511,10 +509,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                      "l"(a.idx + (long long)p.item * a.topk + slot)
                      : "memory");
     };
-    const uint32_t packed = smem_u32(c.packed[pw]);
+    // Piece i = 32 x + lane of the warp's 16 rows of 12 pieces is of row r = i / 12: it lies 16 (i - 12 r) bytes into entry r, and goes
+    // 16 (i + r) bytes into the padded rows.
+    const uint32_t packed = smem_u32(c.packed[pw]) + 16 * lane;
+    uint32_t rows_of = 0;                      // r of x = 0..5, 4 bits each
+#pragma unroll
+    for (int x = 0; x < 6; ++x) rows_of |= uint32_t((32 * x + lane) / 12) << (4 * x);
     uint32_t there = 0;                        // the copied tile's rows that are there
     int last_item = -1;                        // whose sequence's cache this is
-    const uint8_t* cache = a.kv;
+    const uint8_t* cache = a.kv + 16 * lane;
     auto fetch = [&](Place p, int e) {
       if (lane >= kRows || p.item >= n_items || my_slot + p.t * kTile >= a.topk) e = -1;
       if (e >= a.n_entries) {
@@ -524,18 +527,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       there = __ballot_sync(0xffffffffu, e >= 0);
       if (p.item != last_item && p.item < n_items) {
         last_item = p.item;
-        cache = a.kv + (long long)(p.item / a.seq_div) * a.n_entries * kEntry;
+        cache = a.kv + (long long)(p.item / a.seq_div) * a.n_entries * kEntry + 16 * lane;
       }
 #pragma unroll
-      for (int x = 0; x < 6; ++x) {            // 16 rows of 12 pieces
-        const int i = 32 * x + lane, r = i / 12, part = i - 12 * r, entry = __shfl_sync(0xffffffffu, e, r);
-        cp16(packed + r * kPackedRow + 16 * part, entry >= 0 ? cache + (long long)entry * kEntry + 16 * part : nullptr, a.kv);
+      for (int x = 0; x < 6; ++x) {
+        const int r = (rows_of >> (4 * x)) & 15, entry = __shfl_sync(0xffffffffu, e, r);
+        const uint8_t* src = cache + (long long)(max(entry, 0) - r) * kEntry + 512 * x;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(packed + 16 * r + 512 * x), "l"(src), "r"(entry >= 0 ? 16u : 0u)
+                     : "memory");
       }
     };
-    Place here{item0, range.first}, next, next_index;   // the tile in hand, the entries to load next, the indices to copy next
-    move(here, group);
+    // the tile in hand, the entries to copy next, the indices to copy next
+    Place here{item0, range.first + group, range.first + group}, next, next_index;
+    while (here.t >= range.last && here.item < n_items) next_item(here);
     next = here;
-    if (next.t >= range.window) next_main(next);
+    while (next.t >= main_end && next.item < n_items) next_item(next);
     next_index = next;
     int n_index = 0, n_fetch = 0;              // their places among the group's tiles of entries
     for (int j = 0; j < kIndexAhead; ++j) {
@@ -639,7 +645,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&c.full[st]);              // (and every lane has read the packed entries)
         copy_next();
       }
-      move(here, kGroups);
+      here.t += kGroups;
+      while (here.t >= range.last && here.item < n_items) next_item(here);
       st += kGroups;
       if (st >= kStages) {
         st -= kStages;
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (One warp for both left the tensor cores idle while it looked at its barriers: 1,680 cycles a tile.)
     constexpr uint32_t qk_h = idesc_f16(128, kTile, false), pv_h = idesc_f16(128, kDv, true);
     constexpr uint32_t qk_b = idesc_bf16(128, kTile, false), pv_b = idesc_bf16(128, kDv, true);
-    const bool scores = warp == kSoftmaxWarps + kEndWarps + kProducerWarps;
+    const bool scores = warp == kScoresWarp;
     const uint64_t k0 = smem_desc(smem_u32(c.k[0]), 16, 1024), v0 = smem_desc(smem_u32(c.v[0]), kTile * 128, 1024);
     uint32_t items = 0, st = 0, lap = 0, buf = 0, turn = 0;   // as above
     bool ok = true;
