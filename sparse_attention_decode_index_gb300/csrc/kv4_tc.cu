@@ -70,6 +70,7 @@ struct Shared {
   uint64_t mask[kStages];                      // the tile's keys that are there
   float2 stat[128];                            // (exponent, sum) of the rows of an item
   float q_scale[2][128];                       // what a row's fp16 products are multiplied by, of even and odd items
+  uint32_t top[128];                           // bits of the largest magnitude of half a head's query
   float2 part[kH];                             // (exponent, sum) of the CTAs of a split, of the heads that this one adds up
   uint64_t full[kStages], empty[kStages];      // a tile has landed; has been used
   uint64_t s_full[kScores], p_full[kScores];   // S has been computed; P has been written
@@ -338,75 +339,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const uint4* src = reinterpret_cast<const uint4*>(c.q + head * kQRow);
     int e = 0;                                                // of this row's power of two
-    auto scale_q = [&]() {
-      // largest magnitudes of 2^9 .. 2^10 (queries below 2^-91 keep less; their products are 0 all the same)
-      uint32_t top = 0;                                       // bits of the largest magnitude
+    float scale = 0.f;                                        // what the products of its fp16 form are multiplied by
+    auto scale_q = [&]() -> bool {
+      // Largest magnitudes of 2^9 .. 2^10 (queries below 2^-91 keep less; their products are 0 all the same).  A row and its
+      // other half look at half of the head each.
+      uint32_t top = 0;                                       // bits of the largest magnitudes of even and odd dims
 #pragma unroll 4
-      for (int x = 0; x < kDk / 8; ++x) {
-        const uint4 y = src[x];
+      for (int x = 0; x < kDk / 16; ++x) {
+        const uint4 y = src[kDk / 16 * side + x];
+        top = __vmaxu2(__vmaxu2(__vmaxu2(top, y.x & 0x7fff7fffu), __vmaxu2(y.y & 0x7fff7fffu, y.z & 0x7fff7fffu)), y.w & 0x7fff7fffu);
+      }
+      c.top[row] = max(top & 0xffffu, top >> 16);
+      if (!end_sync()) return false;
+      e = max(int(max(c.top[row], c.top[row ^ 64]) >> 7) - 127 - 9, -100);
+      scale = fminf(ldexpf(a.scale * log2e * a.k_up, e), 3e38f);
+      return true;
+    };
+    // Words 16 b .. 16 b + 15 of the row, as they are or as fp16.
+    auto words = [&](int b, bool half, uint32_t (&r)[16]) {
+      const float down = __uint_as_float(uint32_t(127 - e) << 23);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint4 y = src[4 * b + x];
         const uint32_t u[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(u[i] & 0x7fffu, (u[i] >> 16) & 0x7fffu));
+        for (int i = 0; i < 4; ++i)
+          r[4 * x + i] = half ? pack_f16(__uint_as_float(u[i] << 16) * down, __uint_as_float(u[i] & 0xffff0000u) * down) : u[i];
       }
-      e = max(int(top >> 7) - 127 - 9, -100);
     };
-    auto store_half = [&](uint32_t parity) {                  // as fp16 into TMEM
-      const float down = __uint_as_float(uint32_t(127 - e) << 23);
-#pragma unroll 2
-      for (int b = 0; b < 6; ++b) {
-        uint32_t r[16];
+    // The next query into TMEM, as fp16 (i = 0) or as it is (1), as soon as nobody reads the last one there.
+    auto store_q = [&](int i, bool wait, uint32_t phase) -> bool {
+      const uint32_t to = tmem + lanes + (i == 0 ? kQhCol : kQbCol);
+      uint32_t r[16];
+      words(0, i == 0, r);
+      if (wait && !wait_warp(c, &c.q_empty[i], phase, a.err)) return false;
+      tc_fence_after();
+      tmem_st16(to, r);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint4 y = src[4 * b + x];
-          const uint32_t u[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            r[4 * x + i] = pack_f16(__uint_as_float(u[i] << 16) * down, __uint_as_float(u[i] & 0xffff0000u) * down);
-        }
-        tmem_st16(tmem + lanes + kQhCol + 16 * b, r);
-      }
-      c.q_scale[parity][row] = fminf(ldexpf(a.scale * log2e * a.k_up, e), 3e38f);
-      tc_wait_st();
-      tc_fence_before();
-      warp_arrive(&c.q_full[0]);
-    };
-    auto store_q = [&]() {                                    // as it is
-#pragma unroll 2
-      for (int b = 0; b < 6; ++b) {
-        uint32_t r[16];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint4 y = src[4 * b + x];
-          r[4 * x] = y.x, r[4 * x + 1] = y.y, r[4 * x + 2] = y.z, r[4 * x + 3] = y.w;
-        }
-        tmem_st16(tmem + lanes + kQbCol + 16 * b, r);
+      for (int b = 1; b < 6; ++b) {
+        words(b, i == 0, r);
+        tmem_st16(to + 16 * b, r);
       }
       tc_wait_st();
       tc_fence_before();
-      warp_arrive(&c.q_full[1]);
+      warp_arrive(&c.q_full[i]);
+      return true;
     };
     uint32_t items = 0;
     bool ok = true;
     if (item0 < n_items) {
       copy_q(item0);
-      ok = q_here();
-      scale_q();
-      store_half(0);
-      store_q();
-      ok = ok && end_sync();                                  // it has been read
+      ok = q_here() && scale_q();
+      c.q_scale[0][row] = scale;
+      ok = ok && store_q(0, false, 0) && store_q(1, false, 0) && end_sync();
       copy_q(item0 + step);                                   // (later ones when the exchange is over)
     }
     for (int item = item0; item < n_items && ok; item += step, ++items) {
       if (item + step < n_items) {
-        if (!q_here()) break;
-        scale_q();
+        if (!q_here() || !scale_q()) break;
         // (its scales lie where those of the item before this one lay, whose softmax is over)
-        if (!wait_warp(c, &c.q_empty[0], items & 1, a.err)) break;
-        tc_fence_after();
-        store_half((items + 1) & 1);
-        if (!wait_warp(c, &c.q_empty[1], items & 1, a.err)) break;
-        tc_fence_after();
-        store_q();
+        c.q_scale[(items + 1) & 1][row] = scale;
+        if (!store_q(0, true, items & 1) || !store_q(1, true, items & 1)) break;
       }
       if (!wait_warp(c, &c.stat_full, items & 1, a.err)) break;
       const float2 mine = c.stat[row], theirs = c.stat[row ^ 64];
@@ -439,10 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float4 z = *reinterpret_cast<const float4*>(c.x + (row ^ 64) * kXRow + 4 * j);
-        o[4 * j] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j]), f, z.x));
-        o[4 * j + 1] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 1]), f, z.y));
-        o[4 * j + 2] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 2]), f, z.z));
-        o[4 * j + 3] = __float_as_uint(none ? 0.f : __fmaf_rn(__uint_as_float(o[4 * j + 3]), f, z.w));
+        o[4 * j] = __float_as_uint(__fmaf_rn(__uint_as_float(o[4 * j]), f, z.x));
+        o[4 * j + 1] = __float_as_uint(__fmaf_rn(__uint_as_float(o[4 * j + 1]), f, z.y));
+        o[4 * j + 2] = __float_as_uint(__fmaf_rn(__uint_as_float(o[4 * j + 2]), f, z.z));
+        o[4 * j + 3] = __float_as_uint(__fmaf_rn(__uint_as_float(o[4 * j + 3]), f, z.w));
+      }
+      if (none) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j) o[j] = 0u;
       }
       if (ncta > 1) {
         uint4* part = reinterpret_cast<uint4*>(reinterpret_cast<float*>(c.k) + head * kPRow + 64 * side);
