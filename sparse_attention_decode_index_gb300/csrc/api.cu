@@ -1099,7 +1099,7 @@ int csa2_norm_rope(const csa2_norm_rope_slot* slots, int32_t n_slots, int32_t ro
     if (y.x == y.out && y.x_stride != y.out_stride && rows > 1) return CSA2_ERR_INVALID_ARG;
     const uint64_t e = elem_size(y.dtype);
     a.slot[k] = NormRopeArgs::Slot{y.x, y.out, y.gain, y.x_stride, y.out_stride, y.heads, y.dim, rot_dim > 0 ? y.rot_off : 0,
-                                   y.dtype, y.gain_each, 0, 0, 0};
+                                   y.dtype, y.gain_each, 0, 0, 0, 0};
     x[k] = {y.x, width * e, y.x_stride * e, uint64_t(rows)};
     out[k] = {y.out, width * e, y.out_stride * e, uint64_t(rows)};
     gain[k] = {y.gain, uint64_t(y.gain_each ? width : y.dim) * 4, 0, 1};

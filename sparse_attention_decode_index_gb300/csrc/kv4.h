@@ -16,7 +16,7 @@ struct NormRopeArgs {
     const float* gain;       // [dim], or [heads, dim] (nullable: ones)
     long long x_stride, out_stride;
     int heads, dim, off, dtype, gain_each;
-    int bytes, lanes, vecs;  // vectors' bytes (0: element by element), lanes of a head, vectors a lane (set by the launcher)
+    int bytes, lanes, vecs, partner;   // vectors' bytes (0: element by element), lanes of a head, vectors a lane, where partners are (set by the launcher)
   } slot[kMaxRopeSlots];
   int n_slots;
   int rows, per_block;       // rows, rows per block (set by the launcher)
@@ -26,7 +26,7 @@ struct NormRopeArgs {
   const double* freqs;       // [rot / 2] radians per position
 };
 
-cudaError_t launch_norm_rope(NormRopeArgs& a, int rows, cudaStream_t st);
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int rows, cudaStream_t st);
 
 // A packed entry: the codes of the key's groups and of the value's, 8 bytes a
 // group, then a scale's byte a group, padded with zeros to 16 bytes.
@@ -46,12 +46,11 @@ struct Kv4AppendArgs {
   int* n_valid;              // [B] (read and updated)
   int n_entries, nb_cap, k_dim, v_dim, idx_dim, block, round_to_int, dtype;
   float k_down, v_down;      // 2^-k_exp, 2^-v_exp
-  int per_cta;               // entry positions a CTA owns (set by the launcher)
   int wide, wide_idx;        // whole 16-byte pieces at aligned addresses: of keys and values, of indexer keys
   int* err;
 };
 
-cudaError_t launch_kv4_append(Kv4AppendArgs& a, int batch, cudaStream_t st);
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int batch, cudaStream_t st);
 
 struct Kv4RowsArgs {
   const uint8_t* kv;         // [B / seq_div, N, kv4_bytes]

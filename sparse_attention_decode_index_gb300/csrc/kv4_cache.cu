@@ -11,95 +11,159 @@ constexpr int kTileEntries = 32;   // packed in shared memory before they are wr
 
 // ------------------------------------------------------------------ append
 
-// 16 numbers from p (n of them, zeros behind), in the element type.
-CSA2_DEV void load16(const void* p, int n, int dtype, bool wide, float (&x)[16]) {
-  if (wide && dtype == 1) {
+// Groups of 16 numbers that a thread has on their way: as they lie in memory (kWide), or one by one.
+template <bool kF32>
+struct Raw {
+  uint4 v[kF32 ? 4 : 2];
+  CSA2_DEV void load(const uint8_t* p) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = static_cast<const float4*>(p)[i];
-      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-  } else if (wide) {
+    for (int i = 0; i < (kF32 ? 4 : 2); ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  CSA2_DEV void numbers(float (&x)[16]) const {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = static_cast<const uint4*>(p)[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < (kF32 ? 4 : 2); ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
-        x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        if constexpr (kF32) {
+          x[4 * i + e] = __uint_as_float(w[e]);
+        } else {
+          x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
+          x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+        }
       }
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = i < n ? load_elem(p, i, dtype) : 0.f;
   }
-}
+};
 
-// Each CTA owns `per_cta` positions of a sequence's cache, whole blocks of it, of which it writes those that the new
-// entries take, so that every block's summary key is one CTA's.  A thread packs a group of 16 dims
-// at a time into shared memory, from where a tile of entries, contiguous in the cache, goes out in 16-byte pieces.
+// Each CTA packs kTileEntries of a sequence's new entries: a thread packs a group of 16 dims at a time into shared memory, from
+// where the entries, contiguous in the cache, go out in 16-byte pieces.  The first groups are asked for beside the counts,
+// whatever these say (the rows up to max_new can be read).  A block's summary key is the CTA's that has its first new
+// entry; its members come from the cache in front of the new entries and from the new ones, never from what
+// another CTA writes.
+template <bool kF32>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArgs a) {
   extern __shared__ __align__(16) uint8_t tile[];          // [kTileEntries][entry]
+  constexpr int kBatch = kF32 ? 2 : 3, kE = kF32 ? 4 : 2;  // groups a thread has on their way; an element's bytes
   const int b = blockIdx.y, tid = threadIdx.x;
+  const int gk = kv4_groups(a.k_dim), groups = gk + kv4_groups(a.v_dim), bytes = kv4_bytes(a.k_dim, a.v_dim);
+  const uint32_t m_groups = 0xffffffffu / uint32_t(groups) + 1u;   // (two at least)
+  const int s0 = blockIdx.x * kTileEntries, n_most = min(kTileEntries, a.max_new - s0);
+  const long long src = (long long)b * a.max_new + s0;
+  const uint8_t *k_new = static_cast<const uint8_t*>(a.k_new) + src * a.k_dim * kE, *v_new = static_cast<const uint8_t*>(a.v_new) + src * a.v_dim * kE;
   pdl_wait();   // no early trigger: the next launch may read what this one writes before its own wait
+  const int had = a.n_valid[b], added = a.n_new[b];
+  auto place = [&](int i, int& r, int& g) {
+    r = int(__umulhi(uint32_t(i), m_groups));
+    g = i - r * groups;
+  };
+  auto from = [&](int r, int g) -> const uint8_t* {
+    return g < gk ? k_new + ((long long)r * a.k_dim + 16 * g) * kE : v_new + ((long long)r * a.v_dim + 16 * (g - gk)) * kE;
+  };
+  Raw<kF32> raw[kBatch];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      int r, g;
+      place(i0 + x * kThreads, r, g);
+      if (a.wide && r < n_most) raw[x].load(from(r, g));
+    }
+  };
+  fetch(tid);
   int* err = blockIdx.x == 0 && tid == 0 ? a.err : nullptr;
-  const int nv0 = clamp_count(a.n_valid[b], a.n_entries, err);
-  int m = clamp_count(a.n_new[b], a.max_new, err);
+  const int nv0 = clamp_count(had, a.n_entries, err);
+  int m = clamp_count(added, a.max_new, err);
   if (m > a.n_entries - nv0) {
     report(err, kErrBadCount, nv0 + m);
     m = a.n_entries - nv0;
   }
-  const int gk = kv4_groups(a.k_dim), groups = gk + kv4_groups(a.v_dim), bytes = kv4_bytes(a.k_dim, a.v_dim);
-  const int e_size = a.dtype == 1 ? 4 : 2, x_bytes = a.idx_dim * e_size;
-  // positions [lo, hi) of this CTA
-  const long long first = (long long)(nv0 / a.block) * a.block + (long long)blockIdx.x * a.per_cta;
-  const int lo = int(min(max(first, (long long)nv0), (long long)nv0 + m)), hi = int(min(first + a.per_cta, (long long)nv0 + m));
-  const uint8_t *k_new = static_cast<const uint8_t*>(a.k_new), *v_new = static_cast<const uint8_t*>(a.v_new);
-  for (int p0 = lo; p0 < hi; p0 += kTileEntries) {
-    const int n = min(kTileEntries, hi - p0);
-    const long long src = (long long)b * a.max_new + (p0 - nv0);
-    const uint32_t m_groups = groups == 1 ? 0u : 0xffffffffu / uint32_t(groups) + 1u;
-    for (int i = tid; i < n * groups; i += kThreads) {
-      const int r = m_groups == 0 ? i : int(__umulhi(uint32_t(i), m_groups)), g = i - r * groups;
-      const bool key = g < gk;
-      const int d = 16 * (key ? g : g - gk), dim = key ? a.k_dim : a.v_dim;
-      float x[16];
-      load16((key ? k_new : v_new) + ((src + r) * dim + d) * e_size, dim - d, a.dtype, a.wide != 0, x);
+  const int n = min(n_most, m - s0);                       // entries of this CTA (none: <= 0)
+  for (int i0 = tid; i0 < n * groups; i0 += kBatch * kThreads) {
+    if (i0 != tid) fetch(i0);
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      int r, g;
+      place(i0 + x * kThreads, r, g);
+      if (r >= n) continue;
+      float v[16];
+      if (a.wide) {
+        raw[x].numbers(v);
+      } else {
+        const int d = 16 * (g < gk ? g : g - gk), dim = g < gk ? a.k_dim : a.v_dim;
+        const uint8_t* p = from(r, g);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = d + e < dim ? load_elem(p, e, kF32 ? 1 : 0) : 0.f;
+      }
       uint2 codes;
-      const float down = key ? a.k_down : a.v_down;
-      const uint8_t s = a.dtype == 1 ? kv4_quantise<true>(x, down, codes) : kv4_quantise<false>(x, down, codes);
+      const uint8_t s = kv4_quantise<kF32>(v, g < gk ? a.k_down : a.v_down, codes);
       *reinterpret_cast<uint2*>(tile + r * bytes + 8 * g) = codes;
       tile[r * bytes + 8 * groups + g] = s;
     }
-    for (int i = tid; i < n * (bytes - 9 * groups); i += kThreads) {
-      const int r = i / (bytes - 9 * groups);
-      tile[r * bytes + 9 * groups + i - r * (bytes - 9 * groups)] = 0;
-    }
-    __syncthreads();
-    uint4* dst = reinterpret_cast<uint4*>(a.kv + ((long long)b * a.n_entries + p0) * bytes);
-    for (int i = tid; i < n * (bytes / 16); i += kThreads) dst[i] = reinterpret_cast<const uint4*>(tile)[i];
-    const uint8_t* xs = static_cast<const uint8_t*>(a.kidx_new) + src * x_bytes;
-    uint8_t* xd = static_cast<uint8_t*>(a.k_idx) + ((long long)b * a.n_entries + p0) * x_bytes;
+  }
+  const int pad = bytes - 9 * groups;
+  for (int i = tid; i < n * pad; i += kThreads) tile[i / pad * bytes + 9 * groups + i % pad] = 0;
+  const int x_bytes = a.idx_dim * kE;
+  const long long row0 = (long long)b * a.n_entries, dst = row0 + nv0 + s0;
+  const uint8_t* xs = static_cast<const uint8_t*>(a.kidx_new) + src * x_bytes;
+  uint8_t* xd = static_cast<uint8_t*>(a.k_idx) + dst * x_bytes;
+  if (a.wide_idx) {
+    for (int i = tid; i < n * (x_bytes / 16); i += kThreads) reinterpret_cast<uint4*>(xd)[i] = __ldg(reinterpret_cast<const uint4*>(xs) + i);
+  } else {
+    for (int i = tid; i < n * (x_bytes / 2); i += kThreads) reinterpret_cast<uint16_t*>(xd)[i] = reinterpret_cast<const uint16_t*>(xs)[i];
+  }
+  if (a.kb != nullptr && n > 0) {
+    // blocks whose first new entry is s0 .. s0 + n - 1 of the new ones
+    const int nv1 = nv0 + m, p0 = nv0 + s0;
+    const int j0 = s0 == 0 ? nv0 / a.block : (p0 - 1) / a.block + 1, j1 = (p0 + n - 1) / a.block;
+    auto member = [&](int pos) -> const uint8_t* {         // its indexer key
+      return pos < nv0 ? static_cast<const uint8_t*>(a.k_idx) + (row0 + pos) * x_bytes
+                       : static_cast<const uint8_t*>(a.kidx_new) + ((long long)b * a.max_new + pos - nv0) * x_bytes;
+    };
+    // (sums in entry order, as block_key_elem's)
     if (a.wide_idx) {
-      for (int i = tid; i < n * (x_bytes / 16); i += kThreads) reinterpret_cast<uint4*>(xd)[i] = reinterpret_cast<const uint4*>(xs)[i];
+      constexpr int kN = 16 / kE;
+      const int vecs = a.idx_dim / kN;
+      for (int i = tid; i < (j1 - j0 + 1) * vecs; i += kThreads) {
+        const int j = j0 + i / vecs, v = i % vecs, first = j * a.block, count = min(a.block, nv1 - first);
+        float sum[kN];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) sum[e] = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < count; ++r) {
+          const uint4 y = reinterpret_cast<const uint4*>(member(first + r))[v];
+          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (kF32) {
+              sum[e] += __uint_as_float(w[e]);
+            } else {
+              sum[2 * e] += __uint_as_float(w[e] << 16);
+              sum[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+          sum[e] = sum[e] / float(count);
+          if (a.round_to_int) sum[e] = rintf(sum[e]);
+          store_elem(a.kb, ((long long)b * a.nb_cap + j) * a.idx_dim + v * kN + e, a.dtype, sum[e]);
+        }
+      }
     } else {
-      for (int i = tid; i < n * (x_bytes / 2); i += kThreads) reinterpret_cast<uint16_t*>(xd)[i] = reinterpret_cast<const uint16_t*>(xs)[i];
-    }
-    __syncthreads();   // the tile is free again, and its indexer keys are visible to the CTA
-  }
-  if (a.kb != nullptr && lo < hi) {
-    const int j0 = lo / a.block, n = ((hi - 1) / a.block - j0 + 1) * a.idx_dim;
-    for (int i = tid; i < n; i += kThreads) {
-      const int j = j0 + i / a.idx_dim, d = i % a.idx_dim;
-      const float v = block_key_elem(a.k_idx, (long long)b * a.n_entries, a.idx_dim, a.block, nv0 + m, j, d, a.dtype, a.round_to_int);
-      store_elem(a.kb, ((long long)b * a.nb_cap + j) * a.idx_dim + d, a.dtype, v);
+      for (int i = tid; i < (j1 - j0 + 1) * a.idx_dim; i += kThreads) {
+        const int j = j0 + i / a.idx_dim, d = i % a.idx_dim, first = j * a.block, count = min(a.block, nv1 - first);
+        float sum = 0.f;
+        for (int r = 0; r < count; ++r) sum += load_elem(member(first + r), d, a.dtype);
+        sum = sum / float(count);
+        if (a.round_to_int) sum = rintf(sum);
+        store_elem(a.kb, ((long long)b * a.nb_cap + j) * a.idx_dim + d, a.dtype, sum);
+      }
     }
   }
-  if (gridDim.x == 1) {
-    __syncthreads();   // every thread read n_valid[b] before it changes
-    if (tid == 0) a.n_valid[b] = nv0 + m;
-  }
+  __syncthreads();   // the tile is packed; and every thread has read n_valid[b]
+  uint4* out = reinterpret_cast<uint4*>(a.kv + dst * bytes);
+  for (int i = tid; i < n * (bytes / 16); i += kThreads) out[i] = reinterpret_cast<const uint4*>(tile)[i];
+  if (gridDim.x == 1 && tid == 0) a.n_valid[b] = nv0 + m;
 }
 
 // The fill counts of sequences that several CTAs have read them for.
@@ -113,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) kv4_count_kernel(const Kv4AppendArgs
 
 // ------------------------------------------------------------------ rows
 
-constexpr int kBatch = 4;          // 16-byte pieces a thread has on their way
+constexpr int kBatch = 4;          // 16-byte pieces of rows a thread has on their way
 constexpr int kMaxRows = 32;       // of a CTA
 
 // The entries of a CTA's rows, null where there is none, into shared memory.
@@ -193,15 +257,13 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_any_kernel(const Kv4RowsArg
 
 }  // namespace
 
-cudaError_t launch_kv4_append(Kv4AppendArgs& a, int batch, cudaStream_t st) {
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int batch, cudaStream_t st) {
   if (batch == 0 || a.max_new == 0) return cudaSuccess;
-  // whole blocks of at least a tile of entries; the first new one may lie within its block
-  a.per_cta = a.block >= kTileEntries ? a.block : (kTileEntries + a.block - 1) / a.block * a.block;
-  const long long span = (a.max_new < a.n_entries ? a.max_new : a.n_entries) + (a.block - 1LL);
-  const unsigned chunks = unsigned((span + a.per_cta - 1) / a.per_cta);
+  const unsigned chunks = unsigned((a.max_new - 1) / kTileEntries + 1);
   note_launch();
   const size_t smem = size_t(kTileEntries) * kv4_bytes(a.k_dim, a.v_dim);
-  cudaError_t e = launch_pdl(kv4_append_kernel, dim3(chunks, unsigned(batch)), dim3(kThreads), smem, st, 1, a);
+  cudaError_t e = launch_pdl(a.dtype == 1 ? kv4_append_kernel<true> : kv4_append_kernel<false>, dim3(chunks, unsigned(batch)), dim3(kThreads),
+                             smem, st, 1, a);
   if (e != cudaSuccess || chunks == 1) return e;
   note_launch();
   return launch_pdl(kv4_count_kernel, dim3(unsigned((batch + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, 1, a, batch);

@@ -10,8 +10,8 @@
 // share their angles, as in rope.cu.  A head belongs to a group of 1 to 32 lanes
 // that hold up to 4 vectors of it each (192 bf16 dims: 8 lanes with 3 vectors of
 // 16 bytes), chosen so that few lanes are left over; its sums go through log2(lanes)
-// shuffles.  In the half layout a turned vector's partner is loaded a second time
-// (from L1), so that no lane waits for another's numbers.
+// shuffles.  The next head is on its way while one is turned, and gains that the heads
+// share stay in registers.
 #include "common.cuh"
 #include "kv4.h"
 #include "rope.cuh"
@@ -22,6 +22,7 @@ namespace {
 
 constexpr int kThreads = kRopeThreads;
 constexpr int kMaxVecs = 4;       // of a lane
+constexpr int kPerSm = 3;         // blocks
 
 CSA2_DEV float sum_lanes(float v, int lanes) {
   for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -72,37 +73,67 @@ struct Part {
   }
 };
 
-template <bool kBf16, int kBytes, int kNv>
+// Where the partner of a turned vector of the half layout is: nowhere (interleaved pairs, or none at all), in the same lane
+// `hv / lanes` vectors further, in lane l ^ hv, or anywhere (it is loaded a second time).
+enum Partner { kNoPartner, kSameLane, kOtherLane, kLoaded };
+
+template <bool kBf16, int kBytes, int kNv, int kPartner>
 CSA2_DEV void norm_vectors(const NormRopeArgs& a, const NormRopeArgs::Slot& y, const Part& part, const float2* cs) {
   constexpr int kE = kBf16 ? 2 : 4, kV = kBytes / kE;
   const int lanes = y.lanes, l = threadIdx.x & (lanes - 1), n_vecs = y.dim / kV;
-  const int half = a.rot / 2, v0 = y.off / kV, rv = a.rot / kV, hv = a.interleaved ? 0 : rv / 2;
+  const int half = a.rot / 2, v0 = y.off / kV, rv = a.rot / kV, hv = rv / 2;
   const int total = part.nr * part.nh, step = kThreads / lanes;
   const float inv_dim = 1.f / float(y.dim);
-  for (int i0 = 0; i0 < total; i0 += step) {       // (uniform: the shuffles need whole warps)
-    const int i = i0 + int(threadIdx.x) / lanes;
-    const bool on = i < total;
-    int row = 0, head = 0;
-    if (on) part.at(i, row, head);
-    const uint8_t* x = static_cast<const uint8_t*>(y.x) + ((part.row0 + row) * y.x_stride + (long long)head * y.dim) * kE;
-    uint8_t* out = static_cast<uint8_t*>(y.out) + ((part.row0 + row) * y.out_stride + (long long)head * y.dim) * kE;
-    const float* gain = y.gain == nullptr ? nullptr : y.gain + (y.gain_each ? (long long)head * y.dim : 0);
-    Vec<kBytes> va[kNv], vb[kNv];
+  const bool each = y.gain_each != 0;
+  // gains that all heads share stay in registers: a lane's vectors have the same place in every head
+  float g[kNv][kV];
+  auto load_gains = [&](const float* gain) {
 #pragma unroll
     for (int m = 0; m < kNv; ++m) {
-      const int j = l + m * lanes, p = j - v0;      // p: place in the turned vectors
-      if (on && j < n_vecs) {
-        va[m].load(x + j * kBytes);
-        if (hv > 0 && uint32_t(p) < uint32_t(rv)) vb[m].load(x + (p < hv ? j + hv : j - hv) * kBytes);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) g[m][e] = 1.f;
+      if (gain != nullptr && l + m * lanes < n_vecs) load_gain<kV>(gain + (l + m * lanes) * kV, g[m]);
+    }
+  };
+  if (!each) load_gains(y.gain);
+  auto address = [&](int i, long long stride) -> long long {   // of head i of the part, in bytes
+    int row, head;
+    part.at(i, row, head);
+    return ((part.row0 + row) * stride + (long long)head * y.dim) * kE;
+  };
+  Vec<kBytes> next[kNv];                           // the next head, on its way while this one is turned
+  auto fetch = [&](int i) {
+    const uint8_t* x = static_cast<const uint8_t*>(y.x) + (i < total ? address(i, y.x_stride) : 0);
+#pragma unroll
+    for (int m = 0; m < kNv; ++m) {
+      const int j = l + m * lanes;
+      if (i < total && j < n_vecs) {
+        next[m].load(x + j * kBytes);
       } else {
 #pragma unroll
-        for (int e = 0; e < kBytes / 4; ++e) va[m].w[e] = 0u;
+        for (int e = 0; e < kBytes / 4; ++e) next[m].w[e] = 0u;
       }
     }
+  };
+  const int first = int(threadIdx.x) / lanes;
+  fetch(first);
+  for (int i0 = 0; i0 < total; i0 += step) {       // (uniform: the shuffles need whole warps)
+    const int i = i0 + first;
+    const bool on = i < total;
     float f[kNv][kV];
-    float mean = 0.f, sum = 0.f;
+    Vec<kBytes> vb[kPartner == kLoaded ? kNv : 1];
 #pragma unroll
-    for (int m = 0; m < kNv; ++m) unpack<kBf16, kBytes>(va[m], f[m]);
+    for (int m = 0; m < kNv; ++m) unpack<kBf16, kBytes>(next[m], f[m]);
+    if constexpr (kPartner == kLoaded) {
+      const uint8_t* x = static_cast<const uint8_t*>(y.x) + (on ? address(i, y.x_stride) : 0);
+#pragma unroll
+      for (int m = 0; m < kNv; ++m) {
+        const int j = l + m * lanes, p = j - v0;
+        if (on && j < n_vecs && uint32_t(p) < uint32_t(rv)) vb[m].load(x + (p < hv ? j + hv : j - hv) * kBytes);
+      }
+    }
+    fetch(i + step);
+    float mean = 0.f, sum = 0.f;
     if (a.center) {
 #pragma unroll
       for (int m = 0; m < kNv; ++m)
@@ -127,62 +158,80 @@ CSA2_DEV void norm_vectors(const NormRopeArgs& a, const NormRopeArgs::Slot& y, c
     }
     const float inv = __frsqrt_rn(__fmaf_rn(sum_lanes(sum, lanes), inv_dim, a.eps));
     __syncwarp();                                  // in place: every lane has loaded the head
-    if (!on) continue;
+    int row = 0, head = 0;
+    if (on) part.at(i, row, head);
+    const float* gain = y.gain == nullptr || !each ? y.gain : y.gain + (long long)head * y.dim;
+    if (each) load_gains(gain);
+#pragma unroll
+    for (int m = 0; m < kNv; ++m)
+#pragma unroll
+      for (int e = 0; e < kV; ++e) f[m][e] = f[m][e] * inv * g[m][e];
+    uint8_t* out = static_cast<uint8_t*>(y.out) + (on ? address(i, y.out_stride) : 0);
+    const float2* c = cs + row * half;
+    float r[kNv][kV];
 #pragma unroll
     for (int m = 0; m < kNv; ++m) {
-      const int j = l + m * lanes, p = j - v0;
-      if (j >= n_vecs) continue;
-      float g[kV], r[kV];
+      const int j = l + m * lanes, p = j - v0;      // p: place in the turned vectors
+      const bool turned = uint32_t(p) < uint32_t(rv);
 #pragma unroll
-      for (int e = 0; e < kV; ++e) g[e] = 1.f;
-      if (gain != nullptr) load_gain<kV>(gain + j * kV, g);
-#pragma unroll
-      for (int e = 0; e < kV; ++e) r[e] = f[m][e] * inv * g[e];
-      if (uint32_t(p) < uint32_t(rv)) {
-        const float2* c = cs + row * half;
-        if (hv > 0) {
-          const bool low = p < hv;
-          float b[kV];
-          unpack<kBf16, kBytes>(vb[m], b);
-#pragma unroll
-          for (int e = 0; e < kV; ++e) g[e] = 1.f;
-          if (gain != nullptr) load_gain<kV>(gain + (low ? j + hv : j - hv) * kV, g);
-          c += (low ? p : p - hv) * kV;
-#pragma unroll
-          for (int e = 0; e < kV; ++e) {
-            const float other = (b[e] - mean) * inv * g[e];
-            const float2 t = c[e];
-            r[e] = r[e] * t.x + (low ? -other : other) * t.y;
-          }
-        } else {
-          c += p * (kV / 2);
+      for (int e = 0; e < kV; ++e) r[m][e] = f[m][e];
+      if constexpr (kPartner == kNoPartner) {
+        if (turned) {
+          const float2* t = c + p * (kV / 2);
 #pragma unroll
           for (int e = 0; e < kV / 2; ++e) {
-            const float2 t = c[e];
-            const float u = r[2 * e], v = r[2 * e + 1];
-            r[2 * e] = u * t.x - v * t.y;
-            r[2 * e + 1] = v * t.x + u * t.y;
+            const float2 z = t[e];
+            r[m][2 * e] = f[m][2 * e] * z.x - f[m][2 * e + 1] * z.y;
+            r[m][2 * e + 1] = f[m][2 * e + 1] * z.x + f[m][2 * e] * z.y;
+          }
+        }
+      } else {
+        const bool low = p < hv;
+        float b[kV];
+        if constexpr (kPartner == kSameLane) {
+          const int to = low ? m + hv / lanes : m - hv / lanes;
+#pragma unroll
+          for (int k = 0; k < kNv; ++k)
+            if (k == to) {
+#pragma unroll
+              for (int e = 0; e < kV; ++e) b[e] = f[k][e];
+            }
+        } else if constexpr (kPartner == kOtherLane) {
+          // (whole warps: a vector is turned in all lanes or, of a narrow range, in some; the others' numbers are not used)
+#pragma unroll
+          for (int e = 0; e < kV; ++e) b[e] = __shfl_xor_sync(0xffffffffu, f[m][e], hv);
+        } else if (turned) {
+          unpack<kBf16, kBytes>(vb[m], b);
+          float gb[kV];
+#pragma unroll
+          for (int e = 0; e < kV; ++e) gb[e] = 1.f;
+          if (gain != nullptr) load_gain<kV>(gain + (low ? j + hv : j - hv) * kV, gb);
+#pragma unroll
+          for (int e = 0; e < kV; ++e) b[e] = (b[e] - mean) * inv * gb[e];
+        }
+        if (turned) {
+          const float2* t = c + (low ? p : p - hv) * kV;
+#pragma unroll
+          for (int e = 0; e < kV; ++e) {
+            const float2 z = t[e];
+            r[m][e] = f[m][e] * z.x + (low ? -b[e] : b[e]) * z.y;
           }
         }
       }
+    }
+    if (!on) continue;
+#pragma unroll
+    for (int m = 0; m < kNv; ++m) {
+      const int j = l + m * lanes;
+      if (j >= n_vecs) continue;
       Vec<kBytes> w;
 #pragma unroll
       for (int e = 0; e < kBytes / 4; ++e) {
-        if constexpr (kBf16) w.w[e] = pack_bf16(r[2 * e], r[2 * e + 1]);
-        else w.w[e] = __float_as_uint(r[e]);
+        if constexpr (kBf16) w.w[e] = pack_bf16(r[m][2 * e], r[m][2 * e + 1]);
+        else w.w[e] = __float_as_uint(r[m][e]);
       }
       w.store(out + j * kBytes);
     }
-  }
-}
-
-template <bool kBf16, int kBytes>
-CSA2_DEV void norm_wide(const NormRopeArgs& a, const NormRopeArgs::Slot& y, const Part& part, const float2* cs) {
-  switch (y.vecs) {
-    case 1: norm_vectors<kBf16, kBytes, 1>(a, y, part, cs); break;
-    case 2: norm_vectors<kBf16, kBytes, 2>(a, y, part, cs); break;
-    case 3: norm_vectors<kBf16, kBytes, 3>(a, y, part, cs); break;
-    default: norm_vectors<kBf16, kBytes, 4>(a, y, part, cs); break;
   }
 }
 
@@ -230,7 +279,9 @@ CSA2_DEV void norm_scalar(const NormRopeArgs& a, const NormRopeArgs::Slot& y, co
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
+// The tensors of a launch that are alike: one element type, one vector size (0: number by number), one place of partners.
+template <bool kBf16, int kBytes, int kNv, int kPartner>
+__global__ void __launch_bounds__(kThreads, kNv == 4 ? 2 : kPerSm) norm_rope_kernel(const __grid_constant__ NormRopeArgs a) {
   extern __shared__ __align__(16) float2 cs[];           // [per_block][rot / 2]
   __shared__ long long step[kMaxRopePairs];
   const long long row0 = (long long)blockIdx.x * a.per_block;
@@ -241,18 +292,43 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rope_kernel(const __grid_con
   for (int k = 0; k < a.n_slots; ++k) {
     const NormRopeArgs::Slot& y = a.slot[k];
     const Part part(y, row0, nr);
-    const bool f32 = y.dtype == 1;
-    if (y.bytes == 16) f32 ? norm_wide<false, 16>(a, y, part, cs) : norm_wide<true, 16>(a, y, part, cs);
-    else if (y.bytes == 8) f32 ? norm_wide<false, 8>(a, y, part, cs) : norm_wide<true, 8>(a, y, part, cs);
-    else f32 ? norm_scalar<float>(a, y, part, cs) : norm_scalar<__nv_bfloat16>(a, y, part, cs);
+    if constexpr (kBytes == 0) {
+      if (kBf16) norm_scalar<__nv_bfloat16>(a, y, part, cs);
+      else norm_scalar<float>(a, y, part, cs);
+    } else {
+      norm_vectors<kBf16, kBytes, kNv, kPartner>(a, y, part, cs);
+    }
   }
 }
 
-// Vectors of 16 or 8 bytes that fit the tensor's sizes and addresses (0: none do), and the lanes of a head with the
-// vectors of each that leave the fewest over (of those, the most lanes).
+using Kernel = void (*)(NormRopeArgs);
+
+template <bool kBf16, int kBytes, int kNv>
+Kernel kernel_of(int partner) {
+  return partner == kNoPartner  ? norm_rope_kernel<kBf16, kBytes, kNv, kNoPartner>
+         : partner == kSameLane ? norm_rope_kernel<kBf16, kBytes, kNv, (kNv > 1 ? kSameLane : kLoaded)>
+         : partner == kOtherLane ? norm_rope_kernel<kBf16, kBytes, kNv, kOtherLane>
+                                 : norm_rope_kernel<kBf16, kBytes, kNv, kLoaded>;
+}
+
+template <bool kBf16, int kBytes>
+Kernel kernel_of(int vecs, int partner) {
+  return vecs == 1 ? kernel_of<kBf16, kBytes, 1>(partner) : vecs == 2 ? kernel_of<kBf16, kBytes, 2>(partner)
+         : vecs == 3 ? kernel_of<kBf16, kBytes, 3>(partner) : kernel_of<kBf16, kBytes, 4>(partner);
+}
+
+Kernel kernel_of(const NormRopeArgs::Slot& y) {
+  const bool f32 = y.dtype == 1;
+  if (y.bytes == 0) return f32 ? norm_rope_kernel<false, 0, 1, kNoPartner> : norm_rope_kernel<true, 0, 1, kNoPartner>;
+  if (y.bytes == 16) return f32 ? kernel_of<false, 16>(y.vecs, y.partner) : kernel_of<true, 16>(y.vecs, y.partner);
+  return f32 ? kernel_of<false, 8>(y.vecs, y.partner) : kernel_of<true, 8>(y.vecs, y.partner);
+}
+
+// Vectors of 16 or 8 bytes that fit the tensor's sizes and addresses (0: none do), the lanes of a head with the
+// vectors of each that leave the fewest over (of those, two vectors a lane where they can be had), and where partners are.
 void choose_vectors(NormRopeArgs::Slot& y, int rot, bool interleaved) {
   const int e = y.dtype == 1 ? 4 : 2;
-  y.bytes = 0;
+  y.bytes = y.vecs = y.partner = 0;
   for (int w = 16; w >= 8; w /= 2) {
     const int v = w / e;
     const uintptr_t at = reinterpret_cast<uintptr_t>(y.x) | reinterpret_cast<uintptr_t>(y.out);
@@ -264,39 +340,58 @@ void choose_vectors(NormRopeArgs::Slot& y, int rot, bool interleaved) {
     int best = 1 << 30;
     for (int lanes = 32; lanes >= 1; lanes /= 2) {
       const int m = (n + lanes - 1) / lanes;
-      if (m > kMaxVecs || m * lanes - n >= best) continue;
+      if (m > kMaxVecs || m * lanes - n > best - (m > 2)) continue;   // (two vectors a lane rather than one: more bytes on their way)
       best = m * lanes - n;
       y.lanes = lanes;
       y.vecs = m;
     }
     y.bytes = w;
+    const int rv = rot / v, hv = rv / 2, v0 = y.off / v;
+    if (rot == 0 || interleaved) y.partner = kNoPartner;
+    else if (hv % y.lanes == 0) y.partner = kSameLane;
+    else if (y.lanes % rv == 0 && v0 % rv == 0) y.partner = kOtherLane;
+    else y.partner = kLoaded;
     return;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(NormRopeArgs& a, int rows, cudaStream_t st) {
+cudaError_t launch_norm_rope(const NormRopeArgs& a, int rows, cudaStream_t st) {
   if (rows == 0) return cudaSuccess;
-  int heads = 0, vecs = 0;   // heads of the tensor with the most; 16-byte pieces of a row of all tensors
-  for (int k = 0; k < a.n_slots; ++k) {
-    NormRopeArgs::Slot& y = a.slot[k];
-    choose_vectors(y, a.rot, a.interleaved != 0);
-    heads = heads > y.heads ? heads : y.heads;
-    vecs += (y.heads * y.dim * (y.dtype == 1 ? 4 : 2) + 15) / 16;
+  NormRopeArgs left = a;
+  for (int k = 0; k < left.n_slots; ++k) choose_vectors(left.slot[k], a.rot, a.interleaved != 0);
+  while (left.n_slots > 0) {   // a launch for the tensors that are alike: queries and keys mostly are
+    NormRopeArgs now = left;
+    now.n_slots = 0;
+    const NormRopeArgs::Slot& y = left.slot[0];
+    const Kernel kernel = kernel_of(y);
+    int rest = 0, heads = 0;   // heads of the tensor with the most
+    for (int k = 0; k < left.n_slots; ++k) {
+      const NormRopeArgs::Slot z = left.slot[k];
+      if (kernel_of(z) == kernel) {
+        now.slot[now.n_slots++] = z;
+        heads = heads > z.heads ? heads : z.heads;
+      } else {
+        left.slot[rest++] = z;
+      }
+    }
+    left.n_slots = rest;
+    // Rows of a block and blocks of a row as in rope.cu, but that the blocks fit the SMs' places at once.
+    const int want = kPerSm * device_sm_count();
+    int most = 64;
+    while (most > 8 && most * (a.rot / 2) > 8 * kMaxRopePairs) --most;
+    now.rows = rows;
+    now.per_block = (rows - 1) / want + 1 > most ? most : (rows - 1) / want + 1;
+    const int blocks = (rows - 1) / now.per_block + 1;
+    int split = blocks >= want ? 1 : want / blocks;
+    split = split > heads ? heads : split < 1 ? 1 : split;
+    note_launch();
+    const cudaError_t e = launch_pdl(kernel, dim3(unsigned(blocks), unsigned(split)), dim3(kThreads),
+                                     size_t(now.per_block) * (a.rot / 2) * sizeof(float2), st, 1, now);
+    if (e != cudaSuccess) return e;
   }
-  // Rows of a block and blocks of a row as in rope.cu.
-  const int want = 4 * device_sm_count();
-  int most = 64;
-  while (most > 8 && (most * (a.rot / 2) > 8 * kMaxRopePairs || most * vecs > 4096)) --most;
-  a.rows = rows;
-  a.per_block = rows / want < 1 ? 1 : rows / want > most ? most : rows / want;
-  const int blocks = (rows - 1) / a.per_block + 1;
-  int split = blocks >= want ? 1 : (want + blocks - 1) / blocks;
-  split = split > heads ? heads : split;
-  note_launch();
-  return launch_pdl(norm_rope_kernel, dim3(unsigned(blocks), unsigned(split)), dim3(kThreads),
-                    size_t(a.per_block) * (a.rot / 2) * sizeof(float2), st, 1, a);
+  return cudaSuccess;
 }
 
 }  // namespace csa2
