@@ -52,32 +52,32 @@ CSA2_DEV void kv4_eight(uint32_t codes, __half2 scale, float (&x)[8]) {
 
 // 16 numbers as codes and a scale's byte.  The scale is the e4m3 number nearest to a sixth of the
 // largest magnitude (ties to even, at least 2^-9, at most 448), a code the e2m1 number nearest to x / scale (ties to even, at
-// most 6).  kDivide: x are any fp32 numbers, whose quotients are rounded to fp32 first; that moves none onto a
+// most 6); `down` is 2^-exp, which no product here rounds by.
+// kF32: x are any fp32 numbers, whose quotients are rounded to fp32 first; that moves none onto a
 // border between two codes, as the border times the scale is itself an fp32 number and its neighbours' quotients
-// are more than half a step away.  Without it they have 8 significant bits (bf16): a quotient that
-// is not on a border is 2^-8 away from it, so that a product with 1 / scale, off by 2^-23, rounded to 14 bits tells.
-template <bool kDivide>
-CSA2_DEV uint8_t kv4_quantise(float (&x)[16], float down, uint2& codes) {
+// are more than half a step away.  Otherwise they have 8 significant bits (bf16), and a quotient that is not on a border (of 3
+// bits; 5 between two scales) is 2^-8 away from it: products with reciprocals, off by 2^-22, are rounded to 11 bits (fp16,
+// or fp32 bits), which puts those of borders onto them and moves no other as far.
+template <bool kF32>
+CSA2_DEV uint8_t kv4_quantise(const float (&x)[16], float down, uint2& codes) {
   float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    x[i] *= down;
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
-  }
+  for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+  top *= down;
   codes = make_uint2(0u, 0u);
   if (!(top < INFINITY)) return 0x7f;
-  const uint8_t byte = __nv_cvt_float_to_fp8(fmaxf(__fdiv_rn(top, 6.f), 0.001953125f), __NV_SATFINITE, __NV_E4M3);
-  const float scale = __half2float(kv4_scale(byte)), inv = __fdiv_rn(1.f, scale);
+  const float sixth = kF32 ? __fdiv_rn(top, 6.f) : __uint_as_float((__float_as_uint(top * (1.f / 6.f)) + 0x200u) & ~0x3ffu);
+  const uint8_t byte = __nv_cvt_float_to_fp8(fmaxf(sixth, 0.001953125f), __NV_SATFINITE, __NV_E4M3);
+  const float scale = __half2float(kv4_scale(byte));
+  float inv = 0.f;
+  if (!kF32) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  const float mul = inv * down;
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float2 y;
-    if (kDivide) {
-      y = make_float2(__fdiv_rn(x[2 * i], scale), __fdiv_rn(x[2 * i + 1], scale));
-    } else {
-      y = make_float2(__uint_as_float((__float_as_uint(x[2 * i] * inv) + 0x200u) & ~0x3ffu),
-                      __uint_as_float((__float_as_uint(x[2 * i + 1] * inv) + 0x200u) & ~0x3ffu));
-    }
+    if (kF32) y = make_float2(__fdiv_rn(x[2 * i] * down, scale), __fdiv_rn(x[2 * i + 1] * down, scale));
+    else y = __half22float2(__floats2half2_rn(x[2 * i] * mul, x[2 * i + 1] * mul));
     w[i >> 2] |= uint32_t(__nv_cvt_float2_to_fp4x2(y, __NV_E2M1, cudaRoundNearest)) << (8 * (i & 3));
   }
   codes = make_uint2(w[0], w[1]);

@@ -7,7 +7,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileEntries = 32;   // packed in shared memory before they are written as whole lines
+constexpr int kTileEntries = 64;   // packed in shared memory before they are written as whole lines
 
 // ------------------------------------------------------------------ append
 
@@ -42,9 +42,9 @@ struct Raw {
 // entry; its members come from the cache in front of the new entries and from the new ones, never from what
 // another CTA writes.
 template <bool kF32>
-__global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kF32 ? 3 : 5) kv4_append_kernel(const Kv4AppendArgs a) {
   extern __shared__ __align__(16) uint8_t tile[];          // [kTileEntries][entry]
-  constexpr int kBatch = kF32 ? 2 : 3, kE = kF32 ? 4 : 2;  // groups a thread has on their way; an element's bytes
+  constexpr int kBatch = 2, kE = kF32 ? 4 : 2;             // groups a thread has on their way; an element's bytes
   const int b = blockIdx.y, tid = threadIdx.x;
   const int gk = kv4_groups(a.k_dim), groups = gk + kv4_groups(a.v_dim), bytes = kv4_bytes(a.k_dim, a.v_dim);
   const uint32_t m_groups = 0xffffffffu / uint32_t(groups) + 1u;   // (two at least)
@@ -111,6 +111,10 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArg
   } else {
     for (int i = tid; i < n * (x_bytes / 2); i += kThreads) reinterpret_cast<uint16_t*>(xd)[i] = reinterpret_cast<const uint16_t*>(xs)[i];
   }
+  __syncthreads();   // the tile is packed; and every thread has read n_valid[b]
+  uint4* out = reinterpret_cast<uint4*>(a.kv + dst * bytes);
+  for (int i = tid; i < n * (bytes / 16); i += kThreads) out[i] = reinterpret_cast<const uint4*>(tile)[i];
+  if (gridDim.x == 1 && tid == 0) a.n_valid[b] = nv0 + m;
   if (a.kb != nullptr && n > 0) {
     // blocks whose first new entry is s0 .. s0 + n - 1 of the new ones
     const int nv1 = nv0 + m, p0 = nv0 + s0;
@@ -160,10 +164,6 @@ __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4AppendArg
       }
     }
   }
-  __syncthreads();   // the tile is packed; and every thread has read n_valid[b]
-  uint4* out = reinterpret_cast<uint4*>(a.kv + dst * bytes);
-  for (int i = tid; i < n * (bytes / 16); i += kThreads) out[i] = reinterpret_cast<const uint4*>(tile)[i];
-  if (gridDim.x == 1 && tid == 0) a.n_valid[b] = nv0 + m;
 }
 
 // The fill counts of sequences that several CTAs have read them for.
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) kv4_count_kernel(const Kv4AppendArgs
 
 // ------------------------------------------------------------------ rows
 
-constexpr int kBatch = 4;          // 16-byte pieces of rows a thread has on their way
+constexpr int kBatch = 5;          // 16-byte pieces of rows a thread has on their way: 32 rows of 192 / 128 dims at once
 constexpr int kMaxRows = 32;       // of a CTA
 
 // The entries of a CTA's rows, null where there is none, into shared memory.
