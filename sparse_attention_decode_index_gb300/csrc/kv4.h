@@ -46,11 +46,12 @@ struct Kv4AppendArgs {
   int* n_valid;              // [B] (read and updated)
   int n_entries, nb_cap, k_dim, v_dim, idx_dim, block, round_to_int, dtype;
   float k_down, v_down;      // 2^-k_exp, 2^-v_exp
+  int per_cta;               // entries a CTA packs (set by the launcher)
   int wide, wide_idx;        // whole 16-byte pieces at aligned addresses: of keys and values, of indexer keys
   int* err;
 };
 
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int batch, cudaStream_t st);
+cudaError_t launch_kv4_append(Kv4AppendArgs& a, int batch, cudaStream_t st);
 
 struct Kv4RowsArgs {
   const uint8_t* kv;         // [B / seq_div, N, kv4_bytes]

@@ -7,7 +7,7 @@ namespace csa2 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTileEntries = 64;   // packed in shared memory before they are written as whole lines
+constexpr int kTileEntries = 64;   // packed in shared memory before they are written as whole lines (half of it beyond 48 KB)
 
 // ------------------------------------------------------------------ append
 
@@ -36,19 +36,19 @@ struct Raw {
   }
 };
 
-// Each CTA packs kTileEntries of a sequence's new entries: a thread packs a group of 16 dims at a time into shared memory, from
+// Each CTA packs per_cta of a sequence's new entries: a thread packs a group of 16 dims at a time into shared memory, from
 // where the entries, contiguous in the cache, go out in 16-byte pieces.  The first groups are asked for beside the counts,
 // whatever these say (the rows up to max_new can be read).  A block's summary key is the CTA's that has its first new
 // entry; its members come from the cache in front of the new entries and from the new ones, never from what
 // another CTA writes.
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, kF32 ? 3 : 5) kv4_append_kernel(const Kv4AppendArgs a) {
-  extern __shared__ __align__(16) uint8_t tile[];          // [kTileEntries][entry]
+  extern __shared__ __align__(16) uint8_t tile[];          // [per_cta][entry]
   constexpr int kBatch = 2, kE = kF32 ? 4 : 2;             // groups a thread has on their way; an element's bytes
   const int b = blockIdx.y, tid = threadIdx.x;
   const int gk = kv4_groups(a.k_dim), groups = gk + kv4_groups(a.v_dim), bytes = kv4_bytes(a.k_dim, a.v_dim);
   const uint32_t m_groups = 0xffffffffu / uint32_t(groups) + 1u;   // (two at least)
-  const int s0 = blockIdx.x * kTileEntries, n_most = min(kTileEntries, a.max_new - s0);
+  const int s0 = blockIdx.x * a.per_cta, n_most = min(a.per_cta, a.max_new - s0);
   const long long src = (long long)b * a.max_new + s0;
   const uint8_t *k_new = static_cast<const uint8_t*>(a.k_new) + src * a.k_dim * kE, *v_new = static_cast<const uint8_t*>(a.v_new) + src * a.v_dim * kE;
   pdl_wait();   // no early trigger: the next launch may read what this one writes before its own wait
@@ -257,11 +257,13 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_any_kernel(const Kv4RowsArg
 
 }  // namespace
 
-cudaError_t launch_kv4_append(const Kv4AppendArgs& a, int batch, cudaStream_t st) {
+cudaError_t launch_kv4_append(Kv4AppendArgs& a, int batch, cudaStream_t st) {
   if (batch == 0 || a.max_new == 0) return cudaSuccess;
-  const unsigned chunks = unsigned((a.max_new - 1) / kTileEntries + 1);
+  const int bytes = kv4_bytes(a.k_dim, a.v_dim);
+  a.per_cta = kTileEntries * bytes <= 48 << 10 ? kTileEntries : kTileEntries / 2;
+  const unsigned chunks = unsigned((a.max_new - 1) / a.per_cta + 1);
   note_launch();
-  const size_t smem = size_t(kTileEntries) * kv4_bytes(a.k_dim, a.v_dim);
+  const size_t smem = size_t(a.per_cta) * bytes;
   cudaError_t e = launch_pdl(a.dtype == 1 ? kv4_append_kernel<true> : kv4_append_kernel<false>, dim3(chunks, unsigned(batch)), dim3(kThreads),
                              smem, st, 1, a);
   if (e != cudaSuccess || chunks == 1) return e;

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&c.full[i], kGroupWarps);
-      mbar_init(&c.empty[i], 2 + kSoftmaxWarps);   // the values' end; everyone else who looks at its mask
+      mbar_init(&c.empty[i], 1 + kSoftmaxWarps);   // the values' end; its mask has been read
     }
     for (int b = 0; b < kScores; ++b) {
       mbar_init(&c.s_full[b], 1);
@@ -204,28 +204,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = uint32_t(warp * 32) << 16;
     const uint32_t o_addr = tmem + lanes + kOCol;
     const float window_scale = a.scale * log2e, window_up = 1.f / a.v_up;
-    uint32_t items = 0, st = 0, lap = 0, buf = 0, turn = 0;   // buf: of S, turn: its times round, for tiles that have keys
+    uint32_t items = 0, st = 0, buf = 0, turn = 0;            // buf: of S, turn: its times round
     bool ok = true;
     for (int item = item0; item < n_items && ok; item += step) {
       float ref = -INFINITY, sum = 0.f;        // the exponent that P and O are relative to, and the weights' sum
       bool first = true;
       for (int t = range.first; t < range.last; ++t) {
-        ok = wait_warp(c, &c.full[st], lap & 1, a.err);
-        if (!ok) break;
-        const uint64_t all = c.mask[st];
-        warp_arrive(&c.empty[st]);
-        if (++st == kStages) {
-          st = 0;
-          ++lap;
-        }
-        if (all == 0) continue;
-        const uint32_t mask = uint32_t(all >> (32 * half));
-        const bool window = t >= range.window;
-        const uint32_t s_addr = tmem + lanes + kSCol + buf * 64;
         ok = wait_warp(c, &c.s_full[buf], turn & 1, a.err);
         if (!ok) break;
         tc_fence_after();
-        uint32_t p[16];
+        const uint32_t mask = reinterpret_cast<const uint32_t*>(&c.mask[st])[half];
+        warp_arrive(&c.empty[st]);
+        if (++st == kStages) st = 0;
+        const bool window = t >= range.window;
+        const uint32_t s_addr = tmem + lanes + kSCol + buf * 64;
+        uint32_t p[32];                        // weights of the tile's 64 keys: those of the other half are 0
         if (mask != 0) {
           const float sl2 = window ? window_scale : c.q_scale[items & 1][tid];
           uint32_t s[32];
@@ -287,17 +280,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           total = add2(total, other);
           sum += total.x + total.y;
+          first = false;
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) p[j] = 0;
-          // Another half's tile may come first: O is then 0 times anything, and this row's exponent is still open.
         }
-        first = false;
-        uint32_t zero[16];
+        if (half == 0) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) zero[j] = 0;
-        tmem_st16(s_addr + 16 * half, p);
-        tmem_st16(s_addr + 16 * (1 - half), zero);
+          for (int j = 16; j < 32; ++j) p[j] = 0;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            p[16 + j] = p[j];
+            p[j] = 0;
+          }
+        }
+        tmem_st32(s_addr, p);
         tc_wait_st();
         tc_fence_before();
         warp_arrive(&c.p_full[buf]);
@@ -576,30 +574,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int row0 = (here.t - range.window) * kTile;
         const int n = min(max(ns - row0, 0), kTile), y = here.item * a.swa + row0;
-        if (w > 0 || n == 0) {
-          if (w == 0 && lane == 0) c.mask[st] = 0;
+        if (w > 0) {
           warp_arrive(&c.full[st]);
         } else {
           uint64_t* bar = n == kTile ? &c.full[st] : &c.window[group];
           if (lane == 0) {
             c.mask[st] = n == kTile ? ~0ull : (1ull << n) - 1ull;
-            mbar_arrive_expect_tx(bar, kKBytes + kVBytes);
+            if (n > 0) {
+              mbar_arrive_expect_tx(bar, kKBytes + kVBytes);
 #pragma unroll
-            for (int b = 0; b < kDk / 64; ++b) load_box(k_st + b * (kTile * 128), &k_map, 64 * b, y, bar);
+              for (int b = 0; b < kDk / 64; ++b) load_box(k_st + b * (kTile * 128), &k_map, 64 * b, y, bar);
 #pragma unroll
-            for (int b = 0; b < kDv / 64; ++b) load_box(v_st + b * (kTile * 128), &v_map, 64 * b, y, bar);
-          }
-          __syncwarp();
-          if (lane == 0 && here.item + step < n_items) {   // the next item's, which would come from memory (2 us)
-            const int far = y + step * a.swa;
+              for (int b = 0; b < kDv / 64; ++b) load_box(v_st + b * (kTile * 128), &v_map, 64 * b, y, bar);
+            }
+            if (here.item + step < n_items) {  // the next item's, which would come from memory (2 us)
+              const int far = y + step * a.swa;
 #pragma unroll
-            for (int b = 0; b < kDk / 64; ++b) prefetch_box(&k_map, 64 * b, far);
+              for (int b = 0; b < kDk / 64; ++b) prefetch_box(&k_map, 64 * b, far);
 #pragma unroll
-            for (int b = 0; b < kDv / 64; ++b) prefetch_box(&v_map, 64 * b, far);
+              for (int b = 0; b < kDv / 64; ++b) prefetch_box(&v_map, 64 * b, far);
+            }
           }
           __syncwarp();
           if (n < kTile) {                     // values behind the count are zeroed: they meet weights of 0, and might be NaN
-            ok = wait_warp(c, &c.window[group], waits++ & 1, a.err);
+            ok = n == 0 || wait_warp(c, &c.window[group], waits++ & 1, a.err);
             if (!ok) break;
             for (int i = lane; i < (kTile - n) * 16; i += 32) {
               const int r = n + (i >> 4), p = i & 15;
@@ -677,13 +675,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         return wait_warp(c, &c.q_full[1], items & 1, a.err);
       };
       for (int t = range.first; t < range.last && ok; ++t) {
-        // (S lies where the weights of the third tile before lay)
-        if (scores && turn > 0) ok = wait_warp(c, &c.s_free[buf], (turn - 1) & 1, a.err);
-        ok = ok && wait_warp(c, &c.full[st], lap & 1, a.err);
-        if (!ok) break;
-        const uint64_t mask = c.mask[st];
         const uint32_t here = st;
-        if (scores) warp_arrive(&c.empty[here]);
+        const bool window = t >= range.window;
+        if (scores) {
+          if (turn > 0) ok = wait_warp(c, &c.s_free[buf], (turn - 1) & 1, a.err);   // (S lies where the weights of the third tile before lay)
+          ok = ok && wait_warp(c, &c.full[st], lap & 1, a.err);
+        } else {
+          ok = wait_warp(c, &c.p_full[buf], turn & 1, a.err);
+        }
+        if (!ok) break;
         if (++st == kStages) {
           st = 0;
           ++lap;
@@ -691,12 +691,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The rows are generic-proxy writes, which the tensor core reads, and TMA overwrites, by the async proxy.  The fence stands
         // here, behind the wait, and not with the producers: theirs would wait for the copies that are on their way (1.5 us a tile).
         fence_async_smem();
-        const bool window = t >= range.window;
-        if (mask == 0) {                       // no key: nobody looks at it
-          if (!scores && elect_one()) tc_commit(&c.empty[here]);
-          __syncwarp();
-          continue;
-        }
         if (scores) {
           if (window && half) ok = half_done();
           if (!ok) break;
@@ -710,8 +704,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit(&c.s_full[buf]);
           }
         } else {
-          ok = wait_warp(c, &c.p_full[buf], turn & 1, a.err);
-          if (!ok) break;
           tc_fence_after();
           const uint64_t v = v0 + here * (kVBytes >> 4);
           const uint32_t desc = window ? pv_b : pv_h;
