@@ -6,7 +6,7 @@
 namespace csa2 {
 
 // Keys of once_per_device, behind DraftSetupKey's.
-enum Kv4SetupKey { kSetupKv4Tc = 32, kSetupKv4Generic };   // the last and the next two: heads a CTA
+enum Kv4SetupKey { kSetupKv4Tc = 32, kSetupKv4One, kSetupKv4Four, kSetupKv4Full };
 
 // Norm of heads with rotary positions (norm_rope.cu).
 struct NormRopeArgs {

@@ -4,17 +4,15 @@
 // are taken out of the rows: a main key's product is multiplied by 2^k_exp with
 // the softmax scale, a main value's weight by 2^v_exp.
 //
-// Any head count, dims and element type, in fp32: a CTA takes up to four heads of a
+// Any head count, dims and element type, in fp32: a CTA takes one head or four of a
 // query.  Eight lanes go through a row together, a group of 16 dims each, so that a warp has
-// four rows on their way; a lane multiplies its numbers with every head of the CTA.  Scores stay in
+// four rows on their way, or eight (fp32, 228 CTAs: 103 -> 72 us); a lane multiplies its numbers with every head of the CTA.  Scores stay in
 // shared memory; every warp sums the values of its own rows, and the warps' sums are added in order.
 #include "kv4.cuh"
 
 namespace csa2 {
 
 namespace {
-
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 // 16 numbers of dims d .. d + 15 (of dim), zeros behind: of a window row, or of a group's codes.
 CSA2_DEV void window16(const void* rows, long long row, int d, int dim, int dtype, bool wide, float (&x)[16]) {
@@ -55,10 +53,11 @@ CSA2_DEV void packed16(const uint8_t* entry, int group, int groups, float (&x)[1
   for (int i = 0; i < 8; ++i) x[8 + i] = v[i];
 }
 
-// kHeads heads of query blockIdx.y.  Shared memory: q [kHeads][16 gk], weights [kHeads][slots], rows [slots], the warps'
+// kHeads heads of query blockIdx.y, kRows rows at a time for eight lanes.  Shared memory: q [kHeads][16 gk], weights [kHeads][slots], rows [slots], the warps'
 // sums [kWarps][kHeads][128].
-template <int kHeads>
+template <int kHeads, int kThreads, int kRows>
 __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4AttnArgs a) {
+  constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) float sh[];
   __shared__ float red[2][kHeads][kWarps];
   const int b = blockIdx.y, h0 = blockIdx.x * kHeads, nh = min(kHeads, a.heads - h0);
@@ -71,6 +70,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
   int* row = reinterpret_cast<int*>(part + kWarps * kHeads * 128);   // [slots]: entry, window row, or -1
   pdl_launch_dependents();
   pdl_wait();
+  const uint8_t* cache = a.kv + (long long)(b / a.seq_div) * a.n_entries * bytes;
   const int ns = clamp_count(a.n_swa[b], a.swa, blockIdx.x == 0 && tid == 0 ? a.err : nullptr);
   for (int i = tid; i < kHeads * 16 * gk; i += kThreads) {
     const int h = i / (16 * gk), d = i - h * 16 * gk;
@@ -88,45 +88,73 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
       e = j - a.topk;
     }
     row[j] = e < 0 ? -1 : e;
+    if (e >= 0) {
+      if (j < a.topk) {
+        const uint8_t* p = cache + (long long)e * bytes;
+        for (int i = 0; i < bytes; i += 128) asm volatile("prefetch.global.L2 [%0];" :: "l"(p + i));
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(p + bytes - 1));
+      }
+    }
   }
   __syncthreads();
-  const uint8_t* cache = a.kv + (long long)(b / a.seq_div) * a.n_entries * bytes;
+  // Numbers of group g (of key and value) of slot j's row e; zeros when there is none.
+  const auto numbers = [&](int j, int e, int g, float (&x)[16]) {
+    if (e < 0) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    } else if (j < a.topk) {
+      packed16(cache + (long long)e * bytes, g, groups, x);
+    } else if (g < gk) {
+      window16(a.k_swa, (long long)b * a.swa + e, 16 * g, a.k_dim, a.dtype, a.wide != 0, x);
+    } else {
+      window16(a.v_swa, (long long)b * a.swa + e, 16 * (g - gk), a.v_dim, a.dtype, a.wide != 0, x);
+    }
+  };
   // ---- scores
   float top[kHeads];
 #pragma unroll
   for (int h = 0; h < kHeads; ++h) top[h] = -INFINITY;
-  for (int j0 = 4 * warp; j0 < slots; j0 += 4 * kWarps) {
-    const int j = j0 + r4, e = j < slots ? row[j] : -1;
-    const bool main = j < a.topk;
-    float dot[kHeads];
+  for (int j0 = 4 * kRows * warp; j0 < slots; j0 += 4 * kRows * kWarps) {
+    int e[kRows];
+    float dot[kRows][kHeads];
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) dot[h] = 0.f;
-    if (e >= 0) {
-      for (int g = l8; g < gk; g += 8) {
-        float x[16];
-        if (main) packed16(cache + (long long)e * bytes, g, groups, x);
-        else window16(a.k_swa, (long long)b * a.swa + e, 16 * g, a.k_dim, a.dtype, a.wide != 0, x);
+    for (int u = 0; u < kRows; ++u) {
+      const int j = j0 + 4 * u + r4;
+      e[u] = j < slots ? row[j] : -1;
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-          const float4* q = reinterpret_cast<const float4*>(sq + (h * gk + g) * 16);
+      for (int h = 0; h < kHeads; ++h) dot[u][h] = 0.f;
+    }
+    for (int g = l8; g < gk; g += 8) {
+      float x[kRows][16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 y = q[i];
-            dot[h] = __fmaf_rn(x[4 * i], y.x, dot[h]);
-            dot[h] = __fmaf_rn(x[4 * i + 1], y.y, dot[h]);
-            dot[h] = __fmaf_rn(x[4 * i + 2], y.z, dot[h]);
-            dot[h] = __fmaf_rn(x[4 * i + 3], y.w, dot[h]);
+      for (int u = 0; u < kRows; ++u) numbers(j0 + 4 * u + r4, e[u], g, x[u]);
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+        const float4* q = reinterpret_cast<const float4*>(sq + (h * gk + g) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 y = q[i];
+#pragma unroll
+          for (int u = 0; u < kRows; ++u) {
+            dot[u][h] = __fmaf_rn(x[u][4 * i], y.x, dot[u][h]);
+            dot[u][h] = __fmaf_rn(x[u][4 * i + 1], y.y, dot[u][h]);
+            dot[u][h] = __fmaf_rn(x[u][4 * i + 2], y.z, dot[u][h]);
+            dot[u][h] = __fmaf_rn(x[u][4 * i + 3], y.w, dot[u][h]);
           }
         }
       }
     }
 #pragma unroll
-    for (int h = 0; h < kHeads; ++h) {
+    for (int u = 0; u < kRows; ++u) {
+      const int j = j0 + 4 * u + r4;
 #pragma unroll
-      for (int o = 1; o < 8; o <<= 1) dot[h] += __shfl_xor_sync(0xffffffffu, dot[h], o);
-      const float s = e >= 0 ? dot[h] * (main ? a.scale * a.k_up : a.scale) : -INFINITY;
-      if (l8 == 0 && j < slots) sw[h * slots + j] = s;
-      asm("max.NaN.f32 %0, %0, %1;" : "+f"(top[h]) : "f"(s));   // a NaN score makes its head's output NaN
+      for (int h = 0; h < kHeads; ++h) {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) dot[u][h] += __shfl_xor_sync(0xffffffffu, dot[u][h], o);
+        const float s = e[u] >= 0 ? dot[u][h] * (j < a.topk ? a.scale * a.k_up : a.scale) : -INFINITY;
+        if (l8 == 0 && j < slots) sw[h * slots + j] = s;
+        asm("max.NaN.f32 %0, %0, %1;" : "+f"(top[h]) : "f"(s));   // a NaN score makes its head's output NaN
+      }
     }
   }
 #pragma unroll
@@ -172,17 +200,19 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
     for (int h = 0; h < kHeads; ++h)
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[h][i] = 0.f;
-    for (int j = 4 * warp + r4; j < slots; j += 4 * kWarps) {
-      const int e = row[j];
-      if (e < 0 || g >= gv) continue;
-      float x[16];
-      if (j < a.topk) packed16(cache + (long long)e * bytes, gk + g, groups, x);
-      else window16(a.v_swa, (long long)b * a.swa + e, 16 * g, a.v_dim, a.dtype, a.wide != 0, x);
+    for (int j = 4 * kRows * warp + r4; g < gv && j < slots; j += 4 * kRows * kWarps) {
+      float x[kRows][16];
 #pragma unroll
-      for (int h = 0; h < kHeads; ++h) {
-        const float p = sw[h * slots + j];
+      for (int u = 0; u < kRows; ++u) numbers(j + 4 * u, j + 4 * u < slots ? row[j + 4 * u] : -1, gk + g, x[u]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[h][i] = __fmaf_rn(p, x[i], acc[h][i]);
+      for (int u = 0; u < kRows; ++u) {
+        if (j + 4 * u >= slots) continue;
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+          const float p = sw[h * slots + j + 4 * u];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[h][i] = __fmaf_rn(p, x[u][i], acc[h][i]);
+        }
       }
     }
 #pragma unroll
@@ -218,17 +248,17 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
   }
 }
 
-template <int kHeads>
+template <int kHeads, int kThreads, int kRows>
 cudaError_t launch_generic(const Kv4AttnArgs& a, int batch, cudaStream_t st) {
-  const int slots = a.topk + a.swa;
-  const size_t smem = (size_t(kHeads) * 16 * kv4_groups(a.k_dim) + (kHeads * slots + 3) / 4 * 4 + kWarps * kHeads * 128 + slots) * 4;
-  const cudaError_t e = once_per_device(kSetupKv4Generic + (kHeads == 4 ? 2 : kHeads - 1), [] {
-    return cudaFuncSetAttribute(kv4_attn_generic_kernel<kHeads>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10);
+  const auto kernel = kv4_attn_generic_kernel<kHeads, kThreads, kRows>;
+  const int slots = a.topk + a.swa, sums = kThreads / 32 * kHeads * 128;
+  const size_t smem = (size_t(kHeads) * 16 * kv4_groups(a.k_dim) + (kHeads * slots + 3) / 4 * 4 + sums + slots) * 4;
+  const cudaError_t e = once_per_device(kHeads == 1 ? kSetupKv4One : kThreads == 512 ? kSetupKv4Four : kSetupKv4Full, [] {
+    return cudaFuncSetAttribute(kv4_attn_generic_kernel<kHeads, kThreads, kRows>, cudaFuncAttributeMaxDynamicSharedMemorySize, 96 << 10);
   });
   if (e != cudaSuccess) return e;
   note_launch();
-  return launch_pdl(kv4_attn_generic_kernel<kHeads>, dim3(unsigned((a.heads + kHeads - 1) / kHeads), unsigned(batch)), dim3(kThreads),
-                    smem, st, 1, a);
+  return launch_pdl(kernel, dim3(unsigned((a.heads + kHeads - 1) / kHeads), unsigned(batch)), dim3(kThreads), smem, st, 1, a);
 }
 
 }  // namespace
@@ -236,7 +266,17 @@ cudaError_t launch_generic(const Kv4AttnArgs& a, int batch, cudaStream_t st) {
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, bool fast, int batch, cudaStream_t st) {
   if (batch == 0) return cudaSuccess;
   if (fast) return launch_kv4_attn_tc(a, batch, st);
-  return launch_generic<4>(a, batch, st);
+  // Few heads are spread over CTAs of one each; warps that share a query's rows hide their latency while every CTA has
+  // an SM to itself; otherwise more CTAs on an SM do.  Measured (562 keys, 192/128, bf16; 950, 100/72, fp32):
+  //   CTAs of                          1 head, 16 warps   4 heads, 16 warps   4 heads, 8 warps
+  //   160 heads (20 queries of 8)      34.8 us            39.9                49.6
+  //   320 heads (fp32)                 57.8               43.5                51.5
+  //   608 heads (76 queries of 8)      63.9               40.3                50.7
+  //   912 heads (fp32)                 102.7              79.9                72.4
+  const int sms = device_sm_count();
+  if (2 * batch * (long long)a.heads <= 3LL * sms) return launch_generic<1, 512, 1>(a, batch, st);
+  if ((a.heads + 3) / 4 * (long long)batch <= sms) return launch_generic<4, 512, 2>(a, batch, st);
+  return launch_generic<4, 256, 2>(a, batch, st);
 }
 
 }  // namespace csa2

@@ -492,7 +492,7 @@ def test_kv4_attention_fast_path(csa2, B, T, N, K, W, holes):
 
 @pytest.mark.parametrize("H,dk,dv,dtype", [(4, 16, 16, "f32"), (1, 1, 1, "f32"), (16, 64, 72, "bf16"), (40, 100, 33, "f32"), (9, 192, 128, "bf16"),
                                            (3, 1024, 1024, "bf16"), (64, 192, 128, "f32"), (5, 1024, 1024, "f32"), (6, 17, 130, "bf16"), (130, 48, 48, "bf16")])
-@pytest.mark.parametrize("B,T,N,K,W,holes", [(10, 5, 50, 33, 7, 2.0), (1, 1, 9, 3, 0, 0.0), (90, 1, 30, 5, 3, 1.0), (1, 1, 1500, 900, 124, 0.0)])
+@pytest.mark.parametrize("B,T,N,K,W,holes", [(10, 5, 50, 33, 7, 2.0), (1, 1, 9, 3, 0, 0.0), (90, 1, 30, 5, 3, 1.0), (1, 1, 1500, 900, 124, 0.0), (21, 1, 1100, 800, 37, 0.5)])
 def test_kv4_attention_any_shape(csa2, H, dk, dv, dtype, B, T, N, K, W, holes):
     sh = shape(B, tokens=T, n_entries=N, topk=K, swa=W, q_heads=H, k_dim=dk, v_dim=dv, dtype=dtype, k_exp=1, v_exp=-2, scale=0.07)
     d = attn_inputs(csa2, sh, H * 7 + T, holes)
@@ -502,7 +502,9 @@ def test_kv4_attention_any_shape(csa2, H, dk, dv, dtype, B, T, N, K, W, holes):
 
 # (shape arguments, queries) by kernel
 KINDS = {"few": (FAST, 3), "many": (FAST, 330), "generic": (dict(q_heads=5, k_dim=24, v_dim=40, dtype="f32"), 7),
-         "generic bf16": (dict(q_heads=20, k_dim=100, v_dim=72, dtype="bf16"), 7)}
+         "generic bf16": (dict(q_heads=20, k_dim=100, v_dim=72, dtype="bf16"), 7),
+         "generic of four heads": (dict(q_heads=10, k_dim=24, v_dim=40, dtype="f32"), 30),
+         "generic of many queries": (dict(q_heads=5, k_dim=24, v_dim=40, dtype="bf16"), 200)}
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
