@@ -13,18 +13,24 @@
 // cores nothing and halves the exponentials of a thread; the two halves have their own maxima and sums and
 // are added at the end, like the parts of a split.
 //
-// Roles of a CTA (17 warps):
+// Roles of a CTA (18 warps):
 //   4 softmax warps: a thread owns a row; P goes back to TMEM over its S.  O is rescaled only when a
 //     maximum grows by more than 2^8;
 //   4 end warps put the next query into TMEM (as bf16 and as fp16) and write the last one's O out;
-//   8 producer warps: each fetches 8 of a tile's packed entries (192 bytes, 12 pieces)
-//     several tiles ahead, and turns them into a stage's K and V rows (K-major, MN-major, 128-byte swizzled):
-//     lane l takes row l % 8 and the words l / 8, + 4, ... of 8 codes, which meets no bank twice;
-//   1 warp issues S = Q K^T and, a tile later, O += P V.
+//   8 producer warps in two groups that take turns at the tiles, 16 rows a warp: packed entries come by
+//     cp.async one turn ahead, their indices three, and become a stage's K and V rows (K-major, MN-major,
+//     128-byte swizzled): lane l takes row l % 8 and the words l / 8, + 4, ... of 8 codes, which meets no bank
+//     twice.  A window tile comes by TMA;
+//   1 warp issues S = Q K^T, up to three tiles ahead, and 1 warp O += P V.
 // Many queries: persistent, a CTA an SM.  Few: a query's tiles are split over a
 // cluster of up to 8 CTAs, whose partial O are merged through distributed shared memory as in attn.cu.
 //
 // P is rounded to fp16 (entries) or bf16 (window) as the tensor core asks for; the weights' sums stay fp32 and unrounded.
+//
+// Measured (512 entries and 128 window rows a query): 1 query 10.4 us, 64 12.7, 256 24.6, 1,024 in sequences of 32 64.5 (20.5 of
+// which their 139 MB would take, and 14 their products).  Neither bounds it (DRAM 25 %, tensor cores 30 %, issue slots 43 %): a
+// tile's way from S to P, 700 to 1,000 cycles one behind the other, and 2,000 to 4,000 between two queries do.  Two groups of
+// softmax warps, which hand a row's exponent on, took 73.8: 24 warps leave 80 registers a thread.
 #include <cuda.h>
 
 #include "kv4.cuh"
@@ -218,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++st == kStages) st = 0;
         const bool window = t >= range.window;
         const uint32_t s_addr = tmem + lanes + kSCol + buf * 64;
-        uint32_t p[32];                        // weights of the tile's 64 keys: those of the other half are 0
+        uint32_t p[16];                        // weights of this half's keys of the tile
         if (mask != 0) {
           const float sl2 = window ? window_scale : c.q_scale[items & 1][tid];
           uint32_t s[32];
@@ -285,17 +291,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 16; ++j) p[j] = 0;
         }
-        if (half == 0) {
+        uint32_t zeros[16];
 #pragma unroll
-          for (int j = 16; j < 32; ++j) p[j] = 0;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            p[16 + j] = p[j];
-            p[j] = 0;
-          }
-        }
-        tmem_st32(s_addr, p);
+        for (int j = 0; j < 16; ++j) zeros[j] = 0;
+        tmem_st16(s_addr + 16 * half, p);
+        tmem_st16(s_addr + 16 - 16 * half, zeros);
         tc_wait_st();
         tc_fence_before();
         warp_arrive(&c.p_full[buf]);
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto copy_q = [&](int item) {                             // into shared memory
       if (item < n_items) {
         const uint8_t* src = static_cast<const uint8_t*>(a.q) + (long long)item * (kH * kDk * 2);
-#pragma unroll
+#pragma unroll 4
         for (int x = 0; x < kH * kDk / 8 / 128; ++x) {
           const int i = row + 128 * x, r = i / (kDk / 8), p = i - r * (kDk / 8);
           cp16(smem_u32(c.q) + r * kQRow + p * 16, src + i * 16, nullptr);
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (wait && !wait_warp(c, &c.q_empty[i], phase, a.err)) return false;
       tc_fence_after();
       tmem_st16(to, r);
-#pragma unroll
+#pragma unroll 1
       for (int b = 1; b < 6; ++b) {
         words(b, i == 0, r);
         tmem_st16(to + 16 * b, r);
