@@ -43,13 +43,15 @@
  *     stream order.  If the kernel enqueued just before a call lets its
  *     dependents start early (griddepcontrol.launch_dependents), it must not
  *     write those inputs after doing so.  The library's own kernels never
- *     write them; csa2_kv_append and csa2_swa_append, which do, never start
- *     their dependents early.
+ *     write them; csa2_kv_append, csa2_swa_append, csa2_rope, csa2_norm_rope
+ *     and the calls on a packed cache (csa2_kv4_*), which do or may, never
+ *     start their dependents early.
  *   - `ws` is a caller-owned device workspace of at least
  *     csa2_workspace_bytes(shape) bytes, 256-byte aligned, zeroed once with
  *     csa2_workspace_init before first use.  Calls that share a workspace
  *     must be ordered on one stream.  The cache-maintenance calls
- *     (csa2_block_keys, csa2_kv_append, csa2_swa_append) use only the
+ *     (csa2_block_keys, csa2_kv_append, csa2_swa_append, csa2_kv4_append) and
+ *     csa2_kv4_rows use only the
  *     workspace's error word; they also accept ws = NULL with ws_bytes = 0,
  *     and then record device errors in the header of the library's static
  *     scratch array (see csa2_layer_group_static), where
@@ -564,7 +566,8 @@ typedef struct {
  *   pos [rows] int32   freqs [rot_dim / 2] double (device)
  * rows >= 1; 1 <= n_slots <= 16; mag finite and > 0; eps finite and >= 0;
  * rot_dim even, 0..1024; heads and dim up to 1024.  Rows that are not whole vectors of
- * 16 or 8 bytes (dims, turned range, strides and addresses) are taken number by number. */
+ * 16 or 8 bytes (dims, turned range, strides and addresses) are taken number by number.
+ * Tensors alike in type and in those share a launch. */
 int csa2_norm_rope(const csa2_norm_rope_slot* slots, int32_t n_slots, int32_t rows, int32_t rot_dim, int32_t interleaved,
                    int32_t center, const int32_t* pos, const double* freqs, float mag, float eps, csa2_stream_t stream);
 
@@ -603,9 +606,14 @@ int csa2_kv4_rows(const csa2_shape* shape, const void* kv4, const int32_t* idx, 
  *   out [B, H, dv] in the element type (as csa2_tree_attn's)
  *   lse [B, H] fp32 (nullable); out = 0 and -inf where nothing is attended,
  *   both NaN where a key that is attended scores NaN or +inf
- * batch <= 65,535; out and lse overlap nothing else (refused).  Weights are rounded to bf16
- * (half a step, 2^-8 of a weight) where they meet bf16 values on tensor cores; their sums
- * and lse are not. */
+ * batch <= 65,535; out and lse overlap nothing else (refused); n_swa is not read where W = 0.
+ * On tensor cores (csa2_fast_path's attention) weights are rounded where they meet values:
+ * an entry's to fp16, by 2^-12 of itself or 2^-32 of its head's greatest, a window row's to bf16, by
+ * 2^-9; their sums and lse are not.  Queries meet entries in fp16, scaled by a power of two a head: numbers
+ * 2^24 below their head's largest lose bits, those 2^34 below it all; products of windows take bf16
+ * as it is.  Window values are summed in units of 2^v_exp, and
+ * their magnitudes stay below 2^(100 + v_exp).  Dims that an attended value holds a NaN or an infinity in
+ * come out NaN or infinite, whatever its weight; what is not attended is never used. */
 int csa2_kv4_attn(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa,
                   const void* v_swa, const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp, void* ws,
                   size_t ws_bytes, csa2_stream_t stream);

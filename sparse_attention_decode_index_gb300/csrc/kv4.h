@@ -82,8 +82,8 @@ struct Kv4AttnArgs {
   int* err;
 };
 
-// bf16, 64 heads, dk 192, dv 128
-cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, int batch, cudaStream_t st);   // kv4_tc.cu
+// kv4_tc.cu: bf16, 64 heads, dk 192, dv 128, arrays at 16-byte addresses (`fast` of launch_kv4_attn).
+cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, int batch, cudaStream_t st);
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, bool fast, int batch, cudaStream_t st);
 
 }  // namespace csa2

@@ -68,10 +68,9 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
   float* sw = sq + kHeads * 16 * gk;                       // [kHeads][slots]
   float* part = sw + (kHeads * slots + 3) / 4 * 4;         // [kWarps][kHeads][128]
   int* row = reinterpret_cast<int*>(part + kWarps * kHeads * 128);   // [slots]: entry, window row, or -1
-  pdl_launch_dependents();
-  pdl_wait();
+  pdl_wait();   // no early trigger: the next launch may read, before its own wait, what the one before this one writes
   const uint8_t* cache = a.kv + (long long)(b / a.seq_div) * a.n_entries * bytes;
-  const int ns = clamp_count(a.n_swa[b], a.swa, blockIdx.x == 0 && tid == 0 ? a.err : nullptr);
+  const int ns = a.swa == 0 ? 0 : clamp_count(a.n_swa[b], a.swa, blockIdx.x == 0 && tid == 0 ? a.err : nullptr);
   for (int i = tid; i < kHeads * 16 * gk; i += kThreads) {
     const int h = i / (16 * gk), d = i - h * 16 * gk;
     sq[i] = h < nh && d < a.k_dim ? load_elem(a.q, ((long long)b * a.heads + h0 + h) * a.k_dim + d, a.dtype) : 0.f;

