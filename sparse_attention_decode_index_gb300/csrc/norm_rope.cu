@@ -15,7 +15,7 @@
 //
 // Measured: 8 rows 6.1 us; 8,192 rows of 64 + 1 heads of 192 in bf16 73.1 us, 5.6 TB/s (62 % of DRAM's cycles, issue
 // slots 64 %: the next load waits for the shuffles' turn); 4,097 rows of 16 heads of 128 in fp32, layer norm with gains of
-// each head, 22.3 us, 3.2 TB/s (issue slots 63 %, the gains' way through L1 48 %).  Four blocks an SM leave too few registers (124 us),
+// each head, 21.9 us, 3.3 TB/s (issue slots 63 %).  Four blocks an SM leave too few registers (124 us),
 // four vectors a lane for fp32 too few lanes (30 us).
 #include "common.cuh"
 #include "kv4.h"
@@ -100,6 +100,7 @@ CSA2_DEV void norm_vectors(const NormRopeArgs& a, const NormRopeArgs::Slot& y, c
       if (gain != nullptr && l + m * lanes < n_vecs) load_gain<kV>(gain + (l + m * lanes) * kV, g[m]);
     }
   };
+  int have = -1;                                   // whose gains these are, where heads have their own
   if (!each) load_gains(y.gain);
   auto address = [&](int i, long long stride) -> long long {   // of head i of the part, in bytes
     int row, head;
@@ -166,7 +167,10 @@ CSA2_DEV void norm_vectors(const NormRopeArgs& a, const NormRopeArgs::Slot& y, c
     int row = 0, head = 0;
     if (on) part.at(i, row, head);
     const float* gain = y.gain == nullptr || !each ? y.gain : y.gain + (long long)head * y.dim;
-    if (each) load_gains(gain);
+    if (each && head != have) {                    // (a group meets the same heads in turn: one, where step is a multiple of them)
+      load_gains(gain);
+      have = head;
+    }
 #pragma unroll
     for (int m = 0; m < kNv; ++m)
 #pragma unroll
