@@ -758,3 +758,89 @@ def test_calls_on_two_streams_at_once(csa2):
     for d, (out, lse), ws in zip(sets, want, works):
         assert torch.equal(d.out, out) and torch.equal(d.lse, lse)
         assert_no_device_error(csa2, ws)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("ke,ve,near", [(64, -64, False), (-64, 64, False), (-64, -64, True), (64, 64, True)])
+def test_kv4_attention_at_the_exponents_ends(csa2, kind, ke, ve, near):
+    """Keys and values of 2^-64 to 2^64; `near`: window values about 1, far from what the entries' are."""
+    kw, n = KINDS[kind]
+    sh = shape(n, n_entries=70, topk=48, swa=20, k_exp=ke, v_exp=ve, scale=0.1, **kw)
+    d = attn_inputs(csa2, sh, 77, 1.0)
+    if near:
+        d.v_swa.copy_(d.v_swa * 2.0 ** -ve)
+    assert_no_device_error(csa2, run_attn(csa2, sh, d))
+    check_attn(sh, d)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_kv4_attention_captured(csa2, kind):
+    """A captured call reads what its arrays hold when it is replayed; two graphs share a workspace."""
+    kw, n = KINDS[kind]
+    sh = shape(n, n_entries=90, topk=70, swa=30, k_exp=-2, v_exp=0, **kw)
+    sets = [attn_inputs(csa2, sh, seed, 1.0) for seed in (5, 6)]
+    ws, want = csa2.workspace(sh), []
+    for d in sets:
+        run_attn(csa2, sh, d, ws)
+        want.append((d.out.clone(), d.lse.clone()))
+    graphs = []
+    for d in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run_attn(csa2, sh, d, ws)
+        graphs.append(graph)
+    for turn in range(3):
+        for d, graph, (out, lse) in zip(sets, graphs, want):
+            d.out.fill_(9.0)
+            d.lse.fill_(9.0)
+            graph.replay()
+            assert torch.equal(d.out, out) and torch.equal(d.lse, lse), turn
+        for name in ("q", "kv", "idx", "k_swa", "v_swa", "n_swa"):   # each graph with the other's inputs
+            a, b = (getattr(d, name) for d in sets)
+            keep = a.clone()
+            a.copy_(b)
+            b.copy_(keep)
+        want.reverse()
+    assert_no_device_error(csa2, ws)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_kv4_attention_without_windows_takes_no_counts(csa2, kind):
+    kw, n = KINDS[kind]
+    sh = shape(n, n_entries=50, topk=30, swa=0, k_exp=0, v_exp=0, **kw)
+    d = attn_inputs(csa2, sh, 9, 0.0, fill=0)
+    run_attn(csa2, sh, d)
+    out, lse = d.out.clone(), d.lse.clone()
+    d.n_swa.fill_(77)
+    assert_no_device_error(csa2, run_attn(csa2, sh, d))
+    assert torch.equal(d.out, out) and torch.equal(d.lse, lse)
+    check_attn(sh, types.SimpleNamespace(**{**vars(d), "n_swa": torch.zeros_like(d.n_swa)}))
+
+
+def test_norm_rope_before_an_attention_that_reads_early(csa2):
+    """Queries and windows that csa2_norm_rope writes, straight into csa2_sparse_attn, which looks at them before its turn; and
+    rows that csa2_kv4_rows writes as its main cache."""
+    B, N, K, W = 40, 300, 256, 64
+    sh = shape(B, n_entries=N, topk=K, swa=W, k_exp=0, v_exp=0, **FAST)
+    d = attn_inputs(csa2, sh, 3, 0.0)
+    wide = shape(B, n_entries=K, topk=K, swa=W, **FAST)
+    ws = csa2.workspace(wide)
+    rows_k = torch.empty(B, K, 192, dtype=d.dt, device="cuda")
+    rows_v = torch.empty(B, K, 128, dtype=d.dt, device="cuda")
+    own = torch.arange(K, dtype=torch.int32, device="cuda").repeat(B, 1)
+    q = torch.empty_like(d.q)
+    out, lse = torch.empty(B, 64, 128, device="cuda"), torch.empty(B, 64, device="cuda")
+    got = []
+    for wait in (True, False, False, False):
+        for t in (q, rows_k, rows_v):
+            t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        csa2.kv4_rows(sh, d.kv, d.idx, rows_k, rows_v, None)
+        csa2.norm_rope([(d.q, q, None, 0)])
+        if wait:
+            torch.cuda.synchronize()
+        csa2.sparse_attn(wide, q, rows_k, rows_v, own, d.k_swa, d.v_swa, d.n_swa, out, ws, lse=lse)
+        got.append((out.clone(), lse.clone()))
+    for o, l in got[1:]:
+        assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
+    assert torch.isfinite(got[0][0]).all()
