@@ -607,10 +607,10 @@ int csa2_kv4_rows(const csa2_shape* shape, const void* kv4, const int32_t* idx, 
  *   lse [B, H] fp32 (nullable); out = 0 and -inf where nothing is attended,
  *   both NaN where a key that is attended scores NaN or +inf
  * batch <= 65,535; out and lse overlap nothing else (refused); n_swa is not read where W = 0.
- * On tensor cores (csa2_fast_path's attention) weights are rounded where they meet values:
- * an entry's to fp16, by 2^-12 of itself or 2^-32 of its head's greatest, a window row's to bf16, by
- * 2^-9; their sums and lse are not.  Queries meet entries in fp16, scaled by a power of two a head: numbers
- * 2^24 below their head's largest lose bits, those 2^34 below it all; products of windows take bf16
+ * bf16 weights are rounded where they meet values on tensor cores (their sums and lse are not): by 2^-9 of themselves to
+ * bf16, or, those of entries where csa2_fast_path says that the fast kernels serve the attention, to fp16,
+ * by 2^-12 of themselves or 2^-32 of their head's greatest.  There queries meet entries in fp16, scaled by a
+ * power of two a head: numbers 2^24 below their head's largest lose bits, those 2^34 below it all; products of windows take bf16
  * as it is.  Window values are summed in units of 2^v_exp, and
  * their magnitudes stay below 2^(100 + v_exp).  Dims that an attended value holds a NaN or an infinity in
  * come out NaN or infinite, whatever its weight; what is not attended is never used. */

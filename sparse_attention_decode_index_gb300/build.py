@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcsa2.so")
 SOURCES = ["api.cu", "indexer.cu", "topk.cu", "attn.cu", "fused.cu", "static_ws.cu", "append.cu", "shard.cu",
-           "rope.cu", "norm_rope.cu", "kv4_cache.cu", "kv4_attn.cu", "kv4_tc.cu", "tree.cu", "tree_tc.cu", "tree_mma.cu", "weights_tc.cu", "commit.cu", "evict.cu"]
+           "rope.cu", "norm_rope.cu", "kv4_cache.cu", "kv4_attn.cu", "kv4_mma.cu", "kv4_tc.cu", "tree.cu", "tree_tc.cu", "tree_mma.cu", "weights_tc.cu", "commit.cu", "evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

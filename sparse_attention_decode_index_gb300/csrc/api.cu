@@ -1243,7 +1243,7 @@ int csa2_kv4_attn(const csa2_shape* shape, const void* q, const void* kv4, const
   a.scale = softmax_scale(s);
   a.k_up = std::ldexp(1.f, k_exp);
   a.v_up = std::ldexp(1.f, v_exp);
-  a.wide = s.k_dim % 16 == 0 && s.v_dim % 16 == 0 && aligned16(k_swa) && aligned16(v_swa);
+  a.wide = s.dtype == CSA2_F32 && s.k_dim % 16 == 0 && s.v_dim % 16 == 0 && aligned16(k_swa) && aligned16(v_swa);
   a.err = static_cast<int*>(ws);
   return cuda_status(launch_kv4_attn(a, fast, s.batch, stream));
 }

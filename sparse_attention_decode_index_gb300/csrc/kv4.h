@@ -6,7 +6,7 @@
 namespace csa2 {
 
 // Keys of once_per_device, behind DraftSetupKey's.
-enum Kv4SetupKey { kSetupKv4Tc = 32, kSetupKv4One, kSetupKv4Four, kSetupKv4Full };
+enum Kv4SetupKey { kSetupKv4Tc = 32, kSetupKv4One, kSetupKv4Four, kSetupKv4Full, kSetupKv4Mma8, kSetupKv4Mma16 };
 
 // Norm of heads with rotary positions (norm_rope.cu).
 struct NormRopeArgs {
@@ -78,12 +78,15 @@ struct Kv4AttnArgs {
   int seq_div, n_entries, topk, swa, heads, k_dim, v_dim, dtype;
   float scale;               // softmax scale (natural-log domain)
   float k_up, v_up;          // 2^k_exp, 2^v_exp
-  int wide;                  // window rows of 16 dims at 16-byte addresses
+  int wide;                  // fp32 window rows of 16 dims at 16-byte addresses (kv4_attn.cu)
   int* err;
 };
 
 // kv4_tc.cu: bf16, 64 heads, dk 192, dv 128, arrays at 16-byte addresses (`fast` of launch_kv4_attn).
 cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, int batch, cudaStream_t st);
+// kv4_mma.cu: other bf16 shapes.
+bool kv4_mma_fits(const Kv4AttnArgs& a);
+cudaError_t launch_kv4_attn_mma(const Kv4AttnArgs& a, int batch, cudaStream_t st);
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, bool fast, int batch, cudaStream_t st);
 
 }  // namespace csa2

@@ -4,7 +4,8 @@
 // are taken out of the rows: a main key's product is multiplied by 2^k_exp with
 // the softmax scale, a main value's weight by 2^v_exp.
 //
-// Any head count, dims and element type, in fp32: a CTA takes one head or four of a
+// Any head count, dims and element type, in fp32 (fp32 queries and windows, and bf16 ones that kv4_mma.cu does not take:
+// odd dims or addresses): a CTA takes one head or four of a
 // query.  Eight lanes go through a row together, a group of 16 dims each, so that a warp has
 // four rows on their way, or eight (fp32, 228 CTAs: 103 -> 72 us); a lane multiplies its numbers with every head of the CTA.  Scores stay in
 // shared memory; every warp sums the values of its own rows, and the warps' sums are added in order.
@@ -16,24 +17,12 @@ namespace {
 
 // 16 numbers of dims d .. d + 15 (of dim), zeros behind: of a window row, or of a group's codes.
 CSA2_DEV void window16(const void* rows, long long row, int d, int dim, int dtype, bool wide, float (&x)[16]) {
-  if (wide && dtype == 1) {
+  if (wide) {                                  // (fp32)
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(rows) + row * dim + d);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float4 v = p[i];
       x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-  } else if (wide) {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(rows) + row * dim + d);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = p[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[8 * i + 2 * e] = __uint_as_float(w[e] << 16);
-        x[8 * i + 2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-      }
     }
   } else {
 #pragma unroll
@@ -265,15 +254,16 @@ cudaError_t launch_generic(const Kv4AttnArgs& a, int batch, cudaStream_t st) {
 cudaError_t launch_kv4_attn(const Kv4AttnArgs& a, bool fast, int batch, cudaStream_t st) {
   if (batch == 0) return cudaSuccess;
   if (fast) return launch_kv4_attn_tc(a, batch, st);
+  if (kv4_mma_fits(a)) return launch_kv4_attn_mma(a, batch, st);
   // Few heads are spread over CTAs of one each; warps that share a query's rows hide their latency while every CTA has
-  // an SM to itself; otherwise more CTAs on an SM do.  Measured (562 keys, 192/128, bf16; 950, 100/72, fp32):
-  //   CTAs of                          1 head, 16 warps   4 heads, 16 warps   4 heads, 8 warps
-  //   160 heads (20 queries of 8)      34.8 us            39.9                49.6
-  //   320 heads (fp32)                 57.8               43.5                51.5
-  //   608 heads (76 queries of 8)      63.9               40.3                50.7
-  //   912 heads (fp32)                 102.7              79.9                72.4
+  // an SM to itself; otherwise more CTAs on an SM do.  Measured (queries of 8 heads, 562 keys, 192 / 128, fp32):
+  //   CTAs of        1 head, 16 warps   4 heads, 16 warps   4 heads, 8 warps
+  //   8 heads        22.5 us            34.7                38.8
+  //   304 heads      32.7               34.7                38.9
+  //   608 heads      57.3               34.7                38.9
+  //   912 heads      83.9               63.4                55.3
   const int sms = device_sm_count();
-  if (2 * batch * (long long)a.heads <= 3LL * sms) return launch_generic<1, 512, 1>(a, batch, st);
+  if (batch * (long long)a.heads <= 2LL * sms) return launch_generic<1, 512, 1>(a, batch, st);
   if ((a.heads + 3) / 4 * (long long)batch <= sms) return launch_generic<4, 512, 2>(a, batch, st);
   return launch_generic<4, 256, 2>(a, batch, st);
 }

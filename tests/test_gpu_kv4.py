@@ -504,7 +504,9 @@ def test_kv4_attention_any_shape(csa2, H, dk, dv, dtype, B, T, N, K, W, holes):
 KINDS = {"few": (FAST, 3), "many": (FAST, 330), "generic": (dict(q_heads=5, k_dim=24, v_dim=40, dtype="f32"), 7),
          "generic bf16": (dict(q_heads=20, k_dim=100, v_dim=72, dtype="bf16"), 7),
          "generic of four heads": (dict(q_heads=10, k_dim=24, v_dim=40, dtype="f32"), 30),
-         "generic of many queries": (dict(q_heads=5, k_dim=24, v_dim=40, dtype="bf16"), 200)}
+         "generic of many queries": (dict(q_heads=5, k_dim=24, v_dim=40, dtype="bf16"), 200),
+         "fp32 of many queries": (dict(q_heads=5, k_dim=24, v_dim=48, dtype="f32"), 200),
+         "odd bf16": (dict(q_heads=5, k_dim=25, v_dim=42, dtype="bf16"), 9)}
 
 
 @pytest.mark.parametrize("kind", list(KINDS))
@@ -844,3 +846,18 @@ def test_norm_rope_before_an_attention_that_reads_early(csa2):
     for o, l in got[1:]:
         assert torch.equal(o, got[0][0]) and torch.equal(l, got[0][1])
     assert torch.isfinite(got[0][0]).all()
+
+
+@pytest.mark.parametrize("shift", [1, 2, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_kv4_attention_of_windows_at_odd_addresses(csa2, dtype, shift):
+    """Windows (and queries) that begin `shift` elements behind a 16-byte address."""
+    sh = shape(20, n_entries=60, topk=40, swa=33, k_exp=-1, v_exp=1, q_heads=18, k_dim=80, v_dim=48, dtype=dtype)
+    d = attn_inputs(csa2, sh, shift, 1.0)
+    for name in ("q", "k_swa", "v_swa"):
+        x = getattr(d, name)
+        moved = torch.empty(x.numel() + shift, dtype=x.dtype, device="cuda")[shift:].view(x.shape)
+        moved.copy_(x)
+        setattr(d, name, moved)
+    assert_no_device_error(csa2, run_attn(csa2, sh, d))
+    check_attn(sh, d)
