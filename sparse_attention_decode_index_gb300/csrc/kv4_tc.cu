@@ -28,7 +28,7 @@
 // P is rounded to fp16 (entries) or bf16 (window) as the tensor core asks for; the weights' sums stay fp32 and unrounded.
 //
 // Measured (512 entries and 128 window rows a query): 1 query 10.4 us, 64 12.7, 256 24.6, 1,024 in sequences of 32 64.5 (20.5 of
-// which their 139 MB would take, and 14 their products).  Neither bounds it (DRAM 25 %, tensor cores 30 %, issue slots 43 %): a
+// which their 139 MB would take, and 14 their products).  Neither bounds it (DRAM 27 %, tensor cores 33 %, issue slots 45 %): a
 // tile's way from S to P, 700 to 1,000 cycles one behind the other, and 2,000 to 4,000 between two queries do.  Two groups of
 // softmax warps, which hand a row's exponent on, took 73.8: 24 warps leave 80 registers a thread.
 #include <cuda.h>
