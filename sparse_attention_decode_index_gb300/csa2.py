@@ -619,10 +619,10 @@ def _head_rows(t, name: str, dtype, size, device):
         raise ValueError(f"{name} must be a CUDA tensor on {device} (it is on {t.device})")
     if t.dtype != dtype or tuple(t.shape) != tuple(size):
         raise ValueError(f"{name} must be {dtype} {tuple(size)}, got {t.dtype} {tuple(t.shape)}")
-    width = t[0].numel() if t.shape[0] else 0
-    if t.shape[0] and not t[0].is_contiguous():
+    heads, dim, stride = (int(size[1]) if len(size) == 3 else 1), int(size[-1]), t.stride()   # (no views: they cost 2 us each)
+    if (dim > 1 and stride[-1] != 1) or (heads > 1 and stride[1] != dim):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return t.data_ptr(), int(t.stride(0)) if t.shape[0] > 1 else width
+    return t.data_ptr(), int(stride[0]) if t.shape[0] > 1 else heads * dim
 
 
 class NormRopeCall(_Call):

@@ -42,7 +42,7 @@ struct Raw {
 // entry; its members come from the cache in front of the new entries and from the new ones, never from what
 // another CTA writes.
 //
-// Measured: one entry of each of 64 sequences and its row back 17 to 19 us (two launches' latencies); 8,191 entries of each of
+// Measured: one entry of each of 64 sequences 4.6 us, their rows back 1.6 (latency); 8,191 entries of each of
 // 16 sequences 34 us and 4 for the counts, where their 142 MB would take 21: the issue slots (64 %) bound it, most of them
 // conversions.
 template <bool kF32>

@@ -10,12 +10,12 @@
 // share their angles, as in rope.cu.  A head belongs to a group of 1 to 32 lanes
 // that hold up to 4 vectors of it each (192 bf16 dims: 8 lanes with 3 vectors of
 // 16 bytes), chosen so that few lanes are left over; its sums go through log2(lanes)
-// shuffles.  The next head is on its way while one is turned, and gains that the heads
-// share stay in registers.
+// shuffles.  The next head is on its way while one is turned, the first while the angles are made (8 rows 6.1 -> 6.0 us),
+// and gains stay in registers while the head does.
 //
-// Measured: 8 rows 6.1 us; 8,192 rows of 64 + 1 heads of 192 in bf16 73.1 us, 5.6 TB/s (62 % of DRAM's cycles, issue
+// Measured: 8 rows 6.0 us; 8,192 rows of 64 + 1 heads of 192 in bf16 72.6 us, 5.6 TB/s (62 % of DRAM's cycles, issue
 // slots 64 %: the next load waits for the shuffles' turn); 4,097 rows of 16 heads of 128 in fp32, layer norm with gains of
-// each head, 21.9 us, 3.3 TB/s (issue slots 63 %).  Four blocks an SM leave too few registers (124 us),
+// each head, 21.8 us, 3.3 TB/s (issue slots 63 %).  Four blocks an SM leave too few registers (124 us),
 // four vectors a lane for fp32 too few lanes (30 us).
 #include "common.cuh"
 #include "kv4.h"
@@ -82,8 +82,8 @@ struct Part {
 // `hv / lanes` vectors further, in lane l ^ hv, or anywhere (it is loaded a second time).
 enum Partner { kNoPartner, kSameLane, kOtherLane, kLoaded };
 
-template <bool kBf16, int kBytes, int kNv, int kPartner>
-CSA2_DEV void norm_vectors(const NormRopeArgs& a, const NormRopeArgs::Slot& y, const Part& part, const float2* cs) {
+template <bool kBf16, int kBytes, int kNv, int kPartner, class F>
+CSA2_DEV void norm_vectors(const NormRopeArgs& a, const NormRopeArgs::Slot& y, const Part& part, const float2* cs, F meanwhile) {
   constexpr int kE = kBf16 ? 2 : 4, kV = kBytes / kE;
   const int lanes = y.lanes, l = threadIdx.x & (lanes - 1), n_vecs = y.dim / kV;
   const int half = a.rot / 2, v0 = y.off / kV, rv = a.rot / kV, hv = rv / 2;
@@ -123,6 +123,7 @@ CSA2_DEV void norm_vectors(const NormRopeArgs& a, const NormRopeArgs::Slot& y, c
   };
   const int first = int(threadIdx.x) / lanes;
   fetch(first);
+  meanwhile();                                     // what the first head's way leaves time for
   for (int i0 = 0; i0 < total; i0 += step) {       // (uniform: the shuffles need whole warps)
     const int i = i0 + first;
     const bool on = i < total;
@@ -296,8 +297,11 @@ __global__ void __launch_bounds__(kThreads, kNv == 4 ? 2 : kPerSm) norm_rope_ker
   const long long row0 = (long long)blockIdx.x * a.per_block;
   const int nr = int(min((long long)a.per_block, a.rows - row0));
   pdl_wait();   // no early trigger: the attention may read what this kernel writes before its own wait
-  if (a.rot > 0) rope_angles(cs, step, row0, nr, a.rot / 2, a.pos, a.freqs, a.mag, false);
-  __syncthreads();
+  auto angles = [&] {
+    if (a.rot > 0) rope_angles(cs, step, row0, nr, a.rot / 2, a.pos, a.freqs, a.mag, false);
+    __syncthreads();
+  };
+  if constexpr (kBytes == 0) angles();
   for (int k = 0; k < a.n_slots; ++k) {
     const NormRopeArgs::Slot& y = a.slot[k];
     const Part part(y, row0, nr);
@@ -305,7 +309,9 @@ __global__ void __launch_bounds__(kThreads, kNv == 4 ? 2 : kPerSm) norm_rope_ker
       if (kBf16) norm_scalar<__nv_bfloat16>(a, y, part, cs);
       else norm_scalar<float>(a, y, part, cs);
     } else {
-      norm_vectors<kBf16, kBytes, kNv, kPartner>(a, y, part, cs);
+      norm_vectors<kBf16, kBytes, kNv, kPartner>(a, y, part, cs, [&] {
+        if (k == 0) angles();
+      });
     }
   }
 }

@@ -861,3 +861,19 @@ def test_kv4_attention_of_windows_at_odd_addresses(csa2, dtype, shift):
         setattr(d, name, moved)
     assert_no_device_error(csa2, run_attn(csa2, sh, d))
     check_attn(sh, d)
+
+
+def test_norm_rope_of_strided_views(csa2):
+    """Heads that do not lie side by side are refused, rows that lie apart are not; sizes of one may have any stride."""
+    x = torch.randn((4, 6, 16), device="cuda")
+    for view in (x[:, ::2], x[..., ::2], x[:, :, :1], x.transpose(0, 1)[:, :3], x[:, :1].expand(4, 6, 16), x[..., :1].expand(4, 6, 16)):
+        with pytest.raises(ValueError):
+            csa2.norm_rope([(view, torch.empty(view.shape, device="cuda"), None, 0)])
+    with pytest.raises(csa2.CSA2Error):                       # one row for all
+        csa2.norm_rope([(x[:1].expand(4, 6, 16), torch.empty_like(x), None, 0)])
+    for view in (x[::2], x[:, 2:4], x[1:2], x[:, 3], x[:, :1], x[..., 3:4][:, 2:3], x[:1].expand(1, 6, 16)):
+        out = torch.empty(view.shape, device="cuda")
+        csa2.norm_rope([(view, out, None, 0)], eps=0.0)
+        want = view.double() / view.double().square().mean(-1, keepdim=True).sqrt()
+        # 16 squares, their sum, the mean, a root and two products in fp32: 24 half steps of a value
+        assert ((out.double() - want).abs() <= 24 * 2.0 ** -24 * want.abs() + 1e-30).all()
