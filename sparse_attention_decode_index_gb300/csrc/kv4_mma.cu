@@ -1,6 +1,7 @@
 // Sparse attention over a packed main cache for bf16 shapes outside the fast path whose
 // window rows are whole 8-byte pieces: products on mma.sync, operands straight from the
-// gathered entries.  One CTA per (query, 16 heads).
+// gathered entries.  One CTA per (query, 16 heads), or a cluster of up to 8 that share its slots and join their sums through
+// distributed shared memory.
 //   S = Q K^T   a warp takes 16 slots at a time.  mma's B operand wants pairs of k of one key
 //     per lane; a sum has no order, so lane t of a quad takes group 4 s + t of its key, 16 codes in one
 //     8-byte load and their scale, for four products, and Q is read in the same order.  Code * scale is exact in bf16.
@@ -10,8 +11,8 @@
 //     P is rounded to bf16 (half a step, 2^-9 of a weight; its sum is not rounded), which a factor of 2^v_exp for
 //     entries does not change.  The warps' sums are added up in their order.
 // Bound by latency, two round trips to memory per 16 slots of a warp, and the conversions: 90 queries, 40 heads of 192 / 128,
-// 640 slots 32.7 us (fp32 products in kv4_attn.cu: 168), 20 queries of 16 heads 22.4 (36.8), 1 query of 4 heads of 64 / 64
-// 17 (17).  Three CTAs an SM leave 80 registers a thread, which spills (51.1).
+// 640 slots 32.7 us (fp32 products in kv4_attn.cu: 168), 20 queries of 16 heads 13.6 (without clusters 18.8), 1 query of 4 heads of
+// 64 / 64 7.9 (10.6).  Three CTAs an SM leave 80 registers a thread, which spills (51.1).
 #include "kv4.cuh"
 
 namespace csa2 {
@@ -23,6 +24,7 @@ constexpr int kSpan = 64;           // dims of a step of scores: a group for eac
 constexpr int kPassDims = 64;       // dims of a P V pass
 constexpr int kPassPitch = kPassDims + 4;
 constexpr int kMaxSlots = 1024;     // topk + swa
+constexpr int kMaxCluster = 8;
 
 // Bytes of a staged Q row: 8 past a multiple of 128, so that the pieces that half a warp reads, 8 bytes of four rows and four
 // groups, fall into distinct banks.
@@ -76,19 +78,23 @@ struct RawDims {
 };
 
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_kernel(const Kv4AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_kernel(const Kv4AttnArgs a, int ncta) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ float inv_s[kTileHeads];
-  const int b = blockIdx.y, h0 = blockIdx.x * kTileHeads, nh = min(kTileHeads, a.heads - h0);
+  __shared__ float2 total[kTileHeads];         // of a split: the greatest logit and the sum of this CTA's slots
+  const int crank = ncta > 1 ? int(cluster_rank()) : 0, tile = int(blockIdx.x) / ncta;
+  const int b = blockIdx.y, h0 = tile * kTileHeads, nh = min(kTileHeads, a.heads - h0);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int gk = kv4_groups(a.k_dim), gv = kv4_groups(a.v_dim), groups = gk + gv, bytes = kv4_bytes(a.k_dim, a.v_dim);
   const int nslots = a.topk + a.swa, rounded = (nslots + kTileSlots - 1) / kTileSlots * kTileSlots;
   const int ld = p_stride(nslots), stride = q_stride(a.k_dim), spans = (a.k_dim + kSpan - 1) / kSpan;
+  const int lo = rounded / kTileSlots * crank / ncta * kTileSlots, hi = rounded / kTileSlots * (crank + 1) / ncta * kTileSlots;   // this CTA's slots
   int* row = reinterpret_cast<int*>(sm);                          // [rounded] entry or window row, or -1
   float* sp = reinterpret_cast<float*>(row + rounded);            // [kTileHeads][ld] logits -> weights
   uint8_t* sq = reinterpret_cast<uint8_t*>(sp + kTileHeads * ld); // [kTileHeads][q_stride]
   float* part = reinterpret_cast<float*>(sq);                     // later: [kWarps][kTileHeads][kPassPitch]
+  float* mine = part + max(kTileHeads * stride / 4, kWarps * kTileHeads * kPassPitch);   // of a split: [kTileHeads][v_dim]
   pdl_wait();   // no early trigger: the next launch may read, before its own wait, what the one before this one writes
   for (int i = tid; i < kTileHeads * spans * kSpan; i += kThreads) {
     const int h = i / (spans * kSpan), d = i - h * (spans * kSpan);
@@ -96,13 +102,13 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_ker
     reinterpret_cast<__nv_bfloat16*>(sq + h * stride)[d] =
         in ? static_cast<const __nv_bfloat16*>(a.q)[((long long)b * a.heads + h0 + h) * a.k_dim + d] : __nv_bfloat16(0.f);
   }
-  const int ns = a.swa == 0 ? 0 : clamp_count(a.n_swa[b], a.swa, blockIdx.x == 0 && tid == 0 ? a.err : nullptr);
-  for (int j = tid; j < rounded; j += kThreads) {
+  const int ns = a.swa == 0 ? 0 : clamp_count(a.n_swa[b], a.swa, tile == 0 && crank == 0 && tid == 0 ? a.err : nullptr);
+  for (int j = lo + tid; j < hi; j += kThreads) {
     int e = -1;
     if (j < a.topk) {
       e = a.idx[(long long)b * a.topk + j];
       if (e >= a.n_entries) {
-        if (blockIdx.x == 0) report(a.err, kErrBadIndex, e);
+        if (tile == 0) report(a.err, kErrBadIndex, e);
         e = -1;
       }
     } else if (j - a.topk < ns) {
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_ker
   const __nv_bfloat16* k_swa = static_cast<const __nv_bfloat16*>(a.k_swa) + (long long)b * a.swa * a.k_dim;
   const __nv_bfloat16* v_swa = static_cast<const __nv_bfloat16*>(a.v_swa) + (long long)b * a.swa * a.v_dim;
   // ---- scores
-  for (int j = kTileSlots * warp; j < rounded; j += kTileSlots * kWarps) {
+  for (int j = lo + kTileSlots * warp; j < hi; j += kTileSlots * kWarps) {
     constexpr int kBatch = 2;                  // steps whose loads are on their way together
     int e[2];
     float c[2][4];
@@ -173,11 +179,11 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_ker
   for (int h = warp; h < kTileHeads; h += kWarps) {
     float* p = sp + h * ld;
     float m = -INFINITY, l = 0.f;
-    for (int j = lane; j < rounded; j += 32) m = fmaxf(m, p[j]);
+    for (int j = lo + lane; j < hi; j += 32) m = fmaxf(m, p[j]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == -INFINITY ? 0.f : m;
-    for (int j = lane; j < rounded; j += 32) {
+    for (int j = lo + lane; j < hi; j += 32) {
       const float w = expf(p[j] - base);       // (NaN of a NaN or an infinite logit, as the sum then is)
       p[j] = j < a.topk ? w * a.v_up : w;
       l += w;
@@ -185,8 +191,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_ker
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      inv_s[h] = l > 0.f ? 1.f / l : l;        // no key: 0; NaN stays NaN
-      if (h < nh && a.lse != nullptr) a.lse[(long long)b * a.heads + h0 + h] = l == 0.f ? -INFINITY : base + logf(l);
+      inv_s[h] = ncta > 1 ? 1.f : l > 0.f ? 1.f / l : l;   // no key: 0; NaN stays NaN
+      total[h] = make_float2(m, l);
+      if (ncta == 1 && h < nh && a.lse != nullptr) a.lse[(long long)b * a.heads + h0 + h] = l == 0.f ? -INFINITY : base + logf(l);
     }
   }
   __syncthreads();
@@ -197,14 +204,14 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_ker
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc[i >> 2][i & 3] = 0.f;
     const int group = (d0 >> 4) + (g >> 1);
-    for (int j0 = kTileSlots * warp; j0 < rounded; j0 += kBatch * kTileSlots * kWarps) {
+    for (int j0 = lo + kTileSlots * warp; j0 < hi; j0 += kBatch * kTileSlots * kWarps) {
       RawDims<4> v[kBatch][4];
 #pragma unroll
       for (int y = 0; y < kBatch; ++y)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = j0 + y * kTileSlots * kWarps + 2 * t + (r & 1) + 4 * (r & 2);
-          const int e = j < rounded && group < gv ? row[j] : -1;
+          const int e = j < hi && group < gv ? row[j] : -1;
           if (e < 0) {
             v[y][r].none();
           } else if (j < a.topk) {
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_ker
 #pragma unroll
       for (int y = 0; y < kBatch; ++y) {
         const int j = j0 + y * kTileSlots * kWarps;
-        if (j >= rounded) break;
+        if (j >= hi) break;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (j + 2 * t + (r & 1) + 4 * (r & 2) < a.topk) v[y][r].unpack();
@@ -251,27 +258,63 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 2 : 1) kv4_mma_ker
       float o = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) o += part[(w * kTileHeads + h) * kPassPitch + x];
-      store_elem(a.out, ((long long)b * a.heads + h0 + h) * a.v_dim + d0 + x, 0, o * inv_s[h]);
+      if (ncta > 1) mine[h * a.v_dim + d0 + x] = o;
+      else store_elem(a.out, ((long long)b * a.heads + h0 + h) * a.v_dim + d0 + x, 0, o * inv_s[h]);
     }
     __syncthreads();
   }
+  if (ncta == 1) return;
+  // ---- a split's parts, a share of the heads a CTA
+  cluster_sync_all();
+  const int per = kTileHeads / ncta, pieces = a.v_dim / 4;
+  for (int i = tid; i < per * pieces; i += kThreads) {
+    const int h = crank * per + i / pieces, d = i % pieces * 4;
+    if (h >= nh) break;
+    float top = -INFINITY, sum = 0.f;
+    float2 y[kMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < ncta) {
+        y[c] = make_float2(dsmem_ld_f32(dsmem_addr(&total[h].x, uint32_t(c))), dsmem_ld_f32(dsmem_addr(&total[h].y, uint32_t(c))));
+        top = fmaxf(top, y[c].x);
+      }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < kMaxCluster; ++c)
+      if (c < ncta) {
+        const float w = y[c].x == -INFINITY ? 0.f : expf(y[c].x - top);   // (a NaN sum stays)
+        const float4 z = dsmem_ld_v4f(dsmem_addr(mine + h * a.v_dim + d, uint32_t(c)));
+        sum += w * y[c].y;
+        o = make_float4(__fmaf_rn(w, z.x, o.x), __fmaf_rn(w, z.y, o.y), __fmaf_rn(w, z.z, o.z), __fmaf_rn(w, z.w, o.w));
+      }
+    const float inv = sum > 0.f ? 1.f / sum : sum;
+    const long long at = (long long)b * a.heads + h0 + h;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + at * a.v_dim + d;   // (of any address)
+    out[0] = __float2bfloat16_rn(o.x * inv);
+    out[1] = __float2bfloat16_rn(o.y * inv);
+    out[2] = __float2bfloat16_rn(o.z * inv);
+    out[3] = __float2bfloat16_rn(o.w * inv);
+    if (d == 0 && a.lse != nullptr) a.lse[at] = sum == 0.f ? -INFINITY : (top == -INFINITY ? 0.f : top) + logf(sum);
+  }
+  cluster_sync_all();                          // every peer has read this CTA's part
 }
 
-constexpr size_t smem_of(int slots, int k_dim, int threads) {
+constexpr size_t smem_of(int slots, int k_dim, int threads, int split_dims) {
   const size_t rounded = size_t(slots + kTileSlots - 1) / kTileSlots * kTileSlots;
   const size_t q = size_t(kTileHeads) * q_stride(k_dim), sums = size_t(threads / 32) * kTileHeads * kPassPitch * sizeof(float);
-  return rounded * sizeof(int) + size_t(kTileHeads) * p_stride(slots) * sizeof(float) + (q > sums ? q : sums);
+  return rounded * sizeof(int) + size_t(kTileHeads) * p_stride(slots) * sizeof(float) + (q > sums ? q : sums) +
+         size_t(kTileHeads) * split_dims * sizeof(float);
 }
 
 template <int kThreads>
-cudaError_t launch(const Kv4AttnArgs& a, int batch, cudaStream_t st) {
+cudaError_t launch(const Kv4AttnArgs& a, int batch, int ncta, cudaStream_t st) {
   const cudaError_t e = once_per_device(kThreads == 512 ? kSetupKv4Mma16 : kSetupKv4Mma8, [] {
-    return cudaFuncSetAttribute(kv4_mma_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_of(kMaxSlots, 1024, kThreads)));
+    return cudaFuncSetAttribute(kv4_mma_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem_of(kMaxSlots, 1024, kThreads, 1024)));
   });
   if (e != cudaSuccess) return e;
   note_launch();
-  return launch_pdl(kv4_mma_kernel<kThreads>, dim3(unsigned((a.heads + kTileHeads - 1) / kTileHeads), unsigned(batch)), dim3(kThreads),
-                    smem_of(a.topk + a.swa, a.k_dim, kThreads), st, 1, a);
+  return launch_pdl(kv4_mma_kernel<kThreads>, dim3(unsigned((a.heads + kTileHeads - 1) / kTileHeads * ncta), unsigned(batch)), dim3(kThreads),
+                    smem_of(a.topk + a.swa, a.k_dim, kThreads, ncta > 1 ? a.v_dim : 0), st, unsigned(ncta), a, ncta);
 }
 
 }  // namespace
@@ -282,11 +325,15 @@ bool kv4_mma_fits(const Kv4AttnArgs& a) {
          ((reinterpret_cast<uintptr_t>(a.k_swa) | reinterpret_cast<uintptr_t>(a.v_swa)) & 7) == 0;
 }
 
-// 16 warps and one CTA an SM while there are no more CTAs than SMs, 8 warps and two CTAs beyond (96 queries of 16 heads of
-// 192 / 128, 828 slots: 26.6 us and 34.5; 90 of 40 heads, 640 slots: 39.6 and 32.7).
+// Clusters of 8 warps a CTA while they all fit the SMs and a CTA has 64 slots; else 16 warps and one CTA an SM while there are no more
+// CTAs than SMs, 8 warps and two CTAs beyond.  Measured, 640 slots: 8 queries of 16 heads of 192 / 128 in clusters of 8 11.9 us, of 4 13.4, alone
+// 18.9; 96 of 16 heads, 828 slots, 16 warps 26.6, 8 warps 34.5; 90 of 40 heads 39.6 and 32.7.
 cudaError_t launch_kv4_attn_mma(const Kv4AttnArgs& a, int batch, cudaStream_t st) {
-  const bool few = (long long)batch * ((a.heads + kTileHeads - 1) / kTileHeads) <= device_sm_count();
-  return few ? launch<512>(a, batch, st) : launch<256>(a, batch, st);
+  const int sms = device_sm_count();
+  const long long ctas = (long long)batch * ((a.heads + kTileHeads - 1) / kTileHeads);
+  int ncta = 1;
+  while (ncta < kMaxCluster && 2 * ncta * ctas <= sms && 2 * ncta * 64 <= a.topk + a.swa) ncta *= 2;
+  return ncta > 1 ? launch<256>(a, batch, ncta, st) : ctas <= sms ? launch<512>(a, batch, 1, st) : launch<256>(a, batch, 1, st);
 }
 
 }  // namespace csa2

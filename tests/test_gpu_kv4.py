@@ -877,3 +877,30 @@ def test_norm_rope_of_strided_views(csa2):
         want = view.double() / view.double().square().mean(-1, keepdim=True).sqrt()
         # 16 squares, their sum, the mean, a root and two products in fp32: 24 half steps of a value
         assert ((out.double() - want).abs() <= 24 * 2.0 ** -24 * want.abs() + 1e-30).all()
+
+
+@pytest.mark.parametrize("B,H,dk,dv,K,W", [(1, 5, 64, 64, 512, 128), (3, 20, 100, 72, 500, 100), (9, 40, 192, 128, 250, 6), (6, 16, 40, 1024, 900, 124),
+                                           (2, 64, 1024, 24, 128, 0)])
+def test_kv4_attention_of_few_queries_split_over_clusters(csa2, B, H, dk, dv, K, W):
+    """bf16 shapes whose slots several CTAs share: parts that hold nothing, scores that are not finite in one part alone."""
+    sh = shape(B, n_entries=1300, topk=K, swa=W, k_exp=-1, v_exp=1, q_heads=H, k_dim=dk, v_dim=dv, dtype="bf16", scale=0.07)
+    d = attn_inputs(csa2, sh, B + H, 2.0)
+    d.idx[0, :K // 2], d.idx[0, K - 1] = -1, 7                # the first parts of a query have nothing
+    if B > 1:
+        d.idx[1, 10:] = -1                                    # nor the last ones of another
+        d.n_swa[1] = 0
+    if B > 2:
+        d.idx[2] = -1
+        d.n_swa[2] = 0
+    assert_no_device_error(csa2, run_attn(csa2, sh, d))
+    check_attn(sh, d)
+    out, lse = d.out.clone(), d.lse.clone()
+    d.q[0, 1] = float("nan")                                  # one head of one query
+    run_attn(csa2, sh, d)
+    assert torch.isnan(d.out[0, 1]).all() and torch.isnan(d.lse[0, 1])
+    keep = torch.ones_like(d.lse, dtype=torch.bool)
+    keep[0, 1] = False
+    assert torch.equal(d.out[keep], out[keep]) and torch.equal(d.lse[keep], lse[keep])
+    d.idx[0, 3] = 1300                                        # beyond the cache: skipped and recorded
+    assert csa2.read_device_error(run_attn(csa2, sh, d)) == (-5, BAD_INDEX)
+    assert torch.equal(d.out[keep], out[keep])
