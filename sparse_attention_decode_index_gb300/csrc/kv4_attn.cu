@@ -7,9 +7,11 @@
 // Any head count, dims and element type, in fp32 (fp32 queries and windows, and bf16 ones that kv4_mma.cu does not take:
 // odd dims or addresses): a CTA takes one head or four of a
 // query.  Eight lanes go through a row together, a group of 16 dims each, so that a warp has
-// four rows on their way, or eight (fp32, 228 CTAs: 103 -> 72 us); a lane multiplies its numbers with every head of the CTA.  Scores stay in
+// four rows on their way, or eight (fp32, 228 CTAs: 103 -> 72 us; the rows' latency bounds it: two products an
+// instruction gave 211 -> 201 us for 60 queries of 64 heads); a lane multiplies its numbers with every head of the CTA.  Scores stay in
 // shared memory; every warp sums the values of its own rows, and the warps' sums are added in order.
 #include "kv4.cuh"
+#include "tc.cuh"
 
 namespace csa2 {
 
@@ -104,13 +106,13 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
   for (int h = 0; h < kHeads; ++h) top[h] = -INFINITY;
   for (int j0 = 4 * kRows * warp; j0 < slots; j0 += 4 * kRows * kWarps) {
     int e[kRows];
-    float dot[kRows][kHeads];
+    float2 dots[kRows][kHeads];                // sums over even and odd dims
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int j = j0 + 4 * u + r4;
       e[u] = j < slots ? row[j] : -1;
 #pragma unroll
-      for (int h = 0; h < kHeads; ++h) dot[u][h] = 0.f;
+      for (int h = 0; h < kHeads; ++h) dots[u][h] = make_float2(0.f, 0.f);
     }
     for (int g = l8; g < gk; g += 8) {
       float x[kRows][16];
@@ -124,10 +126,8 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
           const float4 y = q[i];
 #pragma unroll
           for (int u = 0; u < kRows; ++u) {
-            dot[u][h] = __fmaf_rn(x[u][4 * i], y.x, dot[u][h]);
-            dot[u][h] = __fmaf_rn(x[u][4 * i + 1], y.y, dot[u][h]);
-            dot[u][h] = __fmaf_rn(x[u][4 * i + 2], y.z, dot[u][h]);
-            dot[u][h] = __fmaf_rn(x[u][4 * i + 3], y.w, dot[u][h]);
+            dots[u][h] = fma2(make_float2(x[u][4 * i], x[u][4 * i + 1]), make_float2(y.x, y.y), dots[u][h]);
+            dots[u][h] = fma2(make_float2(x[u][4 * i + 2], x[u][4 * i + 3]), make_float2(y.z, y.w), dots[u][h]);
           }
         }
       }
@@ -137,9 +137,10 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
       const int j = j0 + 4 * u + r4;
 #pragma unroll
       for (int h = 0; h < kHeads; ++h) {
+        float dot = dots[u][h].x + dots[u][h].y;
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) dot[u][h] += __shfl_xor_sync(0xffffffffu, dot[u][h], o);
-        const float s = e[u] >= 0 ? dot[u][h] * (j < a.topk ? a.scale * a.k_up : a.scale) : -INFINITY;
+        for (int o = 1; o < 8; o <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        const float s = e[u] >= 0 ? dot * (j < a.topk ? a.scale * a.k_up : a.scale) : -INFINITY;
         if (l8 == 0 && j < slots) sw[h * slots + j] = s;
         asm("max.NaN.f32 %0, %0, %1;" : "+f"(top[h]) : "f"(s));   // a NaN score makes its head's output NaN
       }
@@ -183,11 +184,11 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
   // ---- values, 8 groups of 16 dims at a time
   for (int g0 = 0; g0 < gv; g0 += 8) {
     const int g = g0 + l8;
-    float acc[kHeads][16];
+    float2 acc[kHeads][8];
 #pragma unroll
     for (int h = 0; h < kHeads; ++h)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[h][i] = 0.f;
+      for (int i = 0; i < 8; ++i) acc[h][i] = make_float2(0.f, 0.f);
     for (int j = 4 * kRows * warp + r4; g < gv && j < slots; j += 4 * kRows * kWarps) {
       float x[kRows][16];
 #pragma unroll
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
         for (int h = 0; h < kHeads; ++h) {
           const float p = sw[h * slots + j + 4 * u];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[h][i] = __fmaf_rn(p, x[u][i], acc[h][i]);
+          for (int i = 0; i < 8; ++i) acc[h][i] = fma2(make_float2(p, p), make_float2(x[u][2 * i], x[u][2 * i + 1]), acc[h][i]);
         }
       }
     }
@@ -207,9 +208,10 @@ __global__ void __launch_bounds__(kThreads) kv4_attn_generic_kernel(const Kv4Att
     for (int h = 0; h < kHeads; ++h)
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        acc[h][i] += __shfl_xor_sync(0xffffffffu, acc[h][i], 8);
-        acc[h][i] += __shfl_xor_sync(0xffffffffu, acc[h][i], 16);
-        if (r4 == 0) part[(warp * kHeads + h) * 128 + 16 * l8 + i] = acc[h][i];
+        float o = i & 1 ? acc[h][i >> 1].y : acc[h][i >> 1].x;
+        o += __shfl_xor_sync(0xffffffffu, o, 8);
+        o += __shfl_xor_sync(0xffffffffu, o, 16);
+        if (r4 == 0) part[(warp * kHeads + h) * 128 + 16 * l8 + i] = o;
       }
     __syncthreads();
     const int n = min(128, a.v_dim - 16 * g0);
