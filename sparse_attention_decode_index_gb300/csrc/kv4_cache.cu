@@ -43,8 +43,8 @@ struct Raw {
 // another CTA writes.
 //
 // Measured: one entry of each of 64 sequences 4.6 us, their rows back 1.6 (latency); 8,191 entries of each of
-// 16 sequences 34 us and 4 for the counts, where their 142 MB would take 21: the issue slots (64 %) bound it, most of them
-// conversions.
+// 16 sequences 34 us and 4 for the counts, where their 142 MB would take 21: the loads' latency bounds it (DRAM 42 %,
+// issue slots 64 %; fewer conversions gained nothing).
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, kF32 ? 3 : 5) kv4_append_kernel(const Kv4AppendArgs a) {
   extern __shared__ __align__(16) uint8_t tile[];          // [per_cta][entry]
