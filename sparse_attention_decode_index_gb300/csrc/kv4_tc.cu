@@ -350,7 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       c.top[row] = max(top & 0xffffu, top >> 16);
       if (!end_sync()) return false;
       e = max(int(max(c.top[row], c.top[row ^ 64]) >> 7) - 127 - 9, -100);
-      scale = fminf(ldexpf(a.scale * log2e * a.k_up, e), 3e38f);
+      // (above 0 whatever the exponents: -inf of keys that are not there is multiplied by it.  Where the bound counts, products of at
+      // most 2^30 with the true factor are 0 beside any logit.)
+      scale = fminf(fmaxf(ldexpf(a.scale * log2e * a.k_up, e), 1e-37f), 3e38f);
       return true;
     };
     // Words 16 b .. 16 b + 15 of the row, as they are or as fp16.

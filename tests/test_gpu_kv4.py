@@ -904,3 +904,23 @@ def test_kv4_attention_of_few_queries_split_over_clusters(csa2, B, H, dk, dv, K,
     d.idx[0, 3] = 1300                                        # beyond the cache: skipped and recorded
     assert csa2.read_device_error(run_attn(csa2, sh, d)) == (-5, BAD_INDEX)
     assert torch.equal(d.out[keep], out[keep])
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("k_exp,scale", [(-46, 0.0), (-47, 0.0), (-64, 0.0), (64, 0.0), (-2, 1e-30), (-64, 1e-18)])
+def test_kv4_attention_of_queries_of_zeros_and_tiny_ones(csa2, kind, k_exp, scale):
+    """Heads of zeros (rows of a padded batch) and of about 2^-100 weigh all that they attend alike, whatever the exponent, the
+    softmax scale and the holes in their lists."""
+    kw, B = KINDS[kind]
+    sh = shape(B, n_entries=300, topk=200, swa=40, k_exp=k_exp, v_exp=0, scale=scale, **kw)
+    d = attn_inputs(csa2, sh, 31, holes=2.0)
+    d.idx[0, ::2], d.n_swa[0] = -1, 0                       # every second slot of a list is a hole, and nothing else is attended
+    d.q[:, ::2] = 0.0
+    d.q[:, 1] = randn(torch.Generator().manual_seed(3), (B, sh.k_dim), d.dt, 2.0 ** -100)
+    d.q[B - 1] = 0.0
+    assert_no_device_error(csa2, run_attn(csa2, sh, d))
+    check_attn(sh, d)
+    count = (d.idx >= 0).sum(1) + d.n_swa
+    flat = d.lse[:, ::2].double()
+    # log of a count of up to 240: exp and log within 4 steps, the sum exact or half a step an addition
+    assert ((flat - count.double().log()[:, None]).abs() <= 8 * EPS32 * 7 + 240 * 2.0 ** -24)[count > 0].all()
