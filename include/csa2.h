@@ -578,8 +578,8 @@ int csa2_norm_rope(const csa2_norm_rope_slot* slots, int32_t n_slots, int32_t ro
  * dropped and recorded (bad count).  max_new may be a whole prompt.
  * Of a group, with a its largest magnitude / 2^exp: the scale is the e4m3 number
  * nearest to a / 6 (ties to even), at least 2^-9 and at most 448; a code is the e2m1
- * number nearest to x / 2^exp / scale (ties to even), at most 6.  A group whose a is not
- * finite gets the scale NaN: all its dims read as NaN.
+ * number nearest to x / 2^exp / scale (ties to even), at most 6.  A group that holds a NaN or an
+ * infinity gets the scale NaN: all its dims read as NaN.
  *   k_new [B, max_new, dk]  v_new [B, max_new, dv]  kidx_new [B, max_new, dI]  n_new [B]
  *   kv4 [B, N, csa2_kv4_bytes]  k_idx [B, N, dI]  kb [B, ceil(N / block), dI] or NULL
  *   n_valid [B] (read and updated)

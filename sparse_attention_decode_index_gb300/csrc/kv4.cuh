@@ -52,7 +52,7 @@ CSA2_DEV void kv4_eight(uint32_t codes, __half2 scale, float (&x)[8]) {
 
 // 16 numbers as codes and a scale's byte.  The scale is the e4m3 number nearest to a sixth of the
 // largest magnitude (ties to even, at least 2^-9, at most 448), a code the e2m1 number nearest to x / scale (ties to even, at
-// most 6); `down` is 2^-exp, which no product here rounds by.
+// most 6); `down` is 2^-exp, which no product here rounds by that is not 0 or saturated in the end.
 // kF32: x are any fp32 numbers, whose quotients are rounded to fp32 first; that moves none onto a
 // border between two codes, as the border times the scale is itself an fp32 number and its neighbours' quotients
 // are more than half a step away.  Otherwise they have 8 significant bits (bf16), and a quotient that is not on a border (of 3
@@ -63,9 +63,9 @@ CSA2_DEV uint8_t kv4_quantise(const float (&x)[16], float down, uint2& codes) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
-  top *= down;
   codes = make_uint2(0u, 0u);
   if (!(top < INFINITY)) return 0x7f;
+  top *= down;   // (an infinity where 2^-exp takes it beyond fp32: it saturates, as do the numbers it does so with)
   const float sixth = kF32 ? __fdiv_rn(top, 6.f) : __uint_as_float((__float_as_uint(top * (1.f / 6.f)) + 0x200u) & ~0x3ffu);
   const uint8_t byte = __nv_cvt_float_to_fp8(fmaxf(sixth, 0.001953125f), __NV_SATFINITE, __NV_E4M3);
   const float scale = __half2float(kv4_scale(byte));

@@ -924,3 +924,27 @@ def test_kv4_attention_of_queries_of_zeros_and_tiny_ones(csa2, kind, k_exp, scal
     flat = d.lse[:, ::2].double()
     # log of a count of up to 240: exp and log within 4 steps, the sum exact or half a step an addition
     assert ((flat - count.double().log()[:, None]).abs() <= 8 * EPS32 * 7 + 240 * 2.0 ** -24)[count > 0].all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dk,dv", [(192, 128), (20, 24)])
+def test_kv4_append_of_numbers_beyond_the_range_of_their_quotients(csa2, dtype, dk, dv):
+    """Exponents of -64: numbers from 2^64 on, whose quotients by 2^exp are beyond fp32, saturate as any large number does; only
+    NaN and infinities read as NaN."""
+    sh = shape(2, n_entries=40, k_dim=dk, v_dim=dv, dtype=dtype, topk=4, swa=4, k_exp=-64, v_exp=-64)
+    s = append_state(csa2, sh, 24, 13, [3, 0], [24, 24])
+    rng = np.random.default_rng(17)
+    for t in (s.k_new, s.v_new):
+        top = np.exp2(rng.integers(60, 127, t.shape[:2] + (1,)) + rng.random(t.shape[:2] + (1,)))
+        x = rng.choice([1.0, -1.0, 0.6, 2.0 ** -61, -2.0 ** -64, 0.0], t.shape) * top
+        x[0, 0], x[0, 1], x[0, 2] = 2.0 ** 64, -2.0 ** 127, 3e38
+        x[0, 3, 5], x[1, 4, 19] = np.inf, np.nan
+        t.copy_(torch.tensor(x, dtype=torch.float32).to(t.dtype))
+    before, ws = clone(s), csa2.workspace(sh)
+    run_append(csa2, sh, s, ws)
+    assert_no_device_error(csa2, ws)
+    check_append(sh, s, before)
+    k, v = torch.empty_like(s.k_new), torch.empty_like(s.v_new)
+    csa2.kv4_rows(sh, s.kv, i32(np.arange(24) + np.array([[3], [0]])), k, v, ws, k_exp=-64, v_exp=-64)
+    for x in (k, v):
+        assert (x[0, 0] == 2688.0 * 2.0 ** -64).all() and (x[0, 1] == -2688.0 * 2.0 ** -64).all() and int(x.isnan().sum()) == min(16, x.shape[2]) + min(16, x.shape[2] - 16)
