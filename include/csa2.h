@@ -652,6 +652,15 @@ int csa2_debug_wait_timeout(const csa2_shape* shape, const void* q_idx, const fl
                             const int32_t* n_valid, int32_t k, int32_t* idx_out, uint32_t wait_limit_ns,
                             void* ws, size_t ws_bytes, csa2_stream_t stream);
 
+/* The same for csa2_kv4_attn's tensor-core kernel (fast path only, else
+ * CSA2_ERR_UNSUPPORTED): the first stage of every CTA never counts as filled, and
+ * every wait is limited to wait_limit_cycles (10,000 .. 200,000,000) instead of 2 s
+ * (in cycles at the highest clock). All roles give up, CSA2_ERR_TIMEOUT is recorded, and the kernel returns after
+ * 10 ms for copies in flight; out and lse hold anything. */
+int csa2_debug_kv4_wait_timeout(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa,
+                                const void* v_swa, const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp,
+                                uint32_t wait_limit_cycles, void* ws, size_t ws_bytes, csa2_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -88,6 +88,7 @@ _SIGS = {
     "csa2_kv4_append": (ctypes.c_int, [ctypes.POINTER(CShape), _I32] + [_VP] * 8 + [_I32] * 3 + [_VP, _SZ, _VP]),
     "csa2_kv4_rows": (ctypes.c_int, [ctypes.POINTER(CShape), _VP, _VP, _I32, _VP, _VP, _I32, _I32, _VP, _SZ, _VP]),
     "csa2_kv4_attn": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_VP] * 8 + [_I32, _I32, _VP, _SZ, _VP]),
+    "csa2_debug_kv4_wait_timeout": (ctypes.c_int, [ctypes.POINTER(CShape)] + [_VP] * 8 + [_I32, _I32, ctypes.c_uint32, _VP, _SZ, _VP]),
     "csa2_debug_wait_timeout": (ctypes.c_int, [ctypes.POINTER(CShape), _VP, _VP, _VP, _VP, _I32, _VP, ctypes.c_uint32,
                                                _VP, _SZ, _VP]),
 }
@@ -736,6 +737,15 @@ def debug_wait_timeout(shape, q_idx, w, k_idx, n_valid, k: int, idx_out, wait_li
                                          _ptr(k_idx, e, "k_idx"), _ptr(n_valid, torch.int32, "n_valid"), int(k),
                                          _ptr(idx_out, torch.int32, "idx_out"), int(wait_limit_ns),
                                          *_ws(ws), _stream(stream)), "csa2_debug_wait_timeout")
+
+
+def debug_kv4_wait_timeout(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, wait_limit_cycles: int, ws, lse=None, stream=None):
+    """Test hook of the bounded device waits (csa2_debug_kv4_wait_timeout): Kv4AttnCall's fast kernel with a stage that never
+    fills and waits limited to ``wait_limit_cycles``."""
+    call = Kv4AttnCall(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, ws, lse)
+    *args, ws_ptr, ws_bytes = call._args
+    call._bind("csa2_debug_kv4_wait_timeout", call.device, call._keep, (*args, int(wait_limit_cycles), ws_ptr, ws_bytes))
+    call(stream)
 
 
 def launch_count() -> int:

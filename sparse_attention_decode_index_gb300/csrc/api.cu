@@ -400,6 +400,50 @@ int check_attn_args(const csa2_shape& s, const void* q, const void* k_main, cons
   return CSA2_OK;
 }
 
+// The checks and the arguments of csa2_kv4_attn.
+int kv4_attn_args(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa, const void* v_swa,
+                  const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp, void* ws, size_t ws_bytes, Kv4AttnArgs& a) {
+  CSA2_TRY(check_shape(shape));
+  const csa2_shape& s = *shape;
+  CSA2_TRY(check_ws(s, ws, ws_bytes));
+  if (s.batch > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
+  CSA2_TRY(check_exps(k_exp, v_exp));
+  if (q == nullptr || kv4 == nullptr || idx == nullptr || out == nullptr) return CSA2_ERR_INVALID_ARG;
+  CSA2_TRY(check_sswa(s, k_swa, v_swa, n_swa));
+  const bool fast = attn_fast(s);
+  if (!aligned16(kv4) || (fast && !(aligned16(q) && aligned16(k_swa) && aligned16(v_swa) && aligned16(out))))
+    return CSA2_ERR_INVALID_ARG;
+  if (!aligned(elem_size(s.dtype), q, k_swa, v_swa, out) || !aligned(4, idx, n_swa, lse)) return CSA2_ERR_INVALID_ARG;
+  const uint64_t B = s.batch, kb = s.k_dim * elem_size(s.dtype), vb = s.v_dim * elem_size(s.dtype);
+  Span spans[] = {{q, B * s.q_heads * kb, false}, {kv4, B / seqdiv(s) * s.n_entries * kv4_bytes(s.k_dim, s.v_dim), false},
+                  {idx, B * s.topk * 4, false}, {k_swa, B * s.swa * kb, false}, {v_swa, B * s.swa * vb, false}, {n_swa, B * 4, false},
+                  {out, B * s.q_heads * vb, true}, {lse, B * s.q_heads * 4, true}, {ws, ws_bytes, true}};
+  if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
+  a.q = q;
+  a.kv = static_cast<const uint8_t*>(kv4);
+  a.idx = idx;
+  a.k_swa = k_swa;
+  a.v_swa = v_swa;
+  a.n_swa = n_swa;
+  a.out = out;
+  a.lse = lse;
+  a.seq_div = seqdiv(s);
+  a.n_entries = s.n_entries;
+  a.topk = s.topk;
+  a.swa = s.swa;
+  a.heads = s.q_heads;
+  a.k_dim = s.k_dim;
+  a.v_dim = s.v_dim;
+  a.dtype = s.dtype;
+  a.scale = softmax_scale(s);
+  a.k_up = std::ldexp(1.f, k_exp);
+  a.v_up = std::ldexp(1.f, v_exp);
+  a.wide = s.dtype == CSA2_F32 && s.k_dim % 16 == 0 && s.v_dim % 16 == 0 && aligned16(k_swa) && aligned16(v_swa);
+  a.wait_cycles = kKv4WaitCycles;
+  a.err = static_cast<int*>(ws);
+  return CSA2_OK;
+}
+
 }  // namespace
 
 namespace csa2 {
@@ -1207,45 +1251,9 @@ int csa2_kv4_rows(const csa2_shape* shape, const void* kv4, const int32_t* idx, 
 int csa2_kv4_attn(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa,
                   const void* v_swa, const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp, void* ws,
                   size_t ws_bytes, csa2_stream_t stream) {
-  CSA2_TRY(check_shape(shape));
-  const csa2_shape& s = *shape;
-  CSA2_TRY(check_ws(s, ws, ws_bytes));
-  if (s.batch > kMaxGridY) return CSA2_ERR_UNSUPPORTED;
-  CSA2_TRY(check_exps(k_exp, v_exp));
-  if (q == nullptr || kv4 == nullptr || idx == nullptr || out == nullptr) return CSA2_ERR_INVALID_ARG;
-  CSA2_TRY(check_sswa(s, k_swa, v_swa, n_swa));
-  const bool fast = attn_fast(s);
-  if (!aligned16(kv4) || (fast && !(aligned16(q) && aligned16(k_swa) && aligned16(v_swa) && aligned16(out))))
-    return CSA2_ERR_INVALID_ARG;
-  if (!aligned(elem_size(s.dtype), q, k_swa, v_swa, out) || !aligned(4, idx, n_swa, lse)) return CSA2_ERR_INVALID_ARG;
-  const uint64_t B = s.batch, kb = s.k_dim * elem_size(s.dtype), vb = s.v_dim * elem_size(s.dtype);
-  Span spans[] = {{q, B * s.q_heads * kb, false}, {kv4, B / seqdiv(s) * s.n_entries * kv4_bytes(s.k_dim, s.v_dim), false},
-                  {idx, B * s.topk * 4, false}, {k_swa, B * s.swa * kb, false}, {v_swa, B * s.swa * vb, false}, {n_swa, B * 4, false},
-                  {out, B * s.q_heads * vb, true}, {lse, B * s.q_heads * 4, true}, {ws, ws_bytes, true}};
-  if (written_overlap(spans, sizeof(spans) / sizeof(spans[0]))) return CSA2_ERR_INVALID_ARG;
   Kv4AttnArgs a{};
-  a.q = q;
-  a.kv = static_cast<const uint8_t*>(kv4);
-  a.idx = idx;
-  a.k_swa = k_swa;
-  a.v_swa = v_swa;
-  a.n_swa = n_swa;
-  a.out = out;
-  a.lse = lse;
-  a.seq_div = seqdiv(s);
-  a.n_entries = s.n_entries;
-  a.topk = s.topk;
-  a.swa = s.swa;
-  a.heads = s.q_heads;
-  a.k_dim = s.k_dim;
-  a.v_dim = s.v_dim;
-  a.dtype = s.dtype;
-  a.scale = softmax_scale(s);
-  a.k_up = std::ldexp(1.f, k_exp);
-  a.v_up = std::ldexp(1.f, v_exp);
-  a.wide = s.dtype == CSA2_F32 && s.k_dim % 16 == 0 && s.v_dim % 16 == 0 && aligned16(k_swa) && aligned16(v_swa);
-  a.err = static_cast<int*>(ws);
-  return cuda_status(launch_kv4_attn(a, fast, s.batch, stream));
+  CSA2_TRY(kv4_attn_args(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, lse, k_exp, v_exp, ws, ws_bytes, a));
+  return cuda_status(launch_kv4_attn(a, attn_fast(*shape), shape->batch, stream));
 }
 
 const char* csa2_status_str(int status) {
@@ -1294,6 +1302,18 @@ int csa2_debug_wait_timeout(const csa2_shape* shape, const void* q_idx, const fl
   a.wait_ns = wait_limit_ns;
   a.skip_first_copy = 1;
   return cuda_status(launch_index_select(a, false, s.batch, s.n_entries, stream));
+}
+
+int csa2_debug_kv4_wait_timeout(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa,
+                                const void* v_swa, const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp,
+                                uint32_t wait_limit_cycles, void* ws, size_t ws_bytes, csa2_stream_t stream) {
+  Kv4AttnArgs a{};
+  CSA2_TRY(kv4_attn_args(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, lse, k_exp, v_exp, ws, ws_bytes, a));
+  if (wait_limit_cycles < 10000u || wait_limit_cycles > 200000000u) return CSA2_ERR_INVALID_ARG;
+  if (!attn_fast(*shape)) return CSA2_ERR_UNSUPPORTED;
+  a.wait_cycles = wait_limit_cycles;
+  a.never = 1;
+  return cuda_status(launch_kv4_attn(a, true, shape->batch, stream));
 }
 
 int csa2_fast_path(const csa2_shape* shape, int32_t* indexer_fast_out, int32_t* attention_fast_out) {

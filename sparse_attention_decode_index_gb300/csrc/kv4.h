@@ -79,8 +79,12 @@ struct Kv4AttnArgs {
   float scale;               // softmax scale (natural-log domain)
   float k_up, v_up;          // 2^k_exp, 2^v_exp
   int wide;                  // fp32 window rows of 16 dims at 16-byte addresses (kv4_attn.cu)
+  long long wait_cycles;     // limit of a wait (kv4_tc.cu)
+  int never;                 // 1: the first stage never fills (csa2_debug_kv4_wait_timeout; kv4_tc.cu)
   int* err;
 };
+
+constexpr long long kKv4WaitCycles = 4000000000ll;   // 2 s at the highest clock
 
 // kv4_tc.cu: bf16, 64 heads, dk 192, dv 128, arrays at 16-byte addresses (`fast` of launch_kv4_attn).
 cudaError_t launch_kv4_attn_tc(const Kv4AttnArgs& a, int batch, cudaStream_t st);

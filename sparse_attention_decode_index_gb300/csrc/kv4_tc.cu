@@ -108,8 +108,7 @@ CSA2_DEV uint32_t pack_f16(float lo, float hi) {
 }
 
 // A bounded wait of a whole warp, which goes on or gives up together (as tc_wait_warp, counted in cycles: many warps wait here).
-constexpr long long kWaitCycles = 4000000000ll;   // 2 s at the highest clock
-CSA2_DEV bool wait_warp(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
+CSA2_DEV bool wait_warp(Shared& c, uint64_t* bar, uint32_t parity, const Kv4AttnArgs& a) {
   bool here = mbar_try_wait(bar, parity);
   if (!here) {
     const long long t0 = clock64();
@@ -118,9 +117,9 @@ CSA2_DEV bool wait_warp(Shared& c, uint64_t* bar, uint32_t parity, int* err) {
       if (here) break;
       if ((i & 31u) == 0u) {
         if (c.abort) break;
-        if (clock64() - t0 > kWaitCycles) {
+        if (clock64() - t0 > a.wait_cycles) {
           c.abort = 1;
-          report(err, kErrTimeout, int(threadIdx.x));   // which role gave up first
+          report(a.err, kErrTimeout, int(threadIdx.x));   // which role gave up first
           break;
         }
       }
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int item0 = int(blockIdx.x) / ncta, step = int(gridDim.x) / ncta;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&c.full[i], kGroupWarps);
+      mbar_init(&c.full[i], kGroupWarps + (i == 0 ? a.never : 0));
       mbar_init(&c.empty[i], 1 + kSoftmaxWarps);   // the values' end; its mask has been read
     }
     for (int b = 0; b < kScores; ++b) {
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float ref = -INFINITY, sum = 0.f;        // the exponent that P and O are relative to, and the weights' sum
       bool first = true;
       for (int t = range.first; t < range.last; ++t) {
-        ok = wait_warp(c, &c.s_full[buf], turn & 1, a.err);
+        ok = wait_warp(c, &c.s_full[buf], turn & 1, a);
         if (!ok) break;
         tc_fence_after();
         const uint32_t mask = reinterpret_cast<const uint32_t*>(&c.mask[st])[half];
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ref = top;
           } else if (__any_sync(0xffffffffu, grows)) {
             // O holds tiles up to the one before: wait for it.
-            ok = buf > 0 ? wait_warp(c, &c.s_free[buf - 1], turn & 1, a.err) : wait_warp(c, &c.s_free[kScores - 1], (turn - 1) & 1, a.err);
+            ok = buf > 0 ? wait_warp(c, &c.s_free[buf - 1], turn & 1, a) : wait_warp(c, &c.s_free[kScores - 1], (turn - 1) & 1, a);
             if (!ok) break;
             tc_fence_after();
             const float f = grows ? ex2(ref - top) : 1.f;
@@ -305,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      ok = items == 0 || wait_warp(c, &c.stat_free, (items - 1) & 1, a.err);
+      ok = items == 0 || wait_warp(c, &c.stat_free, (items - 1) & 1, a);
       if (!ok) break;
       c.stat[tid] = make_float2(ref - kUp, sum);
       warp_arrive(&c.stat_full);
@@ -318,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t met = 0;
     auto end_sync = [&]() -> bool {                           // the end warps wait for each other (a bounded wait, as all are)
       warp_arrive(&c.ends);
-      return wait_warp(c, &c.ends, met++ & 1, a.err);
+      return wait_warp(c, &c.ends, met++ & 1, a);
     };
     auto copy_q = [&](int item) {                             // into shared memory
       if (item < n_items) {
@@ -372,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t to = tmem + lanes + (i == 0 ? kQhCol : kQbCol);
       uint32_t r[16];
       words(0, i == 0, r);
-      if (wait && !wait_warp(c, &c.q_empty[i], phase, a.err)) return false;
+      if (wait && !wait_warp(c, &c.q_empty[i], phase, a)) return false;
       tc_fence_after();
       tmem_st16(to, r);
 #pragma unroll 1
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         c.q_scale[(items + 1) & 1][row] = scale;
         if (!store_q(0, true, items & 1) || !store_q(1, true, items & 1)) break;
       }
-      if (!wait_warp(c, &c.stat_full, items & 1, a.err)) break;
+      if (!wait_warp(c, &c.stat_full, items & 1, a)) break;
       const float2 mine = c.stat[row], theirs = c.stat[row ^ 64];
       warp_arrive(&c.stat_free);
       const float top = fmaxf(mine.x, theirs.x);
@@ -409,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float sum = mine.y * weight + theirs.y * (theirs.x == -INFINITY ? 0.f : ex2(theirs.x - top));
       const bool none = sum == 0.f;                           // no key: O may hold anything
       const float f = ncta > 1 ? weight : weight * (a.v_up / sum);
-      if (!wait_warp(c, &c.o_last, items & 1, a.err)) break;
+      if (!wait_warp(c, &c.o_last, items & 1, a)) break;
       tc_fence_after();
       // A thread ends with 64 columns of its head: it gives its part of the others to its partner of the other half.  O is free
       // for the next item as soon as this thread's columns are in registers.
@@ -479,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.lse[(long long)item * kH + head] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");   // (given up: the next query's)
   } else if (warp != kScoresWarp && warp != kValuesWarp) {
     // ---------------------------------------------------------------- producers: 16 rows of every second tile a warp
     // (Eight warps on the same tile spent most of it on the latencies of its steps.)
@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (here.item < n_items) {
       const bool window = here.t >= range.window;
-      ok = wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a.err);
+      ok = wait_warp(c, &c.empty[st], (lap & 1) ^ 1, a);
       if (!ok) break;
       const uint32_t k_st = smem_u32(c.k[st]), v_st = smem_u32(c.v[st]);
       if (window) {
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           if (n < kTile) {                     // values behind the count are zeroed: they meet weights of 0, and might be NaN
-            ok = n == 0 || wait_warp(c, &c.window[group], waits++ & 1, a.err);
+            ok = n == 0 || wait_warp(c, &c.window[group], waits++ & 1, a);
             if (!ok) break;
             for (int i = lane; i < (kTile - n) * 16; i += 32) {
               const int r = n + (i >> 4), p = i & 15;
@@ -651,11 +651,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if (!ok) {                                 // given up: 10 ms for window rows that may still be on their way
-      const long long t0 = clock64();
-      while (clock64() - t0 < 20000000) {
-      }
-    }
   } else {
     // ---------------------------------------------------------------- MMA issue: scores by one warp, values by another
     // (One warp for both left the tensor cores idle while it looked at its barriers: 1,680 cycles a tile.)
@@ -667,23 +662,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int item = item0; item < n_items && ok; item += step, ++items) {
       bool first = true;
-      if (scores) ok = wait_warp(c, &c.q_full[0], items & 1, a.err);
-      else if (items > 0) ok = wait_warp(c, &c.o_free, (items - 1) & 1, a.err);   // (of every item, with keys or without)
+      if (scores) ok = wait_warp(c, &c.q_full[0], items & 1, a);
+      else if (items > 0) ok = wait_warp(c, &c.o_free, (items - 1) & 1, a);   // (of every item, with keys or without)
       bool half = true;                        // the query as fp16 is still wanted
       auto half_done = [&]() -> bool {
         half = false;
         if (elect_one()) tc_commit(&c.q_empty[0]);
         __syncwarp();
-        return wait_warp(c, &c.q_full[1], items & 1, a.err);
+        return wait_warp(c, &c.q_full[1], items & 1, a);
       };
       for (int t = range.first; t < range.last && ok; ++t) {
         const uint32_t here = st;
         const bool window = t >= range.window;
         if (scores) {
-          if (turn > 0) ok = wait_warp(c, &c.s_free[buf], (turn - 1) & 1, a.err);   // (S lies where the weights of the third tile before lay)
-          ok = ok && wait_warp(c, &c.full[st], lap & 1, a.err);
+          if (turn > 0) ok = wait_warp(c, &c.s_free[buf], (turn - 1) & 1, a);   // (S lies where the weights of the third tile before lay)
+          ok = ok && wait_warp(c, &c.full[st], lap & 1, a);
         } else {
-          ok = wait_warp(c, &c.p_full[buf], turn & 1, a.err);
+          ok = wait_warp(c, &c.p_full[buf], turn & 1, a);
         }
         if (!ok) break;
         if (++st == kStages) {
@@ -738,6 +733,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (c.abort) {                               // given up: 10 ms for window rows that may still be on their way, whoever asked for them
+    const long long t0 = clock64();
+    while (clock64() - t0 < 20000000) {
+    }
+  }
   if (warp == 0) tmem_free(tmem, kTmemCols);
   if (ncta == 1) return;
 

@@ -948,3 +948,25 @@ def test_kv4_append_of_numbers_beyond_the_range_of_their_quotients(csa2, dtype, 
     csa2.kv4_rows(sh, s.kv, i32(np.arange(24) + np.array([[3], [0]])), k, v, ws, k_exp=-64, v_exp=-64)
     for x in (k, v):
         assert (x[0, 0] == 2688.0 * 2.0 ** -64).all() and (x[0, 1] == -2688.0 * 2.0 ** -64).all() and int(x.isnan().sum()) == min(16, x.shape[2]) + min(16, x.shape[2] - 16)
+
+
+@pytest.mark.parametrize("B,K,W,fill", [(3, 512, 128, 128), (330, 512, 128, 128), (40, 64, 512, 300), (330, 1, 128, 50)])
+def test_kv4_attention_waits_that_give_up(csa2, B, K, W, fill):
+    """A stage that never fills, of a query split over a cluster, of many queries a CTA, and in a window: every role gives up, the
+    call returns with the timeout recorded and writes nothing but its outputs; the same workspace then serves a normal call."""
+    sh = shape(B, n_entries=600, topk=K, swa=W, **FAST)
+    d = attn_inputs(csa2, sh, 12, holes=0.0, fill=fill)
+    if fill == 50:
+        d.idx[:] = -1
+    ws = run_attn(csa2, sh, d)
+    out, lse = d.out.clone(), d.lse.clone()
+    whole, sums = torch.full((B + 2, *out.shape[1:]), 5.0, dtype=out.dtype, device="cuda"), torch.full((B + 2, 64), 5.0, device="cuda")
+    csa2.debug_kv4_wait_timeout(sh, d.q, d.kv, d.idx, d.k_swa, d.v_swa, d.n_swa, whole[1:-1], 2000000, ws, lse=sums[1:-1])
+    st, bits = csa2.read_device_error(ws)
+    assert st == -6 and bits == 4
+    for x in (whole, sums):
+        assert (x[0] == 5.0).all() and (x[-1] == 5.0).all()
+    for t in (d.out, d.lse):
+        t.fill_(9.0)
+    assert_no_device_error(csa2, run_attn(csa2, sh, d, ws))
+    assert torch.equal(d.out, out) and torch.equal(d.lse, lse)

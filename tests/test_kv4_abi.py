@@ -168,3 +168,17 @@ def test_kv4_outputs_over_other_arrays_are_refused(csa2, op):
         for p in (ws, ws + n - 16, ws - (size[x] - 1) // 16 * 16):
             if p + size[x] > ws:
                 assert _call(csa2, op, s, **{x: p}) == INVALID, x
+
+
+def test_wait_hook_refusals(csa2):
+    """The test hook of the attention's waits checks what the attention checks, its limit, and that the fast kernel serves the shape."""
+    def call(s, limit=2000000, **kw):
+        d = {n: FAKE + i * STEP for i, n in enumerate(NAMES["attn"])}
+        d.update(kw)
+        return csa2.lib().csa2_debug_kv4_wait_timeout(ctypes.byref(s), *d.values(), 0, 0, limit, FAKE - STEP, _ws(csa2, s), None)
+
+    s = _shape(csa2)
+    for limit in (0, 9999, 200000001):
+        assert call(s, limit) == INVALID
+    assert call(s, q=None) == INVALID and call(s, out=FAKE) == INVALID
+    assert call(_shape(csa2, q_heads=16)) == UNSUPPORTED
