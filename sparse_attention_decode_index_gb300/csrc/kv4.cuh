@@ -63,9 +63,14 @@ CSA2_DEV uint8_t kv4_quantise(const float (&x)[16], float down, uint2& codes) {
   float top = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
+  top *= down;
   codes = make_uint2(0u, 0u);
-  if (!(top < INFINITY)) return 0x7f;
-  top *= down;   // (an infinity where 2^-exp takes it beyond fp32: it saturates, as do the numbers it does so with)
+  if (!(top < INFINITY)) {   // a NaN or an infinity, or 2^-exp takes numbers beyond fp32, which saturate
+    float raw = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(raw) : "f"(fabsf(x[i])));
+    if (!(raw < INFINITY)) return 0x7f;
+  }
   const float sixth = kF32 ? __fdiv_rn(top, 6.f) : __uint_as_float((__float_as_uint(top * (1.f / 6.f)) + 0x200u) & ~0x3ffu);
   const uint8_t byte = __nv_cvt_float_to_fp8(fmaxf(sixth, 0.001953125f), __NV_SATFINITE, __NV_E4M3);
   const float scale = __half2float(kv4_scale(byte));

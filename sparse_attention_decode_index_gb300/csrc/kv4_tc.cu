@@ -478,7 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         a.lse[(long long)item * kH + head] = none ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");   // (given up: the next query's)
   } else if (warp != kScoresWarp && warp != kValuesWarp) {
     // ---------------------------------------------------------------- producers: 16 rows of every second tile a warp
     // (Eight warps on the same tile spent most of it on the latencies of its steps.)
@@ -733,7 +732,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (c.abort) {                               // given up: 10 ms for window rows that may still be on their way, whoever asked for them
+  if (c.abort) {                               // given up: what may still be on its way, a query here, 10 ms for window rows, whoever asked
+    asm volatile("cp.async.wait_all;" ::: "memory");
     const long long t0 = clock64();
     while (clock64() - t0 < 20000000) {
     }
