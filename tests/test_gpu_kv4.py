@@ -970,3 +970,29 @@ def test_kv4_attention_waits_that_give_up(csa2, B, K, W, fill):
         t.fill_(9.0)
     assert_no_device_error(csa2, run_attn(csa2, sh, d, ws))
     assert torch.equal(d.out, out) and torch.equal(d.lse, lse)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("ve,power", [(64, -60), (-64, 33), (64, 64), (-64, -64)])
+def test_kv4_attention_of_windows_far_from_the_entries(csa2, kind, ve, power):
+    """Windows alone, whose values are of 2^power: down to 2^(v_exp - 126), up to 2^(v_exp + 100)."""
+    kw, B = KINDS[kind]
+    sh = shape(B, n_entries=70, topk=48, swa=40, k_exp=0, v_exp=ve, **kw)
+    d = attn_inputs(csa2, sh, 77, fill=40)
+    d.idx[:] = -1
+    d.v_swa.copy_(d.v_swa.float() * 2.0 ** (power - ve))
+    assert_no_device_error(csa2, run_attn(csa2, sh, d))
+    check_attn(sh, d)
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_kv4_attention_without_lse(csa2, kind):
+    kw, B = KINDS[kind]
+    sh = shape(B, n_entries=90, topk=70, swa=30, k_exp=-2, v_exp=0, **kw)
+    d = attn_inputs(csa2, sh, 5, 1.0)
+    ws = run_attn(csa2, sh, d)
+    out = d.out.clone()
+    d.out.fill_(9.0)
+    csa2.kv4_attn(sh, d.q, d.kv, d.idx, d.k_swa, d.v_swa, d.n_swa, d.out, ws, k_exp=-2, v_exp=0)
+    assert torch.equal(d.out, out)
+    assert_no_device_error(csa2, ws)
