@@ -97,10 +97,7 @@ static_assert(kH * kPRow * 4 + kMaxCluster * kH * 4 <= kStages * kKBytes, "a spl
 // Instruction descriptor of kind::f16: fp16 x fp16 -> fp32.
 constexpr uint32_t idesc_f16(int m, int n, bool b_mn) { return idesc_bf16(m, n, b_mn) & ~((1u << 7) | (1u << 10)); }
 
-CSA2_DEV void cp16(uint32_t dst, const uint8_t* src, const void* any) {   // src null: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src != nullptr ? src : any), "r"(src != nullptr ? 16u : 0u)
-               : "memory");
-}
+CSA2_DEV void cp16(uint32_t dst, const uint8_t* src) { asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory"); }
 CSA2_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 CSA2_DEV uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -325,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
         for (int x = 0; x < kH * kDk / 8 / 128; ++x) {
           const int i = row + 128 * x, r = i / (kDk / 8), p = i - r * (kDk / 8);
-          cp16(smem_u32(c.q) + r * kQRow + p * 16, src + i * 16, nullptr);
+          cp16(smem_u32(c.q) + r * kQRow + p * 16, src + i * 16);
         }
       }
       cp_commit();

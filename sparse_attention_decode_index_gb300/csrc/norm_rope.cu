@@ -320,8 +320,10 @@ using Kernel = void (*)(NormRopeArgs);
 
 template <bool kBf16, int kBytes, int kNv>
 Kernel kernel_of(int partner) {
-  return partner == kNoPartner  ? norm_rope_kernel<kBf16, kBytes, kNv, kNoPartner>
-         : partner == kSameLane ? norm_rope_kernel<kBf16, kBytes, kNv, (kNv > 1 ? kSameLane : kLoaded)>
+  if constexpr (kNv > 1) {   // (where a lane has one vector, its partner is another lane's)
+    if (partner == kSameLane) return norm_rope_kernel<kBf16, kBytes, kNv, kSameLane>;
+  }
+  return partner == kNoPartner    ? norm_rope_kernel<kBf16, kBytes, kNv, kNoPartner>
          : partner == kOtherLane ? norm_rope_kernel<kBf16, kBytes, kNv, kOtherLane>
                                  : norm_rope_kernel<kBf16, kBytes, kNv, kLoaded>;
 }
