@@ -535,8 +535,9 @@ int csa2_kv_evict(const csa2_shape* shape, int32_t trigger, int32_t keep, int32_
  * scales' range: 0 suits groups whose largest magnitude is 0.1 .. 2,688).  bf16
  * holds every such value exactly, but for scales of NaN (see csa2_kv4_append).
  * The kernels read nothing before the preceding kernel of the stream has
- * completed.  kv4 is 16-byte aligned, every other array a multiple of its
- * elements' size, and none lies in the ws_bytes of the call's ws (refused). */
+ * completed.  kv4 is 16-byte aligned, and so are q, k_swa, v_swa and out of
+ * csa2_kv4_attn where the fast kernels serve it (others are refused); every other array's
+ * address is a multiple of its elements' size, and none lies in the ws_bytes of the call's ws (refused). */
 
 /* Bytes of a packed entry, 9 a group of 16 dims, up to a multiple of 16
  * (host only; 0 unless both dims are 1..1024). */
@@ -562,7 +563,8 @@ typedef struct {
  *   center = 1:  y = (x - mean(x)) / sqrt(mean((x - mean(x))^2) + eps) * gain
  * over a head's dim numbers; then the pairs of y are turned by pos[r] * freqs[i]
  * and multiplied by mag.  rot_dim = 0 turns nothing (pos and freqs are not
- * read and may be NULL).  The arithmetic is fp32, rounded once.
+ * read and may be NULL).  The arithmetic is fp32, rounded once; a head whose sum of squares is beyond
+ * fp32 (1,024 numbers of 2^59) comes out as zeros.
  *   pos [rows] int32   freqs [rot_dim / 2] double (device)
  * rows >= 1; 1 <= n_slots <= 16; mag finite and > 0; eps finite and >= 0;
  * rot_dim even, 0..1024; heads and dim up to 1024.  Rows that are not whole vectors of
@@ -607,12 +609,13 @@ int csa2_kv4_rows(const csa2_shape* shape, const void* kv4, const int32_t* idx, 
  *   lse [B, H] fp32 (nullable); out = 0 and -inf where nothing is attended,
  *   both NaN where a key that is attended scores NaN or +inf
  * batch <= 65,535; out and lse overlap nothing else (refused); n_swa is not read where W = 0.
- * bf16 weights are rounded where they meet values on tensor cores (their sums and lse are not): by 2^-9 of themselves to
- * bf16, or, those of entries where csa2_fast_path says that the fast kernels serve the attention, to fp16,
- * by 2^-12 of themselves or 2^-32 of their head's greatest.  There queries meet entries in fp16, scaled by a
+ * bf16 weights are rounded where they meet values on tensor cores (their sums and lse are not), by half a step: to
+ * bf16, at most 2^-8 of themselves, or, those of entries where csa2_fast_path says that the fast kernels serve the attention, to
+ * fp16, at most 2^-11 of themselves or 2^-32 of their head's greatest.  There q, k_swa, v_swa and out are
+ * 16-byte aligned (refused otherwise), and queries meet entries in fp16, scaled by a
  * power of two a head: numbers 2^24 below their head's largest lose bits, those 2^34 below it all; products of windows take bf16
- * as it is.  Window values are summed in units of 2^v_exp, and
- * their magnitudes stay below 2^(100 + v_exp).  Dims that an attended value holds a NaN or an infinity in
+ * as it is.  There too window values are summed in units of 2^v_exp: their magnitudes stay below 2^(v_exp + 100), and
+ * those below 2^(v_exp - 126) lose bits.  Dims that an attended value holds a NaN or an infinity in
  * come out NaN or infinite, whatever its weight; what is not attended is never used. */
 int csa2_kv4_attn(const csa2_shape* shape, const void* q, const void* kv4, const int32_t* idx, const void* k_swa,
                   const void* v_swa, const int32_t* n_swa, void* out, float* lse, int32_t k_exp, int32_t v_exp, void* ws,

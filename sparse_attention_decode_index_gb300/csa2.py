@@ -724,7 +724,8 @@ class Kv4AttnCall(_Call):
 
 def kv4_attn(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, ws, lse=None, k_exp: int = 0, v_exp: int = 0, stream=None):
     """Sparse attention over the packed cache's entries idx [B, K] and the queries' windows (csa2_kv4_attn); out in the
-    element type."""
+    element type. Where ``fast_path(shape)`` says that the fast kernels serve the attention, q, k_swa, v_swa and out begin at 16-byte
+    addresses."""
     Kv4AttnCall(shape, q, kv4, idx, k_swa, v_swa, n_swa, out, ws, lse, k_exp, v_exp)(stream)
 
 

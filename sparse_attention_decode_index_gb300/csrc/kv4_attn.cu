@@ -8,7 +8,8 @@
 // odd dims or addresses): a CTA takes one head or four of a
 // query.  Eight lanes go through a row together, a group of 16 dims each, so that a warp has
 // four rows on their way, or eight (fp32, 228 CTAs: 103 -> 72 us; the rows' latency bounds it: two products an
-// instruction gave 211 -> 201 us for 60 queries of 64 heads); a lane multiplies its numbers with every head of the CTA.  Scores stay in
+// instruction gave 211 -> 201 us for 60 queries of 64 heads, whose 1.6 GFLOP take 21: entries are fetched and converted once
+// for four heads, 16 times for 64); a lane multiplies its numbers with every head of the CTA.  Scores stay in
 // shared memory; every warp sums the values of its own rows, and the warps' sums are added in order.
 #include "kv4.cuh"
 #include "tc.cuh"

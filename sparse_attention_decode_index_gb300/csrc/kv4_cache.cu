@@ -42,9 +42,10 @@ struct Raw {
 // entry; its members come from the cache in front of the new entries and from the new ones, never from what
 // another CTA writes.
 //
-// Measured: one entry of each of 64 sequences 4.6 us, their rows back 1.6 (latency); 8,191 entries of each of
-// 16 sequences 34 us and 4 for the counts, where their 142 MB would take 21: the loads' latency bounds it (DRAM 42 %,
-// issue slots 64 %; fewer conversions gained nothing).
+// Measured: one entry of each of 64 sequences 4.9 us, their rows back 2.1 (latency); 8,191 entries of each of
+// 16 sequences 33.7 us with the counts, where their 142 MB would take 21, in fp32 58.0 (34): a CTA loads, packs, waits and stores
+// once, and nothing of the next entries is on its way meanwhile (DRAM 41 %, issue slots 64 %, fp32 48 % and 48 %; fewer conversions
+// gained nothing).
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads, kF32 ? 3 : 5) kv4_append_kernel(const Kv4AppendArgs a) {
   extern __shared__ __align__(16) uint8_t tile[];          // [per_cta][entry]
@@ -196,7 +197,8 @@ CSA2_DEV void row_entries(const Kv4RowsArgs& a, int row0, int n, int bytes, cons
 }
 
 // A thread writes 16 bytes of a row at a time (8 bf16 or 4 fp32 numbers: half or a quarter of a group).
-// Measured: 32,768 rows of 192 / 128 dims in bf16 6.4 us, 131,072 20.5 us, 5.3 TB/s (issue slots 72 %).
+// Measured: 32,768 rows of 192 / 128 dims in bf16 8.0 us, 131,072 20.8 us, 5.3 TB/s (issue slots
+// 72 %), in fp32 11.8 and 32.6 us, 5.9 TB/s.
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Kv4RowsArgs a, int n_rows, int per_cta) {
   __shared__ const uint8_t* src[kMaxRows];

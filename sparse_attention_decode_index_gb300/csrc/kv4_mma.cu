@@ -8,11 +8,13 @@
 //   softmax     fp32, a warp per head, over all slots in shared memory.
 //   O = P V     the slots go round the warps, 16 a step.  B wants the pairs along the slots: a lane takes eight
 //     dims of its four slots (a word of codes each) and interleaves them, so that column g of product j is dim 8 g + j.
-//     P is rounded to bf16 (half a step, 2^-9 of a weight; its sum is not rounded), which a factor of 2^v_exp for
+//     P is rounded to bf16 (half a step, 2^-8 of a weight; its sum is not rounded), which a factor of 2^v_exp for
 //     entries does not change.  The warps' sums are added up in their order.
 // Bound by latency, two round trips to memory per 16 slots of a warp, and the conversions: 90 queries, 40 heads of 192 / 128,
-// 640 slots 32.7 us (fp32 products in kv4_attn.cu: 168), 20 queries of 16 heads 13.6 (without clusters 18.8), 1 query of 4 heads of
-// 64 / 64 7.9 (10.6).  Three CTAs an SM leave 80 registers a thread, which spills (51.1).
+// 640 slots 32.3 us (fp32 products in kv4_attn.cu: 168), 20 queries of 16 heads 15.1 with distinct inputs in turn, 13.6 in calls from Python
+// (without clusters 18.8), 1 query of 4 heads of
+// 64 / 64 7.9 (10.6).  An entry is gathered and converted once for 16 heads, three times for 40.  Three CTAs an SM leave 80 registers a
+// thread, which spills (51.1).
 #include "kv4.cuh"
 
 namespace csa2 {

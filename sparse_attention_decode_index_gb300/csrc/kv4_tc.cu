@@ -27,10 +27,11 @@
 //
 // P is rounded to fp16 (entries) or bf16 (window) as the tensor core asks for; the weights' sums stay fp32 and unrounded.
 //
-// Measured (512 entries and 128 window rows a query): 1 query 10.4 us, 64 12.7, 256 24.6, 1,024 in sequences of 32 64.5 (20.5 of
-// which their 139 MB would take, and 14 their products).  Neither bounds it (DRAM 27 %, tensor cores 33 %, issue slots 45 %): a
+// Measured (512 entries and 128 window rows a query, distinct inputs in turn in a CUDA graph): 1 query 10.6 us, 64 12.9, 256 24.3,
+// 1,024 in sequences of 32 66.1 (20.5 of which their 139 MB would take, and 14 their products); attn.cu on bf16 rows of the same
+// entries 9.1, 13.7, 56.2, 207.  Neither bounds it (DRAM 27 %, tensor cores 33 %, issue slots 45 %): a
 // tile's way from S to P, 700 to 1,000 cycles one behind the other, and 2,000 to 4,000 between two queries do.  Two groups of
-// softmax warps, which hand a row's exponent on, took 73.8: 24 warps leave 80 registers a thread.
+// softmax warps, which hand a row's exponent on, took 73.8 for 65.8: 24 warps leave 80 registers a thread.
 #include <cuda.h>
 
 #include "kv4.cuh"
@@ -59,7 +60,7 @@ constexpr int kQRow = kDk * 2 + 16;            // query rows on their way to TME
 constexpr int kXRow = 68;                      // fp32 columns of a row that the halves exchange, padded
 constexpr int kPRow = kDv + 4;                 // partial O of a split
 // Weights are held as 2^7 times their relation to their row's exponent: at most 2^15, as that grows by steps of 2^8, which
-// fp16 holds, and rounded by 2^-12 of themselves or, below 2^-21, by 2^-32 of the greatest.
+// fp16 holds, and rounded by at most 2^-11 of themselves or, below 2^-21, by 2^-32 of the greatest.
 constexpr float kUp = 7.f;
 constexpr uint32_t kTmemCols = 512;            // O (128), three S (64 each), Q as fp16 and as bf16 (96 each)
 constexpr uint32_t kOCol = 0, kSCol = 128, kQhCol = 320, kQbCol = 416;

@@ -14,8 +14,9 @@
 // and gains stay in registers while the head does.
 //
 // Measured: 8 rows 6.0 us; 8,192 rows of 64 + 1 heads of 192 in bf16 72.6 us, 5.6 TB/s (62 % of DRAM's cycles, issue
-// slots 64 %: the next load waits for the shuffles' turn); 4,097 rows of 16 heads of 128 in fp32, layer norm with gains of
-// each head, 21.8 us, 3.3 TB/s (issue slots 63 %).  Four blocks an SM leave too few registers (124 us),
+// slots 64 %: the next load waits for the shuffles' turn), in fp32 129.8, 6.3 TB/s; 4,097 rows of 16 + 1 heads of 128 in fp32, layer
+// norm with gains of each head, 22.1 us, 3.2 TB/s, root mean square 20.4 (no unit is busy: issue slots 64 %, DRAM 18 %, warps 35 %;
+// sums' shuffles one behind the other).  Four blocks an SM leave too few registers (124 us),
 // four vectors a lane for fp32 too few lanes (30 us).
 #include "common.cuh"
 #include "kv4.h"
